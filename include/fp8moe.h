@@ -69,6 +69,11 @@ typedef enum {
 
 enum { FP8MOE_SCALES_ROWMAJOR = -2, FP8MOE_NO_GROUPS = -1, FP8MOE_GROUP_ROWS = 0, FP8MOE_GROUP_COLS = 1 };
 
+/* Element types of the arguments that come in more than one (norm weights,
+ * router logits) and the router's score functions. */
+enum { FP8MOE_BF16 = 0, FP8MOE_FP32 = 1 };
+enum { FP8MOE_SCORE_SOFTMAX = 0, FP8MOE_SCORE_SIGMOID = 1 };
+
 /* Largest number of groups (experts) a call with offsets accepts. */
 enum { FP8MOE_MAX_GROUPS = 1024 };
 
@@ -443,6 +448,138 @@ enum { FP8MOE_ROUTE_STATIC_SCRATCH_BYTES = 1 << 20 };
 fp8moe_status fp8moe_route_permute_noalloc(const void* x, int64_t T, int64_t H, const int32_t* topk_idx,
                                            const float* topk_w, int64_t k, int64_t E, void* a, int32_t* offs,
                                            int32_t* row_of, fp8moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Residual addition + RMS norm with an 8-bit output: what stands before the
+ * router and the expert products of a layer.
+ *
+ * Forward, per row of H elements, in fp32 with every output rounded once:
+ *   a = x + residual, rstd = 1 / sqrt(mean(a^2) + eps), y = a * rstd * w.
+ * x        [T, H] bf16, row stride ldx (>= H, a multiple of 8)
+ * residual [T, H] bf16, row stride ldr, or NULL (then ldr is ignored and h
+ *          must be NULL: it would be x)
+ * w        [H] of weight_type (FP8MOE_BF16 or FP8MOE_FP32)
+ * h        [T, H] bf16(a), dense, or NULL; may be x or residual itself where
+ *          that is dense (updated in place)
+ * y        [T, H] bf16(y), dense, or NULL
+ * rstd     [T] fp32 or NULL (the backward reads it)
+ * q, scale the 8-bit output, or both NULL.  The codes come from the fp32 y.
+ *          recipe FP8MOE_MXFP8 (kind e4m3fn, H % 32 == 0): q [T, H] and e8m0
+ *          bytes by the rule of fp8moe_mxfp8_quantize_dim0, in scale_layout
+ *          FP8MOE_SCALES_ROWMAJOR [T, H/32] or FP8MOE_NO_GROUPS (128x4 tiles
+ *          of one matrix, fp8moe_swizzled_scales_bytes(1, T, H/32, 0,
+ *          FP8MOE_NO_GROUPS) bytes, padding written as 0; with room for
+ *          GROUP_ROWS of one group it is the A operand of a one-group GEMM).
+ *          recipe FP8MOE_ROWWISE (either kind, H % 16 == 0): q [T, H] and
+ *          scale fp32 [T] by the rule of fp8moe_quantize_rowwise.
+ *          scale_layout is read for MXFP8 alone.
+ * At least one of h, y, rstd, q is given.  H % 8 == 0, H <= 2^20, eps >= 0
+ * and finite.  Rows of zeros give y = 0 (eps > 0).
+ *
+ * Backward (xh = h * rstd, g = dy * w):
+ *   dx = rstd * (g - xh * mean(g * xh)) + dh,  dw = sum over rows of dy * xh.
+ * dy, h [T, H] bf16 dense (h as the forward wrote it, or x), rstd [T] and w
+ * as in the forward; dh [T, H] bf16 or NULL: the gradient that reaches h by
+ * the residual stream.  dx [T, H] bf16, the gradient of x and of residual;
+ * may be dy or dh itself.  dw [H] fp32 (T == 0: zero).  The codes' rounding
+ * counts as the identity.  workspace: caller-owned,
+ * fp8moe_add_rmsnorm_bwd_workspace_bytes(T, H) bytes, 16-byte aligned; its
+ * contents are of no use after the call.  Row sums and dw are added in a
+ * fixed order: results do not change from run to run.
+ * ------------------------------------------------------------------------ */
+fp8moe_status fp8moe_add_rmsnorm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* w,
+                                     int weight_type, int64_t T, int64_t H, float eps, void* h, void* y, float* rstd,
+                                     int recipe, int kind, void* q, void* scale, int scale_layout,
+                                     fp8moe_stream_t stream);
+int64_t fp8moe_add_rmsnorm_bwd_workspace_bytes(int64_t T, int64_t H);
+fp8moe_status fp8moe_add_rmsnorm_bwd(const void* dy, const void* h, const float* rstd, const void* w,
+                                     int weight_type, const void* dh, int64_t T, int64_t H, void* dx, float* dw,
+                                     void* workspace, int64_t workspace_bytes, fp8moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The router: scores, top-k choice, weights, per-expert counts and balance
+ * loss of T tokens over E experts, and its gradient.
+ *
+ * logits  [T, E] of logits_type (FP8MOE_BF16 or FP8MOE_FP32), row stride ldl
+ *         (>= E); an expert at -inf is masked out for that token
+ * score   FP8MOE_SCORE_SOFTMAX: s = softmax(logits), FP8MOE_SCORE_SIGMOID:
+ *         s = sigmoid(logits)
+ * bias    [E] fp32 or NULL, added to s for the choice alone
+ * token_mask [T] bytes or NULL: 0 marks a row that is no token.  It counts
+ *         as one whose logits are all -inf; its logits are not read.
+ * The k experts with the largest keys are chosen in descending order, ties
+ * to the lowest id; the key is the logit, or s + bias (fp32) where a bias is
+ * given.  Masked experts (and NaN logits) come last, so every token has k
+ * different valid ids; a masked one has weight 0 and is not counted.
+ * topk_idx [T, k] int32, topk_w [T, k] fp32: s of the chosen experts, divided
+ *         by their sum when renormalize is not 0 (a zero sum leaves zeros),
+ *         times route_scale: the arguments of fp8moe_route_permute / _unpermute.
+ * counts  [E + 1] int32: how often each expert was chosen, then the number
+ *         of tokens N
+ * prob_sum [E] fp32: P_e, the sum over the tokens of p = s (softmax) or
+ *         s / sum(s) (sigmoid)
+ * balance_loss [1] fp32: E / (k N^2) * sum_e counts_e P_e (1 when balanced;
+ *         0 without tokens)
+ * counts, prob_sum and balance_loss are all given or all NULL; with them a
+ * caller-owned workspace of fp8moe_router_workspace_bytes(T, E) bytes
+ * (4-byte aligned), of no use after the call.
+ * 1 <= E <= 1024, 1 <= k <= min(E, 32), T <= 2^30 / k.  Sums have a fixed order.
+ *
+ * Backward: dtopk_w [T, k] fp32 or NULL and dloss [1] fp32 (device) or NULL,
+ * not both NULL -> dlogits [T, E] dense, of logits_type.  The counts (NULL
+ * without dloss) and the choice are constants.  Masked tokens and experts get
+ * 0.  The other arguments as the forward's; topk_idx and counts are its
+ * outputs (ids outside [0, E) are skipped).
+ *
+ * fp8moe_route_weight_grad: the gradient of the weights of
+ * fp8moe_route_unpermute: dw[t, j] = sum_n dout[t, n] * y[row_of[t, j], n],
+ * dout [T, N] bf16, y [rows, N] bf16, row_of [T, k] int32 (negative: 0),
+ * dw [T, k] fp32.  N % 8 == 0; dout, y 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+int64_t fp8moe_router_workspace_bytes(int64_t T, int64_t E);
+fp8moe_status fp8moe_router_fwd(const void* logits, int logits_type, int64_t T, int64_t E, int64_t ldl, int64_t k,
+                                int score, int renormalize, float route_scale, const float* bias,
+                                const uint8_t* token_mask, int32_t* topk_idx, float* topk_w, int32_t* counts,
+                                float* prob_sum, float* balance_loss, void* workspace, int64_t workspace_bytes,
+                                fp8moe_stream_t stream);
+fp8moe_status fp8moe_router_bwd(const void* logits, int logits_type, int64_t T, int64_t E, int64_t ldl, int64_t k,
+                                int score, int renormalize, float route_scale, const uint8_t* token_mask,
+                                const int32_t* topk_idx, const int32_t* counts, const float* dtopk_w,
+                                const float* dloss, void* dlogits, fp8moe_stream_t stream);
+fp8moe_status fp8moe_route_weight_grad(const void* dout, const void* y, const int32_t* row_of, int64_t T, int64_t N,
+                                       int64_t k, float* dw, fp8moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Gated activation between the two expert products, with MXFP8 output along
+ * both dimensions in the layouts the grouped GEMMs read.
+ *
+ * Forward:  h [M, 2F] bf16, row stride ldh (>= 2F, a multiple of 8): gate in
+ *   columns [0, F), up in [F, 2F) -> a = gate * sigmoid(gate) * up [M, F].
+ * Backward: dout [M, F] bf16 dense and the same h -> dh [M, 2F]: the gradient
+ *   of gate, then that of up.
+ * The result (W = F or 2F columns) goes to any of
+ *   out / dh bf16 [M, W], dense;
+ *   q0 [M, W] e4m3fn and s0 (scales of [M, W/32]): blocks along the rows, the
+ *     operand of the product that contracts over W; s0_layout
+ *     FP8MOE_SCALES_ROWMAJOR, FP8MOE_NO_GROUPS or FP8MOE_GROUP_ROWS;
+ *   q1 [W, M] e4m3fn and s1 (scales of [W, M/32]): blocks along the columns,
+ *     transposed, the operand of wgrad; s1_layout FP8MOE_SCALES_ROWMAJOR,
+ *     FP8MOE_NO_GROUPS or FP8MOE_GROUP_COLS; M % 32 == 0.
+ * NULL outputs are skipped; at least one is given.  The codes come from the
+ * fp32 result by the rules of fp8moe_mxfp8_quantize_dim0 / dim1; the padding
+ * bytes of swizzled scales are not written, as fp8moe_mxfp8_quantize_dual.
+ * A grouped layout needs offs [E] (device): cumulative ends, multiples of
+ * 32, offs[E-1] = M; invalid offsets set FP8MOE_ERR_DEVICE_OFFSETS and write
+ * nothing.  Without one offs is not read.  F % 32 == 0, M <= 2^30, 1 <= E <=
+ * FP8MOE_MAX_GROUPS; every pointer 16-byte aligned (offs 4).  Outputs do not
+ * overlap inputs.
+ * ------------------------------------------------------------------------ */
+fp8moe_status fp8moe_swiglu_fwd(const void* h, int64_t ldh, int64_t M, int64_t F, const int32_t* offs, int64_t E,
+                                void* out, void* q0, uint8_t* s0, int s0_layout, void* q1, uint8_t* s1,
+                                int s1_layout, fp8moe_stream_t stream);
+fp8moe_status fp8moe_swiglu_bwd(const void* dout, const void* h, int64_t ldh, int64_t M, int64_t F,
+                                const int32_t* offs, int64_t E, void* dh, void* q0, uint8_t* s0, int s0_layout,
+                                void* q1, uint8_t* s1, int s1_layout, fp8moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Device status.  After the work already queued on `stream`, takes the

@@ -11,6 +11,7 @@ device.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -32,17 +33,22 @@ __all__ = [
     "fp8moe_mxfp8_moe_workspace_bytes", "fp8moe_mxfp8_moe_fwd", "fp8moe_mxfp8_moe_bwd",
     "fp8moe_quantize_blockwise_rows", "fp8moe_quantize_blockwise_weight", "fp8moe_blockwise_token_blocks",
     "fp8moe_quantize_blockwise_tokens",
+    "SCORE_SOFTMAX", "SCORE_SIGMOID",
+    "fp8moe_add_rmsnorm_fwd", "fp8moe_add_rmsnorm_bwd", "fp8moe_add_rmsnorm_bwd_workspace_bytes",
+    "fp8moe_router_fwd", "fp8moe_router_bwd", "fp8moe_router_workspace_bytes", "fp8moe_route_weight_grad",
+    "fp8moe_swiglu_fwd", "fp8moe_swiglu_bwd",
 ]
 
 E4M3FN, E4M3FNUZ = 0, 1
 ROWWISE, MXFP8, TENSORWISE, BLOCKWISE = 0, 1, 2, 3
 SCALES_ROWMAJOR, NO_GROUPS, GROUP_ROWS, GROUP_COLS = -2, -1, 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 ROUTE_STATIC_SCRATCH_BYTES = 1 << 20   # the static scratch of fp8moe_route_permute_noalloc
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(HERE, "libfp8moe.so")
 
-_i64, _i32, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
+_i64, _i32, _vp, _f32 = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_float
 
 # name -> (restype, argtypes), mirroring include/fp8moe.h
 SYMBOLS = {
@@ -73,6 +79,18 @@ SYMBOLS = {
     "fp8moe_mxfp8_moe_workspace_bytes": (_i64, [_i64, _i64, _i64, _i64]),
     "fp8moe_mxfp8_moe_fwd": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp]),
     "fp8moe_mxfp8_moe_bwd": (_i32, [_vp, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "fp8moe_add_rmsnorm_fwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i32, _i64, _i64, _f32, _vp, _vp, _vp, _i32, _i32, _vp,
+                                      _vp, _i32, _vp]),
+    "fp8moe_add_rmsnorm_bwd_workspace_bytes": (_i64, [_i64, _i64]),
+    "fp8moe_add_rmsnorm_bwd": (_i32, [_vp, _vp, _vp, _vp, _i32, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp]),
+    "fp8moe_router_workspace_bytes": (_i64, [_i64, _i64]),
+    "fp8moe_router_fwd": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                 _vp, _i64, _vp]),
+    "fp8moe_router_bwd": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                 _vp]),
+    "fp8moe_route_weight_grad": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]),
+    "fp8moe_swiglu_fwd": (_i32, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp]),
+    "fp8moe_swiglu_bwd": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp]),
     "fp8moe_get_device_status": (_i32, [_vp, ctypes.POINTER(ctypes.c_int32)]),
     "fp8moe_testing_stall_next_gemm": (_i32, []),
     "fp8moe_testing_stall_next_tensorwise": (_i32, []),
@@ -140,6 +158,38 @@ def _check(fn: str, code: int):
 
 def _empty(shape, dtype, like):
     return _torch().empty(shape, dtype=dtype, device=like.device)
+
+
+def _want(fn: str, t, dtype, shape, contiguous: bool = True) -> None:
+    """Refuses (status 1) an argument of another type, shape or device, or one
+    whose memory order the call does not take.  ``dtype``: one or a tuple;
+    ``None`` in ``shape`` stands for any size."""
+    if t is None:
+        return
+    ok = t.is_cuda and (t.dtype in dtype if isinstance(dtype, tuple) else t.dtype == dtype)
+    ok = ok and t.dim() == len(shape) and all(w is None or w == n for w, n in zip(shape, t.shape))
+    if not ok or (contiguous and not t.is_contiguous()) or t.device.index != _torch().cuda.current_device():
+        raise Fp8MoeError(fn, 1)
+
+
+def _row_stride(fn: str, t) -> int:
+    """Row stride of a [R, C] argument whose rows are dense."""
+    R, C = t.shape
+    if C > 1 and t.stride(1) != 1:
+        raise Fp8MoeError(fn, 1)
+    return t.stride(0) if R > 1 else C
+
+
+def _on_stream(fn):
+    """Gives ``fn`` a ``stream`` argument: the whole call, its allocations
+    among it, runs with that stream as the current one."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        with _torch().cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return call
 
 
 def _u8(t):
@@ -508,6 +558,249 @@ def fp8moe_mxfp8_moe_bwd(dy, offs, workspace, K: int, need_da: bool = True, need
         _ptr(dy), _ptr(offs), E, M, N, K, _ptr(workspace), workspace.numel(), _ptr(da), _ptr(dw),
         _stream(stream)))
     return da, dw
+
+
+@_on_stream
+def fp8moe_add_rmsnorm_fwd(x, weight, residual=None, eps: float = 1e-6, recipe: Optional[int] = None,
+                           kind: int = E4M3FN, scale_layout: int = SCALES_ROWMAJOR, need_y: bool = True,
+                           need_rstd: bool = True, h=None, y=None, rstd=None, q=None, scale=None):
+    """y = (x + residual) * rsqrt(mean((x + residual)^2) + eps) * weight, rowwise.
+
+    x, residual [T, H] bf16 (row strides may exceed H), weight [H] bf16 or
+    fp32.  Returns (h, y, rstd, q, scale): h = bf16(x + residual) (None
+    without residual), y bf16, rstd fp32 [T], and the 8-bit output of
+    ``recipe``: MXFP8 codes with scales in ``scale_layout`` (SCALES_ROWMAJOR
+    or NO_GROUPS) or ROWWISE codes with fp32 scales [T]; None for what is not
+    asked for.  Outputs are allocated unless given; h may be x or residual."""
+    fn = "fp8moe_add_rmsnorm_fwd"
+    torch = _torch()
+    bf16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    _want(fn, x, bf16, (None, None), False)
+    T, H = x.shape
+    _want(fn, residual, bf16, (T, H), False)
+    _want(fn, weight, (bf16, f32), (H,))
+    if residual is None:
+        if h is not None:
+            raise Fp8MoeError(fn, 1)
+    elif h is None:
+        h = _empty((T, H), bf16, x)
+    y = (_empty((T, H), bf16, x) if y is None else y) if need_y else None
+    rstd = (_empty((T,), f32, x) if rstd is None else rstd) if need_rstd else None
+    tiled = False
+    if recipe is None:
+        q = scale = None
+    else:
+        tiled = recipe == MXFP8 and scale_layout != SCALES_ROWMAJOR
+        q = _empty((T, H), u8, x) if q is None else q
+        if scale is None:
+            if tiled:
+                # room for the tiles of one group, whose layout is the same:
+                # the A operand of a one-group grouped GEMM
+                n = fp8moe_swizzled_scales_bytes(1, T, H // 32, 1, GROUP_ROWS)
+                scale = torch.zeros(max(n, 0), dtype=u8, device=x.device)
+            else:
+                scale = _empty((T, H // 32), u8, x) if recipe == MXFP8 else _empty((T,), f32, x)
+        _want(fn, q, u8, (T, H))
+        if tiled:
+            _want(fn, scale, u8, (None,))
+            if scale.numel() < fp8moe_swizzled_scales_bytes(1, T, H // 32):
+                raise Fp8MoeError(fn, 1)
+        elif recipe == MXFP8:
+            _want(fn, scale, u8, (T, H // 32))
+        else:
+            _want(fn, scale, f32, (T,))
+    _want(fn, h, bf16, (T, H))
+    _want(fn, y, bf16, (T, H))
+    _want(fn, rstd, f32, (T,))
+    _check(fn, _lib_raw().fp8moe_add_rmsnorm_fwd(
+        _ptr(x), _row_stride(fn, x), _ptr(residual), 0 if residual is None else _row_stride(fn, residual),
+        _ptr(weight), int(weight.dtype == f32), T, H, eps, _ptr(h), _ptr(y), _ptr(rstd),
+        ROWWISE if recipe is None else recipe, kind, _ptr(q), _ptr(scale), scale_layout, _stream(None)))
+    return h, y, rstd, q, scale
+
+
+def fp8moe_add_rmsnorm_bwd_workspace_bytes(T: int, H: int) -> int:
+    return int(_lib_raw().fp8moe_add_rmsnorm_bwd_workspace_bytes(T, H))
+
+
+@_on_stream
+def fp8moe_add_rmsnorm_bwd(dy, h, rstd, weight, dh=None, dx=None, dweight=None, workspace=None):
+    """Backward of fp8moe_add_rmsnorm_fwd: dy, h [T, H] bf16, rstd [T] fp32,
+    weight as in the forward, dh [T, H] bf16 the gradient that reaches h
+    otherwise -> (dx [T, H] bf16, the gradient of x and of residual; dweight
+    [H] fp32)."""
+    fn = "fp8moe_add_rmsnorm_bwd"
+    torch = _torch()
+    bf16, f32 = torch.bfloat16, torch.float32
+    _want(fn, dy, bf16, (None, None))
+    T, H = dy.shape
+    _want(fn, h, bf16, (T, H))
+    _want(fn, rstd, f32, (T,))
+    _want(fn, weight, (bf16, f32), (H,))
+    _want(fn, dh, bf16, (T, H))
+    dx = _empty((T, H), bf16, dy) if dx is None else dx
+    dweight = _empty((H,), f32, dy) if dweight is None else dweight
+    _want(fn, dx, bf16, (T, H))
+    _want(fn, dweight, f32, (H,))
+    if workspace is None:
+        workspace = _empty((max(fp8moe_add_rmsnorm_bwd_workspace_bytes(T, H), 0),), torch.uint8, dy)
+    _check(fn, _lib_raw().fp8moe_add_rmsnorm_bwd(
+        _ptr(dy), _ptr(h), _ptr(rstd), _ptr(weight), int(weight.dtype == f32), _ptr(dh), T, H, _ptr(dx),
+        _ptr(dweight), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(None)))
+    return dx, dweight
+
+
+def fp8moe_router_workspace_bytes(T: int, E: int) -> int:
+    return int(_lib_raw().fp8moe_router_workspace_bytes(T, E))
+
+
+@_on_stream
+def fp8moe_router_fwd(logits, k: int, score: int = SCORE_SOFTMAX, renormalize: bool = True, route_scale: float = 1.0,
+                      bias=None, token_mask=None, need_balance: bool = True, topk_idx=None, topk_w=None,
+                      counts=None, prob_sum=None, balance_loss=None, workspace=None):
+    """logits [T, E] bf16 or fp32 (row stride may exceed E), bias [E] fp32 (for
+    the choice alone), token_mask [T] uint8 or bool (0: no token).
+
+    Returns (topk_idx [T, k] int32, topk_w [T, k] fp32, counts [E + 1] int32
+    (per expert, then the number of tokens), prob_sum [E] fp32, balance_loss
+    [1] fp32); the last three are None without ``need_balance``."""
+    fn = "fp8moe_router_fwd"
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    _want(fn, logits, (torch.bfloat16, f32), (None, None), False)
+    T, E = logits.shape
+    _want(fn, bias, f32, (E,))
+    _want(fn, token_mask, (torch.uint8, torch.bool), (T,))
+    topk_idx = _empty((T, k), i32, logits) if topk_idx is None else topk_idx
+    topk_w = _empty((T, k), f32, logits) if topk_w is None else topk_w
+    nbytes = 0
+    if need_balance:
+        counts = _empty((E + 1,), i32, logits) if counts is None else counts
+        prob_sum = _empty((E,), f32, logits) if prob_sum is None else prob_sum
+        balance_loss = _empty((1,), f32, logits) if balance_loss is None else balance_loss
+        if workspace is None:
+            workspace = _empty((max(fp8moe_router_workspace_bytes(T, E), 0),), torch.uint8, logits)
+        nbytes = workspace.numel() * workspace.element_size()
+    else:
+        counts = prob_sum = balance_loss = workspace = None
+    _want(fn, topk_idx, i32, (T, k))
+    _want(fn, topk_w, f32, (T, k))
+    _want(fn, counts, i32, (E + 1,))
+    _want(fn, prob_sum, f32, (E,))
+    _want(fn, balance_loss, f32, (1,))
+    _check(fn, _lib_raw().fp8moe_router_fwd(
+        _ptr(logits), int(logits.dtype == f32), T, E, _row_stride(fn, logits), k, score, int(renormalize),
+        route_scale, _ptr(bias), _ptr(token_mask), _ptr(topk_idx), _ptr(topk_w), _ptr(counts), _ptr(prob_sum),
+        _ptr(balance_loss), _ptr(workspace), nbytes, _stream(None)))
+    return topk_idx, topk_w, counts, prob_sum, balance_loss
+
+
+@_on_stream
+def fp8moe_router_bwd(logits, topk_idx, counts=None, dtopk_w=None, dloss=None, score: int = SCORE_SOFTMAX,
+                      renormalize: bool = True, route_scale: float = 1.0, token_mask=None, dlogits=None):
+    """Gradient of fp8moe_router_fwd: dtopk_w [T, k] fp32 and / or dloss [1]
+    fp32 (with the forward's counts) -> dlogits [T, E] of the logits' type."""
+    fn = "fp8moe_router_bwd"
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    _want(fn, logits, (torch.bfloat16, f32), (None, None), False)
+    T, E = logits.shape
+    _want(fn, topk_idx, i32, (T, None))
+    k = topk_idx.shape[1]
+    _want(fn, counts, i32, (E + 1,))
+    _want(fn, dtopk_w, f32, (T, k))
+    _want(fn, dloss, f32, (1,))
+    _want(fn, token_mask, (torch.uint8, torch.bool), (T,))
+    dlogits = _empty((T, E), logits.dtype, logits) if dlogits is None else dlogits
+    _want(fn, dlogits, logits.dtype, (T, E))
+    _check(fn, _lib_raw().fp8moe_router_bwd(
+        _ptr(logits), int(logits.dtype == f32), T, E, _row_stride(fn, logits), k, score, int(renormalize),
+        route_scale, _ptr(token_mask), _ptr(topk_idx), _ptr(counts), _ptr(dtopk_w), _ptr(dloss), _ptr(dlogits),
+        _stream(None)))
+    return dlogits
+
+
+@_on_stream
+def fp8moe_route_weight_grad(dout, y, row_of, dw=None):
+    """Gradient of fp8moe_route_unpermute's weights: dout [T, N] bf16, y
+    [rows, N] bf16, row_of [T, k] int32 -> dw [T, k] fp32."""
+    fn = "fp8moe_route_weight_grad"
+    torch = _torch()
+    _want(fn, dout, torch.bfloat16, (None, None))
+    T, N = dout.shape
+    _want(fn, y, torch.bfloat16, (None, N))
+    _want(fn, row_of, torch.int32, (T, None))
+    k = row_of.shape[1]
+    dw = _empty((T, k), torch.float32, dout) if dw is None else dw
+    _want(fn, dw, torch.float32, (T, k))
+    _check(fn, _lib_raw().fp8moe_route_weight_grad(
+        _ptr(dout), _ptr(y), _ptr(row_of), T, N, k, _ptr(dw), _stream(None)))
+    return dw
+
+
+def _swiglu(fn, dout, h, offs, s0_layout, s1_layout, need_out, dim0, dim1, out, q0, s0, q1, s1):
+    torch = _torch()
+    bf16, u8 = torch.bfloat16, torch.uint8
+    _want(fn, h, bf16, (None, None), False)
+    M, W2 = h.shape
+    F = W2 // 2
+    if W2 != 2 * F:
+        raise Fp8MoeError(fn, 1)
+    _want(fn, dout, bf16, (M, F))
+    _want(fn, offs, torch.int32, (None,))
+    W = F if dout is None else W2
+    E = offs.numel() if offs is not None else 0
+    out = (_empty((M, W), bf16, h) if out is None else out) if need_out else None
+    if dim0:
+        q0 = _empty((M, W), u8, h) if q0 is None else q0
+        s0 = _scale_buffer(s0_layout, 1, M, W // 32, E, h) if s0 is None else s0
+    else:
+        q0 = s0 = None
+    if dim1:
+        q1 = _empty((W, M), u8, h) if q1 is None else q1
+        s1 = _scale_buffer(s1_layout, 1, W, M // 32, E, h) if s1 is None else s1
+    else:
+        q1 = s1 = None
+    _want(fn, out, bf16, (M, W))
+    _want(fn, q0, u8, (M, W))
+    _want(fn, q1, u8, (W, M))
+    for s, layout, rows, cols in ((s0, s0_layout, M, W // 32), (s1, s1_layout, W, M // 32)):
+        if s is None:
+            continue
+        need = rows * cols if layout == SCALES_ROWMAJOR else fp8moe_swizzled_scales_bytes(1, rows, cols, E, layout)
+        if s.dtype != u8 or not s.is_cuda or not s.is_contiguous() or s.numel() < need:
+            raise Fp8MoeError(fn, 1)
+    args = (_ptr(h), _row_stride(fn, h), M, F, _ptr(offs), E, _ptr(out), _ptr(q0), _ptr(s0), s0_layout, _ptr(q1),
+            _ptr(s1), s1_layout, _stream(None))
+    f = getattr(_lib_raw(), fn)
+    _check(fn, f(*args) if dout is None else f(_ptr(dout), *args))
+    return out, q0, s0, q1, s1
+
+
+@_on_stream
+def fp8moe_swiglu_fwd(h, offs=None, s0_layout: int = NO_GROUPS, s1_layout: int = NO_GROUPS, need_out: bool = True,
+                      dim0: bool = False, dim1: bool = False, out=None, q0=None, s0=None, q1=None, s1=None):
+    """a = gate * sigmoid(gate) * up of h [M, 2F] bf16 (gate | up; the row
+    stride may exceed 2F).
+
+    Returns (out bf16 [M, F], q0 [M, F], s0, q1 [F, M], s1): the MXFP8 codes
+    along the rows (``dim0``) and along the columns, transposed (``dim1``),
+    with scales in the layouts of fp8moe_mxfp8_quantize_dual; None for what
+    is not asked for.  Scale buffers are allocated zero-filled when not given."""
+    return _swiglu("fp8moe_swiglu_fwd", None, h, offs, s0_layout, s1_layout, need_out, dim0, dim1, out, q0, s0, q1,
+                   s1)
+
+
+@_on_stream
+def fp8moe_swiglu_bwd(dout, h, offs=None, s0_layout: int = NO_GROUPS, s1_layout: int = NO_GROUPS,
+                      need_dh: bool = True, dim0: bool = False, dim1: bool = False, out=None, q0=None, s0=None,
+                      q1=None, s1=None):
+    """Backward of fp8moe_swiglu_fwd: dout [M, F] bf16 and the forward's h ->
+    (dh bf16 [M, 2F], q0 [M, 2F], s0, q1 [2F, M], s1), as the forward."""
+    if dout is None:
+        raise Fp8MoeError("fp8moe_swiglu_bwd", 1)
+    return _swiglu("fp8moe_swiglu_bwd", dout, h, offs, s0_layout, s1_layout, need_dh, dim0, dim1, out, q0, s0, q1,
+                   s1)
 
 
 def fp8moe_get_device_status(stream=None) -> int:

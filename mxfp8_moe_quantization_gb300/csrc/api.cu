@@ -1,10 +1,12 @@
 // C-ABI entry points of libfp8moe: argument checks on the host, then launches
 // on the caller's stream.  See include/fp8moe.h for the contract of each call.
+#include <cmath>
 #include <mutex>
 
 #include "common.cuh"
 #include "gemm.h"
 #include "launch.h"
+#include "moe_ops.h"
 
 // Sticky device status word (static device memory: the library allocates
 // nothing).  Kernels receive its address; fp8moe_get_device_status takes it
@@ -458,6 +460,191 @@ fp8moe_status fp8moe_route_unpermute(const void* y, int64_t T, int64_t N, const 
   fp8moe_status st = device_info(&d);
   if (st) return st;
   return cuda_result(fp8moe::launch_route_unpermute(y, N, row_of, topk_w, T, k, out, (cudaStream_t)stream));
+}
+
+fp8moe_status fp8moe_add_rmsnorm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* w,
+                                     int weight_type, int64_t T, int64_t H, float eps, void* h, void* y, float* rstd,
+                                     int recipe, int kind, void* q, void* scale, int scale_layout,
+                                     fp8moe_stream_t stream) {
+  if (T < 0 || H < 1 || T > INT32_MAX - 128 || H > ((int64_t)1 << 20) || ldx < H || (residual && ldr < H))
+    return FP8MOE_ERR_INVALID_ARG;
+  if ((weight_type != FP8MOE_BF16 && weight_type != FP8MOE_FP32) || !(eps >= 0.0f) || std::isinf(eps))
+    return FP8MOE_ERR_INVALID_ARG;
+  if (H % 8 || ldx % 8 || (residual && ldr % 8)) return FP8MOE_ERR_ALIGNMENT;
+  if (T == 0) return FP8MOE_OK;
+  if ((q == nullptr) != (scale == nullptr) || (h && !residual) || !(h || y || rstd || q)) return FP8MOE_ERR_INVALID_ARG;
+  const bool mx = q && recipe == FP8MOE_MXFP8;
+  if (q) {
+    if (!valid_kind(kind)) return FP8MOE_ERR_INVALID_ARG;
+    if (recipe != FP8MOE_MXFP8 && recipe != FP8MOE_ROWWISE) return FP8MOE_ERR_UNSUPPORTED;
+    if (mx && kind != FP8MOE_E4M3FN) return FP8MOE_ERR_UNSUPPORTED;
+    if (mx && scale_layout != FP8MOE_SCALES_ROWMAJOR && scale_layout != FP8MOE_NO_GROUPS)
+      return FP8MOE_ERR_INVALID_ARG;
+    if (H % (mx ? 32 : 16)) return FP8MOE_ERR_ALIGNMENT;
+  }
+  if (!x || !w) return FP8MOE_ERR_INVALID_ARG;
+  if (!al16(x) || !al16(residual) || !al16(w) || !al16(h) || !al16(y) || !al16(q) || ((uintptr_t)rstd & 3) ||
+      (q && !mx && ((uintptr_t)scale & 3)))
+    return FP8MOE_ERR_ALIGNMENT;
+  return cuda_result(fp8moe::launch_norm_fwd(x, ldx, residual, ldr, w, weight_type == FP8MOE_FP32, T, H, eps, h, y,
+                                             rstd, recipe, kind, q, scale, scale_layout, (cudaStream_t)stream));
+}
+
+int64_t fp8moe_add_rmsnorm_bwd_workspace_bytes(int64_t T, int64_t H) {
+  if (T < 0 || H < 1) return -1;
+  return (T < fp8moe::NORM_BWD_PARTS ? T : fp8moe::NORM_BWD_PARTS) * H * (int64_t)sizeof(float);
+}
+
+fp8moe_status fp8moe_add_rmsnorm_bwd(const void* dy, const void* h, const float* rstd, const void* w,
+                                     int weight_type, const void* dh, int64_t T, int64_t H, void* dx, float* dw,
+                                     void* workspace, int64_t workspace_bytes, fp8moe_stream_t stream) {
+  if (T < 0 || H < 1 || H > ((int64_t)1 << 20)) return FP8MOE_ERR_INVALID_ARG;
+  if (weight_type != FP8MOE_BF16 && weight_type != FP8MOE_FP32) return FP8MOE_ERR_INVALID_ARG;
+  if (H % 8) return FP8MOE_ERR_ALIGNMENT;
+  if (!dw || (T > 0 && (!dy || !h || !rstd || !w || !dx || !workspace))) return FP8MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < fp8moe_add_rmsnorm_bwd_workspace_bytes(T, H)) return FP8MOE_ERR_INVALID_ARG;
+  if (!al16(dy) || !al16(h) || !al16(w) || !al16(dh) || !al16(dx) || !al16(workspace) ||
+      (((uintptr_t)rstd | (uintptr_t)dw) & 3))
+    return FP8MOE_ERR_ALIGNMENT;
+  DevInfo* d;
+  fp8moe_status st = device_info(&d);
+  if (st) return st;
+  return cuda_result(fp8moe::launch_norm_bwd(dy, h, rstd, w, weight_type == FP8MOE_FP32, dh, T, H, dx, dw, workspace,
+                                             d->num_sms, (cudaStream_t)stream));
+}
+
+int64_t fp8moe_router_workspace_bytes(int64_t T, int64_t E) {
+  if (T < 0 || E < 1) return -1;
+  return (T < fp8moe::ROUTER_MAX_PARTS ? T : fp8moe::ROUTER_MAX_PARTS) * (2 * E + 1) * (int64_t)sizeof(float);
+}
+
+// the checks that both directions share
+static fp8moe_status router_check(const void* logits, int logits_type, int64_t T, int64_t E, int64_t ldl, int64_t k,
+                                  int score) {
+  if (T < 0 || E < 1 || E > fp8moe::ROUTER_MAX_E || ldl < E || k < 1 || k > E || k > fp8moe::ROUTER_MAX_K ||
+      T > ((int64_t)1 << 30) / k)
+    return FP8MOE_ERR_INVALID_ARG;
+  if (logits_type != FP8MOE_BF16 && logits_type != FP8MOE_FP32) return FP8MOE_ERR_INVALID_ARG;
+  if (score != FP8MOE_SCORE_SOFTMAX && score != FP8MOE_SCORE_SIGMOID) return FP8MOE_ERR_INVALID_ARG;
+  if (T > 0 && !logits) return FP8MOE_ERR_INVALID_ARG;
+  if ((uintptr_t)logits & (logits_type == FP8MOE_FP32 ? 3 : 1)) return FP8MOE_ERR_ALIGNMENT;
+  return FP8MOE_OK;
+}
+
+fp8moe_status fp8moe_router_fwd(const void* logits, int logits_type, int64_t T, int64_t E, int64_t ldl, int64_t k,
+                                int score, int renormalize, float route_scale, const float* bias,
+                                const uint8_t* token_mask, int32_t* topk_idx, float* topk_w, int32_t* counts,
+                                float* prob_sum, float* balance_loss, void* workspace, int64_t workspace_bytes,
+                                fp8moe_stream_t stream) {
+  fp8moe_status st = router_check(logits, logits_type, T, E, ldl, k, score);
+  if (st) return st;
+  if (T > 0 && (!topk_idx || !topk_w)) return FP8MOE_ERR_INVALID_ARG;
+  const int sums = (counts != nullptr) + (prob_sum != nullptr) + (balance_loss != nullptr);
+  if (sums != 0 && sums != 3) return FP8MOE_ERR_INVALID_ARG;
+  if (sums && T > 0 && (!workspace || workspace_bytes < fp8moe_router_workspace_bytes(T, E)))
+    return FP8MOE_ERR_INVALID_ARG;
+  if (((uintptr_t)bias | (uintptr_t)topk_idx | (uintptr_t)topk_w | (uintptr_t)counts | (uintptr_t)prob_sum |
+       (uintptr_t)balance_loss | (uintptr_t)workspace) & 3)
+    return FP8MOE_ERR_ALIGNMENT;
+  if (T == 0 && !sums) return FP8MOE_OK;
+  DevInfo* d;
+  if ((st = device_info(&d))) return st;
+  fp8moe::RouterArgs a{};
+  a.logits = logits;
+  a.bf16 = logits_type == FP8MOE_BF16;
+  a.T = T, a.ld = ldl, a.E = (int)E, a.k = (int)k;
+  a.score = score, a.renorm = renormalize != 0, a.route_scale = route_scale;
+  a.bias = bias, a.mask = token_mask;
+  a.idx = topk_idx, a.w = topk_w;
+  a.counts = counts, a.psum = prob_sum, a.loss = balance_loss, a.workspace = workspace;
+  return cuda_result(fp8moe::launch_router_fwd(a, d->num_sms, (cudaStream_t)stream));
+}
+
+fp8moe_status fp8moe_router_bwd(const void* logits, int logits_type, int64_t T, int64_t E, int64_t ldl, int64_t k,
+                                int score, int renormalize, float route_scale, const uint8_t* token_mask,
+                                const int32_t* topk_idx, const int32_t* counts, const float* dtopk_w,
+                                const float* dloss, void* dlogits, fp8moe_stream_t stream) {
+  fp8moe_status st = router_check(logits, logits_type, T, E, ldl, k, score);
+  if (st) return st;
+  if (!dtopk_w && !dloss) return FP8MOE_ERR_INVALID_ARG;
+  if (T == 0) return FP8MOE_OK;
+  if (!dlogits || (dtopk_w && !topk_idx) || (dloss && !counts)) return FP8MOE_ERR_INVALID_ARG;
+  if ((((uintptr_t)topk_idx | (uintptr_t)counts | (uintptr_t)dtopk_w | (uintptr_t)dloss) & 3) ||
+      ((uintptr_t)dlogits & (logits_type == FP8MOE_FP32 ? 3 : 1)))
+    return FP8MOE_ERR_ALIGNMENT;
+  DevInfo* d;
+  if ((st = device_info(&d))) return st;
+  fp8moe::RouterArgs a{};
+  a.logits = logits;
+  a.bf16 = logits_type == FP8MOE_BF16;
+  a.T = T, a.ld = ldl, a.E = (int)E, a.k = (int)k;
+  a.score = score, a.renorm = renormalize != 0, a.route_scale = route_scale;
+  a.mask = token_mask;
+  a.idx_in = topk_idx, a.counts_in = counts, a.dw = dtopk_w, a.dloss = dloss, a.dlogits = dlogits;
+  return cuda_result(fp8moe::launch_router_bwd(a, d->num_sms, (cudaStream_t)stream));
+}
+
+fp8moe_status fp8moe_route_weight_grad(const void* dout, const void* y, const int32_t* row_of, int64_t T, int64_t N,
+                                       int64_t k, float* dw, fp8moe_stream_t stream) {
+  if (T < 0 || N < 0 || k < 1 || T > ((int64_t)1 << 30) / k) return FP8MOE_ERR_INVALID_ARG;
+  if (N % 8) return FP8MOE_ERR_ALIGNMENT;
+  if (T == 0) return FP8MOE_OK;
+  if (!row_of || !dw || (N > 0 && (!dout || !y))) return FP8MOE_ERR_INVALID_ARG;
+  if (!al16(dout) || !al16(y) || (((uintptr_t)row_of | (uintptr_t)dw) & 3)) return FP8MOE_ERR_ALIGNMENT;
+  DevInfo* d;
+  fp8moe_status st = device_info(&d);
+  if (st) return st;
+  return cuda_result(fp8moe::launch_route_weight_grad(dout, y, row_of, T, N, k, dw, d->num_sms, (cudaStream_t)stream));
+}
+
+static fp8moe_status swiglu(bool bwd, const void* dout, const void* h, int64_t ldh, int64_t M, int64_t F,
+                            const int32_t* offs, int64_t E, void* out, void* q0, uint8_t* s0, int s0_layout, void* q1,
+                            uint8_t* s1, int s1_layout, fp8moe_stream_t stream) {
+  if (M < 0 || F < 1 || M > ((int64_t)1 << 30) || F > ((int64_t)1 << 30) || ldh < 2 * F)
+    return FP8MOE_ERR_INVALID_ARG;
+  if (F % 32 || ldh % 8) return FP8MOE_ERR_ALIGNMENT;
+  if (M == 0) return FP8MOE_OK;
+  if (!(out || q0 || q1) || (q0 == nullptr) != (s0 == nullptr) || (q1 == nullptr) != (s1 == nullptr))
+    return FP8MOE_ERR_INVALID_ARG;
+  const bool ok0 = !q0 || s0_layout == FP8MOE_SCALES_ROWMAJOR || s0_layout == FP8MOE_NO_GROUPS ||
+                   s0_layout == FP8MOE_GROUP_ROWS;
+  const bool ok1 = !q1 || s1_layout == FP8MOE_SCALES_ROWMAJOR || s1_layout == FP8MOE_NO_GROUPS ||
+                   s1_layout == FP8MOE_GROUP_COLS;
+  if (!ok0 || !ok1) return FP8MOE_ERR_INVALID_ARG;
+  const bool g0 = q0 && s0_layout == FP8MOE_GROUP_ROWS, g1 = q1 && s1_layout == FP8MOE_GROUP_COLS;
+  if ((g0 || g1) && (E < 1 || E > FP8MOE_MAX_GROUPS || !offs)) return FP8MOE_ERR_INVALID_ARG;
+  if ((q1 || g0) && M % 32) return FP8MOE_ERR_ALIGNMENT;
+  if ((g0 || g1) && ((uintptr_t)offs & 3)) return FP8MOE_ERR_ALIGNMENT;
+  if (!h || (bwd && !dout)) return FP8MOE_ERR_INVALID_ARG;
+  if (!al16(h) || !al16(dout) || !al16(out) || !al16(q0) || !al16(q1)) return FP8MOE_ERR_ALIGNMENT;
+  DevInfo* d;
+  fp8moe_status st = device_info(&d);
+  if (st) return st;
+  fp8moe::SwigluArgs a{};
+  a.dout = (const uint16_t*)(bwd ? dout : nullptr);
+  a.h = (const uint16_t*)h;
+  a.M = M, a.F = F, a.ldh = ldh;
+  a.offs = offs;
+  a.E0 = g0 ? (int)E : 0;
+  a.E1 = g1 ? (int)E : 0;
+  a.out = (uint16_t*)out;
+  a.q0 = (uint8_t*)q0, a.s0 = s0, a.q1 = (uint8_t*)q1, a.s1 = s1;
+  a.s0_layout = s0_layout, a.s1_layout = s1_layout;
+  a.num_sms = d->num_sms;
+  a.status = d->status;
+  return cuda_result(fp8moe::launch_swiglu(a, (cudaStream_t)stream));
+}
+
+fp8moe_status fp8moe_swiglu_fwd(const void* h, int64_t ldh, int64_t M, int64_t F, const int32_t* offs, int64_t E,
+                                void* out, void* q0, uint8_t* s0, int s0_layout, void* q1, uint8_t* s1,
+                                int s1_layout, fp8moe_stream_t stream) {
+  return swiglu(false, nullptr, h, ldh, M, F, offs, E, out, q0, s0, s0_layout, q1, s1, s1_layout, stream);
+}
+
+fp8moe_status fp8moe_swiglu_bwd(const void* dout, const void* h, int64_t ldh, int64_t M, int64_t F,
+                                const int32_t* offs, int64_t E, void* dh, void* q0, uint8_t* s0, int s0_layout,
+                                void* q1, uint8_t* s1, int s1_layout, fp8moe_stream_t stream) {
+  return swiglu(true, dout, h, ldh, M, F, offs, E, dh, q0, s0, s0_layout, q1, s1, s1_layout, stream);
 }
 
 fp8moe_status fp8moe_get_device_status(fp8moe_stream_t stream, int32_t* out_code) {

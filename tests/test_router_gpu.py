@@ -1,0 +1,256 @@
+"""The router, its gradient and the combine's weight gradient against the
+float64 definitions.
+
+Tolerances.  A score: exp of an argument that is off by 2^-24 of itself (at
+most 100 here: 6e-6), two ulp of exp, and a division: 1e-5 relative covers it
+and the sums of up to 1024 positive terms; weights, probabilities and sums
+take twice that, the loss three times.  Gradients: the same on the sizes of
+the terms that are added.  bf16 logit gradients lie between the roundings of
+the two ends."""
+import numpy as np
+import pytest
+import torch
+
+from code_bounds import check_bf16
+from oracle import moe_ops as OM, routing as RT
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+REL = 1e-5
+
+
+@pytest.fixture(scope="module")
+def F():
+    from mxfp8_moe_quantization_gb300 import build as B
+    B.build()
+    import mxfp8_moe_quantization_gb300 as m
+    return m
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _logits(T, E, seed, bf16, dead=0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, E, generator=g) * 2
+    if dead:
+        x[:, torch.randperm(E, generator=g)[:dead]] = -float("inf")
+    return x.to(torch.bfloat16) if bf16 else x
+
+
+def _score(F, name):
+    return F.SCORE_SOFTMAX if name == "softmax" else F.SCORE_SIGMOID
+
+
+def _check(F, x, k, score, renorm, scale, bias=None, mask=None, ld=None):
+    """One forward against the definition on the kernel's own choice, and the
+    choice against the keys."""
+    T, E = x.shape
+    d = lambda t: None if t is None else t.to(DEV)
+    xd = d(x)
+    if ld is not None:
+        wide = torch.full((T, ld), float("nan"), dtype=x.dtype, device=DEV)
+        wide[:, :E] = xd
+        xd = wide[:, :E]
+    out = F.fp8moe_router_fwd(xd, k, score=_score(F, score), renormalize=renorm, route_scale=scale, bias=d(bias),
+                              token_mask=d(mask))
+    idx, w, counts, psum, loss = (t.cpu() for t in out)
+    idx = idx.numpy().astype(np.int64)
+    m = None if mask is None else mask.numpy()
+    ref = OM.router(_np(x), k, score, renorm, scale, None if bias is None else _np(bias), m, idx=idx)
+    assert np.all((idx >= 0) & (idx < E)) and all(len(set(r)) == k for r in idx.tolist())
+    live = OM._live(_np(x), m)
+    key = live if bias is None else np.where(live == -np.inf, -np.inf, ref["s"] + _np(bias))
+    if bias is None:
+        assert np.array_equal(idx, OM.choose(key, k))
+    else:
+        best = np.take_along_axis(key, OM.choose(key, k), 1)
+        mine = np.take_along_axis(key, idx, 1)
+        dead = best == -np.inf
+        assert np.array_equal(dead, mine == -np.inf)
+        assert np.all(np.where(dead, 0.0, np.abs(np.where(dead, 0.0, best) - np.where(dead, 0.0, mine))) <= 4e-7)
+    assert np.all(np.abs(_np(w) - ref["w"]) <= 2 * REL * np.abs(ref["w"]) + 1e-37)
+    assert np.array_equal(counts.numpy()[:E], ref["counts"]) and int(counts[E]) == ref["tokens"]
+    assert np.all(np.abs(_np(psum) - ref["prob_sum"]) <= 2 * REL * ref["prob_sum"] + 1e-37)
+    assert abs(float(loss) - ref["loss"]) <= 3 * REL * ref["loss"]
+    # without the sums the choice is the same
+    i2, w2, *none = F.fp8moe_router_fwd(xd, k, score=_score(F, score), renormalize=renorm, route_scale=scale,
+                                        bias=d(bias), token_mask=d(mask), need_balance=False)
+    assert none == [None] * 3 and torch.equal(i2, out[0]) and torch.equal(w2, out[1])
+    return out
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (3, 256, 8), (16, 64, 6), (17, 33, 32), (300, 100, 4),
+                                   (2500, 256, 8), (5, 1024, 10), (70, 1000, 32), (1300, 5, 5)])
+@pytest.mark.parametrize("score,renorm,bf16", [("softmax", False, True), ("softmax", True, False),
+                                               ("sigmoid", True, False), ("sigmoid", False, True)])
+def test_forward(F, T, E, k, score, renorm, bf16):
+    x = _logits(T, E, T + E, bf16, dead=min(3, E - 1))
+    bias = torch.randn(E, generator=torch.Generator().manual_seed(1)) * 0.1
+    _check(F, x, k, score, renorm, 2.5)
+    _check(F, x, k, score, renorm, 1.0, bias=bias, ld=E + 5)
+
+
+@pytest.mark.parametrize("T", [4, 700])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_masks(F, T, score):
+    """Padding tokens (whose logits hold anything), rows of nothing but -inf,
+    the type's lowest value, and fewer experts left than k."""
+    E, k = 40, 6
+    for bf16 in (False, True):
+        x = _logits(T, E, 5, bf16)
+        lowest = torch.finfo(x.dtype).min
+        x[0] = -float("inf")
+        x[1] = lowest
+        x[2, 3:] = -float("inf")
+        x[3, ::2] = lowest
+        mask = torch.ones(T, dtype=torch.uint8)
+        if T > 4:
+            mask[10:60:3] = 0
+        _check(F, x, k, score, True, 1.5, mask=mask)
+        bias = torch.linspace(-0.5, 0.5, E)
+        clean = _check(F, x, k, score, False, 1.0, bias=bias, mask=mask)
+        y = x.clone()
+        y[mask == 0] = float("nan")
+        got = F.fp8moe_router_fwd(y.to(DEV), k, score=_score(F, score), renormalize=False, bias=bias.to(DEV),
+                                  token_mask=mask.bool().to(DEV))
+        for a, b in zip(got, clean):
+            assert torch.equal(a, b)
+
+
+def test_ties_and_signed_zero(F):
+    """Equal keys go to the lowest id; 0 and -0 are equal."""
+    x = torch.zeros(40, 96)
+    x[1:, ::2] = -0.0
+    x[2, 70] = x[2, 5] = 1.0
+    for score in ("softmax", "sigmoid"):
+        idx = F.fp8moe_router_fwd(x.to(DEV), 4, score=_score(F, score))[0].cpu()
+        assert idx[0].tolist() == idx[1].tolist() == [0, 1, 2, 3] and idx[2].tolist() == [5, 70, 0, 1]
+        idx = F.fp8moe_router_fwd(x.to(DEV), 4, score=_score(F, score), bias=torch.zeros(96, device=DEV))[0].cpu()
+        assert idx[0].tolist() == [0, 1, 2, 3] and idx[2].tolist() == [5, 70, 0, 1]
+
+
+def test_nan_logits_keep_the_ids_valid(F):
+    x = _logits(64, 64, 1, False)
+    x[7, 3] = x[7, 9] = float("nan")
+    x[8] = float("nan")
+    for score in ("softmax", "sigmoid"):
+        idx, w, *_ = F.fp8moe_router_fwd(x.to(DEV), 6, score=_score(F, score))
+        i = idx.cpu()
+        assert bool(((i >= 0) & (i < 64)).all()) and all(len(set(r)) == 6 for r in i.tolist())
+        assert 3 not in i[7].tolist() and 9 not in i[7].tolist() and i[8].tolist() == [0, 1, 2, 3, 4, 5]
+        assert bool(torch.isfinite(w[:7]).all()) and bool(torch.isnan(w[8]).all())
+
+
+def test_no_tokens(F):
+    x = torch.empty(0, 16, device=DEV)
+    idx, w, counts, psum, loss = F.fp8moe_router_fwd(x, 2)
+    assert idx.shape == w.shape == (0, 2) and not counts.any() and not psum.any() and float(loss) == 0.0
+    assert F.fp8moe_router_bwd(x, idx, counts, w, loss).shape == (0, 16)
+
+
+def test_same_bits_every_time(F):
+    """Large enough for many CTAs; a dirty workspace does not matter."""
+    T, E = 20000, 128
+    x = _logits(T, E, 3, False).to(DEV)
+    ws = torch.full((F.fp8moe_router_workspace_bytes(T, E) // 4,), float("nan"), device=DEV)
+    a = F.fp8moe_router_fwd(x, 8)
+    b = F.fp8moe_router_fwd(x, 8, workspace=ws)
+    for u, v in zip(a, b):
+        assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (2, 8, 2), (33, 256, 8), (257, 100, 4), (9, 1024, 10), (40, 40, 32)])
+@pytest.mark.parametrize("score,renorm,bf16", [("softmax", False, False), ("softmax", True, True),
+                                               ("sigmoid", True, False), ("sigmoid", False, True)])
+def test_backward(F, T, E, k, score, renorm, bf16):
+    x = _logits(T, E, T + E, bf16, dead=min(2, E - 1))
+    mask = torch.ones(T, dtype=torch.uint8)
+    if T > 8:
+        mask[::5] = 0
+        x[1] = -float("inf")
+    xd, md = x.to(DEV), mask.to(DEV)
+    kw = dict(score=_score(F, score), renormalize=renorm, route_scale=2.5, token_mask=md)
+    idx, _, counts, _, _ = F.fp8moe_router_fwd(xd, k, **kw)
+    g = torch.Generator().manual_seed(1)
+    dw, dloss = torch.randn(T, k, generator=g), torch.tensor([3.0])
+    ii, cc, n = idx.cpu().numpy().astype(np.int64), counts.cpu().numpy()[:E], int(counts[E])
+    for use_w, use_l in ((True, True), (True, False), (False, True)):
+        got = F.fp8moe_router_bwd(xd, idx, counts if use_l else None, dw.to(DEV) if use_w else None,
+                                  dloss.to(DEV) if use_l else None, **kw)
+        args = (_np(x), ii, cc, n, _np(dw) if use_w else None, 3.0 if use_l else 0.0, score, renorm, 2.5, mask.numpy())
+        ref = OM.router_grad(*args)
+        # the size of what is added: the same formula on absolute values
+        s, p = OM.scores(OM._live(_np(x), mask.numpy()), score)
+        c = (3.0 if use_l else 0.0) * E / (k * max(n, 1) ** 2) * cc
+        size = p * (c + (p * c).sum(1, keepdims=True))
+        if use_w:
+            sel = np.take_along_axis(s, ii, 1)
+            if renorm:
+                z = sel.sum(1, keepdims=True)
+                sel = sel / np.where(z == 0, 1, z)
+            ad = np.abs(_np(dw))
+            u = 2.5 * sel * (ad + ((ad * sel).sum(1, keepdims=True) if renorm else 0))
+            full = np.zeros_like(s)
+            np.put_along_axis(full, ii, u, 1)
+            size = size + full + (p * u.sum(1, keepdims=True) if score == "softmax" else 0)
+        lim = 4 * REL * size + 1e-37
+        if bf16:
+            check_bf16(got, ref, lim, "dlogits")
+        else:
+            assert got.dtype == x.dtype and np.all(np.abs(_np(got) - ref) <= lim)
+        assert not got[mask.to(DEV) == 0].any()
+
+
+def test_backward_skips_foreign_ids_and_masked_garbage(F):
+    x = _logits(16, 24, 2, False)
+    idx = F.fp8moe_router_fwd(x.to(DEV), 3)[0]
+    dw = torch.ones(16, 3)
+    mask = torch.ones(16, dtype=torch.uint8)
+    mask[4] = 0
+    bad = idx.clone()
+    bad[2, 1], bad[3, 0] = -1, 24
+    x2, dw2 = x.clone(), dw.clone()
+    x2[4], dw2[4] = float("nan"), float("nan")
+    got = F.fp8moe_router_bwd(x2.to(DEV), bad, None, dw2.to(DEV), renormalize=False, token_mask=mask.to(DEV))
+    want = F.fp8moe_router_bwd(x.to(DEV), idx, None, dw.to(DEV), renormalize=False, token_mask=mask.to(DEV))
+    keep = [t for t in range(16) if t not in (2, 3)]
+    assert torch.equal(got[keep], want[keep]) and bool(torch.isfinite(got).all()) and not got[4].any()
+
+
+@pytest.mark.parametrize("T,N,k", [(1, 8, 1), (3, 264, 2), (50, 1032, 4), (7, 7168, 8), (3000, 256, 3), (9, 520, 11),
+                                   (2600, 64, 8)])
+def test_weight_grad(F, T, N, k):
+    """fp32 sums of N products: at most N / 32 terms in a row and 8 joins."""
+    g = torch.Generator().manual_seed(T)
+    rows = T * k + 5
+    y, dout = torch.randn(rows, N, generator=g).to(torch.bfloat16), torch.randn(T, N, generator=g).to(torch.bfloat16)
+    row_of = torch.randperm(rows, generator=g)[:T * k].reshape(T, k).to(torch.int32)
+    row_of[0, 0] = -1
+    got = F.fp8moe_route_weight_grad(dout.to(DEV), y.to(DEV), row_of.to(DEV))
+    r = row_of.numpy()
+    ref = np.einsum("tn,tkn->tk", _np(dout), _np(y)[np.maximum(r, 0)]) * (r >= 0)
+    size = np.einsum("tn,tkn->tk", np.abs(_np(dout)), np.abs(_np(y))[np.maximum(r, 0)])
+    assert np.all(np.abs(_np(got) - ref) <= (N / 32 + 16) * 2.0 ** -24 * size)
+    if T <= 50:
+        assert np.allclose(ref, OM.weight_grad(_np(dout), _np(y), r), rtol=1e-12, atol=1e-9)
+
+
+def test_weight_grad_is_the_difference_of_the_combine(F):
+    """<unpermute(y, w + s e) - unpermute(y, w - s e), dout> / 2s, exact in w up
+    to the combine's bf16 output: values chosen so that it rounds nothing."""
+    T, N, k, E = 20, 64, 3, 7
+    g = torch.Generator().manual_seed(4)
+    idx = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).to(torch.int32)
+    _, _, rrow = RT.route_permute(np.zeros((T, 8), np.float32), idx.numpy(), E)
+    row_of = torch.from_numpy(rrow.astype(np.int32)).to(DEV)
+    y = torch.randint(-2, 3, (RT.route_rows(T, k, E), N), generator=g).to(torch.bfloat16).to(DEV)
+    dout = torch.randint(-4, 5, (T, N), generator=g).to(torch.bfloat16).to(DEV)
+    w = torch.full((T, k), 1.0, device=DEV)
+    got = F.fp8moe_route_weight_grad(dout, y, row_of)
+    for j in range(k):
+        step = torch.zeros(T, k, device=DEV)
+        step[:, j] = 1.0
+        d = F.fp8moe_route_unpermute(y, row_of, w + step).double() - F.fp8moe_route_unpermute(y, row_of, w - step).double()
+        assert torch.equal((d * dout.double()).sum(1) / 2, got[:, j].double())
