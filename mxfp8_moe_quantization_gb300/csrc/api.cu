@@ -600,7 +600,7 @@ fp8moe_status fp8moe_route_weight_grad(const void* dout, const void* y, const in
 static fp8moe_status swiglu(bool bwd, const void* dout, const void* h, int64_t ldh, int64_t M, int64_t F,
                             const int32_t* offs, int64_t E, void* out, void* q0, uint8_t* s0, int s0_layout, void* q1,
                             uint8_t* s1, int s1_layout, fp8moe_stream_t stream) {
-  if (M < 0 || F < 1 || M > ((int64_t)1 << 30) || F > ((int64_t)1 << 30) || ldh < 2 * F)
+  if (M < 0 || F < 1 || M > ((int64_t)1 << 30) || F > ((int64_t)1 << 28) || ldh < 2 * F)
     return FP8MOE_ERR_INVALID_ARG;
   if (F % 32 || ldh % 8) return FP8MOE_ERR_ALIGNMENT;
   if (M == 0) return FP8MOE_OK;

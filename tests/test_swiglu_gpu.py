@@ -113,6 +113,28 @@ def test_groups(F, sizes, bwd):
 
 
 @pytest.mark.parametrize("bwd", [False, True])
+def test_many_tiles(F, bwd):
+    """More tiles than CTAs: every CTA walks several, across row blocks and
+    groups, with ragged last row blocks and a last column tile of half width."""
+    for M, Fd, sizes in ((9824, 416, [32, 0, 4000, 96, 5696]), (20001, 160, None), (70016, 64, [64] * 1000 + [6016])):
+        h, dout = _bf16((M, 2 * Fd), M, 2.0), _bf16((M, Fd), M + 1) if bwd else None
+        offs = None if sizes is None else _offs(sizes)
+        if sizes is None:
+            _check(F, h, dout, None, F.NO_GROUPS, F.NO_GROUPS, False, ldh=2 * Fd + 8)
+        else:
+            _check(F, h, dout, offs, F.GROUP_ROWS, F.GROUP_COLS, True)
+
+
+def test_invalid_offsets_with_many_tiles(F):
+    M, Fd = 20480, 256
+    h = _bf16((M, 2 * Fd), 1).to(DEV)
+    offs = torch.tensor([64, 32, M], dtype=torch.int32, device=DEV)
+    q0 = torch.full((M, Fd), 0xA5, dtype=torch.uint8, device=DEV)
+    F.fp8moe_swiglu_fwd(h, offs, F.GROUP_ROWS, need_out=False, dim0=True, q0=q0)
+    assert F.fp8moe_get_device_status() == 5 and bool((q0 == 0xA5).all())
+
+
+@pytest.mark.parametrize("bwd", [False, True])
 def test_each_output_alone(F, bwd):
     M, Fd = 160, 64
     h, dout = _bf16((M, 2 * Fd), 1).to(DEV), _bf16((M, Fd), 2).to(DEV)
