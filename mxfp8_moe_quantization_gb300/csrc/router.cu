@@ -17,7 +17,9 @@
 //
 // A warp takes a token, a lane every 32nd expert; the logits are read once.
 // Sums over tokens have a fixed order (registers, then warps, then CTAs), so
-// results do not change from run to run.
+// results do not change from run to run.  The CTAs' partial sums are joined by
+// a second kernel of one cluster, which is already resident, waiting, when the
+// first one ends (programmatic dependent launch).
 #include "common.cuh"
 #include "launch.h"
 #include "moe_ops.h"
@@ -68,14 +70,21 @@ FP8MOE_DEV void load_row(const RouterArgs& a, int64_t t, int lane, bool on, floa
   }
 }
 
-// Scores s and probabilities p of a row; returns (for softmax) the maximum
-// and the sum that turn another logit of the row into its score.
+// 1 / (1 + e^-x), each step rounded to nearest (the choice with a bias hangs on it)
+FP8MOE_DEV float sigmoid_rn(float x) { return __frcp_rn(1.0f + expf(-x)); }
+
+// What turns a logit of the row into its score: softmax s = e^(x - m) / z;
+// z is also the sum of the sigmoids.
 struct RowStat {
-  float m, z;
+  float m, rz;   // rz = 1 / z, 0 for a row of nothing but -inf
 };
-FP8MOE_DEV float sigmoid_rn(float x) { return __fdiv_rn(1.0f, 1.0f + expf(-x)); }
+template <bool SIG>
+FP8MOE_DEV float score_of(float x, const RowStat& st) {
+  return SIG ? sigmoid_rn(x) : expf(x - st.m) * st.rz;
+}
+// s: sigmoids, or the softmax's e^(x - m) before the division by z
 template <int V, bool SIG>
-FP8MOE_DEV RowStat row_scores(const float (&x)[V], float (&s)[V], float (&p)[V]) {
+FP8MOE_DEV RowStat row_scores(const float (&x)[V], float (&s)[V]) {
   RowStat st{0.0f, 0.0f};
   float z = 0.0f;
   if constexpr (SIG) {
@@ -91,49 +100,47 @@ FP8MOE_DEV RowStat row_scores(const float (&x)[V], float (&s)[V], float (&p)[V])
     for (int i = 0; i < V; ++i) z += s[i] = expf(x[i] - st.m);
   }
   z = warp_sum(z);
-  st.z = z == 0.0f ? 1.0f : z;   // a row of nothing but -inf is all zero
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    p[i] = __fdiv_rn(s[i], st.z);
-    if constexpr (!SIG) s[i] = p[i];
-  }
+  st.rz = z == 0.0f ? 0.0f : __frcp_rn(z);
   return st;
 }
 
-// counts and probability sums of one CTA (acc: this warp's lanes' sums) into
-// shared memory, summed over its warps in order
-struct CtaSums {
-  float p[RW][ROUTER_MAX_E];
-  int n[ROUTER_MAX_E + 1];
-};
+FP8MOE_DEV float logit_at(const RouterArgs& a, int64_t t, int e) {
+  return a.bf16 ? __uint_as_float((uint32_t)((const uint16_t*)a.logits)[t * a.ld + e] << 16)
+                : ((const float*)a.logits)[t * a.ld + e];
+}
 
-FP8MOE_DEV void final_sums(const RouterArgs& a, int E, const float* psum, const int* n, float* red) {
-  // loss from the whole sums; every thread of the CTA calls it
-  float v = 0.0f;
-  for (int e = threadIdx.x; e < E; e += blockDim.x) v = fmaf((float)n[e], psum[e], v);
+// loss from counts and probability sums; every thread of the CTA calls it.
+// part: this CTA's share of sum n_e P_e (thread 0 has the result)
+FP8MOE_DEV float cta_sum(float v, float* red) {
   v = warp_sum(v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  if (threadIdx.x < 32) {
-    v = threadIdx.x < (blockDim.x >> 5) ? red[threadIdx.x] : 0.0f;
-    v = warp_sum(v);
-    if (threadIdx.x == 0) {
-      const float N = fmaxf((float)n[E], 1.0f);
-      a.loss[0] = v * __fdiv_rn((float)E, (float)a.k) / (N * N);
-    }
-  }
+  v = 0.0f;
+  if (threadIdx.x < 32) v = warp_sum(threadIdx.x < (blockDim.x >> 5) ? red[threadIdx.x] : 0.0f);
+  return v;
 }
+FP8MOE_DEV float loss_of(float np, int tokens, int E, int k) {
+  const float N = fmaxf((float)tokens, 1.0f);
+  return np * __fdiv_rn((float)E, (float)k) / (N * N);
+}
+
+// dynamic shared memory of the forward: probability sums [RW][E], counts [E + 1]
+inline int fwd_smem(int E, bool sums) { return sums ? (RW * E + E + 1) * 4 : 0; }
 
 template <int V, bool SIG>
 __global__ void __launch_bounds__(RW * 32) k_router_fwd(RouterArgs a) {
-  __shared__ CtaSums cs;
+  extern __shared__ float rsm[];
   __shared__ float red[32];
+  float* cp = rsm;                      // [RW][E]
+  int* cn = (int*)(rsm + RW * a.E);     // [E + 1]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool sums = a.counts != nullptr;
+  // the joining kernel may take its place; it waits for this one's end
+  asm volatile("griddepcontrol.launch_dependents;");
   float acc[V] = {};
   int tokens = 0;
   if (sums) {
-    for (int e = threadIdx.x; e <= a.E; e += RW * 32) cs.n[e] = 0;
+    for (int e = threadIdx.x; e <= a.E; e += RW * 32) cn[e] = 0;
     __syncthreads();
   }
   float bias[V];
@@ -141,193 +148,202 @@ __global__ void __launch_bounds__(RW * 32) k_router_fwd(RouterArgs a) {
   for (int i = 0; i < V; ++i) bias[i] = a.bias && i * 32 + lane < a.E ? a.bias[i * 32 + lane] : 0.0f;
   for (int64_t t = (int64_t)blockIdx.x * RW + warp; t < a.T; t += (int64_t)gridDim.x * RW) {
     const bool on = !a.mask || a.mask[t] != 0;
-    float x[V], s[V], p[V];
+    float x[V], s[V];
     load_row<V>(a, t, lane, on, x);
-    row_scores<V, SIG>(x, s, p);
+    const RowStat st = row_scores<V, SIG>(x, s);
     uint32_t key[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      acc[i] += p[i];
+      const float p = s[i] * st.rz;
+      acc[i] += p;
       // dead experts stay below every other whatever their bias
-      const float f = !a.bias ? x[i] : x[i] == NEG_INF ? NEG_INF : s[i] + bias[i];
+      const float f = !a.bias ? x[i] : x[i] == NEG_INF ? NEG_INF : (SIG ? s[i] : p) + bias[i];
       key[i] = i * 32 + lane < a.E ? order_key(f) : 0u;
     }
     tokens += on;
     // k rounds: the warp's largest key, then the lowest id that has it
     int my_e = 0;
-    float my_w = 0.0f;
-    bool my_live = false;
     for (int j = 0; j < a.k; ++j) {
-      uint32_t bk = 0;
-      int be = INT32_MAX;
-      float bs = 0.0f;
-      bool bl = false;
+      uint32_t bk = key[0];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const bool up = key[i] > bk;   // ascending ids: the first of equal keys stays
-        bk = up ? key[i] : bk;
-        be = up ? i * 32 + lane : be;
-        bs = up ? s[i] : bs;
-        bl = up ? x[i] != NEG_INF : bl;
-      }
+      for (int i = 1; i < V; ++i) bk = max(bk, key[i]);
       const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
-      const int e = (int)__reduce_min_sync(0xffffffffu, bk == top ? (uint32_t)be : (uint32_t)INT32_MAX);
-      const float ws = __shfl_sync(0xffffffffu, bs, e & 31);
-      const bool wl = __shfl_sync(0xffffffffu, (int)bl, e & 31) != 0;
-      if (lane == j) {
-        my_e = e;
-        my_w = ws;
-        my_live = wl;
-      }
-      if (lane == (e & 31)) {
+      uint32_t be = 0xffffffffu;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i == (e >> 5)) key[i] = 0u;
-      }
+      for (int i = V - 1; i >= 0; --i)
+        if (key[i] == top) be = (uint32_t)(i * 32 + lane);
+      const uint32_t e = __reduce_min_sync(0xffffffffu, be);
+      if (lane == j) my_e = (int)e;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (e == (uint32_t)(i * 32 + lane)) key[i] = 0u;
+    }
+    // lane j: slot j's weight, from its logit
+    float w = 0.0f;
+    if (lane < a.k) {
+      const float xe = on ? logit_at(a, t, my_e) : NEG_INF;
+      w = score_of<SIG>(xe, st);
+      if (sums && xe != NEG_INF) atomicAdd(&cn[my_e], 1);
     }
     if (a.renorm) {
-      const float z = warp_sum(lane < a.k ? my_w : 0.0f);
-      my_w = __fdiv_rn(my_w, z == 0.0f ? 1.0f : z);
+      const float z = warp_sum(w);
+      w = __fdiv_rn(w, z == 0.0f ? 1.0f : z);
     }
     if (lane < a.k) {
       a.idx[t * a.k + lane] = my_e;
-      a.w[t * a.k + lane] = my_w * a.route_scale;
-      if (sums && my_live) atomicAdd(&cs.n[my_e], 1);
+      a.w[t * a.k + lane] = w * a.route_scale;
     }
   }
   if (!sums) return;
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    if (i * 32 + lane < a.E) cs.p[warp][i * 32 + lane] = acc[i];
-  if (lane == 0) atomicAdd(&cs.n[a.E], tokens);
+    if (i * 32 + lane < a.E) cp[warp * a.E + i * 32 + lane] = acc[i];
+  if (lane == 0) atomicAdd(&cn[a.E], tokens);
   __syncthreads();
   const bool single = gridDim.x == 1;
   float* pp = single ? a.psum : (float*)a.workspace + (int64_t)blockIdx.x * a.E;
   int* pn = single ? a.counts : (int*)((float*)a.workspace + (int64_t)gridDim.x * a.E) + (int64_t)blockIdx.x * (a.E + 1);
+  float np = 0.0f;
   for (int e = threadIdx.x; e <= a.E; e += RW * 32) {
+    const int n = cn[e];
+    pn[e] = n;
     if (e < a.E) {
-      float v = cs.p[0][e];
+      float v = cp[e];
 #pragma unroll
-      for (int i = 1; i < RW; ++i) v += cs.p[i][e];
+      for (int i = 1; i < RW; ++i) v += cp[i * a.E + e];
       pp[e] = v;
-      cs.p[0][e] = v;
+      np = fmaf((float)n, v, np);
     }
-    pn[e] = cs.n[e];
   }
   if (single) {
-    __syncthreads();
-    final_sums(a, a.E, cs.p[0], cs.n, red);
+    np = cta_sum(np, red);
+    if (threadIdx.x == 0) a.loss[0] = loss_of(np, cn[a.E], a.E, a.k);
   }
 }
 
-// counts, probability sums and the loss from the CTAs' partials, in order
-__global__ void __launch_bounds__(1024) k_router_sums(RouterArgs a, int parts) {
-  __shared__ float sp[1024], fp[ROUTER_MAX_E], red[32];
-  __shared__ int sn[1024], fn[ROUTER_MAX_E + 1];
-  const int ew = (a.E + 31) / 32 * 32, groups = 1024 / ew;
-  const int e = threadIdx.x % ew, g = threadIdx.x / ew;
+// Counts, probability sums and the loss from the CTAs' partials, in order: one
+// cluster of JOIN CTAs, CTA c with every JOIN-th block of 32 experts (a warp a
+// slice of the partials, a lane an expert).
+constexpr int JOIN = 8, JOIN_WARPS = 32;
+__global__ void __cluster_dims__(JOIN, 1, 1) __launch_bounds__(JOIN_WARPS * 32) k_router_join(RouterArgs a, int parts) {
+  __shared__ float sp[JOIN_WARPS][33], share, red[32];
+  __shared__ int sn[JOIN_WARPS][33], tok_s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = blockIdx.x;
   const float* pp = (const float*)a.workspace;
   const int* pn = (const int*)(pp + (int64_t)parts * a.E);
-  float v = 0.0f;
-  int n = 0;
-  if (e < a.E && g < groups) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float np = 0.0f;
+  for (int e0 = rank * 32; e0 < a.E; e0 += JOIN * 32) {
+    const int e = e0 + lane;
+    float v = 0.0f;
+    int n = 0;
+    if (e < a.E) {
 #pragma unroll 4
-    for (int i = g; i < parts; i += groups) {
-      v += pp[(int64_t)i * a.E + e];
-      n += pn[(int64_t)i * (a.E + 1) + e];
+      for (int i = warp; i < parts; i += JOIN_WARPS) {
+        v += pp[(int64_t)i * a.E + e];
+        n += pn[(int64_t)i * (a.E + 1) + e];
+      }
     }
+    sp[warp][lane] = v;
+    sn[warp][lane] = n;
+    __syncthreads();
+    // expert e0 + warp: the slices in lane order
+    v = warp_sum(sp[lane][warp]);
+    n = __reduce_add_sync(0xffffffffu, sn[lane][warp]);
+    if (lane == 0 && e0 + warp < a.E) {
+      a.psum[e0 + warp] = v;
+      a.counts[e0 + warp] = n;
+      np = fmaf((float)n, v, np);
+    }
+    __syncthreads();
   }
-  sp[threadIdx.x] = v;
-  sn[threadIdx.x] = n;
-  int tok = 0;
-  if (threadIdx.x < 32) {
-    for (int i = threadIdx.x; i < parts; i += 32) tok += pn[(int64_t)i * (a.E + 1) + a.E];
+  if (rank == 0 && warp == 0) {
+    int tok = 0;
+    for (int i = lane; i < parts; i += 32) tok += pn[(int64_t)i * (a.E + 1) + a.E];
     tok = __reduce_add_sync(0xffffffffu, tok);
+    if (lane == 0) tok_s = a.counts[a.E] = tok;
   }
-  __syncthreads();
-  if (g == 0 && e < a.E) {
-    for (int i = 1; i < groups; ++i) {
-      v += sp[i * ew + e];
-      n += sn[i * ew + e];
+  np = cta_sum(np, red);
+  if (threadIdx.x == 0) share = np;
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (rank == 0 && threadIdx.x == 0) {
+    np = 0.0f;
+    for (int c = 0; c < JOIN; ++c) {
+      uint32_t at;
+      float v;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(&share)), "r"(c));
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+      np += v;
     }
-    fp[e] = a.psum[e] = v;
-    fn[e] = a.counts[e] = n;
+    a.loss[0] = loss_of(np, tok_s, a.E, a.k);
   }
-  if (threadIdx.x == 0) fn[a.E] = a.counts[a.E] = tok;
-  __syncthreads();
-  final_sums(a, a.E, fp, fn, red);
+  // no CTA leaves while its share may still be read
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <int V, bool SIG>
 __global__ void __launch_bounds__(RW * 32) k_router_bwd(RouterArgs a) {
+  extern __shared__ float rsm[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* ubuf = rsm + warp * a.E;   // the chosen experts' u
   float c[V];
   float coef = 0.0f;
-  if (a.dloss) {
-    const float N = fmaxf((float)a.counts_in[a.E], 1.0f);
-    coef = a.dloss[0] * __fdiv_rn((float)a.E, (float)a.k) / (N * N);
-  }
+  if (a.dloss) coef = a.dloss[0] * loss_of(1.0f, a.counts_in[a.E], a.E, a.k);
 #pragma unroll
-  for (int i = 0; i < V; ++i) c[i] = a.dloss && i * 32 + lane < a.E ? coef * (float)a.counts_in[i * 32 + lane] : 0.0f;
+  for (int i = 0; i < V; ++i) {
+    const int e = i * 32 + lane;
+    c[i] = a.dloss && e < a.E ? coef * (float)a.counts_in[e] : 0.0f;
+    if (e < a.E) ubuf[e] = 0.0f;
+  }
+  __syncwarp();
   for (int64_t t = (int64_t)blockIdx.x * RW + warp; t < a.T; t += (int64_t)gridDim.x * RW) {
     const bool on = !a.mask || a.mask[t] != 0;
-    float x[V], s[V], p[V], d[V];
+    int e = -1;
+    float dwj = 0.0f, xj = 0.0f;
+    if (a.dw && lane < a.k && on) {
+      e = a.idx_in[t * a.k + lane];
+      if (e < 0 || e >= a.E) e = -1;
+      dwj = a.dw[t * a.k + lane];
+    }
+    float x[V], s[V];
     load_row<V>(a, t, lane, on, x);
-    const RowStat st = row_scores<V, SIG>(x, s, p);
+    if (e >= 0) xj = logit_at(a, t, e);
+    const RowStat st = row_scores<V, SIG>(x, s);
     float pc = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) pc = fmaf(p[i], c[i], pc);
-    pc = warp_sum(pc);
-#pragma unroll
-    for (int i = 0; i < V; ++i) d[i] = p[i] * (c[i] - pc);
+    for (int i = 0; i < V; ++i) pc = fmaf(s[i] * st.rz, c[i], pc);
     // lane j: slot j's score, from the logit itself
-    int e = -1;
-    float u = 0.0f;
+    const float sj = e >= 0 ? score_of<SIG>(xj, st) : 0.0f;
+    float u = sj * dwj, us = 0.0f;
+    pc = warp_sum(pc);
     if (a.dw) {
-      float sj = 0.0f, dwj = 0.0f;
-      if (lane < a.k && on) {
-        e = a.idx_in[t * a.k + lane];
-        if (e < 0 || e >= a.E) e = -1;
-        dwj = a.dw[t * a.k + lane];
-        if (e >= 0) {
-          const float xj = a.bf16 ? __uint_as_float((uint32_t)((const uint16_t*)a.logits)[t * a.ld + e] << 16)
-                                  : ((const float*)a.logits)[t * a.ld + e];
-          sj = SIG ? sigmoid_rn(xj) : __fdiv_rn(expf(xj - st.m), st.z);
-        }
-      }
       if (a.renorm) {
         const float z = warp_sum(sj);
-        sj = __fdiv_rn(sj, z == 0.0f ? 1.0f : z);
-        u = sj * (dwj - warp_sum(dwj * sj));
-      } else {
-        u = sj * dwj;
+        const float wj = __fdiv_rn(sj, z == 0.0f ? 1.0f : z);
+        u = wj * (dwj - warp_sum(dwj * wj));
       }
       u *= a.route_scale;
-      if constexpr (!SIG) {
-        const float us = warp_sum(u);
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = fmaf(-p[i], us, d[i]);
-      }
-      for (int j = 0; j < a.k; ++j) {
-        const int ej = __shfl_sync(0xffffffffu, e, j);
-        const float uj = __shfl_sync(0xffffffffu, u, j);
-        if (ej >= 0 && lane == (ej & 31)) {
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-            if (i == (ej >> 5)) d[i] += uj;
-        }
-      }
+      if constexpr (!SIG) us = warp_sum(u);
+      if (e >= 0) atomicAdd(&ubuf[e], u);
+      __syncwarp();
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int ei = i * 32 + lane;
       if (ei >= a.E) continue;
-      const float o = SIG ? d[i] * (1.0f - s[i]) : d[i];
+      const float p = s[i] * st.rz;
+      float o = p * (c[i] - pc - us) + ubuf[ei];
+      if (SIG) o *= 1.0f - s[i];
       if (a.bf16) {
         ((__nv_bfloat16*)a.dlogits)[t * a.E + ei] = __float2bfloat16_rn(o);
       } else {
         ((float*)a.dlogits)[t * a.E + ei] = o;
       }
+    }
+    if (a.dw) {
+      __syncwarp();
+      if (e >= 0) ubuf[e] = 0.0f;
+      __syncwarp();
     }
   }
 }
@@ -390,26 +406,36 @@ __global__ void __launch_bounds__(256) k_route_weight_grad(const uint16_t* __res
   }
 }
 
+// CTAs per SM: enough warps to overlap the rounds of different tokens; more
+// would only add partial sums to join
+constexpr int CTAS_PER_SM = 2;
+
 template <int V, bool SIG>
 cudaError_t run_fwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
-  static std::atomic<int> occ{0};
-  int64_t blocks = a.T <= SINGLE_CTA_T ? 1 : (a.T + RW - 1) / RW;
-  const int64_t fit = (int64_t)num_sms * blocks_per_sm(occ, k_router_fwd<V, SIG>, RW * 32, 0, 1);
-  if (blocks > fit) blocks = fit;
-  if (blocks > ROUTER_MAX_PARTS) blocks = ROUTER_MAX_PARTS;
-  k_router_fwd<V, SIG><<<(unsigned)blocks, RW * 32, 0, st>>>(a);
+  const bool sums = a.counts != nullptr;
+  int64_t blocks = sums && a.T <= SINGLE_CTA_T ? 1 : (a.T + RW - 1) / RW;
+  int64_t most = (int64_t)num_sms * (sums ? CTAS_PER_SM : 8);
+  if (sums && most > ROUTER_MAX_PARTS) most = ROUTER_MAX_PARTS;
+  if (blocks > most) blocks = most;
+  k_router_fwd<V, SIG><<<(unsigned)blocks, RW * 32, fwd_smem(a.E, sums), st>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !a.counts || blocks == 1) return e;
-  k_router_sums<<<1, 1024, 0, st>>>(a, (int)blocks);
-  return cudaGetLastError();
+  if (e != cudaSuccess || !sums || blocks == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(JOIN);
+  cfg.blockDim = dim3(JOIN_WARPS * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_router_join, a, (int)blocks);
 }
 template <int V, bool SIG>
 cudaError_t run_bwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
-  static std::atomic<int> occ{0};
   int64_t blocks = (a.T + RW - 1) / RW;
-  const int64_t fit = (int64_t)num_sms * blocks_per_sm(occ, k_router_bwd<V, SIG>, RW * 32, 0, 1);
-  if (blocks > fit) blocks = fit;
-  k_router_bwd<V, SIG><<<(unsigned)blocks, RW * 32, 0, st>>>(a);
+  if (blocks > (int64_t)num_sms * 8) blocks = (int64_t)num_sms * 8;
+  k_router_bwd<V, SIG><<<(unsigned)blocks, RW * 32, RW * a.E * 4, st>>>(a);
   return cudaGetLastError();
 }
 
