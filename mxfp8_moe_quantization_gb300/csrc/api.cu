@@ -486,8 +486,12 @@ fp8moe_status fp8moe_add_rmsnorm_fwd(const void* x, int64_t ldx, const void* res
   if (!al16(x) || !al16(residual) || !al16(w) || !al16(h) || !al16(y) || !al16(q) || ((uintptr_t)rstd & 3) ||
       (q && !mx && ((uintptr_t)scale & 3)))
     return FP8MOE_ERR_ALIGNMENT;
+  DevInfo* d;
+  fp8moe_status st = device_info(&d);
+  if (st) return st;
   return cuda_result(fp8moe::launch_norm_fwd(x, ldx, residual, ldr, w, weight_type == FP8MOE_FP32, T, H, eps, h, y,
-                                             rstd, recipe, kind, q, scale, scale_layout, (cudaStream_t)stream));
+                                             rstd, recipe, kind, q, scale, scale_layout, d->num_sms,
+                                             (cudaStream_t)stream));
 }
 
 int64_t fp8moe_add_rmsnorm_bwd_workspace_bytes(int64_t T, int64_t H) {
@@ -510,7 +514,7 @@ fp8moe_status fp8moe_add_rmsnorm_bwd(const void* dy, const void* h, const float*
   fp8moe_status st = device_info(&d);
   if (st) return st;
   return cuda_result(fp8moe::launch_norm_bwd(dy, h, rstd, w, weight_type == FP8MOE_FP32, dh, T, H, dx, dw, workspace,
-                                             d->num_sms, (cudaStream_t)stream));
+                                             d->num_sms, d->max_smem, d->status, (cudaStream_t)stream));
 }
 
 int64_t fp8moe_router_workspace_bytes(int64_t T, int64_t E) {
@@ -591,10 +595,7 @@ fp8moe_status fp8moe_route_weight_grad(const void* dout, const void* y, const in
   if (T == 0) return FP8MOE_OK;
   if (!row_of || !dw || (N > 0 && (!dout || !y))) return FP8MOE_ERR_INVALID_ARG;
   if (!al16(dout) || !al16(y) || (((uintptr_t)row_of | (uintptr_t)dw) & 3)) return FP8MOE_ERR_ALIGNMENT;
-  DevInfo* d;
-  fp8moe_status st = device_info(&d);
-  if (st) return st;
-  return cuda_result(fp8moe::launch_route_weight_grad(dout, y, row_of, T, N, k, dw, d->num_sms, (cudaStream_t)stream));
+  return cuda_result(fp8moe::launch_route_weight_grad(dout, y, row_of, T, N, k, dw, (cudaStream_t)stream));
 }
 
 static fp8moe_status swiglu(bool bwd, const void* dout, const void* h, int64_t ldh, int64_t M, int64_t F,

@@ -97,17 +97,17 @@ cudaError_t launch_swizzle(const uint8_t* s, int64_t B, int64_t R, int64_t Cs, c
 constexpr int NORM_BWD_PARTS = 512;
 cudaError_t launch_norm_fwd(const void* x, int64_t ldx, const void* r, int64_t ldr, const void* w, int w32, int64_t T,
                             int64_t H, float eps, void* h, void* y, float* rstd, int recipe, int kind, void* q,
-                            void* scale, int scale_layout, cudaStream_t st);
+                            void* scale, int scale_layout, int num_sms, cudaStream_t st);
 cudaError_t launch_norm_bwd(const void* dy, const void* h, const float* rstd, const void* w, int w32, const void* dh,
-                            int64_t T, int64_t H, void* dx, float* dw, void* workspace, int num_sms,
-                            cudaStream_t st);
+                            int64_t T, int64_t H, void* dx, float* dw, void* workspace, int num_sms, int max_smem,
+                            int* status, cudaStream_t st);
 
 // the router (router.cu)
 struct RouterArgs;
 cudaError_t launch_router_fwd(const RouterArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_router_bwd(const RouterArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_route_weight_grad(const void* dout, const void* y, const int32_t* row_of, int64_t T, int64_t N,
-                                     int64_t k, float* dw, int num_sms, cudaStream_t st);
+                                     int64_t k, float* dw, cudaStream_t st);
 
 // gated activation with MXFP8 output (swiglu.cu); dout == NULL: forward
 struct SwigluArgs;

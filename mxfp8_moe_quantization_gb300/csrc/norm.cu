@@ -13,8 +13,10 @@
 // Both directions move each element once and are bound by HBM; a row lives in
 // the registers of its warps between its loads and its stores.
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "launch.h"
 #include "scales.cuh"
+#include "tma.cuh"
 
 namespace fp8moe {
 namespace {
@@ -23,7 +25,11 @@ namespace {
 // up to 64 registers, V = 2 and 4 in up to 128).
 template <int V>
 constexpr int norm_threads() { return V == 1 ? 1024 : 512; }
+constexpr int NORM_BWD_STAGES = 4;   // most slots of the backward's ring
 constexpr int NORM_MAX_CHUNKS = 4 * norm_threads<4>();   // longer rows (H > 16384) take the looping kernels
+
+// partial values of a CTA's rows: at most 16 warps, each row's padded to fours
+constexpr int NORM_RED = 64;
 
 // a load that the same thread may follow with a store to the same place (the
 // residual stream is updated in place), so not through the read-only path
@@ -35,24 +41,21 @@ FP8MOE_DEV uint4 ld16(const void* p) {
                : "memory");
   return v;
 }
-FP8MOE_DEV void unpack8(const uint4& q, float (&f)[8]) {
-  f[0] = bf16_lo(q.x), f[1] = bf16_hi(q.x), f[2] = bf16_lo(q.y), f[3] = bf16_hi(q.y);
-  f[4] = bf16_lo(q.z), f[5] = bf16_hi(q.z), f[6] = bf16_lo(q.w), f[7] = bf16_hi(q.w);
-}
-FP8MOE_DEV uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
-FP8MOE_DEV uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+// eight values as four column pairs
+struct Vec8 {
+  uint64_t p[4];
+};
+FP8MOE_DEV Vec8 unpack8(const uint4& q) { return {{unpk_bf16(q.x), unpk_bf16(q.y), unpk_bf16(q.z), unpk_bf16(q.w)}}; }
+FP8MOE_DEV uint4 pack8(const Vec8& v) {
+  return make_uint4(pack_bf16x2(v.p[0]), pack_bf16x2(v.p[1]), pack_bf16x2(v.p[2]), pack_bf16x2(v.p[3]));
 }
 template <bool W32>
-FP8MOE_DEV void load_w8(const void* w, int64_t ch, float (&f)[8]) {
+FP8MOE_DEV Vec8 load_w8(const void* w, int64_t ch) {
   if constexpr (W32) {
     const float4 a = reinterpret_cast<const float4*>(w)[2 * ch], b = reinterpret_cast<const float4*>(w)[2 * ch + 1];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    return {{pk(a.x, a.y), pk(a.z, a.w), pk(b.x, b.y), pk(b.z, b.w)}};
   } else {
-    unpack8(reinterpret_cast<const uint4*>(w)[ch], f);
+    return unpack8(reinterpret_cast<const uint4*>(w)[ch]);
   }
 }
 
@@ -80,40 +83,43 @@ FP8MOE_DEV float row_reduce(float v, float* red, int wpr, int group, int wrow) {
     v = MAX ? fmaxf(v, u) : v + u;
   }
   if (wpr > 1) {
-    if ((threadIdx.x & 31) == 0) red[group * wpr + wrow] = v;
+    // a row's values start at a multiple of four: read as vectors, padded
+    float* mine = red + group * ((wpr + 3) & ~3);
+    if ((threadIdx.x & 31) == 0) mine[wrow] = v;
     __syncthreads();
-    v = red[group * wpr];
-    for (int i = 1; i < wpr; ++i) v = MAX ? fmaxf(v, red[group * wpr + i]) : v + red[group * wpr + i];
+    v = 0.0f;   // (the maxima are of magnitudes)
+    for (int i = 0; i < wpr; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(mine + i);
+      const float b = i + 1 < wpr ? f.y : 0.0f, c = i + 2 < wpr ? f.z : 0.0f, d = i + 3 < wpr ? f.w : 0.0f;
+      v = MAX ? fmaxf(fmaxf(fmaxf(v, f.x), b), fmaxf(c, d)) : v + f.x + b + (c + d);
+    }
   }
   return v;
 }
 
-// the eight codes of one chunk and, for MXFP8, its block's scale byte
+// the eight codes of one chunk scaled by s
 template <int OUT>
-FP8MOE_DEV uint2 encode8(const float (&v)[8], float s) {
+FP8MOE_DEV uint2 encode8(const Vec8& v, float s) {
   constexpr bool FZ = OUT == NORM_OUT_ROW_FNUZ;
-  return make_uint2(enc4<FZ>(__fmul_rn(v[0], s), __fmul_rn(v[1], s), __fmul_rn(v[2], s), __fmul_rn(v[3], s)),
-                    enc4<FZ>(__fmul_rn(v[4], s), __fmul_rn(v[5], s), __fmul_rn(v[6], s), __fmul_rn(v[7], s)));
+  const uint64_t s2 = pk(enc_mul<FZ>(s), enc_mul<FZ>(s));
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpk(mul2(v.p[i], s2), f[2 * i], f[2 * i + 1]);
+  return make_uint2(enc4_pre<FZ>(f[0], f[1], f[2], f[3]), enc4_pre<FZ>(f[4], f[5], f[6], f[7]));
 }
-FP8MOE_DEV float absmax8(const float (&v)[8]) {
-  return fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
-               fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));
-}
-// e8m0 byte of a block maximum (the dim0 quantizer's rule on an fp32
-// maximum) and the multiplier 2^-e
-FP8MOE_DEV uint32_t mx_byte(float amax, float& mul) {
-  const uint32_t b = max(__float_as_uint(amax) >> 23, 8u) - 8u;
-  mul = __uint_as_float((254u - b) << 23);
-  return b;
+FP8MOE_DEV float absmax8(float m, const Vec8& v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = amax3(m, v.p[i]);
+  return m;
 }
 
 // One chunk of y: its bf16 copy, codes and scale.  Every lane of the warp
 // calls it (the block maximum is a shuffle over four lanes).
 template <int OUT>
-FP8MOE_DEV void put_chunk(const NormFwdArgs& a, int64_t row, int ch, bool ok, const float (&v)[8], float s) {
+FP8MOE_DEV void put_chunk(const NormFwdArgs& a, int64_t row, int ch, bool ok, const Vec8& v, float s) {
   if (a.y && ok) *reinterpret_cast<uint4*>(a.y + row * a.H + (int64_t)ch * 8) = pack8(v);
   if constexpr (OUT == NORM_OUT_MX) {
-    float m = absmax8(v);
+    float m = absmax8(0.0f, v);
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const uint32_t b = mx_byte(m, s);
@@ -135,7 +141,7 @@ FP8MOE_DEV void zero_scale_pad(const NormFwdArgs& a, int64_t row, int t, int n) 
 // A CTA holds `groups` rows, wpr warps each; a thread V chunks of its row.
 template <int V, int OUT, bool W32>
 __global__ void __launch_bounds__(norm_threads<V>()) k_norm_fwd(NormFwdArgs a, int wpr) {
-  __shared__ float red[2][32];
+  __shared__ __align__(16) float red[2][NORM_RED];
   const int warp = threadIdx.x >> 5, group = warp / wpr, wrow = warp % wpr;
   const int tpr = wpr * 32, t = threadIdx.x - group * tpr;
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + group;
@@ -149,22 +155,22 @@ __global__ void __launch_bounds__(norm_threads<V>()) k_norm_fwd(NormFwdArgs a, i
     xv[i] = ok ? ld16(a.x + row * a.ldx + (int64_t)ch * 8) : make_uint4(0, 0, 0, 0);
     rv[i] = ok && a.r ? ld16(a.r + row * a.ldr + (int64_t)ch * 8) : make_uint4(0, 0, 0, 0);
   }
-  float v[V][8];
-  float ss = 0.0f;
+  Vec8 v[V];
+  uint64_t ss2 = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    unpack8(xv[i], v[i]);
+    v[i] = unpack8(xv[i]);
     if (a.r) {
-      float f[8];
-      unpack8(rv[i], f);
+      const Vec8 f = unpack8(rv[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] += f[j];
+      for (int j = 0; j < 4; ++j) v[i].p[j] = add2(v[i].p[j], f.p[j]);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+    for (int j = 0; j < 4; ++j) ss2 = fma2(v[i].p[j], v[i].p[j], ss2);
   }
-  ss = row_reduce<false>(ss, red[0], wpr, group, wrow);
+  const float ss = row_reduce<false>(sum_of(ss2), red[0], wpr, group, wrow);
   const float rstd = rsqrtf(__fdiv_rn(ss, (float)a.H) + a.eps);
+  const uint64_t rstd2 = pk(rstd, rstd);
   if (active && a.rstd && t == 0) a.rstd[row] = rstd;
   float am = 0.0f;
 #pragma unroll
@@ -172,16 +178,11 @@ __global__ void __launch_bounds__(norm_threads<V>()) k_norm_fwd(NormFwdArgs a, i
     const int ch = t + i * tpr;
     const bool ok = active && ch < nch;
     if (a.h && ok) *reinterpret_cast<uint4*>(a.h + row * a.H + (int64_t)ch * 8) = pack8(v[i]);
-    float wf[8];
-    if (ok) {
-      load_w8<W32>(a.w, ch, wf);
-    } else {
+    // (chunks past the row are zero, as their weights are)
+    const Vec8 wf = ok ? load_w8<W32>(a.w, ch) : Vec8{};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) wf[j] = 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = ok ? v[i][j] * rstd * wf[j] : 0.0f;
-    if (OUT >= NORM_OUT_ROW) am = fmaxf(am, absmax8(v[i]));
+    for (int j = 0; j < 4; ++j) v[i].p[j] = ok ? mul2(mul2(v[i].p[j], rstd2), wf.p[j]) : 0;
+    if (OUT >= NORM_OUT_ROW) am = absmax8(am, v[i]);
   }
   float s = 1.0f;
   if constexpr (OUT >= NORM_OUT_ROW) {
@@ -202,44 +203,41 @@ __global__ void __launch_bounds__(norm_threads<V>()) k_norm_fwd(NormFwdArgs a, i
 // row again (from L2) for each pass.
 template <int OUT, bool W32>
 __global__ void __launch_bounds__(1024) k_norm_fwd_long(NormFwdArgs a) {
-  __shared__ float red[2][32];
+  __shared__ __align__(16) float red[2][NORM_RED];
   const int64_t row = blockIdx.x;
   const int t = threadIdx.x, n = blockDim.x, nch = a.H / 8;
   const bool active = row < a.T;
-  auto load = [&](int ch, float (&v)[8]) {
-    unpack8(ld16(a.x + row * a.ldx + (int64_t)ch * 8), v);
+  auto load = [&](int ch) {
+    Vec8 v = unpack8(ld16(a.x + row * a.ldx + (int64_t)ch * 8));
     if (a.r) {
-      float f[8];
-      unpack8(ld16(a.r + row * a.ldr + (int64_t)ch * 8), f);
+      const Vec8 f = unpack8(ld16(a.r + row * a.ldr + (int64_t)ch * 8));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += f[j];
+      for (int j = 0; j < 4; ++j) v.p[j] = add2(v.p[j], f.p[j]);
     }
+    return v;
   };
   if (active) {
-    float ss = 0.0f;
+    uint64_t ss2 = 0;
     for (int ch = t; ch < nch; ch += n) {
-      float v[8];
-      load(ch, v);
+      const Vec8 v = load(ch);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+      for (int j = 0; j < 4; ++j) ss2 = fma2(v.p[j], v.p[j], ss2);
     }
-    ss = row_reduce<false>(ss, red[0], n / 32, 0, t >> 5);
+    const float ss = row_reduce<false>(sum_of(ss2), red[0], n / 32, 0, t >> 5);
     const float rstd = rsqrtf(__fdiv_rn(ss, (float)a.H) + a.eps);
     if (a.rstd && t == 0) a.rstd[row] = rstd;
-    auto norm = [&](int ch, float (&v)[8]) {
-      float wf[8];
-      load_w8<W32>(a.w, ch, wf);
+    auto norm = [&](int ch, Vec8& v) {
+      const Vec8 wf = load_w8<W32>(a.w, ch);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * wf[j];
+      for (int j = 0; j < 4; ++j) v.p[j] = mul2(mul2(v.p[j], pk(rstd, rstd)), wf.p[j]);
     };
     float s = 1.0f;
     if constexpr (OUT >= NORM_OUT_ROW) {
       float am = 0.0f, inv;
       for (int ch = t; ch < nch; ch += n) {
-        float v[8];
-        load(ch, v);
+        Vec8 v = load(ch);
         norm(ch, v);
-        am = fmaxf(am, absmax8(v));
+        am = absmax8(am, v);
       }
       am = row_reduce<true>(am, red[1], n / 32, 0, t >> 5);
       rowwise_scale<OUT == NORM_OUT_ROW_FNUZ>(am, s, inv);
@@ -248,9 +246,9 @@ __global__ void __launch_bounds__(1024) k_norm_fwd_long(NormFwdArgs a) {
     for (int c0 = 0; c0 < nch; c0 += n) {   // every lane takes every trip (block maxima are shuffles)
       const int ch = c0 + t;
       const bool ok = ch < nch;
-      float v[8] = {};
+      Vec8 v{};
       if (ok) {
-        load(ch, v);
+        v = load(ch);
         if (a.h) *reinterpret_cast<uint4*>(a.h + row * a.H + (int64_t)ch * 8) = pack8(v);
         norm(ch, v);
       }
@@ -261,15 +259,21 @@ __global__ void __launch_bounds__(1024) k_norm_fwd_long(NormFwdArgs a) {
 }
 
 template <int OUT, bool W32>
-cudaError_t launch_fwd_t(const NormFwdArgs& a, cudaStream_t st) {
+cudaError_t launch_fwd_t(const NormFwdArgs& a, int num_sms, cudaStream_t st) {
   const int nch = a.H / 8;
   if (nch > NORM_MAX_CHUNKS) {
     k_norm_fwd_long<OUT, W32><<<(unsigned)a.rows, 1024, 0, st>>>(a);
     return cudaGetLastError();
   }
-  const int v = nch <= 256 ? 1 : nch <= 512 ? 2 : 4;
+  // Chunks per thread: a row in one warp where that fits (no barriers), else
+  // four, whose loads in flight carry HBM (8192 x 4096 rowwise: 41 us against
+  // 47 with two and 62 with one); with fewer rows than SMs, where one row's
+  // latency counts, fewer chunks and more threads (one row of 4096: 2.6 us
+  // against 3.0).  CTAs of four warps or one row.
+  const bool few = a.T < num_sms;
+  const int v = few ? (nch <= 512 ? 1 : nch <= 1024 ? 2 : 4) : nch <= 32 ? 1 : nch <= 64 ? 2 : 4;
   const int wpr = (nch + 32 * v - 1) / (32 * v);
-  const int groups = wpr >= 8 ? 1 : 8 / wpr;
+  const int groups = wpr >= 4 ? 1 : 4 / wpr;
   const unsigned blocks = (unsigned)((a.rows + groups - 1) / groups), threads = (unsigned)(wpr * 32 * groups);
   if (v == 1) k_norm_fwd<1, OUT, W32><<<blocks, threads, 0, st>>>(a, wpr);
   if (v == 2) k_norm_fwd<2, OUT, W32><<<blocks, threads, 0, st>>>(a, wpr);
@@ -288,105 +292,164 @@ struct NormBwdArgs {
   int H;
   uint16_t* dx;
   float* part;  // [gridDim.x][H] partial weight gradients
+  int* status;
 };
 
 // A CTA takes rows blockIdx.x, blockIdx.x + gridDim.x, ... whole; a thread
 // keeps the same V chunks of every row, so its share of dw stays in registers.
+// The rows come through a ring of `stages` slots that thread 0 fills with bulk
+// copies: the slot of row i - 1 is free at row i's barrier (every thread has
+// then read it) and takes row i - 1 + stages.
 template <int V, bool W32>
-__global__ void __launch_bounds__(512) k_norm_bwd(NormBwdArgs a) {
-  __shared__ float red[2][32];
+__global__ void __launch_bounds__(512) k_norm_bwd(NormBwdArgs a, int stages) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(16) float red[2][NORM_RED];
+  __shared__ uint64_t full[NORM_BWD_STAGES];
+  __shared__ int abort_s, fills[NORM_BWD_STAGES];   // fills: thread 0's count per slot
+  volatile int* abort_flag = &abort_s;
   const int t = threadIdx.x, n = blockDim.x, nch = a.H / 8, warps = n >> 5;
-  float dw[V][8] = {};
-  int par = 0;
-  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, par ^= 1) {
-    uint4 dyv[V], hv[V], sv[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int ch = t + i * n;
-      const int64_t at = row * a.H + (int64_t)ch * 8;
-      const uint4 z = make_uint4(0, 0, 0, 0);
-      dyv[i] = ch < nch ? ld16(a.dy + at) : z;
-      hv[i] = ch < nch ? ld16(a.h + at) : z;
-      sv[i] = ch < nch && a.dh ? ld16(a.dh + at) : z;
+  const uint32_t row_bytes = (uint32_t)a.H * 2;
+  const uint32_t slot_bytes = row_bytes * (a.dh ? 3 : 2);
+  // thread 0: row nrow, the next to load, goes to slot nslot
+  int64_t nrow = blockIdx.x;
+  int nslot = 0;
+  auto issue = [&]() {
+    uint8_t* dst = ring + nslot * slot_bytes;
+    const int64_t at = nrow * a.H;
+    ++fills[nslot];
+    mbar_expect_tx(&full[nslot], slot_bytes);
+    bulk_load(dst, a.dy + at, row_bytes, &full[nslot]);
+    bulk_load(dst + row_bytes, a.h + at, row_bytes, &full[nslot]);
+    if (a.dh) bulk_load(dst + 2 * row_bytes, a.dh + at, row_bytes, &full[nslot]);
+    nrow += gridDim.x;
+    if (++nslot == stages) nslot = 0;
+  };
+  const float rh = __frcp_rn((float)a.H);
+  if (t == 0) {
+    abort_s = 0;
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      fills[s] = 0;
     }
+    mbar_fence_init();
+    for (int s = 0; s < stages - 1 && nrow < a.T; ++s) issue();
+  }
+  Vec8 dw[V];
+  // bf16 weights stay in registers where there is room; others come from L1
+  constexpr bool KEEP_W = !W32 && V <= 2;
+  uint4 w4[KEEP_W ? V : 1];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    dw[i] = Vec8{};
+    if constexpr (KEEP_W)
+      w4[i] = t + i * n < nch ? reinterpret_cast<const uint4*>(a.w)[t + i * n] : make_uint4(0, 0, 0, 0);
+  }
+  __syncthreads();
+  int s = 0, par = 0;
+  uint32_t phase = 0;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
     const float rstd = a.rstd[row];
-    float dot = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float d[8], x[8], wf[8];
-      if (t + i * n >= nch) continue;
-      unpack8(dyv[i], d);
-      unpack8(hv[i], x);
-      load_w8<W32>(a.w, t + i * n, wf);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float xh = x[j] * rstd;
-        dot = fmaf(d[j] * wf[j], xh, dot);
-        dw[i][j] = fmaf(d[j], xh, dw[i][j]);
-      }
+    const uint64_t rstd2 = pk(rstd, rstd);
+    if (!mbar_wait(&full[s], phase, abort_flag)) {
+      set_status(a.status, FP8MOE_ERR_TIMEOUT);
+      *abort_flag = 1;
     }
-    // the two halves of `red` alternate: a row's sums are read before the
-    // barrier of the next row, which writes the other half
-    dot = row_reduce<false>(dot, red[par], warps, 0, t >> 5);
-    const float c = __fdiv_rn(dot, (float)a.H);
+    const uint8_t* src = ring + s * slot_bytes;
+    Vec8 g[V], xh[V];
+    uint64_t dot2 = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int ch = t + i * n;
       if (ch >= nch) continue;
-      float d[8], x[8], s[8], wf[8], o[8];
-      unpack8(dyv[i], d);
-      unpack8(hv[i], x);
-      unpack8(sv[i], s);
-      load_w8<W32>(a.w, ch, wf);
+      const uint4 dq = *reinterpret_cast<const uint4*>(src + ch * 16);
+      const Vec8 d = unpack8(dq), x = unpack8(*reinterpret_cast<const uint4*>(src + row_bytes + ch * 16));
+      if constexpr (!KEEP_W) {
+        const Vec8 wf = load_w8<W32>(a.w, ch);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = fmaf(rstd, fmaf(-x[j] * rstd, c, d[j] * wf[j]), s[j]);
+        for (int j = 0; j < 4; ++j) g[i].p[j] = mul2(d.p[j], wf.p[j]);
+      } else {
+        g[i] = {{mulx(dq.x, w4[i].x), mulx(dq.y, w4[i].y), mulx(dq.z, w4[i].z), mulx(dq.w, w4[i].w)}};
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        xh[i].p[j] = mul2(x.p[j], rstd2);
+        dot2 = fma2(g[i].p[j], xh[i].p[j], dot2);
+        dw[i].p[j] = fma2(d.p[j], xh[i].p[j], dw[i].p[j]);
+      }
+    }
+    // the two halves of `red` alternate: a row's sums are read before the
+    // barrier of the next row, which writes the other half
+    const float dot = row_reduce<false>(sum_of(dot2), red[par], warps, 0, t >> 5);
+    par ^= 1;
+    if (warps == 1) __syncwarp();
+    // past this barrier every thread has read the row before
+    if (t == 0 && nrow < a.T && !*abort_flag) {
+      fence_proxy_async_smem();
+      issue();
+    }
+    const float c = -dot * rh;
+    const uint64_t c2 = pk(c, c);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int ch = t + i * n;
+      if (ch >= nch) continue;
+      const Vec8 sv = a.dh ? unpack8(*reinterpret_cast<const uint4*>(src + 2 * row_bytes + ch * 16)) : Vec8{};
+      Vec8 o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o.p[j] = fma2(rstd2, fma2(xh[i].p[j], c2, g[i].p[j]), sv.p[j]);
       *reinterpret_cast<uint4*>(a.dx + row * a.H + (int64_t)ch * 8) = pack8(o);
     }
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
   }
+  // after a wait that ran out rows may be in flight still: none may land in
+  // shared memory that is no longer this CTA's
+  if (t == 0 && *abort_flag)
+    for (int i = 0; i < stages; ++i)
+      if (fills[i] > 0) (void)mbar_wait(&full[i], (uint32_t)(fills[i] - 1) & 1u, nullptr);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int ch = t + i * n;
     if (ch >= nch) continue;
-    float4* p = reinterpret_cast<float4*>(a.part + (int64_t)blockIdx.x * a.H + (int64_t)ch * 8);
-    p[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-    p[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+    uint64_t* p = reinterpret_cast<uint64_t*>(a.part + (int64_t)blockIdx.x * a.H + (int64_t)ch * 8);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = dw[i].p[j];
   }
 }
 
 // Rows longer than that: the row is read twice (the second time from L2) and
 // a thread's share of dw stays in its CTA's row of the partials.
 template <bool W32>
-__global__ void __launch_bounds__(512) k_norm_bwd_long(NormBwdArgs a) {
-  __shared__ float red[2][32];
+__global__ void __launch_bounds__(512) k_norm_bwd_long(NormBwdArgs a, int) {
+  __shared__ __align__(16) float red[2][NORM_RED];
   const int t = threadIdx.x, n = blockDim.x, nch = a.H / 8;
   float* part = a.part + (int64_t)blockIdx.x * a.H;
   int par = 0;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, par ^= 1) {
     const float rstd = a.rstd[row];
-    float dot = 0.0f;
+    const uint64_t rstd2 = pk(rstd, rstd);
+    uint64_t dot2 = 0;
     for (int ch = t; ch < nch; ch += n) {
-      float d[8], x[8], wf[8];
-      unpack8(ld16(a.dy + row * a.H + (int64_t)ch * 8), d);
-      unpack8(ld16(a.h + row * a.H + (int64_t)ch * 8), x);
-      load_w8<W32>(a.w, ch, wf);
+      const Vec8 d = unpack8(ld16(a.dy + row * a.H + (int64_t)ch * 8));
+      const Vec8 x = unpack8(ld16(a.h + row * a.H + (int64_t)ch * 8)), wf = load_w8<W32>(a.w, ch);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dot = fmaf(d[j] * wf[j], x[j] * rstd, dot);
+      for (int j = 0; j < 4; ++j) dot2 = fma2(mul2(d.p[j], wf.p[j]), mul2(x.p[j], rstd2), dot2);
     }
-    dot = row_reduce<false>(dot, red[par], n >> 5, 0, t >> 5);
-    const float c = __fdiv_rn(dot, (float)a.H);
+    const float dot = row_reduce<false>(sum_of(dot2), red[par], n >> 5, 0, t >> 5);
+    const float c = -__fdiv_rn(dot, (float)a.H);
     for (int ch = t; ch < nch; ch += n) {
       const int64_t at = row * a.H + (int64_t)ch * 8;
-      float d[8], x[8], s[8] = {}, wf[8], o[8];
-      unpack8(ld16(a.dy + at), d);
-      unpack8(ld16(a.h + at), x);
-      if (a.dh) unpack8(ld16(a.dh + at), s);
-      load_w8<W32>(a.w, ch, wf);
+      const Vec8 d = unpack8(ld16(a.dy + at)), x = unpack8(ld16(a.h + at)), wf = load_w8<W32>(a.w, ch);
+      const Vec8 sv = a.dh ? unpack8(ld16(a.dh + at)) : Vec8{};
+      uint64_t* p = reinterpret_cast<uint64_t*>(part + (int64_t)ch * 8);
+      Vec8 o;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float xh = x[j] * rstd;
-        float* p = part + (int64_t)ch * 8 + j;
-        *p = row == blockIdx.x ? d[j] * xh : fmaf(d[j], xh, *p);
-        o[j] = fmaf(rstd, fmaf(-xh, c, d[j] * wf[j]), s[j]);
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t xh = mul2(x.p[j], rstd2);
+        p[j] = fma2(d.p[j], xh, row == blockIdx.x ? 0 : p[j]);
+        o.p[j] = fma2(rstd2, fma2(xh, pk(c, c), mul2(d.p[j], wf.p[j])), sv.p[j]);
       }
       *reinterpret_cast<uint4*>(a.dx + at) = pack8(o);
     }
@@ -411,23 +474,27 @@ __global__ void __launch_bounds__(1024) k_norm_dw(const float* __restrict__ part
 }
 
 template <bool W32>
-cudaError_t launch_bwd_t(NormBwdArgs a, float* dw, int num_sms, cudaStream_t st) {
+cudaError_t launch_bwd_t(NormBwdArgs a, float* dw, int num_sms, int max_smem, cudaStream_t st) {
   const int nch = a.H / 8;
-  int64_t P = NORM_BWD_PARTS < a.T ? NORM_BWD_PARTS : a.T;
-  auto run = [&](auto kern, std::atomic<int>& slot, int threads) {
-    const int64_t fit = (int64_t)num_sms * blocks_per_sm(slot, kern, threads, 0, 1);
-    if (P > fit) P = fit;
-    kern<<<(unsigned)P, threads, 0, st>>>(a);
-  };
-  // one occupancy figure per CTA size (in warps) of each kernel
-  static std::atomic<int> occ[4][17] = {};
   const int v = nch <= 256 ? 1 : nch <= 1024 ? 2 : 4;
   const int warps = nch > NORM_MAX_CHUNKS ? 16 : (nch + 32 * v - 1) / (32 * v);
-  if (nch > NORM_MAX_CHUNKS) run(k_norm_bwd_long<W32>, occ[3][warps], warps * 32);
-  else if (v == 1) run(k_norm_bwd<1, W32>, occ[0][warps], warps * 32);
-  else if (v == 2) run(k_norm_bwd<2, W32>, occ[1][warps], warps * 32);
-  else run(k_norm_bwd<4, W32>, occ[2][warps], warps * 32);
-  cudaError_t e = cudaGetLastError();
+  // CTAs that fit: at most 2048 threads, and a ring of three rows each
+  const int slot = a.H * 2 * (a.dh ? 3 : 2);
+  const int budget = max_smem - 1024;
+  const int stages = slot * 3 <= budget ? 3 : 2;
+  const bool ring = nch <= NORM_MAX_CHUNKS && slot * stages <= budget;
+  int64_t P = NORM_BWD_PARTS < a.T ? NORM_BWD_PARTS : a.T;
+  auto run = [&](auto kern) {
+    const int smem = ring ? slot * stages : 0;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    int per = 0;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, warps * 32, smem);
+    if (e != cudaSuccess || per < 1) return e == cudaSuccess ? cudaErrorInvalidConfiguration : e;
+    if (P > (int64_t)num_sms * per) P = (int64_t)num_sms * per;
+    kern<<<(unsigned)P, warps * 32, smem, st>>>(a, stages);
+    return cudaGetLastError();
+  };
+  cudaError_t e = !ring ? run(k_norm_bwd_long<W32>) : v == 1 ? run(k_norm_bwd<1, W32>) : v == 2 ? run(k_norm_bwd<2, W32>) : run(k_norm_bwd<4, W32>);
   if (e != cudaSuccess) return e;
   k_norm_dw<<<(unsigned)((a.H + 31) / 32), 1024, 0, st>>>(a.part, (int)P, a.H, dw);
   return cudaGetLastError();
@@ -437,7 +504,7 @@ cudaError_t launch_bwd_t(NormBwdArgs a, float* dw, int num_sms, cudaStream_t st)
 
 cudaError_t launch_norm_fwd(const void* x, int64_t ldx, const void* r, int64_t ldr, const void* w, int w32, int64_t T,
                             int64_t H, float eps, void* h, void* y, float* rstd, int recipe, int kind, void* q,
-                            void* scale, int scale_layout, cudaStream_t st) {
+                            void* scale, int scale_layout, int num_sms, cudaStream_t st) {
   NormFwdArgs a{};
   a.x = (const uint16_t*)x, a.r = (const uint16_t*)r;
   a.ldx = ldx, a.ldr = ldr, a.T = a.rows = T, a.H = (int)H;
@@ -452,7 +519,7 @@ cudaError_t launch_norm_fwd(const void* x, int64_t ldx, const void* r, int64_t l
     a.inv = (float*)scale;
   }
 #define FP8MOE_NORM(O) \
-  if (out == O) return w32 ? launch_fwd_t<O, true>(a, st) : launch_fwd_t<O, false>(a, st);
+  if (out == O) return w32 ? launch_fwd_t<O, true>(a, num_sms, st) : launch_fwd_t<O, false>(a, num_sms, st);
   FP8MOE_NORM(NORM_OUT_NONE)
   FP8MOE_NORM(NORM_OUT_MX)
   FP8MOE_NORM(NORM_OUT_ROW)
@@ -462,13 +529,13 @@ cudaError_t launch_norm_fwd(const void* x, int64_t ldx, const void* r, int64_t l
 }
 
 cudaError_t launch_norm_bwd(const void* dy, const void* h, const float* rstd, const void* w, int w32, const void* dh,
-                            int64_t T, int64_t H, void* dx, float* dw, void* workspace, int num_sms,
-                            cudaStream_t st) {
+                            int64_t T, int64_t H, void* dx, float* dw, void* workspace, int num_sms, int max_smem,
+                            int* status, cudaStream_t st) {
   if (T == 0) return cudaMemsetAsync(dw, 0, (size_t)H * sizeof(float), st);
   NormBwdArgs a{};
   a.dy = (const uint16_t*)dy, a.h = (const uint16_t*)h, a.dh = (const uint16_t*)dh, a.rstd = rstd, a.w = w;
-  a.T = T, a.H = (int)H, a.dx = (uint16_t*)dx, a.part = (float*)workspace;
-  return w32 ? launch_bwd_t<true>(a, dw, num_sms, st) : launch_bwd_t<false>(a, dw, num_sms, st);
+  a.T = T, a.H = (int)H, a.dx = (uint16_t*)dx, a.part = (float*)workspace, a.status = status;
+  return w32 ? launch_bwd_t<true>(a, dw, num_sms, max_smem, st) : launch_bwd_t<false>(a, dw, num_sms, max_smem, st);
 }
 
 }  // namespace fp8moe

@@ -467,13 +467,20 @@ cudaError_t launch_router_bwd(const RouterArgs& a, int num_sms, cudaStream_t st)
 #undef FP8MOE_ROUTER
 
 cudaError_t launch_route_weight_grad(const void* dout, const void* y, const int32_t* row_of, int64_t T, int64_t N,
-                                     int64_t k, float* dw, int num_sms, cudaStream_t st) {
+                                     int64_t k, float* dw, cudaStream_t st) {
   const uint16_t *d = (const uint16_t*)dout, *yp = (const uint16_t*)y;
-  // a warp per token where that fills the GPU, eight where tokens are few
-  const bool many = T >= (int64_t)num_sms * 16;
-#define FP8MOE_WG(UK)                                                                                            \
-  many ? k_route_weight_grad<1, UK><<<(unsigned)((T + 7) / 8), 256, 0, st>>>(d, yp, row_of, T, N, (int)k, dw)    \
-       : k_route_weight_grad<8, UK><<<(unsigned)T, 256, 0, st>>>(d, yp, row_of, T, N, (int)k, dw)
+  // Warps per token: every warp with 32 chunks of its own, at most eight (4096
+  // tokens x 8 rows of 7168: 79.8 us with eight, 82 with four, 101 with one,
+  // whose few long-lived CTAs leave SMs idle at the end)
+  const int64_t nv = N / 8;
+#define FP8MOE_WG_(WPT, UK)                                                                                  \
+  k_route_weight_grad<WPT, UK>                                                                               \
+      <<<(unsigned)((T + 8 / WPT - 1) / (8 / WPT)), 256, 0, st>>>(d, yp, row_of, T, N, (int)k, dw)
+#define FP8MOE_WG(UK)                   \
+  if (nv >= 256) FP8MOE_WG_(8, UK);     \
+  else if (nv >= 128) FP8MOE_WG_(4, UK); \
+  else if (nv >= 64) FP8MOE_WG_(2, UK);  \
+  else FP8MOE_WG_(1, UK)
   if (k <= 1) {
     FP8MOE_WG(1);
   } else if (k <= 2) {
@@ -483,6 +490,7 @@ cudaError_t launch_route_weight_grad(const void* dout, const void* y, const int3
   } else {
     FP8MOE_WG(8);
   }
+#undef FP8MOE_WG_
 #undef FP8MOE_WG
   return cudaGetLastError();
 }

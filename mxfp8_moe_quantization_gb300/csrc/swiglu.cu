@@ -22,6 +22,7 @@
 // with every lane deriving every scale, expf and a division, and 45
 // instructions per element instead of about 20, took 152 and 283 us.
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "launch.h"
 #include "moe_ops.h"
 #include "mxcvt.cuh"
@@ -36,38 +37,6 @@ namespace {
 constexpr int SG_ROWS = 32, SG_COLS = 64, SG_RW = 2, SG_CW = 2, SG_WARPS = SG_RW * SG_CW;
 constexpr int CW = 8;   // columns per lane
 
-FP8MOE_DEV uint64_t pk(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-FP8MOE_DEV void unpk(uint64_t p, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
-FP8MOE_DEV uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-FP8MOE_DEV uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-FP8MOE_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-FP8MOE_DEV uint64_t unpk_bf16(uint32_t w) { return pk(bf16_lo(w), bf16_hi(w)); }
-// the products of two bf16 pairs, exact in fp32 (mixed-precision fma on the
-// halves: no unpacking)
-FP8MOE_DEV uint64_t mulx(uint32_t a, uint32_t b) {
-  float x, y;
-  asm("{\n .reg .b16 a, b, c, d;\n mov.b32 {a, b}, %2;\n mov.b32 {c, d}, %3;\n fma.rn.f32.bf16 %0, a, c, %4;\n"
-      " fma.rn.f32.bf16 %1, b, d, %4;\n}"
-      : "=f"(x), "=f"(y)
-      : "r"(a), "r"(b), "f"(-0.0f));
-  return pk(x, y);
-}
 // -g of a bf16 pair, cut to +-88, as fp32
 FP8MOE_DEV uint64_t neg_cut(uint32_t g) {
   uint32_t n;
@@ -76,19 +45,6 @@ FP8MOE_DEV uint64_t neg_cut(uint32_t g) {
       : "r"(g), "r"(0x42B042B0u), "r"(0xC2B0C2B0u));
   return unpk_bf16(n);
 }
-// max(|a|, |b|, |c|)
-FP8MOE_DEV float amax3(float a, float b, float c) {
-  float r;
-  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-FP8MOE_DEV uint32_t pack_bf16x2(uint64_t p) {
-  float a, b;
-  unpk(p, a, b);
-  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 // sigmoid of a pair from n = -g: 1 / (1 + 2^t (1 + r)) with t = n / ln 2 rounded
 // and r the rest n - t ln 2, whose exponential is 1 + r (Cody and Waite's
 // two-part ln 2; |r| < 2^-17).  |g| is cut at 88, where the sigmoid is 1 or
@@ -138,12 +94,6 @@ FP8MOE_DEV int64_t padded_row(const int32_t* __restrict__ offs, int E, int64_t M
   }
   if (__any_sync(0xffffffffu, bad)) return -1;
   return (int64_t)__reduce_add_sync(0xffffffffu, sum);
-}
-
-FP8MOE_DEV uint32_t block_byte(float amax, float& mul) {
-  const uint32_t b = max(__float_as_uint(amax) >> 23, 8u) - 8u;
-  mul = __uint_as_float((254u - b) << 23);
-  return b;
 }
 
 // One step of a maximum over lanes that differ in `mask`: the lower lane goes
@@ -202,9 +152,7 @@ FP8MOE_DEV void put_tile(const SwigluArgs& a, const TilePlace& tp, int64_t col0,
       m[i] = 0.0f;
 #pragma unroll
       for (int p = 0; p < CW / 2; ++p) {
-        float x, y;
-        unpk(v[i][p], x, y);
-        m[i] = amax3(m[i], x, y);
+        m[i] = amax3(m[i], v[i][p]);
       }
     }
     // a row block is the four lanes that differ in cq's low bits; a lane ends
@@ -217,7 +165,7 @@ FP8MOE_DEV void put_tile(const SwigluArgs& a, const TilePlace& tp, int64_t col0,
     const int64_t c0 = a.s0_layout != FP8MOE_SCALES_ROWMAJOR ? (blk >> 2) * 512 + (blk & 3) : blk;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const uint32_t b = block_byte(mk[s], mul[s]);
+      const uint32_t b = mx_byte(mk[s], mul[s]);
       const int i = own + s;
       if (ok && i < rows) tp.s0[i * tp.step0 + c0] = (uint8_t)b;
     }
@@ -255,7 +203,7 @@ FP8MOE_DEV void put_tile(const SwigluArgs& a, const TilePlace& tp, int64_t col0,
     const int own = ((lane >> 3) & 1) * 4 + ((lane >> 4) & 1) * 2;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const uint32_t b = block_byte(mk[s], mul[s]);
+      const uint32_t b = mx_byte(mk[s], mul[s]);
       const int64_t c = col + own + s;
       if (ok)
         tp.s1[tp.band1 ? (c >> 7) * tp.band1 + (c & 31) * 16 + ((c >> 5) & 3) * 4 : c * (a.M / 32)] = (uint8_t)b;
