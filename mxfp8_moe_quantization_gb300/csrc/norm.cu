@@ -25,7 +25,11 @@ namespace {
 // up to 64 registers, V = 2 and 4 in up to 128).
 template <int V>
 constexpr int norm_threads() { return V == 1 ? 1024 : 512; }
-constexpr int NORM_BWD_STAGES = 4;   // most slots of the backward's ring
+// The backward's: V = 1 and 2 in up to 96 registers, so that two CTAs of 320
+// threads share an SM
+template <int V>
+constexpr int norm_bwd_threads() { return V == 4 ? 512 : 640; }
+constexpr int NORM_BWD_STAGES = 4;   // most slots of its ring
 constexpr int NORM_MAX_CHUNKS = 4 * norm_threads<4>();   // longer rows (H > 16384) take the looping kernels
 
 // partial values of a CTA's rows: at most 16 warps, each row's padded to fours
@@ -295,44 +299,47 @@ struct NormBwdArgs {
   int* status;
 };
 
-// A CTA takes rows blockIdx.x, blockIdx.x + gridDim.x, ... whole; a thread
-// keeps the same V chunks of every row, so its share of dw stays in registers.
-// The rows come through a ring of `stages` slots that thread 0 fills with bulk
-// copies: the slot of row i - 1 is free at row i's barrier (every thread has
-// then read it) and takes row i - 1 + stages.
+// A CTA takes blocks of `groups` consecutive rows, blockIdx.x, blockIdx.x +
+// gridDim.x, ..., wpr warps a row; a thread keeps the same V chunks of every
+// row, so its share of dw stays in registers.  The blocks come through a ring
+// of `stages` slots that thread 0 fills with bulk copies: the slot of a block
+// is free at the next block's barrier (every thread has then read it).
 template <int V, bool W32>
-__global__ void __launch_bounds__(512) k_norm_bwd(NormBwdArgs a, int stages) {
+__global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs a, int wpr, int stages) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(16) float red[2][NORM_RED];
   __shared__ uint64_t full[NORM_BWD_STAGES];
   __shared__ int abort_s, fills[NORM_BWD_STAGES];   // fills: thread 0's count per slot
   volatile int* abort_flag = &abort_s;
-  const int t = threadIdx.x, n = blockDim.x, nch = a.H / 8, warps = n >> 5;
-  const uint32_t row_bytes = (uint32_t)a.H * 2;
-  const uint32_t slot_bytes = row_bytes * (a.dh ? 3 : 2);
-  // thread 0: row nrow, the next to load, goes to slot nslot
-  int64_t nrow = blockIdx.x;
+  const int tpr = wpr * 32, groups = blockDim.x / tpr, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
+  const int nch = a.H / 8;
+  const uint32_t row_bytes = (uint32_t)a.H * 2, ten_bytes = row_bytes * groups;
+  const uint32_t slot_bytes = ten_bytes * (a.dh ? 3 : 2);
+  const int64_t blocks = (a.T + groups - 1) / groups;
+  // thread 0: block nblk, the next to load, goes to slot nslot
+  int64_t nblk = blockIdx.x;
   int nslot = 0;
   auto issue = [&]() {
     uint8_t* dst = ring + nslot * slot_bytes;
-    const int64_t at = nrow * a.H;
+    const int64_t r0 = nblk * groups, at = r0 * a.H;
+    const uint32_t bytes = row_bytes * (uint32_t)(a.T - r0 < groups ? a.T - r0 : groups);
     ++fills[nslot];
-    mbar_expect_tx(&full[nslot], slot_bytes);
-    bulk_load(dst, a.dy + at, row_bytes, &full[nslot]);
-    bulk_load(dst + row_bytes, a.h + at, row_bytes, &full[nslot]);
-    if (a.dh) bulk_load(dst + 2 * row_bytes, a.dh + at, row_bytes, &full[nslot]);
-    nrow += gridDim.x;
+    mbar_expect_tx(&full[nslot], bytes * (a.dh ? 3 : 2));
+    bulk_load(dst, a.dy + at, bytes, &full[nslot]);
+    bulk_load(dst + ten_bytes, a.h + at, bytes, &full[nslot]);
+    if (a.dh) bulk_load(dst + 2 * ten_bytes, a.dh + at, bytes, &full[nslot]);
+    nblk += gridDim.x;
     if (++nslot == stages) nslot = 0;
   };
   const float rh = __frcp_rn((float)a.H);
-  if (t == 0) {
+  if (threadIdx.x == 0) {
     abort_s = 0;
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       fills[s] = 0;
     }
     mbar_fence_init();
-    for (int s = 0; s < stages - 1 && nrow < a.T; ++s) issue();
+    for (int s = 0; s < stages - 1 && nblk < blocks; ++s) issue();
   }
   Vec8 dw[V];
   // bf16 weights stay in registers where there is room; others come from L1
@@ -342,27 +349,32 @@ __global__ void __launch_bounds__(512) k_norm_bwd(NormBwdArgs a, int stages) {
   for (int i = 0; i < V; ++i) {
     dw[i] = Vec8{};
     if constexpr (KEEP_W)
-      w4[i] = t + i * n < nch ? reinterpret_cast<const uint4*>(a.w)[t + i * n] : make_uint4(0, 0, 0, 0);
+      w4[i] = t + i * tpr < nch ? reinterpret_cast<const uint4*>(a.w)[t + i * tpr] : make_uint4(0, 0, 0, 0);
   }
+  // a row's rstd is loaded one block ahead (rows past T: 0, and nothing stored)
+  auto rstd_of = [&](int64_t b) { return b * groups + group < a.T ? a.rstd[b * groups + group] : 0.0f; };
+  float rstd = rstd_of(blockIdx.x);
   __syncthreads();
   int s = 0, par = 0;
   uint32_t phase = 0;
-  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
-    const float rstd = a.rstd[row];
+  for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+    const int64_t row = b * groups + group;
+    const bool live = row < a.T;
+    const float rstd_next = rstd_of(b + gridDim.x);
     const uint64_t rstd2 = pk(rstd, rstd);
     if (!mbar_wait(&full[s], phase, abort_flag)) {
       set_status(a.status, FP8MOE_ERR_TIMEOUT);
       *abort_flag = 1;
     }
-    const uint8_t* src = ring + s * slot_bytes;
+    const uint8_t* src = ring + s * slot_bytes + group * row_bytes;
     Vec8 g[V], xh[V];
     uint64_t dot2 = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int ch = t + i * n;
-      if (ch >= nch) continue;
+      const int ch = t + i * tpr;
+      if (ch >= nch || !live) continue;
       const uint4 dq = *reinterpret_cast<const uint4*>(src + ch * 16);
-      const Vec8 d = unpack8(dq), x = unpack8(*reinterpret_cast<const uint4*>(src + row_bytes + ch * 16));
+      const Vec8 d = unpack8(dq), x = unpack8(*reinterpret_cast<const uint4*>(src + ten_bytes + ch * 16));
       if constexpr (!KEEP_W) {
         const Vec8 wf = load_w8<W32>(a.w, ch);
 #pragma unroll
@@ -377,13 +389,13 @@ __global__ void __launch_bounds__(512) k_norm_bwd(NormBwdArgs a, int stages) {
         dw[i].p[j] = fma2(d.p[j], xh[i].p[j], dw[i].p[j]);
       }
     }
-    // the two halves of `red` alternate: a row's sums are read before the
-    // barrier of the next row, which writes the other half
-    const float dot = row_reduce<false>(sum_of(dot2), red[par], warps, 0, t >> 5);
+    // the two halves of `red` alternate: a block's sums are read before the
+    // barrier of the next one, which writes the other half
+    const float dot = row_reduce<false>(sum_of(dot2), red[par], wpr, group, (threadIdx.x >> 5) - group * wpr);
     par ^= 1;
-    if (warps == 1) __syncwarp();
-    // past this barrier every thread has read the row before
-    if (t == 0 && nrow < a.T && !*abort_flag) {
+    if (wpr == 1) __syncthreads();
+    // past this barrier every thread has read the block before
+    if (threadIdx.x == 0 && nblk < blocks && !*abort_flag) {
       fence_proxy_async_smem();
       issue();
     }
@@ -391,38 +403,54 @@ __global__ void __launch_bounds__(512) k_norm_bwd(NormBwdArgs a, int stages) {
     const uint64_t c2 = pk(c, c);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int ch = t + i * n;
-      if (ch >= nch) continue;
-      const Vec8 sv = a.dh ? unpack8(*reinterpret_cast<const uint4*>(src + 2 * row_bytes + ch * 16)) : Vec8{};
+      const int ch = t + i * tpr;
+      if (ch >= nch || !live) continue;
+      const Vec8 sv = a.dh ? unpack8(*reinterpret_cast<const uint4*>(src + 2 * ten_bytes + ch * 16)) : Vec8{};
       Vec8 o;
 #pragma unroll
       for (int j = 0; j < 4; ++j) o.p[j] = fma2(rstd2, fma2(xh[i].p[j], c2, g[i].p[j]), sv.p[j]);
       *reinterpret_cast<uint4*>(a.dx + row * a.H + (int64_t)ch * 8) = pack8(o);
     }
+    rstd = rstd_next;
     if (++s == stages) {
       s = 0;
       phase ^= 1;
     }
   }
-  // after a wait that ran out rows may be in flight still: none may land in
+  asm volatile("griddepcontrol.launch_dependents;");
+  // after a wait that ran out blocks may be in flight still: none may land in
   // shared memory that is no longer this CTA's
-  if (t == 0 && *abort_flag)
+  if (threadIdx.x == 0 && *abort_flag)
     for (int i = 0; i < stages; ++i)
       if (fills[i] > 0) (void)mbar_wait(&full[i], (uint32_t)(fills[i] - 1) & 1u, nullptr);
+  // the groups' shares of dw, added in order through the ring's memory
+  float* sum = reinterpret_cast<float*>(ring);
+  for (int q = 0; q < groups; ++q) {
+    __syncthreads();
+    if (group != q) continue;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int ch = t + i * n;
-    if (ch >= nch) continue;
-    uint64_t* p = reinterpret_cast<uint64_t*>(a.part + (int64_t)blockIdx.x * a.H + (int64_t)ch * 8);
+    for (int i = 0; i < V; ++i) {
+      const int ch = t + i * tpr;
+      if (ch >= nch) continue;
+      uint64_t* p = reinterpret_cast<uint64_t*>(sum + ch * 8);
+      uint64_t* out = reinterpret_cast<uint64_t*>(a.part + (int64_t)blockIdx.x * a.H + (int64_t)ch * 8);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) p[j] = dw[i].p[j];
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t v = q == 0 ? dw[i].p[j] : add2(p[j], dw[i].p[j]);
+        if (q == groups - 1) {
+          out[j] = v;
+        } else {
+          p[j] = v;
+        }
+      }
+    }
   }
 }
 
 // Rows longer than that: the row is read twice (the second time from L2) and
 // a thread's share of dw stays in its CTA's row of the partials.
 template <bool W32>
-__global__ void __launch_bounds__(512) k_norm_bwd_long(NormBwdArgs a, int) {
+__global__ void __launch_bounds__(512) k_norm_bwd_long(NormBwdArgs a, int, int) {
   __shared__ __align__(16) float red[2][NORM_RED];
   const int t = threadIdx.x, n = blockDim.x, nch = a.H / 8;
   float* part = a.part + (int64_t)blockIdx.x * a.H;
@@ -458,12 +486,13 @@ __global__ void __launch_bounds__(512) k_norm_bwd_long(NormBwdArgs a, int) {
 
 // dw[c] = sum over the P partials in order: 32 columns per CTA, 32 warps that
 // each take every 32nd partial, then a fixed-order sum over the warps.
-__global__ void __launch_bounds__(1024) k_norm_dw(const float* __restrict__ part, int P, int H, float* __restrict__ dw) {
+__global__ void __launch_bounds__(1024) k_norm_dw(const float* part, int P, int H, float* __restrict__ dw) {
   __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float v = 0.0f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c < H)
-#pragma unroll 4
+#pragma unroll 10
     for (int p = warp; p < P; p += 32) v += part[(int64_t)p * H + c];
   s[warp][lane] = v;
   __syncthreads();
@@ -476,28 +505,46 @@ __global__ void __launch_bounds__(1024) k_norm_dw(const float* __restrict__ part
 template <bool W32>
 cudaError_t launch_bwd_t(NormBwdArgs a, float* dw, int num_sms, int max_smem, cudaStream_t st) {
   const int nch = a.H / 8;
-  const int v = nch <= 256 ? 1 : nch <= 1024 ? 2 : 4;
-  const int warps = nch > NORM_MAX_CHUNKS ? 16 : (nch + 32 * v - 1) / (32 * v);
-  // CTAs that fit: at most 2048 threads, and a ring of three rows each
-  const int slot = a.H * 2 * (a.dh ? 3 : 2);
-  const int budget = max_smem - 1024;
-  const int stages = slot * 3 <= budget ? 3 : 2;
+  const int v = nch <= 32 ? 1 : nch <= 1024 ? 2 : 4;
+  // CTAs of eight warps or one row (65536 x 512: 50 us, 114 with a row per CTA)
+  int wpr = nch > NORM_MAX_CHUNKS ? 16 : (nch + 32 * v - 1) / (32 * v);
+  int groups = wpr >= 8 ? 1 : 8 / wpr;
+  // The ring: as deep as lets two CTAs share an SM, at least three blocks if
+  // they fit one (16384 x 5120: 108 us with three, 132 with two)
+  const int64_t budget = max_smem - 2048;
+  const int64_t slot = (int64_t)a.H * 2 * (a.dh ? 3 : 2) * groups;
+  int stages = (int)(budget / 2 / slot < NORM_BWD_STAGES ? budget / 2 / slot : NORM_BWD_STAGES);
+  if (stages < 3) stages = slot * 3 <= budget ? 3 : 2;
   const bool ring = nch <= NORM_MAX_CHUNKS && slot * stages <= budget;
-  int64_t P = NORM_BWD_PARTS < a.T ? NORM_BWD_PARTS : a.T;
+  if (!ring) wpr = 16, groups = 1;
+  const int64_t blocks = (a.T + groups - 1) / groups;
+  int64_t P = NORM_BWD_PARTS < blocks ? NORM_BWD_PARTS : blocks;
   auto run = [&](auto kern) {
-    const int smem = ring ? slot * stages : 0;
+    const int smem = ring ? (int)(slot * stages) : 0;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     int per = 0;
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, warps * 32, smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, wpr * 32 * groups, smem);
     if (e != cudaSuccess || per < 1) return e == cudaSuccess ? cudaErrorInvalidConfiguration : e;
     if (P > (int64_t)num_sms * per) P = (int64_t)num_sms * per;
-    kern<<<(unsigned)P, warps * 32, smem, st>>>(a, stages);
+    kern<<<(unsigned)P, wpr * 32 * groups, smem, st>>>(a, wpr, stages);
     return cudaGetLastError();
   };
-  cudaError_t e = !ring ? run(k_norm_bwd_long<W32>) : v == 1 ? run(k_norm_bwd<1, W32>) : v == 2 ? run(k_norm_bwd<2, W32>) : run(k_norm_bwd<4, W32>);
+  cudaError_t e = !ring    ? run(k_norm_bwd_long<W32>)
+                  : v == 1 ? run(k_norm_bwd<1, W32>)
+                  : v == 2 ? run(k_norm_bwd<2, W32>)
+                           : run(k_norm_bwd<4, W32>);
   if (e != cudaSuccess) return e;
-  k_norm_dw<<<(unsigned)((a.H + 31) / 32), 1024, 0, st>>>(a.part, (int)P, a.H, dw);
-  return cudaGetLastError();
+  // launched ahead of the first kernel's end, for which it waits
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.H + 31) / 32));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_norm_dw, (const float*)a.part, (int)P, a.H, dw);
 }
 
 }  // namespace
