@@ -11,7 +11,6 @@ device.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import Optional, Tuple
 
@@ -160,67 +159,31 @@ def _empty(shape, dtype, like):
     return _torch().empty(shape, dtype=dtype, device=like.device)
 
 
-class _Torch:
-    """What the calls below take from torch, looked up once (small calls spend
-    their time on the host)."""
-    ready = False
-
-    def load(self):
-        import torch
-        self.bf16, self.f32, self.u8, self.i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
-        self.flag = (torch.uint8, torch.bool)
-        self.empty, self.zeros, self.stream_context = torch.empty, torch.zeros, torch.cuda.stream
-        self.device, self.raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-        self.ready = True
+_BINDING = None
 
 
-_t = _Torch()
+def _native():
+    """The compiled marshalling of the small calls (csrc/binding.cpp)."""
+    global _BINDING
+    if _BINDING is None:
+        _torch()
+        _lib_raw()
+        from . import _binding
+        _BINDING = _binding
+    return _BINDING
 
 
-def _on_stream(fn):
-    """Gives ``fn`` a ``stream`` argument: the whole call, its allocations
-    among it, runs with that stream as the current one."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kwargs):
-        if not _t.ready:
-            _t.load()
-        if stream is None:
-            return fn(*args, **kwargs)
-        with _t.stream_context(stream):
-            return fn(*args, **kwargs)
-    return call
-
-
-def _refuse(fn: str):
-    raise Fp8MoeError(fn, 1)
-
-
-def _dense(fn: str, t, dtype, shape, dev: int) -> int:
-    """Address of a contiguous argument of this type and shape on device dev;
-    any other is refused (status 1)."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        _refuse(fn)
-    return t.data_ptr()
-
-
-def _rows(fn: str, t, R: int, C: int, dev: int) -> int:
-    """Row stride of a [R, C] argument on device dev whose rows are dense."""
-    if t.shape != (R, C) or t.get_device() != dev:
-        _refuse(fn)
-    if t.is_contiguous():
-        return C
-    ld, one = t.stride()
-    if one != 1 and C > 1:
-        _refuse(fn)
-    return ld if R > 1 else C
-
-
-def _device_of(fn: str, t) -> int:
-    """The device of the call: the first argument's, which has to be current."""
-    dev = t.get_device()
-    if dev < 0 or dev != _t.device():
-        _refuse(fn)
-    return dev
+def _run(fn: str, stream, call, *args):
+    """``call(*args)``, with ``stream`` (if given) as the current one for the
+    whole call, its allocations among it; a status code becomes an error."""
+    if stream is None:
+        r = call(*args)
+    else:
+        with _torch().cuda.stream(stream):
+            r = call(*args)
+    if r.__class__ is int:
+        raise Fp8MoeError(fn, r)
+    return r
 
 
 def _u8(t):
@@ -591,10 +554,9 @@ def fp8moe_mxfp8_moe_bwd(dy, offs, workspace, K: int, need_da: bool = True, need
     return da, dw
 
 
-@_on_stream
 def fp8moe_add_rmsnorm_fwd(x, weight, residual=None, eps: float = 1e-6, recipe: Optional[int] = None,
                            kind: int = E4M3FN, scale_layout: int = SCALES_ROWMAJOR, need_y: bool = True,
-                           need_rstd: bool = True, h=None, y=None, rstd=None, q=None, scale=None):
+                           need_rstd: bool = True, h=None, y=None, rstd=None, q=None, scale=None, stream=None):
     """y = (x + residual) * rsqrt(mean((x + residual)^2) + eps) * weight, rowwise.
 
     x, residual [T, H] bf16 (row strides may exceed H), weight [H] bf16 or
@@ -603,278 +565,55 @@ def fp8moe_add_rmsnorm_fwd(x, weight, residual=None, eps: float = 1e-6, recipe: 
     ``recipe``: MXFP8 codes with scales in ``scale_layout`` (SCALES_ROWMAJOR
     or NO_GROUPS) or ROWWISE codes with fp32 scales [T]; None for what is not
     asked for.  Outputs are allocated unless given; h may be x or residual."""
-    fn = "fp8moe_add_rmsnorm_fwd"
-    if x.dtype is not _t.bf16 or x.dim() != 2:
-        _refuse(fn)
-    T, H = shape = x.shape
-    dev = _device_of(fn, x)
-    ldx = _rows(fn, x, T, H, dev)
-    w32 = weight.dtype is _t.f32
-    pw = _dense(fn, weight, _t.f32 if w32 else _t.bf16, (H,), dev)
-    pr = ph = py = ps = pq = pscale = None
-    ldr = 0
-    if residual is not None:
-        if residual.dtype is not _t.bf16:
-            _refuse(fn)
-        ldr = _rows(fn, residual, T, H, dev)
-        pr = residual.data_ptr()
-        if h is None:
-            h = _t.empty(shape, dtype=_t.bf16, device=x.device)
-        ph = _dense(fn, h, _t.bf16, shape, dev)
-    elif h is not None:
-        _refuse(fn)
-    if need_y:
-        if y is None:
-            y = _t.empty(shape, dtype=_t.bf16, device=x.device)
-        py = _dense(fn, y, _t.bf16, shape, dev)
-    else:
-        y = None
-    if need_rstd:
-        if rstd is None:
-            rstd = _t.empty((T,), dtype=_t.f32, device=x.device)
-        ps = _dense(fn, rstd, _t.f32, (T,), dev)
-    else:
-        rstd = None
-    if recipe is None:
-        q = scale = None
-    else:
-        if q is None:
-            q = _t.empty(shape, dtype=_t.u8, device=x.device)
-        pq = _dense(fn, q, _t.u8, shape, dev)
-        if recipe != MXFP8:
-            if scale is None:
-                scale = _t.empty((T,), dtype=_t.f32, device=x.device)
-            pscale = _dense(fn, scale, _t.f32, (T,), dev)
-        elif scale_layout == SCALES_ROWMAJOR:
-            if scale is None:
-                scale = _t.empty((T, H // 32), dtype=_t.u8, device=x.device)
-            pscale = _dense(fn, scale, _t.u8, (T, H // 32), dev)
-        else:
-            need = fp8moe_swizzled_scales_bytes(1, T, H // 32)
-            if scale is None:
-                # room for the tiles of one group, whose layout is the same:
-                # the A operand of a one-group grouped GEMM
-                scale = _t.zeros((fp8moe_swizzled_scales_bytes(1, T, H // 32, 1, GROUP_ROWS),), dtype=_t.u8,
-                                 device=x.device)
-            n = scale.numel()
-            if n < need:
-                _refuse(fn)
-            pscale = _dense(fn, scale, _t.u8, (n,), dev)
-    code = _lib_raw().fp8moe_add_rmsnorm_fwd(x.data_ptr(), ldx, pr, ldr, pw, w32, T, H, eps, ph, py, ps,
-                                             ROWWISE if recipe is None else recipe, kind, pq, pscale, scale_layout,
-                                             _t.raw_stream(dev))
-    if code:
-        raise Fp8MoeError(fn, code)
-    return h, y, rstd, q, scale
+    return _run("fp8moe_add_rmsnorm_fwd", stream, _native().add_rmsnorm_fwd, x, weight, residual, eps, recipe, kind, scale_layout,
+                need_y, need_rstd, h, y, rstd, q, scale)
 
 
 def fp8moe_add_rmsnorm_bwd_workspace_bytes(T: int, H: int) -> int:
     return int(_lib_raw().fp8moe_add_rmsnorm_bwd_workspace_bytes(T, H))
 
 
-def _workspace(fn: str, workspace, nbytes: int, like, dev: int):
-    """(workspace, address, bytes); allocated unless given."""
-    if workspace is None:
-        workspace = _t.empty((nbytes,), dtype=_t.u8, device=like.device)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        _refuse(fn)
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-@_on_stream
-def fp8moe_add_rmsnorm_bwd(dy, h, rstd, weight, dh=None, dx=None, dweight=None, workspace=None):
+def fp8moe_add_rmsnorm_bwd(dy, h, rstd, weight, dh=None, dx=None, dweight=None, workspace=None, stream=None):
     """Backward of fp8moe_add_rmsnorm_fwd: dy, h [T, H] bf16, rstd [T] fp32,
     weight as in the forward, dh [T, H] bf16 the gradient that reaches h
     otherwise -> (dx [T, H] bf16, the gradient of x and of residual; dweight
     [H] fp32)."""
-    fn = "fp8moe_add_rmsnorm_bwd"
-    if dy.dim() != 2:
-        _refuse(fn)
-    T, H = shape = dy.shape
-    dev = _device_of(fn, dy)
-    pdy = _dense(fn, dy, _t.bf16, shape, dev)
-    pin = _dense(fn, h, _t.bf16, shape, dev)
-    prstd = _dense(fn, rstd, _t.f32, (T,), dev)
-    w32 = weight.dtype is _t.f32
-    pw = _dense(fn, weight, _t.f32 if w32 else _t.bf16, (H,), dev)
-    pdh = None if dh is None else _dense(fn, dh, _t.bf16, shape, dev)
-    if dx is None:
-        dx = _t.empty(shape, dtype=_t.bf16, device=dy.device)
-    if dweight is None:
-        dweight = _t.empty((H,), dtype=_t.f32, device=dy.device)
-    pdx = _dense(fn, dx, _t.bf16, shape, dev)
-    pdw = _dense(fn, dweight, _t.f32, (H,), dev)
-    l = _lib_raw()
-    workspace, pws, nbytes = _workspace(fn, workspace, l.fp8moe_add_rmsnorm_bwd_workspace_bytes(T, H), dy, dev)
-    code = l.fp8moe_add_rmsnorm_bwd(pdy, pin, prstd, pw, w32, pdh, T, H, pdx, pdw, pws, nbytes, _t.raw_stream(dev))
-    if code:
-        raise Fp8MoeError(fn, code)
-    return dx, dweight
+    return _run("fp8moe_add_rmsnorm_bwd", stream, _native().add_rmsnorm_bwd, dy, h, rstd, weight, dh, dx, dweight, workspace)
 
 
 def fp8moe_router_workspace_bytes(T: int, E: int) -> int:
     return int(_lib_raw().fp8moe_router_workspace_bytes(T, E))
 
 
-def _mask(fn: str, token_mask, T: int, dev: int):
-    if token_mask is None:
-        return None
-    if token_mask.dtype not in _t.flag:
-        _refuse(fn)
-    return _dense(fn, token_mask, token_mask.dtype, (T,), dev)
-
-
-@_on_stream
 def fp8moe_router_fwd(logits, k: int, score: int = SCORE_SOFTMAX, renormalize: bool = True, route_scale: float = 1.0,
                       bias=None, token_mask=None, need_balance: bool = True, topk_idx=None, topk_w=None,
-                      counts=None, prob_sum=None, balance_loss=None, workspace=None):
+                      counts=None, prob_sum=None, balance_loss=None, workspace=None, stream=None):
     """logits [T, E] bf16 or fp32 (row stride may exceed E), bias [E] fp32 (for
     the choice alone), token_mask [T] uint8 or bool (0: no token).
 
     Returns (topk_idx [T, k] int32, topk_w [T, k] fp32, counts [E + 1] int32
     (per expert, then the number of tokens), prob_sum [E] fp32, balance_loss
     [1] fp32); the last three are None without ``need_balance``."""
-    fn = "fp8moe_router_fwd"
-    f32 = logits.dtype is _t.f32
-    if not f32 and logits.dtype is not _t.bf16 or logits.dim() != 2:
-        _refuse(fn)
-    T, E = logits.shape
-    dev, on = _device_of(fn, logits), logits.device
-    ldl = _rows(fn, logits, T, E, dev)
-    pb = None if bias is None else _dense(fn, bias, _t.f32, (E,), dev)
-    pm = _mask(fn, token_mask, T, dev)
-    if topk_idx is None:
-        topk_idx = _t.empty((T, k), dtype=_t.i32, device=on)
-    if topk_w is None:
-        topk_w = _t.empty((T, k), dtype=_t.f32, device=on)
-    pi, pw = _dense(fn, topk_idx, _t.i32, (T, k), dev), _dense(fn, topk_w, _t.f32, (T, k), dev)
-    l = _lib_raw()
-    pc = pp = pl = pws = None
-    nbytes = 0
-    if need_balance:
-        if counts is None:
-            counts = _t.empty((E + 1,), dtype=_t.i32, device=on)
-        if prob_sum is None:
-            prob_sum = _t.empty((E,), dtype=_t.f32, device=on)
-        if balance_loss is None:
-            balance_loss = _t.empty((1,), dtype=_t.f32, device=on)
-        pc, pp = _dense(fn, counts, _t.i32, (E + 1,), dev), _dense(fn, prob_sum, _t.f32, (E,), dev)
-        pl = _dense(fn, balance_loss, _t.f32, (1,), dev)
-        nbytes = l.fp8moe_router_workspace_bytes(T, E)
-        if nbytes > 0:
-            workspace, pws, nbytes = _workspace(fn, workspace, nbytes, logits, dev)
-    else:
-        counts = prob_sum = balance_loss = None
-    code = l.fp8moe_router_fwd(logits.data_ptr(), f32, T, E, ldl, k, score, bool(renormalize), route_scale, pb, pm, pi, pw,
-                               pc, pp, pl, pws, nbytes, _t.raw_stream(dev))
-    if code:
-        raise Fp8MoeError(fn, code)
-    return topk_idx, topk_w, counts, prob_sum, balance_loss
+    return _run("fp8moe_router_fwd", stream, _native().router_fwd, logits, k, score, renormalize, route_scale, bias,
+                token_mask, need_balance, topk_idx, topk_w, counts, prob_sum, balance_loss, workspace)
 
 
-@_on_stream
 def fp8moe_router_bwd(logits, topk_idx, counts=None, dtopk_w=None, dloss=None, score: int = SCORE_SOFTMAX,
-                      renormalize: bool = True, route_scale: float = 1.0, token_mask=None, dlogits=None):
+                      renormalize: bool = True, route_scale: float = 1.0, token_mask=None, dlogits=None, stream=None):
     """Gradient of fp8moe_router_fwd: dtopk_w [T, k] fp32 and / or dloss [1]
     fp32 (with the forward's counts) -> dlogits [T, E] of the logits' type."""
-    fn = "fp8moe_router_bwd"
-    f32 = logits.dtype is _t.f32
-    if not f32 and logits.dtype is not _t.bf16 or logits.dim() != 2 or topk_idx.dim() != 2:
-        _refuse(fn)
-    T, E = logits.shape
-    k = topk_idx.shape[1]
-    dev = _device_of(fn, logits)
-    ldl = _rows(fn, logits, T, E, dev)
-    pi = _dense(fn, topk_idx, _t.i32, (T, k), dev)
-    pc = None if counts is None else _dense(fn, counts, _t.i32, (E + 1,), dev)
-    pw = None if dtopk_w is None else _dense(fn, dtopk_w, _t.f32, (T, k), dev)
-    pl = None if dloss is None else _dense(fn, dloss, _t.f32, (1,), dev)
-    pm = _mask(fn, token_mask, T, dev)
-    if dlogits is None:
-        dlogits = _t.empty((T, E), dtype=logits.dtype, device=logits.device)
-    pd = _dense(fn, dlogits, logits.dtype, (T, E), dev)
-    code = _lib_raw().fp8moe_router_bwd(logits.data_ptr(), f32, T, E, ldl, k, score, bool(renormalize), route_scale, pm, pi,
-                                        pc, pw, pl, pd, _t.raw_stream(dev))
-    if code:
-        raise Fp8MoeError(fn, code)
-    return dlogits
+    return _run("fp8moe_router_bwd", stream, _native().router_bwd, logits, topk_idx, counts, dtopk_w, dloss, score, renormalize,
+                route_scale, token_mask, dlogits)
 
 
-@_on_stream
-def fp8moe_route_weight_grad(dout, y, row_of, dw=None):
+def fp8moe_route_weight_grad(dout, y, row_of, dw=None, stream=None):
     """Gradient of fp8moe_route_unpermute's weights: dout [T, N] bf16, y
     [rows, N] bf16, row_of [T, k] int32 -> dw [T, k] fp32."""
-    fn = "fp8moe_route_weight_grad"
-    if dout.dim() != 2 or y.dim() != 2 or row_of.dim() != 2:
-        _refuse(fn)
-    T, N = dout.shape
-    k = row_of.shape[1]
-    dev = _device_of(fn, dout)
-    pd, py = _dense(fn, dout, _t.bf16, (T, N), dev), _dense(fn, y, _t.bf16, (y.shape[0], N), dev)
-    pr = _dense(fn, row_of, _t.i32, (T, k), dev)
-    if dw is None:
-        dw = _t.empty((T, k), dtype=_t.f32, device=dout.device)
-    pw = _dense(fn, dw, _t.f32, (T, k), dev)
-    code = _lib_raw().fp8moe_route_weight_grad(pd, py, pr, T, N, k, pw, _t.raw_stream(dev))
-    if code:
-        raise Fp8MoeError(fn, code)
-    return dw
+    return _run("fp8moe_route_weight_grad", stream, _native().route_weight_grad, dout, y, row_of, dw)
 
 
-def _mx_outputs(fn, q, s, layout, R, C, E, on, dev):
-    """(q, address, s, address) of MXFP8 codes [R, C] and their scales, allocated
-    unless given."""
-    need = R * (C // 32) if layout == SCALES_ROWMAJOR else fp8moe_swizzled_scales_bytes(1, R, C // 32, E, layout)
-    if q is None:
-        q = _t.empty((R, C), dtype=_t.u8, device=on)
-    if s is None:
-        if need < 0:
-            _refuse(fn)
-        s = (_t.empty((R, C // 32), dtype=_t.u8, device=on) if layout == SCALES_ROWMAJOR
-             else _t.zeros((need,), dtype=_t.u8, device=on))
-    elif s.numel() < need:
-        _refuse(fn)
-    return q, _dense(fn, q, _t.u8, (R, C), dev), s, _dense(fn, s, _t.u8, s.shape, dev)
-
-
-def _swiglu(fn, dout, h, offs, s0_layout, s1_layout, need_out, dim0, dim1, out, q0, s0, q1, s1):
-    if h.dtype is not _t.bf16 or h.dim() != 2 or h.shape[1] % 2:
-        _refuse(fn)
-    M, W2 = h.shape
-    F = W2 // 2
-    W = F if dout is None else W2
-    dev, on = _device_of(fn, h), h.device
-    ldh = _rows(fn, h, M, W2, dev)
-    pd = None if dout is None else _dense(fn, dout, _t.bf16, (M, F), dev)
-    E, po = 0, None
-    if offs is not None:
-        E = offs.numel()
-        po = _dense(fn, offs, _t.i32, (E,), dev)
-    pout = p0 = ps0 = p1 = ps1 = None
-    if need_out:
-        if out is None:
-            out = _t.empty((M, W), dtype=_t.bf16, device=on)
-        pout = _dense(fn, out, _t.bf16, (M, W), dev)
-    else:
-        out = None
-    if dim0:
-        q0, p0, s0, ps0 = _mx_outputs(fn, q0, s0, s0_layout, M, W, E, on, dev)
-    else:
-        q0 = s0 = None
-    if dim1:
-        q1, p1, s1, ps1 = _mx_outputs(fn, q1, s1, s1_layout, W, M, E, on, dev)
-    else:
-        q1 = s1 = None
-    args = (h.data_ptr(), ldh, M, F, po, E, pout, p0, ps0, s0_layout, p1, ps1, s1_layout, _t.raw_stream(dev))
-    code = _lib_raw().fp8moe_swiglu_fwd(*args) if dout is None else _lib_raw().fp8moe_swiglu_bwd(pd, *args)
-    if code:
-        raise Fp8MoeError(fn, code)
-    return out, q0, s0, q1, s1
-
-
-@_on_stream
 def fp8moe_swiglu_fwd(h, offs=None, s0_layout: int = NO_GROUPS, s1_layout: int = NO_GROUPS, need_out: bool = True,
-                      dim0: bool = False, dim1: bool = False, out=None, q0=None, s0=None, q1=None, s1=None):
+                      dim0: bool = False, dim1: bool = False, out=None, q0=None, s0=None, q1=None, s1=None, stream=None):
     """a = gate * sigmoid(gate) * up of h [M, 2F] bf16 (gate | up; the row
     stride may exceed 2F).
 
@@ -882,18 +621,19 @@ def fp8moe_swiglu_fwd(h, offs=None, s0_layout: int = NO_GROUPS, s1_layout: int =
     along the rows (``dim0``) and along the columns, transposed (``dim1``),
     with scales in the layouts of fp8moe_mxfp8_quantize_dual; None for what
     is not asked for.  Scale buffers are allocated zero-filled when not given."""
-    return _swiglu("fp8moe_swiglu_fwd", None, h, offs, s0_layout, s1_layout, need_out, dim0, dim1, out, q0, s0, q1, s1)
+    return _run("fp8moe_swiglu_fwd", stream, _native().swiglu, None, h, offs, s0_layout, s1_layout, need_out, dim0, dim1, out, q0,
+                s0, q1, s1)
 
 
-@_on_stream
 def fp8moe_swiglu_bwd(dout, h, offs=None, s0_layout: int = NO_GROUPS, s1_layout: int = NO_GROUPS,
                       need_dh: bool = True, dim0: bool = False, dim1: bool = False, out=None, q0=None, s0=None,
-                      q1=None, s1=None):
+                      q1=None, s1=None, stream=None):
     """Backward of fp8moe_swiglu_fwd: dout [M, F] bf16 and the forward's h ->
     (dh bf16 [M, 2F], q0 [M, 2F], s0, q1 [2F, M], s1), as the forward."""
     if dout is None:
-        _refuse("fp8moe_swiglu_bwd")
-    return _swiglu("fp8moe_swiglu_bwd", dout, h, offs, s0_layout, s1_layout, need_dh, dim0, dim1, out, q0, s0, q1, s1)
+        raise Fp8MoeError("fp8moe_swiglu_bwd", 1)
+    return _run("fp8moe_swiglu_bwd", stream, _native().swiglu, dout, h, offs, s0_layout, s1_layout, need_dh, dim0, dim1, out, q0,
+                s0, q1, s1)
 
 
 def fp8moe_get_device_status(stream=None) -> int:

@@ -1,8 +1,10 @@
-"""Build libfp8moe.so in-tree with nvcc for sm_103a (GB300).
+"""Build libfp8moe.so in-tree with nvcc for sm_103a (GB300), and the module
+that marshals PyTorch tensors for the small calls with the host compiler.
 
-Each CUDA translation unit compiles in parallel; the objects link into
-``mxfp8_moe_quantization_gb300/libfp8moe.so``.  A rebuild happens only when a
-source or header is newer than the library.  No cmake, one -gencode.
+Each translation unit compiles in parallel; the CUDA objects link into
+``mxfp8_moe_quantization_gb300/libfp8moe.so``, the binding into ``_binding.so``
+beside it.  A rebuild happens only when a source or header is newer than the
+libraries.  No cmake, one -gencode.
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8moe.so")
+BINDING = os.path.join(HERE, "_binding.so")
 
 SOURCES = ["api.cu", "quant.cu", "colwise.cu", "colwise_cluster.cu", "colwise_jagged.cu", "dual.cu", "tensorwise.cu", "blockwise.cu", "routing.cu", "swizzle.cu",
            "grouped_mm.cu", "blockwise_mm.cu", "layer.cu", "norm.cu", "router.cu", "swiglu.cu"]
@@ -40,10 +44,15 @@ def _deps():
     return out
 
 
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -65,14 +74,36 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    torch_dir = _torch_dir()
+    binding_obj = os.path.join(BUILD, "binding.o")
+
+    def run(what, cmd):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{what} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+
+    def compile_binding():
+        cuda_include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+        run("binding", [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-I", os.path.join(torch_dir, "include"),
+                        "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), "-I", cuda_include,
+                        "-I", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "binding.cpp"), "-o", binding_obj])
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BINDING + ".tmp"
+    torch_lib = os.path.join(torch_dir, "lib")
+    run("binding link", [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, binding_obj, "-L", HERE, "-l:libfp8moe.so",
+                         "-L", torch_lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+                         "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"])
+    os.replace(tmp, BINDING)
     return LIB
 
 
