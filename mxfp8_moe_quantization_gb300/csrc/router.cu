@@ -18,8 +18,14 @@
 // A warp takes a token, a lane every 32nd expert; the logits are read once.
 // Sums over tokens have a fixed order (registers, then warps, then CTAs), so
 // results do not change from run to run.  The CTAs' partial sums are joined by
-// a second kernel of one cluster, which is already resident, waiting, when the
-// first one ends (programmatic dependent launch).
+// a second kernel of one cluster, launched ahead of the first one's end.
+//
+// Bound by latency, then by instruction issue (a token of 256 experts, top 8:
+// about 1100 warp instructions, half of them the rounds of the choice).  In a
+// graph: 4096 x 256, top 8, 10.4 us forward with the sums and 6.0 without, 5.0
+// backward; 8192 x 64, top 6, 10.1; 3 tokens 3.9.  The first form, which
+// carried scores through the rounds and joined 512 partial sums in one CTA,
+// took 29.9 us on the first.
 #include "common.cuh"
 #include "launch.h"
 #include "moe_ops.h"
@@ -27,15 +33,17 @@
 namespace fp8moe {
 namespace {
 
-constexpr int RW = 8;               // warps per CTA
-constexpr int SINGLE_CTA_T = 2 * RW;  // up to so many tokens one CTA does everything
+// Most warps of a CTA whose lanes hold V experts each (its registers).
+template <int V>
+constexpr int most_warps() { return V <= 8 ? 32 : V == 16 ? 16 : 8; }
+constexpr int BWD_WARPS = 8;
+constexpr int SINGLE_CTA_T = 16;   // up to so many tokens one CTA does everything
 
 // order-preserving key: larger float, larger key; NaN sorts with -inf; every
 // key is above 0, the mark of what is taken or absent
 FP8MOE_DEV uint32_t order_key(float f) {
-  const uint32_t u = __float_as_uint(f + 0.0f);   // -0 and 0 are equal
-  if (f != f) return 0x007FFFFFu;
-  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+  const int u = __float_as_int(fmaxf(f + 0.0f, -__builtin_huge_valf()));   // -0 and 0 are equal
+  return (uint32_t)u ^ ((uint32_t)(u >> 31) | 0x80000000u);
 }
 
 FP8MOE_DEV float warp_sum(float v) {
@@ -124,11 +132,9 @@ FP8MOE_DEV float loss_of(float np, int tokens, int E, int k) {
   return np * __fdiv_rn((float)E, (float)k) / (N * N);
 }
 
-// dynamic shared memory of the forward: probability sums [RW][E], counts [E + 1]
-inline int fwd_smem(int E, bool sums) { return sums ? (RW * E + E + 1) * 4 : 0; }
-
 template <int V, bool SIG>
-__global__ void __launch_bounds__(RW * 32) k_router_fwd(RouterArgs a) {
+__global__ void __launch_bounds__(most_warps<V>() * 32) k_router_fwd(RouterArgs a) {
+  const int RW = blockDim.x >> 5;
   extern __shared__ float rsm[];
   __shared__ float red[32];
   float* cp = rsm;                      // [RW][E]
@@ -209,7 +215,7 @@ __global__ void __launch_bounds__(RW * 32) k_router_fwd(RouterArgs a) {
     pn[e] = n;
     if (e < a.E) {
       float v = cp[e];
-#pragma unroll
+#pragma unroll 4
       for (int i = 1; i < RW; ++i) v += cp[i * a.E + e];
       pp[e] = v;
       np = fmaf((float)n, v, np);
@@ -224,65 +230,91 @@ __global__ void __launch_bounds__(RW * 32) k_router_fwd(RouterArgs a) {
 // Counts, probability sums and the loss from the CTAs' partials, in order: one
 // cluster of JOIN CTAs, CTA c with every JOIN-th block of 32 experts (a warp a
 // slice of the partials, a lane an expert).
-constexpr int JOIN = 8, JOIN_WARPS = 32;
+constexpr int JOIN = 8, JOIN_WARPS = 16, JOIN_U = 10;
 __global__ void __cluster_dims__(JOIN, 1, 1) __launch_bounds__(JOIN_WARPS * 32) k_router_join(RouterArgs a, int parts) {
-  __shared__ float sp[JOIN_WARPS][33], share, red[32];
-  __shared__ int sn[JOIN_WARPS][33], tok_s;
+  __shared__ float sp[JOIN_WARPS][32], share[JOIN];
+  __shared__ int sn[JOIN_WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = blockIdx.x;
   const float* pp = (const float*)a.workspace;
   const int* pn = (const int*)(pp + (int64_t)parts * a.E);
+  // a remote store needs its target CTA to have started: waited for below
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float np = 0.0f;
+  // the token counts, in flight beside the sums
+  int tok = 0;
+  if (rank == 0 && warp == 0)
+    for (int i = lane; i < parts; i += 32) tok += __ldcg(pn + (int64_t)i * (a.E + 1) + a.E);
+  float np = 0.0f, v = 0.0f;
+  int n = 0, last = -1;   // the block whose results are stored at the end
   for (int e0 = rank * 32; e0 < a.E; e0 += JOIN * 32) {
     const int e = e0 + lane;
-    float v = 0.0f;
-    int n = 0;
+    if (last >= 0) {
+      if (warp == 0) a.psum[last + lane] = v, a.counts[last + lane] = n;
+      __syncthreads();   // sp, sn are read
+    }
+    last = e0;
+    v = 0.0f;
+    n = 0;
     if (e < a.E) {
-#pragma unroll 4
-      for (int i = warp; i < parts; i += JOIN_WARPS) {
-        v += pp[(int64_t)i * a.E + e];
-        n += pn[(int64_t)i * (a.E + 1) + e];
+      // every load of a round in flight at once (one round up to 160 parts)
+      for (int i0 = warp; i0 < parts; i0 += JOIN_WARPS * JOIN_U) {
+        float vv[JOIN_U];
+        int nn[JOIN_U];
+#pragma unroll
+        for (int j = 0; j < JOIN_U; ++j) {
+          const int i = i0 + j * JOIN_WARPS;
+          vv[j] = i < parts ? __ldcg(pp + (int64_t)i * a.E + e) : 0.0f;
+          nn[j] = i < parts ? __ldcg(pn + (int64_t)i * (a.E + 1) + e) : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < JOIN_U; ++j) {
+          v += vv[j];
+          n += nn[j];
+        }
       }
     }
     sp[warp][lane] = v;
     sn[warp][lane] = n;
     __syncthreads();
-    // expert e0 + warp: the slices in lane order
-    v = warp_sum(sp[lane][warp]);
-    n = __reduce_add_sync(0xffffffffu, sn[lane][warp]);
-    if (lane == 0 && e0 + warp < a.E) {
-      a.psum[e0 + warp] = v;
-      a.counts[e0 + warp] = n;
+    if (warp == 0 && e < a.E) {
+#pragma unroll
+      for (int i = 1; i < JOIN_WARPS; ++i) {
+        v += sp[i][lane];
+        n += sn[i][lane];
+      }
       np = fmaf((float)n, v, np);
     }
-    __syncthreads();
   }
-  if (rank == 0 && warp == 0) {
-    int tok = 0;
-    for (int i = lane; i < parts; i += 32) tok += pn[(int64_t)i * (a.E + 1) + a.E];
-    tok = __reduce_add_sync(0xffffffffu, tok);
-    if (lane == 0) tok_s = a.counts[a.E] = tok;
-  }
-  np = cta_sum(np, red);
-  if (threadIdx.x == 0) share = np;
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  if (rank == 0 && threadIdx.x == 0) {
-    np = 0.0f;
-    for (int c = 0; c < JOIN; ++c) {
+  // every CTA's share of sum n_e P_e into rank 0's shared memory
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (warp == 0) {
+    np = warp_sum(np);
+    if (lane == 0) {
       uint32_t at;
-      float v;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(&share)), "r"(c));
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-      np += v;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(&share[rank])));
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(np) : "memory");
     }
-    a.loss[0] = loss_of(np, tok_s, a.E, a.k);
   }
-  // no CTA leaves while its share may still be read
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  // (after the arrival, whose release would wait for these stores)
+  if (warp == 0 && last >= 0 && last + lane < a.E) {
+    a.psum[last + lane] = v;
+    a.counts[last + lane] = n;
+  }
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (rank == 0 && warp == 0) {
+    tok = __reduce_add_sync(0xffffffffu, tok);
+    np = warp_sum(lane < JOIN ? share[lane] : 0.0f);
+    if (lane == 0) {
+      a.counts[a.E] = tok;
+      a.loss[0] = loss_of(np, tok, a.E, a.k);
+    }
+  }
 }
 
 template <int V, bool SIG>
-__global__ void __launch_bounds__(RW * 32) k_router_bwd(RouterArgs a) {
+__global__ void __launch_bounds__(BWD_WARPS * 32) k_router_bwd(RouterArgs a) {
+  constexpr int RW = BWD_WARPS;
   extern __shared__ float rsm[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* ubuf = rsm + warp * a.E;   // the chosen experts' u
@@ -406,18 +438,21 @@ __global__ void __launch_bounds__(256) k_route_weight_grad(const uint16_t* __res
   }
 }
 
-// CTAs per SM: enough warps to overlap the rounds of different tokens; more
-// would only add partial sums to join
-constexpr int CTAS_PER_SM = 2;
-
 template <int V, bool SIG>
 cudaError_t run_fwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
   const bool sums = a.counts != nullptr;
-  int64_t blocks = sums && a.T <= SINGLE_CTA_T ? 1 : (a.T + RW - 1) / RW;
-  int64_t most = (int64_t)num_sms * (sums ? CTAS_PER_SM : 8);
-  if (sums && most > ROUTER_MAX_PARTS) most = ROUTER_MAX_PARTS;
+  // one CTA per SM, of as many warps as it gets tokens: few partial sums, and
+  // tokens spread over the SMs (512 tokens: 3.7 us with CTAs of four warps,
+  // 6.4 with CTAs of 32, without the sums)
+  const bool single = sums && a.T <= SINGLE_CTA_T;
+  const int64_t want = single ? a.T : (a.T + num_sms - 1) / num_sms;
+  const int RW = want < 4 ? 4 : want > most_warps<V>() ? most_warps<V>() : (int)want;
+  const int smem = sums ? (RW * a.E + a.E + 1) * 4 : 0;   // probability sums per warp, counts
+  int64_t blocks = single ? 1 : (a.T + RW - 1) / RW;
+  const int64_t most = (int64_t)num_sms * (32 / most_warps<V>());
   if (blocks > most) blocks = most;
-  k_router_fwd<V, SIG><<<(unsigned)blocks, RW * 32, fwd_smem(a.E, sums), st>>>(a);
+  if (sums && blocks > ROUTER_MAX_PARTS) blocks = ROUTER_MAX_PARTS;
+  k_router_fwd<V, SIG><<<(unsigned)blocks, RW * 32, smem, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !sums || blocks == 1) return e;
   cudaLaunchConfig_t cfg = {};
@@ -433,6 +468,7 @@ cudaError_t run_fwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
 }
 template <int V, bool SIG>
 cudaError_t run_bwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
+  constexpr int RW = BWD_WARPS;
   int64_t blocks = (a.T + RW - 1) / RW;
   if (blocks > (int64_t)num_sms * 8) blocks = (int64_t)num_sms * 8;
   k_router_bwd<V, SIG><<<(unsigned)blocks, RW * 32, RW * a.E * 4, st>>>(a);
