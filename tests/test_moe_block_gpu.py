@@ -60,7 +60,7 @@ def test_gradients(B, score):
     assert float(balance) == pytest.approx(float(bal.detach()), rel=1e-2)
 
     def cosine(a, b):
-        return float(torch.nn.functional.cosine_similarity(a.float().flatten(), b.float().flatten(), dim=0))
+        return float(torch.nn.functional.cosine_similarity(a.detach().float().flatten(), b.detach().float().flatten(), dim=0))
 
     assert cosine(out, ref) > 0.99 and torch.equal(h, (x.float() + r.float()).to(torch.bfloat16))
     assert cosine(dx, xa.grad) > 0.99
