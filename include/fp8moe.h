@@ -473,8 +473,8 @@ fp8moe_status fp8moe_route_permute_noalloc(const void* x, int64_t T, int64_t H, 
  *          recipe FP8MOE_ROWWISE (either kind, H % 16 == 0): q [T, H] and
  *          scale fp32 [T] by the rule of fp8moe_quantize_rowwise.
  *          scale_layout is read for MXFP8 alone.
- * At least one of h, y, rstd, q is given.  H % 8 == 0, H <= 2^20, eps >= 0
- * and finite.  Rows of zeros give y = 0 (eps > 0).
+ * At least one of h, y, rstd, q is given.  H % 8 == 0, H <= 2^20, T < 2^31 -
+ * 128, eps >= 0 and finite.  Rows of zeros give y = 0 (eps > 0).
  *
  * Backward (xh = h * rstd, g = dy * w):
  *   dx = rstd * (g - xh * mean(g * xh)) + dh,  dw = sum over rows of dy * xh.

@@ -502,7 +502,7 @@ int64_t fp8moe_add_rmsnorm_bwd_workspace_bytes(int64_t T, int64_t H) {
 fp8moe_status fp8moe_add_rmsnorm_bwd(const void* dy, const void* h, const float* rstd, const void* w,
                                      int weight_type, const void* dh, int64_t T, int64_t H, void* dx, float* dw,
                                      void* workspace, int64_t workspace_bytes, fp8moe_stream_t stream) {
-  if (T < 0 || H < 1 || H > ((int64_t)1 << 20)) return FP8MOE_ERR_INVALID_ARG;
+  if (T < 0 || H < 1 || T > INT32_MAX - 128 || H > ((int64_t)1 << 20)) return FP8MOE_ERR_INVALID_ARG;
   if (weight_type != FP8MOE_BF16 && weight_type != FP8MOE_FP32) return FP8MOE_ERR_INVALID_ARG;
   if (H % 8) return FP8MOE_ERR_ALIGNMENT;
   if (!dw || (T > 0 && (!dy || !h || !rstd || !w || !dx || !workspace))) return FP8MOE_ERR_INVALID_ARG;

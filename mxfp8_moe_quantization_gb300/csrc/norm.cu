@@ -10,8 +10,15 @@
 // Backward (xh = h * rstd, g = dy * w):
 //   dx = rstd * (g - xh * mean(g * xh)) + dh,   dw = sum over rows of dy * xh
 //
-// Both directions move each element once and are bound by HBM; a row lives in
-// the registers of its warps between its loads and its stores.
+// Both directions move each element once and are bound by HBM as long as they
+// spend few instructions and keep enough loads in flight: packed fp32 pairs
+// throughout; the forward holds a row in the registers of its warps and lets
+// many CTAs overlap; the backward, whose share of dw has to stay with a CTA
+// over many rows, streams them through a ring of bulk copies.  Measured (bytes
+// that the formulas cannot do without, of a copy's 6.68 TB/s): 16384 x 5120
+// with residual, bf16 and MXFP8 outputs 115 us (98%); 8191 x 4096 rowwise 41 us
+// (85%: two maxima a row); 16384 x 5120 backward 106 us (94%); one row of 7168
+// 3.0 us in a graph.  The first forms took 116, 46, 118 and 3.4 us.
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "launch.h"
@@ -32,8 +39,7 @@ constexpr int norm_bwd_threads() { return V == 4 ? 512 : 640; }
 constexpr int NORM_BWD_STAGES = 4;   // most slots of its ring
 constexpr int NORM_MAX_CHUNKS = 4 * norm_threads<4>();   // longer rows (H > 16384) take the looping kernels
 
-// partial values of a CTA's rows: at most 16 warps, each row's padded to fours
-constexpr int NORM_RED = 64;
+constexpr int NORM_RED = 32;   // warps of a CTA
 
 // a load that the same thread may follow with a store to the same place (the
 // residual stream is updated in place), so not through the read-only path
@@ -87,16 +93,17 @@ FP8MOE_DEV float row_reduce(float v, float* red, int wpr, int group, int wrow) {
     v = MAX ? fmaxf(v, u) : v + u;
   }
   if (wpr > 1) {
-    // a row's values start at a multiple of four: read as vectors, padded
-    float* mine = red + group * ((wpr + 3) & ~3);
-    if ((threadIdx.x & 31) == 0) mine[wrow] = v;
+    // a row's values, every lane one of them, zero past the last (the maxima
+    // are of magnitudes)
+    if ((threadIdx.x & 31) == 0) red[group * wpr + wrow] = v;
     __syncthreads();
-    v = 0.0f;   // (the maxima are of magnitudes)
-    for (int i = 0; i < wpr; i += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(mine + i);
-      const float b = i + 1 < wpr ? f.y : 0.0f, c = i + 2 < wpr ? f.z : 0.0f, d = i + 3 < wpr ? f.w : 0.0f;
-      v = MAX ? fmaxf(fmaxf(fmaxf(v, f.x), b), fmaxf(c, d)) : v + f.x + b + (c + d);
+    const int lane = threadIdx.x & 31;
+    v = lane < wpr ? red[group * wpr + lane] : 0.0f;
+    for (int o = wpr > 16 ? 16 : wpr > 8 ? 8 : wpr > 4 ? 4 : 2; o > 0; o >>= 1) {
+      const float u = __shfl_xor_sync(0xffffffffu, v, o);
+      v = MAX ? fmaxf(v, u) : v + u;
     }
+    v = __shfl_sync(0xffffffffu, v, 0);
   }
   return v;
 }
@@ -145,7 +152,7 @@ FP8MOE_DEV void zero_scale_pad(const NormFwdArgs& a, int64_t row, int t, int n) 
 // A CTA holds `groups` rows, wpr warps each; a thread V chunks of its row.
 template <int V, int OUT, bool W32>
 __global__ void __launch_bounds__(norm_threads<V>()) k_norm_fwd(NormFwdArgs a, int wpr) {
-  __shared__ __align__(16) float red[2][NORM_RED];
+  __shared__ float red[2][NORM_RED];
   const int warp = threadIdx.x >> 5, group = warp / wpr, wrow = warp % wpr;
   const int tpr = wpr * 32, t = threadIdx.x - group * tpr;
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + group;
@@ -207,7 +214,7 @@ __global__ void __launch_bounds__(norm_threads<V>()) k_norm_fwd(NormFwdArgs a, i
 // row again (from L2) for each pass.
 template <int OUT, bool W32>
 __global__ void __launch_bounds__(1024) k_norm_fwd_long(NormFwdArgs a) {
-  __shared__ __align__(16) float red[2][NORM_RED];
+  __shared__ float red[2][NORM_RED];
   const int64_t row = blockIdx.x;
   const int t = threadIdx.x, n = blockDim.x, nch = a.H / 8;
   const bool active = row < a.T;
@@ -307,7 +314,7 @@ struct NormBwdArgs {
 template <int V, bool W32>
 __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs a, int wpr, int stages) {
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ __align__(16) float red[2][NORM_RED];
+  __shared__ float red[2][NORM_RED];
   __shared__ uint64_t full[NORM_BWD_STAGES];
   __shared__ int abort_s, fills[NORM_BWD_STAGES];   // fills: thread 0's count per slot
   volatile int* abort_flag = &abort_s;
@@ -315,13 +322,12 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
   const int nch = a.H / 8;
   const uint32_t row_bytes = (uint32_t)a.H * 2, ten_bytes = row_bytes * groups;
   const uint32_t slot_bytes = ten_bytes * (a.dh ? 3 : 2);
-  const int64_t blocks = (a.T + groups - 1) / groups;
+  const int blocks = (int)((a.T + groups - 1) / groups);
   // thread 0: block nblk, the next to load, goes to slot nslot
-  int64_t nblk = blockIdx.x;
-  int nslot = 0;
+  int nblk = blockIdx.x, nslot = 0;
   auto issue = [&]() {
     uint8_t* dst = ring + nslot * slot_bytes;
-    const int64_t r0 = nblk * groups, at = r0 * a.H;
+    const int64_t r0 = (int64_t)nblk * groups, at = r0 * a.H;
     const uint32_t bytes = row_bytes * (uint32_t)(a.T - r0 < groups ? a.T - r0 : groups);
     ++fills[nslot];
     mbar_expect_tx(&full[nslot], bytes * (a.dh ? 3 : 2));
@@ -352,15 +358,18 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
       w4[i] = t + i * tpr < nch ? reinterpret_cast<const uint4*>(a.w)[t + i * tpr] : make_uint4(0, 0, 0, 0);
   }
   // a row's rstd is loaded one block ahead (rows past T: 0, and nothing stored)
-  auto rstd_of = [&](int64_t b) { return b * groups + group < a.T ? a.rstd[b * groups + group] : 0.0f; };
-  float rstd = rstd_of(blockIdx.x);
+  const int64_t step = (int64_t)gridDim.x * groups;
+  int64_t row = (int64_t)blockIdx.x * groups + group;
+  const float* prstd = a.rstd + row;
+  uint16_t* pdx = a.dx + row * a.H + t * 8;
+  float rstd = row < a.T ? *prstd : 0.0f;
   __syncthreads();
   int s = 0, par = 0;
   uint32_t phase = 0;
-  for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-    const int64_t row = b * groups + group;
+  for (int b = blockIdx.x; b < blocks; b += gridDim.x, row += step, pdx += step * a.H) {
     const bool live = row < a.T;
-    const float rstd_next = rstd_of(b + gridDim.x);
+    prstd += step;
+    const float rstd_next = row + step < a.T ? *prstd : 0.0f;
     const uint64_t rstd2 = pk(rstd, rstd);
     if (!mbar_wait(&full[s], phase, abort_flag)) {
       set_status(a.status, FP8MOE_ERR_TIMEOUT);
@@ -409,7 +418,7 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
       Vec8 o;
 #pragma unroll
       for (int j = 0; j < 4; ++j) o.p[j] = fma2(rstd2, fma2(xh[i].p[j], c2, g[i].p[j]), sv.p[j]);
-      *reinterpret_cast<uint4*>(a.dx + row * a.H + (int64_t)ch * 8) = pack8(o);
+      *reinterpret_cast<uint4*>(pdx + i * tpr * 8) = pack8(o);
     }
     rstd = rstd_next;
     if (++s == stages) {
@@ -451,7 +460,7 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
 // a thread's share of dw stays in its CTA's row of the partials.
 template <bool W32>
 __global__ void __launch_bounds__(512) k_norm_bwd_long(NormBwdArgs a, int, int) {
-  __shared__ __align__(16) float red[2][NORM_RED];
+  __shared__ float red[2][NORM_RED];
   const int t = threadIdx.x, n = blockDim.x, nch = a.H / 8;
   float* part = a.part + (int64_t)blockIdx.x * a.H;
   int par = 0;
