@@ -864,6 +864,46 @@ def bench_rows(F, iters=30, only=None):
             emit("next2", "k_route_unpermute", f"{wl.name} T={T} k={k} N={H}", ms, nbytes=T * k * H * 2 + T * H * 2)
             del xt, a, outt
 
+    # ---- the operators around the expert products
+    if want("moe_ops"):
+        rand = lambda *s: torch.randn(*s, device=dev).to(torch.bfloat16)
+        T, H = sc.tokens, sc.K
+        xn, rn, wn = rand(T, H), rand(T, H), torch.ones(H, device=dev)
+        h, y, rs, q, s = F.fp8moe_add_rmsnorm_fwd(xn, wn, rn, recipe=F.MXFP8, scale_layout=F.NO_GROUPS)
+        ms = timed(lambda: F.fp8moe_add_rmsnorm_fwd(xn, wn, rn, recipe=F.MXFP8, scale_layout=F.NO_GROUPS, h=h, y=y, rstd=rs,
+                                                    q=q, scale=s))
+        emit("ops", "k_norm_fwd", f"scout [{T},{H}] residual, bf16 and MXFP8", ms, nbytes=T * H * (9 + 1 / 32))
+        ms = timed(lambda: F.fp8moe_add_rmsnorm_bwd(xn, h, rs, wn, rn, dx=y))
+        emit("ops", "k_norm_bwd", f"scout [{T},{H}]", ms, nbytes=T * H * 8)
+        del xn, rn, h, y, q, s
+        T, E, k = v3.tokens, v3.E, 8
+        lg, bias = torch.randn(T, E, device=dev), 0.05 * torch.randn(E, device=dev)
+        fwd = lambda: F.fp8moe_router_fwd(lg, k, score=F.SCORE_SIGMOID, bias=bias)
+        idx, wt, cnt, _, loss = fwd()
+        emit("ops", "k_router_fwd", f"dsv3 [{T},{E}] top {k}", timed(fwd), nbytes=T * (4 * E + 8 * k))
+        ms = timed(lambda: F.fp8moe_router_bwd(lg, idx, cnt, wt, loss, score=F.SCORE_SIGMOID))
+        emit("ops", "k_router_bwd", f"dsv3 [{T},{E}] top {k}", ms, nbytes=T * (8 * E + 8 * k))
+        yr, do = rand(T * k, v3.K), rand(T, v3.K)
+        row_of = torch.randperm(T * k, device=dev).reshape(T, k).to(torch.int32)
+        ms = timed(lambda: F.fp8moe_route_weight_grad(do, yr, row_of))
+        emit("ops", "k_route_weight_grad", f"dsv3 [{T},{v3.K}] x {k}", ms, nbytes=T * v3.K * 2 * (k + 1))
+        del yr, do
+        for wl in (v3, ds):
+            offs = torch.from_numpy(wl.offs()).to(dev)
+            M, Fd = wl.M // 32 * 32, wl.N
+            offs = (offs // 32 * 32).to(torch.int32)
+            hh, do = rand(M, 2 * Fd), rand(M, Fd)
+            lay = (F.GROUP_ROWS, F.GROUP_COLS)
+            o = F.fp8moe_swiglu_fwd(hh, offs, *lay, need_out=False, dim0=True, dim1=True)
+            kw = dict(zip(("q0", "s0", "q1", "s1"), o[1:]))
+            ms = timed(lambda: F.fp8moe_swiglu_fwd(hh, offs, *lay, need_out=False, dim0=True, dim1=True, **kw))
+            emit("ops", "k_swiglu<fwd>", f"{wl.name} [{M},{Fd}] both directions", ms, nbytes=M * Fd * (6 + 2 / 32))
+            o = F.fp8moe_swiglu_bwd(do, hh, offs, *lay, need_dh=False, dim0=True, dim1=True)
+            kw = dict(zip(("q0", "s0", "q1", "s1"), o[1:]))
+            ms = timed(lambda: F.fp8moe_swiglu_bwd(do, hh, offs, *lay, need_dh=False, dim0=True, dim1=True, **kw))
+            emit("ops", "k_swiglu<bwd>", f"{wl.name} [{M},{Fd}] both directions", ms, nbytes=M * Fd * (10 + 4 / 32))
+            del hh, do, o, kw
+
 
 def dual_case(F, dev):
     """The fused dual-direction MXFP8 quantization of the Scout activations
@@ -951,7 +991,7 @@ def main():
     ap.add_argument("--no-dsv3", action="store_true", help="skip the DeepSeek-V3 layer measurements")
     ap.add_argument("--only", default=None,
                     help="with --rows: comma-separated sections (rowwise, colwise, tensorwise, mx, swizzle, gemm, gemm_rowwise, "
-                         "fused, layer, blockwise, routing)")
+                         "fused, layer, blockwise, routing, moe_ops)")
     ap.add_argument("--gemm-case", type=int, default=0, metavar="E",
                     help="run the Scout W1 grouped GEMMs on the first E experts only (a reduced case for "
                          "profiler captures) and exit")

@@ -616,17 +616,20 @@ fp8moe_status fp8moe_testing_stall_next_gemm(void);
 fp8moe_status fp8moe_testing_stall_next_tensorwise(void);
 
 /* ------------------------------------------------------------------------
- * Testing hook of the failure-detection path of the warp-specialised
- * quantizers (no counterpart on the pages): fp8moe_mxfp8_quantize_dual with
- * both directions and at least 128 columns, and fp8moe_quantize_colwise_3d of
- * routed rows with transposed output.  Arms a one-shot flag: the next such
- * launch of the process never loads one tile (the dual quantizer: the first
- * CTA's first tile; the routed-rows colwise kernel: the first tile of its
- * first unit, whichever CTA takes it), so the consumer warps waiting for it
- * run out of their bounded wait (2 s) and the launch sets
- * FP8MOE_ERR_TIMEOUT (its outputs are then not valid).  The CTA's producer
- * still waits (bounded) for the loads it issued, so no copy is in flight when
- * it exits and the context stays usable.
+ * Testing hook of the failure-detection path of the kernels that work
+ * through rings of loads (no counterpart on the pages):
+ * fp8moe_mxfp8_quantize_dual with both directions and at least 128 columns,
+ * fp8moe_quantize_colwise_3d of routed rows with transposed output,
+ * fp8moe_swiglu_fwd / _bwd of more tiles (64 rows x 128 columns) than the
+ * device has SMs, and fp8moe_add_rmsnorm_bwd of rows up to 16384 elements.
+ * Arms a one-shot flag: the next such launch of the process never loads one
+ * tile (the first CTA's first tile or rows; the routed-rows colwise kernel:
+ * the first tile of its first unit, whichever CTA takes it; the gated
+ * activation: the first warp's), so the warps waiting for it run out of
+ * their bounded wait (2 s) and the launch sets FP8MOE_ERR_TIMEOUT (its
+ * outputs are then not valid).  The loads that were issued are still waited
+ * for (bounded), so no copy is in flight when a CTA exits and the context
+ * stays usable.
  * ------------------------------------------------------------------------ */
 fp8moe_status fp8moe_testing_stall_next_quant_ring(void);
 

@@ -656,9 +656,10 @@ def fp8moe_testing_stall_next_tensorwise() -> None:
 
 
 def fp8moe_testing_stall_next_quant_ring() -> None:
-    """Arm the one-shot stall of the next warp-specialised quantization launch
-    (dual-direction MXFP8 or routed-rows transposed colwise; tests of their
-    rings' timeout path)."""
+    """Arm the one-shot stall of the next launch that works through a ring of
+    loads (dual-direction MXFP8 or routed-rows transposed colwise
+    quantization, gated activation, norm backward; tests of the rings' timeout
+    path)."""
     _check("fp8moe_testing_stall_next_quant_ring", _lib_raw().fp8moe_testing_stall_next_quant_ring())
 
 

@@ -46,6 +46,7 @@ struct SwigluArgs {
   int s0_layout, s1_layout;
   int num_sms;
   int* status;
+  int stall;             // test hook: the first CTA's first warp never loads its first tile
 };
 
 }  // namespace fp8moe

@@ -304,6 +304,7 @@ struct NormBwdArgs {
   uint16_t* dx;
   float* part;  // [gridDim.x][H] partial weight gradients
   int* status;
+  int stall;    // test hook: the first CTA never loads its first rows
 };
 
 // A CTA takes blocks of `groups` consecutive rows, blockIdx.x, blockIdx.x +
@@ -329,11 +330,13 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
     uint8_t* dst = ring + nslot * slot_bytes;
     const int64_t r0 = (int64_t)nblk * groups, at = r0 * a.H;
     const uint32_t bytes = row_bytes * (uint32_t)(a.T - r0 < groups ? a.T - r0 : groups);
-    ++fills[nslot];
-    mbar_expect_tx(&full[nslot], bytes * (a.dh ? 3 : 2));
-    bulk_load(dst, a.dy + at, bytes, &full[nslot]);
-    bulk_load(dst + ten_bytes, a.h + at, bytes, &full[nslot]);
-    if (a.dh) bulk_load(dst + 2 * ten_bytes, a.dh + at, bytes, &full[nslot]);
+    if (!a.stall || nblk > 0) {
+      ++fills[nslot];
+      mbar_expect_tx(&full[nslot], bytes * (a.dh ? 3 : 2));
+      bulk_load(dst, a.dy + at, bytes, &full[nslot]);
+      bulk_load(dst + ten_bytes, a.h + at, bytes, &full[nslot]);
+      if (a.dh) bulk_load(dst + 2 * ten_bytes, a.dh + at, bytes, &full[nslot]);
+    }
     nblk += gridDim.x;
     if (++nslot == stages) nslot = 0;
   };
@@ -528,6 +531,7 @@ cudaError_t launch_bwd_t(NormBwdArgs a, float* dw, int num_sms, int max_smem, cu
   if (!ring) wpr = 16, groups = 1;
   const int64_t blocks = (a.T + groups - 1) / groups;
   int64_t P = NORM_BWD_PARTS < blocks ? NORM_BWD_PARTS : blocks;
+  if (ring) a.stall = take_ring_stall_hook();
   auto run = [&](auto kern) {
     const int smem = ring ? (int)(slot * stages) : 0;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(SG_WARPS * 32, BWD ? 3 : 4)
   // the tile's boxes (one lane); a warp whose rows lie past M loads nothing
   auto issue = [&](int64_t t) {
     const int64_t r = row_of(t), c = col_of(t);
-    if (r >= a.M || c >= a.F) return;
+    if (r >= a.M || c >= a.F || (a.stall && blockIdx.x == 0 && warp == 0)) return;
     mbar_expect_tx(wbar, warp_bytes<BWD>());
     tma_load_2d(wbuf, &th, wbar, (int)c, (int)r);
     tma_load_2d(wbuf + BOX_BYTES, &th, wbar, (int)(a.F + c), (int)r);
@@ -360,7 +360,7 @@ cudaError_t launch_t(const CUtensorMap& th, const CUtensorMap& td, const SwigluA
 }
 
 template <bool BWD>
-cudaError_t launch_dir(const SwigluArgs& a, cudaStream_t st) {
+cudaError_t launch_dir(SwigluArgs a, cudaStream_t st) {
   const int64_t W = BWD ? 2 * a.F : a.F;
   const int64_t cp0 = (W / 32 + 3) / 4 * 4;
   const int64_t cp1 = (a.M / 32 + 3) / 4 * 4 + (int64_t)a.E1 * 4;
@@ -377,6 +377,7 @@ cudaError_t launch_dir(const SwigluArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   static std::atomic<int> occ{0};
   const int64_t fit = (int64_t)a.num_sms * blocks_per_sm(occ, k_swiglu<BWD, true>, SG_WARPS * 32, cta_bytes<BWD>(), 1);
+  a.stall = take_ring_stall_hook();
   cuuint64_t dims[2] = {(cuuint64_t)(2 * a.F), (cuuint64_t)a.M}, strides[1] = {(cuuint64_t)(a.ldh * 2)};
   const cuuint32_t box[2] = {SG_COLS, SG_ROWS};
   if (!make_tmap(&th, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.h, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))

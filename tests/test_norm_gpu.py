@@ -222,3 +222,18 @@ def test_other_stream(F):
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     assert F.fp8moe_get_device_status() == 0
+
+
+def test_ring_wait_timeout_sets_status(F):
+    """A block of rows that never arrives: the bounded wait runs out, the status
+    says so, and the next call in the same context is exact."""
+    T, H = 3000, 1024
+    h, dy = _bf16((T, H), 1).to(DEV), _bf16((T, H), 2).to(DEV)
+    w, rstd = _weight(H, 3, False).to(DEV), torch.ones(T, device=DEV)
+    want = F.fp8moe_add_rmsnorm_bwd(dy, h, rstd, w)
+    F.fp8moe_testing_stall_next_quant_ring()
+    F.fp8moe_add_rmsnorm_bwd(dy, h, rstd, w)
+    assert F.fp8moe_get_device_status() == 6
+    got = F.fp8moe_add_rmsnorm_bwd(dy, h, rstd, w)
+    assert F.fp8moe_get_device_status() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -239,3 +239,20 @@ def test_no_rows(F):
     e = torch.empty(0, 64, dtype=torch.bfloat16, device=DEV)
     out, q0, s0, q1, s1 = F.fp8moe_swiglu_fwd(e, dim0=True, dim1=True)
     assert out.shape == (0, 32) and q0.shape == (0, 32) and q1.shape == (32, 0)
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+def test_load_wait_timeout_sets_status(F, bwd):
+    """A tile that never arrives: the bounded wait runs out, the status says so,
+    and the next call in the same context is exact."""
+    M, Fd = 8192, 512
+    h, dout = _bf16((M, 2 * Fd), 1).to(DEV), _bf16((M, Fd), 2).to(DEV)
+    call = (lambda: F.fp8moe_swiglu_bwd(dout, h, dim0=True, dim1=True)) if bwd else (
+        lambda: F.fp8moe_swiglu_fwd(h, dim0=True, dim1=True))
+    want = call()
+    F.fp8moe_testing_stall_next_quant_ring()
+    call()
+    assert F.fp8moe_get_device_status() == 6
+    got = call()
+    assert F.fp8moe_get_device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
