@@ -101,7 +101,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     tmp = BINDING + ".tmp"
     torch_lib = os.path.join(torch_dir, "lib")
     run("binding link", [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, binding_obj, "-L", HERE, "-l:libfp8moe.so",
-                         "-L", torch_lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+                         "-L", torch_lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
                          "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"])
     os.replace(tmp, BINDING)
     return LIB

@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -75,7 +76,8 @@ struct Call {
   Tensor empty(Shape s, at::ScalarType t) const {
     for (int64_t n : s)
       if (n < 0) refuse();
-    return at::empty(s, on.dtype(t));
+    // (at::empty without its dispatch)
+    return at::detail::empty_cuda(s, t, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt);
   }
   bool here(const Tensor& t, at::ScalarType ty, Shape s) const {
     return t.is_cuda() && t.get_device() == dev && t.scalar_type() == ty && t.sizes() == s;

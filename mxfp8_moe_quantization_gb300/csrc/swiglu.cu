@@ -240,9 +240,8 @@ constexpr int cta_bytes() { return SG_WARPS * (warp_bytes<BWD>() + 8); }   // + 
 // current one from registers.  Without PF every CTA has one tile (few tiles:
 // nothing to overlap), loaded straight into registers.
 template <bool BWD, bool PF>
-__global__ void __launch_bounds__(SG_WARPS * 32, BWD ? 3 : 4)
-    k_swiglu(const __grid_constant__ CUtensorMap th, const __grid_constant__ CUtensorMap td, SwigluArgs a, int64_t cp0,
-             int64_t cp1, int64_t col_tiles, int64_t tiles) {
+FP8MOE_DEV void swiglu_body(const CUtensorMap* th, const CUtensorMap* td, const SwigluArgs& a, int64_t cp0, int64_t cp1,
+                            int64_t col_tiles, int64_t tiles) {
   extern __shared__ __align__(128) uint8_t dsm[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rq = lane >> 3, cq = lane & 7;
   uint8_t* wbuf = dsm + warp * warp_bytes<BWD>();
@@ -256,9 +255,9 @@ __global__ void __launch_bounds__(SG_WARPS * 32, BWD ? 3 : 4)
     const int64_t r = row_of(t), c = col_of(t);
     if (r >= a.M || c >= a.F || (a.stall && blockIdx.x == 0 && warp == 0)) return;
     mbar_expect_tx(wbar, warp_bytes<BWD>());
-    tma_load_2d(wbuf, &th, wbar, (int)c, (int)r);
-    tma_load_2d(wbuf + BOX_BYTES, &th, wbar, (int)(a.F + c), (int)r);
-    if (BWD) tma_load_2d(wbuf + 2 * BOX_BYTES, &td, wbar, (int)c, (int)r);
+    tma_load_2d(wbuf, th, wbar, (int)c, (int)r);
+    tma_load_2d(wbuf + BOX_BYTES, th, wbar, (int)(a.F + c), (int)r);
+    if (BWD) tma_load_2d(wbuf + 2 * BOX_BYTES, td, wbar, (int)c, (int)r);
   };
   if (PF) {
     if (lane == 0) {
@@ -352,11 +351,16 @@ __global__ void __launch_bounds__(SG_WARPS * 32, BWD ? 3 : 4)
   }
 }
 
-template <bool BWD, bool PF>
-cudaError_t launch_t(const CUtensorMap& th, const CUtensorMap& td, const SwigluArgs& a, int64_t cp0, int64_t cp1,
-                     int64_t col_tiles, int64_t tiles, int64_t blocks, cudaStream_t st) {
-  k_swiglu<BWD, PF><<<(unsigned)blocks, SG_WARPS * 32, PF ? cta_bytes<BWD>() : 0, st>>>(th, td, a, cp0, cp1, col_tiles, tiles);
-  return cudaGetLastError();
+template <bool BWD>
+__global__ void __launch_bounds__(SG_WARPS * 32, BWD ? 3 : 4)
+    k_swiglu_run(const __grid_constant__ CUtensorMap th, const __grid_constant__ CUtensorMap td, SwigluArgs a, int64_t cp0,
+                 int64_t cp1, int64_t col_tiles, int64_t tiles) {
+  swiglu_body<BWD, true>(&th, &td, a, cp0, cp1, col_tiles, tiles);
+}
+template <bool BWD>
+__global__ void __launch_bounds__(SG_WARPS * 32, BWD ? 3 : 4)
+    k_swiglu_few(SwigluArgs a, int64_t cp0, int64_t cp1, int64_t col_tiles, int64_t tiles) {
+  swiglu_body<BWD, false>(nullptr, nullptr, a, cp0, cp1, col_tiles, tiles);
 }
 
 template <bool BWD>
@@ -367,16 +371,18 @@ cudaError_t launch_dir(SwigluArgs a, cudaStream_t st) {
   const int64_t col_tiles = (a.F + SG_COLS * SG_CW - 1) / (SG_COLS * SG_CW);
   const int64_t tiles = (a.M + SG_ROWS * SG_RW - 1) / (SG_ROWS * SG_RW) * col_tiles;
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  CUtensorMap th{}, td{};
   // Fewer tiles than SMs: straight into registers, without the boxes' barrier
   // and descriptors (16 tiles: 3.6 us forward and 5.5 backward against 3.8 and
   // 5.9; even at 256).  A box is not wider than a result row.
-  if (tiles <= a.num_sms || a.F < SG_COLS)
-    return launch_t<BWD, false>(th, td, a, cp0, cp1, col_tiles, tiles, tiles, st);
-  cudaError_t e = cudaFuncSetAttribute(k_swiglu<BWD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, cta_bytes<BWD>());
+  if (tiles <= a.num_sms || a.F < SG_COLS) {
+    k_swiglu_few<BWD><<<(unsigned)tiles, SG_WARPS * 32, 0, st>>>(a, cp0, cp1, col_tiles, tiles);
+    return cudaGetLastError();
+  }
+  CUtensorMap th{}, td{};
+  cudaError_t e = cudaFuncSetAttribute(k_swiglu_run<BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, cta_bytes<BWD>());
   if (e != cudaSuccess) return e;
   static std::atomic<int> occ{0};
-  const int64_t fit = (int64_t)a.num_sms * blocks_per_sm(occ, k_swiglu<BWD, true>, SG_WARPS * 32, cta_bytes<BWD>(), 1);
+  const int64_t fit = (int64_t)a.num_sms * blocks_per_sm(occ, k_swiglu_run<BWD>, SG_WARPS * 32, cta_bytes<BWD>(), 1);
   a.stall = take_ring_stall_hook();
   cuuint64_t dims[2] = {(cuuint64_t)(2 * a.F), (cuuint64_t)a.M}, strides[1] = {(cuuint64_t)(a.ldh * 2)};
   const cuuint32_t box[2] = {SG_COLS, SG_ROWS};
@@ -393,7 +399,9 @@ cudaError_t launch_dir(SwigluArgs a, cudaStream_t st) {
   // 2048: 99 us against 76), one run of tiles per resident CTA waits for the
   // slowest (51136 x 1408 backward: 150 us against 125).
   const int64_t per = tiles >= 3 * fit ? 3 : tiles >= 2 * fit ? 2 : 1;
-  return launch_t<BWD, true>(th, td, a, cp0, cp1, col_tiles, tiles, (tiles + per - 1) / per, st);
+  k_swiglu_run<BWD><<<(unsigned)((tiles + per - 1) / per), SG_WARPS * 32, cta_bytes<BWD>(), st>>>(th, td, a, cp0, cp1,
+                                                                                               col_tiles, tiles);
+  return cudaGetLastError();
 }
 
 }  // namespace
