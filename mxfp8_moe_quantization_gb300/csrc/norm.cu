@@ -166,6 +166,13 @@ __global__ void __launch_bounds__(norm_threads<V>()) k_norm_fwd(NormFwdArgs a, i
     xv[i] = ok ? ld16(a.x + row * a.ldx + (int64_t)ch * 8) : make_uint4(0, 0, 0, 0);
     rv[i] = ok && a.r ? ld16(a.r + row * a.ldr + (int64_t)ch * 8) : make_uint4(0, 0, 0, 0);
   }
+  // the weights ahead of the row's sum where registers allow
+  constexpr bool EARLY_W = V <= 2;
+  Vec8 we[EARLY_W ? V : 1];
+  if constexpr (EARLY_W) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) we[i] = t + i * tpr < nch ? load_w8<W32>(a.w, t + i * tpr) : Vec8{};
+  }
   Vec8 v[V];
   uint64_t ss2 = 0;
 #pragma unroll
@@ -190,7 +197,7 @@ __global__ void __launch_bounds__(norm_threads<V>()) k_norm_fwd(NormFwdArgs a, i
     const bool ok = active && ch < nch;
     if (a.h && ok) *reinterpret_cast<uint4*>(a.h + row * a.H + (int64_t)ch * 8) = pack8(v[i]);
     // (chunks past the row are zero, as their weights are)
-    const Vec8 wf = ok ? load_w8<W32>(a.w, ch) : Vec8{};
+    const Vec8 wf = EARLY_W ? we[EARLY_W ? i : 0] : ok ? load_w8<W32>(a.w, ch) : Vec8{};
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[i].p[j] = ok ? mul2(mul2(v[i].p[j], rstd2), wf.p[j]) : 0;
     if (OUT >= NORM_OUT_ROW) am = absmax8(am, v[i]);
