@@ -17,8 +17,8 @@
 // from the lane's registers, so the transposed codes need no byte transposes.
 //
 // Bound by HBM: 6.06 bytes per element forward, 10.1 backward.  Measured: 36448
-// x 2048 in 256 groups forward, both directions, 76 us = 5.9 TB/s (89% of a
-// copy's rate); 51136 x 1408 backward 125 us = 5.9 TB/s (88%).  The first form,
+// x 2048 in 256 groups forward, both directions, 74 us = 6.1 TB/s (91% of a
+// copy's rate); 51136 x 1408 backward 120 us = 6.1 TB/s (91%).  The first form,
 // with every lane deriving every scale, expf and a division, and 45
 // instructions per element instead of about 20, took 152 and 283 us.
 #include "common.cuh"
@@ -241,29 +241,46 @@ constexpr int cta_bytes() { return SG_WARPS * (warp_bytes<BWD>() + 8); }   // + 
 // nothing to overlap), loaded straight into registers.
 template <bool BWD, bool PF>
 FP8MOE_DEV void swiglu_body(const CUtensorMap* th, const CUtensorMap* td, const SwigluArgs& a, int64_t cp0, int64_t cp1,
-                            int64_t col_tiles, int64_t tiles) {
+                            int col_tiles, int tiles, int per) {
   extern __shared__ __align__(128) uint8_t dsm[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rq = lane >> 3, cq = lane & 7;
   uint8_t* wbuf = dsm + warp * warp_bytes<BWD>();
   uint64_t* wbar = reinterpret_cast<uint64_t*>(dsm + SG_WARPS * warp_bytes<BWD>()) + warp;
-  const int64_t t0 = PF ? tiles * blockIdx.x / gridDim.x : blockIdx.x;
-  const int64_t t1 = PF ? tiles * (blockIdx.x + 1) / gridDim.x : t0 + 1;
-  auto row_of = [&](int64_t t) { return (t / col_tiles * SG_RW + warp % SG_RW) * SG_ROWS; };
-  auto col_of = [&](int64_t t) { return (t % col_tiles * SG_CW + warp / SG_RW) * SG_COLS; };
+  // the CTA's run of tiles, and a tile's place stepped along it
+  const int t0 = blockIdx.x * per, t1 = tiles - t0 < per ? tiles : t0 + per;
+  struct Place {
+    int64_t row;
+    int col;
+  };
+  auto first = [&](int t) {
+    const int rb = t / col_tiles;
+    return Place{((int64_t)rb * SG_RW + warp % SG_RW) * SG_ROWS, ((t - rb * col_tiles) * SG_CW + warp / SG_RW) * SG_COLS};
+  };
+  const int col_end = col_tiles * SG_CW * SG_COLS;
+  auto next = [&](Place p) {
+    p.col += SG_CW * SG_COLS;
+    if (p.col >= col_end) {
+      p.col -= col_end;
+      p.row += SG_RW * SG_ROWS;
+    }
+    return p;
+  };
   // the tile's boxes (one lane); a warp whose rows lie past M loads nothing
-  auto issue = [&](int64_t t) {
-    const int64_t r = row_of(t), c = col_of(t);
+  auto issue = [&](const Place& p) {
+    const int64_t r = p.row;
+    const int c = p.col;
     if (r >= a.M || c >= a.F || (a.stall && blockIdx.x == 0 && warp == 0)) return;
     mbar_expect_tx(wbar, warp_bytes<BWD>());
-    tma_load_2d(wbuf, th, wbar, (int)c, (int)r);
-    tma_load_2d(wbuf + BOX_BYTES, th, wbar, (int)(a.F + c), (int)r);
-    if (BWD) tma_load_2d(wbuf + 2 * BOX_BYTES, td, wbar, (int)c, (int)r);
+    tma_load_2d(wbuf, th, wbar, c, (int)r);
+    tma_load_2d(wbuf + BOX_BYTES, th, wbar, (int)a.F + c, (int)r);
+    if (BWD) tma_load_2d(wbuf + 2 * BOX_BYTES, td, wbar, c, (int)r);
   };
+  Place cur = first(t0);
   if (PF) {
     if (lane == 0) {
       mbar_init(wbar, 1);
       mbar_fence_init();
-      if (t0 < t1) issue(t0);
+      issue(cur);
     }
     __syncwarp();
   }
@@ -271,12 +288,13 @@ FP8MOE_DEV void swiglu_body(const CUtensorMap* th, const CUtensorMap* td, const 
   tp.W = BWD ? 2 * a.F : a.F;
   tp.row0 = -1;
   uint32_t parity = 0;
-  for (int64_t t = t0; t < t1; ++t) {
-    const int64_t row0 = row_of(t);
+  for (int t = t0; t < t1; ++t) {
+    const int64_t row0 = cur.row;
     if (row0 >= a.M) break;   // column tiles are fastest: the later tiles' rows are not lower
-    const int64_t col0 = col_of(t), col = col0 + cq * CW;
+    const int64_t col0 = cur.col, col = col0 + cq * CW;
+    cur = next(cur);
     if (col0 >= a.F) {   // this warp's half of the last column tile is empty
-      if (PF && lane == 0 && t + 1 < t1) issue(t + 1);
+      if (PF && lane == 0 && t + 1 < t1) issue(cur);
       continue;
     }
     const bool ok = col < a.F;
@@ -343,7 +361,7 @@ FP8MOE_DEV void swiglu_body(const CUtensorMap* th, const CUtensorMap* td, const 
       __syncwarp();   // the boxes are read
       if (lane == 0 && t + 1 < t1) {
         fence_proxy_async_smem();
-        issue(t + 1);
+        issue(cur);
       }
     }
     put_tile(a, tp, col0, ok, lane, v);
@@ -354,13 +372,13 @@ FP8MOE_DEV void swiglu_body(const CUtensorMap* th, const CUtensorMap* td, const 
 template <bool BWD>
 __global__ void __launch_bounds__(SG_WARPS * 32, BWD ? 3 : 4)
     k_swiglu_run(const __grid_constant__ CUtensorMap th, const __grid_constant__ CUtensorMap td, SwigluArgs a, int64_t cp0,
-                 int64_t cp1, int64_t col_tiles, int64_t tiles) {
-  swiglu_body<BWD, true>(&th, &td, a, cp0, cp1, col_tiles, tiles);
+                 int64_t cp1, int col_tiles, int tiles, int per) {
+  swiglu_body<BWD, true>(&th, &td, a, cp0, cp1, col_tiles, tiles, per);
 }
 template <bool BWD>
-__global__ void __launch_bounds__(SG_WARPS * 32, BWD ? 3 : 4)
-    k_swiglu_few(SwigluArgs a, int64_t cp0, int64_t cp1, int64_t col_tiles, int64_t tiles) {
-  swiglu_body<BWD, false>(nullptr, nullptr, a, cp0, cp1, col_tiles, tiles);
+__global__ void __launch_bounds__(SG_WARPS * 32)
+    k_swiglu_few(SwigluArgs a, int64_t cp0, int64_t cp1, int col_tiles, int tiles) {
+  swiglu_body<BWD, false>(nullptr, nullptr, a, cp0, cp1, col_tiles, tiles, 1);
 }
 
 template <bool BWD>
@@ -373,9 +391,9 @@ cudaError_t launch_dir(SwigluArgs a, cudaStream_t st) {
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   // Fewer tiles than SMs: straight into registers, without the boxes' barrier
   // and descriptors (16 tiles: 3.6 us forward and 5.5 backward against 3.8 and
-  // 5.9; even at 256).  A box is not wider than a result row.
+  // 5.9; no difference at 256).  A box is not wider than a result row.
   if (tiles <= a.num_sms || a.F < SG_COLS) {
-    k_swiglu_few<BWD><<<(unsigned)tiles, SG_WARPS * 32, 0, st>>>(a, cp0, cp1, col_tiles, tiles);
+    k_swiglu_few<BWD><<<(unsigned)tiles, SG_WARPS * 32, 0, st>>>(a, cp0, cp1, (int)col_tiles, (int)tiles);
     return cudaGetLastError();
   }
   CUtensorMap th{}, td{};
@@ -399,8 +417,8 @@ cudaError_t launch_dir(SwigluArgs a, cudaStream_t st) {
   // 2048: 99 us against 76), one run of tiles per resident CTA waits for the
   // slowest (51136 x 1408 backward: 150 us against 125).
   const int64_t per = tiles >= 3 * fit ? 3 : tiles >= 2 * fit ? 2 : 1;
-  k_swiglu_run<BWD><<<(unsigned)((tiles + per - 1) / per), SG_WARPS * 32, cta_bytes<BWD>(), st>>>(th, td, a, cp0, cp1,
-                                                                                               col_tiles, tiles);
+  k_swiglu_run<BWD><<<(unsigned)((tiles + per - 1) / per), SG_WARPS * 32, cta_bytes<BWD>(), st>>>(
+      th, td, a, cp0, cp1, (int)col_tiles, (int)tiles, (int)per);
   return cudaGetLastError();
 }
 
