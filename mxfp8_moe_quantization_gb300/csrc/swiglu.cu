@@ -66,31 +66,39 @@ FP8MOE_DEV uint64_t sigmoid2(uint64_t n2) {
 
 // The padded row (in a layout whose groups start at multiples of 128 rows) of
 // row `row0`, a multiple of 32; -1 if the offsets are invalid.  A warp calls
-// it; each of its lanes takes every 32nd group, the loads of eight in flight.
+// it; each of its lanes takes every 32nd group, U of them with their loads in
+// flight together.
+template <int U>
+FP8MOE_DEV uint32_t rows_before(const int32_t* __restrict__ offs, int E, int m, int r, int e0, bool& bad) {
+  int end[U], start[U];
+  uint32_t sum = 0;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int e = e0 + 32 * i;
+    end[i] = e < E ? __ldg(offs + e) : 0;
+    start[i] = e < E && e > 0 ? __ldg(offs + e - 1) : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int e = e0 + 32 * i;
+    if (e >= E) break;
+    bad |= start[i] < 0 || end[i] < start[i] || end[i] > m || (end[i] & 31) || (e == E - 1 && end[i] != m);
+    if (end[i] <= r) {
+      sum += ((uint32_t)(end[i] - start[i]) + 127u) & ~127u;
+    } else if (start[i] <= r) {
+      sum += (uint32_t)(r - start[i]);
+    }
+  }
+  return sum;
+}
 FP8MOE_DEV int64_t padded_row(const int32_t* __restrict__ offs, int E, int64_t M, int64_t row0, int lane) {
-  constexpr int U = 8;
   const int m = (int)M, r = (int)row0;   // both at most 2^30
   uint32_t sum = 0;
   bool bad = false;
-  for (int e0 = lane; e0 < E; e0 += 32 * U) {
-    int end[U], start[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int e = e0 + 32 * i;
-      end[i] = e < E ? __ldg(offs + e) : 0;
-      start[i] = e < E && e > 0 ? __ldg(offs + e - 1) : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int e = e0 + 32 * i;
-      if (e >= E) break;
-      bad |= start[i] < 0 || end[i] < start[i] || end[i] > m || (end[i] & 31) || (e == E - 1 && end[i] != m);
-      if (end[i] <= r) {
-        sum += ((uint32_t)(end[i] - start[i]) + 127u) & ~127u;
-      } else if (start[i] <= r) {
-        sum += (uint32_t)(r - start[i]);
-      }
-    }
+  if (E <= 32) {
+    sum = rows_before<1>(offs, E, m, r, lane, bad);
+  } else {
+    for (int e0 = lane; e0 < E; e0 += 256) sum += rows_before<8>(offs, E, m, r, e0, bad);
   }
   if (__any_sync(0xffffffffu, bad)) return -1;
   return (int64_t)__reduce_add_sync(0xffffffffu, sum);
