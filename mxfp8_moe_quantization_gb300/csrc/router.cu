@@ -36,7 +36,6 @@ namespace {
 // Most warps of a CTA whose lanes hold V experts each (its registers).
 template <int V>
 constexpr int most_warps() { return V <= 8 ? 32 : V == 16 ? 16 : 8; }
-constexpr int BWD_WARPS = 8;
 constexpr int SINGLE_CTA_T = 16;   // up to so many tokens one CTA does everything
 
 // order-preserving key: larger float, larger key; NaN sorts with -inf; every
@@ -313,8 +312,8 @@ __global__ void __cluster_dims__(JOIN, 1, 1) __launch_bounds__(JOIN_WARPS * 32) 
 }
 
 template <int V, bool SIG>
-__global__ void __launch_bounds__(BWD_WARPS * 32) k_router_bwd(RouterArgs a) {
-  constexpr int RW = BWD_WARPS;
+__global__ void __launch_bounds__(most_warps<V>() * 32) k_router_bwd(RouterArgs a) {
+  const int RW = blockDim.x >> 5;
   extern __shared__ float rsm[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* ubuf = rsm + warp * a.E;   // the chosen experts' u
@@ -468,10 +467,13 @@ cudaError_t run_fwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
 }
 template <int V, bool SIG>
 cudaError_t run_bwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
-  constexpr int RW = BWD_WARPS;
+  const int64_t want = (a.T + num_sms - 1) / num_sms;
+  const int RW = want < 4 ? 4 : want > most_warps<V>() ? most_warps<V>() : (int)want;
+  const int smem = RW * a.E * 4;
   int64_t blocks = (a.T + RW - 1) / RW;
-  if (blocks > (int64_t)num_sms * 8) blocks = (int64_t)num_sms * 8;
-  k_router_bwd<V, SIG><<<(unsigned)blocks, RW * 32, RW * a.E * 4, st>>>(a);
+  const int64_t most = (int64_t)num_sms * (64 / most_warps<V>());
+  if (blocks > most) blocks = most;
+  k_router_bwd<V, SIG><<<(unsigned)blocks, RW * 32, smem, st>>>(a);
   return cudaGetLastError();
 }
 
