@@ -15,15 +15,16 @@
 //   u_j = scale * s_j dw_j,
 //   softmax: dl = r + u - p sum(u);   sigmoid: dl = (1 - s)(r + u).
 //
-// A warp takes a token, a lane every 32nd expert; the logits are read once.
+// A warp takes a token, a lane every 32nd expert (eight or sixteen lanes where
+// experts are few and tokens many); the logits are read once.
 // Sums over tokens have a fixed order (registers, then warps, then CTAs), so
 // results do not change from run to run.  The CTAs' partial sums are joined by
 // a second kernel of one cluster, launched ahead of the first one's end.
 //
 // Bound by latency, then by instruction issue (a token of 256 experts, top 8:
 // about 1100 warp instructions, half of them the rounds of the choice).  In a
-// graph: 4096 x 256, top 8, 10.4 us forward with the sums and 6.0 without, 5.0
-// backward; 8192 x 64, top 6, 10.1; 3 tokens 3.9.  The first form, which
+// graph: 4096 x 256, top 8, 10.4 us forward with the sums and 6.0 without, 4.6
+// backward; 8192 x 64, top 6, 8.4 and 4.2; 3 tokens 3.9.  The first form, which
 // carried scores through the rounds and joined 512 partial sums in one CTA,
 // took 29.9 us on the first.
 #include "common.cuh"
@@ -45,33 +46,52 @@ FP8MOE_DEV uint32_t order_key(float f) {
   return (uint32_t)u ^ ((uint32_t)(u >> 31) | 0x80000000u);
 }
 
-FP8MOE_DEV float warp_sum(float v) {
+// sums and maxima over the G lanes of a token (every lane gets the result)
+template <int G = 32>
+FP8MOE_DEV float lane_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-FP8MOE_DEV float warp_max(float v) {
+template <int G>
+FP8MOE_DEV float lane_max(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+template <int G>
+FP8MOE_DEV uint32_t lane_umax(uint32_t v) {
+  if constexpr (G == 32) return __reduce_max_sync(0xffffffffu, v);
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+template <int G>
+FP8MOE_DEV uint32_t lane_umin(uint32_t v) {
+  if constexpr (G == 32) return __reduce_min_sync(0xffffffffu, v);
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
 constexpr float NEG_INF = -__builtin_huge_valf();
 
-template <int V>
-FP8MOE_DEV void load_row(const RouterArgs& a, int64_t t, int lane, bool on, float (&x)[V]) {
+// the logits of token t at this lane's experts i G + l; -inf past the last one
+// and everywhere in a row that is no token
+template <int V, int G>
+FP8MOE_DEV void load_row(const RouterArgs& a, int64_t t, int l, bool on, float (&x)[V]) {
   if (a.bf16) {
     const uint16_t* p = (const uint16_t*)a.logits + t * a.ld;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = i * 32 + lane;
+      const int e = i * G + l;
       x[i] = on && e < a.E ? __uint_as_float((uint32_t)p[e] << 16) : NEG_INF;
     }
   } else {
     const float* p = (const float*)a.logits + t * a.ld;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = i * 32 + lane;
+      const int e = i * G + l;
       x[i] = on && e < a.E ? p[e] : NEG_INF;
     }
   }
@@ -90,7 +110,7 @@ FP8MOE_DEV float score_of(float x, const RowStat& st) {
   return SIG ? sigmoid_rn(x) : expf(x - st.m) * st.rz;
 }
 // s: sigmoids, or the softmax's e^(x - m) before the division by z
-template <int V, bool SIG>
+template <int V, int G, bool SIG>
 FP8MOE_DEV RowStat row_scores(const float (&x)[V], float (&s)[V]) {
   RowStat st{0.0f, 0.0f};
   float z = 0.0f;
@@ -101,12 +121,12 @@ FP8MOE_DEV RowStat row_scores(const float (&x)[V], float (&s)[V]) {
     float m = NEG_INF;
 #pragma unroll
     for (int i = 0; i < V; ++i) m = fmaxf(m, x[i]);
-    m = warp_max(m);
+    m = lane_max<G>(m);
     st.m = m == NEG_INF ? 0.0f : m;
 #pragma unroll
     for (int i = 0; i < V; ++i) z += s[i] = expf(x[i] - st.m);
   }
-  z = warp_sum(z);
+  z = lane_sum<G>(z);
   st.rz = z == 0.0f ? 0.0f : __frcp_rn(z);
   return st;
 }
@@ -119,11 +139,11 @@ FP8MOE_DEV float logit_at(const RouterArgs& a, int64_t t, int e) {
 // loss from counts and probability sums; every thread of the CTA calls it.
 // part: this CTA's share of sum n_e P_e (thread 0 has the result)
 FP8MOE_DEV float cta_sum(float v, float* red) {
-  v = warp_sum(v);
+  v = lane_sum(v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   v = 0.0f;
-  if (threadIdx.x < 32) v = warp_sum(threadIdx.x < (blockDim.x >> 5) ? red[threadIdx.x] : 0.0f);
+  if (threadIdx.x < 32) v = lane_sum(threadIdx.x < (blockDim.x >> 5) ? red[threadIdx.x] : 0.0f);
   return v;
 }
 FP8MOE_DEV float loss_of(float np, int tokens, int E, int k) {
@@ -131,31 +151,34 @@ FP8MOE_DEV float loss_of(float np, int tokens, int E, int k) {
   return np * __fdiv_rn((float)E, (float)k) / (N * N);
 }
 
-template <int V, bool SIG>
+// G lanes take a token, a lane every G-th expert; a warp 32 / G tokens at a time.
+template <int V, int G, bool SIG>
 __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_fwd(RouterArgs a) {
-  const int RW = blockDim.x >> 5;
+  constexpr int TPW = 32 / G;
   extern __shared__ float rsm[];
   __shared__ float red[32];
+  const int RW = blockDim.x >> 5;
   float* cp = rsm;                      // [RW][E]
   int* cn = (int*)(rsm + RW * a.E);     // [E + 1]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % G;
   const bool sums = a.counts != nullptr;
   // the joining kernel may take its place; it waits for this one's end
   asm volatile("griddepcontrol.launch_dependents;");
   float acc[V] = {};
   int tokens = 0;
   if (sums) {
-    for (int e = threadIdx.x; e <= a.E; e += RW * 32) cn[e] = 0;
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) cn[e] = 0;
     __syncthreads();
   }
   float bias[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) bias[i] = a.bias && i * 32 + lane < a.E ? a.bias[i * 32 + lane] : 0.0f;
-  for (int64_t t = (int64_t)blockIdx.x * RW + warp; t < a.T; t += (int64_t)gridDim.x * RW) {
-    const bool on = !a.mask || a.mask[t] != 0;
+  for (int i = 0; i < V; ++i) bias[i] = a.bias && i * G + l < a.E ? a.bias[i * G + l] : 0.0f;
+  for (int64_t tw = ((int64_t)blockIdx.x * RW + warp) * TPW; tw < a.T; tw += (int64_t)gridDim.x * RW * TPW) {
+    const int64_t t = tw + lane / G;   // past T: no token, nothing stored
+    const bool row = t < a.T, on = row && (!a.mask || a.mask[t] != 0);
     float x[V], s[V];
-    load_row<V>(a, t, lane, on, x);
-    const RowStat st = row_scores<V, SIG>(x, s);
+    load_row<V, G>(a, t, l, on, x);
+    const RowStat st = row_scores<V, G, SIG>(x, s);
     uint32_t key[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -163,53 +186,58 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_fwd(RouterArgs 
       acc[i] += p;
       // dead experts stay below every other whatever their bias
       const float f = !a.bias ? x[i] : x[i] == NEG_INF ? NEG_INF : (SIG ? s[i] : p) + bias[i];
-      key[i] = i * 32 + lane < a.E ? order_key(f) : 0u;
+      key[i] = i * G + l < a.E ? order_key(f) : 0u;
     }
     tokens += on;
-    // k rounds: the warp's largest key, then the lowest id that has it
+    // k rounds: the token's largest key, then the lowest id that has it
     int my_e = 0;
     for (int j = 0; j < a.k; ++j) {
       uint32_t bk = key[0];
 #pragma unroll
       for (int i = 1; i < V; ++i) bk = max(bk, key[i]);
-      const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
+      const uint32_t top = lane_umax<G>(bk);
       uint32_t be = 0xffffffffu;
 #pragma unroll
       for (int i = V - 1; i >= 0; --i)
-        if (key[i] == top) be = (uint32_t)(i * 32 + lane);
-      const uint32_t e = __reduce_min_sync(0xffffffffu, be);
-      if (lane == j) my_e = (int)e;
+        if (key[i] == top) be = (uint32_t)(i * G + l);
+      const uint32_t e = lane_umin<G>(be);
+      if (l == j) my_e = (int)e;
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (e == (uint32_t)(i * 32 + lane)) key[i] = 0u;
+        if (e == (uint32_t)(i * G + l)) key[i] = 0u;
     }
     // lane j: slot j's weight, from its logit
     float w = 0.0f;
-    if (lane < a.k) {
+    if (l < a.k && row) {
       const float xe = on ? logit_at(a, t, my_e) : NEG_INF;
       w = score_of<SIG>(xe, st);
       if (sums && xe != NEG_INF) atomicAdd(&cn[my_e], 1);
     }
     if (a.renorm) {
-      const float z = warp_sum(w);
+      const float z = lane_sum<G>(w);
       w = __fdiv_rn(w, z == 0.0f ? 1.0f : z);
     }
-    if (lane < a.k) {
-      a.idx[t * a.k + lane] = my_e;
-      a.w[t * a.k + lane] = w * a.route_scale;
+    if (l < a.k && row) {
+      a.idx[t * a.k + l] = my_e;
+      a.w[t * a.k + l] = w * a.route_scale;
     }
   }
   if (!sums) return;
+  // the lanes that share experts, in lane order, then the warps
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    if (i * 32 + lane < a.E) cp[warp * a.E + i * 32 + lane] = acc[i];
-  if (lane == 0) atomicAdd(&cn[a.E], tokens);
+#pragma unroll
+    for (int o = G; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (lane < G && i * G + l < a.E) cp[warp * a.E + i * G + l] = acc[i];
+  if (l == 0) atomicAdd(&cn[a.E], tokens);
   __syncthreads();
   const bool single = gridDim.x == 1;
   float* pp = single ? a.psum : (float*)a.workspace + (int64_t)blockIdx.x * a.E;
   int* pn = single ? a.counts : (int*)((float*)a.workspace + (int64_t)gridDim.x * a.E) + (int64_t)blockIdx.x * (a.E + 1);
   float np = 0.0f;
-  for (int e = threadIdx.x; e <= a.E; e += RW * 32) {
+  for (int e = threadIdx.x; e <= a.E; e += blockDim.x) {
     const int n = cn[e];
     pn[e] = n;
     if (e < a.E) {
@@ -287,7 +315,7 @@ __global__ void __cluster_dims__(JOIN, 1, 1) __launch_bounds__(JOIN_WARPS * 32) 
   // every CTA's share of sum n_e P_e into rank 0's shared memory
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (warp == 0) {
-    np = warp_sum(np);
+    np = lane_sum(np);
     if (lane == 0) {
       uint32_t at;
       asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(&share[rank])));
@@ -303,7 +331,7 @@ __global__ void __cluster_dims__(JOIN, 1, 1) __launch_bounds__(JOIN_WARPS * 32) 
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (rank == 0 && warp == 0) {
     tok = __reduce_add_sync(0xffffffffu, tok);
-    np = warp_sum(lane < JOIN ? share[lane] : 0.0f);
+    np = lane_sum(lane < JOIN ? share[lane] : 0.0f);
     if (lane == 0) {
       a.counts[a.E] = tok;
       a.loss[0] = loss_of(np, tok, a.E, a.k);
@@ -311,57 +339,59 @@ __global__ void __cluster_dims__(JOIN, 1, 1) __launch_bounds__(JOIN_WARPS * 32) 
   }
 }
 
-template <int V, bool SIG>
+template <int V, int G, bool SIG>
 __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_bwd(RouterArgs a) {
-  const int RW = blockDim.x >> 5;
+  constexpr int TPW = 32 / G;
   extern __shared__ float rsm[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* ubuf = rsm + warp * a.E;   // the chosen experts' u
+  const int RW = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % G;
+  float* ubuf = rsm + (warp * TPW + lane / G) * a.E;   // the chosen experts' u
   float c[V];
   float coef = 0.0f;
   if (a.dloss) coef = a.dloss[0] * loss_of(1.0f, a.counts_in[a.E], a.E, a.k);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = i * 32 + lane;
+    const int e = i * G + l;
     c[i] = a.dloss && e < a.E ? coef * (float)a.counts_in[e] : 0.0f;
     if (e < a.E) ubuf[e] = 0.0f;
   }
   __syncwarp();
-  for (int64_t t = (int64_t)blockIdx.x * RW + warp; t < a.T; t += (int64_t)gridDim.x * RW) {
-    const bool on = !a.mask || a.mask[t] != 0;
+  for (int64_t tw = ((int64_t)blockIdx.x * RW + warp) * TPW; tw < a.T; tw += (int64_t)gridDim.x * RW * TPW) {
+    const int64_t t = tw + lane / G;   // past T: no token, nothing stored
+    const bool row = t < a.T, on = row && (!a.mask || a.mask[t] != 0);
     int e = -1;
     float dwj = 0.0f, xj = 0.0f;
-    if (a.dw && lane < a.k && on) {
-      e = a.idx_in[t * a.k + lane];
+    if (a.dw && l < a.k && on) {
+      e = a.idx_in[t * a.k + l];
       if (e < 0 || e >= a.E) e = -1;
-      dwj = a.dw[t * a.k + lane];
+      dwj = a.dw[t * a.k + l];
     }
     float x[V], s[V];
-    load_row<V>(a, t, lane, on, x);
+    load_row<V, G>(a, t, l, on, x);
     if (e >= 0) xj = logit_at(a, t, e);
-    const RowStat st = row_scores<V, SIG>(x, s);
+    const RowStat st = row_scores<V, G, SIG>(x, s);
     float pc = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) pc = fmaf(s[i] * st.rz, c[i], pc);
     // lane j: slot j's score, from the logit itself
     const float sj = e >= 0 ? score_of<SIG>(xj, st) : 0.0f;
     float u = sj * dwj, us = 0.0f;
-    pc = warp_sum(pc);
+    pc = lane_sum<G>(pc);
     if (a.dw) {
       if (a.renorm) {
-        const float z = warp_sum(sj);
+        const float z = lane_sum<G>(sj);
         const float wj = __fdiv_rn(sj, z == 0.0f ? 1.0f : z);
-        u = wj * (dwj - warp_sum(dwj * wj));
+        u = wj * (dwj - lane_sum<G>(dwj * wj));
       }
       u *= a.route_scale;
-      if constexpr (!SIG) us = warp_sum(u);
+      if constexpr (!SIG) us = lane_sum<G>(u);
       if (e >= 0) atomicAdd(&ubuf[e], u);
       __syncwarp();
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int ei = i * 32 + lane;
-      if (ei >= a.E) continue;
+      const int ei = i * G + l;
+      if (ei >= a.E || !row) continue;
       const float p = s[i] * st.rz;
       float o = p * (c[i] - pc - us) + ubuf[ei];
       if (SIG) o *= 1.0f - s[i];
@@ -420,7 +450,7 @@ __global__ void __launch_bounds__(256) k_route_weight_grad(const uint16_t* __res
     }
 #pragma unroll
     for (int j = 0; j < UK; ++j) {
-      acc[j] = warp_sum(acc[j]);
+      acc[j] = lane_sum(acc[j]);
       if (WPT > 1 && lane == 0) red[warp][j] = acc[j];
     }
     if (WPT > 1) __syncthreads();
@@ -437,21 +467,26 @@ __global__ void __launch_bounds__(256) k_route_weight_grad(const uint16_t* __res
   }
 }
 
-template <int V, bool SIG>
+// Warps per CTA: one CTA per SM, of as many warps as it gets tokens to fill:
+// few partial sums, and tokens spread over the SMs (512 tokens: 3.7 us with CTAs
+// of four warps, 6.4 with CTAs of 32, without the sums).
+template <int V, int G>
+int cta_warps(int64_t T, int64_t sms) {
+  const int64_t want = (T + sms * (32 / G) - 1) / (sms * (32 / G));
+  return want < 4 ? 4 : want > most_warps<V>() ? most_warps<V>() : (int)want;
+}
+
+template <int V, int G, bool SIG>
 cudaError_t run_fwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
   const bool sums = a.counts != nullptr;
-  // one CTA per SM, of as many warps as it gets tokens: few partial sums, and
-  // tokens spread over the SMs (512 tokens: 3.7 us with CTAs of four warps,
-  // 6.4 with CTAs of 32, without the sums)
   const bool single = sums && a.T <= SINGLE_CTA_T;
-  const int64_t want = single ? a.T : (a.T + num_sms - 1) / num_sms;
-  const int RW = want < 4 ? 4 : want > most_warps<V>() ? most_warps<V>() : (int)want;
+  const int RW = cta_warps<V, G>(a.T, single ? 1 : num_sms), rows = RW * (32 / G);
   const int smem = sums ? (RW * a.E + a.E + 1) * 4 : 0;   // probability sums per warp, counts
-  int64_t blocks = single ? 1 : (a.T + RW - 1) / RW;
+  int64_t blocks = single ? 1 : (a.T + rows - 1) / rows;
   const int64_t most = (int64_t)num_sms * (32 / most_warps<V>());
   if (blocks > most) blocks = most;
   if (sums && blocks > ROUTER_MAX_PARTS) blocks = ROUTER_MAX_PARTS;
-  k_router_fwd<V, SIG><<<(unsigned)blocks, RW * 32, smem, st>>>(a);
+  k_router_fwd<V, G, SIG><<<(unsigned)blocks, RW * 32, smem, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !sums || blocks == 1) return e;
   cudaLaunchConfig_t cfg = {};
@@ -465,43 +500,52 @@ cudaError_t run_fwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, k_router_join, a, (int)blocks);
 }
-template <int V, bool SIG>
+template <int V, int G, bool SIG>
 cudaError_t run_bwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
-  const int64_t want = (a.T + num_sms - 1) / num_sms;
-  const int RW = want < 4 ? 4 : want > most_warps<V>() ? most_warps<V>() : (int)want;
-  const int smem = RW * a.E * 4;
-  int64_t blocks = (a.T + RW - 1) / RW;
+  const int RW = cta_warps<V, G>(a.T, num_sms), rows = RW * (32 / G);
+  const int smem = rows * a.E * 4;
+  int64_t blocks = (a.T + rows - 1) / rows;
   const int64_t most = (int64_t)num_sms * (64 / most_warps<V>());
   if (blocks > most) blocks = most;
-  k_router_bwd<V, SIG><<<(unsigned)blocks, RW * 32, smem, st>>>(a);
+  k_router_bwd<V, G, SIG><<<(unsigned)blocks, RW * 32, smem, st>>>(a);
   return cudaGetLastError();
+}
+
+// Lanes per token: a whole warp, or for many tokens over few experts eight or
+// sixteen lanes of up to eight experts each, which share the steps that do not
+// depend on the experts (65536 x 64, top 6: 22 us forward with eight against 33;
+// 65536 x 128, top 8: 40 with sixteen against 45).  Below eight (32) tokens an
+// SM a warp's shorter way counts for more: no difference at 2048 x 64, 8.3 us
+// against 8.8 at 4096 x 128.  The choice needs k <= lanes.
+int lanes_per_token(const RouterArgs& a, int num_sms) {
+  if (a.E <= 64 && a.k <= 8 && a.T >= 8 * (int64_t)num_sms) return 8;
+  if (a.E > 64 && a.E <= 128 && a.k <= 16 && a.T >= 32 * (int64_t)num_sms) return 16;
+  return 32;
 }
 
 }  // namespace
 
-#define FP8MOE_ROUTER(V, FN)                                                         \
-  if (a.E <= 32 * V)                                                                 \
-    return a.score == FP8MOE_SCORE_SIGMOID ? FN<V, true>(a, num_sms, st) : FN<V, false>(a, num_sms, st);
+#define FP8MOE_ROUTER(V, G, FN)                                                                               \
+  if (g == G && a.E <= G * V)                                                                                 \
+    return a.score == FP8MOE_SCORE_SIGMOID ? FN<V, G, true>(a, num_sms, st) : FN<V, G, false>(a, num_sms, st);
+#define FP8MOE_ROUTER_ALL(FN)                                                                                 \
+  FP8MOE_ROUTER(1, 8, FN) FP8MOE_ROUTER(2, 8, FN) FP8MOE_ROUTER(4, 8, FN) FP8MOE_ROUTER(8, 8, FN)             \
+  FP8MOE_ROUTER(8, 16, FN)                                                                                    \
+  FP8MOE_ROUTER(1, 32, FN) FP8MOE_ROUTER(2, 32, FN) FP8MOE_ROUTER(4, 32, FN) FP8MOE_ROUTER(8, 32, FN)         \
+  FP8MOE_ROUTER(16, 32, FN) FP8MOE_ROUTER(32, 32, FN)
 
 // T == 0: one CTA writes the empty sums
 cudaError_t launch_router_fwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
-  FP8MOE_ROUTER(1, run_fwd)
-  FP8MOE_ROUTER(2, run_fwd)
-  FP8MOE_ROUTER(4, run_fwd)
-  FP8MOE_ROUTER(8, run_fwd)
-  FP8MOE_ROUTER(16, run_fwd)
-  FP8MOE_ROUTER(32, run_fwd)
+  const int g = lanes_per_token(a, num_sms);
+  FP8MOE_ROUTER_ALL(run_fwd)
   return cudaErrorInvalidValue;
 }
 cudaError_t launch_router_bwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
-  FP8MOE_ROUTER(1, run_bwd)
-  FP8MOE_ROUTER(2, run_bwd)
-  FP8MOE_ROUTER(4, run_bwd)
-  FP8MOE_ROUTER(8, run_bwd)
-  FP8MOE_ROUTER(16, run_bwd)
-  FP8MOE_ROUTER(32, run_bwd)
+  const int g = lanes_per_token(a, num_sms);
+  FP8MOE_ROUTER_ALL(run_bwd)
   return cudaErrorInvalidValue;
 }
+#undef FP8MOE_ROUTER_ALL
 #undef FP8MOE_ROUTER
 
 cudaError_t launch_route_weight_grad(const void* dout, const void* y, const int32_t* row_of, int64_t T, int64_t N,

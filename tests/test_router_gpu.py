@@ -119,6 +119,24 @@ def test_masks(F, T, score):
             assert torch.equal(a, b)
 
 
+# many tokens over few experts: eight or sixteen lanes a token, ragged tokens
+# per warp, k up to the lanes and (the last two) past them
+MANY = [(1301, 8, 8), (1250, 16, 2), (2431, 31, 5), (1999, 64, 6), (4999, 100, 9), (5003, 128, 16), (1301, 64, 9),
+        (4999, 128, 17)]
+
+
+@pytest.mark.parametrize("T,E,k", MANY)
+@pytest.mark.parametrize("score,bf16", [("softmax", False), ("sigmoid", True)])
+def test_many_tokens(F, T, E, k, score, bf16):
+    x = _logits(T, E, T + E, bf16, dead=1)
+    x[5] = -float("inf")
+    mask = torch.ones(T, dtype=torch.uint8)
+    mask[::7] = 0
+    bias = torch.randn(E, generator=torch.Generator().manual_seed(1)) * 0.1
+    _check(F, x, k, score, True, 2.5, mask=mask)
+    _check(F, x, k, score, False, 1.0, bias=bias, ld=E + 3)
+
+
 def test_ties_and_signed_zero(F):
     """Equal keys go to the lowest id; 0 and -0 are equal."""
     x = torch.zeros(40, 96)
@@ -161,7 +179,7 @@ def test_same_bits_every_time(F):
         assert torch.equal(u, v)
 
 
-@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (2, 8, 2), (33, 256, 8), (257, 100, 4), (9, 1024, 10), (40, 40, 32)])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (2, 8, 2), (33, 256, 8), (257, 100, 4), (9, 1024, 10), (40, 40, 32)] + MANY)
 @pytest.mark.parametrize("score,renorm,bf16", [("softmax", False, False), ("softmax", True, True),
                                                ("sigmoid", True, False), ("sigmoid", False, True)])
 def test_backward(F, T, E, k, score, renorm, bf16):
