@@ -100,23 +100,31 @@ FP8MOE_DEV void load_row(const RouterArgs& a, int64_t t, int l, bool on, float (
 // 1 / (1 + e^-x), each step rounded to nearest (the choice with a bias hangs on it)
 FP8MOE_DEV float sigmoid_rn(float x) { return __frcp_rn(1.0f + expf(-x)); }
 
+// the same for the gradient: the reciprocal off by an ulp at most, without the
+// steps that round it
+FP8MOE_DEV float sigmoid_grad(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-x)));
+  return r;
+}
+
 // What turns a logit of the row into its score: softmax s = e^(x - m) / z;
 // z is also the sum of the sigmoids.
 struct RowStat {
   float m, rz;   // rz = 1 / z, 0 for a row of nothing but -inf
 };
-template <bool SIG>
+template <bool SIG, bool GRAD = false>
 FP8MOE_DEV float score_of(float x, const RowStat& st) {
-  return SIG ? sigmoid_rn(x) : expf(x - st.m) * st.rz;
+  return SIG ? (GRAD ? sigmoid_grad(x) : sigmoid_rn(x)) : expf(x - st.m) * st.rz;
 }
 // s: sigmoids, or the softmax's e^(x - m) before the division by z
-template <int V, int G, bool SIG>
+template <int V, int G, bool SIG, bool GRAD = false>
 FP8MOE_DEV RowStat row_scores(const float (&x)[V], float (&s)[V]) {
   RowStat st{0.0f, 0.0f};
   float z = 0.0f;
   if constexpr (SIG) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) z += s[i] = sigmoid_rn(x[i]);
+    for (int i = 0; i < V; ++i) z += s[i] = GRAD ? sigmoid_grad(x[i]) : sigmoid_rn(x[i]);
   } else {
     float m = NEG_INF;
 #pragma unroll
@@ -369,12 +377,12 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_bwd(RouterArgs 
     float x[V], s[V];
     load_row<V, G>(a, t, l, on, x);
     if (e >= 0) xj = logit_at(a, t, e);
-    const RowStat st = row_scores<V, G, SIG>(x, s);
+    const RowStat st = row_scores<V, G, SIG, true>(x, s);
     float pc = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) pc = fmaf(s[i] * st.rz, c[i], pc);
     // lane j: slot j's score, from the logit itself
-    const float sj = e >= 0 ? score_of<SIG>(xj, st) : 0.0f;
+    const float sj = e >= 0 ? score_of<SIG, true>(xj, st) : 0.0f;
     float u = sj * dwj, us = 0.0f;
     pc = lane_sum<G>(pc);
     if (a.dw) {
