@@ -3,9 +3,9 @@
 Argument marshalling only: every function below passes device pointers,
 sizes and the current CUDA stream of PyTorch to the C ABI declared in
 ``include/fp8moe.h`` (the operators around the expert products through the
-compiled module ``_binding``, the others through ctypes) and raises ``Fp8MoeError`` on any non-OK status.  PyTorch
-provides device memory and streams; all arithmetic runs in the library's CUDA
-kernels.  There is no CPU path: importing works without a GPU (so the host
+compiled module ``_binding``, the others through ctypes) and raises
+``Fp8MoeError`` on any non-OK status.  PyTorch provides device memory and
+streams; all arithmetic runs in the library's CUDA kernels.  There is no CPU path: importing works without a GPU (so the host
 logic can be tested), but every call needs the built library and a CUDA
 device.
 """

@@ -61,17 +61,23 @@ FP8MOE_DEV float lane_max(float v) {
 }
 template <int G>
 FP8MOE_DEV uint32_t lane_umax(uint32_t v) {
-  if constexpr (G == 32) return __reduce_max_sync(0xffffffffu, v);
+  if constexpr (G == 32) {
+    return __reduce_max_sync(0xffffffffu, v);
+  } else {
 #pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+    for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
 }
 template <int G>
 FP8MOE_DEV uint32_t lane_umin(uint32_t v) {
-  if constexpr (G == 32) return __reduce_min_sync(0xffffffffu, v);
+  if constexpr (G == 32) {
+    return __reduce_min_sync(0xffffffffu, v);
+  } else {
 #pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+    for (int o = G / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
 }
 
 constexpr float NEG_INF = -__builtin_huge_valf();
