@@ -595,7 +595,10 @@ fp8moe_status fp8moe_route_weight_grad(const void* dout, const void* y, const in
   if (T == 0) return FP8MOE_OK;
   if (!row_of || !dw || (N > 0 && (!dout || !y))) return FP8MOE_ERR_INVALID_ARG;
   if (!al16(dout) || !al16(y) || (((uintptr_t)row_of | (uintptr_t)dw) & 3)) return FP8MOE_ERR_ALIGNMENT;
-  return cuda_result(fp8moe::launch_route_weight_grad(dout, y, row_of, T, N, k, dw, (cudaStream_t)stream));
+  DevInfo* d;
+  fp8moe_status s = device_info(&d);
+  if (s) return s;
+  return cuda_result(fp8moe::launch_route_weight_grad(dout, y, row_of, T, N, k, dw, d->num_sms, (cudaStream_t)stream));
 }
 
 static fp8moe_status swiglu(bool bwd, const void* dout, const void* h, int64_t ldh, int64_t M, int64_t F,

@@ -107,7 +107,7 @@ struct RouterArgs;
 cudaError_t launch_router_fwd(const RouterArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_router_bwd(const RouterArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_route_weight_grad(const void* dout, const void* y, const int32_t* row_of, int64_t T, int64_t N,
-                                     int64_t k, float* dw, cudaStream_t st);
+                                     int64_t k, float* dw, int num_sms, cudaStream_t st);
 
 // gated activation with MXFP8 output (swiglu.cu); dout == NULL: forward
 struct SwigluArgs;

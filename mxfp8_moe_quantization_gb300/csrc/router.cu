@@ -423,37 +423,40 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_bwd(RouterArgs 
   }
 }
 
-// dw[t, j] = sum over n of dout[t, n] * y[row_of[t, j], n]: WPT warps share a
-// token (each every WPT-th group of 32 chunks), UK rows of y at a time.
-template <int WPT, int UK>
-__global__ void __launch_bounds__(256) k_route_weight_grad(const uint16_t* __restrict__ dout,
-                                                           const uint16_t* __restrict__ y,
-                                                           const int32_t* __restrict__ row_of, int64_t T, int64_t N,
-                                                           int k, float* __restrict__ dw) {
+// dw[t, j] = sum over n of dout[t, n] * y[row_of[t, j], n]: L lanes take a token
+// (several tokens a warp, or several warps a token), a lane every L-th chunk of
+// 16 bytes, of UK rows of y at a time.  The row numbers rather than pointers are
+// kept, so that four CTAs fit an SM (16384 tokens x 6 rows of 2048: 70.5 us against
+// 80.0 with three; what spills is outside the loop's loads).
+template <int L, int UK>
+__global__ void __launch_bounds__(256, 4) k_route_weight_grad(const uint16_t* __restrict__ dout,
+                                                              const uint16_t* __restrict__ y,
+                                                              const int32_t* __restrict__ row_of, int64_t T, int64_t N,
+                                                              int k, float* __restrict__ dw) {
+  constexpr int WPT = L / 32;   // warps per token (0: less than one)
   __shared__ float red[8][UK];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPT;
-  const int64_t t = (int64_t)blockIdx.x * (8 / WPT) + warp / WPT;
+  const int warp = threadIdx.x >> 5, l = threadIdx.x % L;
+  const int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
   const int64_t nv = N / 8;
   for (int j0 = 0; j0 < k; j0 += UK) {
-    const uint16_t* src[UK];
+    int row[UK];
     float acc[UK];
 #pragma unroll
     for (int j = 0; j < UK; ++j) {
-      const int r = t < T && j0 + j < k ? row_of[t * k + j0 + j] : -1;
-      src[j] = r < 0 ? nullptr : y + (int64_t)r * N;
+      row[j] = t < T && j0 + j < k ? row_of[t * k + j0 + j] : -1;
       acc[j] = 0.0f;
     }
     if (t < T) {
-      for (int64_t v = part * 32 + lane; v < nv; v += 32 * WPT) {
+      for (int64_t v = l; v < nv; v += L) {
         const uint4 d = ld_nc16(dout + t * N + v * 8);
         uint4 q[UK];
 #pragma unroll
-        for (int j = 0; j < UK; ++j) q[j] = src[j] ? ld_nc16(src[j] + v * 8) : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < UK; ++j) q[j] = row[j] < 0 ? make_uint4(0, 0, 0, 0) : ld_nc16(y + row[j] * N + v * 8);
         const uint32_t dd[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
         for (int j = 0; j < UK; ++j) {
           const uint32_t qq[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
-          if (!src[j]) continue;
+          if (row[j] < 0) continue;
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             acc[j] = fmaf(bf16_lo(dd[h]), bf16_lo(qq[h]), acc[j]);
@@ -464,11 +467,11 @@ __global__ void __launch_bounds__(256) k_route_weight_grad(const uint16_t* __res
     }
 #pragma unroll
     for (int j = 0; j < UK; ++j) {
-      acc[j] = lane_sum(acc[j]);
-      if (WPT > 1 && lane == 0) red[warp][j] = acc[j];
+      acc[j] = lane_sum<(L < 32 ? L : 32)>(acc[j]);
+      if (WPT > 1 && (threadIdx.x & 31) == 0) red[warp][j] = acc[j];
     }
     if (WPT > 1) __syncthreads();
-    if (t < T && part == 0 && lane == 0) {
+    if (t < T && l == 0) {
 #pragma unroll
       for (int j = 0; j < UK; ++j) {
         float v = acc[j];
@@ -563,30 +566,35 @@ cudaError_t launch_router_bwd(const RouterArgs& a, int num_sms, cudaStream_t st)
 #undef FP8MOE_ROUTER
 
 cudaError_t launch_route_weight_grad(const void* dout, const void* y, const int32_t* row_of, int64_t T, int64_t N,
-                                     int64_t k, float* dw, cudaStream_t st) {
+                                     int64_t k, float* dw, int num_sms, cudaStream_t st) {
   const uint16_t *d = (const uint16_t*)dout, *yp = (const uint16_t*)y;
-  // Warps per token: every warp with 32 chunks of its own, at most eight (4096
-  // tokens x 8 rows of 7168: 79.8 us with eight, 82 with four, 101 with one,
-  // whose few long-lived CTAs leave SMs idle at the end)
+  // Lanes per token. Few enough that a lane has chunks to do and a CTA's tokens
+  // overlap their dependent loads (60000 tokens x 8 rows of 128: 24.6 us with 16,
+  // 39.3 with 32, 109 with 128; of 256: 43.9, 44.3, 111; 49311 x 5 of 528: 57.0,
+  // 58.7, 82.4; 8192 x 1 of 1024: 5.5 with 32, 7.5 with 128); many where rows are
+  // long, as few long-lived CTAs leave SMs idle at the end (30000 x 8 of 1024:
+  // 85.4 with 128, 87.0 with 32; 4096 x 8 of 7168: 79.5 with 256, 80.4 with 128,
+  // 81.4 with 32; 2000 x 2 of 8192: 17.8 with 256, 20.2 with 128), and where the
+  // tokens would not give every SM a CTA (64 x 8 of 7168: 5.5 with 256, 25.1 with 32).
   const int64_t nv = N / 8;
-#define FP8MOE_WG_(WPT, UK)                                                                                  \
-  k_route_weight_grad<WPT, UK>                                                                               \
-      <<<(unsigned)((T + 8 / WPT - 1) / (8 / WPT)), 256, 0, st>>>(d, yp, row_of, T, N, (int)k, dw)
-#define FP8MOE_WG(UK)                   \
-  if (nv >= 256) FP8MOE_WG_(8, UK);     \
-  else if (nv >= 128) FP8MOE_WG_(4, UK); \
-  else if (nv >= 64) FP8MOE_WG_(2, UK);  \
-  else FP8MOE_WG_(1, UK)
-  if (k <= 1) {
-    FP8MOE_WG(1);
-  } else if (k <= 2) {
-    FP8MOE_WG(2);
-  } else if (k <= 4) {
-    FP8MOE_WG(4);
-  } else {
-    FP8MOE_WG(8);
+  int L = nv <= 48 ? 16 : nv < 128 || (k == 1 && nv < 512) ? 32 : nv < 512 ? 128 : 256;
+  while (L < 256 && L < nv && T * L < (int64_t)256 * num_sms) L = L == 32 ? 128 : 2 * L;
+  const unsigned grid = (unsigned)((T + 256 / L - 1) / (256 / L));
+  auto run = [&](auto kern) { kern<<<grid, 256, 0, st>>>(d, yp, row_of, T, N, (int)k, dw); };
+#define FP8MOE_WG(UK)                                     \
+  if (L == 16) run(k_route_weight_grad<16, UK>);          \
+  else if (L == 32) run(k_route_weight_grad<32, UK>);     \
+  else if (L == 128) run(k_route_weight_grad<128, UK>);   \
+  else run(k_route_weight_grad<256, UK>)
+  switch (k) {
+    case 1: FP8MOE_WG(1); break;
+    case 2: FP8MOE_WG(2); break;
+    case 3:
+    case 4: FP8MOE_WG(4); break;
+    case 5:
+    case 6: FP8MOE_WG(6); break;
+    default: FP8MOE_WG(8);
   }
-#undef FP8MOE_WG_
 #undef FP8MOE_WG
   return cudaGetLastError();
 }

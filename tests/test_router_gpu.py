@@ -255,6 +255,28 @@ def test_weight_grad(F, T, N, k):
         assert np.allclose(ref, OM.weight_grad(_np(dout), _np(y), r), rtol=1e-12, atol=1e-9)
 
 
+@pytest.mark.parametrize("T,N,k", [(2503, 8, 3), (5000, 376, 5), (2503, 392, 6), (1301, 968, 7), (1301, 1032, 1),
+                                   (1301, 2048, 2), (310, 4088, 4), (161, 8200, 8), (2435, 248, 13), (77, 640, 6)])
+def test_weight_grad_lane_counts(F, T, N, k):
+    """Sizes on both sides of each choice of lanes per token: many and few
+    tokens, short and long rows; missing rows anywhere, and rows of y that no
+    pair names hold NaN.  The bound is test_weight_grad's."""
+    g = torch.Generator().manual_seed(N)
+    rows = T * k + 9
+    y, dout = torch.randn(rows, N, generator=g).to(torch.bfloat16), torch.randn(T, N, generator=g).to(torch.bfloat16)
+    perm = torch.randperm(rows, generator=g)
+    row_of = perm[:T * k].reshape(T, k).to(torch.int32)
+    y[perm[T * k:]] = float("nan")
+    gone = torch.rand(T, k, generator=g) < 0.2
+    y[row_of[gone].long()] = float("nan")
+    row_of[gone] = -1
+    got = _np(F.fp8moe_route_weight_grad(dout.to(DEV), y.to(DEV), row_of.to(DEV)))
+    r, yn = row_of.numpy(), _np(torch.nan_to_num(y))
+    ref = np.einsum("tn,tkn->tk", _np(dout), yn[np.maximum(r, 0)]) * (r >= 0)
+    size = np.einsum("tn,tkn->tk", np.abs(_np(dout)), np.abs(yn)[np.maximum(r, 0)])
+    assert np.all(np.abs(got - ref) <= (N / 32 + 16) * 2.0 ** -24 * size) and not got[r < 0].any()
+
+
 def test_weight_grad_is_the_difference_of_the_combine(F):
     """<unpermute(y, w + s e) - unpermute(y, w - s e), dout> / 2s, exact in w up
     to the combine's bf16 output: values chosen so that it rounds nothing."""
