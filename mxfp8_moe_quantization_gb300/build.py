@@ -82,10 +82,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"{what} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
 
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+
     def compile_binding():
-        cuda_include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
         run("binding", [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-I", os.path.join(torch_dir, "include"),
-                        "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), "-I", cuda_include,
+                        "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
                         "-I", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "binding.cpp"), "-o", binding_obj])
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
@@ -102,7 +103,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     torch_lib = os.path.join(torch_dir, "lib")
     run("binding link", [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, binding_obj, "-L", HERE, "-l:libfp8moe.so",
                          "-L", torch_lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
-                         "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"])
+                         "-L", os.path.join(cuda, "lib64"), "-lcudart", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"])
     os.replace(tmp, BINDING)
     return LIB
 

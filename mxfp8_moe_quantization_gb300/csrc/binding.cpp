@@ -13,6 +13,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -65,12 +66,10 @@ bool flag(PyObject* o) {
 // The call's device: that of its first argument, which has to be current.
 struct Call {
   int dev;
-  at::TensorOptions on;
   explicit Call(const Tensor& t) {
     if (!t.is_cuda()) refuse();
     dev = t.get_device();
     if (dev != c10::cuda::current_device()) refuse();
-    on = at::TensorOptions().device(t.device());
   }
   fp8moe_stream_t stream() const { return (fp8moe_stream_t)c10::cuda::getCurrentCUDAStream(dev).stream(); }
   Tensor empty(Shape s, at::ScalarType t) const {
@@ -78,6 +77,22 @@ struct Call {
       if (n < 0) refuse();
     // (at::empty without its dispatch)
     return at::detail::empty_cuda(s, t, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt);
+  }
+  // bytes, zeroed on the call's stream (at::zeros: 10.5 us of host time against
+  // 3.3; where padding is written by nobody and has to be valid)
+  Tensor zeros(int64_t n) const {
+    Tensor t = empty({n}, at::kByte);
+    if (n > 0 && cudaMemsetAsync(t.data_ptr(), 0, (size_t)n, (cudaStream_t)stream()) != cudaSuccess) throw Refused{FP8MOE_ERR_CUDA};
+    return t;
+  }
+  // n elements of type ty from byte `at` (a multiple of their size) of the byte
+  // tensor t, whose storage they share: 0.3 us where an allocation takes 0.9
+  static Tensor part(const Tensor& t, int64_t at, int64_t n, at::ScalarType ty) {
+    const caffe2::TypeMeta meta = c10::scalarTypeToTypeMeta(ty);
+    Tensor p = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(), meta);
+    p.unsafeGetTensorImpl()->set_storage_offset(at / (int64_t)meta.itemsize());
+    p.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+    return p;
   }
   bool here(const Tensor& t, at::ScalarType ty, Shape s) const {
     return t.is_cuda() && t.get_device() == dev && t.scalar_type() == ty && t.sizes() == s;
@@ -170,7 +185,7 @@ PyObject* add_rmsnorm_fwd(PyObject* const* a) {
       if (a[13] == Py_None) {
         // room for the tiles of one group, whose layout is the same: the A
         // operand of a one-group grouped GEMM
-        scale = at::zeros({fp8moe_swizzled_scales_bytes(1, T, H / 32, 1, FP8MOE_GROUP_ROWS)}, c.on.dtype(at::kByte));
+        scale = c.zeros(fp8moe_swizzled_scales_bytes(1, T, H / 32, 1, FP8MOE_GROUP_ROWS));
       } else {
         scale = tensor(a[13]);
       }
@@ -230,9 +245,17 @@ PyObject* router_fwd(PyObject* const* a) {
   void* pw = c.out(w, a[9], at::kFloat, {T, k});
   void *pc = nullptr, *pp = nullptr, *pl = nullptr, *pws = nullptr;
   if (flag(a[7])) {
-    pc = c.out(counts, a[10], at::kInt, {E + 1});
-    pp = c.out(psum, a[11], at::kFloat, {E});
-    pl = c.out(loss, a[12], at::kFloat, {1});
+    if (a[10] == Py_None && a[11] == Py_None && a[12] == Py_None) {
+      const Tensor all = c.empty({(2 * E + 2) * 4}, at::kByte);
+      counts = Call::part(all, 0, E + 1, at::kInt);
+      psum = Call::part(all, (E + 1) * 4, E, at::kFloat);
+      loss = Call::part(all, (2 * E + 1) * 4, 1, at::kFloat);
+      pc = counts.data_ptr(), pp = psum.data_ptr(), pl = loss.data_ptr();
+    } else {
+      pc = c.out(counts, a[10], at::kInt, {E + 1});
+      pp = c.out(psum, a[11], at::kFloat, {E});
+      pl = c.out(loss, a[12], at::kFloat, {1});
+    }
     nbytes = fp8moe_router_workspace_bytes(T, E);
     if (nbytes > 0) pws = c.workspace(ws, a[13], nbytes);
   }
@@ -285,7 +308,7 @@ void mx_out(const Call& c, Tensor& q, PyObject* gq, Tensor& s, PyObject* gs, int
   if (need < 0) refuse();
   pq = c.out(q, gq, at::kByte, {R, C});
   if (gs == Py_None) {
-    s = plain ? c.empty({R, C / 32}, at::kByte) : at::zeros({need}, c.on.dtype(at::kByte));
+    s = plain ? c.empty({R, C / 32}, at::kByte) : c.zeros(need);
   } else {
     s = tensor(gs);
     if (s.numel() < need) refuse();
