@@ -522,6 +522,11 @@ int64_t fp8moe_router_workspace_bytes(int64_t T, int64_t E) {
   return (T < fp8moe::ROUTER_MAX_PARTS ? T : fp8moe::ROUTER_MAX_PARTS) * (2 * E + 1) * (int64_t)sizeof(float);
 }
 
+// rows of logits that accesses of four experts reach
+static bool router_wide(const void* p, int type, int64_t E, int64_t ld) {
+  return E % 4 == 0 && ld % 4 == 0 && (uintptr_t)p % (type == FP8MOE_BF16 ? 8 : 16) == 0;
+}
+
 // the checks that both directions share
 static fp8moe_status router_check(const void* logits, int logits_type, int64_t T, int64_t E, int64_t ldl, int64_t k,
                                   int score) {
@@ -556,6 +561,7 @@ fp8moe_status fp8moe_router_fwd(const void* logits, int logits_type, int64_t T, 
   fp8moe::RouterArgs a{};
   a.logits = logits;
   a.bf16 = logits_type == FP8MOE_BF16;
+  a.wide = router_wide(logits, logits_type, E, ldl);
   a.T = T, a.ld = ldl, a.E = (int)E, a.k = (int)k;
   a.score = score, a.renorm = renormalize != 0, a.route_scale = route_scale;
   a.bias = bias, a.mask = token_mask;
@@ -581,6 +587,7 @@ fp8moe_status fp8moe_router_bwd(const void* logits, int logits_type, int64_t T, 
   fp8moe::RouterArgs a{};
   a.logits = logits;
   a.bf16 = logits_type == FP8MOE_BF16;
+  a.wide = router_wide(logits, logits_type, E, ldl) && router_wide(dlogits, logits_type, E, E);
   a.T = T, a.ld = ldl, a.E = (int)E, a.k = (int)k;
   a.score = score, a.renorm = renormalize != 0, a.route_scale = route_scale;
   a.mask = token_mask;

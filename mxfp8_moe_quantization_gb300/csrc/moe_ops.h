@@ -8,6 +8,7 @@ namespace fp8moe {
 struct RouterArgs {
   const void* logits;   // [T, E], row stride ld; fp32 or bf16
   int bf16;
+  int wide;             // E a multiple of 4, rows of logits and dlogits aligned to four elements
   int64_t T, ld;
   int E, k;
   int score;            // FP8MOE_SCORE_*

@@ -15,19 +15,21 @@
 //   u_j = scale * s_j dw_j,
 //   softmax: dl = r + u - p sum(u);   sigmoid: dl = (1 - s)(r + u).
 //
-// A warp takes a token, a lane every 32nd expert (eight or sixteen lanes where
-// experts are few and tokens many); the logits are read once.
+// A warp takes a token, or several where experts are few and tokens many; a lane
+// has pieces of four neighbouring experts.  The logits are read once.
 // Sums over tokens have a fixed order (registers, then warps, then CTAs), so
 // results do not change from run to run.  The CTAs' partial sums are joined by
 // a second kernel of one cluster, launched ahead of the first one's end.
 //
-// Bound by latency, then by instruction issue (a token of 256 experts, top 8:
-// about 1100 warp instructions, half of them the rounds of the choice).  In a
-// graph: 4096 x 256, top 8, 10.4 us forward with the sums and 6.0 without, 4.6
-// backward; 8192 x 64, top 6, 8.4 and 4.2; 3 tokens 3.9.  The first form, which
-// carried scores through the rounds and joined 512 partial sums in one CTA,
-// took 29.9 us on the first.
+// Bound by latency, then by instruction issue (a token of 256 fp32 experts, top
+// 8: about 1100 warp instructions, half of them the rounds of the choice; bf16
+// logits without a bias need one maximum a round instead of two reductions:
+// 65536 x 128, top 8, 31.4 us against 39.4).  In a graph: 4096 x 256, top 8,
+// 10.1 us forward with the sums and 5.8 without, 4.5 backward; 8192 x 64, top 6,
+// 7.4 and 3.4; 3 tokens 3.9.  The first form, which carried scores through the
+// rounds and joined 512 partial sums in one CTA, took 29.9 us on the first.
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "launch.h"
 #include "moe_ops.h"
 
@@ -82,24 +84,61 @@ FP8MOE_DEV uint32_t lane_umin(uint32_t v) {
 
 constexpr float NEG_INF = -__builtin_huge_valf();
 
-// the logits of token t at this lane's experts i G + l; -inf past the last one
-// and everywhere in a row that is no token
+FP8MOE_DEV float logit_at(const RouterArgs& a, int64_t t, int e) {
+  return a.bf16 ? __uint_as_float((uint32_t)((const uint16_t*)a.logits)[t * a.ld + e] << 16)
+                : ((const float*)a.logits)[t * a.ld + e];
+}
+
+// A lane's V experts are pieces of up to four neighbours, the lanes' pieces
+// side by side: wide accesses to memory, and to shared memory without a bank
+// met twice.
+template <int V>
+constexpr int piece() { return V < 4 ? V : 4; }
+template <int V, int G>
+FP8MOE_DEV int expert(int l, int i) {
+  constexpr int P = piece<V>();
+  return (i / P * G + l) * P + i % P;
+}
+
+// the logits of token t at this lane's experts; -inf past the last one and
+// everywhere in a row that is no token
 template <int V, int G>
 FP8MOE_DEV void load_row(const RouterArgs& a, int64_t t, int l, bool on, float (&x)[V]) {
-  if (a.bf16) {
-    const uint16_t* p = (const uint16_t*)a.logits + t * a.ld;
+  constexpr int P = piece<V>();
+  if (P > 1 && a.wide) {   // E is a multiple of a piece
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = i * G + l;
-      x[i] = on && e < a.E ? __uint_as_float((uint32_t)p[e] << 16) : NEG_INF;
+    for (int p = 0; p < V; p += P) {
+      const int e = expert<V, G>(l, p);
+      const bool here = on && e < a.E;
+      if (a.bf16) {
+        const uint16_t* at = (const uint16_t*)a.logits + t * a.ld + e;
+        constexpr uint32_t NONE = 0xFF80FF80u;   // -inf, -inf
+        uint2 v = make_uint2(NONE, NONE);
+        if (here) {
+          if constexpr (P == 4) v = *reinterpret_cast<const uint2*>(at);
+          if constexpr (P == 2) v.x = *reinterpret_cast<const uint32_t*>(at);
+        }
+        x[p] = bf16_lo(v.x);
+        if constexpr (P >= 2) x[p + 1] = bf16_hi(v.x);
+        if constexpr (P == 4) x[p + 2] = bf16_lo(v.y), x[p + 3] = bf16_hi(v.y);
+      } else {
+        const float* at = (const float*)a.logits + t * a.ld + e;
+        float4 v = make_float4(NEG_INF, NEG_INF, NEG_INF, NEG_INF);
+        if (here) {
+          if constexpr (P == 4) v = *reinterpret_cast<const float4*>(at);
+          if constexpr (P == 2) v.x = at[0], v.y = at[1];
+        }
+        x[p] = v.x;
+        if constexpr (P >= 2) x[p + 1] = v.y;
+        if constexpr (P == 4) x[p + 2] = v.z, x[p + 3] = v.w;
+      }
     }
-  } else {
-    const float* p = (const float*)a.logits + t * a.ld;
+    return;
+  }
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = i * G + l;
-      x[i] = on && e < a.E ? p[e] : NEG_INF;
-    }
+  for (int i = 0; i < V; ++i) {
+    const int e = expert<V, G>(l, i);
+    x[i] = on && e < a.E ? logit_at(a, t, e) : NEG_INF;
   }
 }
 
@@ -145,11 +184,6 @@ FP8MOE_DEV RowStat row_scores(const float (&x)[V], float (&s)[V]) {
   return st;
 }
 
-FP8MOE_DEV float logit_at(const RouterArgs& a, int64_t t, int e) {
-  return a.bf16 ? __uint_as_float((uint32_t)((const uint16_t*)a.logits)[t * a.ld + e] << 16)
-                : ((const float*)a.logits)[t * a.ld + e];
-}
-
 // loss from counts and probability sums; every thread of the CTA calls it.
 // part: this CTA's share of sum n_e P_e (thread 0 has the result)
 FP8MOE_DEV float cta_sum(float v, float* red) {
@@ -165,15 +199,52 @@ FP8MOE_DEV float loss_of(float np, int tokens, int E, int k) {
   return np * __fdiv_rn((float)E, (float)k) / (N * N);
 }
 
-// G lanes take a token, a lane every G-th expert; a warp 32 / G tokens at a time.
+// Slots of a token's choice that a lane looks after: its k <= G * slots<G>().
+template <int G>
+constexpr int slots() { return G >= 8 ? 1 : 8 / G; }
+
+// k rounds: the token's largest key, then the lowest id that has it (PACK: the
+// key's lower half says which).  Lane l ends with slots l, l + G, ..
+template <int V, int G, bool PACK>
+FP8MOE_DEV void choose(uint32_t (&key)[V], int (&my_e)[slots<G>()], int k, int l) {
+#pragma unroll
+  for (int q = 0; q < slots<G>(); ++q) {
+    my_e[q] = 0;
+    for (int j = q * G; j < k && j < (q + 1) * G; ++j) {
+      uint32_t bk = key[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) bk = max(bk, key[i]);
+      const uint32_t top = lane_umax<G>(bk);
+      if constexpr (PACK) {
+        if (l == j % G) my_e[q] = (int)(0xFFFFu - (top & 0xFFFFu));
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (key[i] == top) key[i] = 0u;
+      } else {
+        uint32_t be = 0xffffffffu;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+          if (key[i] == top) be = (uint32_t)expert<V, G>(l, i);
+        const uint32_t e = lane_umin<G>(be);
+        if (l == j % G) my_e[q] = (int)e;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (e == (uint32_t)expert<V, G>(l, i)) key[i] = 0u;
+      }
+    }
+  }
+}
+
+// G lanes take a token, a lane V experts; a warp 32 / G tokens at a time.
 template <int V, int G, bool SIG>
 __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_fwd(RouterArgs a) {
+  constexpr int S = slots<G>();
   constexpr int TPW = 32 / G;
-  extern __shared__ float rsm[];
+  extern __shared__ __align__(16) float rsm[];
   __shared__ float red[32];
   const int RW = blockDim.x >> 5;
-  float* cp = rsm;                      // [RW][E]
-  int* cn = (int*)(rsm + RW * a.E);     // [E + 1]
+  float* cp = rsm;                      // [RW][G V]
+  int* cn = (int*)(rsm + RW * G * V);   // [E + 1]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % G;
   const bool sums = a.counts != nullptr;
   // the joining kernel may take its place; it waits for this one's end
@@ -186,7 +257,7 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_fwd(RouterArgs 
   }
   float bias[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) bias[i] = a.bias && i * G + l < a.E ? a.bias[i * G + l] : 0.0f;
+  for (int i = 0; i < V; ++i) bias[i] = a.bias && expert<V, G>(l, i) < a.E ? a.bias[expert<V, G>(l, i)] : 0.0f;
   for (int64_t tw = ((int64_t)blockIdx.x * RW + warp) * TPW; tw < a.T; tw += (int64_t)gridDim.x * RW * TPW) {
     const int64_t t = tw + lane / G;   // past T: no token, nothing stored
     const bool row = t < a.T, on = row && (!a.mask || a.mask[t] != 0);
@@ -200,40 +271,42 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_fwd(RouterArgs 
       acc[i] += p;
       // dead experts stay below every other whatever their bias
       const float f = !a.bias ? x[i] : x[i] == NEG_INF ? NEG_INF : (SIG ? s[i] : p) + bias[i];
-      key[i] = i * G + l < a.E ? order_key(f) : 0u;
+      key[i] = expert<V, G>(l, i) < a.E ? order_key(f) : 0u;
     }
     tokens += on;
-    // k rounds: the token's largest key, then the lowest id that has it
-    int my_e = 0;
-    for (int j = 0; j < a.k; ++j) {
-      uint32_t bk = key[0];
-#pragma unroll
-      for (int i = 1; i < V; ++i) bk = max(bk, key[i]);
-      const uint32_t top = lane_umax<G>(bk);
-      uint32_t be = 0xffffffffu;
-#pragma unroll
-      for (int i = V - 1; i >= 0; --i)
-        if (key[i] == top) be = (uint32_t)(i * G + l);
-      const uint32_t e = lane_umin<G>(be);
-      if (l == j) my_e = (int)e;
+    int my_e[S];
+    if (a.bf16 && !a.bias) {
+      // a bf16 logit leaves the key's lower half to the expert: the lowest id
+      // has the largest key, and one maximum a round is enough
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (e == (uint32_t)(i * G + l)) key[i] = 0u;
+        if (key[i] != 0u) key[i] = (key[i] & 0xFFFF0000u) | (uint32_t)(0xFFFF - expert<V, G>(l, i));
+      choose<V, G, true>(key, my_e, a.k, l);
+    } else {
+      choose<V, G, false>(key, my_e, a.k, l);
     }
-    // lane j: slot j's weight, from its logit
-    float w = 0.0f;
-    if (l < a.k && row) {
-      const float xe = on ? logit_at(a, t, my_e) : NEG_INF;
-      w = score_of<SIG>(xe, st);
-      if (sums && xe != NEG_INF) atomicAdd(&cn[my_e], 1);
+    // lane l: the weights of slots l, l + G, .. from their logits
+    float w[S], z = 0.0f;
+#pragma unroll
+    for (int q = 0; q < S; ++q) {
+      w[q] = 0.0f;
+      if (q * G + l < a.k && row) {
+        const float xe = on ? logit_at(a, t, my_e[q]) : NEG_INF;
+        w[q] = score_of<SIG>(xe, st);
+        if (sums && xe != NEG_INF) atomicAdd(&cn[my_e[q]], 1);
+      }
+      z += w[q];
     }
     if (a.renorm) {
-      const float z = lane_sum<G>(w);
-      w = __fdiv_rn(w, z == 0.0f ? 1.0f : z);
+      z = lane_sum<G>(z);
+      z = z == 0.0f ? 1.0f : z;
     }
-    if (l < a.k && row) {
-      a.idx[t * a.k + l] = my_e;
-      a.w[t * a.k + l] = w * a.route_scale;
+#pragma unroll
+    for (int q = 0; q < S; ++q) {
+      if (q * G + l < a.k && row) {
+        a.idx[t * a.k + q * G + l] = my_e[q];
+        a.w[t * a.k + q * G + l] = (a.renorm ? __fdiv_rn(w[q], z) : w[q]) * a.route_scale;
+      }
     }
   }
   if (!sums) return;
@@ -242,9 +315,10 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_fwd(RouterArgs 
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int o = G; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+  if (lane < G) {
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (lane < G && i * G + l < a.E) cp[warp * a.E + i * G + l] = acc[i];
+    for (int i = 0; i < V; ++i) cp[warp * G * V + expert<V, G>(l, i)] = acc[i];
+  }
   if (l == 0) atomicAdd(&cn[a.E], tokens);
   __syncthreads();
   const bool single = gridDim.x == 1;
@@ -255,9 +329,10 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_fwd(RouterArgs 
     const int n = cn[e];
     pn[e] = n;
     if (e < a.E) {
-      float v = cp[e];
+      const float* c = cp + e;
+      float v = c[0];
 #pragma unroll 4
-      for (int i = 1; i < RW; ++i) v += cp[i * a.E + e];
+      for (int i = 1; i < RW; ++i) v += c[i * G * V];
       pp[e] = v;
       np = fmaf((float)n, v, np);
     }
@@ -355,69 +430,124 @@ __global__ void __cluster_dims__(JOIN, 1, 1) __launch_bounds__(JOIN_WARPS * 32) 
 
 template <int V, int G, bool SIG>
 __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_bwd(RouterArgs a) {
-  constexpr int TPW = 32 / G;
-  extern __shared__ float rsm[];
+  constexpr int TPW = 32 / G, S = slots<G>(), P = piece<V>();
+  extern __shared__ __align__(16) float rsm[];
   const int RW = blockDim.x >> 5;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % G;
-  float* ubuf = rsm + (warp * TPW + lane / G) * a.E;   // the chosen experts' u
+  float* ubuf = rsm + (warp * TPW + lane / G) * G * V;   // the chosen experts' u
   float c[V];
   float coef = 0.0f;
   if (a.dloss) coef = a.dloss[0] * loss_of(1.0f, a.counts_in[a.E], a.E, a.k);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = i * G + l;
+    const int e = expert<V, G>(l, i);
     c[i] = a.dloss && e < a.E ? coef * (float)a.counts_in[e] : 0.0f;
-    if (e < a.E) ubuf[e] = 0.0f;
+    ubuf[e] = 0.0f;
   }
   __syncwarp();
   for (int64_t tw = ((int64_t)blockIdx.x * RW + warp) * TPW; tw < a.T; tw += (int64_t)gridDim.x * RW * TPW) {
     const int64_t t = tw + lane / G;   // past T: no token, nothing stored
     const bool row = t < a.T, on = row && (!a.mask || a.mask[t] != 0);
-    int e = -1;
-    float dwj = 0.0f, xj = 0.0f;
-    if (a.dw && l < a.k && on) {
-      e = a.idx_in[t * a.k + l];
-      if (e < 0 || e >= a.E) e = -1;
-      dwj = a.dw[t * a.k + l];
+    // lane l: the token's slots l, l + G, ..
+    int e[S];
+    float dwj[S], xj[S];
+#pragma unroll
+    for (int q = 0; q < S; ++q) {
+      const int j = q * G + l;
+      e[q] = -1;
+      dwj[q] = xj[q] = 0.0f;
+      if (a.dw && j < a.k && on) {
+        e[q] = a.idx_in[t * a.k + j];
+        if (e[q] < 0 || e[q] >= a.E) e[q] = -1;
+        dwj[q] = a.dw[t * a.k + j];
+      }
     }
     float x[V], s[V];
     load_row<V, G>(a, t, l, on, x);
-    if (e >= 0) xj = logit_at(a, t, e);
+#pragma unroll
+    for (int q = 0; q < S; ++q)
+      if (e[q] >= 0) xj[q] = logit_at(a, t, e[q]);
     const RowStat st = row_scores<V, G, SIG, true>(x, s);
     float pc = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) pc = fmaf(s[i] * st.rz, c[i], pc);
-    // lane j: slot j's score, from the logit itself
-    const float sj = e >= 0 ? score_of<SIG, true>(xj, st) : 0.0f;
-    float u = sj * dwj, us = 0.0f;
     pc = lane_sum<G>(pc);
+    float us = 0.0f;
     if (a.dw) {
-      if (a.renorm) {
-        const float z = lane_sum<G>(sj);
-        const float wj = __fdiv_rn(sj, z == 0.0f ? 1.0f : z);
-        u = wj * (dwj - lane_sum<G>(dwj * wj));
-      }
-      u *= a.route_scale;
-      if constexpr (!SIG) us = lane_sum<G>(u);
-      if (e >= 0) atomicAdd(&ubuf[e], u);
-      __syncwarp();
-    }
+      // the slots' scores, from the logits themselves
+      float u[S], z = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int ei = i * G + l;
-      if (ei >= a.E || !row) continue;
-      const float p = s[i] * st.rz;
-      float o = p * (c[i] - pc - us) + ubuf[ei];
-      if (SIG) o *= 1.0f - s[i];
-      if (a.bf16) {
-        ((__nv_bfloat16*)a.dlogits)[t * a.E + ei] = __float2bfloat16_rn(o);
-      } else {
-        ((float*)a.dlogits)[t * a.E + ei] = o;
+      for (int q = 0; q < S; ++q) {
+        const float sj = e[q] >= 0 ? score_of<SIG, true>(xj[q], st) : 0.0f;
+        z += sj;
+        u[q] = sj * (a.renorm ? 1.0f : dwj[q]);
+      }
+      if (a.renorm) {
+        z = lane_sum<G>(z);
+        float d = 0.0f;
+#pragma unroll
+        for (int q = 0; q < S; ++q) {
+          u[q] = __fdiv_rn(u[q], z == 0.0f ? 1.0f : z);
+          d += dwj[q] * u[q];
+        }
+        d = lane_sum<G>(d);
+#pragma unroll
+        for (int q = 0; q < S; ++q) u[q] *= dwj[q] - d;
+      }
+#pragma unroll
+      for (int q = 0; q < S; ++q) us += u[q] *= a.route_scale;
+      if constexpr (!SIG) us = lane_sum<G>(us);
+#pragma unroll
+      for (int q = 0; q < S; ++q)
+        if (e[q] >= 0) atomicAdd(&ubuf[e[q]], u[q]);
+      __syncwarp();
+    }
+    if (row) {
+#pragma unroll
+      for (int p = 0; p < V; p += P) {
+        const int e0 = expert<V, G>(l, p);
+        float o[P];
+        if constexpr (P == 4) {
+          const float4 b = *reinterpret_cast<const float4*>(ubuf + e0);
+          o[0] = b.x, o[1] = b.y, o[2] = b.z, o[3] = b.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < P; ++i) o[i] = ubuf[e0 + i];
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          o[i] += s[p + i] * st.rz * (c[p + i] - pc - (SIG ? 0.0f : us));
+          if (SIG) o[i] *= 1.0f - s[p + i];
+        }
+        if (P > 1 && a.wide) {
+          if (e0 >= a.E) break;
+          if (a.bf16) {
+            uint16_t* at = (uint16_t*)a.dlogits + t * a.E + e0;
+            if constexpr (P == 4) *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(pk(o[0], o[1])), pack_bf16x2(pk(o[2], o[3])));
+            if constexpr (P == 2) *reinterpret_cast<uint32_t*>(at) = pack_bf16x2(pk(o[0], o[1]));
+          } else {
+            float* at = (float*)a.dlogits + t * a.E + e0;
+            if constexpr (P == 4) *reinterpret_cast<float4*>(at) = make_float4(o[0], o[1], o[2], o[3]);
+            if constexpr (P == 2) at[0] = o[0], at[1] = o[1];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            if (e0 + i >= a.E) break;
+            if (a.bf16) {
+              ((__nv_bfloat16*)a.dlogits)[t * a.E + e0 + i] = __float2bfloat16_rn(o[i]);
+            } else {
+              ((float*)a.dlogits)[t * a.E + e0 + i] = o[i];
+            }
+          }
+        }
       }
     }
     if (a.dw) {
       __syncwarp();
-      if (e >= 0) ubuf[e] = 0.0f;
+#pragma unroll
+      for (int q = 0; q < S; ++q)
+        if (e[q] >= 0) ubuf[e[q]] = 0.0f;
       __syncwarp();
     }
   }
@@ -498,7 +628,7 @@ cudaError_t run_fwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
   const bool sums = a.counts != nullptr;
   const bool single = sums && a.T <= SINGLE_CTA_T;
   const int RW = cta_warps<V, G>(a.T, single ? 1 : num_sms), rows = RW * (32 / G);
-  const int smem = sums ? (RW * a.E + a.E + 1) * 4 : 0;   // probability sums per warp, counts
+  const int smem = sums ? (RW * G * V + a.E + 1) * 4 : 0;   // probability sums per warp, counts
   int64_t blocks = single ? 1 : (a.T + rows - 1) / rows;
   const int64_t most = (int64_t)num_sms * (32 / most_warps<V>());
   if (blocks > most) blocks = most;
@@ -520,7 +650,7 @@ cudaError_t run_fwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
 template <int V, int G, bool SIG>
 cudaError_t run_bwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
   const int RW = cta_warps<V, G>(a.T, num_sms), rows = RW * (32 / G);
-  const int smem = rows * a.E * 4;
+  const int smem = rows * G * V * 4;
   int64_t blocks = (a.T + rows - 1) / rows;
   const int64_t most = (int64_t)num_sms * (64 / most_warps<V>());
   if (blocks > most) blocks = most;
@@ -528,14 +658,18 @@ cudaError_t run_bwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Lanes per token: a whole warp, or for many tokens over few experts eight or
-// sixteen lanes of up to eight experts each, which share the steps that do not
-// depend on the experts (65536 x 64, top 6: 22 us forward with eight against 33;
-// 65536 x 128, top 8: 40 with sixteen against 45).  Below eight (32) tokens an
-// SM a warp's shorter way counts for more: no difference at 2048 x 64, 8.3 us
-// against 8.8 at 4096 x 128.  The choice needs k <= lanes.
+// Lanes per token: a whole warp, or for many tokens over few experts a lane to
+// every eight of them, so that the steps that do not depend on the experts are
+// shared by more tokens (65536 tokens forward: 8 experts, top 2, 7.4 us with one
+// lane against 22.8 with 32; 16, top 4, 9.5 against 27.2; 64, top 6, 18.3
+// against 27.9; 65536 x 128, top 8, 40 against 45 before both got faster).
+// Below eight (32) tokens an SM a warp's shorter way counts for as much or more
+// (2048 x 64, top 6: 6.3 us either way; 4096 x 128: 8.3 with 32, 8.8 with 16).
+// The backward starts at two lanes: one lane's eight slots took 4.3 us on 4096 x
+// 8 against 3.5.  The choice needs k <= lanes x slots.
 int lanes_per_token(const RouterArgs& a, int num_sms) {
-  if (a.E <= 64 && a.k <= 8 && a.T >= 8 * (int64_t)num_sms) return 8;
+  if (a.E <= 64 && a.k <= 8 && a.T >= 8 * (int64_t)num_sms)
+    return a.E <= 8 && !a.dlogits ? 1 : a.E <= 16 ? 2 : a.E <= 32 ? 4 : 8;
   if (a.E > 64 && a.E <= 128 && a.k <= 16 && a.T >= 32 * (int64_t)num_sms) return 16;
   return 32;
 }
@@ -546,14 +680,14 @@ int lanes_per_token(const RouterArgs& a, int num_sms) {
   if (g == G && a.E <= G * V)                                                                                 \
     return a.score == FP8MOE_SCORE_SIGMOID ? FN<V, G, true>(a, num_sms, st) : FN<V, G, false>(a, num_sms, st);
 #define FP8MOE_ROUTER_ALL(FN)                                                                                 \
-  FP8MOE_ROUTER(1, 8, FN) FP8MOE_ROUTER(2, 8, FN) FP8MOE_ROUTER(4, 8, FN) FP8MOE_ROUTER(8, 8, FN)             \
-  FP8MOE_ROUTER(8, 16, FN)                                                                                    \
+  FP8MOE_ROUTER(8, 2, FN) FP8MOE_ROUTER(8, 4, FN) FP8MOE_ROUTER(8, 8, FN) FP8MOE_ROUTER(8, 16, FN)            \
   FP8MOE_ROUTER(1, 32, FN) FP8MOE_ROUTER(2, 32, FN) FP8MOE_ROUTER(4, 32, FN) FP8MOE_ROUTER(8, 32, FN)         \
   FP8MOE_ROUTER(16, 32, FN) FP8MOE_ROUTER(32, 32, FN)
 
 // T == 0: one CTA writes the empty sums
 cudaError_t launch_router_fwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
   const int g = lanes_per_token(a, num_sms);
+  FP8MOE_ROUTER(8, 1, run_fwd)
   FP8MOE_ROUTER_ALL(run_fwd)
   return cudaErrorInvalidValue;
 }

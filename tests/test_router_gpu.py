@@ -149,6 +149,50 @@ def test_ties_and_signed_zero(F):
         assert idx[0].tolist() == [0, 1, 2, 3] and idx[2].tolist() == [5, 70, 0, 1]
 
 
+@pytest.mark.parametrize("E,k", [(4, 3), (15, 5), (20, 8), (60, 6), (96, 8), (256, 8), (384, 12), (1024, 8)])
+@pytest.mark.parametrize("T", [37, 1301])
+def test_bf16_ties(F, T, E, k):
+    """Rows of few different values, signed zeros and NaN: the lowest ids of
+    equal logits win, in any layout of lanes."""
+    g = torch.Generator().manual_seed(E)
+    x = (torch.randint(-3, 4, (T, E), generator=g) * 0.25).to(torch.bfloat16)
+    x[1] = -0.0
+    x[2, ::2] = -float("inf")
+    x[3] = torch.finfo(torch.bfloat16).min
+    _check(F, x, k, "softmax", True, 2.5)
+    x[5, 1] = float("nan")
+    x[6] = float("nan")
+    idx = F.fp8moe_router_fwd(x.to(DEV), k, score=F.SCORE_SIGMOID)[0].cpu()
+    live = _np(x).copy()
+    live[np.isnan(live)] = -np.inf
+    assert np.array_equal(idx.numpy(), OM.choose(live, k))
+
+
+@pytest.mark.parametrize("E", [4, 8, 12, 28, 64, 100, 128, 256, 384, 1024])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_row_strides_and_offsets(F, E, bf16):
+    """Rows that start anywhere give the bits of aligned rows, forward and
+    backward."""
+    k, score = min(E, 6), F.SCORE_SOFTMAX
+    for T in (41, 1303):
+        x = _logits(T, E, E, bf16).to(DEV)
+        mask = torch.ones(T, dtype=torch.uint8, device=DEV)
+        mask[3::5] = 0
+        base = F.fp8moe_router_fwd(x, k, score=score, token_mask=mask)
+        dw, dl = torch.randn(T, k, device=DEV), torch.full((1,), 0.5, device=DEV)
+        grad = F.fp8moe_router_bwd(x, base[0], base[2], dw, dl, score=score, token_mask=mask)
+        for ld, at in ((E + 1, 0), (E + 4, 2), (E + 4, 4), (E + 2, 1), (E + 8, 8)):
+            buf = torch.full((T * ld + at,), float("nan"), dtype=x.dtype, device=DEV)
+            v = buf[at:].view(T, ld)[:, :E]
+            v.copy_(x)
+            for a, b in zip(F.fp8moe_router_fwd(v, k, score=score, token_mask=mask), base):
+                assert torch.equal(a, b)
+            assert torch.equal(F.fp8moe_router_bwd(v, base[0], base[2], dw, dl, score=score, token_mask=mask), grad)
+            out = torch.empty(T * E + 1, dtype=x.dtype, device=DEV)[1:].view(T, E)
+            F.fp8moe_router_bwd(v, base[0], base[2], dw, dl, score=score, token_mask=mask, dlogits=out)
+            assert torch.equal(out, grad)
+
+
 def test_nan_logits_keep_the_ids_valid(F):
     x = _logits(64, 64, 1, False)
     x[7, 3] = x[7, 9] = float("nan")
