@@ -17,8 +17,8 @@
 // from the lane's registers, so the transposed codes need no byte transposes.
 //
 // Bound by HBM: 6.06 bytes per element forward, 10.1 backward.  Measured: 36448
-// x 2048 in 256 groups forward, both directions, 74 us = 6.1 TB/s (91% of a
-// copy's rate); 51136 x 1408 backward 120 us = 6.1 TB/s (91%).  The first form,
+// x 2048 in 256 groups forward, both directions, 71 us = 6.4 TB/s (95% of a
+// copy's rate); 51136 x 1408 backward 118 us = 6.2 TB/s (92%).  The first form,
 // with every lane deriving every scale, expf and a division, and 45
 // instructions per element instead of about 20, took 152 and 283 us.
 #include "common.cuh"
@@ -33,7 +33,8 @@ namespace fp8moe {
 namespace {
 
 // A warp's tile, and a CTA's: 2 x 2 warps, 64 rows x 128 columns.  (4 x 1 warps
-// read 128 bytes of a row at a time and took 2% longer; 1 x 2 the same.)
+// read 128 bytes of a row at a time: 2 to 4% longer, 16 to 0% shorter only where
+// half of the last tile of few is empty; 1 x 2 the same as 2 x 2.)
 constexpr int SG_ROWS = 32, SG_COLS = 64, SG_RW = 2, SG_CW = 2, SG_WARPS = SG_RW * SG_CW;
 constexpr int CW = 8;   // columns per lane
 
@@ -389,6 +390,27 @@ __global__ void __launch_bounds__(SG_WARPS * 32)
   swiglu_body<BWD, false>(nullptr, nullptr, a, cp0, cp1, col_tiles, tiles, 1);
 }
 
+// Tiles per CTA, of which an SM holds occ at a time.  With many a CTA takes
+// two: one exposes its first load and group lookup, longer runs wait for the
+// slowest (51136 x 1408 backward: 123.5 us with one, 115.8 two, 117.3 three, 120
+// four, 126.6 six).  With few it is the last round of CTAs that counts, where an
+// SM may have one CTA left: what leaves the shortest sum over the rounds, a
+// tile taking as long as k CTAs on an SM share it but at least 2.1 of that
+// (46720 x 192 backward, 1460 tiles: 21.1 us with two, 27.5 with three; 4096 x 4096
+// backward, 2048 tiles: 35.3 and, with five, 32.2; 38176 x 288 forward, 1791
+// tiles: 12.2 with three, 16.0 with two).
+int64_t tiles_per_cta(int64_t tiles, int64_t num_sms, int64_t occ) {
+  const int64_t fit = num_sms * occ;
+  if (tiles > 6 * fit) return 2;
+  int64_t best = 1, least = INT64_MAX;
+  for (int64_t per = 1; per <= 5; ++per) {
+    const int64_t n = (tiles + per - 1) / per, rest = n % fit, k = (rest + num_sms - 1) / num_sms;
+    const int64_t cost = n / fit * (per * 10 * occ + 5) + (rest ? per * (k > 2 ? 10 * k : 21) + 5 : 0);
+    if (cost < least) least = cost, best = per;
+  }
+  return best;
+}
+
 template <bool BWD>
 cudaError_t launch_dir(SwigluArgs a, cudaStream_t st) {
   const int64_t W = BWD ? 2 * a.F : a.F;
@@ -408,7 +430,7 @@ cudaError_t launch_dir(SwigluArgs a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(k_swiglu_run<BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, cta_bytes<BWD>());
   if (e != cudaSuccess) return e;
   static std::atomic<int> occ{0};
-  const int64_t fit = (int64_t)a.num_sms * blocks_per_sm(occ, k_swiglu_run<BWD>, SG_WARPS * 32, cta_bytes<BWD>(), 1);
+  const int64_t per_sm = blocks_per_sm(occ, k_swiglu_run<BWD>, SG_WARPS * 32, cta_bytes<BWD>(), 1);
   a.stall = take_ring_stall_hook();
   cuuint64_t dims[2] = {(cuuint64_t)(2 * a.F), (cuuint64_t)a.M}, strides[1] = {(cuuint64_t)(a.ldh * 2)};
   const cuuint32_t box[2] = {SG_COLS, SG_ROWS};
@@ -420,11 +442,7 @@ cudaError_t launch_dir(SwigluArgs a, cudaStream_t st) {
     if (!make_tmap(&td, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.dout, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
       return cudaErrorInvalidValue;
   }
-  // Tiles per CTA: three where that still leaves every SM its fill of CTAs.
-  // One CTA per tile exposes its first load and group lookup (forward 36448 x
-  // 2048: 99 us against 76), one run of tiles per resident CTA waits for the
-  // slowest (51136 x 1408 backward: 150 us against 125).
-  const int64_t per = tiles >= 3 * fit ? 3 : tiles >= 2 * fit ? 2 : 1;
+  const int64_t per = tiles_per_cta(tiles, a.num_sms, per_sm);
   k_swiglu_run<BWD><<<(unsigned)((tiles + per - 1) / per), SG_WARPS * 32, cta_bytes<BWD>(), st>>>(
       th, td, a, cp0, cp1, (int)col_tiles, (int)tiles, (int)per);
   return cudaGetLastError();
