@@ -157,6 +157,13 @@ def test_backward(F, T, H, stream, w32):
     _near(_np(dw), rdw, GREL * np.abs(_np(dy) * xh).sum(0), "dw")
 
 
+@pytest.mark.parametrize("T,H", [(77, 264), (201, 904), (1303, 1568), (31, 2048), (613, 448)])
+@pytest.mark.parametrize("stream,w32", [(True, True), (True, False), (False, True), (False, False)])
+def test_backward_short_rows(F, T, H, stream, w32):
+    """Rows of a few warps, several to a CTA, in every form of the inputs."""
+    test_backward(F, T, H, stream, w32)
+
+
 def test_backward_in_place_and_same_bits(F):
     """dx may be dy or dh; two calls give the same bits; a dirty workspace does not matter."""
     T, H = 3000, 1024
