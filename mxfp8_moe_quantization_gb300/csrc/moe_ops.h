@@ -12,6 +12,7 @@ struct RouterArgs {
   int64_t T, ld;
   int E, k;
   int score;            // FP8MOE_SCORE_*
+  int two;              // the choice keeps every lane's two best at hand
   int renorm;
   float route_scale;
   const float* bias;    // [E] or NULL: added to the score for the choice alone

@@ -203,10 +203,70 @@ FP8MOE_DEV float loss_of(float np, int tokens, int E, int k) {
 template <int G>
 constexpr int slots() { return G >= 8 ? 1 : 8 / G; }
 
+// A lane's two best experts that rank after (lk, li), b1 = 0 or b2 = 0 where
+// there is none; PACK: keys differ, and carry their ids.
+template <int V, int G, bool PACK, bool AFTER>
+FP8MOE_DEV void best_two(const uint32_t (&key)[V], int l, uint32_t lk, int li, uint32_t& b1, uint32_t& b2, int& i1, int& i2) {
+  b1 = b2 = 0u;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = expert<V, G>(l, i);
+    uint32_t x = key[i];
+    if constexpr (PACK) {
+      if (AFTER && x >= lk) x = 0u;
+      b2 = max(b2, min(b1, x));
+      b1 = max(b1, x);
+    } else {
+      if (AFTER && (x > lk || (x == lk && e <= li))) x = 0u;
+      const bool c1 = x > b1, c2 = x > b2;   // ids rise with i: the first of equal keys stays ahead
+      b2 = c1 ? b1 : c2 ? x : b2;
+      i2 = c1 ? i1 : c2 ? e : i2;
+      b1 = c1 ? x : b1;
+      i1 = c1 ? e : i1;
+    }
+  }
+}
+
 // k rounds: the token's largest key, then the lowest id that has it (PACK: the
 // key's lower half says which).  Lane l ends with slots l, l + G, ..
+//
+// two: a lane's two best experts are kept at hand, so that a round costs the
+// same for any V; a lane that loses both looks through its experts again.  Fewer
+// instructions where lanes, their experts and rounds are many (65536 x 256, top
+// 8: 61.0 us against 67.6, 65536 x 384, top 6: 112 against 129; over 16 lanes of
+// eight 46.3 against 41.6, with four experts a lane 8.8 against 8.4 on 4096 x 128,
+// with two rounds 38.4 against 37.2), but a longer way for one token (4096 x
+// 256: 10.2 against 10.0).
 template <int V, int G, bool PACK>
-FP8MOE_DEV void choose(uint32_t (&key)[V], int (&my_e)[slots<G>()], int k, int l) {
+FP8MOE_DEV void choose(uint32_t (&key)[V], int (&my_e)[slots<G>()], int k, int l, bool two) {
+  if (V >= 8 && G == 32 && two) {
+    my_e[0] = 0;
+    uint32_t b1, b2, lk = 0u;
+    int i1 = 0, i2 = 0, li = 0;
+    best_two<V, G, PACK, false>(key, l, 0u, 0, b1, b2, i1, i2);
+    for (int j = 0; j < k; ++j) {
+      const uint32_t top = lane_umax<G>(b1);
+      bool mine = b1 == top;
+      uint32_t e = 0xFFFFu - (top & 0xFFFFu);
+      if constexpr (!PACK) {
+        e = lane_umin<G>(mine ? (uint32_t)i1 : 0xffffffffu);
+        mine = mine && e == (uint32_t)i1;
+      }
+      if (l == j) my_e[0] = (int)e;
+      if (mine) {
+        lk = b1, li = i1;
+        b1 = b2, i1 = i2;
+        b2 = 0u;
+      }
+      if (__any_sync(0xffffffffu, mine && b1 == 0u)) {
+        uint32_t n1, n2;
+        int m1 = 0, m2 = 0;
+        best_two<V, G, PACK, true>(key, l, lk, li, n1, n2, m1, m2);
+        if (mine && b1 == 0u) b1 = n1, b2 = n2, i1 = m1, i2 = m2;
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int q = 0; q < slots<G>(); ++q) {
     my_e[q] = 0;
@@ -281,9 +341,9 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_fwd(RouterArgs 
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (key[i] != 0u) key[i] = (key[i] & 0xFFFF0000u) | (uint32_t)(0xFFFF - expert<V, G>(l, i));
-      choose<V, G, true>(key, my_e, a.k, l);
+      choose<V, G, true>(key, my_e, a.k, l, a.two);
     } else {
-      choose<V, G, false>(key, my_e, a.k, l);
+      choose<V, G, false>(key, my_e, a.k, l, a.two);
     }
     // lane l: the weights of slots l, l + G, .. from their logits
     float w[S], z = 0.0f;
@@ -624,7 +684,8 @@ int cta_warps(int64_t T, int64_t sms) {
 }
 
 template <int V, int G, bool SIG>
-cudaError_t run_fwd(const RouterArgs& a, int num_sms, cudaStream_t st) {
+cudaError_t run_fwd(RouterArgs a, int num_sms, cudaStream_t st) {
+  a.two = a.k >= 4 && a.T >= 2 * most_warps<V>() * (int64_t)num_sms;
   const bool sums = a.counts != nullptr;
   const bool single = sums && a.T <= SINGLE_CTA_T;
   const int RW = cta_warps<V, G>(a.T, single ? 1 : num_sms), rows = RW * (32 / G);

@@ -149,6 +149,26 @@ def test_ties_and_signed_zero(F):
         assert idx[0].tolist() == [0, 1, 2, 3] and idx[2].tolist() == [5, 70, 0, 1]
 
 
+@pytest.mark.parametrize("E,k", [(130, 6), (256, 8), (384, 12), (1000, 32), (1024, 20)])
+@pytest.mark.parametrize("T", [37, 9999])
+def test_one_lane_has_the_best(F, T, E, k):
+    """Runs of equal or falling keys within one lane's experts, which lose more
+    of them than a lane keeps at hand."""
+    g = torch.Generator().manual_seed(E)
+    x = (torch.randint(-2, 3, (T, E), generator=g) * 0.5).float()
+    x[1] = 0.0
+    x[2] = -torch.arange(E, dtype=torch.float32)
+    x[3] = torch.arange(E, dtype=torch.float32) / E
+    for piece in range(min(E // 128, 8)):      # the four neighbours of one lane in every piece
+        x[4, 128 * piece + 8:128 * piece + 12] = 9.0 - piece
+        x[5, 128 * piece + 8:128 * piece + 12] = 9.0
+    x[6, 3:] = -float("inf")
+    _check(F, x, k, "softmax", True, 2.5)
+    _check(F, x.to(torch.bfloat16), k, "sigmoid", False, 1.0)
+    bias = (torch.randint(-1, 2, (E,), generator=g) * 0.25).float()
+    _check(F, x, k, "sigmoid", True, 1.0, bias=bias)
+
+
 @pytest.mark.parametrize("E,k", [(4, 3), (15, 5), (20, 8), (60, 6), (96, 8), (256, 8), (384, 12), (1024, 8)])
 @pytest.mark.parametrize("T", [37, 1301])
 def test_bf16_ties(F, T, E, k):
