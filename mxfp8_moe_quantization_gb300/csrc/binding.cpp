@@ -66,33 +66,54 @@ bool flag(PyObject* o) {
 // The call's device: that of its first argument, which has to be current.
 struct Call {
   int dev;
+  Tensor shared;      // see together()
+  int64_t used = 0;
   explicit Call(const Tensor& t) {
     if (!t.is_cuda()) refuse();
     dev = t.get_device();
     if (dev != c10::cuda::current_device()) refuse();
   }
   fp8moe_stream_t stream() const { return (fp8moe_stream_t)c10::cuda::getCurrentCUDAStream(dev).stream(); }
-  Tensor empty(Shape s, at::ScalarType t) const {
-    for (int64_t n : s)
-      if (n < 0) refuse();
+  // Small results that a call makes together share one allocation (0.9 us of
+  // host time each, a view of it 0.3): give their bytes first, 0 for one that the
+  // caller brings or does not want; empty() then takes them from it in any order.
+  // Large ones stay apart, as each holds the memory of all.
+  static constexpr int64_t TOGETHER = 256 << 10;
+  static int64_t padded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+  void together(std::initializer_list<int64_t> bytes) {
+    int64_t sum = 0, n = 0;
+    for (int64_t b : bytes) {
+      if (b < 0 || b > TOGETHER) return;
+      sum += padded(b);
+      n += b > 0;
+    }
+    if (n < 2 || sum > TOGETHER) return;
+    shared = at::detail::empty_cuda({sum}, at::kByte, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt);
+  }
+  Tensor empty(Shape s, at::ScalarType t) {
+    int64_t n = 1;
+    for (int64_t d : s) {
+      if (d < 0) refuse();
+      n *= d;
+    }
+    const caffe2::TypeMeta meta = c10::scalarTypeToTypeMeta(t);
+    const int64_t bytes = n * (int64_t)meta.itemsize();
+    if (shared.defined() && bytes > 0 && used + bytes <= shared.numel()) {
+      Tensor p = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(shared.storage()), shared.key_set(), meta);
+      p.unsafeGetTensorImpl()->set_storage_offset(used / (int64_t)meta.itemsize());
+      p.unsafeGetTensorImpl()->set_sizes_contiguous(s);
+      used += padded(bytes);
+      return p;
+    }
     // (at::empty without its dispatch)
     return at::detail::empty_cuda(s, t, at::Device(at::kCUDA, (c10::DeviceIndex)dev), std::nullopt);
   }
   // bytes, zeroed on the call's stream (at::zeros: 10.5 us of host time against
   // 3.3; where padding is written by nobody and has to be valid)
-  Tensor zeros(int64_t n) const {
+  Tensor zeros(int64_t n) {
     Tensor t = empty({n}, at::kByte);
     if (n > 0 && cudaMemsetAsync(t.data_ptr(), 0, (size_t)n, (cudaStream_t)stream()) != cudaSuccess) throw Refused{FP8MOE_ERR_CUDA};
     return t;
-  }
-  // n elements of type ty from byte `at` (a multiple of their size) of the byte
-  // tensor t, whose storage they share: 0.3 us where an allocation takes 0.9
-  static Tensor part(const Tensor& t, int64_t at, int64_t n, at::ScalarType ty) {
-    const caffe2::TypeMeta meta = c10::scalarTypeToTypeMeta(ty);
-    Tensor p = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(), meta);
-    p.unsafeGetTensorImpl()->set_storage_offset(at / (int64_t)meta.itemsize());
-    p.unsafeGetTensorImpl()->set_sizes_contiguous({n});
-    return p;
   }
   bool here(const Tensor& t, at::ScalarType ty, Shape s) const {
     return t.is_cuda() && t.get_device() == dev && t.scalar_type() == ty && t.sizes() == s;
@@ -110,7 +131,7 @@ struct Call {
     return t.data_ptr();
   }
   // the given tensor or a new one, checked; its address
-  void* out(Tensor& o, PyObject* given, at::ScalarType ty, Shape s) const {
+  void* out(Tensor& o, PyObject* given, at::ScalarType ty, Shape s) {
     if (given == Py_None) {
       o = empty(s, ty);
       return o.data_ptr();
@@ -119,7 +140,7 @@ struct Call {
     return dense(o, ty, s);
   }
   // a workspace of nbytes: the given one (any type) or a new one
-  void* workspace(Tensor& o, PyObject* given, int64_t& nbytes) const {
+  void* workspace(Tensor& o, PyObject* given, int64_t& nbytes) {
     if (given == Py_None) {
       o = empty({nbytes < 0 ? 0 : nbytes}, at::kByte);
     } else {
@@ -156,13 +177,16 @@ PyObject* add_rmsnorm_fwd(PyObject* const* a) {
   const Tensor* r = maybe(a[2]);
   if (x.dim() != 2) refuse();
   const int64_t T = x.size(0), H = x.size(1);
-  const Call c(x);
+  Call c(x);
   int64_t ldx = 0, ldr = 0;
   const void* px = c.rows(x, at::kBFloat16, {T, H}, ldx);
   const at::ScalarType wt = real_type(w);
   const void* pw = c.dense(w, wt, {H});
   const void* pr = r ? c.rows(*r, at::kBFloat16, {T, H}, ldr) : nullptr;
   Tensor h, y, rstd, q, scale;
+  const bool mx = a[4] != Py_None;
+  c.together({r && a[9] == Py_None ? T * H * 2 : 0, flag(a[7]) && a[10] == Py_None ? T * H * 2 : 0,
+              flag(a[8]) && a[11] == Py_None ? T * 4 : 0, mx && a[12] == Py_None ? T * H : 0});
   void *ph = nullptr, *py = nullptr, *ps = nullptr, *pq = nullptr, *pscale = nullptr;
   if (r) {
     ph = c.out(h, a[9], at::kBFloat16, {T, H});
@@ -203,7 +227,7 @@ PyObject* add_rmsnorm_bwd(PyObject* const* a) {
   const Tensor& dy = tensor(a[0]);
   if (dy.dim() != 2) refuse();
   const int64_t T = dy.size(0), H = dy.size(1);
-  const Call c(dy);
+  Call c(dy);
   const void* pdy = c.dense(dy, at::kBFloat16, {T, H});
   const void* ph = c.dense(tensor(a[1]), at::kBFloat16, {T, H});
   const void* prstd = c.dense(tensor(a[2]), at::kFloat, {T});
@@ -212,6 +236,7 @@ PyObject* add_rmsnorm_bwd(PyObject* const* a) {
   const void* pw = c.dense(w, wt, {H});
   const void* pdh = c.dense(maybe(a[4]), at::kBFloat16, {T, H});
   Tensor dx, dw, ws;
+  c.together({a[5] == Py_None ? T * H * 2 : 0, a[6] == Py_None ? H * 4 : 0});
   void* pdx = c.out(dx, a[5], at::kBFloat16, {T, H});
   void* pdw = c.out(dw, a[6], at::kFloat, {H});
   int64_t nbytes = fp8moe_add_rmsnorm_bwd_workspace_bytes(T, H);
@@ -234,28 +259,24 @@ PyObject* router_fwd(PyObject* const* a) {
   const Tensor& x = tensor(a[0]);
   if (x.dim() != 2) refuse();
   const int64_t T = x.size(0), E = x.size(1), k = integer(a[1]);
+  if (k < 1 || k > E) refuse();
   const at::ScalarType xt = real_type(x);
-  const Call c(x);
+  Call c(x);
   int64_t ld = 0, nbytes = 0;
   const void* px = c.rows(x, xt, {T, E}, ld);
   const void* pb = c.dense(maybe(a[5]), at::kFloat, {E});
   const uint8_t* pm = token_mask(c, maybe(a[6]), T);
   Tensor idx, w, counts, psum, loss, ws;
+  const bool sums = flag(a[7]);
+  c.together({a[8] == Py_None ? T * k * 4 : 0, a[9] == Py_None ? T * k * 4 : 0, sums && a[10] == Py_None ? (E + 1) * 4 : 0,
+              sums && a[11] == Py_None ? E * 4 : 0, sums && a[12] == Py_None ? 4 : 0});
   void* pi = c.out(idx, a[8], at::kInt, {T, k});
   void* pw = c.out(w, a[9], at::kFloat, {T, k});
   void *pc = nullptr, *pp = nullptr, *pl = nullptr, *pws = nullptr;
-  if (flag(a[7])) {
-    if (a[10] == Py_None && a[11] == Py_None && a[12] == Py_None) {
-      const Tensor all = c.empty({(2 * E + 2) * 4}, at::kByte);
-      counts = Call::part(all, 0, E + 1, at::kInt);
-      psum = Call::part(all, (E + 1) * 4, E, at::kFloat);
-      loss = Call::part(all, (2 * E + 1) * 4, 1, at::kFloat);
-      pc = counts.data_ptr(), pp = psum.data_ptr(), pl = loss.data_ptr();
-    } else {
-      pc = c.out(counts, a[10], at::kInt, {E + 1});
-      pp = c.out(psum, a[11], at::kFloat, {E});
-      pl = c.out(loss, a[12], at::kFloat, {1});
-    }
+  if (sums) {
+    pc = c.out(counts, a[10], at::kInt, {E + 1});
+    pp = c.out(psum, a[11], at::kFloat, {E});
+    pl = c.out(loss, a[12], at::kFloat, {1});
     nbytes = fp8moe_router_workspace_bytes(T, E);
     if (nbytes > 0) pws = c.workspace(ws, a[13], nbytes);
   }
@@ -270,7 +291,7 @@ PyObject* router_bwd(PyObject* const* a) {
   if (x.dim() != 2 || idx.dim() != 2) refuse();
   const int64_t T = x.size(0), E = x.size(1), k = idx.size(1);
   const at::ScalarType xt = real_type(x);
-  const Call c(x);
+  Call c(x);
   int64_t ld = 0;
   const void* px = c.rows(x, xt, {T, E}, ld);
   const void* pi = c.dense(idx, at::kInt, {T, k});
@@ -290,7 +311,7 @@ PyObject* route_weight_grad(PyObject* const* a) {
   const Tensor &dout = tensor(a[0]), &y = tensor(a[1]), &row_of = tensor(a[2]);
   if (dout.dim() != 2 || y.dim() != 2 || row_of.dim() != 2) refuse();
   const int64_t T = dout.size(0), N = dout.size(1), k = row_of.size(1);
-  const Call c(dout);
+  Call c(dout);
   const void* pd = c.dense(dout, at::kBFloat16, {T, N});
   const void* py = c.dense(y, at::kBFloat16, {y.size(0), N});
   const void* pr = c.dense(row_of, at::kInt, {T, k});
@@ -301,7 +322,7 @@ PyObject* route_weight_grad(PyObject* const* a) {
 }
 
 // MXFP8 codes [R, C] and their scales; E: groups of a grouped layout
-void mx_out(const Call& c, Tensor& q, PyObject* gq, Tensor& s, PyObject* gs, int layout, int64_t R, int64_t C, int64_t E,
+void mx_out(Call& c, Tensor& q, PyObject* gq, Tensor& s, PyObject* gs, int layout, int64_t R, int64_t C, int64_t E,
             void*& pq, uint8_t*& ps) {
   const bool plain = layout == FP8MOE_SCALES_ROWMAJOR;
   const int64_t need = plain ? R * (C / 32) : fp8moe_swizzled_scales_bytes(1, R, C / 32, E, layout);
@@ -323,7 +344,7 @@ PyObject* swiglu(PyObject* const* a) {
   const Tensor* offs = maybe(a[2]);
   if (h.dim() != 2 || h.size(1) % 2) refuse();
   const int64_t M = h.size(0), F = h.size(1) / 2, W = dout ? 2 * F : F;
-  const Call c(h);
+  Call c(h);
   int64_t ldh = 0;
   const void* ph = c.rows(h, at::kBFloat16, {M, 2 * F}, ldh);
   const void* pd = c.dense(dout, at::kBFloat16, {M, F});
@@ -333,9 +354,11 @@ PyObject* swiglu(PyObject* const* a) {
   Tensor out, q0, s0, q1, s1;
   void *pout = nullptr, *p0 = nullptr, *p1 = nullptr;
   uint8_t *ps0 = nullptr, *ps1 = nullptr;
-  if (flag(a[5])) pout = c.out(out, a[8], at::kBFloat16, {M, W});
-  if (flag(a[6])) mx_out(c, q0, a[9], s0, a[10], l0, M, W, E, p0, ps0);
-  if (flag(a[7])) mx_out(c, q1, a[11], s1, a[12], l1, W, M, E, p1, ps1);
+  const bool o = flag(a[5]), d0 = flag(a[6]), d1 = flag(a[7]);
+  c.together({o && a[8] == Py_None ? M * W * 2 : 0, d0 && a[9] == Py_None ? M * W : 0, d1 && a[11] == Py_None ? M * W : 0});
+  if (o) pout = c.out(out, a[8], at::kBFloat16, {M, W});
+  if (d0) mx_out(c, q0, a[9], s0, a[10], l0, M, W, E, p0, ps0);
+  if (d1) mx_out(c, q1, a[11], s1, a[12], l1, W, M, E, p1, ps1);
   if (dout) {
     check(fp8moe_swiglu_bwd(pd, ph, ldh, M, F, (const int32_t*)po, E, pout, p0, ps0, l0, p1, ps1, l1, c.stream()));
   } else {

@@ -69,3 +69,34 @@ def test_swiglu(F, M, Fd):
                         s0=g((n, Fd // 32), U8))
     g.check("gated activation")
     assert F.fp8moe_get_device_status() == 0
+
+
+@pytest.mark.parametrize("T", [1, 3, 40, 3000])
+def test_new_results_are_apart(F, T):
+    """Results that a call allocates are contiguous, aligned, do not overlap and
+    outlive one another."""
+    H, E, k = 512, 64, 6
+    x, w = torch.randn(T, H, device=DEV).to(torch.bfloat16), torch.ones(H, device=DEV)
+    h2 = torch.randn(32 * T, 2 * H, device=DEV).to(torch.bfloat16)
+    logits = torch.randn(T, E, device=DEV)
+    rstd = torch.ones(T, device=DEV)
+    calls = [lambda: F.fp8moe_add_rmsnorm_fwd(x, w, x, recipe=F.MXFP8, need_y=True, need_rstd=True),
+             lambda: F.fp8moe_add_rmsnorm_fwd(x, w, recipe=F.ROWWISE, need_y=True, need_rstd=True),
+             lambda: F.fp8moe_add_rmsnorm_bwd(x, x, rstd, w),
+             lambda: F.fp8moe_router_fwd(logits, k),
+             lambda: F.fp8moe_swiglu_fwd(h2, dim0=True, dim1=True)]
+    for call in calls:
+        first = [t for t in call() if t is not None]
+        want = [t.clone() for t in first]
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in first)
+        assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+        assert all(t.is_contiguous() and t.data_ptr() % 16 == 0 for t in first)
+        for i, t in enumerate(first):
+            t.zero_()
+            assert all(torch.equal(a, b) for a, b in zip(first[i + 1:], want[i + 1:]))
+        first = [t for t in call() if t is not None]
+        last = first[-1]
+        first = None
+        call()
+        torch.cuda.synchronize()
+        assert torch.equal(last, want[-1])
