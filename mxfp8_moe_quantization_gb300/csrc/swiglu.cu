@@ -17,8 +17,8 @@
 // from the lane's registers, so the transposed codes need no byte transposes.
 //
 // Bound by HBM: 6.06 bytes per element forward, 10.1 backward.  Measured: 36448
-// x 2048 in 256 groups forward, both directions, 71 us = 6.4 TB/s (95% of a
-// copy's rate); 51136 x 1408 backward 118 us = 6.2 TB/s (92%).  The first form,
+// x 2048 in 256 groups forward, both directions, 72 us = 6.3 TB/s (94% of a
+// copy's rate); 51136 x 1408 backward 119 us = 6.1 TB/s (92%).  The first form,
 // with every lane deriving every scale, expf and a division, and 45
 // instructions per element instead of about 20, took 152 and 283 us.
 #include "common.cuh"
