@@ -596,7 +596,9 @@ cudaError_t launch_bwd_t(NormBwdArgs a, float* dw, int num_sms, int max_smem, cu
   if (ring) a.stall = take_ring_stall_hook();
   auto run = [&](auto kern) {
     const int smem = ring ? (int)(slot * stages) : 0;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // (the limit belongs to the kernel and every host thread that launches it:
+    // always the same, whatever this call's rows take of it)
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ring ? (int)budget : 0);
     int per = 0;
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, wpr * 32 * groups, smem);
     if (e != cudaSuccess || per < 1) return e == cudaSuccess ? cudaErrorInvalidConfiguration : e;
