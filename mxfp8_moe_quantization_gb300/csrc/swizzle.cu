@@ -279,7 +279,9 @@ cudaError_t launch_swizzle(const uint8_t* s, int64_t B, int64_t R, int64_t Cs, c
     int per = (int)(c & 0xFFFFFFFF);
     if ((size_t)(c >> 32) != smem || per <= 0) {
       auto kern = grows ? k_swizzle_rows<true> : k_swizzle_rows<false>;
-      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      // (the limit belongs to the kernel and every host thread that launches it:
+      // the widest rows', whatever this call takes of it)
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(128 * SWR_MAX_CS));
       if (e != cudaSuccess) return e;
       if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, SWR_THREADS, smem) != cudaSuccess || per < 1) {
         (void)cudaGetLastError();

@@ -64,3 +64,13 @@ def test_norm_backward_of_two_row_lengths(F):
         torch.cuda.synchronize()
         assert torch.equal(dx, keep[4]) and torch.equal(dw, keep[5])
 
+
+def test_scale_swizzle_of_two_widths(F):
+    """Rows of 16-byte multiples, one kernel for every width."""
+    def call(R, Cs):
+        s = torch.randint(0, 255, (R, Cs), dtype=torch.uint8, device=DEV)
+        out = torch.empty(F.fp8moe_swizzled_scales_bytes(1, R, Cs), dtype=torch.uint8, device=DEV)
+        return lambda stream: F.lib().fp8moe_swizzle_scales_128x4(s.data_ptr(), 1, R, Cs, None, 0, F.NO_GROUPS, out.data_ptr(),
+                                                                  stream)
+
+    assert _together([call(256, 384), call(256, 16)]) == [{0}, {0}]
