@@ -408,7 +408,8 @@ fp8moe_status fp8moe_mxfp8_moe_bwd(const void* dy, const int32_t* offs, int64_t 
  * fp8moe_route_unpermute: y [rows, N] bf16 (a grouped GEMM output), row_of as
  * above -> out [T, N] bf16 with out[t] = sum over j (in order, fp32) of
  * w[t, j] * y[row_of[t, j]] (w = 1 when topk_w is NULL: the backward of
- * permute).  Alignment: y, out 16 bytes, N % 8 == 0.
+ * permute).  row_of's numbers have to be below the rows of y (it is not told
+ * how many these are).  Alignment: y, out 16 bytes, N % 8 == 0.
  * ------------------------------------------------------------------------ */
 int64_t fp8moe_route_rows(int64_t T, int64_t k, int64_t E);
 int64_t fp8moe_route_workspace_bytes(int64_t T, int64_t k, int64_t E);
@@ -534,7 +535,11 @@ fp8moe_status fp8moe_add_rmsnorm_bwd(const void* dy, const void* h, const float*
  * fp8moe_route_weight_grad: the gradient of the weights of
  * fp8moe_route_unpermute: dw[t, j] = sum_n dout[t, n] * y[row_of[t, j], n],
  * dout [T, N] bf16, y [rows, N] bf16, row_of [T, k] int32 (negative: 0),
- * dw [T, k] fp32.  N % 8 == 0; dout, y 16-byte aligned.
+ * dw [T, k] fp32.  N % 8 == 0; dout, y 16-byte aligned.  It is not told how many
+ * rows y has: every number in row_of has to be below that, as for
+ * fp8moe_route_unpermute.  fp8moe_route_weight_grad_bounded is the same with
+ * that number (0 <= rows <= 2^31; y may be NULL where it is 0): a row number
+ * outside [0, rows) gives 0 and nothing is read for it.
  * ------------------------------------------------------------------------ */
 int64_t fp8moe_router_workspace_bytes(int64_t T, int64_t E);
 fp8moe_status fp8moe_router_fwd(const void* logits, int logits_type, int64_t T, int64_t E, int64_t ldl, int64_t k,
@@ -548,6 +553,8 @@ fp8moe_status fp8moe_router_bwd(const void* logits, int logits_type, int64_t T, 
                                 const float* dloss, void* dlogits, fp8moe_stream_t stream);
 fp8moe_status fp8moe_route_weight_grad(const void* dout, const void* y, const int32_t* row_of, int64_t T, int64_t N,
                                        int64_t k, float* dw, fp8moe_stream_t stream);
+fp8moe_status fp8moe_route_weight_grad_bounded(const void* dout, const void* y, int64_t rows, const int32_t* row_of,
+                                               int64_t T, int64_t N, int64_t k, float* dw, fp8moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Gated activation between the two expert products, with MXFP8 output along

@@ -89,6 +89,7 @@ SYMBOLS = {
     "fp8moe_router_bwd": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp,
                                  _vp]),
     "fp8moe_route_weight_grad": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]),
+    "fp8moe_route_weight_grad_bounded": (_i32, [_vp, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp]),
     "fp8moe_swiglu_fwd": (_i32, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp]),
     "fp8moe_swiglu_bwd": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp]),
     "fp8moe_get_device_status": (_i32, [_vp, ctypes.POINTER(ctypes.c_int32)]),
@@ -609,7 +610,7 @@ def fp8moe_router_bwd(logits, topk_idx, counts=None, dtopk_w=None, dloss=None, s
 
 def fp8moe_route_weight_grad(dout, y, row_of, dw=None, stream=None):
     """Gradient of fp8moe_route_unpermute's weights: dout [T, N] bf16, y
-    [rows, N] bf16, row_of [T, k] int32 -> dw [T, k] fp32."""
+    [rows, N] bf16, row_of [T, k] int32 (outside [0, rows): 0) -> dw [T, k] fp32."""
     return _run("fp8moe_route_weight_grad", stream, _native().route_weight_grad, dout, y, row_of, dw)
 
 

@@ -595,17 +595,23 @@ fp8moe_status fp8moe_router_bwd(const void* logits, int logits_type, int64_t T, 
   return cuda_result(fp8moe::launch_router_bwd(a, d->num_sms, (cudaStream_t)stream));
 }
 
-fp8moe_status fp8moe_route_weight_grad(const void* dout, const void* y, const int32_t* row_of, int64_t T, int64_t N,
-                                       int64_t k, float* dw, fp8moe_stream_t stream) {
-  if (T < 0 || N < 0 || k < 1 || T > ((int64_t)1 << 30) / k) return FP8MOE_ERR_INVALID_ARG;
+fp8moe_status fp8moe_route_weight_grad_bounded(const void* dout, const void* y, int64_t rows, const int32_t* row_of,
+                                               int64_t T, int64_t N, int64_t k, float* dw, fp8moe_stream_t stream) {
+  if (rows < 0 || rows > ((int64_t)1 << 31) || T < 0 || N < 0 || k < 1 || T > ((int64_t)1 << 30) / k) return FP8MOE_ERR_INVALID_ARG;
   if (N % 8) return FP8MOE_ERR_ALIGNMENT;
   if (T == 0) return FP8MOE_OK;
-  if (!row_of || !dw || (N > 0 && (!dout || !y))) return FP8MOE_ERR_INVALID_ARG;
+  if (!row_of || !dw || (N > 0 && (!dout || (!y && rows > 0)))) return FP8MOE_ERR_INVALID_ARG;
   if (!al16(dout) || !al16(y) || (((uintptr_t)row_of | (uintptr_t)dw) & 3)) return FP8MOE_ERR_ALIGNMENT;
   DevInfo* d;
   fp8moe_status s = device_info(&d);
   if (s) return s;
-  return cuda_result(fp8moe::launch_route_weight_grad(dout, y, row_of, T, N, k, dw, d->num_sms, (cudaStream_t)stream));
+  return cuda_result(
+      fp8moe::launch_route_weight_grad(dout, y, rows, row_of, T, N, k, dw, d->num_sms, (cudaStream_t)stream));
+}
+
+fp8moe_status fp8moe_route_weight_grad(const void* dout, const void* y, const int32_t* row_of, int64_t T, int64_t N,
+                                       int64_t k, float* dw, fp8moe_stream_t stream) {
+  return fp8moe_route_weight_grad_bounded(dout, y, (int64_t)1 << 31, row_of, T, N, k, dw, stream);
 }
 
 static fp8moe_status swiglu(bool bwd, const void* dout, const void* h, int64_t ldh, int64_t M, int64_t F,

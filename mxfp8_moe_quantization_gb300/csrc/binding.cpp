@@ -317,7 +317,7 @@ PyObject* route_weight_grad(PyObject* const* a) {
   const void* pr = c.dense(row_of, at::kInt, {T, k});
   Tensor dw;
   void* pw = c.out(dw, a[3], at::kFloat, {T, k});
-  check(fp8moe_route_weight_grad(pd, py, (const int32_t*)pr, T, N, k, (float*)pw, c.stream()));
+  check(fp8moe_route_weight_grad_bounded(pd, py, y.size(0), (const int32_t*)pr, T, N, k, (float*)pw, c.stream()));
   return give(dw);
 }
 

@@ -106,8 +106,9 @@ cudaError_t launch_norm_bwd(const void* dy, const void* h, const float* rstd, co
 struct RouterArgs;
 cudaError_t launch_router_fwd(const RouterArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_router_bwd(const RouterArgs& a, int num_sms, cudaStream_t st);
-cudaError_t launch_route_weight_grad(const void* dout, const void* y, const int32_t* row_of, int64_t T, int64_t N,
-                                     int64_t k, float* dw, int num_sms, cudaStream_t st);
+// (rows of y: at most 2^31; a row number past them is a missing one)
+cudaError_t launch_route_weight_grad(const void* dout, const void* y, int64_t rows, const int32_t* row_of, int64_t T,
+                                     int64_t N, int64_t k, float* dw, int num_sms, cudaStream_t st);
 
 // gated activation with MXFP8 output (swiglu.cu); dout == NULL: forward
 struct SwigluArgs;

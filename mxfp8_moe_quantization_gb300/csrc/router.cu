@@ -616,13 +616,13 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_bwd(RouterArgs 
 // dw[t, j] = sum over n of dout[t, n] * y[row_of[t, j], n]: L lanes take a token
 // (several tokens a warp, or several warps a token), a lane every L-th chunk of
 // 16 bytes, of UK rows of y at a time.  The row numbers rather than pointers are
-// kept, so that four CTAs fit an SM (16384 tokens x 6 rows of 2048: 70.5 us against
+// kept (-1: missing, or no row of y), so that four CTAs fit an SM (16384 tokens x 6 rows of 2048: 70.5 us against
 // 80.0 with three; what spills is outside the loop's loads).
 template <int L, int UK>
 __global__ void __launch_bounds__(256, 4) k_route_weight_grad(const uint16_t* __restrict__ dout,
                                                               const uint16_t* __restrict__ y,
-                                                              const int32_t* __restrict__ row_of, int64_t T, int64_t N,
-                                                              int k, float* __restrict__ dw) {
+                                                              const int32_t* __restrict__ row_of, uint32_t rows,
+                                                              int64_t T, int64_t N, int k, float* __restrict__ dw) {
   constexpr int WPT = L / 32;   // warps per token (0: less than one)
   __shared__ float red[8][UK];
   const int warp = threadIdx.x >> 5, l = threadIdx.x % L;
@@ -634,6 +634,7 @@ __global__ void __launch_bounds__(256, 4) k_route_weight_grad(const uint16_t* __
 #pragma unroll
     for (int j = 0; j < UK; ++j) {
       row[j] = t < T && j0 + j < k ? row_of[t * k + j0 + j] : -1;
+      if ((uint32_t)row[j] >= rows) row[j] = -1;
       acc[j] = 0.0f;
     }
     if (t < T) {
@@ -760,8 +761,8 @@ cudaError_t launch_router_bwd(const RouterArgs& a, int num_sms, cudaStream_t st)
 #undef FP8MOE_ROUTER_ALL
 #undef FP8MOE_ROUTER
 
-cudaError_t launch_route_weight_grad(const void* dout, const void* y, const int32_t* row_of, int64_t T, int64_t N,
-                                     int64_t k, float* dw, int num_sms, cudaStream_t st) {
+cudaError_t launch_route_weight_grad(const void* dout, const void* y, int64_t rows, const int32_t* row_of, int64_t T,
+                                     int64_t N, int64_t k, float* dw, int num_sms, cudaStream_t st) {
   const uint16_t *d = (const uint16_t*)dout, *yp = (const uint16_t*)y;
   // Lanes per token. Few enough that a lane has chunks to do and a CTA's tokens
   // overlap their dependent loads (60000 tokens x 8 rows of 128: 24.6 us with 16,
@@ -775,7 +776,7 @@ cudaError_t launch_route_weight_grad(const void* dout, const void* y, const int3
   int L = nv <= 48 ? 16 : nv < 128 || (k == 1 && nv < 512) ? 32 : nv < 512 ? 128 : 256;
   while (L < 256 && L < nv && T * L < (int64_t)256 * num_sms) L = L == 32 ? 128 : 2 * L;
   const unsigned grid = (unsigned)((T + 256 / L - 1) / (256 / L));
-  auto run = [&](auto kern) { kern<<<grid, 256, 0, st>>>(d, yp, row_of, T, N, (int)k, dw); };
+  auto run = [&](auto kern) { kern<<<grid, 256, 0, st>>>(d, yp, row_of, (uint32_t)rows, T, N, (int)k, dw); };
 #define FP8MOE_WG(UK)                                     \
   if (L == 16) run(k_route_weight_grad<16, UK>);          \
   else if (L == 32) run(k_route_weight_grad<32, UK>);     \
