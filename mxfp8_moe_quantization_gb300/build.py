@@ -4,7 +4,8 @@ that marshals PyTorch tensors for the small calls with the host compiler.
 Each translation unit compiles in parallel; the CUDA objects link into
 ``mxfp8_moe_quantization_gb300/libfp8moe.so``, the binding into ``_binding.so``
 beside it.  A rebuild happens only when a source or header is newer than the
-libraries.  No cmake, one -gencode.
+libraries, or when the binding was made for another PyTorch or Python (it is
+compiled against their internals).  No cmake, one -gencode.
 """
 from __future__ import annotations
 
@@ -22,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8moe.so")
 BINDING = os.path.join(HERE, "_binding.so")
+STAMP = os.path.join(BUILD, "binding.for")   # what BINDING was compiled against
 
 SOURCES = ["api.cu", "quant.cu", "colwise.cu", "colwise_cluster.cu", "colwise_jagged.cu", "dual.cu", "tensorwise.cu", "blockwise.cu", "routing.cu", "swizzle.cu",
            "grouped_mm.cu", "blockwise_mm.cu", "layer.cu", "norm.cu", "router.cu", "swiglu.cu"]
@@ -49,8 +51,21 @@ def _torch_dir() -> str:
     return os.path.dirname(torch.__file__)
 
 
+def _made_for() -> str:
+    import torch
+    return "\n".join([torch.__version__, os.path.realpath(_torch_dir()), sys.version, os.uname().machine])
+
+
+def _stamped() -> str:
+    try:
+        with open(STAMP) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING) or _stamped() != _made_for():
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _deps())
@@ -105,6 +120,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
                          "-L", torch_lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
                          "-L", os.path.join(cuda, "lib64"), "-lcudart", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"])
     os.replace(tmp, BINDING)
+    with open(STAMP + ".tmp", "w") as f:
+        f.write(_made_for())
+    os.replace(STAMP + ".tmp", STAMP)
     return LIB
 
 
