@@ -38,10 +38,10 @@ namespace {
 constexpr int SG_ROWS = 32, SG_COLS = 64, SG_RW = 2, SG_CW = 2, SG_WARPS = SG_RW * SG_CW;
 constexpr int CW = 8;   // columns per lane
 
-// -g of a bf16 pair, cut to +-88, as fp32
+// -g of a bf16 pair, cut to +-88, as fp32; NaN stays NaN
 FP8MOE_DEV uint64_t neg_cut(uint32_t g) {
   uint32_t n;
-  asm("{\n .reg .b32 t;\n neg.bf16x2 t, %1;\n min.bf16x2 t, t, %2;\n max.bf16x2 %0, t, %3;\n}"
+  asm("{\n .reg .b32 t;\n neg.bf16x2 t, %1;\n min.NaN.bf16x2 t, t, %2;\n max.NaN.bf16x2 %0, t, %3;\n}"
       : "=r"(n)
       : "r"(g), "r"(0x42B042B0u), "r"(0xC2B0C2B0u));
   return unpk_bf16(n);
