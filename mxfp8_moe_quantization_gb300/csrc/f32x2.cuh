@@ -49,16 +49,22 @@ FP8MOE_DEV uint64_t mulx(uint32_t a, uint32_t b) {
       : "r"(a), "r"(b), "f"(-0.0f));
   return pk(x, y);
 }
-// max(|a|, |b|, |c|); NaN ignored
+// max(|a|, |b|, |c|), NaN above every number
 FP8MOE_DEV float amax3(float a, float b, float c) {
   float r;
-  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 FP8MOE_DEV float amax3(float m, uint64_t p) {
   float a, b;
   unpk(p, a, b);
   return amax3(m, a, b);
+}
+// max(a, b), NaN above every number
+FP8MOE_DEV float nanmax(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 // e8m0 byte of a block maximum (the dim0 quantizer's rule on an fp32 maximum)
 // and the multiplier 2^-e

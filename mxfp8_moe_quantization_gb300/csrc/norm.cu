@@ -90,7 +90,7 @@ FP8MOE_DEV float row_reduce(float v, float* red, int wpr, int group, int wrow) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = MAX ? fmaxf(v, u) : v + u;
+    v = MAX ? nanmax(v, u) : v + u;
   }
   if (wpr > 1) {
     // a row's values, every lane one of them, zero past the last (the maxima
@@ -101,7 +101,7 @@ FP8MOE_DEV float row_reduce(float v, float* red, int wpr, int group, int wrow) {
     v = lane < wpr ? red[group * wpr + lane] : 0.0f;
     for (int o = wpr > 16 ? 16 : wpr > 8 ? 8 : wpr > 4 ? 4 : 2; o > 0; o >>= 1) {
       const float u = __shfl_xor_sync(0xffffffffu, v, o);
-      v = MAX ? fmaxf(v, u) : v + u;
+      v = MAX ? nanmax(v, u) : v + u;
     }
     v = __shfl_sync(0xffffffffu, v, 0);
   }
@@ -131,8 +131,8 @@ FP8MOE_DEV void put_chunk(const NormFwdArgs& a, int64_t row, int ch, bool ok, co
   if (a.y && ok) *reinterpret_cast<uint4*>(a.y + row * a.H + (int64_t)ch * 8) = pack8(v);
   if constexpr (OUT == NORM_OUT_MX) {
     float m = absmax8(0.0f, v);
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m = nanmax(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = nanmax(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const uint32_t b = mx_byte(m, s);
     if (ok && (ch & 3) == 0) {
       const int64_t c = ch >> 2;
@@ -161,17 +161,17 @@ FP8MOE_DEV void put_mx(const NormFwdArgs& a, int64_t row, int t, int tpr, int nc
     float p[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      p[i] = fmaxf(b0 ? m[i + 2] : m[i], __shfl_xor_sync(0xffffffffu, b0 ? m[i] : m[i + 2], 1));
-    mk = fmaxf(b1 ? p[1] : p[0], __shfl_xor_sync(0xffffffffu, b1 ? p[0] : p[1], 2));
+      p[i] = nanmax(b0 ? m[i + 2] : m[i], __shfl_xor_sync(0xffffffffu, b0 ? m[i] : m[i + 2], 1));
+    mk = nanmax(b1 ? p[1] : p[0], __shfl_xor_sync(0xffffffffu, b1 ? p[0] : p[1], 2));
     own = b0 * 2 + b1;
   } else {
     if constexpr (V == 2) {
-      mk = fmaxf(b0 ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, b0 ? m[0] : m[1], 1));
+      mk = nanmax(b0 ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, b0 ? m[0] : m[1], 1));
       own = b0;
     } else {
-      mk = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
+      mk = nanmax(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
     }
-    mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, 2));
+    mk = nanmax(mk, __shfl_xor_sync(0xffffffffu, mk, 2));
   }
   float s;
   const uint32_t b = mx_byte(mk, s);

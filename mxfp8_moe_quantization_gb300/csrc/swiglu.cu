@@ -113,7 +113,7 @@ FP8MOE_DEV void halve(const float (&m)[N], float (&out)[N / 2], int lane, int ma
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) {
     const float other = __shfl_xor_sync(0xffffffffu, up ? m[i] : m[i + N / 2], mask);
-    out[i] = fmaxf(up ? m[i + N / 2] : m[i], other);
+    out[i] = nanmax(up ? m[i + N / 2] : m[i], other);
   }
 }
 
