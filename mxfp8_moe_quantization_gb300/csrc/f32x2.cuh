@@ -67,7 +67,8 @@ FP8MOE_DEV float nanmax(float a, float b) {
   return r;
 }
 // e8m0 byte of a block maximum (the dim0 quantizer's rule on an fp32 maximum)
-// and the multiplier 2^-e
+// and the multiplier 2^-e; infinity and NaN give a byte that no number gives
+constexpr uint32_t MX_NOT_FINITE = 247;
 FP8MOE_DEV uint32_t mx_byte(float amax, float& mul) {
   const uint32_t b = max(__float_as_uint(amax) >> 23, 8u) - 8u;
   mul = __uint_as_float((254u - b) << 23);

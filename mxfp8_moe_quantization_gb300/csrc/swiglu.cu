@@ -18,7 +18,7 @@
 //
 // Bound by HBM: 6.06 bytes per element forward, 10.1 backward.  Measured: 36448
 // x 2048 in 256 groups forward, both directions, 72 us = 6.3 TB/s (94% of a
-// copy's rate); 51136 x 1408 backward 119 us = 6.1 TB/s (92%).  The first form,
+// copy's rate); 51136 x 1408 backward 120 us = 6.1 TB/s (91%).  The first form,
 // with every lane deriving every scale, expf and a division, and 45
 // instructions per element instead of about 20, took 152 and 283 us.
 #include "common.cuh"
@@ -38,31 +38,75 @@ namespace {
 constexpr int SG_ROWS = 32, SG_COLS = 64, SG_RW = 2, SG_CW = 2, SG_WARPS = SG_RW * SG_CW;
 constexpr int CW = 8;   // columns per lane
 
-// -g of a bf16 pair, cut to +-88, as fp32; NaN stays NaN
-FP8MOE_DEV uint64_t neg_cut(uint32_t g) {
-  uint32_t n;
-  asm("{\n .reg .b32 t;\n neg.bf16x2 t, %1;\n min.NaN.bf16x2 t, t, %2;\n max.NaN.bf16x2 %0, t, %3;\n}"
-      : "=r"(n)
-      : "r"(g), "r"(0x42B042B0u), "r"(0xC2B0C2B0u));
-  return unpk_bf16(n);
-}
-// sigmoid of a pair from n = -g: 1 / (1 + 2^t (1 + r)) with t = n / ln 2 rounded
-// and r the rest n - t ln 2, whose exponential is 1 + r (Cody and Waite's
-// two-part ln 2; |r| < 2^-17).  |g| is cut at 88, where the sigmoid is 1 or
-// below the normal range, so that nothing overflows.
-FP8MOE_DEV uint64_t sigmoid2(uint64_t n2) {
+// sigmoid of a pair g: 1 / D with D = 1 + 2^-t (1 - r), t = g / ln 2 rounded and
+// r the rest g - t ln 2, whose exponential is 1 + r (Cody and Waite's two-part
+// ln 2; |r| < 2^-17).  The reciprocal is that of D / 4, which is normal for
+// every finite D, with one step of Newton's iteration.  Where e^-g is not finite
+// (g below -88.72) the step's 0 * inf, and for g far up to the other side the
+// infinite t, leave NaN.  Mean relative error over all bf16 |g| in (2^-10, 80)
+// 3.36e-8; 1 / (1 + expf(-g)) with every step rounded 3.2e-8.
+FP8MOE_DEV uint64_t sigmoid2(uint64_t g2) {
   constexpr float L = 1.44269504f, LN2_HI = 0.693147182f, LN2_LO = -1.90465421e-9f;
-  const uint64_t t2 = mul2(n2, pk(L, L));
-  const uint64_t r2 = fma2(t2, pk(-LN2_LO, -LN2_LO), fma2(t2, pk(-LN2_HI, -LN2_HI), n2));
+  const uint64_t t2 = mul2(g2, pk(L, L));
+  const uint64_t r2 = fma2(t2, pk(-LN2_LO, -LN2_LO), fma2(t2, pk(-LN2_HI, -LN2_HI), g2));
   float t, u, x, y;
   unpk(t2, t, u);
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(t));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(u));
-  const uint64_t e2 = pk(x, y);
-  unpk(add2(fma2(e2, r2, e2), pk(1.0f, 1.0f)), x, y);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(x));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(y));
-  return pk(x, y);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(-t));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-u));
+  const uint64_t d2 = fma2(pk(x, y), fma2(r2, pk(0.25f, 0.25f), pk(-0.25f, -0.25f)), pk(-0.25f, -0.25f));   // -D / 4
+  unpk(d2, t, u);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(-t));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-u));
+  const uint64_t q2 = pk(x, y), s2 = mul2(q2, pk(0.25f, 0.25f));
+  return fma2(s2, fma2(d2, q2, pk(1.0f, 1.0f)), s2);
+}
+
+// A pair of results: v, and backward the gradient of gate in v, of up in v2.
+// Where sigmoid2 has no number, or a product of two inputs is beyond fp32, the
+// result is not finite, by which far_tiles knows it.
+template <bool BWD>
+FP8MOE_DEV void act_pair(uint32_t g, uint32_t u, uint32_t d, uint64_t& v, uint64_t& v2) {
+  const uint64_t g2 = unpk_bf16(g), s2 = sigmoid2(g2);
+  if constexpr (BWD) {
+    // 1 + g (1 - sig)
+    const uint64_t f2 = fma2(g2, fma2(s2, pk(-1.0f, -1.0f), pk(1.0f, 1.0f)), pk(1.0f, 1.0f));
+    v = mul2(mul2(mulx(d, u), s2), f2);
+    v2 = mul2(mulx(d, g), s2);
+  } else {
+    v = mul2(mulx(g, u), s2);
+  }
+}
+
+// The same for any inputs, from the sigmoid on in 64 bits.  Below -80 the
+// sigmoid is (e^(g/4))^4, whose factors are normal as long as a result can
+// differ from 0, and 0 where 64 bits have no number for it either.
+FP8MOE_DEV double far_sigmoid(float g) {
+  if (g < -745.0f) return 0.0;
+  if (!(g < -80.0f)) return (double)__frcp_rn(1.0f + expf(-g));
+  const double e = (double)expf(0.25f * fmaxf(g, -300.0f)), e2 = e * e;
+  return e2 * e2;
+}
+template <bool BWD>
+FP8MOE_DEV float far_one(float gate, float u, float d, float& du) {
+  const double s = far_sigmoid(gate), g = gate;
+  if constexpr (!BWD) return (float)(g * s * (double)u);
+  du = (float)((double)d * g * s);
+  return (float)((double)d * (double)u * s * (1.0 + g * (1.0 - s)));
+}
+FP8MOE_DEV bool finite2(uint64_t p) {
+  float a, b;
+  unpk(p, a, b);
+  return amax3(0.0f, a, b) <= 3.402823466e38f;
+}
+template <bool BWD>
+FP8MOE_DEV void far_pair(uint32_t g, uint32_t u, uint32_t d, uint64_t& v, uint64_t& v2) {
+  act_pair<BWD>(g, u, d, v, v2);
+  if (finite2(v) && (!BWD || finite2(v2))) return;
+  float x = 0.0f, y = 0.0f;
+  const float lo = far_one<BWD>(bf16_lo(g), bf16_lo(u), bf16_lo(d), x);
+  const float hi = far_one<BWD>(bf16_hi(g), bf16_hi(u), bf16_hi(d), y);
+  v = pk(lo, hi);
+  if constexpr (BWD) v2 = pk(x, y);
 }
 
 // The padded row (in a layout whose groups start at multiples of 128 rows) of
@@ -120,8 +164,8 @@ FP8MOE_DEV void halve(const float (&m)[N], float (&out)[N / 2], int lane, int ma
 // Where a warp's 32 rows go.  Scale bytes: row 8 rq + i, block c of s0 is at
 // s0 + i * step0 + off0(c); column c of s1 at s1 + off1(c).
 struct TilePlace {
-  int64_t row0;   // first row of the tile
-  int64_t W;      // columns of the result
+  int row0;       // first row of the tile
+  int W;          // columns of the result
   uint8_t *s0, *s1;
   int64_t step0;  // row-major: W / 32; tiled: 16
   int64_t band1;  // tiled s1: bytes of 128 of its rows; row-major: 0
@@ -132,18 +176,19 @@ FP8MOE_DEV void place_scales(const SwigluArgs& a, TilePlace& tp, int64_t prow0, 
                              int rq) {
   const bool t0 = a.s0_layout != FP8MOE_SCALES_ROWMAJOR, t1 = a.s1_layout != FP8MOE_SCALES_ROWMAJOR;
   tp.step0 = t0 ? 16 : tp.W / 32;
-  tp.s0 = a.s0 + (t0 ? tile_off(prow0, 0, cp0) : tp.row0 * (tp.W / 32)) + rq * 8 * tp.step0;
+  tp.s0 = a.s0 + (t0 ? tile_off(prow0, 0, cp0) : (int64_t)tp.row0 * (tp.W / 32)) + rq * 8 * tp.step0;
   tp.band1 = t1 ? cp1 * 128 : 0;
   tp.s1 = a.s1 + (t1 ? (pcol1 >> 2) * 512 + (pcol1 & 3) : tp.row0 / 32);
 }
 
 // One tile of results to every output.  v: rows 8 rq .. 8 rq + 7 and columns
 // CW cq .. of the tile, as column pairs; col0: the tile's first column; ok:
-// this lane's columns exist.
+// this lane's columns exist; top: the largest scale byte that the lane derived
+// (the lanes together derive every block's).
 FP8MOE_DEV void put_tile(const SwigluArgs& a, const TilePlace& tp, int64_t col0, bool ok, int lane,
-                         const uint64_t (&v)[8][CW / 2]) {
+                         const uint64_t (&v)[8][CW / 2], uint32_t& top) {
   const int rq = lane >> 3, cq = lane & 7;
-  const int64_t W = tp.W, col = col0 + cq * CW, rbase = tp.row0 + rq * 8;
+  const int64_t W = tp.W, col = col0 + cq * CW, rbase = (int64_t)tp.row0 + rq * 8;
   const int rows = rbase + 8 <= a.M ? 8 : rbase < a.M ? (int)(a.M - rbase) : 0;
   if (a.out && ok) {
     uint16_t* o = a.out + rbase * W + col;
@@ -153,6 +198,14 @@ FP8MOE_DEV void put_tile(const SwigluArgs& a, const TilePlace& tp, int64_t col0,
       *reinterpret_cast<uint4*>(o + i * W) = make_uint4(pack_bf16x2(v[i][0]), pack_bf16x2(v[i][1]),
                                                         pack_bf16x2(v[i][2]), pack_bf16x2(v[i][3]));
     }
+  }
+  if (!a.q0 && !a.q1) {
+    float m = 0.0f, s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int p = 0; p < CW / 2; ++p) m = amax3(m, v[i][p]);
+    top = max(top, mx_byte(m, s));
   }
   if (a.q0) {
     float m[8];
@@ -176,6 +229,7 @@ FP8MOE_DEV void put_tile(const SwigluArgs& a, const TilePlace& tp, int64_t col0,
     for (int s = 0; s < 2; ++s) {
       const uint32_t b = mx_byte(mk[s], mul[s]);
       const int i = own + s;
+      top = max(top, b);
       if (ok && i < rows) tp.s0[i * tp.step0 + c0] = (uint8_t)b;
     }
     uint8_t* q = a.q0 + rbase * W + col;
@@ -214,6 +268,7 @@ FP8MOE_DEV void put_tile(const SwigluArgs& a, const TilePlace& tp, int64_t col0,
     for (int s = 0; s < 2; ++s) {
       const uint32_t b = mx_byte(mk[s], mul[s]);
       const int64_t c = col + own + s;
+      top = max(top, b);
       if (ok)
         tp.s1[tp.band1 ? (c >> 7) * tp.band1 + (c & 31) * 16 + ((c >> 5) & 3) * 4 : c * (a.M / 32)] = (uint8_t)b;
     }
@@ -244,6 +299,56 @@ constexpr int warp_bytes() { return (BWD ? 3 : 2) * BOX_BYTES; }
 template <bool BWD>
 constexpr int cta_bytes() { return SG_WARPS * (warp_bytes<BWD>() + 8); }   // + a barrier per warp
 
+// A warp's `n` tiles from `row`, `col` on once more, if one of them has a result
+// that is not finite (gates below -88.72, NaN, infinities, products beyond
+// fp32): every result by far_pair, from memory, over what stands there (from the
+// same lane).  After the run, when nothing else is live: inside it, or with a
+// flag of its own beside the scale bytes, 51136 x 1408 backward took 131 to 152
+// us without any such tile.  With such gates in 1 column of 2048, 36448 rows
+// take 127 us forward instead of 76, 248 instead of 128 backward.
+template <bool BWD>
+FP8MOE_DEV void far_tiles(const SwigluArgs& a, TilePlace tp, int64_t row, int64_t col, int n, int col_end, int64_t cp0,
+                          int64_t cp1) {
+  const int lane = threadIdx.x & 31, rq = lane >> 3, cq = lane & 7;
+#pragma unroll 1
+  for (; n > 0 && row < a.M; --n) {
+    if (col < a.F) {
+      const int64_t pr = a.E0 + a.E1 > 0 ? padded_row(a.offs, a.E0 > 0 ? a.E0 : a.E1, a.M, row, lane) : row;
+      tp.row0 = (int)row;
+      place_scales(a, tp, a.E0 > 0 ? pr : row, (a.E1 > 0 ? pr : row) / 32, cp0, cp1, rq);
+      const int64_t c = col + cq * CW;
+      const bool ok = c < a.F;
+      uint64_t v[8][CW / 2], v2[BWD ? 8 : 1][CW / 2];
+      uint32_t top = 0;
+      // one pair at a time: 32 copies of far_pair do not stay in the instruction cache
+#pragma unroll 1
+      for (int k = 0; k < 8 * (CW / 2); ++k) {
+        const int64_t r = row + rq * 8 + k / (CW / 2), at = c + k % (CW / 2) * 2;
+        const bool on = ok && r < a.M;
+        auto pair = [&](const uint16_t* p) { return on ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u; };
+        uint64_t x, y;
+        far_pair<BWD>(pair(a.h + r * a.ldh + at), pair(a.h + r * a.ldh + a.F + at), BWD ? pair(a.dout + r * a.F + at) : 0u, x, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int p = 0; p < CW / 2; ++p) {
+            if (k != i * (CW / 2) + p) continue;
+            v[i][p] = x;
+            if constexpr (BWD) v2[i][p] = y;
+          }
+      }
+      put_tile(a, tp, col, ok, lane, v, top);
+      if constexpr (BWD) put_tile(a, tp, a.F + col, ok, lane, v2, top);
+    }
+    // the next tile of the run
+    col += SG_CW * SG_COLS;
+    if (col >= col_end) {
+      col -= col_end;
+      row += SG_RW * SG_ROWS;
+    }
+  }
+}
+
 // PF: a CTA walks a contiguous run of tiles, column tiles fastest, and each of
 // its warps has the next tile's boxes loaded by TMA while it works on the
 // current one from registers.  Without PF every CTA has one tile (few tiles:
@@ -258,12 +363,12 @@ FP8MOE_DEV void swiglu_body(const CUtensorMap* th, const CUtensorMap* td, const 
   // the CTA's run of tiles, and a tile's place stepped along it
   const int t0 = blockIdx.x * per, t1 = tiles - t0 < per ? tiles : t0 + per;
   struct Place {
-    int64_t row;
+    int row;
     int col;
   };
   auto first = [&](int t) {
     const int rb = t / col_tiles;
-    return Place{((int64_t)rb * SG_RW + warp % SG_RW) * SG_ROWS, ((t - rb * col_tiles) * SG_CW + warp / SG_RW) * SG_COLS};
+    return Place{(rb * SG_RW + warp % SG_RW) * SG_ROWS, ((t - rb * col_tiles) * SG_CW + warp / SG_RW) * SG_COLS};
   };
   const int col_end = col_tiles * SG_CW * SG_COLS;
   auto next = [&](Place p) {
@@ -294,11 +399,11 @@ FP8MOE_DEV void swiglu_body(const CUtensorMap* th, const CUtensorMap* td, const 
     __syncwarp();
   }
   TilePlace tp;
-  tp.W = BWD ? 2 * a.F : a.F;
+  tp.W = (int)(BWD ? 2 * a.F : a.F);
   tp.row0 = -1;
-  uint32_t parity = 0;
+  uint32_t parity = 0, top = 0;
   for (int t = t0; t < t1; ++t) {
-    const int64_t row0 = cur.row;
+    const int row0 = cur.row;
     if (row0 >= a.M) break;   // column tiles are fastest: the later tiles' rows are not lower
     const int64_t col0 = cur.col, col = col0 + cq * CW;
     cur = next(cur);
@@ -314,7 +419,7 @@ FP8MOE_DEV void swiglu_body(const CUtensorMap* th, const CUtensorMap* td, const 
       const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int64_t r = row0 + rq * 8 + i;
+        const int64_t r = (int64_t)row0 + rq * 8 + i;
         const bool on = ok && r < a.M;
         g[i] = on ? ld_nc16(a.h + r * a.ldh + col) : z;
         u[i] = on ? ld_nc16(a.h + r * a.ldh + a.F + col) : z;
@@ -355,15 +460,7 @@ FP8MOE_DEV void swiglu_body(const CUtensorMap* th, const CUtensorMap* td, const 
       const uint32_t dw[4] = {dq.x, dq.y, dq.z, dq.w};
 #pragma unroll
       for (int p = 0; p < CW / 2; ++p) {
-        const uint64_t n2 = neg_cut(gw[p]), s2 = sigmoid2(n2);
-        if constexpr (BWD) {
-          // 1 + g (1 - sig)
-          const uint64_t f2 = fma2(n2, add2(s2, pk(-1.0f, -1.0f)), pk(1.0f, 1.0f));
-          v[i][p] = mul2(mul2(mulx(dw[p], uw[p]), s2), f2);
-          v2[i][p] = mul2(mulx(dw[p], gw[p]), s2);
-        } else {
-          v[i][p] = mul2(mulx(gw[p], uw[p]), s2);
-        }
+        act_pair<BWD>(gw[p], uw[p], dw[p], v[i][p], v2[BWD ? i : 0][p]);
       }
     }
     if (PF) {
@@ -373,8 +470,12 @@ FP8MOE_DEV void swiglu_body(const CUtensorMap* th, const CUtensorMap* td, const 
         issue(cur);
       }
     }
-    put_tile(a, tp, col0, ok, lane, v);
-    if constexpr (BWD) put_tile(a, tp, a.F + col0, ok, lane, v2);
+    put_tile(a, tp, col0, ok, lane, v, top);
+    if constexpr (BWD) put_tile(a, tp, a.F + col0, ok, lane, v2, top);
+  }
+  if (__any_sync(0xffffffffu, top == MX_NOT_FINITE)) {
+    const Place p = first(t0);
+    far_tiles<BWD>(a, tp, p.row, p.col, t1 - t0, col_end, cp0, cp1);
   }
 }
 
