@@ -469,7 +469,10 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
       fence_proxy_async_smem();
       issue();
     }
-    const float c = -dot * rh;
+    // -dot / H, rounded once: the quotient by the reciprocal and one step of
+    // Markstein's correction, which an infinite sum has no use for
+    const float m = dot * rh, rest = fmaf(-m, (float)a.H, dot);
+    const float c = rest == rest ? -fmaf(rest, rh, m) : -m;
     const uint64_t c2 = pk(c, c);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
