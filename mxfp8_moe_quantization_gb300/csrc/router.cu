@@ -145,31 +145,42 @@ FP8MOE_DEV void load_row(const RouterArgs& a, int64_t t, int l, bool on, float (
 // 1 / (1 + e^-x), each step rounded to nearest (the choice with a bias hangs on it)
 FP8MOE_DEV float sigmoid_rn(float x) { return __frcp_rn(1.0f + expf(-x)); }
 
-// the same for the gradient: the reciprocal off by an ulp at most, without the
-// steps that round it
-FP8MOE_DEV float sigmoid_grad(float x) {
+// For the gradient both the sigmoid s and 1 - s, each to a few ulp: the smaller
+// of the two is t / (1 + t) with t = e^-|x|, and the other one 1 minus that.  The
+// smaller one is kept, with a sign where it is 1 - s.  (1 - s from a rounded s
+// is off by 5e-4 of itself at a logit of 10, and 0 from 17 on.)  The reciprocal
+// of 1 + t, which lies in [1, 2], takes one step of Newton's iteration.
+FP8MOE_DEV float sigmoid_side(float x) {
+  const float t = expf(-fabsf(x)), d = 1.0f + t;
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-x)));
-  return r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  r = fmaf(fmaf(-d, r, 1.0f), r, r);
+  return __int_as_float(__float_as_int(t * r) | (~__float_as_int(x) & 0x80000000));
 }
+FP8MOE_DEV float side_score(float q) { return __float_as_int(q) < 0 ? 1.0f + q : q; }   // s
+FP8MOE_DEV float side_rest(float q) { return __float_as_int(q) < 0 ? -q : 1.0f - q; }    // 1 - s
 
 // What turns a logit of the row into its score: softmax s = e^(x - m) / z;
 // z is also the sum of the sigmoids.
 struct RowStat {
-  float m, rz;   // rz = 1 / z, 0 for a row of nothing but -inf
+  float m, rz;   // rz = 1 / z, 0 for a row of nothing but -inf (or sigmoids whose sum has no reciprocal)
 };
 template <bool SIG, bool GRAD = false>
 FP8MOE_DEV float score_of(float x, const RowStat& st) {
-  return SIG ? (GRAD ? sigmoid_grad(x) : sigmoid_rn(x)) : expf(x - st.m) * st.rz;
+  return SIG ? (GRAD ? side_score(sigmoid_side(x)) : sigmoid_rn(x)) : expf(x - st.m) * st.rz;
 }
-// s: sigmoids, or the softmax's e^(x - m) before the division by z
+// s: sigmoids (GRAD: their sides), or the softmax's e^(x - m) before the division
+// by z
 template <int V, int G, bool SIG, bool GRAD = false>
 FP8MOE_DEV RowStat row_scores(const float (&x)[V], float (&s)[V]) {
   RowStat st{0.0f, 0.0f};
   float z = 0.0f;
   if constexpr (SIG) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) z += s[i] = GRAD ? sigmoid_grad(x[i]) : sigmoid_rn(x[i]);
+    for (int i = 0; i < V; ++i) {
+      s[i] = GRAD ? sigmoid_side(x[i]) : sigmoid_rn(x[i]);
+      z += GRAD ? side_score(s[i]) : s[i];
+    }
   } else {
     float m = NEG_INF;
 #pragma unroll
@@ -180,7 +191,7 @@ FP8MOE_DEV RowStat row_scores(const float (&x)[V], float (&s)[V]) {
     for (int i = 0; i < V; ++i) z += s[i] = expf(x[i] - st.m);
   }
   z = lane_sum<G>(z);
-  st.rz = z == 0.0f ? 0.0f : __frcp_rn(z);
+  st.rz = z < 2.9387359e-39f ? 0.0f : __frcp_rn(z);   // (below that 1 / z is beyond fp32, as for z = 0)
   return st;
 }
 
@@ -530,7 +541,7 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_bwd(RouterArgs 
     const RowStat st = row_scores<V, G, SIG, true>(x, s);
     float pc = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) pc = fmaf(s[i] * st.rz, c[i], pc);
+    for (int i = 0; i < V; ++i) pc = fmaf((SIG ? side_score(s[i]) : s[i]) * st.rz, c[i], pc);
     pc = lane_sum<G>(pc);
     float us = 0.0f;
     if (a.dw) {
@@ -576,8 +587,8 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_bwd(RouterArgs 
         }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          o[i] += s[p + i] * st.rz * (c[p + i] - pc - (SIG ? 0.0f : us));
-          if (SIG) o[i] *= 1.0f - s[p + i];
+          o[i] += (SIG ? side_score(s[p + i]) : s[p + i]) * st.rz * (c[p + i] - pc - (SIG ? 0.0f : us));
+          if (SIG) o[i] *= side_rest(s[p + i]);
         }
         if (P > 1 && a.wide) {
           if (e0 >= a.E) break;

@@ -1,0 +1,62 @@
+"""What the router's results hang on to the last bit: the sigmoid's slope where
+it is nearly one."""
+import numpy as np
+import pytest
+import torch
+
+from code_bounds import check_bf16
+from oracle import moe_ops as OM
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+REL = 1e-5   # see test_router_gpu
+
+
+@pytest.fixture(scope="module")
+def F():
+    from mxfp8_moe_quantization_gb300 import build as B
+    B.build()
+    import mxfp8_moe_quantization_gb300 as m
+    return m
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("T,E,k", [(5, 8, 2), (64, 64, 6), (300, 256, 8), (1400, 33, 4), (5000, 100, 9), (40, 700, 8)])
+@pytest.mark.parametrize("renorm,bf16", [(False, False), (True, False), (False, True)])
+def test_slope_of_confident_experts(F, T, E, k, renorm, bf16):
+    """The gradient carries the factor 1 - s, which is e^-x and not the
+    difference of two numbers near one: bounds on the terms with that factor."""
+    g = torch.Generator().manual_seed(T)
+    x = torch.rand(T, E, generator=g) * 16 + 4
+    far = torch.rand(T, E, generator=g)
+    x = torch.where(far < 0.2, -x, x)
+    x[torch.rand(T, E, generator=g) < 0.02] = 60.0
+    x[torch.rand(T, E, generator=g) < 0.02] = -95.0
+    x[0], x[1] = 18.0, torch.linspace(-90, 90, E)
+    x = x.to(torch.bfloat16) if bf16 else x
+    kw = dict(score=F.SCORE_SIGMOID, renormalize=renorm, route_scale=2.5)
+    idx, _, counts, _, _ = F.fp8moe_router_fwd(x.to(DEV), k, **kw)
+    dw = torch.randn(T, k, generator=g)
+    got = F.fp8moe_router_bwd(x.to(DEV), idx, counts, dw.to(DEV), torch.full((1,), 3.0, device=DEV), **kw)
+    ii, cc = idx.cpu().numpy().astype(np.int64), counts.cpu().numpy()[:E]
+    # 1 - s of the sigmoid in 64 bits is s of -x
+    s, p = OM.scores(_np(x), "sigmoid")
+    rest = OM.scores(-_np(x), "sigmoid")[0]
+    c = 3.0 * E / (k * T ** 2) * cc
+    r, size = p * (c - (p * c).sum(1, keepdims=True)), p * (c + (p * c).sum(1, keepdims=True))
+    sel, d = np.take_along_axis(s, ii, 1), _np(dw)
+    if renorm:
+        sel = sel / sel.sum(1, keepdims=True)
+    u = 2.5 * sel * (d - ((d * sel).sum(1, keepdims=True) if renorm else 0))
+    au = 2.5 * sel * (np.abs(d) + ((np.abs(d) * sel).sum(1, keepdims=True) if renorm else 0))
+    full, afull = np.zeros_like(s), np.zeros_like(s)
+    np.put_along_axis(full, ii, u, 1)
+    np.put_along_axis(afull, ii, au, 1)
+    ref, lim = rest * (r + full), 4 * REL * rest * (size + afull) + 1e-37
+    if bf16:
+        check_bf16(got, ref, lim, "dlogits")
+    else:
+        assert np.all(np.abs(_np(got) - ref) <= lim)
