@@ -163,17 +163,23 @@ FP8MOE_DEV float side_rest(float q) { return __float_as_int(q) < 0 ? -q : 1.0f -
 // What turns a logit of the row into its score: softmax s = e^(x - m) / z;
 // z is also the sum of the sigmoids.
 struct RowStat {
-  float m, rz;   // rz = 1 / z, 0 for a row of nothing but -inf (or sigmoids whose sum has no reciprocal)
+  float m, z, rz;   // rz = 1 / z, 0 for a row of nothing but -inf (or sigmoids whose sum has no reciprocal)
 };
+// e / z, rounded once: the quotient by the rounded reciprocal and one step of
+// Markstein's correction (e <= z; 0 where the reciprocal stands at 0)
+FP8MOE_DEV float over_z(float e, const RowStat& st) {
+  const float q = e * st.rz;
+  return fmaf(fmaf(-st.z, q, e), st.rz, q);
+}
 template <bool SIG, bool GRAD = false>
 FP8MOE_DEV float score_of(float x, const RowStat& st) {
-  return SIG ? (GRAD ? side_score(sigmoid_side(x)) : sigmoid_rn(x)) : expf(x - st.m) * st.rz;
+  return SIG ? (GRAD ? side_score(sigmoid_side(x)) : sigmoid_rn(x)) : over_z(expf(x - st.m), st);
 }
 // s: sigmoids (GRAD: their sides), or the softmax's e^(x - m) before the division
 // by z
 template <int V, int G, bool SIG, bool GRAD = false>
 FP8MOE_DEV RowStat row_scores(const float (&x)[V], float (&s)[V]) {
-  RowStat st{0.0f, 0.0f};
+  RowStat st{0.0f, 0.0f, 0.0f};
   float z = 0.0f;
   if constexpr (SIG) {
 #pragma unroll
@@ -190,7 +196,7 @@ FP8MOE_DEV RowStat row_scores(const float (&x)[V], float (&s)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) z += s[i] = expf(x[i] - st.m);
   }
-  z = lane_sum<G>(z);
+  st.z = z = lane_sum<G>(z);
   st.rz = z < 2.9387359e-39f ? 0.0f : __frcp_rn(z);   // (below that 1 / z is beyond fp32, as for z = 0)
   return st;
 }
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_fwd(RouterArgs 
     uint32_t key[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float p = s[i] * st.rz;
+      const float p = over_z(s[i], st);
       acc[i] += p;
       // dead experts stay below every other whatever their bias
       const float f = !a.bias ? x[i] : x[i] == NEG_INF ? NEG_INF : (SIG ? s[i] : p) + bias[i];
@@ -541,7 +547,7 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_bwd(RouterArgs 
     const RowStat st = row_scores<V, G, SIG, true>(x, s);
     float pc = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) pc = fmaf((SIG ? side_score(s[i]) : s[i]) * st.rz, c[i], pc);
+    for (int i = 0; i < V; ++i) pc = fmaf(over_z(SIG ? side_score(s[i]) : s[i], st), c[i], pc);
     pc = lane_sum<G>(pc);
     float us = 0.0f;
     if (a.dw) {
@@ -587,7 +593,7 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_bwd(RouterArgs 
         }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          o[i] += (SIG ? side_score(s[p + i]) : s[p + i]) * st.rz * (c[p + i] - pc - (SIG ? 0.0f : us));
+          o[i] += over_z(SIG ? side_score(s[p + i]) : s[p + i], st) * (c[p + i] - pc - (SIG ? 0.0f : us));
           if (SIG) o[i] *= side_rest(s[p + i]);
         }
         if (P > 1 && a.wide) {

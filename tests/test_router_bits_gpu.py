@@ -1,5 +1,5 @@
-"""What the router's results hang on to the last bit: the sigmoid's slope where
-it is nearly one."""
+"""What the router's results hang on to the last bit: the division by the scores'
+sum, and the sigmoid's slope where it is nearly one."""
 import numpy as np
 import pytest
 import torch
@@ -22,6 +22,21 @@ def F():
 
 def _np(t):
     return t.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("E,T", [(1, 9), (1, 4096), (7, 2000), (64, 4096), (100, 6000), (256, 300)])
+def test_the_only_live_expert_has_probability_one(F, E, T):
+    """s / s = 1 whatever s is: the sum over the tokens is their number, the
+    loss E N N / N^2, and its gradient p (c - p c) is zero."""
+    g = torch.Generator().manual_seed(E)
+    x = torch.full((T, E), -float("inf"))
+    x[:, E // 2] = torch.randn(T, generator=g) * 3
+    x = x.to(DEV)
+    idx, w, counts, psum, loss = F.fp8moe_router_fwd(x, 1, score=F.SCORE_SIGMOID)
+    assert bool((idx == E // 2).all()) and float(psum[E // 2]) == T and float(psum.sum()) == T and float(loss) == E
+    for xs in (x, x.to(torch.bfloat16)):
+        d = F.fp8moe_router_bwd(xs, idx, counts, None, torch.ones(1, device=DEV), score=F.SCORE_SIGMOID)
+        assert not d.any()
 
 
 @pytest.mark.parametrize("T,E,k", [(5, 8, 2), (64, 64, 6), (300, 256, 8), (1400, 33, 4), (5000, 100, 9), (40, 700, 8)])
