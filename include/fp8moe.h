@@ -511,7 +511,9 @@ fp8moe_status fp8moe_add_rmsnorm_bwd(const void* dy, const void* h, const float*
  * The k experts with the largest keys are chosen in descending order, ties
  * to the lowest id; the key is the logit, or s + bias (fp32) where a bias is
  * given.  Masked experts (and NaN logits) come last, so every token has k
- * different valid ids; a masked one has weight 0 and is not counted.
+ * different valid ids; a masked one has weight 0 and is not counted.  The ids
+ * and weights of a token depend on its own row alone: the same bits in any
+ * batch.  Every expert competes: no choice of groups of experts goes before.
  * topk_idx [T, k] int32, topk_w [T, k] fp32: s of the chosen experts, divided
  *         by their sum when renormalize is not 0 (a zero sum leaves zeros),
  *         times route_scale: the arguments of fp8moe_route_permute / _unpermute.

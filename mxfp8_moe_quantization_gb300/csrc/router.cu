@@ -17,9 +17,11 @@
 //
 // A warp takes a token, or several where experts are few and tokens many; a lane
 // has pieces of four neighbouring experts.  The logits are read once.
-// Sums over tokens have a fixed order (registers, then warps, then CTAs), so
-// results do not change from run to run.  The CTAs' partial sums are joined by
-// a second kernel of one cluster, launched ahead of the first one's end.
+// A row's sums have an order of their own, so that a token's choice and weights
+// do not depend on the batch.  Sums over tokens have a fixed order (registers,
+// then warps, then CTAs), so results do not change from run to run.  The CTAs'
+// partial sums are joined by a second kernel of one cluster, launched ahead of
+// the first one's end.
 //
 // Bound by latency, then by instruction issue (a token of 256 fp32 experts, top
 // 8: about 1100 warp instructions, half of them the rounds of the choice; bf16
@@ -160,6 +162,44 @@ FP8MOE_DEV float sigmoid_side(float x) {
 FP8MOE_DEV float side_score(float q) { return __float_as_int(q) < 0 ? 1.0f + q : q; }   // s
 FP8MOE_DEV float side_rest(float q) { return __float_as_int(q) < 0 ? -q : 1.0f - q; }    // 1 - s
 
+// A row's sum, in an order that hangs on the experts' numbers alone, whatever
+// lanes hold them (a token gets the same bits in any batch): bits 0 and 1 of the
+// number first, then from the highest bit down.  Experts past the last are 0.
+template <int V, int G>
+FP8MOE_DEV float row_sum(const float (&s)[V]) {
+  constexpr int P = piece<V>(), N = V / P;
+  float a[N];
+#pragma unroll
+  for (int p = 0; p < N; ++p) {
+    if constexpr (P == 4) a[p] = (s[4 * p] + s[4 * p + 1]) + (s[4 * p + 2] + s[4 * p + 3]);
+    if constexpr (P == 2) a[p] = s[2 * p] + s[2 * p + 1];
+    if constexpr (P == 1) a[p] = s[p];
+  }
+#pragma unroll
+  for (int h = N / 2; h > 0; h >>= 1)
+#pragma unroll
+    for (int p = 0; p < h; ++p) a[p] += a[p + h];
+  float v = a[0];
+  // the lanes that differ in bits 0 and 1 of the number, where a piece is short
+#pragma unroll
+  for (int o = 1; o < 4 / P; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+  for (int o = G / 2; o >= 4 / P; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// likewise over a token's slots, l, l + G, .., from the highest bit down
+template <int G, int S>
+FP8MOE_DEV float slot_sum(const float (&w)[S]) {
+  float a[S];
+#pragma unroll
+  for (int q = 0; q < S; ++q) a[q] = w[q];
+#pragma unroll
+  for (int h = S / 2; h > 0; h >>= 1)
+#pragma unroll
+    for (int q = 0; q < h; ++q) a[q] += a[q + h];
+  return lane_sum<G>(a[0]);
+}
+
 // What turns a logit of the row into its score: softmax s = e^(x - m) / z;
 // z is also the sum of the sigmoids.
 struct RowStat {
@@ -180,13 +220,9 @@ FP8MOE_DEV float score_of(float x, const RowStat& st) {
 template <int V, int G, bool SIG, bool GRAD = false>
 FP8MOE_DEV RowStat row_scores(const float (&x)[V], float (&s)[V]) {
   RowStat st{0.0f, 0.0f, 0.0f};
-  float z = 0.0f;
   if constexpr (SIG) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      s[i] = GRAD ? sigmoid_side(x[i]) : sigmoid_rn(x[i]);
-      z += GRAD ? side_score(s[i]) : s[i];
-    }
+    for (int i = 0; i < V; ++i) s[i] = GRAD ? sigmoid_side(x[i]) : sigmoid_rn(x[i]);
   } else {
     float m = NEG_INF;
 #pragma unroll
@@ -194,10 +230,17 @@ FP8MOE_DEV RowStat row_scores(const float (&x)[V], float (&s)[V]) {
     m = lane_max<G>(m);
     st.m = m == NEG_INF ? 0.0f : m;
 #pragma unroll
-    for (int i = 0; i < V; ++i) z += s[i] = expf(x[i] - st.m);
+    for (int i = 0; i < V; ++i) s[i] = expf(x[i] - st.m);
   }
-  st.z = z = lane_sum<G>(z);
-  st.rz = z < 2.9387359e-39f ? 0.0f : __frcp_rn(z);   // (below that 1 / z is beyond fp32, as for z = 0)
+  if constexpr (SIG && GRAD) {
+    float f[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = side_score(s[i]);
+    st.z = row_sum<V, G>(f);
+  } else {
+    st.z = row_sum<V, G>(s);
+  }
+  st.rz = st.z < 2.9387359e-39f ? 0.0f : __frcp_rn(st.z);   // (below that 1 / z is beyond fp32, as for z = 0)
   return st;
 }
 
@@ -363,7 +406,7 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_fwd(RouterArgs 
       choose<V, G, false>(key, my_e, a.k, l, a.two);
     }
     // lane l: the weights of slots l, l + G, .. from their logits
-    float w[S], z = 0.0f;
+    float w[S], z = 1.0f;
 #pragma unroll
     for (int q = 0; q < S; ++q) {
       w[q] = 0.0f;
@@ -372,10 +415,9 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_fwd(RouterArgs 
         w[q] = score_of<SIG>(xe, st);
         if (sums && xe != NEG_INF) atomicAdd(&cn[my_e[q]], 1);
       }
-      z += w[q];
     }
     if (a.renorm) {
-      z = lane_sum<G>(z);
+      z = slot_sum<G>(w);
       z = z == 0.0f ? 1.0f : z;
     }
 #pragma unroll
@@ -552,15 +594,14 @@ __global__ void __launch_bounds__(most_warps<V>() * 32) k_router_bwd(RouterArgs 
     float us = 0.0f;
     if (a.dw) {
       // the slots' scores, from the logits themselves
-      float u[S], z = 0.0f;
+      float u[S], sc[S];
 #pragma unroll
       for (int q = 0; q < S; ++q) {
-        const float sj = e[q] >= 0 ? score_of<SIG, true>(xj[q], st) : 0.0f;
-        z += sj;
-        u[q] = sj * (a.renorm ? 1.0f : dwj[q]);
+        sc[q] = e[q] >= 0 ? score_of<SIG, true>(xj[q], st) : 0.0f;
+        u[q] = sc[q] * (a.renorm ? 1.0f : dwj[q]);
       }
       if (a.renorm) {
-        z = lane_sum<G>(z);
+        const float z = slot_sum<G>(sc);
         float d = 0.0f;
 #pragma unroll
         for (int q = 0; q < S; ++q) {

@@ -1,5 +1,5 @@
-"""What the router's results hang on to the last bit: the division by the scores'
-sum, and the sigmoid's slope where it is nearly one."""
+"""What the router's results hang on to the last bit: the size of the batch, the
+division by the scores' sum, and the sigmoid's slope where it is nearly one."""
 import numpy as np
 import pytest
 import torch
@@ -22,6 +22,28 @@ def F():
 
 def _np(t):
     return t.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("E,k", [(3, 2), (8, 2), (8, 8), (16, 4), (20, 8), (31, 5), (33, 4), (64, 6), (64, 8), (100, 9),
+                                 (128, 16), (256, 8)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_a_token_does_not_depend_on_its_batch(F, E, k, score, bf16):
+    """A token's choice and weights have the same bits alone, among a few and
+    among many tokens."""
+    T = 5003
+    g = torch.Generator().manual_seed(E + k)
+    x = (torch.randn(T, E, generator=g) * 2).to(torch.bfloat16 if bf16 else torch.float32).to(DEV)
+    b = (torch.randn(E, generator=g) * 0.1).to(DEV)
+    sc = F.SCORE_SOFTMAX if score == "softmax" else F.SCORE_SIGMOID
+    for bias in (None, b):
+        for renorm in (False, True):
+            kw = dict(score=sc, renormalize=renorm, bias=bias, need_balance=False)
+            idx, w = F.fp8moe_router_fwd(x, k, **kw)[:2]
+            for n in (1, 37, 1250):
+                for at in range(0, T, n) if n > 1 else range(0, T, 101):
+                    i, v = F.fp8moe_router_fwd(x[at:at + n], k, **kw)[:2]
+                    assert torch.equal(i, idx[at:at + n]) and torch.equal(v, w[at:at + n])
 
 
 @pytest.mark.parametrize("E,T", [(1, 9), (1, 4096), (7, 2000), (64, 4096), (100, 6000), (256, 300)])
