@@ -880,9 +880,9 @@ def bench_rows(F, iters=30, only=None):
         lg, bias = torch.randn(T, E, device=dev), 0.05 * torch.randn(E, device=dev)
         fwd = lambda: F.fp8moe_router_fwd(lg, k, score=F.SCORE_SIGMOID, bias=bias)
         idx, wt, cnt, _, loss = fwd()
-        emit("ops", "k_router_fwd", f"dsv3 [{T},{E}] top {k}", timed(fwd), nbytes=T * (4 * E + 8 * k))
+        emit("ops", "k_router_fwd", f"[{T},{E}] top {k}, sigmoid and bias", timed(fwd), nbytes=T * (4 * E + 8 * k))
         ms = timed(lambda: F.fp8moe_router_bwd(lg, idx, cnt, wt, loss, score=F.SCORE_SIGMOID))
-        emit("ops", "k_router_bwd", f"dsv3 [{T},{E}] top {k}", ms, nbytes=T * (8 * E + 8 * k))
+        emit("ops", "k_router_bwd", f"[{T},{E}] top {k}", ms, nbytes=T * (8 * E + 8 * k))
         yr, do = rand(T * k, v3.K), rand(T, v3.K)
         row_of = torch.randperm(T * k, device=dev).reshape(T, k).to(torch.int32)
         ms = timed(lambda: F.fp8moe_route_weight_grad(do, yr, row_of))
