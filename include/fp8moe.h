@@ -486,7 +486,9 @@ fp8moe_status fp8moe_route_permute_noalloc(const void* x, int64_t T, int64_t H, 
  * counts as the identity.  workspace: caller-owned,
  * fp8moe_add_rmsnorm_bwd_workspace_bytes(T, H) bytes, 16-byte aligned; its
  * contents are of no use after the call.  Row sums and dw are added in a
- * fixed order: results do not change from run to run.
+ * fixed order: results do not change from run to run.  The order hangs on T and
+ * H, the forward's too (fewer rows than the device has SMs share out a row
+ * differently), so a row's last bits may differ between batches of other sizes.
  * ------------------------------------------------------------------------ */
 fp8moe_status fp8moe_add_rmsnorm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* w,
                                      int weight_type, int64_t T, int64_t H, float eps, void* h, void* y, float* rstd,
@@ -541,7 +543,8 @@ fp8moe_status fp8moe_add_rmsnorm_bwd(const void* dy, const void* h, const float*
  * rows y has: every number in row_of has to be below that, as for
  * fp8moe_route_unpermute.  fp8moe_route_weight_grad_bounded is the same with
  * that number (0 <= rows <= 2^31; y may be NULL where it is 0): a row number
- * outside [0, rows) gives 0 and nothing is read for it.
+ * outside [0, rows) gives 0 and nothing is read for it.  The order of a sum
+ * hangs on T, N and k.
  * ------------------------------------------------------------------------ */
 int64_t fp8moe_router_workspace_bytes(int64_t T, int64_t E);
 fp8moe_status fp8moe_router_fwd(const void* logits, int logits_type, int64_t T, int64_t E, int64_t ldl, int64_t k,

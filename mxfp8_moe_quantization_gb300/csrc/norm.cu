@@ -17,7 +17,7 @@
 // over many rows, streams them through a ring of bulk copies.  Measured (bytes
 // that the formulas cannot do without, of a copy's 6.68 TB/s): 16384 x 5120
 // with residual, bf16 and MXFP8 outputs 115 us (99%); 8191 x 4096 rowwise 41 us
-// (85%: two maxima a row); 16384 x 5120 backward 106 us (94%); one row of 7168
+// (85%: a sum and then a maximum a row); 16384 x 5120 backward 106 us (95%); one row of 7168
 // 3.0 us in a graph.  The first forms took 116, 46, 118 and 3.4 us.
 #include "common.cuh"
 #include "f32x2.cuh"

@@ -24,11 +24,11 @@
 // the first one's end.
 //
 // Bound by latency, then by instruction issue (a token of 256 fp32 experts, top
-// 8: about 1100 warp instructions, half of them the rounds of the choice; bf16
+// 8: about 1200 warp instructions, half of them the rounds of the choice; bf16
 // logits without a bias need one maximum a round instead of two reductions:
 // 65536 x 128, top 8, 31.4 us against 39.4).  In a graph: 4096 x 256, top 8,
-// 10.1 us forward with the sums and 5.8 without, 4.5 backward; 8192 x 64, top 6,
-// 7.4 and 3.4; 3 tokens 3.9.  The first form, which carried scores through the
+// 10.2 us forward with the sums and 6.0 without, 4.7 backward; 8192 x 64, top 6,
+// 7.2 and 3.3; 3 tokens 3.8.  The first form, which carried scores through the
 // rounds and joined 512 partial sums in one CTA, took 29.9 us on the first.
 #include "common.cuh"
 #include "f32x2.cuh"
