@@ -594,6 +594,42 @@ fp8moe_status fp8moe_swiglu_bwd(const void* dout, const void* h, int64_t ldh, in
                                 void* q1, uint8_t* s1, int s1_layout, fp8moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * The expert layer of a few tokens (decoding) in one launch, on the MXFP8
+ * weights of the grouped products:
+ *   out[t] = sum over j of w[t, j] * W2[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])),
+ *   e = topk_idx[t, j], W1 = gate rows, then up rows.
+ * x        [T, H] bf16, row stride ldx (>= H, a multiple of 8)
+ * topk_idx, topk_w [T, k] int32, fp32: the router's.  A choice whose weight is
+ *          0 (masked tokens and experts) or whose id is outside [0, E) (an
+ *          expert that another device holds) contributes nothing and its expert
+ *          is not read for it; a token without any gives a row of zeros.  The
+ *          same expert twice in a row counts twice.
+ * w1       [E, 2F, H] e4m3fn codes, w1_scale their e8m0 scales in the 128x4
+ *          layout (FP8MOE_NO_GROUPS, B = E): fp8moe_mxfp8_quantize_dual of the
+ *          bf16 weights, or fp8moe_mxfp8_quantize_dim0 and the swizzle
+ * w2       [E, H, F], w2_scale likewise
+ * out      [T, H] bf16, dense; overlaps no input
+ * Sums in fp32, in an order that hangs on the routing of the whole batch; x
+ * counts with all its digits and the activation to 2^-12 of itself: the output
+ * is rounded once.  The same call gives the
+ * same bits.  A value of x that is not finite makes its token's row NaN, a NaN
+ * weight those of the tokens that chose its expert; no other row.
+ * workspace: caller-owned, fp8moe_mxfp8_moe_decode_workspace_bytes bytes (-1 for
+ * sizes that are refused), 16-byte aligned, of no use after the call.
+ * T * k <= FP8MOE_DECODE_MAX_PAIRS (more: the grouped products), 1 <= E <=
+ * FP8MOE_MAX_GROUPS, H and F multiples of 32 up to 2^20.  An expert with more
+ * than 64 choices is read once per 64.  One cooperative launch of a CTA per SM:
+ * it starts once every SM can take one.  A wait inside it that exceeds its limit
+ * sets FP8MOE_ERR_TIMEOUT in the device status.
+ * ------------------------------------------------------------------------ */
+enum { FP8MOE_DECODE_MAX_PAIRS = 1024 };
+int64_t fp8moe_mxfp8_moe_decode_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F);
+fp8moe_status fp8moe_mxfp8_moe_decode(const void* x, int64_t ldx, const int32_t* topk_idx, const float* topk_w, int64_t T,
+                                      int64_t k, const void* w1, const uint8_t* w1_scale, const void* w2,
+                                      const uint8_t* w2_scale, int64_t E, int64_t H, int64_t F, void* out, void* workspace,
+                                      int64_t workspace_bytes, fp8moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Device status.  After the work already queued on `stream`, takes the
  * sticky device error code of the current device (an fp8moe_status value, 0
  * if none) and clears it in one atomic exchange on the device, then

@@ -37,12 +37,14 @@ __all__ = [
     "fp8moe_add_rmsnorm_fwd", "fp8moe_add_rmsnorm_bwd", "fp8moe_add_rmsnorm_bwd_workspace_bytes",
     "fp8moe_router_fwd", "fp8moe_router_bwd", "fp8moe_router_workspace_bytes", "fp8moe_route_weight_grad",
     "fp8moe_swiglu_fwd", "fp8moe_swiglu_bwd",
+    "DECODE_MAX_PAIRS", "fp8moe_mxfp8_moe_decode", "fp8moe_mxfp8_moe_decode_workspace_bytes",
 ]
 
 E4M3FN, E4M3FNUZ = 0, 1
 ROWWISE, MXFP8, TENSORWISE, BLOCKWISE = 0, 1, 2, 3
 SCALES_ROWMAJOR, NO_GROUPS, GROUP_ROWS, GROUP_COLS = -2, -1, 0, 1
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+DECODE_MAX_PAIRS = 1024                # tokens times choices of fp8moe_mxfp8_moe_decode
 ROUTE_STATIC_SCRATCH_BYTES = 1 << 20   # the static scratch of fp8moe_route_permute_noalloc
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -92,6 +94,9 @@ SYMBOLS = {
     "fp8moe_route_weight_grad_bounded": (_i32, [_vp, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp]),
     "fp8moe_swiglu_fwd": (_i32, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp]),
     "fp8moe_swiglu_bwd": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp]),
+    "fp8moe_mxfp8_moe_decode_workspace_bytes": (_i64, [_i64, _i64, _i64, _i64, _i64]),
+    "fp8moe_mxfp8_moe_decode": (_i32, [_vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64,
+                                       _vp]),
     "fp8moe_get_device_status": (_i32, [_vp, ctypes.POINTER(ctypes.c_int32)]),
     "fp8moe_testing_stall_next_gemm": (_i32, []),
     "fp8moe_testing_stall_next_tensorwise": (_i32, []),
@@ -636,6 +641,23 @@ def fp8moe_swiglu_bwd(dout, h, offs=None, s0_layout: int = NO_GROUPS, s1_layout:
         raise Fp8MoeError("fp8moe_swiglu_bwd", 1)
     return _run("fp8moe_swiglu_bwd", stream, _native().swiglu, dout, h, offs, s0_layout, s1_layout, need_dh, dim0, dim1, out, q0,
                 s0, q1, s1)
+
+
+def fp8moe_mxfp8_moe_decode_workspace_bytes(T: int, k: int, E: int, H: int, F: int) -> int:
+    """Bytes of the workspace of fp8moe_mxfp8_moe_decode (-1 for unsupported sizes)."""
+    return int(_lib_raw().fp8moe_mxfp8_moe_decode_workspace_bytes(T, k, E, H, F))
+
+
+def fp8moe_mxfp8_moe_decode(x, topk_idx, topk_w, w1, w1_scale, w2, w2_scale, out=None, workspace=None, stream=None):
+    """The expert layer of a few tokens (T * k <= DECODE_MAX_PAIRS) in one launch.
+
+    x [T, H] bf16 (the row stride may exceed H), topk_idx [T, k] int32 and
+    topk_w [T, k] fp32 as the router gives them (weight 0 or an id outside
+    [0, E): no contribution), w1 [E, 2F, H] (gate rows, then up rows) and w2
+    [E, H, F] e4m3 codes (uint8) with their scales in the 128x4 layout
+    (fp8moe_mxfp8_quantize_dual's q0, s0) -> out [T, H] bf16."""
+    return _run("fp8moe_mxfp8_moe_decode", stream, _native().moe_decode, x, topk_idx, topk_w, w1, w1_scale, w2, w2_scale, out,
+                workspace)
 
 
 def fp8moe_get_device_status(stream=None) -> int:

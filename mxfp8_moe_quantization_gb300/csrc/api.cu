@@ -664,6 +664,42 @@ fp8moe_status fp8moe_swiglu_bwd(const void* dout, const void* h, int64_t ldh, in
   return swiglu(true, dout, h, ldh, M, F, offs, E, dh, q0, s0, s0_layout, q1, s1, s1_layout, stream);
 }
 
+static bool decode_sizes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F) {
+  return T >= 0 && k >= 1 && T <= fp8moe::DECODE_MAX_PAIRS / k && E >= 1 && E <= FP8MOE_MAX_GROUPS && H >= 32 && F >= 32 &&
+         H <= ((int64_t)1 << 20) && F <= ((int64_t)1 << 20) && fp8moe::decode_fits(T * k, E, H, F);
+}
+
+int64_t fp8moe_mxfp8_moe_decode_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F) {
+  if (!decode_sizes(T, k, E, H, F) || H % 32 || F % 32) return -1;
+  return fp8moe::decode_workspace_bytes(T * k, H, F);
+}
+
+fp8moe_status fp8moe_mxfp8_moe_decode(const void* x, int64_t ldx, const int32_t* topk_idx, const float* topk_w, int64_t T,
+                                      int64_t k, const void* w1, const uint8_t* w1_scale, const void* w2,
+                                      const uint8_t* w2_scale, int64_t E, int64_t H, int64_t F, void* out, void* workspace,
+                                      int64_t workspace_bytes, fp8moe_stream_t stream) {
+  if (!decode_sizes(T, k, E, H, F) || ldx < H) return FP8MOE_ERR_INVALID_ARG;
+  if (H % 32 || F % 32 || ldx % 8) return FP8MOE_ERR_ALIGNMENT;
+  if (T == 0) return FP8MOE_OK;
+  if (!x || !topk_idx || !topk_w || !w1 || !w1_scale || !w2 || !w2_scale || !out || !workspace)
+    return FP8MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < fp8moe::decode_workspace_bytes(T * k, H, F)) return FP8MOE_ERR_INVALID_ARG;
+  if (!al16(x) || !al16(w1) || !al16(w1_scale) || !al16(w2) || !al16(w2_scale) || !al16(out) || !al16(workspace) ||
+      (((uintptr_t)topk_idx | (uintptr_t)topk_w) & 3))
+    return FP8MOE_ERR_ALIGNMENT;
+  DevInfo* d;
+  fp8moe_status st = device_info(&d);
+  if (st) return st;
+  fp8moe::DecodeArgs a{};
+  a.x = (const uint16_t*)x, a.ldx = ldx;
+  a.T = (int)T, a.k = (int)k, a.E = (int)E, a.H = (int)H, a.F = (int)F;
+  a.idx = topk_idx, a.w = topk_w;
+  a.q1 = (const uint8_t*)w1, a.s1 = w1_scale, a.q2 = (const uint8_t*)w2, a.s2 = w2_scale;
+  a.out = (uint16_t*)out;
+  a.status = d->status;
+  return cuda_result(fp8moe::launch_decode(a, workspace, d->num_sms, d->max_smem, (cudaStream_t)stream));
+}
+
 fp8moe_status fp8moe_get_device_status(fp8moe_stream_t stream, int32_t* out_code) {
   if (!out_code) return FP8MOE_ERR_INVALID_ARG;
   DevInfo* d;

@@ -367,6 +367,31 @@ PyObject* swiglu(PyObject* const* a) {
   return give_all(out, q0, s0, q1, s1);
 }
 
+// x, topk_idx, topk_w, w1, w1_scale, w2, w2_scale, out, workspace
+PyObject* moe_decode(PyObject* const* a) {
+  const Tensor &x = tensor(a[0]), &idx = tensor(a[1]), &w1 = tensor(a[3]), &w2 = tensor(a[5]);
+  if (x.dim() != 2 || idx.dim() != 2 || w1.dim() != 3 || w2.dim() != 3) refuse();
+  const int64_t T = x.size(0), H = x.size(1), k = idx.size(1), E = w2.size(0), F = w2.size(2);
+  Call c(x);
+  int64_t ldx = 0, nbytes = fp8moe_mxfp8_moe_decode_workspace_bytes(T, k, E, H, F);
+  const void* px = c.rows(x, at::kBFloat16, {T, H}, ldx);
+  const void* pi = c.dense(idx, at::kInt, {T, k});
+  const void* pw = c.dense(tensor(a[2]), at::kFloat, {T, k});
+  const void* p1 = c.dense(w1, at::kByte, {E, 2 * F, H});
+  const void* p2 = c.dense(w2, at::kByte, {E, H, F});
+  const Tensor &t1 = tensor(a[4]), &t2 = tensor(a[6]);
+  if (t1.numel() < fp8moe_swizzled_scales_bytes(E, 2 * F, H / 32, 0, FP8MOE_NO_GROUPS) ||
+      t2.numel() < fp8moe_swizzled_scales_bytes(E, H, F / 32, 0, FP8MOE_NO_GROUPS))
+    refuse();
+  const void *s1 = c.dense(t1, at::kByte, t1.sizes()), *s2 = c.dense(t2, at::kByte, t2.sizes());
+  Tensor out, ws;
+  void* po = c.out(out, a[7], at::kBFloat16, {T, H});
+  void* pws = c.workspace(ws, a[8], nbytes);
+  check(fp8moe_mxfp8_moe_decode(px, ldx, (const int32_t*)pi, (const float*)pw, T, k, p1, (const uint8_t*)s1, p2,
+                                (const uint8_t*)s2, E, H, F, po, pws, nbytes, c.stream()));
+  return give(out);
+}
+
 // The Python entry of F with N positional arguments; no C++ exception leaves it.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -390,6 +415,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 PyMethodDef methods[] = {FP8MOE_ENTRY(add_rmsnorm_fwd, 14),   FP8MOE_ENTRY(add_rmsnorm_bwd, 8),
                          FP8MOE_ENTRY(router_fwd, 14),        FP8MOE_ENTRY(router_bwd, 10),
                          FP8MOE_ENTRY(route_weight_grad, 4),  FP8MOE_ENTRY(swiglu, 13),
+                         FP8MOE_ENTRY(moe_decode, 9),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -51,4 +51,25 @@ struct SwigluArgs {
   int stall;             // test hook: the first CTA's first warp never loads its first tile
 };
 
+// The expert layer of a few tokens (decode.cu).
+constexpr int DECODE_MAX_PAIRS = 1024;      // T * k
+constexpr int DECODE_ENTRY_PAIRS = 64;      // pairs that one reading of an expert serves
+constexpr int DECODE_MIN_RUN = 4;           // pieces a CTA takes at least: fewer CTAs, fewer partial sums
+constexpr int DECODE_MAX_CTAS = 160;        // the workspace is sized for as many
+constexpr int DECODE_MEETS_BYTES = 512;     // three counters, 128 bytes apart
+struct DecodeArgs {
+  const uint16_t* x;     // [T, H] bf16, row stride ldx
+  int64_t ldx;
+  int T, k, E, H, F;
+  int P, max_ent;        // pairs, entries at most
+  const int32_t* idx;    // [T, k]
+  const float* w;        // [T, k]
+  const uint8_t *q1, *s1, *q2, *s2;
+  uint16_t* out;         // [T, H]
+  uint32_t* meets;
+  float *part, *act;     // partial sums [parts][live pairs][rows]; activations [live pairs][F]
+  int* status;
+  int stall;             // test hook: the first CTA never loads its first piece
+};
+
 }  // namespace fp8moe

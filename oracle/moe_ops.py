@@ -140,3 +140,32 @@ def swiglu_grad(dout, h):
     g, u = np.split(_f64(h), 2, axis=1)
     d, s = _f64(dout), _sig(g)
     return np.concatenate([d * u * s * (1.0 + g * (1.0 - s)), d * g * s], axis=1)
+
+
+# --- the expert layer of a few tokens ---------------------------------------------
+
+def moe_decode(x, idx, w, w1, w2, gamma: float = 0.0, act_rel: float = 0.0):
+    """(out [T, H], bound): sum_j w[t, j] W2[e] swiglu(W1[e] x[t]) over the choices
+    with 0 <= e < E and w != 0; w1 [E, 2F, H], w2 [E, H, F] values.  ``bound``:
+    how far out may be off when every sum of products is known to gamma times
+    the sum of their magnitudes and the activation to act_rel of itself."""
+    x, w = _f64(x), _f64(w)
+    T, H = x.shape
+    E, _, F = w2.shape
+    out, bound = np.zeros((T, H)), np.zeros((T, H))
+    for e in range(E):
+        t, j = np.nonzero((idx == e) & (w != 0))
+        if not len(t):
+            continue
+        gu = x[t] @ w1[e].T
+        d = gamma * (np.abs(x[t]) @ np.abs(w1[e]).T)
+        g, u = gu[:, :F], gu[:, F:]
+        with np.errstate(over="ignore", invalid="ignore"):
+            s = g * _sig(g)
+        a = s * u
+        # |d silu| <= 1.1
+        da = 1.1 * d[:, :F] * (np.abs(u) + d[:, F:]) + np.abs(s) * d[:, F:] + act_rel * np.abs(a)
+        y, dy = a @ w2[e].T, (da + gamma * np.abs(a)) @ np.abs(w2[e]).T
+        np.add.at(out, t, w[t, j][:, None] * y)
+        np.add.at(bound, t, np.abs(w[t, j])[:, None] * (dy + gamma * np.abs(y)))
+    return out, bound
