@@ -18,10 +18,12 @@
 // Both products are one stream of 16 KB pieces (128 rows x 128 of K) over all
 // (expert, row tile, k) in order, cut into equal runs, one per CTA; a tile's
 // partial sums (fp32, at most a few per tile) go to the workspace and are added
-// in order after a grid-wide meeting.  The producer does not take part in the
-// meetings: while the others add, it fills its ring with W2.
-//   warps 0-3   accumulators to partial sums;  4  weights by TMA;  5  MMA issue;
-//   warps 6-13  the tokens' terms, one group of four warps a piece in turn.
+// in order after a grid-wide meeting.  The terms are made once, into the
+// workspace, as the tensor core reads them (128-byte swizzle, 128x4 scales): a
+// piece's share of them is one bulk copy.  The weights' producer takes no part in
+// the meetings: while the others add, it fills its ring with W2.
+//   warps 0-3  accumulators to partial sums;  4  weights by TMA;  5  MMA issue;
+//   6  terms and scales to shared memory;  0-3 and 7-13  terms, sums, results.
 #include <cooperative_groups.h>
 #include <cuda.h>
 
@@ -37,8 +39,8 @@ namespace fp8moe {
 namespace {
 
 constexpr int DC_THREADS = 448;
-constexpr int DC_JOIN = 384;              // threads that add partial sums: all but the producer's and the issuer's
 constexpr int DC_WARP_TMA = 4, DC_WARP_MMA = 5, DC_WARP_B = 6;
+constexpr int DC_JOIN = DC_THREADS - 96;  // threads that make terms and add partial sums: all but those three warps'
 constexpr int DC_A_BYTES = 128 * 128;
 constexpr int DC_NB = DECODE_ENTRY_PAIRS;   // pairs of one entry: a pass over an expert's weights
 constexpr int DC_ACC = 3 * DC_NB;         // TMEM columns of an accumulator
@@ -49,10 +51,11 @@ constexpr int DC_DEAD = 0xFFFF;
 
 __host__ __device__ constexpr int up16(int v) { return (v + 15) / 16 * 16; }
 
-// Shared memory: rings of weights (sa slots) and of terms (sb slots), the plan.
+// Shared memory: the ring of weights (sa slots, at 0), that of terms with the
+// terms' and the weights' scales (sb slots each), the plan.
 struct DecodeSmem {
   int sa, sb, b_bytes, sfb_bytes;
-  int sfa, b, sfb, bars, plan, total;     // the weights' ring is at 0
+  int sfa, b, sfb, bars, plan, total;
 };
 
 // The plan of a call, in shared memory: the live pairs (token, choice) in the
@@ -189,32 +192,45 @@ struct Stream {
   FP8MOE_DEV int parts(uint32_t tile) const { return (int)(owner(tile * kt + kt - 1) - owner(tile * kt)) + 1; }
 };
 
-// A CTA's place in a stream, stepped piece by piece.
-struct Walk {
-  uint32_t left;      // pieces to go in this run
-  int ent, row, k;    // entry, row tile, piece of K
-  uint32_t tile;
-  FP8MOE_DEV Walk(const Stream& s, uint32_t cta) {
-    const uint32_t lo = s.first(cta), hi = s.first(cta + 1);
-    left = hi - lo;
+// A CTA's run of a stream, segment by segment: the pieces of one tile that are
+// in the run.
+struct Run {
+  uint32_t left, tile;   // pieces to go, this segment's among them; row tile over all entries
+  int n, k;              // pieces of this segment, the first one's place along K
+  int ent, row;
+  FP8MOE_DEV Run(const Stream& s, uint32_t cta) {
+    const uint32_t lo = s.first(cta);
+    left = s.first(cta + 1) - lo;
     tile = lo / s.kt;
     k = (int)(lo - tile * s.kt);
     ent = (int)(tile / s.rt);
     row = (int)(tile - (uint32_t)ent * s.rt);
+    n = (int)min(left, (uint32_t)(s.kt - k));
   }
-  FP8MOE_DEV bool last(const Stream& s) const { return left == 1 || k == s.kt - 1; }   // of its tile, in this run
-  FP8MOE_DEV void step(const Stream& s) {
-    --left;
-    if (++k == s.kt) {
-      k = 0;
-      ++tile;
-      if (++row == s.rt) row = 0, ++ent;
-    }
+  FP8MOE_DEV void next(const Stream& s) {
+    left -= n;
+    k = 0;
+    ++tile;
+    if (++row == s.rt) row = 0, ++ent;
+    n = (int)min(left, (uint32_t)s.kt);
   }
 };
 
-FP8MOE_DEV void cp_scales(uint32_t taddr, uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+// A place in a ring and the parity of its turn.
+struct Slot {
+  int i = 0;
+  uint32_t turn = 0;
+  FP8MOE_DEV void step(int by, int size) {
+    i += by;
+    if (i >= size) i -= size, turn ^= 1u;
+  }
+};
+
+// descriptor of a 128x4 scale tile: 32 rows of 16 bytes, no swizzle
+FP8MOE_DEV uint64_t sdesc_scales(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
+FP8MOE_DEV void cp_scales(uint32_t taddr, uint64_t d) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d));
 }
 FP8MOE_DEV void mma_mx1(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accum) {
@@ -234,17 +250,20 @@ FP8MOE_DEV uint32_t ld_acquire_gpu(const uint32_t* p) {
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-// one CTA more at a meeting, and the (bounded) wait for the others; one thread
-FP8MOE_DEV void meet(uint32_t* count, uint32_t n, int* status, volatile int* abort_flag) {
-  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
+// One CTA more at a meeting; the (bounded) wait until all have come.  One thread.
+// (A CTA whose own wait ran out still comes: the limit is twice that.)
+FP8MOE_DEV void come(uint32_t* count) { asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory"); }
+FP8MOE_DEV bool came(const uint32_t* count, uint32_t n, int* status, volatile int* abort_flag) {
+  if (ld_acquire_gpu(count) >= n) return true;
   const uint64_t t0 = globaltimer();
   while (ld_acquire_gpu(count) < n) {
-    if (globaltimer() - t0 > 2 * WAIT_LIMIT_NS) {   // (a CTA whose own wait ran out still comes)
+    if (globaltimer() - t0 > 2 * WAIT_LIMIT_NS) {
       set_status(status, FP8MOE_ERR_TIMEOUT);
       *abort_flag = 1;
-      return;
+      return false;
     }
   }
+  return true;
 }
 
 // two e4m3 codes -> their values
@@ -256,9 +275,9 @@ FP8MOE_DEV float2 e4m3x2_value(uint32_t c) {
   return v;
 }
 
-// Eight neighbouring values of a row to NT terms each (rows r0 .. of the term
-// tile, 128-byte swizzle; scale bytes in 128x4 order).  Four lanes hold a block.
-// A block that is not finite becomes NaN, and so does its token.
+// Eight neighbouring values of a row, place 8 j in the piece, to NT terms each:
+// rows r0 .. of the piece's tile.  Four lanes hold a block.  A block that is not
+// finite becomes NaN, and so does its token.
 template <int NT>
 FP8MOE_DEV void put_terms(float (&v)[8], uint8_t* tile, uint8_t* sf, int r0, int j, bool on) {
   float m = 0.0f;
@@ -323,7 +342,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   if (warp == DC_WARP_TMA && lane == 0) {
     abort_s = 0;
     for (int i = 0; i < L.sa; ++i) mbar_init(&a_full[i], 1), mbar_init(&a_empty[i], 1);
-    for (int i = 0; i < L.sb; ++i) mbar_init(&b_full[i], 4), mbar_init(&b_empty[i], 1);
+    for (int i = 0; i < L.sb; ++i) mbar_init(&b_full[i], 1), mbar_init(&b_empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 4);
     mbar_init(drain, 1);
     mbar_fence_init();
@@ -335,46 +354,78 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   }
   if (cta == 0 && tid < 3) a.meets[tid * 32] = 0;
   if (a.P <= 32) {
-    if (warp == DC_WARP_TMA) plan_warp(a, pl, lane);
+    if (warp == DC_WARP_TMA) {
+      plan_warp(a, pl, lane);
+      asm volatile("bar.arrive 3, %0;" ::"n"(DC_THREADS) : "memory");
+    } else {
+      bar_sync(3, DC_THREADS);
+    }
   } else {
     plan_block(a, pl, (int*)(smem + L.b));   // (ends with a block barrier)
   }
 
-  // ---- the producer's first ring fills leave before the grid meets
-  // (piece i of the CTA's two runs goes to slot i % sa)
-  uint32_t issued = 0;
-  auto produce = [&](const Stream& s1, const Stream& s2, Walk& w1, Walk& w2, uint32_t upto) {
-    for (; issued < upto; ++issued) {
-      const bool one = w1.left > 0;
-      const Stream& s = one ? s1 : s2;
-      Walk& w = one ? w1 : w2;
-      const int slot = (int)(issued % (uint32_t)L.sa);
-      const uint32_t turn = issued / (uint32_t)L.sa;
-      if (!mbar_wait(&a_empty[slot], (turn & 1u) ^ 1u, abort_flag)) {
-        fail();
-        return;
-      }
-      const int e = (int)(pl.ent[w.ent] & 1023u);
-      if (!(a.stall && cta == 0 && issued == 0)) {
-        mbar_expect_tx(&a_full[slot], DC_A_BYTES + 512);
-        tma_load_3d(smem + slot * DC_A_BYTES, one ? &tm1 : &tm2, &a_full[slot], w.k * 128, w.row * 128, e);
-        bulk_load(smem + L.sfa + slot * 512, (one ? a.s1 : a.s2) + (((int64_t)e * s.rt + w.row) * s.kt + w.k) * 512, 512,
-                  &a_full[slot]);
-      }
-      w.step(s);
-    }
-  };
   const int K1 = a.H, K2 = a.F, R1 = 2 * a.F, R2 = a.H;
   const int rt1 = (R1 + 127) / 128, kt1 = (K1 + 127) / 128, rt2 = (R2 + 127) / 128, kt2 = (K2 + 127) / 128;
-  if (warp == DC_WARP_TMA && lane == 0) {
-    const int ne = pl.num[1];
-    const Stream s1(ne, rt1, kt1, grid), s2(ne, rt2, kt2, grid);
-    Walk w1(s1, cta), w2(s2, cta);
-    const uint32_t all = w1.left + w2.left;
-    produce(s1, s2, w1, w2, all < (uint32_t)L.sa ? all : (uint32_t)L.sa);
+  // ---- weights: a ring fill per piece, of the first product's run and then of
+  // the second's; `first` fills leave before the grid meets
+  auto produce = [&](uint32_t from, uint32_t upto) {
+    Slot slot;
+    uint32_t i = 0;
+    for (int ph = 0; ph < 2; ++ph) {
+      const Stream s(pl.num[1], ph ? rt2 : rt1, ph ? kt2 : kt1, grid);
+      const CUtensorMap* tm = ph ? &tm2 : &tm1;
+      for (Run r(s, cta); r.left > 0; r.next(s)) {
+        if (i >= upto) return i;
+        const int e = (int)(pl.ent[r.ent] & 1023u);
+        int x = r.k * 128;
+        for (int c = 0; c < r.n; ++c, ++i, x += 128, slot.step(1, L.sa)) {
+          if (i < from) continue;
+          if (i >= upto) return i;
+          uint64_t* bar = &a_full[slot.i];
+          if (!mbar_wait(&a_empty[slot.i], slot.turn ^ 1u, abort_flag)) {
+            fail();
+            return i;
+          }
+          if (a.stall && cta == 0 && i == 0) continue;
+          mbar_expect_tx(bar, DC_A_BYTES);
+          tma_load_3d(smem + slot.i * DC_A_BYTES, tm, bar, x, r.row * 128, e);
+        }
+      }
+    }
+    return i;
+  };
+  uint32_t issued = 0;
+  const bool epi = warp < 4, joins = epi || warp > DC_WARP_B;
+  const int jt = epi ? tid : tid - 96;             // thread among those that make terms and add
+  // a piece's terms and their scales in the workspace
+  auto tile_of = [&](uint32_t ent, int c, int kt, int nt) {
+    return a.terms + ((int64_t)(ent >> 10 & 1023u) * kt + (int64_t)c * (int)(ent >> 20)) * nt * 128;
+  };
+  auto sf_of = [&](int e, int c, int kt) { return a.term_scales + ((int64_t)e * kt + c) * L.sfb_bytes; };
+  if (warp == DC_WARP_TMA) {
+    if (lane == 0) issued = produce(0, (uint32_t)L.sa);
+    __syncwarp();
+  } else if (joins) {
+    // the first product's terms: sixteen threads a pair's piece
+    const int units = pl.num[0] * kt1, step = (int)grid * (DC_JOIN / 16), j = jt & 15;
+    for (int u = (jt >> 4) * (int)grid + (int)cta; u - (jt >> 4 & 1) * (int)grid < units; u += step) {
+      const bool on = u < units;                    // (a warp has two pieces, and shuffles)
+      const int place = on ? u / kt1 : 0, c = on ? u - place * kt1 : 0, k = c * 128 + j * 8;
+      const int e = pl.ent_of[place];
+      const uint32_t ent = pl.ent[e];
+      const bool in = on && k < K1;
+      float v[8] = {};
+      if (in) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)(pl.order[place] / a.k) * a.ldx + k));
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
+      }
+      put_terms<2>(v, tile_of(ent, c, kt1, 2), sf_of(e, c, kt1), (place - (int)(ent >> 10 & 1023u)) * 2, j, in);
+    }
+    asm volatile("fence.proxy.async;" ::: "memory");   // bulk copies of other CTAs read them
   }
-  __syncwarp();
-  // the meetings' counters are zero, the barriers exist, the plan is made
+  // the meetings' counters are zero, the barriers exist, the plan and the first terms are made
   cooperative_groups::this_grid().sync();
   tc_fence_after();
   const uint32_t tmem = tmem_s;
@@ -384,10 +435,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   if (warp == DC_WARP_TMA) {
     // ======================= weights =======================
     if (lane == 0) {
-      Walk w1(s1, cta), w2(s2, cta);
-      const uint32_t all = w1.left + w2.left;
-      for (uint32_t i = 0; i < issued; ++i) w1.left > 0 ? w1.step(s1) : w2.step(s2);
-      produce(s1, s2, w1, w2, all);
+      issued = produce(issued, UINT32_MAX);
       // no copy stays in flight after a wait that ran out
       if (*abort_flag)
         for (uint32_t i = issued > (uint32_t)L.sa ? issued - L.sa : 0; i < issued; ++i)
@@ -397,154 +445,132 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   } else if (warp == DC_WARP_MMA) {
     // ======================= products =======================
     if (lane == 0) {
-      uint32_t n = 0, seg = 0;
+      Slot sa, sb, acc;
+      const uint64_t ad0 = sdesc_sw128(smem_u32(smem)), bd0 = sdesc_sw128(smem_u32(smem + L.b));
+      const uint64_t sfa0 = sdesc_scales(smem_u32(smem + L.sfa)), sfb0 = sdesc_scales(smem_u32(smem + L.sfb));
       bool ok = true;
       for (int ph = 0; ph < 2 && ok; ++ph) {
         const Stream& s = ph ? s2 : s1;
-        const int K = ph ? K2 : K1, terms = ph ? 3 : 2;
-        bool fresh = true;
-        for (Walk w(s, cta); w.left > 0; w.step(s), ++n) {
-          const int sa = (int)(n % (uint32_t)L.sa), sb = (int)(n % (uint32_t)L.sb);
-          if (fresh && !mbar_wait(&acc_empty[seg & 1], ((seg >> 1) & 1u) ^ 1u, abort_flag)) ok = false;
-          if (!ok || !mbar_wait(&a_full[sa], (n / (uint32_t)L.sa) & 1u, abort_flag) ||
-              !mbar_wait(&b_full[sb], (n / (uint32_t)L.sb) & 1u, abort_flag)) {
-            fail();
-            ok = false;
-            break;
+        const int tail = ((ph ? K2 : K1) / 32 - 1) % 4 + 1;   // blocks of a row's last piece
+        for (Run r(s, cta); r.left > 0 && ok; r.next(s)) {
+          const int cols = up16((int)(pl.ent[r.ent] >> 20) * (ph ? 3 : 2));
+          const uint32_t id = (uint32_t)(cols >> 3) << 17 | 1u << 23 | 8u << 24, d = tmem + acc.i * DC_ACC;
+          if (!mbar_wait(&acc_empty[acc.i], acc.turn ^ 1u, abort_flag)) ok = false;
+          uint32_t add = 0;
+          for (int c = 0; c < r.n; ++c) {
+            if (!ok || !mbar_wait(&a_full[sa.i], sa.turn, abort_flag) || !mbar_wait(&b_full[sb.i], sb.turn, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sf = tmem + DC_SF + sb.i * 12;
+            const uint64_t sfb = sfb0 + (uint32_t)(sb.i * L.sfb_bytes >> 4);
+            cp_scales(sf, sfa0 + (uint32_t)(sb.i * 32));
+            cp_scales(sf + 4, sfb);
+            if (cols > 128) cp_scales(sf + 8, sfb + 32);
+            const uint64_t ad = ad0 + (uint32_t)(sa.i * (DC_A_BYTES >> 4)), bd = bd0 + (uint32_t)(sb.i * L.b_bytes >> 4);
+            auto block = [&](int k, uint32_t plus) {
+              mma_mx1(d, ad + 2 * k, bd + 2 * k, id | (uint32_t)k << 4 | (uint32_t)k << 29, sf, sf + 4, plus);
+            };
+            if (tail == 4 || r.k + c + 1 < s.kt) {
+              block(0, add), block(1, 1), block(2, 1), block(3, 1);
+            } else {
+              block(0, add);
+              if (tail > 1) block(1, 1);
+              if (tail > 2) block(2, 1);
+            }
+            add = 1;
+            tc_commit(&a_empty[sa.i]);
+            tc_commit(&b_empty[sb.i]);
+            sa.step(1, L.sa);
+            sb.step(1, L.sb);
           }
-          tc_fence_after();
-          const int cols = up16((int)(pl.ent[w.ent] >> 20) * terms);
-          const uint32_t sf = tmem + DC_SF + sb * 12, d = tmem + (seg & 1) * DC_ACC;
-          const uint32_t sfb = smem_u32(smem + L.sfb + sb * L.sfb_bytes);
-          cp_scales(sf, smem_u32(smem + L.sfa + sa * 512));
-          cp_scales(sf + 4, sfb);
-          if (cols > 128) cp_scales(sf + 8, sfb + 512);
-          const uint64_t ad = sdesc_sw128(smem_u32(smem + sa * DC_A_BYTES));
-          const uint64_t bd = sdesc_sw128(smem_u32(smem + L.b + sb * L.b_bytes));
-          const uint32_t id = (uint32_t)(cols >> 3) << 17 | 1u << 23 | 8u << 24;
-          const int blocks = min(4, (K - w.k * 128) / 32);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < blocks)
-              mma_mx1(d, ad + 2 * k, bd + 2 * k, id | (uint32_t)k << 4 | (uint32_t)k << 29, sf, sf + 4, !fresh || k > 0);
-          tc_commit(&a_empty[sa]);
-          tc_commit(&b_empty[sb]);
-          fresh = w.last(s);
-          if (fresh) tc_commit(&acc_full[seg++ & 1]);
+          if (!ok) break;
+          tc_commit(&acc_full[acc.i]);
+          acc.step(1, 2);
         }
       }
+      if (!ok) fail();
       // every product has completed before tensor memory is given back
       tc_commit(drain);
       if (!mbar_wait(drain, 0, nullptr)) set_status(a.status, FP8MOE_ERR_TIMEOUT);
     }
     __syncwarp();
-  } else {
-    const bool epi = warp < 4;
-    const int jt = epi ? tid : tid - 64;           // thread among those that add
-    uint32_t n = 0, seg = 0;                       // pieces and segments so far
-    // ======================= terms =======================
-    auto terms_of = [&](auto phase) {
-      constexpr int PH = decltype(phase)::value, NT = PH ? 3 : 2;
-      const Stream& s = PH ? s2 : s1;
-      const int K = PH ? K2 : K1;
-      const int group = (warp - DC_WARP_B) >> 2, sub = ((warp - DC_WARP_B) & 3) * 2 + (lane >> 4), j = lane & 15;
-      auto load = [&](const Walk& w, int i, uint32_t ent, uint4 (&r)[2]) {
-        const int place = (int)(ent >> 10 & 1023u) + i, k = w.k * 128 + j * 8;
-        if (i >= (int)(ent >> 20) || k >= K) return;
-        if constexpr (PH == 0) {
-          r[0] = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)(pl.order[place] / a.k) * a.ldx + k));
-        } else {
-          const uint4* p = reinterpret_cast<const uint4*>(a.act + (int64_t)place * a.F + k);
-          r[0] = __ldcg(p);
-          r[1] = __ldcg(p + 1);
-        }
-      };
-      uint4 next[2] = {};
-      Walk w(s, cta);
-      const uint32_t total = w.left;
-      const uint32_t n0 = n;
-      // (the groups alternate over both runs together)
-      auto skip = [&]() {
-        w.step(s);
-        ++n;
-      };
-      while (w.left > 0 && (n & 1u) != (uint32_t)group) skip();
-      if (w.left > 0) load(w, sub, pl.ent[w.ent], next);
-      while (w.left > 0) {
-        const int sb = (int)(n % (uint32_t)L.sb);
-        const uint32_t ent = pl.ent[w.ent], turn = n / (uint32_t)L.sb;
-        const int pairs = (int)(ent >> 20), k0 = w.k * 128;
-        uint4 cur[2] = {next[0], next[1]};
-        Walk here = w;
-        skip();
-        if (w.left > 0) skip();
-        if (w.left > 0) load(w, sub, pl.ent[w.ent], next);
-        if (!mbar_wait(&b_empty[sb], (turn & 1u) ^ 1u, abort_flag)) {
-          fail();
-          break;
-        }
-        uint8_t *tile = smem + L.b + sb * L.b_bytes, *sf = smem + L.sfb + sb * L.sfb_bytes;
-        for (int i0 = 0; i0 < pairs; i0 += 8) {
-          const int i = i0 + sub;
-          if (i0 > 0) load(here, i, ent, cur);
-          float v[8];
-          if constexpr (PH == 0) {
-            const uint32_t q[4] = {cur[0].x, cur[0].y, cur[0].z, cur[0].w};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) v[2 * c] = bf16_lo(q[c]), v[2 * c + 1] = bf16_hi(q[c]);
-          } else {
-            const uint32_t q[8] = {cur[0].x, cur[0].y, cur[0].z, cur[0].w, cur[1].x, cur[1].y, cur[1].z, cur[1].w};
-#pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] = __uint_as_float(q[c]);
+  } else if (warp == DC_WARP_B) {
+    // ======================= terms and scales =======================
+    if (lane == 0) {
+      Slot slot;
+      uint32_t i = 0;
+      bool ok = true;
+      for (int ph = 0; ph < 2 && ok; ++ph) {
+        const Stream& s = ph ? s2 : s1;
+        const int nt = ph ? 3 : 2;
+        if (ph == 1 && !came(a.meets + 32, grid, a.status, abort_flag)) break;
+        asm volatile("fence.proxy.async;" ::: "memory");
+        for (Run r(s, cta); r.left > 0 && ok; r.next(s)) {
+          const uint32_t ent = pl.ent[r.ent];
+          const int rows = (int)(ent >> 20) * nt;
+          const uint32_t bytes = (uint32_t)rows * 128, sfb = rows <= 32 ? (uint32_t)rows * 16 : rows <= 128 ? 512 : 1024;
+          const uint8_t* b = tile_of(ent, r.k, s.kt, nt);
+          const uint8_t* sb = sf_of(r.ent, r.k, s.kt);
+          const uint8_t* sa = (ph ? a.s2 : a.s1) + (((int64_t)(ent & 1023u) * s.rt + r.row) * s.kt + r.k) * 512;
+          for (int c = 0; c < r.n; ++c, ++i, b += bytes, sb += L.sfb_bytes, sa += 512, slot.step(1, L.sb)) {
+            if (!mbar_wait(&b_empty[slot.i], slot.turn ^ 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            uint64_t* bar = &b_full[slot.i];
+            mbar_expect_tx(bar, bytes + sfb + 512);
+            bulk_load(smem + L.b + slot.i * L.b_bytes, b, bytes, bar);
+            bulk_load(smem + L.sfb + slot.i * L.sfb_bytes, sb, sfb, bar);
+            bulk_load(smem + L.sfa + slot.i * 512, sa, 512, bar);
           }
-          const bool on = i < pairs && k0 + j * 8 < K;
-          // (a block's four lanes are on or off together; the shuffles are the warp's)
-          if (__any_sync(0xffffffffu, on)) put_terms<NT>(v, tile, sf, i * NT, j, on);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b_full[sb]);
       }
-      n = n0 + total;
-    };
+      if (!ok) fail();
+      if (*abort_flag)
+        for (uint32_t n = i > (uint32_t)L.sb ? i - L.sb : 0; n < i; ++n)
+          (void)mbar_wait(&b_full[n % L.sb], (n / (uint32_t)L.sb) & 1u, nullptr);
+    }
+    __syncwarp();
+  } else {
     // ======================= accumulators =======================
+    Slot acc;
     auto sums_of = [&](auto phase) {
       constexpr int PH = decltype(phase)::value, NT = PH ? 3 : 2;
       const Stream& s = PH ? s2 : s1;
       const int R = PH ? R2 : R1;
-      for (Walk w(s, cta); w.left > 0; w.step(s)) {
-        if (!w.last(s)) continue;
-        const uint32_t ent = pl.ent[w.ent];
+      for (Run r(s, cta); r.left > 0; r.next(s)) {
+        const uint32_t ent = pl.ent[r.ent];
         const int first = (int)(ent >> 10 & 1023u), pairs = (int)(ent >> 20);
-        const int part = (int)(cta - s.owner(w.tile * s.kt));
-        const int row = w.row * 128 + warp * 32 + lane;
+        const int part = (int)(cta - s.owner(r.tile * s.kt));
+        const int row = r.row * 128 + warp * 32 + lane;
         float* dst = a.part + ((int64_t)part * nlive + first) * R + row;
-        const uint32_t buf = seg & 1;
-        if (!mbar_wait(&acc_full[buf], (seg >> 1) & 1u, abort_flag)) {
+        if (!mbar_wait(&acc_full[acc.i], acc.turn, abort_flag)) {
           fail();
           break;
         }
-        ++seg;
         tc_fence_after();
-        const uint32_t src = tmem + buf * DC_ACC + ((uint32_t)(warp * 32) << 16);
+        const uint32_t src = tmem + acc.i * DC_ACC + ((uint32_t)(warp * 32) << 16);
         for (int i0 = 0; i0 < pairs; i0 += 8) {
-          uint32_t r[24];
+          uint32_t q[24];
 #pragma unroll
-          for (int c = 0; c < NT; ++c) tmem_ld8(src + i0 * NT + c * 8, *reinterpret_cast<uint32_t(*)[8]>(r + c * 8));
+          for (int c = 0; c < NT; ++c) tmem_ld8(src + i0 * NT + c * 8, *reinterpret_cast<uint32_t(*)[8]>(q + c * 8));
           tmem_ld_wait();
           if (i0 + 8 >= pairs) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            if (lane == 0) mbar_arrive(&acc_empty[acc.i]);
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float v = 0.0f;   // the smallest term first
 #pragma unroll
-            for (int t = NT - 1; t >= 0; --t) v += __uint_as_float(r[i * NT + t]);
+            for (int t = NT - 1; t >= 0; --t) v += __uint_as_float(q[i * NT + t]);
             if (i0 + i < pairs && row < R) dst[(int64_t)(i0 + i) * R] = v;
           }
         }
+        acc.step(1, 2);
       }
     };
     // partial sums of a tile in order, four neighbouring rows
@@ -559,54 +585,59 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       }
       return v;
     };
-    // task i of a join: runs of eight tasks a CTA in turn
-    const uint32_t t0 = (((uint32_t)jt >> 3) * grid + cta) * 8 + (jt & 7), tstep = DC_JOIN / 8 * grid * 8;
-
     using One = std::integral_constant<int, 0>;
     using Two = std::integral_constant<int, 1>;
+    // the accumulating warps come to meeting i and wait for it, with the others
     auto meeting = [&](int i) {
       if (epi) {
-        if (tid == 0) meet(a.meets + 32 * i, grid, a.status, abort_flag);
+        bar_sync(1, 128);
+        if (tid == 0) {
+          __threadfence();
+          come(a.meets + 32 * i);
+          (void)came(a.meets + 32 * i, grid, a.status, abort_flag);
+        }
       }
       bar_sync(2, DC_JOIN);
     };
-    if (epi) {
-      sums_of(One{});
-      __threadfence();
-      bar_sync(1, 128);
-    } else {
-      terms_of(One{});
-    }
+    if (epi) sums_of(One{});
     meeting(0);
-    // the activation, from the first product's partial sums
+    // the activation, from the first product's partial sums, and its terms:
+    // sixteen threads a pair's piece
     {
-      const uint32_t per = (uint32_t)a.F / 4, tasks = (uint32_t)nlive * per;
-      for (uint32_t i = t0; i < tasks; i += tstep) {
-        const int place = (int)(i / per), f = (int)(i - (uint32_t)place * per) * 4, ent = pl.ent_of[place];
-        const float4 g = gather(s1, R1, place, ent, f), u = gather(s1, R1, place, ent, a.F + f);
-        float4 o;
-        o.x = g.x / (1.0f + expf(-g.x)) * u.x;
-        o.y = g.y / (1.0f + expf(-g.y)) * u.y;
-        o.z = g.z / (1.0f + expf(-g.z)) * u.z;
-        o.w = g.w / (1.0f + expf(-g.w)) * u.w;
-        __stcg(reinterpret_cast<float4*>(a.act + (int64_t)place * a.F + f), o);
+      const int units = nlive * kt2, step = (int)grid * (DC_JOIN / 16), j = jt & 15;
+      for (int u = (jt >> 4) * (int)grid + (int)cta; u - (jt >> 4 & 1) * (int)grid < units; u += step) {
+        const bool on = u < units;
+        const int place = on ? u / kt2 : 0, c = on ? u - place * kt2 : 0, f = c * 128 + j * 8;
+        const int e = pl.ent_of[place];
+        const uint32_t ent = pl.ent[e];
+        const bool in = on && f < a.F;
+        float v[8] = {};
+        if (in) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4 g = gather(s1, R1, place, e, f + 4 * h), y = gather(s1, R1, place, e, a.F + f + 4 * h);
+            v[4 * h] = g.x / (1.0f + expf(-g.x)) * y.x;
+            v[4 * h + 1] = g.y / (1.0f + expf(-g.y)) * y.y;
+            v[4 * h + 2] = g.z / (1.0f + expf(-g.z)) * y.z;
+            v[4 * h + 3] = g.w / (1.0f + expf(-g.w)) * y.w;
+          }
+        }
+        put_terms<3>(v, tile_of(ent, c, kt2, 3), sf_of(e, c, kt2), (place - (int)(ent >> 10 & 1023u)) * 3, j, in);
       }
     }
-    __threadfence();
+    asm volatile("fence.proxy.async;" ::: "memory");
     bar_sync(2, DC_JOIN);
-    meeting(1);
-    if (epi) {
-      sums_of(Two{});
+    if (tid == 0) {
       __threadfence();
-      bar_sync(1, 128);
-    } else {
-      terms_of(Two{});
+      come(a.meets + 32);
     }
+    if (epi) sums_of(Two{});
     meeting(2);
-    // the weighted sum over a token's experts
+    // the weighted sum over a token's experts, four neighbouring columns a thread,
+    // runs of eight threads' a CTA in turn
     {
       const uint32_t per = (uint32_t)a.H / 4, tasks = (uint32_t)a.T * per;
-      for (uint32_t i = t0; i < tasks; i += tstep) {
+      for (uint32_t i = (((uint32_t)jt >> 3) * grid + cta) * 8 + (jt & 7); i < tasks; i += DC_JOIN * grid) {
         const int t = (int)(i / per), h = (int)(i - (uint32_t)t * per) * 4;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int j = 0; j < a.k; ++j) {
@@ -647,20 +678,23 @@ int64_t part_floats(int64_t P, int64_t R, int64_t K) {
   return most;
 }
 
+// bytes of the scales of a piece's terms
+constexpr int term_scale_bytes(int P) { return 3 * (P < DC_NB ? P : DC_NB) > 128 ? 1024 : 512; }
+
 DecodeSmem layout(int P, int max_ent, int max_smem) {
   DecodeSmem L{};
-  const int nb = P < DC_NB ? (P + 7) / 8 * 8 : DC_NB, rows = up16(3 * nb);
-  L.b_bytes = (rows * 128 + 1023) / 1024 * 1024;
-  L.sfb_bytes = rows > 128 ? 1024 : 512;
-  L.sb = nb <= 16 ? 6 : nb <= 32 ? 4 : 2;
+  const int nb = P < DC_NB ? P : DC_NB;
+  L.b_bytes = (up16(3 * nb) * 128 + 1023) / 1024 * 1024;
+  L.sfb_bytes = term_scale_bytes(P);
+  L.sb = nb <= 8 ? 8 : nb <= 16 ? 6 : nb <= 32 ? 4 : 3;
   const int plan = 16 + max_ent * 4 + P * 10;
   const int bars = 8 * (2 * 16 + 2 * DC_MAX_BS + 8);
-  const int fixed = L.sb * (L.b_bytes + L.sfb_bytes) + bars + plan + 64;
-  L.sa = (max_smem - 2048 - fixed) / (DC_A_BYTES + 512);   // 1024 to align the rings, 1024 for what is static
+  const int fixed = L.sb * (L.b_bytes + L.sfb_bytes + 512) + bars + plan + 64;
+  L.sa = (max_smem - 2048 - fixed) / DC_A_BYTES;   // 1024 to align the rings, 1024 for what is static
   if (L.sa > 13) L.sa = 13;
   L.b = L.sa * DC_A_BYTES;
   L.sfa = L.b + L.sb * L.b_bytes;
-  L.sfb = L.sfa + L.sa * 512;
+  L.sfb = L.sfa + L.sb * 512;
   L.bars = L.sfb + L.sb * L.sfb_bytes;
   L.plan = L.bars + bars;
   L.total = (L.plan + plan + 15) / 16 * 16;
@@ -677,9 +711,21 @@ bool decode_fits(int64_t P, int64_t E, int64_t H, int64_t F) {
   return max_entries(P, E) * kh * (f2 > kf ? f2 : kf) * DECODE_MAX_CTAS < (int64_t)1 << 32;
 }
 
-int64_t decode_workspace_bytes(int64_t P, int64_t H, int64_t F) {
+// What the workspace holds behind the counters: partial sums, terms, their
+// scales.  Both products' in turn in the same place.
+struct DecodeSpace {
+  int64_t parts, terms, scales;   // bytes
+};
+static DecodeSpace space_of(int64_t P, int64_t E, int64_t H, int64_t F) {
   const int64_t p1 = part_floats(P, 2 * F, H), p2 = part_floats(P, H, F);
-  return DECODE_MEETS_BYTES + ((p1 > p2 ? p1 : p2) + P * F) * (int64_t)sizeof(float);
+  const int64_t kh = (H + 127) / 128, kf = (F + 127) / 128;
+  return {(p1 > p2 ? p1 : p2) * (int64_t)sizeof(float), P * 128 * (2 * kh > 3 * kf ? 2 * kh : 3 * kf),
+          max_entries(P, E) * (kh > kf ? kh : kf) * term_scale_bytes((int)P)};
+}
+
+int64_t decode_workspace_bytes(int64_t P, int64_t E, int64_t H, int64_t F) {
+  const DecodeSpace w = space_of(P, E, H, F);
+  return DECODE_MEETS_BYTES + w.parts + w.terms + w.scales;
 }
 
 cudaError_t launch_decode(DecodeArgs a, void* workspace, int num_sms, int max_smem, cudaStream_t st) {
@@ -692,10 +738,11 @@ cudaError_t launch_decode(DecodeArgs a, void* workspace, int num_sms, int max_sm
   const int64_t c = c1 > c2 ? c1 : c2, want = (c + DECODE_MIN_RUN - 1) / DECODE_MIN_RUN;
   int64_t grid = num_sms < DECODE_MAX_CTAS ? num_sms : DECODE_MAX_CTAS;
   if (want < grid) grid = want;
-  const int64_t p1 = part_floats(a.P, 2 * (int64_t)a.F, a.H), p2 = part_floats(a.P, a.H, a.F);
+  const DecodeSpace w = space_of(a.P, a.E, a.H, a.F);
   a.meets = (uint32_t*)workspace;
   a.part = (float*)((uint8_t*)workspace + DECODE_MEETS_BYTES);
-  a.act = a.part + (p1 > p2 ? p1 : p2);
+  a.terms = (uint8_t*)a.part + w.parts;
+  a.term_scales = a.terms + w.terms;
   a.stall = take_ring_stall_hook();
   CUtensorMap tm[2];
   const int64_t R[2] = {2 * (int64_t)a.F, a.H}, K[2] = {a.H, a.F};

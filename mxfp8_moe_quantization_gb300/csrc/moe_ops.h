@@ -67,7 +67,8 @@ struct DecodeArgs {
   const uint8_t *q1, *s1, *q2, *s2;
   uint16_t* out;         // [T, H]
   uint32_t* meets;
-  float *part, *act;     // partial sums [parts][live pairs][rows]; activations [live pairs][F]
+  float* part;           // partial sums [parts][live pairs][rows]
+  uint8_t *terms, *term_scales;
   int* status;
   int stall;             // test hook: the first CTA never loads its first piece
 };
