@@ -15,16 +15,16 @@
 // terms are further columns of N, where the tensor core has room: N is at least
 // 16, and the weights' arrival leaves it idle most of the time.
 //
-// Both products are one stream of 16 KB pieces (128 rows x 128 of K) over all
+// Both products are one stream of 32 KB pieces (128 rows x 256 of K) over all
 // (expert, row tile, k) in order, cut into equal runs, one per CTA; a tile's
 // partial sums (fp32, at most a few per tile) go to the workspace and are added
 // in order after a grid-wide meeting.  The terms are made once, into the
 // workspace, as the tensor core reads them (128-byte swizzle, 128x4 scales): a
 // piece's share of them is one bulk copy.  The weights' producer takes no part in
 // the meetings: while the others add, it fills its ring with W2.
+// (With pieces of 128 of K the copies' issue set the pace, about 200 cycles each.)
 //   warps 0-3  accumulators to partial sums;  4  weights by TMA;  5  MMA issue;
 //   6  terms and scales to shared memory;  0-3 and 7-13  terms, sums, results.
-#include <cooperative_groups.h>
 #include <cuda.h>
 
 #include <type_traits>
@@ -41,21 +41,31 @@ namespace {
 constexpr int DC_THREADS = 448;
 constexpr int DC_WARP_TMA = 4, DC_WARP_MMA = 5, DC_WARP_B = 6;
 constexpr int DC_JOIN = DC_THREADS - 96;  // threads that make terms and add partial sums: all but those three warps'
-constexpr int DC_A_BYTES = 128 * 128;
+constexpr int DC_G = 2;                   // tiles of 128 x 128 in a piece
+constexpr int DC_TILE = 128 * 128, DC_A_BYTES = DC_G * DC_TILE;
 constexpr int DC_NB = DECODE_ENTRY_PAIRS;   // pairs of one entry: a pass over an expert's weights
 constexpr int DC_ACC = 3 * DC_NB;         // TMEM columns of an accumulator
 constexpr int DC_SF = 2 * DC_ACC;         // first TMEM column of the scales: 12 per slot
-constexpr int DC_MAX_BS = 8;
-static_assert(DC_SF + 12 * DC_MAX_BS <= 512, "tensor memory");
+constexpr int DC_MAX_BS = 4;
+static_assert(DC_SF + 12 * DC_G * DC_MAX_BS <= 512, "tensor memory");
 constexpr int DC_DEAD = 0xFFFF;
 
 __host__ __device__ constexpr int up16(int v) { return (v + 15) / 16 * 16; }
 
 // Shared memory: the ring of weights (sa slots, at 0), that of terms with the
-// terms' and the weights' scales (sb slots each), the plan.
+// terms and their scales and that of the weights' scales (sb slots each), the plan.
 struct DecodeSmem {
-  int sa, sb, b_bytes, sfb_bytes;
-  int sfa, b, sfb, bars, plan, total;
+  int sa, sb, b_bytes;
+  int sfa, b, bars, plan, total;
+};
+
+// The terms of an entry of n pairs, piece by piece: DC_G tiles of their rows,
+// rounded up to 8, then the tiles' scales (of up to 32 rows that is the first part
+// of a 128x4 tile).
+struct TermTiles {
+  int rows, sf;   // rows of a tile; bytes of its scales
+  __host__ __device__ constexpr TermTiles(int terms) : rows((terms + 7) / 8 * 8), sf(rows <= 32 ? rows * 16 : rows <= 128 ? 512 : 1024) {}
+  __host__ __device__ constexpr int bytes() const { return DC_G * (rows * 128 + sf); }
 };
 
 // The plan of a call, in shared memory: the live pairs (token, choice) in the
@@ -177,19 +187,19 @@ FP8MOE_DEV void plan_block(const DecodeArgs& a, const Plan& pl, int* scratch) {
   __syncthreads();
 }
 
-// One product's stream of pieces: nent entries x rt row tiles x kt pieces.
+// One product's stream of pieces: nent entries x rt row tiles x kp pieces.
 struct Stream {
   uint32_t C, runs;   // pieces, CTAs that have a run of them
-  int rt, kt;
-  FP8MOE_DEV Stream(int nent, int rt_, int kt_, uint32_t grid) : rt(rt_), kt(kt_) {
-    C = (uint32_t)nent * rt * kt;
+  int rt, kp;
+  FP8MOE_DEV Stream(int nent, int rt_, int kp_, uint32_t grid) : rt(rt_), kp(kp_) {
+    C = (uint32_t)nent * rt * kp;
     const uint32_t want = (C + DECODE_MIN_RUN - 1) / DECODE_MIN_RUN;
     runs = want < grid ? want : grid;
   }
   FP8MOE_DEV uint32_t first(uint32_t cta) const { return cta < runs ? cta * C / runs : C; }
   FP8MOE_DEV uint32_t owner(uint32_t c) const { return ((c + 1) * runs - 1) / C; }
   // partial sums of a tile: the CTAs whose runs meet it
-  FP8MOE_DEV int parts(uint32_t tile) const { return (int)(owner(tile * kt + kt - 1) - owner(tile * kt)) + 1; }
+  FP8MOE_DEV int parts(uint32_t tile) const { return (int)(owner(tile * kp + kp - 1) - owner(tile * kp)) + 1; }
 };
 
 // A CTA's run of a stream, segment by segment: the pieces of one tile that are
@@ -201,18 +211,18 @@ struct Run {
   FP8MOE_DEV Run(const Stream& s, uint32_t cta) {
     const uint32_t lo = s.first(cta);
     left = s.first(cta + 1) - lo;
-    tile = lo / s.kt;
-    k = (int)(lo - tile * s.kt);
+    tile = lo / s.kp;
+    k = (int)(lo - tile * s.kp);
     ent = (int)(tile / s.rt);
     row = (int)(tile - (uint32_t)ent * s.rt);
-    n = (int)min(left, (uint32_t)(s.kt - k));
+    n = (int)min(left, (uint32_t)(s.kp - k));
   }
   FP8MOE_DEV void next(const Stream& s) {
     left -= n;
     k = 0;
     ++tile;
     if (++row == s.rt) row = 0, ++ent;
-    n = (int)min(left, (uint32_t)s.kt);
+    n = (int)min(left, (uint32_t)s.kp);
   }
 };
 
@@ -245,15 +255,24 @@ FP8MOE_DEV void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "r"(taddr));
 }
 FP8MOE_DEV void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-FP8MOE_DEV uint32_t ld_acquire_gpu(const uint32_t* p) {
-  uint32_t v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+FP8MOE_DEV uint64_t ld_acquire_gpu(const unsigned long long* p) {
+  uint64_t v;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
   return v;
 }
+// Grid-wide meetings: a counter each, to which every CTA of a launch adds one.
+// They are the library's own, per device, as no caller's memory starts at zero:
+// a CTA fills an SM's shared memory and the grid all SMs, so that no two launches
+// ever run at a time, and each leaves every counter one grid further.
+constexpr int DC_MEETS = 4;
+__device__ unsigned long long g_meets[DC_MEETS * 16];
 // One CTA more at a meeting; the (bounded) wait until all have come.  One thread.
 // (A CTA whose own wait ran out still comes: the limit is twice that.)
-FP8MOE_DEV void come(uint32_t* count) { asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory"); }
-FP8MOE_DEV bool came(const uint32_t* count, uint32_t n, int* status, volatile int* abort_flag) {
+FP8MOE_DEV void come(int i) {
+  asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(g_meets + 16 * i) : "memory");
+}
+FP8MOE_DEV bool came(int i, uint64_t n, int* status, volatile int* abort_flag) {
+  const unsigned long long* count = g_meets + 16 * i;
   if (ld_acquire_gpu(count) >= n) return true;
   const uint64_t t0 = globaltimer();
   while (ld_acquire_gpu(count) < n) {
@@ -338,6 +357,11 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     set_status(a.status, FP8MOE_ERR_TIMEOUT);
     *abort_flag = 1;
   };
+  // every meeting's count when all have come: the last one's stands still until
+  // this CTA has been at the others
+  uint64_t meets;
+  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(meets) : "l"(g_meets + 16 * (DC_MEETS - 1)));
+  meets += grid;
 
   if (warp == DC_WARP_TMA && lane == 0) {
     abort_s = 0;
@@ -352,94 +376,72 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     tc_fence_before();
   }
-  if (cta == 0 && tid < 3) a.meets[tid * 32] = 0;
   if (a.P <= 32) {
-    if (warp == DC_WARP_TMA) {
-      plan_warp(a, pl, lane);
-      asm volatile("bar.arrive 3, %0;" ::"n"(DC_THREADS) : "memory");
-    } else {
-      bar_sync(3, DC_THREADS);
-    }
+    if (warp == DC_WARP_TMA) plan_warp(a, pl, lane);
+    __syncthreads();
   } else {
     plan_block(a, pl, (int*)(smem + L.b));   // (ends with a block barrier)
   }
-
-  const int K1 = a.H, K2 = a.F, R1 = 2 * a.F, R2 = a.H;
-  const int rt1 = (R1 + 127) / 128, kt1 = (K1 + 127) / 128, rt2 = (R2 + 127) / 128, kt2 = (K2 + 127) / 128;
-  // ---- weights: a ring fill per piece, of the first product's run and then of
-  // the second's; `first` fills leave before the grid meets
-  auto produce = [&](uint32_t from, uint32_t upto) {
-    Slot slot;
-    uint32_t i = 0;
-    for (int ph = 0; ph < 2; ++ph) {
-      const Stream s(pl.num[1], ph ? rt2 : rt1, ph ? kt2 : kt1, grid);
-      const CUtensorMap* tm = ph ? &tm2 : &tm1;
-      for (Run r(s, cta); r.left > 0; r.next(s)) {
-        if (i >= upto) return i;
-        const int e = (int)(pl.ent[r.ent] & 1023u);
-        int x = r.k * 128;
-        for (int c = 0; c < r.n; ++c, ++i, x += 128, slot.step(1, L.sa)) {
-          if (i < from) continue;
-          if (i >= upto) return i;
-          uint64_t* bar = &a_full[slot.i];
-          if (!mbar_wait(&a_empty[slot.i], slot.turn ^ 1u, abort_flag)) {
-            fail();
-            return i;
-          }
-          if (a.stall && cta == 0 && i == 0) continue;
-          mbar_expect_tx(bar, DC_A_BYTES);
-          tma_load_3d(smem + slot.i * DC_A_BYTES, tm, bar, x, r.row * 128, e);
-        }
-      }
-    }
-    return i;
-  };
-  uint32_t issued = 0;
-  const bool epi = warp < 4, joins = epi || warp > DC_WARP_B;
-  const int jt = epi ? tid : tid - 96;             // thread among those that make terms and add
-  // a piece's terms and their scales in the workspace
-  auto tile_of = [&](uint32_t ent, int c, int kt, int nt) {
-    return a.terms + ((int64_t)(ent >> 10 & 1023u) * kt + (int64_t)c * (int)(ent >> 20)) * nt * 128;
-  };
-  auto sf_of = [&](int e, int c, int kt) { return a.term_scales + ((int64_t)e * kt + c) * L.sfb_bytes; };
-  if (warp == DC_WARP_TMA) {
-    if (lane == 0) issued = produce(0, (uint32_t)L.sa);
-    __syncwarp();
-  } else if (joins) {
-    // the first product's terms: sixteen threads a pair's piece
-    const int units = pl.num[0] * kt1, step = (int)grid * (DC_JOIN / 16), j = jt & 15;
-    for (int u = (jt >> 4) * (int)grid + (int)cta; u - (jt >> 4 & 1) * (int)grid < units; u += step) {
-      const bool on = u < units;                    // (a warp has two pieces, and shuffles)
-      const int place = on ? u / kt1 : 0, c = on ? u - place * kt1 : 0, k = c * 128 + j * 8;
-      const int e = pl.ent_of[place];
-      const uint32_t ent = pl.ent[e];
-      const bool in = on && k < K1;
-      float v[8] = {};
-      if (in) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)(pl.order[place] / a.k) * a.ldx + k));
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
-      }
-      put_terms<2>(v, tile_of(ent, c, kt1, 2), sf_of(e, c, kt1), (place - (int)(ent >> 10 & 1023u)) * 2, j, in);
-    }
-    asm volatile("fence.proxy.async;" ::: "memory");   // bulk copies of other CTAs read them
-  }
-  // the meetings' counters are zero, the barriers exist, the plan and the first terms are made
-  cooperative_groups::this_grid().sync();
   tc_fence_after();
   const uint32_t tmem = tmem_s;
   const int nlive = pl.num[0], nent = pl.num[1];
-  const Stream s1(nent, rt1, kt1, grid), s2(nent, rt2, kt2, grid);
+
+  const int K1 = a.H, K2 = a.F, R1 = 2 * a.F, R2 = a.H;
+  const int rt1 = (R1 + 127) / 128, kt1 = (K1 + 127) / 128, rt2 = (R2 + 127) / 128, kt2 = (K2 + 127) / 128;
+  const int kp1 = (kt1 + DC_G - 1) / DC_G, kp2 = (kt2 + DC_G - 1) / DC_G;
+  const Stream s1(nent, rt1, kp1, grid), s2(nent, rt2, kp2, grid);
+  const bool epi = warp < 4;
+  const int jt = epi ? tid : tid - 96;             // thread among those that make terms and add
+  // an entry's terms in the workspace
+  auto terms_of = [&](int e, uint32_t ent, int kp, int nt) {
+    return a.terms + (int64_t)kp * DC_G * ((nt * (int)(ent >> 10 & 1023u) + 7 * e) * 128 + 1024 * e);
+  };
+  // terms of eight values, place 8 j of tile c, of the pair at `place`
+  auto put = [&](auto nt, float (&v)[8], int place, int c, int kp, int j, bool on) {
+    constexpr int NT = decltype(nt)::value;
+    const int e = pl.ent_of[place];
+    const uint32_t ent = pl.ent[e];
+    const TermTiles tt((int)(ent >> 20) * NT);
+    uint8_t* p = terms_of(e, ent, kp, NT) + (int64_t)(c / DC_G) * tt.bytes();
+    put_terms<NT>(v, p + c % DC_G * tt.rows * 128, p + DC_G * tt.rows * 128 + c % DC_G * tt.sf,
+                  (place - (int)(ent >> 10 & 1023u)) * NT, j, on);
+  };
+  using Two = std::integral_constant<int, 2>;     // terms of a bf16 value, of an fp32 one
+  using Three = std::integral_constant<int, 3>;
 
   if (warp == DC_WARP_TMA) {
     // ======================= weights =======================
     if (lane == 0) {
-      issued = produce(issued, UINT32_MAX);
+      Slot slot;
+      uint32_t i = 0;
+      bool ok = true;
+      for (int ph = 0; ph < 2 && ok; ++ph) {
+        const Stream& s = ph ? s2 : s1;
+        const CUtensorMap* tm = ph ? &tm2 : &tm1;
+        const int kt = ph ? kt2 : kt1;
+        for (Run r(s, cta); r.left > 0 && ok; r.next(s)) {
+          const int e = (int)(pl.ent[r.ent] & 1023u);
+          int x = r.k * DC_G;   // the piece's first tile
+          for (int c = 0; c < r.n; ++c, ++i, x += DC_G, slot.step(1, L.sa)) {
+            uint64_t* bar = &a_full[slot.i];
+            if (!mbar_wait(&a_empty[slot.i], slot.turn ^ 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (a.stall && cta == 0 && i == 0) continue;
+            const int tiles = min(DC_G, kt - x);
+            mbar_expect_tx(bar, tiles * DC_TILE);
+#pragma unroll
+            for (int g = 0; g < DC_G; ++g)
+              if (g < tiles) tma_load_3d(smem + slot.i * DC_A_BYTES + g * DC_TILE, tm, bar, (x + g) * 128, r.row * 128, e);
+          }
+        }
+      }
+      if (!ok) fail();
       // no copy stays in flight after a wait that ran out
       if (*abort_flag)
-        for (uint32_t i = issued > (uint32_t)L.sa ? issued - L.sa : 0; i < issued; ++i)
-          if (!(a.stall && cta == 0 && i == 0)) (void)mbar_wait(&a_full[i % L.sa], (i / (uint32_t)L.sa) & 1u, nullptr);
+        for (uint32_t n = i > (uint32_t)L.sa ? i - L.sa : 0; n < i; ++n)
+          if (!(a.stall && cta == 0 && n == 0)) (void)mbar_wait(&a_full[n % L.sa], (n / (uint32_t)L.sa) & 1u, nullptr);
     }
     __syncwarp();
   } else if (warp == DC_WARP_MMA) {
@@ -447,13 +449,15 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     if (lane == 0) {
       Slot sa, sb, acc;
       const uint64_t ad0 = sdesc_sw128(smem_u32(smem)), bd0 = sdesc_sw128(smem_u32(smem + L.b));
-      const uint64_t sfa0 = sdesc_scales(smem_u32(smem + L.sfa)), sfb0 = sdesc_scales(smem_u32(smem + L.sfb));
+      const uint64_t sfa0 = sdesc_scales(smem_u32(smem + L.sfa)), sfb0 = sdesc_scales(smem_u32(smem + L.b));
       bool ok = true;
       for (int ph = 0; ph < 2 && ok; ++ph) {
         const Stream& s = ph ? s2 : s1;
-        const int tail = ((ph ? K2 : K1) / 32 - 1) % 4 + 1;   // blocks of a row's last piece
+        const int kt = ph ? kt2 : kt1;
+        const int tail = ((ph ? K2 : K1) / 32 - 1) % 4 + 1;   // blocks of a row's last tile
         for (Run r(s, cta); r.left > 0 && ok; r.next(s)) {
-          const int cols = up16((int)(pl.ent[r.ent] >> 20) * (ph ? 3 : 2));
+          const TermTiles tt((int)(pl.ent[r.ent] >> 20) * (ph ? 3 : 2));
+          const int cols = up16(tt.rows);
           const uint32_t id = (uint32_t)(cols >> 3) << 17 | 1u << 23 | 8u << 24, d = tmem + acc.i * DC_ACC;
           if (!mbar_wait(&acc_empty[acc.i], acc.turn ^ 1u, abort_flag)) ok = false;
           uint32_t add = 0;
@@ -463,23 +467,30 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
               break;
             }
             tc_fence_after();
-            const uint32_t sf = tmem + DC_SF + sb.i * 12;
-            const uint64_t sfb = sfb0 + (uint32_t)(sb.i * L.sfb_bytes >> 4);
-            cp_scales(sf, sfa0 + (uint32_t)(sb.i * 32));
-            cp_scales(sf + 4, sfb);
-            if (cols > 128) cp_scales(sf + 8, sfb + 32);
-            const uint64_t ad = ad0 + (uint32_t)(sa.i * (DC_A_BYTES >> 4)), bd = bd0 + (uint32_t)(sb.i * L.b_bytes >> 4);
-            auto block = [&](int k, uint32_t plus) {
-              mma_mx1(d, ad + 2 * k, bd + 2 * k, id | (uint32_t)k << 4 | (uint32_t)k << 29, sf, sf + 4, plus);
-            };
-            if (tail == 4 || r.k + c + 1 < s.kt) {
-              block(0, add), block(1, 1), block(2, 1), block(3, 1);
-            } else {
-              block(0, add);
-              if (tail > 1) block(1, 1);
-              if (tail > 2) block(2, 1);
+            const uint32_t at_b = (uint32_t)(sb.i * L.b_bytes);
+#pragma unroll
+            for (int g = 0; g < DC_G; ++g) {
+              const int left = kt - (r.k + c) * DC_G - g;   // tiles of the row from this one on
+              if (left <= 0) break;
+              const uint32_t sf = tmem + DC_SF + (sb.i * DC_G + g) * 12;
+              const uint64_t sfb = sfb0 + (at_b + (uint32_t)(DC_G * tt.rows * 128 + g * tt.sf) >> 4);
+              cp_scales(sf, sfa0 + (uint32_t)((sb.i * DC_G + g) * 32));
+              cp_scales(sf + 4, sfb);
+              if (cols > 128) cp_scales(sf + 8, sfb + 32);
+              const uint64_t ad = ad0 + (uint32_t)(sa.i * DC_A_BYTES + g * DC_TILE >> 4);
+              const uint64_t bd = bd0 + (at_b + (uint32_t)(g * tt.rows * 128) >> 4);
+              auto block = [&](int k, uint32_t plus) {
+                mma_mx1(d, ad + 2 * k, bd + 2 * k, id | (uint32_t)k << 4 | (uint32_t)k << 29, sf, sf + 4, plus);
+              };
+              if (tail == 4 || left > 1) {
+                block(0, add), block(1, 1), block(2, 1), block(3, 1);
+              } else {
+                block(0, add);
+                if (tail > 1) block(1, 1);
+                if (tail > 2) block(2, 1);
+              }
+              add = 1;
             }
-            add = 1;
             tc_commit(&a_empty[sa.i]);
             tc_commit(&b_empty[sb.i]);
             sa.step(1, L.sa);
@@ -504,26 +515,26 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       bool ok = true;
       for (int ph = 0; ph < 2 && ok; ++ph) {
         const Stream& s = ph ? s2 : s1;
-        const int nt = ph ? 3 : 2;
-        if (ph == 1 && !came(a.meets + 32, grid, a.status, abort_flag)) break;
+        const int nt = ph ? 3 : 2, kt = ph ? kt2 : kt1;
+        if (!came(ph ? 2 : 0, meets, a.status, abort_flag)) break;
         asm volatile("fence.proxy.async;" ::: "memory");
         for (Run r(s, cta); r.left > 0 && ok; r.next(s)) {
           const uint32_t ent = pl.ent[r.ent];
-          const int rows = (int)(ent >> 20) * nt;
-          const uint32_t bytes = (uint32_t)rows * 128, sfb = rows <= 32 ? (uint32_t)rows * 16 : rows <= 128 ? 512 : 1024;
-          const uint8_t* b = tile_of(ent, r.k, s.kt, nt);
-          const uint8_t* sb = sf_of(r.ent, r.k, s.kt);
-          const uint8_t* sa = (ph ? a.s2 : a.s1) + (((int64_t)(ent & 1023u) * s.rt + r.row) * s.kt + r.k) * 512;
-          for (int c = 0; c < r.n; ++c, ++i, b += bytes, sb += L.sfb_bytes, sa += 512, slot.step(1, L.sb)) {
+          const TermTiles tt((int)(ent >> 20) * nt);
+          const uint32_t bytes = (uint32_t)tt.bytes();
+          const uint8_t* b = terms_of(r.ent, ent, s.kp, nt) + (int64_t)r.k * bytes;
+          const uint8_t* sa = (ph ? a.s2 : a.s1) + (((int64_t)(ent & 1023u) * s.rt + r.row) * kt + r.k * DC_G) * 512;
+          int left = kt - r.k * DC_G;
+          for (int c = 0; c < r.n; ++c, ++i, b += bytes, sa += DC_G * 512, left -= DC_G, slot.step(1, L.sb)) {
             if (!mbar_wait(&b_empty[slot.i], slot.turn ^ 1u, abort_flag)) {
               ok = false;
               break;
             }
             uint64_t* bar = &b_full[slot.i];
-            mbar_expect_tx(bar, bytes + sfb + 512);
+            const uint32_t sfa = (uint32_t)min(left, DC_G) * 512;
+            mbar_expect_tx(bar, bytes + sfa);
             bulk_load(smem + L.b + slot.i * L.b_bytes, b, bytes, bar);
-            bulk_load(smem + L.sfb + slot.i * L.sfb_bytes, sb, sfb, bar);
-            bulk_load(smem + L.sfa + slot.i * 512, sa, 512, bar);
+            bulk_load(smem + L.sfa + slot.i * DC_G * 512, sa, sfa, bar);
           }
         }
       }
@@ -534,16 +545,37 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     }
     __syncwarp();
   } else {
+    // the first product's terms: sixteen threads a pair's piece
+    const int units = pl.num[0] * kt1, step = (int)grid * (DC_JOIN / 16), j = jt & 15;
+    for (int u = (jt >> 4) * (int)grid + (int)cta; u - (jt >> 4 & 1) * (int)grid < units; u += step) {
+      const bool on = u < units;                    // (a warp has two pieces, and shuffles)
+      const int place = on ? u / kt1 : 0, c = on ? u - place * kt1 : 0, k = c * 128 + j * 8;
+      const bool in = on && k < K1;
+      float v[8] = {};
+      if (in) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)(pl.order[place] / a.k) * a.ldx + k));
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
+      }
+      put(Two{}, v, place, c, kp1, j, in);
+    }
+    asm volatile("fence.proxy.async;" ::: "memory");   // bulk copies of other CTAs read them
+    bar_sync(2, DC_JOIN);
+    if (tid == 0) {
+      __threadfence();
+      come(0);
+    }
     // ======================= accumulators =======================
     Slot acc;
-    auto sums_of = [&](auto phase) {
-      constexpr int PH = decltype(phase)::value, NT = PH ? 3 : 2;
+    auto sums_of = [&](auto nt) {
+      constexpr int NT = decltype(nt)::value, PH = NT == 3;
       const Stream& s = PH ? s2 : s1;
       const int R = PH ? R2 : R1;
       for (Run r(s, cta); r.left > 0; r.next(s)) {
         const uint32_t ent = pl.ent[r.ent];
         const int first = (int)(ent >> 10 & 1023u), pairs = (int)(ent >> 20);
-        const int part = (int)(cta - s.owner(r.tile * s.kt));
+        const int part = (int)(cta - s.owner(r.tile * s.kp));
         const int row = r.row * 128 + warp * 32 + lane;
         float* dst = a.part + ((int64_t)part * nlive + first) * R + row;
         if (!mbar_wait(&acc_full[acc.i], acc.turn, abort_flag)) {
@@ -573,34 +605,46 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         acc.step(1, 2);
       }
     };
-    // partial sums of a tile in order, four neighbouring rows
-    auto gather = [&](const Stream& s, int R, int place, int ent, int row) {
-      const int parts = s.parts((uint32_t)ent * s.rt + row / 128);
-      const float4* p = reinterpret_cast<const float4*>(a.part + (int64_t)place * R + row);
-      const int64_t step = (int64_t)nlive * R / 4;
-      float4 v = __ldcg(p);
-      for (int i = 1; i < parts; ++i) {
-        const float4 u = __ldcg(p + i * step);
-        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-      }
-      return v;
+    // Partial sums in order, of four neighbouring rows each; N in flight together.
+    struct Parts {
+      const float4* p;
+      int n;
     };
-    using One = std::integral_constant<int, 0>;
-    using Two = std::integral_constant<int, 1>;
+    auto parts_of = [&](const Stream& s, int R, int place, int row) {
+      const uint32_t tile = (uint32_t)pl.ent_of[place] * s.rt + row / 128;
+      return Parts{reinterpret_cast<const float4*>(a.part + (int64_t)place * R + row), s.parts(tile)};
+    };
+    auto gather = [&](int R, const auto& src, auto& v) {
+      constexpr int N = std::extent_v<std::remove_reference_t<decltype(v)>>;
+      const int64_t step = (int64_t)nlive * R / 4;
+      int most = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        v[i] = src[i].n > 0 ? __ldcg(src[i].p) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        most = max(most, src[i].n);
+      }
+      for (int q = 1; q < most; ++q) {
+        float4 u[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) u[i] = q < src[i].n ? __ldcg(src[i].p + q * step) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i].x += u[i].x, v[i].y += u[i].y, v[i].z += u[i].z, v[i].w += u[i].w;
+      }
+    };
     // the accumulating warps come to meeting i and wait for it, with the others
     auto meeting = [&](int i) {
       if (epi) {
         bar_sync(1, 128);
         if (tid == 0) {
           __threadfence();
-          come(a.meets + 32 * i);
-          (void)came(a.meets + 32 * i, grid, a.status, abort_flag);
+          come(i);
+          (void)came(i, meets, a.status, abort_flag);
         }
       }
       bar_sync(2, DC_JOIN);
     };
-    if (epi) sums_of(One{});
-    meeting(0);
+    if (epi) sums_of(Two{});
+    meeting(1);
     // the activation, from the first product's partial sums, and its terms:
     // sixteen threads a pair's piece
     {
@@ -608,31 +652,29 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       for (int u = (jt >> 4) * (int)grid + (int)cta; u - (jt >> 4 & 1) * (int)grid < units; u += step) {
         const bool on = u < units;
         const int place = on ? u / kt2 : 0, c = on ? u - place * kt2 : 0, f = c * 128 + j * 8;
-        const int e = pl.ent_of[place];
-        const uint32_t ent = pl.ent[e];
         const bool in = on && f < a.F;
         float v[8] = {};
         if (in) {
+          const Parts g = parts_of(s1, R1, place, f), y = parts_of(s1, R1, place, a.F + f);
+          const Parts src[4] = {g, {g.p + 1, g.n}, y, {y.p + 1, y.n}};
+          float4 q[4];
+          gather(R1, src, q);
+          const float gs[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+          const float us[8] = {q[2].x, q[2].y, q[2].z, q[2].w, q[3].x, q[3].y, q[3].z, q[3].w};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float4 g = gather(s1, R1, place, e, f + 4 * h), y = gather(s1, R1, place, e, a.F + f + 4 * h);
-            v[4 * h] = g.x / (1.0f + expf(-g.x)) * y.x;
-            v[4 * h + 1] = g.y / (1.0f + expf(-g.y)) * y.y;
-            v[4 * h + 2] = g.z / (1.0f + expf(-g.z)) * y.z;
-            v[4 * h + 3] = g.w / (1.0f + expf(-g.w)) * y.w;
-          }
+          for (int i = 0; i < 8; ++i) v[i] = gs[i] / (1.0f + expf(-gs[i])) * us[i];
         }
-        put_terms<3>(v, tile_of(ent, c, kt2, 3), sf_of(e, c, kt2), (place - (int)(ent >> 10 & 1023u)) * 3, j, in);
+        put(Three{}, v, place, c, kp2, j, in);
       }
     }
     asm volatile("fence.proxy.async;" ::: "memory");
     bar_sync(2, DC_JOIN);
     if (tid == 0) {
       __threadfence();
-      come(a.meets + 32);
+      come(2);
     }
-    if (epi) sums_of(Two{});
-    meeting(2);
+    if (epi) sums_of(Three{});
+    meeting(3);
     // the weighted sum over a token's experts, four neighbouring columns a thread,
     // runs of eight threads' a CTA in turn
     {
@@ -640,12 +682,21 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       for (uint32_t i = (((uint32_t)jt >> 3) * grid + cta) * 8 + (jt & 7); i < tasks; i += DC_JOIN * grid) {
         const int t = (int)(i / per), h = (int)(i - (uint32_t)t * per) * 4;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int j = 0; j < a.k; ++j) {
-          const int place = pl.pos[t * a.k + j];
-          if (place == DC_DEAD) continue;
-          const float wj = pl.w[t * a.k + j];
-          const float4 v = gather(s2, R2, place, pl.ent_of[place], h);
-          o.x = fmaf(wj, v.x, o.x), o.y = fmaf(wj, v.y, o.y), o.z = fmaf(wj, v.z, o.z), o.w = fmaf(wj, v.w, o.w);
+        for (int j0 = 0; j0 < a.k; j0 += 8) {
+          Parts src[8];
+          float4 v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int place = j0 + j < a.k ? pl.pos[t * a.k + j0 + j] : DC_DEAD;
+            src[j] = place != DC_DEAD ? parts_of(s2, R2, place, h) : Parts{nullptr, 0};
+          }
+          gather(R2, src, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (src[j].n == 0) continue;
+            const float w = pl.w[t * a.k + j0 + j];
+            o.x = fmaf(w, v[j].x, o.x), o.y = fmaf(w, v[j].y, o.y), o.z = fmaf(w, v[j].z, o.z), o.w = fmaf(w, v[j].w, o.w);
+          }
         }
         *reinterpret_cast<uint2*>(a.out + (int64_t)t * a.H + h) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
       }
@@ -656,6 +707,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   tc_fence_after();
   if (warp == DC_WARP_MMA) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
+
+int64_t pieces_of(int64_t K) { return ((K + 127) / 128 + DC_G - 1) / DC_G; }
 
 // Largest number of partial sums of a tile, whatever the routing, when at least
 // `ents` entries are live: a run has at least `s` pieces.
@@ -668,7 +721,7 @@ int64_t most_parts(int64_t ents, int64_t rt, int64_t kt) {
 }
 // floats of the partial sums [parts][live pairs][R]: the most over any number of live pairs
 int64_t part_floats(int64_t P, int64_t R, int64_t K) {
-  const int64_t rt = (R + 127) / 128, kt = (K + 127) / 128;
+  const int64_t rt = (R + 127) / 128, kt = pieces_of(K);
   int64_t most = 0;
   for (int64_t ents = 1; (ents - 1) * DC_NB < P; ++ents) {
     const int64_t n = ents * DC_NB < P ? ents * DC_NB : P;
@@ -678,24 +731,19 @@ int64_t part_floats(int64_t P, int64_t R, int64_t K) {
   return most;
 }
 
-// bytes of the scales of a piece's terms
-constexpr int term_scale_bytes(int P) { return 3 * (P < DC_NB ? P : DC_NB) > 128 ? 1024 : 512; }
-
 DecodeSmem layout(int P, int max_ent, int max_smem) {
   DecodeSmem L{};
   const int nb = P < DC_NB ? P : DC_NB;
-  L.b_bytes = (up16(3 * nb) * 128 + 1023) / 1024 * 1024;
-  L.sfb_bytes = term_scale_bytes(P);
-  L.sb = nb <= 8 ? 8 : nb <= 16 ? 6 : nb <= 32 ? 4 : 3;
+  // (up to 8 rows that no term fills are read behind a tile, up to 512 bytes behind its scales)
+  L.b_bytes = (TermTiles(3 * nb).bytes() + 1023) / 1024 * 1024;
+  L.sb = nb <= 8 ? 4 : nb <= 32 ? 3 : 2;
   const int plan = 16 + max_ent * 4 + P * 10;
   const int bars = 8 * (2 * 16 + 2 * DC_MAX_BS + 8);
-  const int fixed = L.sb * (L.b_bytes + L.sfb_bytes + 512) + bars + plan + 64;
+  const int fixed = L.sb * (L.b_bytes + DC_G * 512) + 1024 + bars + plan + 64;
   L.sa = (max_smem - 2048 - fixed) / DC_A_BYTES;   // 1024 to align the rings, 1024 for what is static
-  if (L.sa > 13) L.sa = 13;
   L.b = L.sa * DC_A_BYTES;
-  L.sfa = L.b + L.sb * L.b_bytes;
-  L.sfb = L.sfa + L.sb * 512;
-  L.bars = L.sfb + L.sb * L.sfb_bytes;
+  L.sfa = L.b + L.sb * L.b_bytes + 1024;
+  L.bars = L.sfa + L.sb * DC_G * 512;
   L.plan = L.bars + bars;
   L.total = (L.plan + plan + 15) / 16 * 16;
   return L;
@@ -707,42 +755,35 @@ int64_t max_entries(int64_t P, int64_t E) { return (P < E ? P : E) + P / DC_NB; 
 
 // pieces are counted in 32 bits, times the CTAs
 bool decode_fits(int64_t P, int64_t E, int64_t H, int64_t F) {
-  const int64_t kh = (H + 127) / 128, kf = (F + 127) / 128, f2 = (2 * F + 127) / 128;
-  return max_entries(P, E) * kh * (f2 > kf ? f2 : kf) * DECODE_MAX_CTAS < (int64_t)1 << 32;
+  const int64_t h = (H + 127) / 128, f2 = (2 * F + 127) / 128, c1 = pieces_of(H) * f2, c2 = pieces_of(F) * h;
+  return max_entries(P, E) * (c1 > c2 ? c1 : c2) * DECODE_MAX_CTAS < (int64_t)1 << 32;
 }
 
-// What the workspace holds behind the counters: partial sums, terms, their
-// scales.  Both products' in turn in the same place.
+// What the workspace holds: partial sums, and terms with their scales; both
+// products' in turn in the same place.
 struct DecodeSpace {
-  int64_t parts, terms, scales;   // bytes
+  int64_t parts, terms;   // bytes
 };
 static DecodeSpace space_of(int64_t P, int64_t E, int64_t H, int64_t F) {
-  const int64_t p1 = part_floats(P, 2 * F, H), p2 = part_floats(P, H, F);
-  const int64_t kh = (H + 127) / 128, kf = (F + 127) / 128;
-  return {(p1 > p2 ? p1 : p2) * (int64_t)sizeof(float), P * 128 * (2 * kh > 3 * kf ? 2 * kh : 3 * kf),
-          max_entries(P, E) * (kh > kf ? kh : kf) * term_scale_bytes((int)P)};
+  const int64_t p1 = part_floats(P, 2 * F, H), p2 = part_floats(P, H, F), ents = max_entries(P, E);
+  auto terms = [&](int64_t K, int64_t nt) { return pieces_of(K) * DC_G * ((nt * P + 7 * ents) * 128 + 1024 * ents); };
+  const int64_t t1 = terms(H, 2), t2 = terms(F, 3);
+  return {(p1 > p2 ? p1 : p2) * (int64_t)sizeof(float), t1 > t2 ? t1 : t2};
 }
 
 int64_t decode_workspace_bytes(int64_t P, int64_t E, int64_t H, int64_t F) {
   const DecodeSpace w = space_of(P, E, H, F);
-  return DECODE_MEETS_BYTES + w.parts + w.terms + w.scales;
+  return w.parts + w.terms;
 }
 
 cudaError_t launch_decode(DecodeArgs a, void* workspace, int num_sms, int max_smem, cudaStream_t st) {
   a.P = a.T * a.k;
   a.max_ent = (int)max_entries(a.P, a.E);
   const DecodeSmem L = layout(a.P, a.max_ent, max_smem);
-  if (L.sa < 2 || (a.P > 32 && (a.E + a.P + 64) * 4 > L.sb * L.b_bytes)) return cudaErrorNotSupported;
-  const int64_t c1 = (int64_t)a.max_ent * ((2 * a.F + 127) / 128) * ((a.H + 127) / 128);
-  const int64_t c2 = (int64_t)a.max_ent * ((a.H + 127) / 128) * ((a.F + 127) / 128);
-  const int64_t c = c1 > c2 ? c1 : c2, want = (c + DECODE_MIN_RUN - 1) / DECODE_MIN_RUN;
-  int64_t grid = num_sms < DECODE_MAX_CTAS ? num_sms : DECODE_MAX_CTAS;
-  if (want < grid) grid = want;
+  if (num_sms > DECODE_MAX_CTAS || L.sa < 2 || (a.P > 32 && (a.E + a.P + 64) * 4 > L.sb * L.b_bytes)) return cudaErrorNotSupported;
   const DecodeSpace w = space_of(a.P, a.E, a.H, a.F);
-  a.meets = (uint32_t*)workspace;
-  a.part = (float*)((uint8_t*)workspace + DECODE_MEETS_BYTES);
-  a.terms = (uint8_t*)a.part + w.parts;
-  a.term_scales = a.terms + w.terms;
+  a.part = (float*)workspace;
+  a.terms = (uint8_t*)workspace + w.parts;
   a.stall = take_ring_stall_hook();
   CUtensorMap tm[2];
   const int64_t R[2] = {2 * (int64_t)a.F, a.H}, K[2] = {a.H, a.F};
@@ -756,7 +797,7 @@ cudaError_t launch_decode(DecodeArgs a, void* workspace, int num_sms, int max_sm
   cudaError_t e = cudaFuncSetAttribute(k_decode, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem - 1024);
   if (e != cudaSuccess) return e;
   void* args[] = {&tm[0], &tm[1], &a, const_cast<DecodeSmem*>(&L)};
-  return cudaLaunchCooperativeKernel((const void*)k_decode, dim3((unsigned)grid), dim3(DC_THREADS), args, L.total + 1024, st);
+  return cudaLaunchCooperativeKernel((const void*)k_decode, dim3((unsigned)num_sms), dim3(DC_THREADS), args, L.total + 1024, st);
 }
 
 }  // namespace fp8moe

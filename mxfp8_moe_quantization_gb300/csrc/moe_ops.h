@@ -54,9 +54,8 @@ struct SwigluArgs {
 // The expert layer of a few tokens (decode.cu).
 constexpr int DECODE_MAX_PAIRS = 1024;      // T * k
 constexpr int DECODE_ENTRY_PAIRS = 64;      // pairs that one reading of an expert serves
-constexpr int DECODE_MIN_RUN = 4;           // pieces a CTA takes at least: fewer CTAs, fewer partial sums
+constexpr int DECODE_MIN_RUN = 2;           // pieces a CTA takes at least: fewer CTAs, fewer partial sums
 constexpr int DECODE_MAX_CTAS = 160;        // the workspace is sized for as many
-constexpr int DECODE_MEETS_BYTES = 512;     // three counters, 128 bytes apart
 struct DecodeArgs {
   const uint16_t* x;     // [T, H] bf16, row stride ldx
   int64_t ldx;
@@ -66,9 +65,8 @@ struct DecodeArgs {
   const float* w;        // [T, k]
   const uint8_t *q1, *s1, *q2, *s2;
   uint16_t* out;         // [T, H]
-  uint32_t* meets;
   float* part;           // partial sums [parts][live pairs][rows]
-  uint8_t *terms, *term_scales;
+  uint8_t* terms;
   int* status;
   int stall;             // test hook: the first CTA never loads its first piece
 };
