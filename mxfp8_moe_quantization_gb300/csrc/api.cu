@@ -666,12 +666,12 @@ fp8moe_status fp8moe_swiglu_bwd(const void* dout, const void* h, int64_t ldh, in
 
 static bool decode_sizes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F) {
   return T >= 0 && k >= 1 && T <= fp8moe::DECODE_MAX_PAIRS / k && E >= 1 && E <= FP8MOE_MAX_GROUPS && H >= 32 && F >= 32 &&
-         H <= ((int64_t)1 << 20) && F <= ((int64_t)1 << 20) && fp8moe::decode_fits(T * k, E, H, F);
+         H <= ((int64_t)1 << 20) && F <= ((int64_t)1 << 20) && fp8moe::decode_fits(T, k, E, H, F);
 }
 
 int64_t fp8moe_mxfp8_moe_decode_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F) {
   if (!decode_sizes(T, k, E, H, F) || H % 32 || F % 32) return -1;
-  return fp8moe::decode_workspace_bytes(T * k, E, H, F);
+  return fp8moe::decode_workspace_bytes(T, k, E, H, F);
 }
 
 fp8moe_status fp8moe_mxfp8_moe_decode(const void* x, int64_t ldx, const int32_t* topk_idx, const float* topk_w, int64_t T,
@@ -683,7 +683,7 @@ fp8moe_status fp8moe_mxfp8_moe_decode(const void* x, int64_t ldx, const int32_t*
   if (T == 0) return FP8MOE_OK;
   if (!x || !topk_idx || !topk_w || !w1 || !w1_scale || !w2 || !w2_scale || !out || !workspace)
     return FP8MOE_ERR_INVALID_ARG;
-  if (workspace_bytes < fp8moe::decode_workspace_bytes(T * k, E, H, F)) return FP8MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < fp8moe::decode_workspace_bytes(T, k, E, H, F)) return FP8MOE_ERR_INVALID_ARG;
   if (!al16(x) || !al16(w1) || !al16(w1_scale) || !al16(w2) || !al16(w2_scale) || !al16(out) || !al16(workspace) ||
       (((uintptr_t)topk_idx | (uintptr_t)topk_w) & 3))
     return FP8MOE_ERR_ALIGNMENT;

@@ -18,13 +18,14 @@
 // Both products are one stream of 32 KB pieces (128 rows x 256 of K) over all
 // (expert, row tile, k) in order, cut into equal runs, one per CTA; a tile's
 // partial sums (fp32, at most a few per tile) go to the workspace and are added
-// in order after a grid-wide meeting.  The terms are made once, into the
-// workspace, as the tensor core reads them (128-byte swizzle, 128x4 scales): a
-// piece's share of them is one bulk copy.  The weights' producer takes no part in
-// the meetings: while the others add, it fills its ring with W2.
-// (With pieces of 128 of K the copies' issue set the pace, about 200 cycles each.)
+// in order after a grid-wide meeting.  The terms of x and of the activation are
+// made once, into the workspace, as the tensor core reads them, and copied to a
+// ring beside the weights'; through registers, as bulk copies queue behind the
+// weights' in flight.  The weights' producer takes no part in the meetings: while
+// the others add, it fills its ring with W2.
 //   warps 0-3  accumulators to partial sums;  4  weights by TMA;  5  MMA issue;
-//   6  terms and scales to shared memory;  0-3 and 7-13  terms, sums, results.
+//   6  scales to tensor memory;  7-14  terms to shared memory;  all but 4-6  terms
+//   and the final sums.
 #include <cuda.h>
 
 #include <type_traits>
@@ -38,24 +39,23 @@
 namespace fp8moe {
 namespace {
 
-constexpr int DC_THREADS = 448;
-constexpr int DC_WARP_TMA = 4, DC_WARP_MMA = 5, DC_WARP_B = 6;
-constexpr int DC_JOIN = DC_THREADS - 96;  // threads that make terms and add partial sums: all but those three warps'
+constexpr int DC_THREADS = 480;
+constexpr int DC_WARP_TMA = 4, DC_WARP_MMA = 5, DC_WARP_SF = 6, DC_WARP_B = 7;
+constexpr int DC_BWARPS = DC_THREADS / 32 - DC_WARP_B;
+constexpr int DC_JOIN = DC_THREADS - 96;  // threads that make terms and add partial sums: all but warps 4-6's
 constexpr int DC_G = 2;                   // tiles of 128 x 128 in a piece
 constexpr int DC_TILE = 128 * 128, DC_A_BYTES = DC_G * DC_TILE;
-constexpr int DC_NB = DECODE_ENTRY_PAIRS;   // pairs of one entry: a pass over an expert's weights
-constexpr int DC_ACC = 3 * DC_NB;         // TMEM columns of an accumulator
-constexpr int DC_SF = 2 * DC_ACC;         // first TMEM column of the scales: 12 per slot
-constexpr int DC_MAX_BS = 4;
-static_assert(DC_SF + 12 * DC_G * DC_MAX_BS <= 512, "tensor memory");
+constexpr int DC_MAX_SLOTS = 6;
 constexpr int DC_DEAD = 0xFFFF;
 
 __host__ __device__ constexpr int up16(int v) { return (v + 15) / 16 * 16; }
 
-// Shared memory: the ring of weights (sa slots, at 0), that of terms with the
-// terms and their scales and that of the weights' scales (sb slots each), the plan.
+// Shared memory: the rings of weights (at 0) and of their scales (sa slots), that
+// of terms and their scales (sb slots), the plan.
 struct DecodeSmem {
   int sa, sb, b_bytes;
+  int team, teams;                         // warps that fill a slot of terms together
+  int acc;                                 // tensor memory columns of an accumulator
   int sfa, b, bars, plan, total;
 };
 
@@ -69,7 +69,7 @@ struct TermTiles {
 };
 
 // The plan of a call, in shared memory: the live pairs (token, choice) in the
-// order of their experts, cut into entries of one expert and at most DC_NB pairs.
+// order of their experts, cut into entries of one expert and at most nb pairs.
 struct Plan {
   uint32_t* ent;      // expert | first pair << 10 | pairs << 20
   float* w;           // [P] weights of the pairs
@@ -103,8 +103,9 @@ FP8MOE_DEV void plan_warp(const DecodeArgs& a, const Plan& pl, int lane) {
     before += eq == e && q < lane;
     same += eq == e;
   }
-  const uint32_t heads = __ballot_sync(0xffffffffu, live && before == 0);
-  int ent = 0;
+  const bool head = live && before % a.nb == 0;
+  const uint32_t heads = __ballot_sync(0xffffffffu, head);
+  int ent = before / a.nb;
   for (int q = 0; q < P; ++q) {
     const int eq = __shfl_sync(0xffffffffu, e, q);
     ent += (heads >> q & 1) && eq < e;
@@ -116,7 +117,7 @@ FP8MOE_DEV void plan_warp(const DecodeArgs& a, const Plan& pl, int lane) {
   if (live) {
     pl.order[rank] = (uint16_t)lane;
     pl.ent_of[rank] = (uint16_t)ent;
-    if (before == 0) pl.ent[ent] = (uint32_t)e | (uint32_t)rank << 10 | (uint32_t)same << 20;
+    if (head) pl.ent[ent] = (uint32_t)e | (uint32_t)rank << 10 | (uint32_t)min(a.nb, same - before) << 20;
   }
   const int n = __popc(__ballot_sync(0xffffffffu, live));
   if (lane == 0) pl.num[0] = n, pl.num[1] = __popc(heads);
@@ -145,7 +146,7 @@ FP8MOE_DEV void plan_block(const DecodeArgs& a, const Plan& pl, int* scratch) {
   const int chunks = (a.E + 31) / 32;
   for (int c = warp; c < chunks; c += DC_THREADS / 32) {
     const int e = c * 32 + lane, n = e < a.E ? cnt[e] : 0;
-    const uint32_t own = (uint32_t)n << 16 | (uint32_t)((n + DC_NB - 1) / DC_NB);
+    const uint32_t own = (uint32_t)n << 16 | (uint32_t)((n + a.nb - 1) / a.nb);
     uint32_t v = own;
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
@@ -175,12 +176,12 @@ FP8MOE_DEV void plan_block(const DecodeArgs& a, const Plan& pl, int* scratch) {
     int before = 0, after = 0;
     for (int q = 0; q < p; ++q) before += ids[q] == e;
     const uint32_t base = (uint32_t)cnt[e] + (uint32_t)tot[e >> 5];
-    const int place = (int)(base >> 16) + before, ent = (int)(base & 0xFFFFu) + before / DC_NB;
+    const int place = (int)(base >> 16) + before, ent = (int)(base & 0xFFFFu) + before / a.nb;
     pl.order[place] = (uint16_t)p;
     pl.pos[p] = (uint16_t)place;
     pl.ent_of[place] = (uint16_t)ent;
-    if (before % DC_NB == 0) {
-      for (int q = p; q < a.P && after < DC_NB; ++q) after += ids[q] == e;
+    if (before % a.nb == 0) {
+      for (int q = p; q < a.P && after < a.nb; ++q) after += ids[q] == e;
       pl.ent[ent] = (uint32_t)e | (uint32_t)place << 10 | (uint32_t)after << 20;
     }
   }
@@ -255,34 +256,31 @@ FP8MOE_DEV void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "r"(taddr));
 }
 FP8MOE_DEV void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+// Grid-wide meetings: a counter each, to which every CTA of a launch adds one.
+// They are the library's own, per device, as no caller's memory starts at zero: a
+// CTA fills an SM's shared memory and the grid all SMs, so that no two launches
+// run at a time, and each leaves its counters one grid further.  (A CTA that gives
+// up still comes.)
+enum { MEET_X = 0, MEET_SUMS, MEET_ACT, MEET_END, DC_MEETS };
+__device__ unsigned long long g_meets[DC_MEETS][16];
 FP8MOE_DEV uint64_t ld_acquire_gpu(const unsigned long long* p) {
   uint64_t v;
   asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
   return v;
 }
-// Grid-wide meetings: a counter each, to which every CTA of a launch adds one.
-// They are the library's own, per device, as no caller's memory starts at zero:
-// a CTA fills an SM's shared memory and the grid all SMs, so that no two launches
-// ever run at a time, and each leaves every counter one grid further.
-constexpr int DC_MEETS = 4;
-__device__ unsigned long long g_meets[DC_MEETS * 16];
-// One CTA more at a meeting; the (bounded) wait until all have come.  One thread.
-// (A CTA whose own wait ran out still comes: the limit is twice that.)
-FP8MOE_DEV void come(int i) {
-  asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(g_meets + 16 * i) : "memory");
-}
-FP8MOE_DEV bool came(int i, uint64_t n, int* status, volatile int* abort_flag) {
-  const unsigned long long* count = g_meets + 16 * i;
-  if (ld_acquire_gpu(count) >= n) return true;
+// One thread comes for its CTA, which is at a barrier, and waits until the counter
+// says n: all have come.  (The limit is twice that of the waits before it.)
+FP8MOE_DEV void meet(unsigned long long* count, uint64_t n, int* status, volatile int* abort_flag) {
+  asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(count) : "memory");
+  if (ld_acquire_gpu(count) >= n) return;
   const uint64_t t0 = globaltimer();
   while (ld_acquire_gpu(count) < n) {
     if (globaltimer() - t0 > 2 * WAIT_LIMIT_NS) {
       set_status(status, FP8MOE_ERR_TIMEOUT);
       *abort_flag = 1;
-      return false;
+      return;
     }
   }
-  return true;
 }
 
 // two e4m3 codes -> their values
@@ -294,47 +292,57 @@ FP8MOE_DEV float2 e4m3x2_value(uint32_t c) {
   return v;
 }
 
-// Eight neighbouring values of a row, place 8 j in the piece, to NT terms each:
-// rows r0 .. of the piece's tile.  Four lanes hold a block.  A block that is not
-// finite becomes NaN, and so does its token.
+// NT terms of eight neighbouring values of a row, four lanes a block: codes, and
+// the byte of the first term's scale (each further one's is 5 less).  A block that
+// is not finite becomes NaN, and so does its token.
 template <int NT>
-FP8MOE_DEV void put_terms(float (&v)[8], uint8_t* tile, uint8_t* sf, int r0, int j, bool on) {
-  float m = 0.0f;
+struct Terms {
+  uint2 q[NT];
+  uint32_t byte;
+  bool finite;
+  FP8MOE_DEV explicit Terms(float (&v)[8]) {
+    float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[i])));
+    for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[i])));
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    const float u = __shfl_xor_sync(0xffffffffu, m, o);
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(u));
-  }
-  const uint32_t field = (__float_as_uint(m) >> 23) & 0xFFu;
-  // (blocks below 2^-110 are not scaled all the way up: the last term's byte stays above 0)
-  const uint32_t ef = field < 17u ? 17u : field;
-  const bool finite = field != 255u;
-  const float mul = __uint_as_float((261u - ef) << 23);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= mul;
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[i] = cvt_e4m3x2(v[2 * i], v[2 * i + 1]);
-      if (t + 1 < NT) {
-        const float2 b = e4m3x2_value(c[i]);
-        v[2 * i] = (v[2 * i] - b.x) * 32.0f;
-        v[2 * i + 1] = (v[2 * i + 1] - b.y) * 32.0f;
-      }
+    for (int o = 1; o < 4; o <<= 1) {
+      const float u = __shfl_xor_sync(0xffffffffu, m, o);
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(u));
     }
-    uint2 q = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-    if (!finite) q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    if (!on) continue;
-    const int r = r0 + t;
-    *reinterpret_cast<uint2*>(tile + r * 128 + (((j >> 1) ^ (r & 7)) << 4) + (j & 1) * 8) = q;
-    if ((j & 3) == 0)
-      sf[(r >> 7) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (j >> 2)] = (uint8_t)(finite ? ef - 7u - 5u * t : 127u);
+    const uint32_t field = (__float_as_uint(m) >> 23) & 0xFFu;
+    // (blocks below 2^-110 are not scaled all the way up: the last term's byte stays above 0)
+    const uint32_t ef = field < 17u ? 17u : field;
+    finite = field != 255u;
+    byte = ef - 7u;
+    const float mul = __uint_as_float((261u - ef) << 23);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= mul;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      uint32_t c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = cvt_e4m3x2(v[2 * i], v[2 * i + 1]);
+        if (t + 1 < NT) {
+          const float2 b = e4m3x2_value(c[i]);
+          v[2 * i] = (v[2 * i] - b.x) * 32.0f;
+          v[2 * i + 1] = (v[2 * i + 1] - b.y) * 32.0f;
+        }
+      }
+      q[t] = finite ? make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16) : make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    }
   }
-}
+  // to rows r0 .. of a tile, place 8 j in it: 128-byte swizzle; scales in 128x4 order
+  FP8MOE_DEV void put(uint8_t* tile, uint8_t* sf, int r0, int j) const {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = r0 + t;
+      *reinterpret_cast<uint2*>(tile + r * 128 + (((j >> 1) ^ (r & 7)) << 4) + (j & 1) * 8) = q[t];
+      if ((j & 3) == 0)
+        sf[(r >> 7) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (j >> 2)] = (uint8_t)(finite ? byte - 5u * t : 127u);
+    }
+  }
+};
 
 __global__ void __launch_bounds__(DC_THREADS, 1)
     k_decode(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2, DecodeArgs a, DecodeSmem L) {
@@ -349,26 +357,22 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   uint64_t* a_empty = a_full + L.sa;
   uint64_t* b_full = a_empty + L.sa;
   uint64_t* b_empty = b_full + L.sb;
-  uint64_t* acc_full = b_empty + L.sb;
+  uint64_t* sf_full = b_empty + L.sb;
+  uint64_t* acc_full = sf_full + L.sb;
   uint64_t* acc_empty = acc_full + 2;
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* drain = acc_empty + 2;   // the issuer's, the copier's
   const Plan pl(smem + L.plan, a.P, a.max_ent);
   auto fail = [&]() {
     set_status(a.status, FP8MOE_ERR_TIMEOUT);
     *abort_flag = 1;
   };
-  // every meeting's count when all have come: the last one's stands still until
-  // this CTA has been at the others
-  uint64_t meets;
-  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(meets) : "l"(g_meets + 16 * (DC_MEETS - 1)));
-  meets += grid;
 
   if (warp == DC_WARP_TMA && lane == 0) {
     abort_s = 0;
     for (int i = 0; i < L.sa; ++i) mbar_init(&a_full[i], 1), mbar_init(&a_empty[i], 1);
-    for (int i = 0; i < L.sb; ++i) mbar_init(&b_full[i], 1), mbar_init(&b_empty[i], 1);
+    for (int i = 0; i < L.sb; ++i) mbar_init(&b_full[i], L.team), mbar_init(&b_empty[i], 1), mbar_init(&sf_full[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 4);
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1), mbar_init(&drain[1], 1);
     mbar_fence_init();
   }
   if (warp == DC_WARP_MMA) {
@@ -376,6 +380,18 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     tc_fence_before();
   }
+  const int K1 = a.H, K2 = a.F, R1 = 2 * a.F, R2 = a.H;
+  const int kt1 = (K1 + 127) / 128, kt2 = (K2 + 127) / 128;
+  const bool epi = warp < 4;
+  const int jt = epi ? tid : tid - 96;             // thread among those that make terms and add
+  // The terms' units: a tile of a row, sixteen threads each, a warp's two a grid apart.
+  const int unit0 = (jt >> 4) * (int)grid + (int)cta, unit_step = (int)grid * (DC_JOIN / 16), j16 = jt & 15;
+  auto x_at = [&](int u) {                         // this thread's eight values of x
+    const int t = u / kt1, k = (u - t * kt1) * 128 + j16 * 8;
+    return u < a.T * kt1 && k < K1 ? __ldg(reinterpret_cast<const uint4*>(a.x + t * a.ldx + k)) : make_uint4(0, 0, 0, 0);
+  };
+  uint4 x0 = make_uint4(0, 0, 0, 0);               // the first unit's, on its way while the plan is made
+  if (warp < DC_WARP_TMA || warp >= DC_WARP_B) x0 = x_at(unit0);
   if (a.P <= 32) {
     if (warp == DC_WARP_TMA) plan_warp(a, pl, lane);
     __syncthreads();
@@ -385,29 +401,9 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_s;
   const int nlive = pl.num[0], nent = pl.num[1];
-
-  const int K1 = a.H, K2 = a.F, R1 = 2 * a.F, R2 = a.H;
-  const int rt1 = (R1 + 127) / 128, kt1 = (K1 + 127) / 128, rt2 = (R2 + 127) / 128, kt2 = (K2 + 127) / 128;
-  const int kp1 = (kt1 + DC_G - 1) / DC_G, kp2 = (kt2 + DC_G - 1) / DC_G;
-  const Stream s1(nent, rt1, kp1, grid), s2(nent, rt2, kp2, grid);
-  const bool epi = warp < 4;
-  const int jt = epi ? tid : tid - 96;             // thread among those that make terms and add
-  // an entry's terms in the workspace
-  auto terms_of = [&](int e, uint32_t ent, int kp, int nt) {
-    return a.terms + (int64_t)kp * DC_G * ((nt * (int)(ent >> 10 & 1023u) + 7 * e) * 128 + 1024 * e);
-  };
-  // terms of eight values, place 8 j of tile c, of the pair at `place`
-  auto put = [&](auto nt, float (&v)[8], int place, int c, int kp, int j, bool on) {
-    constexpr int NT = decltype(nt)::value;
-    const int e = pl.ent_of[place];
-    const uint32_t ent = pl.ent[e];
-    const TermTiles tt((int)(ent >> 20) * NT);
-    uint8_t* p = terms_of(e, ent, kp, NT) + (int64_t)(c / DC_G) * tt.bytes();
-    put_terms<NT>(v, p + c % DC_G * tt.rows * 128, p + DC_G * tt.rows * 128 + c % DC_G * tt.sf,
-                  (place - (int)(ent >> 10 & 1023u)) * NT, j, on);
-  };
-  using Two = std::integral_constant<int, 2>;     // terms of a bf16 value, of an fp32 one
-  using Three = std::integral_constant<int, 3>;
+  const Stream s1(nent, (R1 + 127) / 128, (kt1 + DC_G - 1) / DC_G, grid), s2(nent, (R2 + 127) / 128, (kt2 + DC_G - 1) / DC_G, grid);
+  using Two = std::integral_constant<int, 2>;     // terms of a bf16 value: the first product's
+  using Three = std::integral_constant<int, 3>;   // of an fp32 value: the second's
 
   if (warp == DC_WARP_TMA) {
     // ======================= weights =======================
@@ -422,7 +418,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         for (Run r(s, cta); r.left > 0 && ok; r.next(s)) {
           const int e = (int)(pl.ent[r.ent] & 1023u);
           int x = r.k * DC_G;   // the piece's first tile
-          for (int c = 0; c < r.n; ++c, ++i, x += DC_G, slot.step(1, L.sa)) {
+          const uint8_t* sc = (ph ? a.s2 : a.s1) + (((int64_t)e * s.rt + r.row) * kt + x) * 512;
+          for (int c = 0; c < r.n; ++c, ++i, x += DC_G, sc += DC_G * 512, slot.step(1, L.sa)) {
             uint64_t* bar = &a_full[slot.i];
             if (!mbar_wait(&a_empty[slot.i], slot.turn ^ 1u, abort_flag)) {
               ok = false;
@@ -430,10 +427,12 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
             }
             if (a.stall && cta == 0 && i == 0) continue;
             const int tiles = min(DC_G, kt - x);
-            mbar_expect_tx(bar, tiles * DC_TILE);
+            uint8_t* dst = smem + slot.i * DC_A_BYTES;
+            mbar_expect_tx(bar, tiles * (DC_TILE + 512));
 #pragma unroll
             for (int g = 0; g < DC_G; ++g)
-              if (g < tiles) tma_load_3d(smem + slot.i * DC_A_BYTES + g * DC_TILE, tm, bar, (x + g) * 128, r.row * 128, e);
+              if (g < tiles) tma_load_3d(dst + g * DC_TILE, tm, bar, (x + g) * 128, r.row * 128, e);
+            bulk_load(smem + L.sfa + slot.i * DC_G * 512, sc, tiles * 512, bar);
           }
         }
       }
@@ -449,7 +448,6 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     if (lane == 0) {
       Slot sa, sb, acc;
       const uint64_t ad0 = sdesc_sw128(smem_u32(smem)), bd0 = sdesc_sw128(smem_u32(smem + L.b));
-      const uint64_t sfa0 = sdesc_scales(smem_u32(smem + L.sfa)), sfb0 = sdesc_scales(smem_u32(smem + L.b));
       bool ok = true;
       for (int ph = 0; ph < 2 && ok; ++ph) {
         const Stream& s = ph ? s2 : s1;
@@ -458,11 +456,12 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         for (Run r(s, cta); r.left > 0 && ok; r.next(s)) {
           const TermTiles tt((int)(pl.ent[r.ent] >> 20) * (ph ? 3 : 2));
           const int cols = up16(tt.rows);
-          const uint32_t id = (uint32_t)(cols >> 3) << 17 | 1u << 23 | 8u << 24, d = tmem + acc.i * DC_ACC;
+          const uint32_t id = (uint32_t)(cols >> 3) << 17 | 1u << 23 | 8u << 24, d = tmem + acc.i * L.acc;
           if (!mbar_wait(&acc_empty[acc.i], acc.turn ^ 1u, abort_flag)) ok = false;
           uint32_t add = 0;
           for (int c = 0; c < r.n; ++c) {
-            if (!ok || !mbar_wait(&a_full[sa.i], sa.turn, abort_flag) || !mbar_wait(&b_full[sb.i], sb.turn, abort_flag)) {
+            if (!ok || !mbar_wait(&a_full[sa.i], sa.turn, abort_flag) || !mbar_wait(&b_full[sb.i], sb.turn, abort_flag) ||
+                !mbar_wait(&sf_full[sb.i], sb.turn, abort_flag)) {
               ok = false;
               break;
             }
@@ -472,13 +471,9 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
             for (int g = 0; g < DC_G; ++g) {
               const int left = kt - (r.k + c) * DC_G - g;   // tiles of the row from this one on
               if (left <= 0) break;
-              const uint32_t sf = tmem + DC_SF + (sb.i * DC_G + g) * 12;
-              const uint64_t sfb = sfb0 + (at_b + (uint32_t)(DC_G * tt.rows * 128 + g * tt.sf) >> 4);
-              cp_scales(sf, sfa0 + (uint32_t)((sb.i * DC_G + g) * 32));
-              cp_scales(sf + 4, sfb);
-              if (cols > 128) cp_scales(sf + 8, sfb + 32);
-              const uint64_t ad = ad0 + (uint32_t)(sa.i * DC_A_BYTES + g * DC_TILE >> 4);
-              const uint64_t bd = bd0 + (at_b + (uint32_t)(g * tt.rows * 128) >> 4);
+              const uint32_t sf = tmem + 2 * L.acc + (sb.i * DC_G + g) * 12;
+              const uint64_t ad = ad0 + ((uint32_t)(sa.i * DC_A_BYTES + g * DC_TILE) >> 4);
+              const uint64_t bd = bd0 + ((at_b + (uint32_t)(g * tt.rows * 128)) >> 4);
               auto block = [&](int k, uint32_t plus) {
                 mma_mx1(d, ad + 2 * k, bd + 2 * k, id | (uint32_t)k << 4 | (uint32_t)k << 29, sf, sf + 4, plus);
               };
@@ -503,87 +498,170 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       }
       if (!ok) fail();
       // every product has completed before tensor memory is given back
-      tc_commit(drain);
-      if (!mbar_wait(drain, 0, nullptr)) set_status(a.status, FP8MOE_ERR_TIMEOUT);
+      tc_commit(&drain[0]);
+      if (!mbar_wait(&drain[0], 0, nullptr)) set_status(a.status, FP8MOE_ERR_TIMEOUT);
     }
     __syncwarp();
-  } else if (warp == DC_WARP_B) {
-    // ======================= terms and scales =======================
+  } else if (warp == DC_WARP_SF) {
+    // ======================= scales to tensor memory =======================
+    // From a thread of their own the copies overlap the products.  A slot's columns
+    // are free when its terms are new: the products of its last turn are over.
     if (lane == 0) {
-      Slot slot;
-      uint32_t i = 0;
+      Slot sa, sb;
+      const uint64_t sfa0 = sdesc_scales(smem_u32(smem + L.sfa)), sfb0 = sdesc_scales(smem_u32(smem + L.b));
       bool ok = true;
       for (int ph = 0; ph < 2 && ok; ++ph) {
         const Stream& s = ph ? s2 : s1;
-        const int nt = ph ? 3 : 2, kt = ph ? kt2 : kt1;
-        if (!came(ph ? 2 : 0, meets, a.status, abort_flag)) break;
-        asm volatile("fence.proxy.async;" ::: "memory");
+        const int kt = ph ? kt2 : kt1;
         for (Run r(s, cta); r.left > 0 && ok; r.next(s)) {
-          const uint32_t ent = pl.ent[r.ent];
-          const TermTiles tt((int)(ent >> 20) * nt);
-          const uint32_t bytes = (uint32_t)tt.bytes();
-          const uint8_t* b = terms_of(r.ent, ent, s.kp, nt) + (int64_t)r.k * bytes;
-          const uint8_t* sa = (ph ? a.s2 : a.s1) + (((int64_t)(ent & 1023u) * s.rt + r.row) * kt + r.k * DC_G) * 512;
-          int left = kt - r.k * DC_G;
-          for (int c = 0; c < r.n; ++c, ++i, b += bytes, sa += DC_G * 512, left -= DC_G, slot.step(1, L.sb)) {
-            if (!mbar_wait(&b_empty[slot.i], slot.turn ^ 1u, abort_flag)) {
+          const TermTiles tt((int)(pl.ent[r.ent] >> 20) * (ph ? 3 : 2));
+          for (int c = 0; c < r.n; ++c) {
+            if (!mbar_wait(&a_full[sa.i], sa.turn, abort_flag) || !mbar_wait(&b_full[sb.i], sb.turn, abort_flag)) {
               ok = false;
               break;
             }
-            uint64_t* bar = &b_full[slot.i];
-            const uint32_t sfa = (uint32_t)min(left, DC_G) * 512;
-            mbar_expect_tx(bar, bytes + sfa);
-            bulk_load(smem + L.b + slot.i * L.b_bytes, b, bytes, bar);
-            bulk_load(smem + L.sfa + slot.i * DC_G * 512, sa, sfa, bar);
+            tc_fence_after();
+#pragma unroll
+            for (int g = 0; g < DC_G; ++g) {
+              if ((r.k + c) * DC_G + g >= kt) break;
+              const uint32_t sf = tmem + 2 * L.acc + (sb.i * DC_G + g) * 12;
+              const uint64_t sfb = sfb0 + ((uint32_t)(sb.i * L.b_bytes + DC_G * tt.rows * 128 + g * tt.sf) >> 4);
+              cp_scales(sf, sfa0 + (uint32_t)((sa.i * DC_G + g) * 32));
+              cp_scales(sf + 4, sfb);
+              if (tt.rows > 128) cp_scales(sf + 8, sfb + 32);
+            }
+            tc_commit(&sf_full[sb.i]);
+            sa.step(1, L.sa);
+            sb.step(1, L.sb);
           }
         }
       }
       if (!ok) fail();
-      if (*abort_flag)
-        for (uint32_t n = i > (uint32_t)L.sb ? i - L.sb : 0; n < i; ++n)
-          (void)mbar_wait(&b_full[n % L.sb], (n / (uint32_t)L.sb) & 1u, nullptr);
+      tc_commit(&drain[1]);
+      if (!mbar_wait(&drain[1], 0, nullptr)) set_status(a.status, FP8MOE_ERR_TIMEOUT);
     }
     __syncwarp();
   } else {
-    // the first product's terms: sixteen threads a pair's piece
-    const int units = pl.num[0] * kt1, step = (int)grid * (DC_JOIN / 16), j = jt & 15;
-    for (int u = (jt >> 4) * (int)grid + (int)cta; u - (jt >> 4 & 1) * (int)grid < units; u += step) {
-      const bool on = u < units;                    // (a warp has two pieces, and shuffles)
-      const int place = on ? u / kt1 : 0, c = on ? u - place * kt1 : 0, k = c * 128 + j * 8;
-      const bool in = on && k < K1;
-      float v[8] = {};
-      if (in) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)(pl.order[place] / a.k) * a.ldx + k));
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    // every meeting's count when all have come: the last one's stands still until
+    // this CTA has been at the others
+    uint64_t meets;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(meets) : "l"(g_meets[MEET_END]));
+    meets += grid;
+    auto meeting = [&](int i) {
+      bar_sync(2, DC_JOIN);
+      if (tid == 0) meet(g_meets[i], meets, a.status, abort_flag);
+      bar_sync(2, DC_JOIN);
+    };
+
+    // Partial sums in order, of four neighbouring rows each; N in flight together.
+    struct Parts {
+      const float4* p;
+      int n;
+    };
+    auto parts_of = [&](const Stream& s, const float* part, int R, int place, int row) {
+      const uint32_t tile = (uint32_t)pl.ent_of[place] * s.rt + row / 128;
+      return Parts{reinterpret_cast<const float4*>(part + (int64_t)place * R + row), s.parts(tile)};
+    };
+    auto gather = [&](int R, const auto& src, auto& v) {
+      constexpr int N = std::extent_v<std::remove_reference_t<decltype(v)>>;
+      const int64_t step = (int64_t)nlive * R / 4;
+      int most = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
+      for (int i = 0; i < N; ++i) {
+        v[i] = src[i].n > 0 ? __ldcg(src[i].p) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        most = max(most, src[i].n);
       }
-      put(Two{}, v, place, c, kp1, j, in);
-    }
-    asm volatile("fence.proxy.async;" ::: "memory");   // bulk copies of other CTAs read them
-    bar_sync(2, DC_JOIN);
-    if (tid == 0) {
-      __threadfence();
-      come(0);
-    }
-    // ======================= accumulators =======================
+      for (int q = 1; q < most; ++q) {
+        float4 u[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) u[i] = q < src[i].n ? __ldcg(src[i].p + q * step) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i].x += u[i].x, v[i].y += u[i].y, v[i].z += u[i].z, v[i].w += u[i].w;
+      }
+    };
+    // eight values of the activation, from the first product's partial sums
+    auto act_at = [&](int place, int f, float (&v)[8]) {
+      const Parts g = parts_of(s1, a.part1, R1, place, f), y = parts_of(s1, a.part1, R1, place, a.F + f);
+      const Parts src[4] = {g, {g.p + 1, g.n}, y, {y.p + 1, y.n}};
+      float4 q[4];
+      gather(R1, src, q);
+      const float gs[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+      const float us[8] = {q[2].x, q[2].y, q[2].z, q[2].w, q[3].x, q[3].y, q[3].z, q[3].w};
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] = gs[c] / (1.0f + expf(-gs[c])) * us[c];
+    };
+    // where an entry's terms are in the workspace
+    auto terms_of = [&](int e, uint32_t ent, int kp, int nt) {
+      return a.terms + (int64_t)kp * DC_G * ((nt * (int)(ent >> 10 & 1023u) + 7 * e) * 128 + 1024 * e);
+    };
+
+    // ======================= terms into shared memory =======================
+    // Teams of warps take the pieces of both runs in turn.  (Not more teams than
+    // slots: a slot's barrier tells the last turn from the one before, and a team
+    // that has filled its last piece knows that the slots' turns before are over.)
+    const int team = (warp - DC_WARP_B) / L.team, rank = (warp - DC_WARP_B) - team * L.team;
+    uint32_t piece = (uint32_t)team;
+    int ahead = team;                                // pieces before the team's next one
+    auto feed = [&](auto nt) {
+      constexpr int NT = decltype(nt)::value;
+      const Stream& s = NT == 2 ? s1 : s2;
+      Run r(s, cta);
+      int c = ahead;                                 // the team's next piece, counted in segment r
+      for (; team < L.teams; c += L.teams, piece += L.teams) {
+        while (r.left > 0 && c >= r.n) {
+          c -= r.n;
+          r.next(s);
+        }
+        if (r.left == 0) break;
+        const uint32_t ent = pl.ent[r.ent], turn = piece / (uint32_t)L.sb;
+        const int slot = (int)(piece - turn * (uint32_t)L.sb);
+        const TermTiles tt((int)(ent >> 20) * NT);
+        uint4* dst = reinterpret_cast<uint4*>(smem + L.b + slot * L.b_bytes);
+        const uint4* src = reinterpret_cast<const uint4*>(terms_of(r.ent, ent, s.kp, NT) + (int64_t)(r.k + c) * tt.bytes());
+        // 16 bytes at a time, 4 KB in flight a warp
+        const int chunks = tt.bytes() / 16, at = rank * 32 + lane, step = L.team * 32;
+        bool ready = false, ok = true;
+        for (int i0 = at; i0 - lane < chunks; i0 += 8 * step) {
+          uint4 q[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i0 + step * i < chunks) q[i] = __ldcg(src + i0 + step * i);
+          if (!ready) ok = __all_sync(0xffffffffu, mbar_wait(&b_empty[slot], (turn & 1u) ^ 1u, abort_flag));
+          ready = true;
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i0 + step * i < chunks) dst[i0 + step * i] = q[i];
+        }
+        if (!ok) {
+          fail();
+          break;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_full[slot]);
+      }
+      ahead = c;                                     // past the run's end: into the next run
+    };
+    // ======================= accumulators to partial sums =======================
     Slot acc;
-    auto sums_of = [&](auto nt) {
-      constexpr int NT = decltype(nt)::value, PH = NT == 3;
-      const Stream& s = PH ? s2 : s1;
-      const int R = PH ? R2 : R1;
+    auto drain_acc = [&](auto nt) {
+      constexpr int NT = decltype(nt)::value;
+      const Stream& s = NT == 2 ? s1 : s2;
+      const int R = NT == 2 ? R1 : R2;
+      float* part = NT == 2 ? a.part1 : a.part2;
       for (Run r(s, cta); r.left > 0; r.next(s)) {
         const uint32_t ent = pl.ent[r.ent];
         const int first = (int)(ent >> 10 & 1023u), pairs = (int)(ent >> 20);
-        const int part = (int)(cta - s.owner(r.tile * s.kp));
+        const int mine = (int)(cta - s.owner(r.tile * s.kp));
         const int row = r.row * 128 + warp * 32 + lane;
-        float* dst = a.part + ((int64_t)part * nlive + first) * R + row;
+        float* dst = part + ((int64_t)mine * nlive + first) * R + row;
         if (!mbar_wait(&acc_full[acc.i], acc.turn, abort_flag)) {
           fail();
           break;
         }
         tc_fence_after();
-        const uint32_t src = tmem + acc.i * DC_ACC + ((uint32_t)(warp * 32) << 16);
+        const uint32_t src = tmem + acc.i * L.acc + ((uint32_t)(warp * 32) << 16);
         for (int i0 = 0; i0 < pairs; i0 += 8) {
           uint32_t q[24];
 #pragma unroll
@@ -605,101 +683,73 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         acc.step(1, 2);
       }
     };
-    // Partial sums in order, of four neighbouring rows each; N in flight together.
-    struct Parts {
-      const float4* p;
-      int n;
+    // ======================= terms into the workspace =======================
+    auto put = [&](const auto& terms, int place, int c, int kp) {
+      constexpr int NT = sizeof(terms.q) / sizeof(uint2);
+      const int e = pl.ent_of[place];
+      const uint32_t ent = pl.ent[e];
+      const TermTiles tt((int)(ent >> 20) * NT);
+      uint8_t* p = terms_of(e, ent, kp, NT) + (int64_t)(c / DC_G) * tt.bytes();
+      terms.put(p + c % DC_G * tt.rows * 128, p + DC_G * tt.rows * 128 + c % DC_G * tt.sf,
+                (place - (int)(ent >> 10 & 1023u)) * NT, j16);
     };
-    auto parts_of = [&](const Stream& s, int R, int place, int row) {
-      const uint32_t tile = (uint32_t)pl.ent_of[place] * s.rt + row / 128;
-      return Parts{reinterpret_cast<const float4*>(a.part + (int64_t)place * R + row), s.parts(tile)};
-    };
-    auto gather = [&](int R, const auto& src, auto& v) {
-      constexpr int N = std::extent_v<std::remove_reference_t<decltype(v)>>;
-      const int64_t step = (int64_t)nlive * R / 4;
-      int most = 0;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        v[i] = src[i].n > 0 ? __ldcg(src[i].p) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        most = max(most, src[i].n);
-      }
-      for (int q = 1; q < most; ++q) {
-        float4 u[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) u[i] = q < src[i].n ? __ldcg(src[i].p + q * step) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i].x += u[i].x, v[i].y += u[i].y, v[i].z += u[i].z, v[i].w += u[i].w;
-      }
-    };
-    // the accumulating warps come to meeting i and wait for it, with the others
-    auto meeting = [&](int i) {
-      if (epi) {
-        bar_sync(1, 128);
-        if (tid == 0) {
-          __threadfence();
-          come(i);
-          (void)came(i, meets, a.status, abort_flag);
-        }
-      }
-      bar_sync(2, DC_JOIN);
-    };
-    if (epi) sums_of(Two{});
-    meeting(1);
-    // the activation, from the first product's partial sums, and its terms:
-    // sixteen threads a pair's piece
-    {
-      const int units = nlive * kt2, step = (int)grid * (DC_JOIN / 16), j = jt & 15;
-      for (int u = (jt >> 4) * (int)grid + (int)cta; u - (jt >> 4 & 1) * (int)grid < units; u += step) {
-        const bool on = u < units;
-        const int place = on ? u / kt2 : 0, c = on ? u - place * kt2 : 0, f = c * 128 + j * 8;
-        const bool in = on && f < a.F;
-        float v[8] = {};
-        if (in) {
-          const Parts g = parts_of(s1, R1, place, f), y = parts_of(s1, R1, place, a.F + f);
-          const Parts src[4] = {g, {g.p + 1, g.n}, y, {y.p + 1, y.n}};
-          float4 q[4];
-          gather(R1, src, q);
-          const float gs[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
-          const float us[8] = {q[2].x, q[2].y, q[2].z, q[2].w, q[3].x, q[3].y, q[3].z, q[3].w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = gs[i] / (1.0f + expf(-gs[i])) * us[i];
-        }
-        put(Three{}, v, place, c, kp2, j, in);
-      }
+    const int back = (jt >> 4 & 1) * (int)grid;     // a warp stays together for its shuffles
+    // x, a token's for all its experts
+    for (int u = unit0, units = a.T * kt1; u - back < units; u += unit_step) {
+      const uint4 q = u == unit0 ? x0 : x_at(u);
+      float v[8] = {bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y), bf16_lo(q.z), bf16_hi(q.z), bf16_lo(q.w), bf16_hi(q.w)};
+      const Terms<2> terms(v);
+      const int t = u / kt1, c = u - t * kt1;
+      if (u < units && c * 128 + j16 * 8 < K1)
+        for (int i = t * a.k; i < (t + 1) * a.k; ++i)
+          if (pl.pos[i] != DC_DEAD) put(terms, pl.pos[i], c, s1.kp);
     }
-    asm volatile("fence.proxy.async;" ::: "memory");
-    bar_sync(2, DC_JOIN);
-    if (tid == 0) {
-      __threadfence();
-      come(2);
+    meeting(MEET_X);
+    if (epi) {
+      drain_acc(Two{});
+    } else {
+      feed(Two{});
     }
-    if (epi) sums_of(Three{});
-    meeting(3);
+    meeting(MEET_SUMS);
+    // the activation
+    for (int u = unit0, units = nlive * kt2; u - back < units; u += unit_step) {
+      const int place = u < units ? u / kt2 : 0, c = u - place * kt2, f = c * 128 + j16 * 8;
+      const bool in = u < units && f < K2;
+      float v[8] = {};
+      if (in) act_at(place, f, v);
+      const Terms<3> terms(v);
+      if (in) put(terms, place, c, s2.kp);
+    }
+    meeting(MEET_ACT);
+    if (epi) {
+      drain_acc(Three{});
+    } else {
+      feed(Three{});
+    }
+    meeting(MEET_END);
     // the weighted sum over a token's experts, four neighbouring columns a thread,
     // runs of eight threads' a CTA in turn
-    {
-      const uint32_t per = (uint32_t)a.H / 4, tasks = (uint32_t)a.T * per;
-      for (uint32_t i = (((uint32_t)jt >> 3) * grid + cta) * 8 + (jt & 7); i < tasks; i += DC_JOIN * grid) {
-        const int t = (int)(i / per), h = (int)(i - (uint32_t)t * per) * 4;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int j0 = 0; j0 < a.k; j0 += 8) {
-          Parts src[8];
-          float4 v[8];
+    const uint32_t per = (uint32_t)a.H / 4, tasks = (uint32_t)a.T * per;
+    for (uint32_t i = (((uint32_t)jt >> 3) * grid + cta) * 8 + (jt & 7); i < tasks; i += DC_JOIN * grid) {
+      const int t = (int)(i / per), h = (int)(i - (uint32_t)t * per) * 4;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int j0 = 0; j0 < a.k; j0 += 8) {
+        Parts src[8];
+        float4 v[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int place = j0 + j < a.k ? pl.pos[t * a.k + j0 + j] : DC_DEAD;
-            src[j] = place != DC_DEAD ? parts_of(s2, R2, place, h) : Parts{nullptr, 0};
-          }
-          gather(R2, src, v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (src[j].n == 0) continue;
-            const float w = pl.w[t * a.k + j0 + j];
-            o.x = fmaf(w, v[j].x, o.x), o.y = fmaf(w, v[j].y, o.y), o.z = fmaf(w, v[j].z, o.z), o.w = fmaf(w, v[j].w, o.w);
-          }
+        for (int j = 0; j < 8; ++j) {
+          const int place = j0 + j < a.k ? pl.pos[t * a.k + j0 + j] : DC_DEAD;
+          src[j] = place != DC_DEAD ? parts_of(s2, a.part2, R2, place, h) : Parts{nullptr, 0};
         }
-        *reinterpret_cast<uint2*>(a.out + (int64_t)t * a.H + h) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+        gather(R2, src, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (src[j].n == 0) continue;
+          const float w = pl.w[t * a.k + j0 + j];
+          o.x = fmaf(w, v[j].x, o.x), o.y = fmaf(w, v[j].y, o.y), o.z = fmaf(w, v[j].z, o.z), o.w = fmaf(w, v[j].w, o.w);
+        }
       }
+      *reinterpret_cast<uint2*>(a.out + (int64_t)t * a.H + h) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
     }
   }
   tc_fence_before();
@@ -719,71 +769,88 @@ int64_t most_parts(int64_t ents, int64_t rt, int64_t kt) {
   const int64_t p = (kt - 1) / s + 2;
   return p < kt ? p : kt;
 }
+// Pairs of an entry, that is, of one reading of an expert: its terms have to fit a
+// ring slot, and larger slots leave room for fewer.  T where a token's choices
+// differ and T is small, else room for more than most experts get.
+int entry_pairs(int64_t T, int64_t k, int64_t E) {
+  const int64_t each = T * k / E;   // pairs an expert gets on average
+  return T < 2 ? 2 : T <= 16 ? (int)T : each <= 10 ? 16 : each <= 24 ? 32 : 64;
+}
+
 // floats of the partial sums [parts][live pairs][R]: the most over any number of live pairs
-int64_t part_floats(int64_t P, int64_t R, int64_t K) {
-  const int64_t rt = (R + 127) / 128, kt = pieces_of(K);
+int64_t part_floats(int64_t P, int64_t nb, int64_t R, int64_t K) {
+  const int64_t rt = (R + 127) / 128, kp = pieces_of(K);
   int64_t most = 0;
-  for (int64_t ents = 1; (ents - 1) * DC_NB < P; ++ents) {
-    const int64_t n = ents * DC_NB < P ? ents * DC_NB : P;
-    const int64_t v = most_parts(ents, rt, kt) * n * R;
+  for (int64_t ents = 1; (ents - 1) * nb < P; ++ents) {
+    const int64_t n = ents * nb < P ? ents * nb : P;
+    const int64_t v = most_parts(ents, rt, kp) * n * R;
     if (v > most) most = v;
   }
   return most;
 }
 
-DecodeSmem layout(int P, int max_ent, int max_smem) {
+DecodeSmem layout(int P, int nb, int max_ent, int max_smem) {
   DecodeSmem L{};
-  const int nb = P < DC_NB ? P : DC_NB;
   // (up to 8 rows that no term fills are read behind a tile, up to 512 bytes behind its scales)
   L.b_bytes = (TermTiles(3 * nb).bytes() + 1023) / 1024 * 1024;
-  L.sb = nb <= 8 ? 4 : nb <= 32 ? 3 : 2;
+  L.acc = 3 * ((nb + 7) / 8 * 8);
   const int plan = 16 + max_ent * 4 + P * 10;
-  const int bars = 8 * (2 * 16 + 2 * DC_MAX_BS + 8);
-  const int fixed = L.sb * (L.b_bytes + DC_G * 512) + 1024 + bars + plan + 64;
-  L.sa = (max_smem - 2048 - fixed) / DC_A_BYTES;   // 1024 to align the rings, 1024 for what is static
+  const int bars = 8 * (5 * DC_MAX_SLOTS + 8);
+  const int fixed = 1024 + bars + plan + 64;
+  // 1024 to align the rings, 1024 for what is static
+  L.sa = (max_smem - 2048 - fixed) / (DC_A_BYTES + DC_G * 512 + L.b_bytes);
+  if (L.sa > DC_MAX_SLOTS) L.sa = DC_MAX_SLOTS;
+  L.sb = L.sa;
+  L.team = L.sb >= 3 ? 2 : 4;
+  L.teams = DC_BWARPS / L.team < L.sb ? DC_BWARPS / L.team : L.sb;
   L.b = L.sa * DC_A_BYTES;
   L.sfa = L.b + L.sb * L.b_bytes + 1024;
-  L.bars = L.sfa + L.sb * DC_G * 512;
+  L.bars = L.sfa + L.sa * DC_G * 512;
   L.plan = L.bars + bars;
   L.total = (L.plan + plan + 15) / 16 * 16;
   return L;
 }
 
-int64_t max_entries(int64_t P, int64_t E) { return (P < E ? P : E) + P / DC_NB; }
+int64_t max_entries(int64_t P, int64_t E, int64_t nb) { return (P < E ? P : E) + P / nb; }
 
 }  // namespace
 
 // pieces are counted in 32 bits, times the CTAs
-bool decode_fits(int64_t P, int64_t E, int64_t H, int64_t F) {
+bool decode_fits(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F) {
   const int64_t h = (H + 127) / 128, f2 = (2 * F + 127) / 128, c1 = pieces_of(H) * f2, c2 = pieces_of(F) * h;
-  return max_entries(P, E) * (c1 > c2 ? c1 : c2) * DECODE_MAX_CTAS < (int64_t)1 << 32;
+  return max_entries(T * k, E, entry_pairs(T, k, E)) * (c1 > c2 ? c1 : c2) * DECODE_MAX_CTAS < (int64_t)1 << 32;
 }
 
-// What the workspace holds: partial sums, and terms with their scales; both
-// products' in turn in the same place.
+// What the workspace holds: both products' partial sums, and terms with their
+// scales, both products' in turn in the same place.
 struct DecodeSpace {
-  int64_t parts, terms;   // bytes
+  int64_t part1, part2, terms;   // bytes
 };
-static DecodeSpace space_of(int64_t P, int64_t E, int64_t H, int64_t F) {
-  const int64_t p1 = part_floats(P, 2 * F, H), p2 = part_floats(P, H, F), ents = max_entries(P, E);
+static DecodeSpace space_of(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F) {
+  const int64_t P = T * k, nb = entry_pairs(T, k, E), ents = max_entries(P, E, nb);
   auto terms = [&](int64_t K, int64_t nt) { return pieces_of(K) * DC_G * ((nt * P + 7 * ents) * 128 + 1024 * ents); };
   const int64_t t1 = terms(H, 2), t2 = terms(F, 3);
-  return {(p1 > p2 ? p1 : p2) * (int64_t)sizeof(float), t1 > t2 ? t1 : t2};
+  return {part_floats(P, nb, 2 * F, H) * (int64_t)sizeof(float), part_floats(P, nb, H, F) * (int64_t)sizeof(float),
+          t1 > t2 ? t1 : t2};
 }
 
-int64_t decode_workspace_bytes(int64_t P, int64_t E, int64_t H, int64_t F) {
-  const DecodeSpace w = space_of(P, E, H, F);
-  return w.parts + w.terms;
+int64_t decode_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F) {
+  const DecodeSpace w = space_of(T, k, E, H, F);
+  return w.part1 + w.part2 + w.terms;
 }
 
 cudaError_t launch_decode(DecodeArgs a, void* workspace, int num_sms, int max_smem, cudaStream_t st) {
   a.P = a.T * a.k;
-  a.max_ent = (int)max_entries(a.P, a.E);
-  const DecodeSmem L = layout(a.P, a.max_ent, max_smem);
-  if (num_sms > DECODE_MAX_CTAS || L.sa < 2 || (a.P > 32 && (a.E + a.P + 64) * 4 > L.sb * L.b_bytes)) return cudaErrorNotSupported;
-  const DecodeSpace w = space_of(a.P, a.E, a.H, a.F);
-  a.part = (float*)workspace;
-  a.terms = (uint8_t*)workspace + w.parts;
+  a.nb = entry_pairs(a.T, a.k, a.E);
+  a.max_ent = (int)max_entries(a.P, a.E, a.nb);
+  const DecodeSmem L = layout(a.P, a.nb, a.max_ent, max_smem);
+  if (num_sms > DECODE_MAX_CTAS || L.sa < 2 || 2 * L.acc + 12 * DC_G * L.sb > 512 ||
+      (a.P > 32 && (a.E + a.P + 64) * 4 > L.sb * L.b_bytes))
+    return cudaErrorNotSupported;
+  const DecodeSpace w = space_of(a.T, a.k, a.E, a.H, a.F);
+  a.part1 = (float*)workspace;
+  a.part2 = (float*)((uint8_t*)workspace + w.part1);
+  a.terms = (uint8_t*)a.part2 + w.part2;
   a.stall = take_ring_stall_hook();
   CUtensorMap tm[2];
   const int64_t R[2] = {2 * (int64_t)a.F, a.H}, K[2] = {a.H, a.F};

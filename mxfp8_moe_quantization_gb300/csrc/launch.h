@@ -116,8 +116,8 @@ cudaError_t launch_swiglu(const SwigluArgs& a, cudaStream_t st);
 
 // the expert layer of a few tokens (decode.cu)
 struct DecodeArgs;
-bool decode_fits(int64_t P, int64_t E, int64_t H, int64_t F);
-int64_t decode_workspace_bytes(int64_t P, int64_t E, int64_t H, int64_t F);
+bool decode_fits(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F);
+int64_t decode_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F);
 cudaError_t launch_decode(DecodeArgs a, void* workspace, int num_sms, int max_smem, cudaStream_t st);
 
 struct GemmArgs;

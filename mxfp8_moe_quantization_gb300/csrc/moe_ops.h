@@ -53,19 +53,18 @@ struct SwigluArgs {
 
 // The expert layer of a few tokens (decode.cu).
 constexpr int DECODE_MAX_PAIRS = 1024;      // T * k
-constexpr int DECODE_ENTRY_PAIRS = 64;      // pairs that one reading of an expert serves
 constexpr int DECODE_MIN_RUN = 2;           // pieces a CTA takes at least: fewer CTAs, fewer partial sums
 constexpr int DECODE_MAX_CTAS = 160;        // the workspace is sized for as many
 struct DecodeArgs {
   const uint16_t* x;     // [T, H] bf16, row stride ldx
   int64_t ldx;
   int T, k, E, H, F;
-  int P, max_ent;        // pairs, entries at most
+  int P, nb, max_ent;    // pairs, pairs of an entry, entries at most
   const int32_t* idx;    // [T, k]
   const float* w;        // [T, k]
   const uint8_t *q1, *s1, *q2, *s2;
   uint16_t* out;         // [T, H]
-  float* part;           // partial sums [parts][live pairs][rows]
+  float *part1, *part2;  // the products' partial sums [parts][live pairs][rows]
   uint8_t* terms;
   int* status;
   int stall;             // test hook: the first CTA never loads its first piece
