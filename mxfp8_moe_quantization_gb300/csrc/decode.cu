@@ -46,17 +46,32 @@ constexpr int DC_JOIN = DC_THREADS - 96;  // threads that make terms and add par
 constexpr int DC_G = 2;                   // tiles of 128 x 128 in a piece
 constexpr int DC_TILE = 128 * 128, DC_A_BYTES = DC_G * DC_TILE;
 constexpr int DC_MAX_SLOTS = 6;
+constexpr int DC_FLIGHT = 3;              // pieces of weights in flight at most
 constexpr int DC_DEAD = 0xFFFF;
 
 __host__ __device__ constexpr int up16(int v) { return (v + 15) / 16 * 16; }
+
+// Division by a number that the host knows.
+struct Div {
+  uint32_t d, m;   // m: 2^32 / d, rounded down (and below 2^32)
+  __host__ __device__ Div() : d(1), m(0xFFFFFFFFu) {}
+  explicit Div(int64_t by) : d((uint32_t)by), m(by > 1 ? (uint32_t)(((int64_t)1 << 32) / by) : 0xFFFFFFFFu) {}
+  FP8MOE_DEV uint32_t quot(uint32_t n) const {
+    const uint32_t q = __umulhi(n, m);   // the quotient or one less
+    return n - q * d >= d ? q + 1 : q;
+  }
+};
 
 // Shared memory: the rings of weights (at 0) and of their scales (sa slots), that
 // of terms and their scales (sb slots), the plan.
 struct DecodeSmem {
   int sa, sb, b_bytes;
-  int team, teams;                         // warps that fill a slot of terms together
+  int flight;                              // pieces of weights in flight, at most sa
+  int team_log, teams;                     // 2^team_log warps fill a slot of terms together
   int acc;                                 // tensor memory columns of an accumulator
   int sfa, b, bars, plan, total;
+  // tiles and pieces of the products' K, tiles of their rows; the grid; H / 4; choices
+  Div kt[2], kp[2], rt[2], grid, quads, k;
 };
 
 // The terms of an entry of n pairs, piece by piece: DC_G tiles of their rows,
@@ -188,19 +203,36 @@ FP8MOE_DEV void plan_block(const DecodeArgs& a, const Plan& pl, int* scratch) {
   __syncthreads();
 }
 
-// One product's stream of pieces: nent entries x rt row tiles x kp pieces.
+// One product's stream of pieces: nent entries x row tiles x pieces of K, in runs
+// of `base` pieces, one more for the first `rest` CTAs.
 struct Stream {
-  uint32_t C, runs;   // pieces, CTAs that have a run of them
-  int rt, kp;
-  FP8MOE_DEV Stream(int nent, int rt_, int kp_, uint32_t grid) : rt(rt_), kp(kp_) {
-    C = (uint32_t)nent * rt * kp;
-    const uint32_t want = (C + DECODE_MIN_RUN - 1) / DECODE_MIN_RUN;
-    runs = want < grid ? want : grid;
+  uint32_t C, runs, base, rest;   // pieces; CTAs that have a run of them
+  float per0, per1;               // 1 / base, 1 / (base + 1)
+  const Div &rt, &kp;
+  FP8MOE_DEV Stream(int nent, const Div& rt_, const Div& kp_, const Div& grid) : rt(rt_), kp(kp_) {
+    static_assert(DECODE_MIN_RUN == 2, "base of a short stream");
+    C = (uint32_t)nent * rt.d * kp.d;
+    const uint32_t want = (C + 1) / 2;
+    runs = want < grid.d ? want : grid.d;
+    base = want < grid.d ? (C == 2 * runs ? 2 : 1) : grid.quot(C);
+    rest = C - base * runs;
+    per0 = __frcp_rn((float)base);
+    per1 = __frcp_rn((float)(base + 1));
   }
-  FP8MOE_DEV uint32_t first(uint32_t cta) const { return cta < runs ? cta * C / runs : C; }
-  FP8MOE_DEV uint32_t owner(uint32_t c) const { return ((c + 1) * runs - 1) / C; }
+  FP8MOE_DEV uint32_t first(uint32_t cta) const { return cta < runs ? cta * base + min(cta, rest) : C; }
+  // the CTA whose run has piece c: below 2^8, so that the quotient in fp32 is off by
+  // one at most
+  FP8MOE_DEV uint32_t owner(uint32_t c) const {
+    const uint32_t wide = rest * (base + 1);
+    const bool late = c >= wide;
+    const uint32_t n = late ? c - wide : c, d = late ? base : base + 1;
+    uint32_t q = (uint32_t)((float)n * (late ? per0 : per1));
+    if (q * d > n) --q;
+    if (n - q * d >= d) ++q;
+    return late ? q + rest : q;
+  }
   // partial sums of a tile: the CTAs whose runs meet it
-  FP8MOE_DEV int parts(uint32_t tile) const { return (int)(owner(tile * kp + kp - 1) - owner(tile * kp)) + 1; }
+  FP8MOE_DEV int parts(uint32_t tile) const { return (int)(owner(tile * kp.d + kp.d - 1) - owner(tile * kp.d)) + 1; }
 };
 
 // A CTA's run of a stream, segment by segment: the pieces of one tile that are
@@ -212,18 +244,18 @@ struct Run {
   FP8MOE_DEV Run(const Stream& s, uint32_t cta) {
     const uint32_t lo = s.first(cta);
     left = s.first(cta + 1) - lo;
-    tile = lo / s.kp;
-    k = (int)(lo - tile * s.kp);
-    ent = (int)(tile / s.rt);
-    row = (int)(tile - (uint32_t)ent * s.rt);
-    n = (int)min(left, (uint32_t)(s.kp - k));
+    tile = s.kp.quot(lo);
+    k = (int)(lo - tile * s.kp.d);
+    ent = (int)s.rt.quot(tile);
+    row = (int)(tile - (uint32_t)ent * s.rt.d);
+    n = (int)min(left, (uint32_t)(s.kp.d - k));
   }
   FP8MOE_DEV void next(const Stream& s) {
     left -= n;
     k = 0;
     ++tile;
-    if (++row == s.rt) row = 0, ++ent;
-    n = (int)min(left, (uint32_t)s.kp);
+    if (++row == (int)s.rt.d) row = 0, ++ent;
+    n = (int)min(left, s.kp.d);
   }
 };
 
@@ -269,9 +301,11 @@ FP8MOE_DEV uint64_t ld_acquire_gpu(const unsigned long long* p) {
   return v;
 }
 // One thread comes for its CTA, which is at a barrier, and waits until the counter
-// says n: all have come.  (The limit is twice that of the waits before it.)
-FP8MOE_DEV void meet(unsigned long long* count, uint64_t n, int* status, volatile int* abort_flag) {
+// says n: all have come.  (With twice the limit of the waits before it.)
+FP8MOE_DEV void come(unsigned long long* count) {
   asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(count) : "memory");
+}
+FP8MOE_DEV void came(unsigned long long* count, uint64_t n, int* status, volatile int* abort_flag) {
   if (ld_acquire_gpu(count) >= n) return;
   const uint64_t t0 = globaltimer();
   while (ld_acquire_gpu(count) < n) {
@@ -367,28 +401,28 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     *abort_flag = 1;
   };
 
-  if (warp == DC_WARP_TMA && lane == 0) {
-    abort_s = 0;
-    for (int i = 0; i < L.sa; ++i) mbar_init(&a_full[i], 1), mbar_init(&a_empty[i], 1);
-    for (int i = 0; i < L.sb; ++i) mbar_init(&b_full[i], L.team), mbar_init(&b_empty[i], 1), mbar_init(&sf_full[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 4);
-    mbar_init(&drain[0], 1), mbar_init(&drain[1], 1);
+  if (warp == DC_WARP_MMA) {
+    if (lane == 0) abort_s = 0;
+    if (lane < L.sa) mbar_init(&a_full[lane], 1), mbar_init(&a_empty[lane], 1);
+    if (lane < L.sb) mbar_init(&b_full[lane], 1 << L.team_log), mbar_init(&b_empty[lane], 1), mbar_init(&sf_full[lane], 1);
+    if (lane < 2) mbar_init(&acc_full[lane], 1), mbar_init(&acc_empty[lane], 4), mbar_init(&drain[lane], 1);
     mbar_fence_init();
   }
-  if (warp == DC_WARP_MMA) {
+  if (warp == DC_WARP_SF) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_s)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     tc_fence_before();
   }
   const int K1 = a.H, K2 = a.F, R1 = 2 * a.F, R2 = a.H;
-  const int kt1 = (K1 + 127) / 128, kt2 = (K2 + 127) / 128;
+  const int kt1 = (int)L.kt[0].d, kt2 = (int)L.kt[1].d;
   const bool epi = warp < 4;
   const int jt = epi ? tid : tid - 96;             // thread among those that make terms and add
-  // The terms' units: a tile of a row, sixteen threads each, a warp's two a grid apart.
+  // The terms' units: a pair's tile, sixteen threads each, a warp's two a grid apart.
   const int unit0 = (jt >> 4) * (int)grid + (int)cta, unit_step = (int)grid * (DC_JOIN / 16), j16 = jt & 15;
   auto x_at = [&](int u) {                         // this thread's eight values of x
-    const int t = u / kt1, k = (u - t * kt1) * 128 + j16 * 8;
-    return u < a.T * kt1 && k < K1 ? __ldg(reinterpret_cast<const uint4*>(a.x + t * a.ldx + k)) : make_uint4(0, 0, 0, 0);
+    const int p = (int)L.kt[0].quot(u), k = (u - p * kt1) * 128 + j16 * 8;
+    return u < a.P * kt1 && k < K1 ? __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)L.k.quot(p) * a.ldx + k))
+                                   : make_uint4(0, 0, 0, 0);
   };
   uint4 x0 = make_uint4(0, 0, 0, 0);               // the first unit's, on its way while the plan is made
   if (warp < DC_WARP_TMA || warp >= DC_WARP_B) x0 = x_at(unit0);
@@ -401,14 +435,17 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_s;
   const int nlive = pl.num[0], nent = pl.num[1];
-  const Stream s1(nent, (R1 + 127) / 128, (kt1 + DC_G - 1) / DC_G, grid), s2(nent, (R2 + 127) / 128, (kt2 + DC_G - 1) / DC_G, grid);
+  const Stream s1(nent, L.rt[0], L.kp[0], L.grid), s2(nent, L.rt[1], L.kp[1], L.grid);
   using Two = std::integral_constant<int, 2>;     // terms of a bf16 value: the first product's
   using Three = std::integral_constant<int, 3>;   // of an fp32 value: the second's
 
   if (warp == DC_WARP_TMA) {
     // ======================= weights =======================
+    // The first fills leave behind this CTA's terms of x: in front of them, what
+    // follows them meets its first instructions and loads in a full memory system.
+    bar_sync(1, DC_JOIN + 32);
     if (lane == 0) {
-      Slot slot;
+      Slot slot, late;
       uint32_t i = 0;
       bool ok = true;
       for (int ph = 0; ph < 2 && ok; ++ph) {
@@ -418,7 +455,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         for (Run r(s, cta); r.left > 0 && ok; r.next(s)) {
           const int e = (int)(pl.ent[r.ent] & 1023u);
           int x = r.k * DC_G;   // the piece's first tile
-          const uint8_t* sc = (ph ? a.s2 : a.s1) + (((int64_t)e * s.rt + r.row) * kt + x) * 512;
+          const uint8_t* sc = (ph ? a.s2 : a.s1) + (((int64_t)e * s.rt.d + r.row) * kt + x) * 512;
           for (int c = 0; c < r.n; ++c, ++i, x += DC_G, sc += DC_G * 512, slot.step(1, L.sa)) {
             uint64_t* bar = &a_full[slot.i];
             if (!mbar_wait(&a_empty[slot.i], slot.turn ^ 1u, abort_flag)) {
@@ -426,6 +463,13 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
               break;
             }
             if (a.stall && cta == 0 && i == 0) continue;
+            // no more in flight than keeps HBM busy: everything else in the memory
+            // system waits behind it
+            if (i >= (uint32_t)L.flight && !mbar_wait(&a_full[late.i], late.turn, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (i >= (uint32_t)L.flight) late.step(1, L.sa);
             const int tiles = min(DC_G, kt - x);
             uint8_t* dst = smem + slot.i * DC_A_BYTES;
             mbar_expect_tx(bar, tiles * (DC_TILE + 512));
@@ -547,9 +591,12 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     uint64_t meets;
     asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(meets) : "l"(g_meets[MEET_END]));
     meets += grid;
-    auto meeting = [&](int i) {
+    // (`meanwhile`: what the next step can work out without the others' results)
+    auto meeting = [&](int i, auto meanwhile) {
       bar_sync(2, DC_JOIN);
-      if (tid == 0) meet(g_meets[i], meets, a.status, abort_flag);
+      if (tid == 0) come(g_meets[i]);
+      meanwhile();
+      if (tid == 0) came(g_meets[i], meets, a.status, abort_flag);
       bar_sync(2, DC_JOIN);
     };
 
@@ -559,7 +606,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       int n;
     };
     auto parts_of = [&](const Stream& s, const float* part, int R, int place, int row) {
-      const uint32_t tile = (uint32_t)pl.ent_of[place] * s.rt + row / 128;
+      const uint32_t tile = (uint32_t)pl.ent_of[place] * s.rt.d + row / 128;
       return Parts{reinterpret_cast<const float4*>(part + (int64_t)place * R + row), s.parts(tile)};
     };
     auto gather = [&](int R, const auto& src, auto& v) {
@@ -579,17 +626,6 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         for (int i = 0; i < N; ++i) v[i].x += u[i].x, v[i].y += u[i].y, v[i].z += u[i].z, v[i].w += u[i].w;
       }
     };
-    // eight values of the activation, from the first product's partial sums
-    auto act_at = [&](int place, int f, float (&v)[8]) {
-      const Parts g = parts_of(s1, a.part1, R1, place, f), y = parts_of(s1, a.part1, R1, place, a.F + f);
-      const Parts src[4] = {g, {g.p + 1, g.n}, y, {y.p + 1, y.n}};
-      float4 q[4];
-      gather(R1, src, q);
-      const float gs[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
-      const float us[8] = {q[2].x, q[2].y, q[2].z, q[2].w, q[3].x, q[3].y, q[3].z, q[3].w};
-#pragma unroll
-      for (int c = 0; c < 8; ++c) v[c] = gs[c] / (1.0f + expf(-gs[c])) * us[c];
-    };
     // where an entry's terms are in the workspace
     auto terms_of = [&](int e, uint32_t ent, int kp, int nt) {
       return a.terms + (int64_t)kp * DC_G * ((nt * (int)(ent >> 10 & 1023u) + 7 * e) * 128 + 1024 * e);
@@ -599,34 +635,35 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     // Teams of warps take the pieces of both runs in turn.  (Not more teams than
     // slots: a slot's barrier tells the last turn from the one before, and a team
     // that has filled its last piece knows that the slots' turns before are over.)
-    const int team = (warp - DC_WARP_B) / L.team, rank = (warp - DC_WARP_B) - team * L.team;
-    uint32_t piece = (uint32_t)team;
-    int ahead = team;                                // pieces before the team's next one
+    const int team = (warp - DC_WARP_B) >> L.team_log, rank = (warp - DC_WARP_B) & ((1 << L.team_log) - 1);
+    Slot slot;
+    slot.step(team, L.sb);
+    Run r(s1, cta);                           // of the stream to come, at the team's next piece
+    int c = team;                                    // this, counted in r's segment
+    auto enter = [&](const Stream& s) {
+      while (r.left > 0 && c >= r.n) {
+        c -= r.n;
+        r.next(s);
+      }
+    };
+    if (!epi) enter(s1);
     auto feed = [&](auto nt) {
       constexpr int NT = decltype(nt)::value;
       const Stream& s = NT == 2 ? s1 : s2;
-      Run r(s, cta);
-      int c = ahead;                                 // the team's next piece, counted in segment r
-      for (; team < L.teams; c += L.teams, piece += L.teams) {
-        while (r.left > 0 && c >= r.n) {
-          c -= r.n;
-          r.next(s);
-        }
-        if (r.left == 0) break;
-        const uint32_t ent = pl.ent[r.ent], turn = piece / (uint32_t)L.sb;
-        const int slot = (int)(piece - turn * (uint32_t)L.sb);
+      for (; team < L.teams && r.left > 0; c += L.teams, slot.step(L.teams, L.sb), enter(s)) {
+        const uint32_t ent = pl.ent[r.ent];
         const TermTiles tt((int)(ent >> 20) * NT);
-        uint4* dst = reinterpret_cast<uint4*>(smem + L.b + slot * L.b_bytes);
-        const uint4* src = reinterpret_cast<const uint4*>(terms_of(r.ent, ent, s.kp, NT) + (int64_t)(r.k + c) * tt.bytes());
+        uint4* dst = reinterpret_cast<uint4*>(smem + L.b + slot.i * L.b_bytes);
+        const uint4* src = reinterpret_cast<const uint4*>(terms_of(r.ent, ent, s.kp.d, NT) + (int64_t)(r.k + c) * tt.bytes());
         // 16 bytes at a time, 4 KB in flight a warp
-        const int chunks = tt.bytes() / 16, at = rank * 32 + lane, step = L.team * 32;
+        const int chunks = tt.bytes() / 16, at = rank * 32 + lane, step = 32 << L.team_log;
         bool ready = false, ok = true;
         for (int i0 = at; i0 - lane < chunks; i0 += 8 * step) {
           uint4 q[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (i0 + step * i < chunks) q[i] = __ldcg(src + i0 + step * i);
-          if (!ready) ok = __all_sync(0xffffffffu, mbar_wait(&b_empty[slot], (turn & 1u) ^ 1u, abort_flag));
+          if (!ready) ok = __all_sync(0xffffffffu, mbar_wait(&b_empty[slot.i], slot.turn ^ 1u, abort_flag));
           ready = true;
           if (!ok) break;
 #pragma unroll
@@ -639,9 +676,9 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b_full[slot]);
+        if (lane == 0) mbar_arrive(&b_full[slot.i]);
       }
-      ahead = c;                                     // past the run's end: into the next run
+      // c is past the run's end: into the next run
     };
     // ======================= accumulators to partial sums =======================
     Slot acc;
@@ -653,7 +690,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       for (Run r(s, cta); r.left > 0; r.next(s)) {
         const uint32_t ent = pl.ent[r.ent];
         const int first = (int)(ent >> 10 & 1023u), pairs = (int)(ent >> 20);
-        const int mine = (int)(cta - s.owner(r.tile * s.kp));
+        const int mine = (int)(cta - s.owner(r.tile * s.kp.d));
         const int row = r.row * 128 + warp * 32 + lane;
         float* dst = part + ((int64_t)mine * nlive + first) * R + row;
         if (!mbar_wait(&acc_full[acc.i], acc.turn, abort_flag)) {
@@ -694,53 +731,84 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
                 (place - (int)(ent >> 10 & 1023u)) * NT, j16);
     };
     const int back = (jt >> 4 & 1) * (int)grid;     // a warp stays together for its shuffles
-    // x, a token's for all its experts
-    for (int u = unit0, units = a.T * kt1; u - back < units; u += unit_step) {
+    for (int u = unit0, units = a.P * kt1; u - back < units; u += unit_step) {
       const uint4 q = u == unit0 ? x0 : x_at(u);
       float v[8] = {bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y), bf16_lo(q.z), bf16_hi(q.z), bf16_lo(q.w), bf16_hi(q.w)};
       const Terms<2> terms(v);
-      const int t = u / kt1, c = u - t * kt1;
-      if (u < units && c * 128 + j16 * 8 < K1)
-        for (int i = t * a.k; i < (t + 1) * a.k; ++i)
-          if (pl.pos[i] != DC_DEAD) put(terms, pl.pos[i], c, s1.kp);
+      const int p = (int)L.kt[0].quot(u), c = u - p * kt1, place = u < units ? pl.pos[p] : DC_DEAD;
+      if (place != DC_DEAD && c * 128 + j16 * 8 < K1) put(terms, place, c, s1.kp.d);
     }
-    meeting(MEET_X);
+    asm volatile("bar.arrive 1, %0;" ::"n"(DC_JOIN + 32) : "memory");
+    meeting(MEET_X, [] {});
     if (epi) {
       drain_acc(Two{});
     } else {
       feed(Two{});
     }
-    meeting(MEET_SUMS);
-    // the activation
-    for (int u = unit0, units = nlive * kt2; u - back < units; u += unit_step) {
-      const int place = u < units ? u / kt2 : 0, c = u - place * kt2, f = c * 128 + j16 * 8;
-      const bool in = u < units && f < K2;
-      float v[8] = {};
-      if (in) act_at(place, f, v);
+    // the activation, a unit a pair's tile
+    struct Act {
+      int place, c;
+      bool in;
+      Parts g, y;
+    } next;
+    const int units = nlive * kt2;
+    auto act_of = [&](int u) {
+      Act n;
+      n.place = u < units ? (int)L.kt[1].quot(u) : 0, n.c = u - n.place * kt2;
+      const int f = n.c * 128 + j16 * 8;
+      n.in = u < units && f < K2;
+      n.g = n.in ? parts_of(s1, a.part1, R1, n.place, f) : Parts{nullptr, 0};
+      n.y = n.in ? parts_of(s1, a.part1, R1, n.place, a.F + f) : Parts{nullptr, 0};
+      return n;
+    };
+    meeting(MEET_SUMS, [&] { next = act_of(unit0); });
+    for (int u = unit0; u - back < units; u += unit_step) {
+      const Parts src[4] = {next.g, {next.g.p + 1, next.g.n}, next.y, {next.y.p + 1, next.y.n}};
+      float4 q[4];
+      gather(R1, src, q);
+      const float gs[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+      const float us[8] = {q[2].x, q[2].y, q[2].z, q[2].w, q[3].x, q[3].y, q[3].z, q[3].w};
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = gs[i] / (1.0f + expf(-gs[i])) * us[i];
       const Terms<3> terms(v);
-      if (in) put(terms, place, c, s2.kp);
+      if (next.in) put(terms, next.place, next.c, s2.kp.d);
+      if (u + unit_step - back < units) next = act_of(u + unit_step);
     }
-    meeting(MEET_ACT);
+    meeting(MEET_ACT, [&] {
+      if (epi) return;
+      r = Run(s2, cta);
+      enter(s2);
+    });
     if (epi) {
       drain_acc(Three{});
     } else {
       feed(Three{});
     }
-    meeting(MEET_END);
     // the weighted sum over a token's experts, four neighbouring columns a thread,
     // runs of eight threads' a CTA in turn
-    const uint32_t per = (uint32_t)a.H / 4, tasks = (uint32_t)a.T * per;
-    for (uint32_t i = (((uint32_t)jt >> 3) * grid + cta) * 8 + (jt & 7); i < tasks; i += DC_JOIN * grid) {
-      const int t = (int)(i / per), h = (int)(i - (uint32_t)t * per) * 4;
+    const uint32_t tasks = (uint32_t)a.T * L.quads.d;
+    const uint32_t task0 = (((uint32_t)jt >> 3) * grid + cta) * 8 + (jt & 7);
+    Parts src[8];
+    auto parts_at = [&](int t, int h, int j0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int place = j0 + j < a.k ? pl.pos[t * a.k + j0 + j] : DC_DEAD;
+        src[j] = place != DC_DEAD ? parts_of(s2, a.part2, R2, place, h) : Parts{nullptr, 0};
+      }
+    };
+    int t, h;
+    auto task_of = [&](uint32_t i) {
+      if (i >= tasks) return;
+      t = (int)L.quads.quot(i), h = (int)(i - (uint32_t)t * L.quads.d) * 4;
+      parts_at(t, h, 0);
+    };
+    meeting(MEET_END, [&] { task_of(task0); });
+    for (uint32_t i = task0; i < tasks; i += DC_JOIN * grid) {
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       for (int j0 = 0; j0 < a.k; j0 += 8) {
-        Parts src[8];
+        if (j0 > 0) parts_at(t, h, j0);
         float4 v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int place = j0 + j < a.k ? pl.pos[t * a.k + j0 + j] : DC_DEAD;
-          src[j] = place != DC_DEAD ? parts_of(s2, a.part2, R2, place, h) : Parts{nullptr, 0};
-        }
         gather(R2, src, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -750,12 +818,13 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         }
       }
       *reinterpret_cast<uint2*>(a.out + (int64_t)t * a.H + h) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+      task_of(i + DC_JOIN * grid);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == DC_WARP_MMA) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  if (warp == DC_WARP_SF) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 int64_t pieces_of(int64_t K) { return ((K + 127) / 128 + DC_G - 1) / DC_G; }
@@ -801,8 +870,9 @@ DecodeSmem layout(int P, int nb, int max_ent, int max_smem) {
   L.sa = (max_smem - 2048 - fixed) / (DC_A_BYTES + DC_G * 512 + L.b_bytes);
   if (L.sa > DC_MAX_SLOTS) L.sa = DC_MAX_SLOTS;
   L.sb = L.sa;
-  L.team = L.sb >= 3 ? 2 : 4;
-  L.teams = DC_BWARPS / L.team < L.sb ? DC_BWARPS / L.team : L.sb;
+  L.flight = DC_FLIGHT < L.sa ? DC_FLIGHT : L.sa;
+  L.team_log = L.sb >= 3 ? 1 : 2;
+  L.teams = (DC_BWARPS >> L.team_log) < L.sb ? DC_BWARPS >> L.team_log : L.sb;
   L.b = L.sa * DC_A_BYTES;
   L.sfa = L.b + L.sb * L.b_bytes + 1024;
   L.bars = L.sfa + L.sa * DC_G * 512;
@@ -843,7 +913,7 @@ cudaError_t launch_decode(DecodeArgs a, void* workspace, int num_sms, int max_sm
   a.P = a.T * a.k;
   a.nb = entry_pairs(a.T, a.k, a.E);
   a.max_ent = (int)max_entries(a.P, a.E, a.nb);
-  const DecodeSmem L = layout(a.P, a.nb, a.max_ent, max_smem);
+  DecodeSmem L = layout(a.P, a.nb, a.max_ent, max_smem);
   if (num_sms > DECODE_MAX_CTAS || L.sa < 2 || 2 * L.acc + 12 * DC_G * L.sb > 512 ||
       (a.P > 32 && (a.E + a.P + 64) * 4 > L.sb * L.b_bytes))
     return cudaErrorNotSupported;
@@ -854,6 +924,9 @@ cudaError_t launch_decode(DecodeArgs a, void* workspace, int num_sms, int max_sm
   a.stall = take_ring_stall_hook();
   CUtensorMap tm[2];
   const int64_t R[2] = {2 * (int64_t)a.F, a.H}, K[2] = {a.H, a.F};
+  for (int i = 0; i < 2; ++i)
+    L.kt[i] = Div((K[i] + 127) / 128), L.kp[i] = Div(pieces_of(K[i])), L.rt[i] = Div((R[i] + 127) / 128);
+  L.grid = Div(num_sms), L.quads = Div(a.H / 4), L.k = Div(a.k);
   const uint8_t* q[2] = {a.q1, a.q2};
   for (int i = 0; i < 2; ++i) {
     const cuuint64_t dims[3] = {(cuuint64_t)K[i], (cuuint64_t)R[i], (cuuint64_t)a.E};
@@ -863,7 +936,7 @@ cudaError_t launch_decode(DecodeArgs a, void* workspace, int num_sms, int max_sm
   }
   cudaError_t e = cudaFuncSetAttribute(k_decode, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem - 1024);
   if (e != cudaSuccess) return e;
-  void* args[] = {&tm[0], &tm[1], &a, const_cast<DecodeSmem*>(&L)};
+  void* args[] = {&tm[0], &tm[1], &a, &L};
   return cudaLaunchCooperativeKernel((const void*)k_decode, dim3((unsigned)num_sms), dim3(DC_THREADS), args, L.total + 1024, st);
 }
 
