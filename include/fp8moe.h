@@ -594,6 +594,41 @@ fp8moe_status fp8moe_swiglu_bwd(const void* dout, const void* h, int64_t ldh, in
                                 void* q1, uint8_t* s1, int s1_layout, fp8moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Training with activations kept in 8 bits: what the backward passes read of the
+ * forward's activations as MXFP8 (codes [R, C] e4m3fn and row-major e8m0 bytes
+ * [R, C/32], the rule of fp8moe_mxfp8_quantize_dim0), 1.03 bytes an element
+ * instead of two.  The calls are those of the same name without _ckpt, on the
+ * values that the codes stand for; a code or scale that is NaN is a NaN, values
+ * below 2^-126 may be rounded to multiples of 2^-133.
+ *
+ * fp8moe_swiglu_fwd_ckpt: fp8moe_swiglu_fwd that also writes h's checkpoint, hq
+ *   [M, 2F] and hs [M, 2F/32], from the same reading (bit-identical to
+ *   fp8moe_mxfp8_quantize_dim0 of h); it may be the only output.
+ * fp8moe_swiglu_bwd_ckpt: fp8moe_swiglu_bwd with hq, hs (dense) in place of h.
+ *   aq1 [F, M] and as1 (scales of [F, M/32] in s1_layout; M % 32 == 0), or both
+ *   NULL: the activation of the checkpoint's values along its columns, the operand
+ *   of the second product's weight gradient, which the forward then need not keep.
+ * fp8moe_add_rmsnorm_bwd_ckpt: fp8moe_add_rmsnorm_bwd with hq [T, H] and hs
+ *   [T, H/32] in place of h; H % 32 == 0; the same workspace.
+ * fp8moe_route_weight_grad_ckpt: fp8moe_route_weight_grad_bounded with the expert
+ *   outputs yq [rows, N] and ys [rows, N/32] in place of y; N % 32 == 0.
+ * Codes 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+fp8moe_status fp8moe_swiglu_fwd_ckpt(const void* h, int64_t ldh, int64_t M, int64_t F, const int32_t* offs, int64_t E,
+                                     void* out, void* q0, uint8_t* s0, int s0_layout, void* q1, uint8_t* s1,
+                                     int s1_layout, void* hq, uint8_t* hs, fp8moe_stream_t stream);
+fp8moe_status fp8moe_swiglu_bwd_ckpt(const void* dout, const void* hq, const uint8_t* hs, int64_t M, int64_t F,
+                                     const int32_t* offs, int64_t E, void* dh, void* q0, uint8_t* s0, int s0_layout,
+                                     void* q1, uint8_t* s1, int s1_layout, void* aq1, uint8_t* as1,
+                                     fp8moe_stream_t stream);
+fp8moe_status fp8moe_add_rmsnorm_bwd_ckpt(const void* dy, const void* hq, const uint8_t* hs, const float* rstd,
+                                          const void* w, int weight_type, const void* dh, int64_t T, int64_t H, void* dx,
+                                          float* dw, void* workspace, int64_t workspace_bytes, fp8moe_stream_t stream);
+fp8moe_status fp8moe_route_weight_grad_ckpt(const void* dout, const void* yq, const uint8_t* ys, int64_t rows,
+                                            const int32_t* row_of, int64_t T, int64_t N, int64_t k, float* dw,
+                                            fp8moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * The expert layer of a few tokens (decoding) in one launch, on the MXFP8
  * weights of the grouped products:
  *   out[t] = sum over j of w[t, j] * W2[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])),
@@ -669,11 +704,13 @@ fp8moe_status fp8moe_testing_stall_next_tensorwise(void);
  * fp8moe_mxfp8_quantize_dual with both directions and at least 128 columns,
  * fp8moe_quantize_colwise_3d of routed rows with transposed output,
  * fp8moe_swiglu_fwd / _bwd of more tiles (64 rows x 128 columns) than the
- * device has SMs, and fp8moe_add_rmsnorm_bwd of rows up to 16384 elements.
+ * device has SMs, fp8moe_add_rmsnorm_bwd of rows up to 16384 elements (both
+ * with _ckpt too), and fp8moe_mxfp8_moe_decode.
  * Arms a one-shot flag: the next such launch of the process never loads one
  * tile (the first CTA's first tile or rows; the routed-rows colwise kernel:
  * the first tile of its first unit, whichever CTA takes it; the gated
- * activation: the first warp's), so the warps waiting for it run out of
+ * activation: the first warp's; the few tokens' layer: the first piece of
+ * weights), so the warps waiting for it run out of
  * their bounded wait (2 s) and the launch sets FP8MOE_ERR_TIMEOUT (its
  * outputs are then not valid).  The loads that were issued are still waited
  * for (bounded), so no copy is in flight when a CTA exits and the context

@@ -37,6 +37,7 @@ __all__ = [
     "fp8moe_add_rmsnorm_fwd", "fp8moe_add_rmsnorm_bwd", "fp8moe_add_rmsnorm_bwd_workspace_bytes",
     "fp8moe_router_fwd", "fp8moe_router_bwd", "fp8moe_router_workspace_bytes", "fp8moe_route_weight_grad",
     "fp8moe_swiglu_fwd", "fp8moe_swiglu_bwd",
+    "fp8moe_swiglu_fwd_ckpt", "fp8moe_swiglu_bwd_ckpt", "fp8moe_add_rmsnorm_bwd_ckpt", "fp8moe_route_weight_grad_ckpt",
     "DECODE_MAX_PAIRS", "fp8moe_mxfp8_moe_decode", "fp8moe_mxfp8_moe_decode_workspace_bytes",
 ]
 
@@ -94,6 +95,11 @@ SYMBOLS = {
     "fp8moe_route_weight_grad_bounded": (_i32, [_vp, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp]),
     "fp8moe_swiglu_fwd": (_i32, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp]),
     "fp8moe_swiglu_bwd": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp]),
+    "fp8moe_swiglu_fwd_ckpt": (_i32, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp]),
+    "fp8moe_swiglu_bwd_ckpt": (_i32, [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _vp,
+                                      _vp]),
+    "fp8moe_add_rmsnorm_bwd_ckpt": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp]),
+    "fp8moe_route_weight_grad_ckpt": (_i32, [_vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp]),
     "fp8moe_mxfp8_moe_decode_workspace_bytes": (_i64, [_i64, _i64, _i64, _i64, _i64]),
     "fp8moe_mxfp8_moe_decode": (_i32, [_vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64,
                                        _vp]),
@@ -585,7 +591,7 @@ def fp8moe_add_rmsnorm_bwd(dy, h, rstd, weight, dh=None, dx=None, dweight=None, 
     weight as in the forward, dh [T, H] bf16 the gradient that reaches h
     otherwise -> (dx [T, H] bf16, the gradient of x and of residual; dweight
     [H] fp32)."""
-    return _run("fp8moe_add_rmsnorm_bwd", stream, _native().add_rmsnorm_bwd, dy, h, rstd, weight, dh, dx, dweight, workspace)
+    return _run("fp8moe_add_rmsnorm_bwd", stream, _native().add_rmsnorm_bwd, dy, h, rstd, weight, dh, dx, dweight, workspace, None)
 
 
 def fp8moe_router_workspace_bytes(T: int, E: int) -> int:
@@ -616,7 +622,7 @@ def fp8moe_router_bwd(logits, topk_idx, counts=None, dtopk_w=None, dloss=None, s
 def fp8moe_route_weight_grad(dout, y, row_of, dw=None, stream=None):
     """Gradient of fp8moe_route_unpermute's weights: dout [T, N] bf16, y
     [rows, N] bf16, row_of [T, k] int32 (outside [0, rows): 0) -> dw [T, k] fp32."""
-    return _run("fp8moe_route_weight_grad", stream, _native().route_weight_grad, dout, y, row_of, dw)
+    return _run("fp8moe_route_weight_grad", stream, _native().route_weight_grad, dout, y, row_of, dw, None)
 
 
 def fp8moe_swiglu_fwd(h, offs=None, s0_layout: int = NO_GROUPS, s1_layout: int = NO_GROUPS, need_out: bool = True,
@@ -641,6 +647,44 @@ def fp8moe_swiglu_bwd(dout, h, offs=None, s0_layout: int = NO_GROUPS, s1_layout:
         raise Fp8MoeError("fp8moe_swiglu_bwd", 1)
     return _run("fp8moe_swiglu_bwd", stream, _native().swiglu, dout, h, offs, s0_layout, s1_layout, need_dh, dim0, dim1, out, q0,
                 s0, q1, s1)
+
+
+def fp8moe_swiglu_fwd_ckpt(h, offs=None, s0_layout: int = NO_GROUPS, s1_layout: int = NO_GROUPS, need_out: bool = True,
+                           dim0: bool = False, dim1: bool = False, out=None, q0=None, s0=None, q1=None, s1=None, hq=None,
+                           hs=None, stream=None):
+    """fp8moe_swiglu_fwd that also keeps its input in 8 bits: returns (out, q0,
+    s0, q1, s1, hq uint8 [M, 2F], hs uint8 [M, 2F/32]), the last two the MXFP8
+    codes and row-major scales of h."""
+    return _run("fp8moe_swiglu_fwd_ckpt", stream, _native().swiglu_fwd_ckpt, h, offs, s0_layout, s1_layout, need_out, dim0, dim1,
+                out, q0, s0, q1, s1, hq, hs)
+
+
+def fp8moe_swiglu_bwd_ckpt(dout, hq, hs, offs=None, s0_layout: int = NO_GROUPS, s1_layout: int = NO_GROUPS,
+                           need_dh: bool = True, dim0: bool = False, dim1: bool = False, act1: bool = False, out=None,
+                           q0=None, s0=None, q1=None, s1=None, aq1=None, as1=None, stream=None):
+    """fp8moe_swiglu_bwd on the values of hq, hs: returns (dh, q0, s0, q1, s1,
+    aq1 [F, M], as1), the last two (``act1``) the activation's MXFP8 codes along
+    its columns with scales in ``s1_layout``: the operand of the second product's
+    weight gradient."""
+    return _run("fp8moe_swiglu_bwd_ckpt", stream, _native().swiglu_bwd_ckpt, dout, hq, hs, offs, s0_layout, s1_layout, need_dh,
+                dim0, dim1, act1, out, q0, s0, q1, s1, aq1, as1)
+
+
+def fp8moe_add_rmsnorm_bwd_ckpt(dy, hq, hs, rstd, weight, dh=None, dx=None, dweight=None, workspace=None, stream=None):
+    """fp8moe_add_rmsnorm_bwd on the values of hq [T, H], hs [T, H/32] (uint8:
+    MXFP8 codes and row-major scales, fp8moe_mxfp8_quantize_dim0 of h)."""
+    if hs is None:
+        raise Fp8MoeError("fp8moe_add_rmsnorm_bwd_ckpt", 1)
+    return _run("fp8moe_add_rmsnorm_bwd_ckpt", stream, _native().add_rmsnorm_bwd, dy, hq, rstd, weight, dh, dx, dweight,
+                workspace, hs)
+
+
+def fp8moe_route_weight_grad_ckpt(dout, yq, ys, row_of, dw=None, stream=None):
+    """fp8moe_route_weight_grad on the values of yq [rows, N], ys [rows, N/32]
+    (uint8: MXFP8 codes and row-major scales)."""
+    if ys is None:
+        raise Fp8MoeError("fp8moe_route_weight_grad_ckpt", 1)
+    return _run("fp8moe_route_weight_grad_ckpt", stream, _native().route_weight_grad, dout, yq, row_of, dw, ys)
 
 
 def fp8moe_mxfp8_moe_decode_workspace_bytes(T: int, k: int, E: int, H: int, F: int) -> int:

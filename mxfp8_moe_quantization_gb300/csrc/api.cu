@@ -499,9 +499,10 @@ int64_t fp8moe_add_rmsnorm_bwd_workspace_bytes(int64_t T, int64_t H) {
   return (T < fp8moe::NORM_BWD_PARTS ? T : fp8moe::NORM_BWD_PARTS) * H * (int64_t)sizeof(float);
 }
 
-fp8moe_status fp8moe_add_rmsnorm_bwd(const void* dy, const void* h, const float* rstd, const void* w,
-                                     int weight_type, const void* dh, int64_t T, int64_t H, void* dx, float* dw,
-                                     void* workspace, int64_t workspace_bytes, fp8moe_stream_t stream) {
+// h: bf16, or MXFP8 codes with their scales hs
+static fp8moe_status rmsnorm_bwd(const void* dy, const void* h, const uint8_t* hs, const float* rstd, const void* w,
+                                 int weight_type, const void* dh, int64_t T, int64_t H, void* dx, float* dw,
+                                 void* workspace, int64_t workspace_bytes, fp8moe_stream_t stream) {
   if (T < 0 || H < 1 || T > INT32_MAX - 128 || H > ((int64_t)1 << 20)) return FP8MOE_ERR_INVALID_ARG;
   if (weight_type != FP8MOE_BF16 && weight_type != FP8MOE_FP32) return FP8MOE_ERR_INVALID_ARG;
   if (H % 8) return FP8MOE_ERR_ALIGNMENT;
@@ -513,8 +514,22 @@ fp8moe_status fp8moe_add_rmsnorm_bwd(const void* dy, const void* h, const float*
   DevInfo* d;
   fp8moe_status st = device_info(&d);
   if (st) return st;
-  return cuda_result(fp8moe::launch_norm_bwd(dy, h, rstd, w, weight_type == FP8MOE_FP32, dh, T, H, dx, dw, workspace,
+  return cuda_result(fp8moe::launch_norm_bwd(dy, h, hs, rstd, w, weight_type == FP8MOE_FP32, dh, T, H, dx, dw, workspace,
                                              d->num_sms, d->max_smem, d->status, (cudaStream_t)stream));
+}
+
+fp8moe_status fp8moe_add_rmsnorm_bwd(const void* dy, const void* h, const float* rstd, const void* w,
+                                     int weight_type, const void* dh, int64_t T, int64_t H, void* dx, float* dw,
+                                     void* workspace, int64_t workspace_bytes, fp8moe_stream_t stream) {
+  return rmsnorm_bwd(dy, h, nullptr, rstd, w, weight_type, dh, T, H, dx, dw, workspace, workspace_bytes, stream);
+}
+
+fp8moe_status fp8moe_add_rmsnorm_bwd_ckpt(const void* dy, const void* hq, const uint8_t* hs, const float* rstd,
+                                          const void* w, int weight_type, const void* dh, int64_t T, int64_t H, void* dx,
+                                          float* dw, void* workspace, int64_t workspace_bytes, fp8moe_stream_t stream) {
+  if (H > 0 && H % 32) return FP8MOE_ERR_ALIGNMENT;
+  if (T > 0 && !hs) return FP8MOE_ERR_INVALID_ARG;
+  return rmsnorm_bwd(dy, hq, hs, rstd, w, weight_type, dh, T, H, dx, dw, workspace, workspace_bytes, stream);
 }
 
 int64_t fp8moe_router_workspace_bytes(int64_t T, int64_t E) {
@@ -614,25 +629,54 @@ fp8moe_status fp8moe_route_weight_grad(const void* dout, const void* y, const in
   return fp8moe_route_weight_grad_bounded(dout, y, (int64_t)1 << 31, row_of, T, N, k, dw, stream);
 }
 
+fp8moe_status fp8moe_route_weight_grad_ckpt(const void* dout, const void* yq, const uint8_t* ys, int64_t rows,
+                                            const int32_t* row_of, int64_t T, int64_t N, int64_t k, float* dw,
+                                            fp8moe_stream_t stream) {
+  if (rows < 0 || rows > ((int64_t)1 << 31) || T < 0 || N < 0 || k < 1 || T > ((int64_t)1 << 30) / k) return FP8MOE_ERR_INVALID_ARG;
+  if (N % 32) return FP8MOE_ERR_ALIGNMENT;
+  if (T == 0) return FP8MOE_OK;
+  if (!row_of || !dw || (N > 0 && (!dout || (rows > 0 && (!yq || !ys))))) return FP8MOE_ERR_INVALID_ARG;
+  if (!al16(dout) || !al16(yq) || (((uintptr_t)row_of | (uintptr_t)dw) & 3)) return FP8MOE_ERR_ALIGNMENT;
+  DevInfo* d;
+  fp8moe_status s = device_info(&d);
+  if (s) return s;
+  return cuda_result(fp8moe::launch_route_weight_grad_ckpt(dout, yq, ys, rows, row_of, T, N, k, dw, d->num_sms,
+                                                           (cudaStream_t)stream));
+}
+
+// What the checkpointed forms add: the codes and scales of h, written (forward) or
+// read in place of h (backward), and the activation along its columns.
+struct SwigluCkpt {
+  void* q;
+  uint8_t* s;
+  const void* hq;
+  const uint8_t* hs;
+  void* aq1;
+  uint8_t* as1;
+};
 static fp8moe_status swiglu(bool bwd, const void* dout, const void* h, int64_t ldh, int64_t M, int64_t F,
                             const int32_t* offs, int64_t E, void* out, void* q0, uint8_t* s0, int s0_layout, void* q1,
-                            uint8_t* s1, int s1_layout, fp8moe_stream_t stream) {
+                            uint8_t* s1, int s1_layout, const SwigluCkpt* ck, fp8moe_stream_t stream) {
   if (M < 0 || F < 1 || M > ((int64_t)1 << 30) || F > ((int64_t)1 << 28) || ldh < 2 * F)
     return FP8MOE_ERR_INVALID_ARG;
   if (F % 32 || ldh % 8) return FP8MOE_ERR_ALIGNMENT;
   if (M == 0) return FP8MOE_OK;
-  if (!(out || q0 || q1) || (q0 == nullptr) != (s0 == nullptr) || (q1 == nullptr) != (s1 == nullptr))
+  const bool act = ck && ck->aq1;
+  if (!(out || q0 || q1 || act || (ck && !bwd)) || (q0 == nullptr) != (s0 == nullptr) || (q1 == nullptr) != (s1 == nullptr))
     return FP8MOE_ERR_INVALID_ARG;
   const bool ok0 = !q0 || s0_layout == FP8MOE_SCALES_ROWMAJOR || s0_layout == FP8MOE_NO_GROUPS ||
                    s0_layout == FP8MOE_GROUP_ROWS;
-  const bool ok1 = !q1 || s1_layout == FP8MOE_SCALES_ROWMAJOR || s1_layout == FP8MOE_NO_GROUPS ||
+  if (act && !ck->as1) return FP8MOE_ERR_INVALID_ARG;
+  const bool ok1 = !(q1 || act) || s1_layout == FP8MOE_SCALES_ROWMAJOR || s1_layout == FP8MOE_NO_GROUPS ||
                    s1_layout == FP8MOE_GROUP_COLS;
   if (!ok0 || !ok1) return FP8MOE_ERR_INVALID_ARG;
-  const bool g0 = q0 && s0_layout == FP8MOE_GROUP_ROWS, g1 = q1 && s1_layout == FP8MOE_GROUP_COLS;
+  const bool g0 = q0 && s0_layout == FP8MOE_GROUP_ROWS, g1 = (q1 || act) && s1_layout == FP8MOE_GROUP_COLS;
   if ((g0 || g1) && (E < 1 || E > FP8MOE_MAX_GROUPS || !offs)) return FP8MOE_ERR_INVALID_ARG;
-  if ((q1 || g0) && M % 32) return FP8MOE_ERR_ALIGNMENT;
+  if ((q1 || act || g0) && M % 32) return FP8MOE_ERR_ALIGNMENT;
   if ((g0 || g1) && ((uintptr_t)offs & 3)) return FP8MOE_ERR_ALIGNMENT;
-  if (!h || (bwd && !dout)) return FP8MOE_ERR_INVALID_ARG;
+  if ((bwd && ck ? !ck->hq || !ck->hs : !h) || (bwd && !dout) || (ck && !bwd && (!ck->q || !ck->s)))
+    return FP8MOE_ERR_INVALID_ARG;
+  if (ck && (!al16(ck->q) || !al16(ck->hq) || !al16(ck->aq1))) return FP8MOE_ERR_ALIGNMENT;
   if (!al16(h) || !al16(dout) || !al16(out) || !al16(q0) || !al16(q1)) return FP8MOE_ERR_ALIGNMENT;
   DevInfo* d;
   fp8moe_status st = device_info(&d);
@@ -647,6 +691,11 @@ static fp8moe_status swiglu(bool bwd, const void* dout, const void* h, int64_t l
   a.out = (uint16_t*)out;
   a.q0 = (uint8_t*)q0, a.s0 = s0, a.q1 = (uint8_t*)q1, a.s1 = s1;
   a.s0_layout = s0_layout, a.s1_layout = s1_layout;
+  if (ck) {
+    a.ckpt_q = (uint8_t*)ck->q, a.ckpt_s = ck->s;
+    a.hq = (const uint8_t*)ck->hq, a.hs = ck->hs;
+    a.aq1 = (uint8_t*)ck->aq1, a.as1 = ck->as1;
+  }
   a.num_sms = d->num_sms;
   a.status = d->status;
   return cuda_result(fp8moe::launch_swiglu(a, (cudaStream_t)stream));
@@ -655,13 +704,30 @@ static fp8moe_status swiglu(bool bwd, const void* dout, const void* h, int64_t l
 fp8moe_status fp8moe_swiglu_fwd(const void* h, int64_t ldh, int64_t M, int64_t F, const int32_t* offs, int64_t E,
                                 void* out, void* q0, uint8_t* s0, int s0_layout, void* q1, uint8_t* s1,
                                 int s1_layout, fp8moe_stream_t stream) {
-  return swiglu(false, nullptr, h, ldh, M, F, offs, E, out, q0, s0, s0_layout, q1, s1, s1_layout, stream);
+  return swiglu(false, nullptr, h, ldh, M, F, offs, E, out, q0, s0, s0_layout, q1, s1, s1_layout, nullptr, stream);
 }
 
 fp8moe_status fp8moe_swiglu_bwd(const void* dout, const void* h, int64_t ldh, int64_t M, int64_t F,
                                 const int32_t* offs, int64_t E, void* dh, void* q0, uint8_t* s0, int s0_layout,
                                 void* q1, uint8_t* s1, int s1_layout, fp8moe_stream_t stream) {
-  return swiglu(true, dout, h, ldh, M, F, offs, E, dh, q0, s0, s0_layout, q1, s1, s1_layout, stream);
+  return swiglu(true, dout, h, ldh, M, F, offs, E, dh, q0, s0, s0_layout, q1, s1, s1_layout, nullptr, stream);
+}
+
+fp8moe_status fp8moe_swiglu_fwd_ckpt(const void* h, int64_t ldh, int64_t M, int64_t F, const int32_t* offs, int64_t E,
+                                     void* out, void* q0, uint8_t* s0, int s0_layout, void* q1, uint8_t* s1,
+                                     int s1_layout, void* hq, uint8_t* hs, fp8moe_stream_t stream) {
+  const SwigluCkpt ck{hq, hs, nullptr, nullptr, nullptr, nullptr};
+  return swiglu(false, nullptr, h, ldh, M, F, offs, E, out, q0, s0, s0_layout, q1, s1, s1_layout, &ck, stream);
+}
+
+fp8moe_status fp8moe_swiglu_bwd_ckpt(const void* dout, const void* hq, const uint8_t* hs, int64_t M, int64_t F,
+                                     const int32_t* offs, int64_t E, void* dh, void* q0, uint8_t* s0, int s0_layout,
+                                     void* q1, uint8_t* s1, int s1_layout, void* aq1, uint8_t* as1,
+                                     fp8moe_stream_t stream) {
+  const SwigluCkpt ck{nullptr, nullptr, hq, hs, aq1, as1};
+  if (F > ((int64_t)1 << 28)) return FP8MOE_ERR_INVALID_ARG;
+  if ((aq1 == nullptr) != (as1 == nullptr)) return FP8MOE_ERR_INVALID_ARG;
+  return swiglu(true, dout, nullptr, 2 * F, M, F, offs, E, dh, q0, s0, s0_layout, q1, s1, s1_layout, &ck, stream);
 }
 
 static bool decode_sizes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F) {

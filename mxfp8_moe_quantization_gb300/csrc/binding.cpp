@@ -222,14 +222,16 @@ PyObject* add_rmsnorm_fwd(PyObject* const* a) {
   return give_all(h, y, rstd, q, scale);
 }
 
-// dy, h, rstd, weight, dh, dx, dweight, workspace
+// dy, h, rstd, weight, dh, dx, dweight, workspace, hs (None: h is bf16; else MXFP8 codes)
 PyObject* add_rmsnorm_bwd(PyObject* const* a) {
   const Tensor& dy = tensor(a[0]);
+  const Tensor* hs = maybe(a[8]);
   if (dy.dim() != 2) refuse();
   const int64_t T = dy.size(0), H = dy.size(1);
   Call c(dy);
   const void* pdy = c.dense(dy, at::kBFloat16, {T, H});
-  const void* ph = c.dense(tensor(a[1]), at::kBFloat16, {T, H});
+  const void* ph = c.dense(tensor(a[1]), hs ? at::kByte : at::kBFloat16, {T, H});
+  const void* phs = c.dense(hs, at::kByte, {T, H / 32});
   const void* prstd = c.dense(tensor(a[2]), at::kFloat, {T});
   const Tensor& w = tensor(a[3]);
   const at::ScalarType wt = real_type(w);
@@ -241,8 +243,13 @@ PyObject* add_rmsnorm_bwd(PyObject* const* a) {
   void* pdw = c.out(dw, a[6], at::kFloat, {H});
   int64_t nbytes = fp8moe_add_rmsnorm_bwd_workspace_bytes(T, H);
   void* pws = c.workspace(ws, a[7], nbytes);
-  check(fp8moe_add_rmsnorm_bwd(pdy, ph, (const float*)prstd, pw, type_code(wt), pdh, T, H, pdx, (float*)pdw, pws, nbytes,
-                               c.stream()));
+  if (hs) {
+    check(fp8moe_add_rmsnorm_bwd_ckpt(pdy, ph, (const uint8_t*)phs, (const float*)prstd, pw, type_code(wt), pdh, T, H, pdx,
+                                      (float*)pdw, pws, nbytes, c.stream()));
+  } else {
+    check(fp8moe_add_rmsnorm_bwd(pdy, ph, (const float*)prstd, pw, type_code(wt), pdh, T, H, pdx, (float*)pdw, pws, nbytes,
+                                 c.stream()));
+  }
   return give_all(dx, dw);
 }
 
@@ -306,18 +313,25 @@ PyObject* router_bwd(PyObject* const* a) {
   return give(d);
 }
 
-// dout, y, row_of, dw
+// dout, y, row_of, dw, ys (None: y is bf16; else MXFP8 codes)
 PyObject* route_weight_grad(PyObject* const* a) {
+  const Tensor* ys = maybe(a[4]);
   const Tensor &dout = tensor(a[0]), &y = tensor(a[1]), &row_of = tensor(a[2]);
   if (dout.dim() != 2 || y.dim() != 2 || row_of.dim() != 2) refuse();
   const int64_t T = dout.size(0), N = dout.size(1), k = row_of.size(1);
   Call c(dout);
   const void* pd = c.dense(dout, at::kBFloat16, {T, N});
-  const void* py = c.dense(y, at::kBFloat16, {y.size(0), N});
+  const void* py = c.dense(y, ys ? at::kByte : at::kBFloat16, {y.size(0), N});
+  const void* pys = c.dense(ys, at::kByte, {y.size(0), N / 32});
   const void* pr = c.dense(row_of, at::kInt, {T, k});
   Tensor dw;
   void* pw = c.out(dw, a[3], at::kFloat, {T, k});
-  check(fp8moe_route_weight_grad_bounded(pd, py, y.size(0), (const int32_t*)pr, T, N, k, (float*)pw, c.stream()));
+  if (ys) {
+    check(fp8moe_route_weight_grad_ckpt(pd, py, (const uint8_t*)pys, y.size(0), (const int32_t*)pr, T, N, k, (float*)pw,
+                                        c.stream()));
+  } else {
+    check(fp8moe_route_weight_grad_bounded(pd, py, y.size(0), (const int32_t*)pr, T, N, k, (float*)pw, c.stream()));
+  }
   return give(dw);
 }
 
@@ -367,6 +381,62 @@ PyObject* swiglu(PyObject* const* a) {
   return give_all(out, q0, s0, q1, s1);
 }
 
+// h, offs, s0_layout, s1_layout, need_out, dim0, dim1, out, q0, s0, q1, s1, hq, hs
+PyObject* swiglu_fwd_ckpt(PyObject* const* a) {
+  const Tensor& h = tensor(a[0]);
+  const Tensor* offs = maybe(a[1]);
+  if (h.dim() != 2 || h.size(1) % 64) refuse();
+  const int64_t M = h.size(0), F = h.size(1) / 2;
+  Call c(h);
+  int64_t ldh = 0;
+  const void* ph = c.rows(h, at::kBFloat16, {M, 2 * F}, ldh);
+  const int64_t E = offs ? offs->numel() : 0;
+  const void* po = c.dense(offs, at::kInt, {E});
+  const int l0 = small(a[2]), l1 = small(a[3]);
+  Tensor out, q0, s0, q1, s1, hq, hs;
+  void *pout = nullptr, *p0 = nullptr, *p1 = nullptr;
+  uint8_t *ps0 = nullptr, *ps1 = nullptr;
+  const bool o = flag(a[4]), d0 = flag(a[5]), d1 = flag(a[6]);
+  c.together({o && a[7] == Py_None ? M * F * 2 : 0, d0 && a[8] == Py_None ? M * F : 0, d1 && a[10] == Py_None ? M * F : 0,
+              a[12] == Py_None ? M * 2 * F : 0, a[13] == Py_None ? M * F / 16 : 0});
+  if (o) pout = c.out(out, a[7], at::kBFloat16, {M, F});
+  if (d0) mx_out(c, q0, a[8], s0, a[9], l0, M, F, E, p0, ps0);
+  if (d1) mx_out(c, q1, a[10], s1, a[11], l1, F, M, E, p1, ps1);
+  void* phq = c.out(hq, a[12], at::kByte, {M, 2 * F});
+  void* phs = c.out(hs, a[13], at::kByte, {M, F / 16});
+  check(fp8moe_swiglu_fwd_ckpt(ph, ldh, M, F, (const int32_t*)po, E, pout, p0, ps0, l0, p1, ps1, l1, phq, (uint8_t*)phs,
+                               c.stream()));
+  return give_all(out, q0, s0, q1, s1, hq, hs);
+}
+
+// dout, hq, hs, offs, s0_layout, s1_layout, need_dh, dim0, dim1, act1, out, q0, s0, q1, s1, aq1, as1
+PyObject* swiglu_bwd_ckpt(PyObject* const* a) {
+  const Tensor &dout = tensor(a[0]), &hq = tensor(a[1]), &hs = tensor(a[2]);
+  const Tensor* offs = maybe(a[3]);
+  if (dout.dim() != 2 || dout.size(1) % 32) refuse();
+  const int64_t M = dout.size(0), F = dout.size(1);
+  Call c(dout);
+  const void* pd = c.dense(dout, at::kBFloat16, {M, F});
+  const void* phq = c.dense(hq, at::kByte, {M, 2 * F});
+  const void* phs = c.dense(hs, at::kByte, {M, F / 16});
+  const int64_t E = offs ? offs->numel() : 0;
+  const void* po = c.dense(offs, at::kInt, {E});
+  const int l0 = small(a[4]), l1 = small(a[5]);
+  Tensor out, q0, s0, q1, s1, aq1, as1;
+  void *pout = nullptr, *p0 = nullptr, *p1 = nullptr, *pa = nullptr;
+  uint8_t *ps0 = nullptr, *ps1 = nullptr, *psa = nullptr;
+  const bool o = flag(a[6]), d0 = flag(a[7]), d1 = flag(a[8]), act = flag(a[9]);
+  c.together({o && a[10] == Py_None ? M * F * 4 : 0, d0 && a[11] == Py_None ? M * F * 2 : 0,
+              d1 && a[13] == Py_None ? M * F * 2 : 0, act && a[15] == Py_None ? M * F : 0});
+  if (o) pout = c.out(out, a[10], at::kBFloat16, {M, 2 * F});
+  if (d0) mx_out(c, q0, a[11], s0, a[12], l0, M, 2 * F, E, p0, ps0);
+  if (d1) mx_out(c, q1, a[13], s1, a[14], l1, 2 * F, M, E, p1, ps1);
+  if (act) mx_out(c, aq1, a[15], as1, a[16], l1, F, M, E, pa, psa);
+  check(fp8moe_swiglu_bwd_ckpt(pd, phq, (const uint8_t*)phs, M, F, (const int32_t*)po, E, pout, p0, ps0, l0, p1, ps1, l1, pa,
+                               psa, c.stream()));
+  return give_all(out, q0, s0, q1, s1, aq1, as1);
+}
+
 // x, topk_idx, topk_w, w1, w1_scale, w2, w2_scale, out, workspace
 PyObject* moe_decode(PyObject* const* a) {
   const Tensor &x = tensor(a[0]), &idx = tensor(a[1]), &w1 = tensor(a[3]), &w2 = tensor(a[5]);
@@ -412,10 +482,11 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 #define FP8MOE_ENTRY(NAME, N) \
   {#NAME, (PyCFunction)(void (*)(void))entry<NAME, N>, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FP8MOE_ENTRY(add_rmsnorm_fwd, 14),   FP8MOE_ENTRY(add_rmsnorm_bwd, 8),
+PyMethodDef methods[] = {FP8MOE_ENTRY(add_rmsnorm_fwd, 14),   FP8MOE_ENTRY(add_rmsnorm_bwd, 9),
                          FP8MOE_ENTRY(router_fwd, 14),        FP8MOE_ENTRY(router_bwd, 10),
-                         FP8MOE_ENTRY(route_weight_grad, 4),  FP8MOE_ENTRY(swiglu, 13),
-                         FP8MOE_ENTRY(moe_decode, 9),
+                         FP8MOE_ENTRY(route_weight_grad, 5),  FP8MOE_ENTRY(swiglu, 13),
+                         FP8MOE_ENTRY(moe_decode, 9),         FP8MOE_ENTRY(swiglu_fwd_ckpt, 14),
+                         FP8MOE_ENTRY(swiglu_bwd_ckpt, 17),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -98,8 +98,9 @@ constexpr int NORM_BWD_PARTS = 512;
 cudaError_t launch_norm_fwd(const void* x, int64_t ldx, const void* r, int64_t ldr, const void* w, int w32, int64_t T,
                             int64_t H, float eps, void* h, void* y, float* rstd, int recipe, int kind, void* q,
                             void* scale, int scale_layout, int num_sms, cudaStream_t st);
-cudaError_t launch_norm_bwd(const void* dy, const void* h, const float* rstd, const void* w, int w32, const void* dh,
-                            int64_t T, int64_t H, void* dx, float* dw, void* workspace, int num_sms, int max_smem,
+// (hs: h is MXFP8 codes with these row-major scales; NULL: bf16)
+cudaError_t launch_norm_bwd(const void* dy, const void* h, const uint8_t* hs, const float* rstd, const void* w, int w32,
+                            const void* dh, int64_t T, int64_t H, void* dx, float* dw, void* workspace, int num_sms, int max_smem,
                             int* status, cudaStream_t st);
 
 // the router (router.cu)
@@ -109,6 +110,10 @@ cudaError_t launch_router_bwd(const RouterArgs& a, int num_sms, cudaStream_t st)
 // (rows of y: at most 2^31; a row number past them is a missing one)
 cudaError_t launch_route_weight_grad(const void* dout, const void* y, int64_t rows, const int32_t* row_of, int64_t T,
                                      int64_t N, int64_t k, float* dw, int num_sms, cudaStream_t st);
+
+cudaError_t launch_route_weight_grad_ckpt(const void* dout, const void* yq, const uint8_t* ys, int64_t rows,
+                                          const int32_t* row_of, int64_t T, int64_t N, int64_t k, float* dw, int num_sms,
+                                          cudaStream_t st);
 
 // gated activation with MXFP8 output (swiglu.cu); dout == NULL: forward
 struct SwigluArgs;

@@ -46,6 +46,11 @@ struct SwigluArgs {
   uint16_t* out;         // [M, W] bf16 or NULL (W = F forward, 2F backward)
   uint8_t *q0, *s0, *q1, *s1;
   int s0_layout, s1_layout;
+  // h in MXFP8 with row-major scales: written by a forward with a checkpoint
+  // (ckpt_q not NULL), read by a backward from it (hq not NULL, in place of h)
+  uint8_t *ckpt_q, *ckpt_s;
+  const uint8_t *hq, *hs;
+  uint8_t *aq1, *as1;    // that backward's: the activation along its columns, scales in s1's layout, or NULL
   int num_sms;
   int* status;
   int stall;             // test hook: the first CTA's first warp never loads its first tile

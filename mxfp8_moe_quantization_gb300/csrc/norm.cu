@@ -355,6 +355,7 @@ cudaError_t launch_fwd_t(const NormFwdArgs& a, int num_sms, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 struct NormBwdArgs {
   const uint16_t *dy, *h, *dh;
+  const uint8_t *hq, *hs;   // h in MXFP8, row-major scales (CK)
   const float* rstd;
   const void* w;
   int64_t T;
@@ -370,7 +371,9 @@ struct NormBwdArgs {
 // row, so its share of dw stays in registers.  The blocks come through a ring
 // of `stages` slots that thread 0 fills with bulk copies: the slot of a block
 // is free at the next block's barrier (every thread has then read it).
-template <int V, bool W32>
+// CK: h comes as e4m3 codes through the ring, behind dy and dh, and its scale bytes
+// by plain loads, one block ahead as rstd.
+template <int V, bool W32, bool CK>
 __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs a, int wpr, int stages) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float red[2][NORM_RED];
@@ -380,7 +383,9 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
   const int tpr = wpr * 32, groups = blockDim.x / tpr, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
   const int nch = a.H / 8;
   const uint32_t row_bytes = (uint32_t)a.H * 2, ten_bytes = row_bytes * groups;
-  const uint32_t slot_bytes = ten_bytes * (a.dh ? 3 : 2);
+  const uint32_t slot_bytes = ten_bytes * (a.dh ? 3 : 2) - (CK ? ten_bytes / 2 : 0);
+  // where h and dh are in a slot
+  const uint32_t at_h = CK && a.dh ? 2 * ten_bytes : ten_bytes, at_dh = CK ? ten_bytes : 2 * ten_bytes;
   const int blocks = (int)((a.T + groups - 1) / groups);
   // thread 0: block nblk, the next to load, goes to slot nslot
   int nblk = blockIdx.x, nslot = 0;
@@ -390,10 +395,14 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
     const uint32_t bytes = row_bytes * (uint32_t)(a.T - r0 < groups ? a.T - r0 : groups);
     if (!a.stall || nblk > 0) {
       ++fills[nslot];
-      mbar_expect_tx(&full[nslot], bytes * (a.dh ? 3 : 2));
+      mbar_expect_tx(&full[nslot], bytes * (a.dh ? 3 : 2) - (CK ? bytes / 2 : 0));
       bulk_load(dst, a.dy + at, bytes, &full[nslot]);
-      bulk_load(dst + ten_bytes, a.h + at, bytes, &full[nslot]);
-      if (a.dh) bulk_load(dst + 2 * ten_bytes, a.dh + at, bytes, &full[nslot]);
+      if constexpr (CK) {
+        bulk_load(dst + at_h, a.hq + at, bytes / 2, &full[nslot]);
+      } else {
+        bulk_load(dst + at_h, a.h + at, bytes, &full[nslot]);
+      }
+      if (a.dh) bulk_load(dst + at_dh, a.dh + at, bytes, &full[nslot]);
     }
     nblk += gridDim.x;
     if (++nslot == stages) nslot = 0;
@@ -424,6 +433,17 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
   const float* prstd = a.rstd + row;
   uint16_t* pdx = a.dx + row * a.H + t * 8;
   float rstd = row < a.T ? *prstd : 0.0f;
+  uint32_t sc[CK ? V : 1] = {}, sc_next[CK ? V : 1] = {};
+  auto load_scales = [&](int64_t r) {
+    if constexpr (CK) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int ch = t + i * tpr;
+        sc_next[i] = r < a.T && ch < nch ? (uint32_t)__ldg(a.hs + r * (nch >> 2) + (ch >> 2)) : 0u;
+      }
+    }
+  };
+  load_scales(row);
   __syncthreads();
   int s = 0, par = 0;
   uint32_t phase = 0;
@@ -432,11 +452,17 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
     prstd += step;
     const float rstd_next = row + step < a.T ? *prstd : 0.0f;
     const uint64_t rstd2 = pk(rstd, rstd);
+    if constexpr (CK) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) sc[i] = sc_next[i];
+      load_scales(row + step);
+    }
     if (!mbar_wait(&full[s], phase, abort_flag)) {
       set_status(a.status, FP8MOE_ERR_TIMEOUT);
       *abort_flag = 1;
     }
     const uint8_t* src = ring + s * slot_bytes + group * row_bytes;
+    const uint8_t* src_h = ring + s * slot_bytes + at_h + group * (CK ? row_bytes / 2 : row_bytes);
     Vec8 g[V], xh[V];
     uint64_t dot2 = 0;
 #pragma unroll
@@ -444,7 +470,13 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
       const int ch = t + i * tpr;
       if (ch >= nch || !live) continue;
       const uint4 dq = *reinterpret_cast<const uint4*>(src + ch * 16);
-      const Vec8 d = unpack8(dq), x = unpack8(*reinterpret_cast<const uint4*>(src + ten_bytes + ch * 16));
+      const Vec8 d = unpack8(dq);
+      Vec8 x;
+      if constexpr (CK) {
+        mx_unpack8(*reinterpret_cast<const uint2*>(src_h + ch * 8), mx_power(sc[i]), x.p);
+      } else {
+        x = unpack8(*reinterpret_cast<const uint4*>(src_h + ch * 16));
+      }
       if constexpr (!KEEP_W) {
         const Vec8 wf = load_w8<W32>(a.w, ch);
 #pragma unroll
@@ -478,7 +510,7 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
     for (int i = 0; i < V; ++i) {
       const int ch = t + i * tpr;
       if (ch >= nch || !live) continue;
-      const Vec8 sv = a.dh ? unpack8(*reinterpret_cast<const uint4*>(src + 2 * ten_bytes + ch * 16)) : Vec8{};
+      const Vec8 sv = a.dh ? unpack8(*reinterpret_cast<const uint4*>(src + at_dh + ch * 16)) : Vec8{};
       Vec8 o;
 #pragma unroll
       for (int j = 0; j < 4; ++j) o.p[j] = fma2(rstd2, fma2(xh[i].p[j], c2, g[i].p[j]), sv.p[j]);
@@ -522,11 +554,20 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
 
 // Rows longer than that: the row is read twice (the second time from L2) and
 // a thread's share of dw stays in its CTA's row of the partials.
-template <bool W32>
+template <bool W32, bool CK>
 __global__ void __launch_bounds__(512) k_norm_bwd_long(NormBwdArgs a, int, int) {
   __shared__ float red[2][NORM_RED];
   const int t = threadIdx.x, n = blockDim.x, nch = a.H / 8;
   float* part = a.part + (int64_t)blockIdx.x * a.H;
+  auto load_h = [&](int64_t at) {
+    if constexpr (CK) {
+      Vec8 x;
+      mx_unpack8(__ldg(reinterpret_cast<const uint2*>(a.hq + at)), mx_power(__ldg(a.hs + (at >> 5))), x.p);
+      return x;
+    } else {
+      return unpack8(ld16(a.h + at));
+    }
+  };
   int par = 0;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, par ^= 1) {
     const float rstd = a.rstd[row];
@@ -534,7 +575,7 @@ __global__ void __launch_bounds__(512) k_norm_bwd_long(NormBwdArgs a, int, int) 
     uint64_t dot2 = 0;
     for (int ch = t; ch < nch; ch += n) {
       const Vec8 d = unpack8(ld16(a.dy + row * a.H + (int64_t)ch * 8));
-      const Vec8 x = unpack8(ld16(a.h + row * a.H + (int64_t)ch * 8)), wf = load_w8<W32>(a.w, ch);
+      const Vec8 x = load_h(row * a.H + (int64_t)ch * 8), wf = load_w8<W32>(a.w, ch);
 #pragma unroll
       for (int j = 0; j < 4; ++j) dot2 = fma2(mul2(d.p[j], wf.p[j]), mul2(x.p[j], rstd2), dot2);
     }
@@ -542,7 +583,7 @@ __global__ void __launch_bounds__(512) k_norm_bwd_long(NormBwdArgs a, int, int) 
     const float c = -__fdiv_rn(dot, (float)a.H);
     for (int ch = t; ch < nch; ch += n) {
       const int64_t at = row * a.H + (int64_t)ch * 8;
-      const Vec8 d = unpack8(ld16(a.dy + at)), x = unpack8(ld16(a.h + at)), wf = load_w8<W32>(a.w, ch);
+      const Vec8 d = unpack8(ld16(a.dy + at)), x = load_h(at), wf = load_w8<W32>(a.w, ch);
       const Vec8 sv = a.dh ? unpack8(ld16(a.dh + at)) : Vec8{};
       uint64_t* p = reinterpret_cast<uint64_t*>(part + (int64_t)ch * 8);
       Vec8 o;
@@ -575,7 +616,7 @@ __global__ void __launch_bounds__(1024) k_norm_dw(const float* part, int P, int 
   if (lane == 0 && blockIdx.x * 32 + warp < H) dw[blockIdx.x * 32 + warp] = v;
 }
 
-template <bool W32>
+template <bool W32, bool CK>
 cudaError_t launch_bwd_t(NormBwdArgs a, float* dw, int num_sms, int max_smem, cudaStream_t st) {
   const int nch = a.H / 8;
   // One chunk a thread while rows are short and there is more to read for it than
@@ -589,7 +630,7 @@ cudaError_t launch_bwd_t(NormBwdArgs a, float* dw, int num_sms, int max_smem, cu
   // The ring: as deep as lets two CTAs share an SM, at least three blocks if
   // they fit one (16384 x 5120: 108 us with three, 132 with two)
   const int64_t budget = max_smem - 2048;
-  const int64_t slot = (int64_t)a.H * 2 * (a.dh ? 3 : 2) * groups;
+  const int64_t slot = (int64_t)a.H * ((a.dh ? 6 : 4) - (CK ? 1 : 0)) * groups;
   int stages = (int)(budget / 2 / slot < NORM_BWD_STAGES ? budget / 2 / slot : NORM_BWD_STAGES);
   if (stages < 3) stages = slot * 3 <= budget ? 3 : 2;
   const bool ring = nch <= NORM_MAX_CHUNKS && slot * stages <= budget;
@@ -609,10 +650,10 @@ cudaError_t launch_bwd_t(NormBwdArgs a, float* dw, int num_sms, int max_smem, cu
     kern<<<(unsigned)P, wpr * 32 * groups, smem, st>>>(a, wpr, stages);
     return cudaGetLastError();
   };
-  cudaError_t e = !ring    ? run(k_norm_bwd_long<W32>)
-                  : v == 1 ? run(k_norm_bwd<1, W32>)
-                  : v == 2 ? run(k_norm_bwd<2, W32>)
-                           : run(k_norm_bwd<4, W32>);
+  cudaError_t e = !ring    ? run(k_norm_bwd_long<W32, CK>)
+                  : v == 1 ? run(k_norm_bwd<1, W32, CK>)
+                  : v == 2 ? run(k_norm_bwd<2, W32, CK>)
+                           : run(k_norm_bwd<4, W32, CK>);
   if (e != cudaSuccess) return e;
   // launched ahead of the first kernel's end, for which it waits
   cudaLaunchConfig_t cfg = {};
@@ -655,14 +696,15 @@ cudaError_t launch_norm_fwd(const void* x, int64_t ldx, const void* r, int64_t l
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_norm_bwd(const void* dy, const void* h, const float* rstd, const void* w, int w32, const void* dh,
-                            int64_t T, int64_t H, void* dx, float* dw, void* workspace, int num_sms, int max_smem,
+cudaError_t launch_norm_bwd(const void* dy, const void* h, const uint8_t* hs, const float* rstd, const void* w, int w32,
+                            const void* dh, int64_t T, int64_t H, void* dx, float* dw, void* workspace, int num_sms, int max_smem,
                             int* status, cudaStream_t st) {
   if (T == 0) return cudaMemsetAsync(dw, 0, (size_t)H * sizeof(float), st);
   NormBwdArgs a{};
-  a.dy = (const uint16_t*)dy, a.h = (const uint16_t*)h, a.dh = (const uint16_t*)dh, a.rstd = rstd, a.w = w;
+  a.dy = (const uint16_t*)dy, a.h = (const uint16_t*)h, a.hq = (const uint8_t*)h, a.hs = hs, a.dh = (const uint16_t*)dh, a.rstd = rstd, a.w = w;
   a.T = T, a.H = (int)H, a.dx = (uint16_t*)dx, a.part = (float*)workspace, a.status = status;
-  return w32 ? launch_bwd_t<true>(a, dw, num_sms, max_smem, st) : launch_bwd_t<false>(a, dw, num_sms, max_smem, st);
+  if (hs) return w32 ? launch_bwd_t<true, true>(a, dw, num_sms, max_smem, st) : launch_bwd_t<false, true>(a, dw, num_sms, max_smem, st);
+  return w32 ? launch_bwd_t<true, false>(a, dw, num_sms, max_smem, st) : launch_bwd_t<false, false>(a, dw, num_sms, max_smem, st);
 }
 
 }  // namespace fp8moe
