@@ -704,8 +704,9 @@ fp8moe_status fp8moe_testing_stall_next_tensorwise(void);
  * fp8moe_mxfp8_quantize_dual with both directions and at least 128 columns,
  * fp8moe_quantize_colwise_3d of routed rows with transposed output,
  * fp8moe_swiglu_fwd / _bwd of more tiles (64 rows x 128 columns) than the
- * device has SMs, fp8moe_add_rmsnorm_bwd of rows up to 16384 elements (both
- * with _ckpt too), and fp8moe_mxfp8_moe_decode.
+ * device has SMs, fp8moe_add_rmsnorm_bwd of rows up to 16384 elements (and
+ * fp8moe_swiglu_fwd_ckpt, fp8moe_add_rmsnorm_bwd_ckpt), and
+ * fp8moe_mxfp8_moe_decode.
  * Arms a one-shot flag: the next such launch of the process never loads one
  * tile (the first CTA's first tile or rows; the routed-rows colwise kernel:
  * the first tile of its first unit, whichever CTA takes it; the gated

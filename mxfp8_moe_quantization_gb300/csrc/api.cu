@@ -632,7 +632,7 @@ fp8moe_status fp8moe_route_weight_grad(const void* dout, const void* y, const in
 fp8moe_status fp8moe_route_weight_grad_ckpt(const void* dout, const void* yq, const uint8_t* ys, int64_t rows,
                                             const int32_t* row_of, int64_t T, int64_t N, int64_t k, float* dw,
                                             fp8moe_stream_t stream) {
-  if (rows < 0 || rows > ((int64_t)1 << 31) || T < 0 || N < 0 || k < 1 || T > ((int64_t)1 << 30) / k) return FP8MOE_ERR_INVALID_ARG;
+  if (rows < 0 || rows > ((int64_t)1 << 31) || T < 0 || N < 0 || N > INT32_MAX || k < 1 || T > ((int64_t)1 << 30) / k) return FP8MOE_ERR_INVALID_ARG;
   if (N % 32) return FP8MOE_ERR_ALIGNMENT;
   if (T == 0) return FP8MOE_OK;
   if (!row_of || !dw || (N > 0 && (!dout || (rows > 0 && (!yq || !ys))))) return FP8MOE_ERR_INVALID_ARG;

@@ -69,7 +69,7 @@ FP8MOE_DEV float nanmax(float a, float b) {
 // MXFP8 back to values: an e8m0 byte's power of two (255 is NaN), and eight e4m3
 // codes times it, as pairs; exact.
 FP8MOE_DEV float mx_power(uint32_t byte) {
-  return __uint_as_float(byte == 0u ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
+  return __uint_as_float(byte == 255u ? 0x7FC00000u : max(byte << 23, 0x00400000u));
 }
 FP8MOE_DEV uint64_t e4m3x2_f32(uint32_t c) {   // of the low 16 bits
   float x, y;
@@ -83,12 +83,6 @@ FP8MOE_DEV void mx_unpack8(uint2 c, float power, uint64_t (&p)[4]) {
   const uint64_t s = pk(power, power);
   p[0] = mul2(e4m3x2_f32(c.x), s), p[1] = mul2(e4m3x2_f32(c.x >> 16), s);
   p[2] = mul2(e4m3x2_f32(c.y), s), p[3] = mul2(e4m3x2_f32(c.y >> 16), s);
-}
-// the same as bf16 pairs: exact from 2^-126 on, multiples of 2^-133 below
-FP8MOE_DEV uint4 mx_unpack8_bf16(uint2 c, float power) {
-  uint64_t p[4];
-  mx_unpack8(c, power, p);
-  return make_uint4(pack_bf16x2(p[0]), pack_bf16x2(p[1]), pack_bf16x2(p[2]), pack_bf16x2(p[3]));
 }
 // e8m0 byte of a block maximum (the dim0 quantizer's rule on an fp32 maximum)
 // and the multiplier 2^-e; infinity and NaN give a byte that no number gives

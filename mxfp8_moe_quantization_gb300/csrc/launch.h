@@ -118,6 +118,8 @@ cudaError_t launch_route_weight_grad_ckpt(const void* dout, const void* yq, cons
 // gated activation with MXFP8 output (swiglu.cu); dout == NULL: forward
 struct SwigluArgs;
 cudaError_t launch_swiglu(const SwigluArgs& a, cudaStream_t st);
+// its backward from a checkpoint (swiglu_ckpt.cu)
+cudaError_t launch_swiglu_bwd_ckpt(const SwigluArgs& a, cudaStream_t st);
 
 // the expert layer of a few tokens (decode.cu)
 struct DecodeArgs;

@@ -355,7 +355,7 @@ cudaError_t launch_fwd_t(const NormFwdArgs& a, int num_sms, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 struct NormBwdArgs {
   const uint16_t *dy, *h, *dh;
-  const uint8_t *hq, *hs;   // h in MXFP8, row-major scales (CK)
+  const uint8_t *hq, *hs;   // h in MXFP8, row-major scales (the checkpointed forms)
   const float* rstd;
   const void* w;
   int64_t T;
@@ -371,9 +371,7 @@ struct NormBwdArgs {
 // row, so its share of dw stays in registers.  The blocks come through a ring
 // of `stages` slots that thread 0 fills with bulk copies: the slot of a block
 // is free at the next block's barrier (every thread has then read it).
-// CK: h comes as e4m3 codes through the ring, behind dy and dh, and its scale bytes
-// by plain loads, one block ahead as rstd.
-template <int V, bool W32, bool CK>
+template <int V, bool W32>
 __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs a, int wpr, int stages) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float red[2][NORM_RED];
@@ -383,9 +381,7 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
   const int tpr = wpr * 32, groups = blockDim.x / tpr, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
   const int nch = a.H / 8;
   const uint32_t row_bytes = (uint32_t)a.H * 2, ten_bytes = row_bytes * groups;
-  const uint32_t slot_bytes = ten_bytes * (a.dh ? 3 : 2) - (CK ? ten_bytes / 2 : 0);
-  // where h and dh are in a slot
-  const uint32_t at_h = CK && a.dh ? 2 * ten_bytes : ten_bytes, at_dh = CK ? ten_bytes : 2 * ten_bytes;
+  const uint32_t slot_bytes = ten_bytes * (a.dh ? 3 : 2);
   const int blocks = (int)((a.T + groups - 1) / groups);
   // thread 0: block nblk, the next to load, goes to slot nslot
   int nblk = blockIdx.x, nslot = 0;
@@ -395,14 +391,10 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
     const uint32_t bytes = row_bytes * (uint32_t)(a.T - r0 < groups ? a.T - r0 : groups);
     if (!a.stall || nblk > 0) {
       ++fills[nslot];
-      mbar_expect_tx(&full[nslot], bytes * (a.dh ? 3 : 2) - (CK ? bytes / 2 : 0));
+      mbar_expect_tx(&full[nslot], bytes * (a.dh ? 3 : 2));
       bulk_load(dst, a.dy + at, bytes, &full[nslot]);
-      if constexpr (CK) {
-        bulk_load(dst + at_h, a.hq + at, bytes / 2, &full[nslot]);
-      } else {
-        bulk_load(dst + at_h, a.h + at, bytes, &full[nslot]);
-      }
-      if (a.dh) bulk_load(dst + at_dh, a.dh + at, bytes, &full[nslot]);
+      bulk_load(dst + ten_bytes, a.h + at, bytes, &full[nslot]);
+      if (a.dh) bulk_load(dst + 2 * ten_bytes, a.dh + at, bytes, &full[nslot]);
     }
     nblk += gridDim.x;
     if (++nslot == stages) nslot = 0;
@@ -433,17 +425,6 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
   const float* prstd = a.rstd + row;
   uint16_t* pdx = a.dx + row * a.H + t * 8;
   float rstd = row < a.T ? *prstd : 0.0f;
-  uint32_t sc[CK ? V : 1] = {}, sc_next[CK ? V : 1] = {};
-  auto load_scales = [&](int64_t r) {
-    if constexpr (CK) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int ch = t + i * tpr;
-        sc_next[i] = r < a.T && ch < nch ? (uint32_t)__ldg(a.hs + r * (nch >> 2) + (ch >> 2)) : 0u;
-      }
-    }
-  };
-  load_scales(row);
   __syncthreads();
   int s = 0, par = 0;
   uint32_t phase = 0;
@@ -452,17 +433,11 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
     prstd += step;
     const float rstd_next = row + step < a.T ? *prstd : 0.0f;
     const uint64_t rstd2 = pk(rstd, rstd);
-    if constexpr (CK) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) sc[i] = sc_next[i];
-      load_scales(row + step);
-    }
     if (!mbar_wait(&full[s], phase, abort_flag)) {
       set_status(a.status, FP8MOE_ERR_TIMEOUT);
       *abort_flag = 1;
     }
     const uint8_t* src = ring + s * slot_bytes + group * row_bytes;
-    const uint8_t* src_h = ring + s * slot_bytes + at_h + group * (CK ? row_bytes / 2 : row_bytes);
     Vec8 g[V], xh[V];
     uint64_t dot2 = 0;
 #pragma unroll
@@ -470,13 +445,7 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
       const int ch = t + i * tpr;
       if (ch >= nch || !live) continue;
       const uint4 dq = *reinterpret_cast<const uint4*>(src + ch * 16);
-      const Vec8 d = unpack8(dq);
-      Vec8 x;
-      if constexpr (CK) {
-        mx_unpack8(*reinterpret_cast<const uint2*>(src_h + ch * 8), mx_power(sc[i]), x.p);
-      } else {
-        x = unpack8(*reinterpret_cast<const uint4*>(src_h + ch * 16));
-      }
+      const Vec8 d = unpack8(dq), x = unpack8(*reinterpret_cast<const uint4*>(src + ten_bytes + ch * 16));
       if constexpr (!KEEP_W) {
         const Vec8 wf = load_w8<W32>(a.w, ch);
 #pragma unroll
@@ -510,13 +479,215 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
     for (int i = 0; i < V; ++i) {
       const int ch = t + i * tpr;
       if (ch >= nch || !live) continue;
-      const Vec8 sv = a.dh ? unpack8(*reinterpret_cast<const uint4*>(src + at_dh + ch * 16)) : Vec8{};
+      const Vec8 sv = a.dh ? unpack8(*reinterpret_cast<const uint4*>(src + 2 * ten_bytes + ch * 16)) : Vec8{};
       Vec8 o;
 #pragma unroll
       for (int j = 0; j < 4; ++j) o.p[j] = fma2(rstd2, fma2(xh[i].p[j], c2, g[i].p[j]), sv.p[j]);
       *reinterpret_cast<uint4*>(pdx + i * tpr * 8) = pack8(o);
     }
     rstd = rstd_next;
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;");
+  // after a wait that ran out blocks may be in flight still: none may land in
+  // shared memory that is no longer this CTA's
+  if (threadIdx.x == 0 && *abort_flag)
+    for (int i = 0; i < stages; ++i)
+      if (fills[i] > 0) (void)mbar_wait(&full[i], (uint32_t)(fills[i] - 1) & 1u, nullptr);
+  // the groups' shares of dw, added in order through the ring's memory
+  float* sum = reinterpret_cast<float*>(ring);
+  for (int q = 0; q < groups; ++q) {
+    __syncthreads();
+    if (group != q) continue;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int ch = t + i * tpr;
+      if (ch >= nch) continue;
+      uint64_t* p = reinterpret_cast<uint64_t*>(sum + ch * 8);
+      uint64_t* out = reinterpret_cast<uint64_t*>(a.part + (int64_t)blockIdx.x * a.H + (int64_t)ch * 8);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t v = q == 0 ? dw[i].p[j] : add2(p[j], dw[i].p[j]);
+        if (q == groups - 1) {
+          out[j] = v;
+        } else {
+          p[j] = v;
+        }
+      }
+    }
+  }
+}
+
+// Backward from a checkpoint of h: e4m3 codes through the ring, behind dy and dh,
+// and row-major scale bytes by plain loads a block ahead.  As the bf16 form, but a
+// thread takes R rows at a time where rows are short: what a row costs besides its
+// elements (the wait, the sum over its warps, addresses) is as many instructions as
+// two chunks.
+template <int V, int R>
+constexpr int norm_ck_threads() { return R > 1 ? 256 : V == 4 ? 512 : 640; }
+template <int V, int R>
+constexpr int norm_ck_ctas() { return R > 1 ? 2 : 1; }
+
+template <int V, int R, bool W32>
+__global__ void __launch_bounds__(norm_ck_threads<V, R>(), norm_ck_ctas<V, R>()) k_norm_bwd_ckpt(NormBwdArgs a, int wpr, int stages) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float red[2][NORM_RED * R];
+  __shared__ uint64_t full[NORM_BWD_STAGES];
+  __shared__ int abort_s, fills[NORM_BWD_STAGES];   // fills: thread 0's count per slot
+  volatile int* abort_flag = &abort_s;
+  const int tpr = wpr * 32, groups = blockDim.x / tpr, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
+  const int nch = a.H / 8, ns = a.H / 32, block = groups * R;
+  const uint32_t row_bytes = (uint32_t)a.H * 2, ten_bytes = row_bytes * block;
+  const uint32_t slot_bytes = ten_bytes / 2 * (a.dh ? 5 : 3), at_h = a.dh ? 2 * ten_bytes : ten_bytes;
+  const int blocks = (int)((a.T + block - 1) / block);
+  // thread 0: block nblk, the next to load, goes to slot nslot
+  int nblk = blockIdx.x, nslot = 0;
+  auto issue = [&]() {
+    uint8_t* dst = ring + nslot * slot_bytes;
+    const int64_t r0 = (int64_t)nblk * block, at = r0 * a.H;
+    const uint32_t bytes = row_bytes * (uint32_t)(a.T - r0 < block ? a.T - r0 : block);
+    if (!a.stall || nblk > 0) {
+      ++fills[nslot];
+      mbar_expect_tx(&full[nslot], bytes / 2 * (a.dh ? 5 : 3));
+      bulk_load(dst, a.dy + at, bytes, &full[nslot]);
+      if (a.dh) bulk_load(dst + ten_bytes, a.dh + at, bytes, &full[nslot]);
+      bulk_load(dst + at_h, a.hq + at, bytes / 2, &full[nslot]);
+    }
+    nblk += gridDim.x;
+    if (++nslot == stages) nslot = 0;
+  };
+  const float rh = __frcp_rn((float)a.H);
+  if (threadIdx.x == 0) {
+    abort_s = 0;
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      fills[s] = 0;
+    }
+    mbar_fence_init();
+    for (int s = 0; s < stages - 1 && nblk < blocks; ++s) issue();
+  }
+  Vec8 dw[V];
+  // bf16 weights stay in registers where there is room; others come from L1
+  constexpr bool KEEP_W = !W32 && V <= 2;
+  uint4 w4[KEEP_W ? V : 1];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    dw[i] = Vec8{};
+    if constexpr (KEEP_W)
+      w4[i] = t + i * tpr < nch ? reinterpret_cast<const uint4*>(a.w)[t + i * tpr] : make_uint4(0, 0, 0, 0);
+  }
+  // the rows' rstd and scales are loaded one block ahead (rows past T: 0, and nothing stored)
+  int64_t row = (int64_t)blockIdx.x * block + group * R;
+  const int64_t step = (int64_t)gridDim.x * block;
+  float rstd_next[R];
+  uint32_t sc_next[R][V];
+  auto ahead = [&](int64_t r0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool on = r0 + r < a.T;
+      rstd_next[r] = on ? __ldg(a.rstd + r0 + r) : 0.0f;
+      const uint8_t* s = a.hs + (r0 + r) * ns + (t >> 2);
+#pragma unroll
+      for (int i = 0; i < V; ++i) sc_next[r][i] = on && t + i * tpr < nch ? (uint32_t)__ldg(s + i * (tpr >> 2)) : 0u;
+    }
+  };
+  ahead(row);
+  __syncthreads();
+  int s = 0, par = 0;
+  uint32_t phase = 0;
+  for (int b = blockIdx.x; b < blocks; b += gridDim.x, row += step) {
+    // of a row's chunk: 2^e and 2^e rstd
+    float rstd[R], xs[R][V];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      rstd[r] = rstd_next[r];
+#pragma unroll
+      for (int i = 0; i < V; ++i) xs[r][i] = mx_power(sc_next[r][i]);
+    }
+    ahead(row + step);
+    if (!mbar_wait(&full[s], phase, abort_flag)) {
+      set_status(a.status, FP8MOE_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    const uint8_t* src = ring + s * slot_bytes + group * R * row_bytes;
+    const uint8_t* src_h = ring + s * slot_bytes + at_h + group * R * (row_bytes / 2);
+    Vec8 g[R][V], xh[R][V];
+    uint64_t dot2[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      dot2[r] = 0;
+      const uint64_t rstd2 = pk(rstd[r], rstd[r]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int ch = t + i * tpr;
+        if (ch >= nch || row + r >= a.T) continue;
+        const uint4 dq = *reinterpret_cast<const uint4*>(src + r * row_bytes + ch * 16);
+        const Vec8 d = unpack8(dq);
+        mx_unpack8(*reinterpret_cast<const uint2*>(src_h + r * (row_bytes / 2) + ch * 8), xs[r][i], xh[r][i].p);
+        if constexpr (!KEEP_W) {
+          const Vec8 wf = load_w8<W32>(a.w, ch);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) g[r][i].p[j] = mul2(d.p[j], wf.p[j]);
+        } else {
+          g[r][i] = {{mulx(dq.x, w4[i].x), mulx(dq.y, w4[i].y), mulx(dq.z, w4[i].z), mulx(dq.w, w4[i].w)}};
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          xh[r][i].p[j] = mul2(xh[r][i].p[j], rstd2);
+          dot2[r] = fma2(g[r][i].p[j], xh[r][i].p[j], dot2[r]);
+          dw[i].p[j] = fma2(d.p[j], xh[r][i].p[j], dw[i].p[j]);
+        }
+      }
+    }
+    float dot[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) dot[r] = sum_of(dot2[r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) dot[r] += __shfl_xor_sync(0xffffffffu, dot[r], o);
+    // the two halves of `red` alternate: a block's sums are read before the
+    // barrier of the next one, which writes the other half
+    if (wpr > 1 && (threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int r = 0; r < R; ++r) red[par][(threadIdx.x >> 5) * R + r] = dot[r];
+    __syncthreads();
+    // past this barrier every thread has read the block before
+    if (threadIdx.x == 0 && nblk < blocks && !*abort_flag) {
+      fence_proxy_async_smem();
+      issue();
+    }
+    if (wpr > 1) {
+      const float* p = red[par] + group * wpr * R;
+#pragma unroll
+      for (int r = 0; r < R; ++r) dot[r] = p[r];
+      for (int i = 1; i < wpr; ++i)
+#pragma unroll
+        for (int r = 0; r < R; ++r) dot[r] += p[i * R + r];
+    }
+    par ^= 1;
+    uint16_t* pdx = a.dx + row * a.H;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      // -dot / H, rounded once: the quotient by the reciprocal and one step of
+      // Markstein's correction, which an infinite sum has no use for
+      const float m = dot[r] * rh, rest = fmaf(-m, (float)a.H, dot[r]);
+      const float c = rest == rest ? -fmaf(rest, rh, m) : -m;
+      const uint64_t c2 = pk(c, c), rstd2 = pk(rstd[r], rstd[r]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int ch = t + i * tpr;
+        if (ch >= nch || row + r >= a.T) continue;
+        const Vec8 sv = a.dh ? unpack8(*reinterpret_cast<const uint4*>(src + ten_bytes + r * row_bytes + ch * 16)) : Vec8{};
+        Vec8 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o.p[j] = fma2(rstd2, fma2(xh[r][i].p[j], c2, g[r][i].p[j]), sv.p[j]);
+        *reinterpret_cast<uint4*>(pdx + r * a.H + ch * 8) = pack8(o);
+      }
+    }
     if (++s == stages) {
       s = 0;
       phase ^= 1;
@@ -616,7 +787,21 @@ __global__ void __launch_bounds__(1024) k_norm_dw(const float* part, int P, int 
   if (lane == 0 && blockIdx.x * 32 + warp < H) dw[blockIdx.x * 32 + warp] = v;
 }
 
-template <bool W32, bool CK>
+cudaError_t launch_dw(const NormBwdArgs& a, int P, float* dw, cudaStream_t st) {
+  // launched ahead of the first kernel's end, for which it waits
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.H + 31) / 32));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_norm_dw, (const float*)a.part, P, a.H, dw);
+}
+
+template <bool W32>
 cudaError_t launch_bwd_t(NormBwdArgs a, float* dw, int num_sms, int max_smem, cudaStream_t st) {
   const int nch = a.H / 8;
   // One chunk a thread while rows are short and there is more to read for it than
@@ -630,7 +815,7 @@ cudaError_t launch_bwd_t(NormBwdArgs a, float* dw, int num_sms, int max_smem, cu
   // The ring: as deep as lets two CTAs share an SM, at least three blocks if
   // they fit one (16384 x 5120: 108 us with three, 132 with two)
   const int64_t budget = max_smem - 2048;
-  const int64_t slot = (int64_t)a.H * ((a.dh ? 6 : 4) - (CK ? 1 : 0)) * groups;
+  const int64_t slot = (int64_t)a.H * 2 * (a.dh ? 3 : 2) * groups;
   int stages = (int)(budget / 2 / slot < NORM_BWD_STAGES ? budget / 2 / slot : NORM_BWD_STAGES);
   if (stages < 3) stages = slot * 3 <= budget ? 3 : 2;
   const bool ring = nch <= NORM_MAX_CHUNKS && slot * stages <= budget;
@@ -650,22 +835,47 @@ cudaError_t launch_bwd_t(NormBwdArgs a, float* dw, int num_sms, int max_smem, cu
     kern<<<(unsigned)P, wpr * 32 * groups, smem, st>>>(a, wpr, stages);
     return cudaGetLastError();
   };
-  cudaError_t e = !ring    ? run(k_norm_bwd_long<W32, CK>)
-                  : v == 1 ? run(k_norm_bwd<1, W32, CK>)
-                  : v == 2 ? run(k_norm_bwd<2, W32, CK>)
-                           : run(k_norm_bwd<4, W32, CK>);
+  cudaError_t e = !ring    ? run(k_norm_bwd_long<W32, false>)
+                  : v == 1 ? run(k_norm_bwd<1, W32>)
+                  : v == 2 ? run(k_norm_bwd<2, W32>)
+                           : run(k_norm_bwd<4, W32>);
   if (e != cudaSuccess) return e;
-  // launched ahead of the first kernel's end, for which it waits
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.H + 31) / 32));
-  cfg.blockDim = dim3(1024);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_norm_dw, (const float*)a.part, (int)P, a.H, dw);
+  return launch_dw(a, (int)P, dw, st);
+}
+
+template <bool W32>
+cudaError_t launch_bwd_ckpt(NormBwdArgs a, float* dw, int num_sms, int max_smem, cudaStream_t st) {
+  const int nch = a.H / 8;
+  // chunks and rows of a thread at a time
+  const int v = nch <= 256 ? 1 : nch <= 1024 ? 2 : 4, rows = nch <= 256 ? 4 : nch <= 512 ? 2 : 1;
+  int wpr = nch > NORM_MAX_CHUNKS ? 16 : (nch + 32 * v - 1) / (32 * v);
+  int groups = wpr >= 8 ? 1 : 8 / wpr;
+  // the ring as the bf16 form's
+  const int64_t budget = max_smem - 2048;
+  const int64_t slot = (int64_t)a.H * (a.dh ? 5 : 3) * groups * rows;
+  int stages = (int)(budget / 2 / slot < NORM_BWD_STAGES ? budget / 2 / slot : NORM_BWD_STAGES);
+  if (stages < (rows > 1 ? 2 : 3)) stages = slot * 3 <= budget ? 3 : 2;
+  const bool ring = nch <= NORM_MAX_CHUNKS && slot * stages <= budget;
+  if (!ring) wpr = 16, groups = 1;
+  const int64_t blocks = ring ? (a.T + groups * rows - 1) / (groups * rows) : a.T;
+  int64_t P = NORM_BWD_PARTS < blocks ? NORM_BWD_PARTS : blocks;
+  if (ring) a.stall = take_ring_stall_hook();
+  auto run = [&](auto kern) {
+    const int smem = ring ? (int)(slot * stages) : 0;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ring ? (int)budget : 0);
+    int per = 0;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, wpr * 32 * groups, smem);
+    if (e != cudaSuccess || per < 1) return e == cudaSuccess ? cudaErrorInvalidConfiguration : e;
+    if (P > (int64_t)num_sms * per) P = (int64_t)num_sms * per;
+    kern<<<(unsigned)P, wpr * 32 * groups, smem, st>>>(a, wpr, stages);
+    return cudaGetLastError();
+  };
+  const cudaError_t e = !ring      ? run(k_norm_bwd_long<W32, true>)
+                        : v == 1    ? run(k_norm_bwd_ckpt<1, 4, W32>)
+                        : rows == 2 ? run(k_norm_bwd_ckpt<2, 2, W32>)
+                        : v == 2    ? run(k_norm_bwd_ckpt<2, 1, W32>)
+                                    : run(k_norm_bwd_ckpt<4, 1, W32>);
+  return e != cudaSuccess ? e : launch_dw(a, (int)P, dw, st);
 }
 
 }  // namespace
@@ -703,8 +913,8 @@ cudaError_t launch_norm_bwd(const void* dy, const void* h, const uint8_t* hs, co
   NormBwdArgs a{};
   a.dy = (const uint16_t*)dy, a.h = (const uint16_t*)h, a.hq = (const uint8_t*)h, a.hs = hs, a.dh = (const uint16_t*)dh, a.rstd = rstd, a.w = w;
   a.T = T, a.H = (int)H, a.dx = (uint16_t*)dx, a.part = (float*)workspace, a.status = status;
-  if (hs) return w32 ? launch_bwd_t<true, true>(a, dw, num_sms, max_smem, st) : launch_bwd_t<false, true>(a, dw, num_sms, max_smem, st);
-  return w32 ? launch_bwd_t<true, false>(a, dw, num_sms, max_smem, st) : launch_bwd_t<false, false>(a, dw, num_sms, max_smem, st);
+  if (hs) return w32 ? launch_bwd_ckpt<true>(a, dw, num_sms, max_smem, st) : launch_bwd_ckpt<false>(a, dw, num_sms, max_smem, st);
+  return w32 ? launch_bwd_t<true>(a, dw, num_sms, max_smem, st) : launch_bwd_t<false>(a, dw, num_sms, max_smem, st);
 }
 
 }  // namespace fp8moe

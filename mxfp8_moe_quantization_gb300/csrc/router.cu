@@ -734,42 +734,47 @@ __global__ void __launch_bounds__(256, 4) k_route_weight_grad(const uint16_t* __
 }
 
 // The same with y in MXFP8 (row-major scales): a lane's chunk is 16 codes, half a
-// block, whose products are summed before the block's power of two.
+// block, whose products are summed before the block's power of two.  For a missing
+// row the loop reads row 0 and the result is dropped: choosing in the loop cost a
+// fifth of its instructions, which are what bounds it (4096 x 7168 x 8: 86 a chunk).
 template <int L, int UK>
 __global__ void __launch_bounds__(256, 3) k_route_weight_grad_ckpt(const uint16_t* __restrict__ dout,
                                                                    const uint8_t* __restrict__ yq,
                                                                    const uint8_t* __restrict__ ys,
                                                                    const int32_t* __restrict__ row_of, uint32_t rows,
-                                                                   int64_t T, int64_t N, int k, float* __restrict__ dw) {
+                                                                   int64_t T, uint32_t N, int k, float* __restrict__ dw) {
   constexpr int WPT = L / 32;
   __shared__ float red[8][UK];
   const int warp = threadIdx.x >> 5, l = threadIdx.x % L;
   const int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-  const int64_t nv = N / 16, ns = N / 32;
+  const uint32_t nv = rows > 0 ? N / 16 : 0, ns = N / 32;
   for (int j0 = 0; j0 < k; j0 += UK) {
-    int row[UK];
+    uint32_t row[UK];
+    bool there[UK];
     float acc[UK];
 #pragma unroll
     for (int j = 0; j < UK; ++j) {
-      row[j] = t < T && j0 + j < k ? row_of[t * k + j0 + j] : -1;
-      if ((uint32_t)row[j] >= rows) row[j] = -1;
+      row[j] = t < T && j0 + j < k ? (uint32_t)row_of[t * k + j0 + j] : 0xFFFFFFFFu;
+      there[j] = row[j] < rows;
+      row[j] = there[j] ? row[j] : 0u;
       acc[j] = 0.0f;
     }
     if (t < T) {
-      for (int64_t v = l; v < nv; v += L) {
-        const uint4 d0 = ld_nc16(dout + t * N + v * 16), d1 = ld_nc16(dout + t * N + v * 16 + 8);
+      for (uint32_t v = l; v < nv; v += L) {
+        const uint16_t* dv = dout + t * N + v * 16;
+        const uint4 d0 = ld_nc16(dv), d1 = ld_nc16(dv + 8);
+        const uint8_t *qv = yq + v * 16, *sv = ys + (v >> 1);
         uint4 q[UK];
         uint32_t b[UK];
 #pragma unroll
         for (int j = 0; j < UK; ++j) {
-          q[j] = row[j] < 0 ? make_uint4(0, 0, 0, 0) : ld_nc16(yq + row[j] * N + v * 16);
-          b[j] = row[j] < 0 ? 0u : (uint32_t)__ldg(ys + row[j] * ns + (v >> 1));
+          q[j] = ld_nc16(qv + (uint64_t)row[j] * N);
+          b[j] = (uint32_t)__ldg(sv + (uint64_t)row[j] * ns);
         }
         const uint64_t d[8] = {unpk_bf16(d0.x), unpk_bf16(d0.y), unpk_bf16(d0.z), unpk_bf16(d0.w),
                                unpk_bf16(d1.x), unpk_bf16(d1.y), unpk_bf16(d1.z), unpk_bf16(d1.w)};
 #pragma unroll
         for (int j = 0; j < UK; ++j) {
-          if (row[j] < 0) continue;
           const uint32_t qq[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
           uint64_t s = 0;
 #pragma unroll
@@ -793,7 +798,7 @@ __global__ void __launch_bounds__(256, 3) k_route_weight_grad_ckpt(const uint16_
         float v = acc[j];
         if (WPT > 1)
           for (int i = 1; i < WPT; ++i) v += red[warp + i][j];
-        if (j0 + j < k) dw[t * k + j0 + j] = v;
+        if (j0 + j < k) dw[t * k + j0 + j] = there[j] ? v : 0.0f;
       }
     }
     if (WPT > 1) __syncthreads();
@@ -925,14 +930,15 @@ cudaError_t launch_route_weight_grad_ckpt(const void* dout, const void* yq, cons
                                           cudaStream_t st) {
   // lanes per token by the rule of the bf16 form, of chunks twice as long
   const int64_t nv = N / 16;
-  int L = nv <= 48 ? 16 : nv < 128 || (k == 1 && nv < 512) ? 32 : nv < 512 ? 128 : 256;
+  int L = nv <= 8 ? 8 : nv <= 48 ? 16 : nv < 256 || (k == 1 && nv < 512) ? 32 : nv < 512 ? 128 : 256;
   while (L < 256 && L < nv && T * L < (int64_t)256 * num_sms) L = L == 32 ? 128 : 2 * L;
   const unsigned grid = (unsigned)((T + 256 / L - 1) / (256 / L));
   auto run = [&](auto kern) {
-    kern<<<grid, 256, 0, st>>>((const uint16_t*)dout, (const uint8_t*)yq, ys, row_of, (uint32_t)rows, T, N, (int)k, dw);
+    kern<<<grid, 256, 0, st>>>((const uint16_t*)dout, (const uint8_t*)yq, ys, row_of, (uint32_t)rows, T, (uint32_t)N, (int)k, dw);
   };
 #define FP8MOE_WG(UK)                                          \
-  if (L == 16) run(k_route_weight_grad_ckpt<16, UK>);          \
+  if (L == 8) run(k_route_weight_grad_ckpt<8, UK>);            \
+  else if (L == 16) run(k_route_weight_grad_ckpt<16, UK>);     \
   else if (L == 32) run(k_route_weight_grad_ckpt<32, UK>);     \
   else if (L == 128) run(k_route_weight_grad_ckpt<128, UK>);   \
   else run(k_route_weight_grad_ckpt<256, UK>)

@@ -21,14 +21,13 @@
 // copy's rate); 51136 x 1408 backward 120 us = 6.1 TB/s (91%).  The first form,
 // with every lane deriving every scale, expf and a division, and 45
 // instructions per element instead of about 20, took 152 and 283 us.
-#include <type_traits>
-
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "launch.h"
 #include "moe_ops.h"
 #include "mxcvt.cuh"
 #include "scales.cuh"
+#include "swiglu.cuh"
 #include "tma.cuh"
 
 namespace fp8moe {
@@ -40,135 +39,12 @@ namespace {
 constexpr int SG_ROWS = 32, SG_COLS = 64, SG_RW = 2, SG_CW = 2, SG_WARPS = SG_RW * SG_CW;
 constexpr int CW = 8;   // columns per lane
 
-// sigmoid of a pair g: 1 / D with D = 1 + 2^-t (1 - r), t = g / ln 2 rounded and
-// r the rest g - t ln 2, whose exponential is 1 + r (Cody and Waite's two-part
-// ln 2; |r| < 2^-17).  The reciprocal is that of D / 4, which is normal for
-// every finite D, with one step of Newton's iteration.  Where e^-g is not finite
-// (g below -88.72) the step's 0 * inf, and for g far up to the other side the
-// infinite t, leave NaN.  Mean relative error over all bf16 |g| in (2^-10, 80)
-// 3.36e-8; 1 / (1 + expf(-g)) with every step rounded 3.2e-8.
-FP8MOE_DEV uint64_t sigmoid2(uint64_t g2) {
-  constexpr float L = 1.44269504f, LN2_HI = 0.693147182f, LN2_LO = -1.90465421e-9f;
-  const uint64_t t2 = mul2(g2, pk(L, L));
-  const uint64_t r2 = fma2(t2, pk(-LN2_LO, -LN2_LO), fma2(t2, pk(-LN2_HI, -LN2_HI), g2));
-  float t, u, x, y;
-  unpk(t2, t, u);
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(-t));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-u));
-  const uint64_t d2 = fma2(pk(x, y), fma2(r2, pk(0.25f, 0.25f), pk(-0.25f, -0.25f)), pk(-0.25f, -0.25f));   // -D / 4
-  unpk(d2, t, u);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(-t));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-u));
-  const uint64_t q2 = pk(x, y), s2 = mul2(q2, pk(0.25f, 0.25f));
-  return fma2(s2, fma2(d2, q2, pk(1.0f, 1.0f)), s2);
-}
-
-// A pair of results: v, and backward the gradient of gate in v, of up in v2.
-// Where sigmoid2 has no number, or a product of two inputs is beyond fp32, the
-// result is not finite, by which far_tiles knows it.
-template <bool BWD>
-FP8MOE_DEV void act_pair(uint32_t g, uint32_t u, uint32_t d, uint64_t& v, uint64_t& v2) {
-  const uint64_t g2 = unpk_bf16(g), s2 = sigmoid2(g2);
-  if constexpr (BWD) {
-    // 1 + g (1 - sig)
-    const uint64_t f2 = fma2(g2, fma2(s2, pk(-1.0f, -1.0f), pk(1.0f, 1.0f)), pk(1.0f, 1.0f));
-    v = mul2(mul2(mulx(d, u), s2), f2);
-    v2 = mul2(mulx(d, g), s2);
-  } else {
-    v = mul2(mulx(g, u), s2);
-  }
-}
-
-// The same for any inputs, from the sigmoid on in 64 bits.  Below -80 the
-// sigmoid is (e^(g/4))^4, whose factors are normal as long as a result can
-// differ from 0, and 0 where 64 bits have no number for it either.
-FP8MOE_DEV double far_sigmoid(float g) {
-  if (g < -745.0f) return 0.0;
-  if (!(g < -80.0f)) return (double)__frcp_rn(1.0f + expf(-g));
-  const double e = (double)expf(0.25f * fmaxf(g, -300.0f)), e2 = e * e;
-  return e2 * e2;
-}
-template <bool BWD>
-FP8MOE_DEV float far_one(float gate, float u, float d, float& du) {
-  const double s = far_sigmoid(gate), g = gate;
-  if constexpr (!BWD) return (float)(g * s * (double)u);
-  du = (float)((double)d * g * s);
-  return (float)((double)d * (double)u * s * (1.0 + g * (1.0 - s)));
-}
-FP8MOE_DEV bool finite2(uint64_t p) {
-  float a, b;
-  unpk(p, a, b);
-  return amax3(0.0f, a, b) <= 3.402823466e38f;
-}
-template <bool BWD>
-FP8MOE_DEV void far_pair(uint32_t g, uint32_t u, uint32_t d, uint64_t& v, uint64_t& v2) {
-  act_pair<BWD>(g, u, d, v, v2);
-  if (finite2(v) && (!BWD || finite2(v2))) return;
-  float x = 0.0f, y = 0.0f;
-  const float lo = far_one<BWD>(bf16_lo(g), bf16_lo(u), bf16_lo(d), x);
-  const float hi = far_one<BWD>(bf16_hi(g), bf16_hi(u), bf16_hi(d), y);
-  v = pk(lo, hi);
-  if constexpr (BWD) v2 = pk(x, y);
-}
-
-// The padded row (in a layout whose groups start at multiples of 128 rows) of
-// row `row0`, a multiple of 32; -1 if the offsets are invalid.  A warp calls
-// it; each of its lanes takes every 32nd group, U of them with their loads in
-// flight together.
-template <int U>
-FP8MOE_DEV uint32_t rows_before(const int32_t* __restrict__ offs, int E, int m, int r, int e0, bool& bad) {
-  int end[U], start[U];
-  uint32_t sum = 0;
-#pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const int e = e0 + 32 * i;
-    end[i] = e < E ? __ldg(offs + e) : 0;
-    start[i] = e < E && e > 0 ? __ldg(offs + e - 1) : 0;
-  }
-#pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const int e = e0 + 32 * i;
-    if (e >= E) break;
-    bad |= start[i] < 0 || end[i] < start[i] || end[i] > m || (end[i] & 31) || (e == E - 1 && end[i] != m);
-    if (end[i] <= r) {
-      sum += ((uint32_t)(end[i] - start[i]) + 127u) & ~127u;
-    } else if (start[i] <= r) {
-      sum += (uint32_t)(r - start[i]);
-    }
-  }
-  return sum;
-}
-FP8MOE_DEV int64_t padded_row(const int32_t* __restrict__ offs, int E, int64_t M, int64_t row0, int lane) {
-  const int m = (int)M, r = (int)row0;   // both at most 2^30
-  uint32_t sum = 0;
-  bool bad = false;
-  if (E <= 32) {
-    sum = rows_before<1>(offs, E, m, r, lane, bad);
-  } else {
-    for (int e0 = lane; e0 < E; e0 += 256) sum += rows_before<8>(offs, E, m, r, e0, bad);
-  }
-  if (__any_sync(0xffffffffu, bad)) return -1;
-  return (int64_t)__reduce_add_sync(0xffffffffu, sum);
-}
-
-// One step of a maximum over lanes that differ in `mask`: the lower lane goes
-// on with the first half of m, the upper one with the second.
-template <int N>
-FP8MOE_DEV void halve(const float (&m)[N], float (&out)[N / 2], int lane, int mask) {
-  const bool up = lane & mask;
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) {
-    const float other = __shfl_xor_sync(0xffffffffu, up ? m[i] : m[i + N / 2], mask);
-    out[i] = nanmax(up ? m[i + N / 2] : m[i], other);
-  }
-}
-
 // Where a warp's 32 rows go.  Scale bytes: row 8 rq + i, block c of s0 is at
 // s0 + i * step0 + off0(c); column c of s1 at s1 + off1(c).
 struct TilePlace {
   int row0;       // first row of the tile
   int W;          // columns of the result
-  uint8_t *s0, *s1, *as1;
+  uint8_t *s0, *s1;
   int64_t step0;  // row-major: W / 32; tiled: 16
   int64_t band1;  // tiled s1: bytes of 128 of its rows; row-major: 0
 };
@@ -180,58 +56,7 @@ FP8MOE_DEV void place_scales(const SwigluArgs& a, TilePlace& tp, int64_t prow0, 
   tp.step0 = t0 ? 16 : tp.W / 32;
   tp.s0 = a.s0 + (t0 ? tile_off(prow0, 0, cp0) : (int64_t)tp.row0 * (tp.W / 32)) + rq * 8 * tp.step0;
   tp.band1 = t1 ? cp1 * 128 : 0;
-  const int64_t at1 = t1 ? (pcol1 >> 2) * 512 + (pcol1 & 3) : tp.row0 / 32;
-  tp.s1 = a.s1 + at1;
-  tp.as1 = a.as1 + at1;
-}
-
-// The transposed codes and scales of a tile (M % 32 == 0: every row exists).  q1: of
-// row 8 rq, s1: of the tile's block of rows, both of column 0.
-FP8MOE_DEV void put_columns(const SwigluArgs& a, int64_t band1, uint8_t* q1, uint8_t* s1, int64_t col, bool ok, int lane,
-                            const uint64_t (&v)[8][CW / 2], uint32_t& top) {
-  float m[CW];
-#pragma unroll
-  for (int p = 0; p < CW / 2; ++p) {
-    m[2 * p] = m[2 * p + 1] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      float x, y, z, w;
-      unpk(v[i][p], x, y);
-      unpk(v[i + 1][p], z, w);
-      m[2 * p] = amax3(m[2 * p], x, z);
-      m[2 * p + 1] = amax3(m[2 * p + 1], y, w);
-    }
-  }
-  // a column block is the four lanes that differ in rq; a lane ends with
-  // columns own and own + 1
-  float mh[4], mk[2], mul[2];
-  halve<8>(m, mh, lane, 8);
-  halve<4>(mh, mk, lane, 16);
-  const int own = ((lane >> 3) & 1) * 4 + ((lane >> 4) & 1) * 2;
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const uint32_t b = mx_byte(mk[s], mul[s]);
-    const int64_t c = col + own + s;
-    top = max(top, b);
-    if (ok)
-      s1[band1 ? (c >> 7) * band1 + (c & 31) * 16 + ((c >> 5) & 3) * 4 : c * (a.M / 32)] = (uint8_t)b;
-  }
-  uint8_t* q = q1 + col * a.M;
-#pragma unroll
-  for (int p = 0; p < CW / 2; ++p) {
-    // columns 2 p and 2 p + 1 are the two of one lane
-    const int src = (lane & 7) | (p >> 1) << 3 | (p & 1) << 4;
-    const float sc0 = __shfl_sync(0xffffffffu, mul[0], src), sc1 = __shfl_sync(0xffffffffu, mul[1], src);
-    const uint64_t s2 = pk(sc0, sc1);
-    float x[8], y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) unpk(mul2(v[i][p], s2), x[i], y[i]);
-    if (ok) {
-      *reinterpret_cast<uint2*>(q + (2 * p) * a.M) = make_uint2(cvt4(x[0], x[1], x[2], x[3]), cvt4(x[4], x[5], x[6], x[7]));
-      *reinterpret_cast<uint2*>(q + (2 * p + 1) * a.M) =
-          make_uint2(cvt4(y[0], y[1], y[2], y[3]), cvt4(y[4], y[5], y[6], y[7]));
-    }
-  }
+  tp.s1 = a.s1 + (t1 ? (pcol1 >> 2) * 512 + (pcol1 & 3) : tp.row0 / 32);
 }
 
 // One tile of results to every output.  v: rows 8 rq .. 8 rq + 7 and columns
@@ -297,13 +122,51 @@ FP8MOE_DEV void put_tile(const SwigluArgs& a, const TilePlace& tp, int64_t col0,
         *reinterpret_cast<uint2*>(q + i * W) = make_uint2(cvt4(f[0], f[1], f[2], f[3]), cvt4(f[4], f[5], f[6], f[7]));
     }
   }
-  if (a.q1) put_columns(a, tp.band1, a.q1 + rbase, tp.s1, col, ok, lane, v, top);
-}
-
-// The activation along its columns, of a tile of the checkpointed backward.
-FP8MOE_DEV void put_act(const SwigluArgs& a, const TilePlace& tp, int64_t col0, bool ok, int lane,
-                        const uint64_t (&v)[8][CW / 2], uint32_t& top) {
-  put_columns(a, tp.band1, a.aq1 + tp.row0 + (lane >> 3) * 8, tp.as1, col0 + (lane & 7) * CW, ok, lane, v, top);
+  if (a.q1) {   // M % 32 == 0: every row exists
+    float m[CW];
+#pragma unroll
+    for (int p = 0; p < CW / 2; ++p) {
+      m[2 * p] = m[2 * p + 1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        float x, y, z, w;
+        unpk(v[i][p], x, y);
+        unpk(v[i + 1][p], z, w);
+        m[2 * p] = amax3(m[2 * p], x, z);
+        m[2 * p + 1] = amax3(m[2 * p + 1], y, w);
+      }
+    }
+    // a column block is the four lanes that differ in rq; a lane ends with
+    // columns own and own + 1
+    float mh[4], mk[2], mul[2];
+    halve<8>(m, mh, lane, 8);
+    halve<4>(mh, mk, lane, 16);
+    const int own = ((lane >> 3) & 1) * 4 + ((lane >> 4) & 1) * 2;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t b = mx_byte(mk[s], mul[s]);
+      const int64_t c = col + own + s;
+      top = max(top, b);
+      if (ok)
+        tp.s1[tp.band1 ? (c >> 7) * tp.band1 + (c & 31) * 16 + ((c >> 5) & 3) * 4 : c * (a.M / 32)] = (uint8_t)b;
+    }
+    uint8_t* q = a.q1 + col * a.M + rbase;
+#pragma unroll
+    for (int p = 0; p < CW / 2; ++p) {
+      // columns 2 p and 2 p + 1 are the two of one lane
+      const int src = (lane & 7) | (p >> 1) << 3 | (p & 1) << 4;
+      const float sc0 = __shfl_sync(0xffffffffu, mul[0], src), sc1 = __shfl_sync(0xffffffffu, mul[1], src);
+      const uint64_t s2 = pk(sc0, sc1);
+      float x[8], y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) unpk(mul2(v[i][p], s2), x[i], y[i]);
+      if (ok) {
+        *reinterpret_cast<uint2*>(q + (2 * p) * a.M) = make_uint2(cvt4(x[0], x[1], x[2], x[3]), cvt4(x[4], x[5], x[6], x[7]));
+        *reinterpret_cast<uint2*>(q + (2 * p + 1) * a.M) =
+            make_uint2(cvt4(y[0], y[1], y[2], y[3]), cvt4(y[4], y[5], y[6], y[7]));
+      }
+    }
+  }
 }
 
 // One row's chunks of gate and up (column col of both) into the checkpoint: the
@@ -330,17 +193,12 @@ FP8MOE_DEV void put_ckpt(const SwigluArgs& a, int64_t row, int64_t col, bool on,
 }
 
 // Shared memory of a warp with PF: one 32 x 64 box each of gate, up and, backward,
-// dout, rows of 128 bytes (gate and up of a checkpoint: 64).  The checkpointed
-// backward, which goes over a tile twice, has two sets.
+// dout, rows of 128 bytes.
 constexpr int BOX_BYTES = SG_ROWS * SG_COLS * 2;
-template <bool BWD, bool CK>
-constexpr int h_box() { return BWD && CK ? BOX_BYTES / 2 : BOX_BYTES; }
-template <bool BWD, bool CK>
-constexpr int set_bytes() { return 2 * h_box<BWD, CK>() + (BWD ? BOX_BYTES : 0); }
-template <bool BWD, bool CK>
-constexpr int sets() { return BWD && CK ? 2 : 1; }
-template <bool BWD, bool CK>
-constexpr int cta_bytes() { return SG_WARPS * sets<BWD, CK>() * (set_bytes<BWD, CK>() + 8); }   // + a barrier per set
+template <bool BWD>
+constexpr int warp_bytes() { return (BWD ? 3 : 2) * BOX_BYTES; }
+template <bool BWD>
+constexpr int cta_bytes() { return SG_WARPS * (warp_bytes<BWD>() + 8); }   // + a barrier per warp
 
 // A warp's `n` tiles from `row`, `col` on once more, if one of them has a result
 // that is not finite (gates below -88.72, NaN, infinities, products beyond
@@ -349,7 +207,7 @@ constexpr int cta_bytes() { return SG_WARPS * sets<BWD, CK>() * (set_bytes<BWD, 
 // flag of its own beside the scale bytes, 51136 x 1408 backward took 131 to 152
 // us without any such tile.  With such gates in 1 column of 2048, 36448 rows
 // take 127 us forward instead of 76, 248 instead of 128 backward.
-template <bool BWD, bool CK>
+template <bool BWD>
 FP8MOE_DEV void far_tiles(const SwigluArgs& a, TilePlace tp, int64_t row, int64_t col, int n, int col_end, int64_t cp0,
                           int64_t cp1) {
   const int lane = threadIdx.x & 31, rq = lane >> 3, cq = lane & 7;
@@ -363,43 +221,23 @@ FP8MOE_DEV void far_tiles(const SwigluArgs& a, TilePlace tp, int64_t row, int64_
       const bool ok = c < a.F;
       uint64_t v[8][CW / 2], v2[BWD ? 8 : 1][CW / 2];
       uint32_t top = 0;
-      // (back: the gradients; else the activation)
-      auto values = [&](auto back) {
-        constexpr bool B = decltype(back)::value;
-        // one pair at a time: 32 copies of far_pair do not stay in the instruction cache
+      // one pair at a time: 32 copies of far_pair do not stay in the instruction cache
 #pragma unroll 1
-        for (int k = 0; k < 8 * (CW / 2); ++k) {
-          const int64_t r = row + rq * 8 + k / (CW / 2), at = c + k % (CW / 2) * 2;
-          const bool on = ok && r < a.M;
-          auto pair = [&](const uint16_t* p) { return on ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u; };
-          auto h_pair = [&](int64_t i) {   // columns i and i + 1 of h
-            if constexpr (BWD && CK) {
-              if (!on) return 0u;
-              const float s = mx_power(__ldg(a.hs + r * (a.F / 16) + i / 32));
-              return pack_bf16x2(mul2(e4m3x2_f32(__ldg(reinterpret_cast<const uint16_t*>(a.hq + r * 2 * a.F + i))), pk(s, s)));
-            } else {
-              return pair(a.h + r * a.ldh + i);
-            }
-          };
-          uint64_t x, y;
-          far_pair<B>(h_pair(at), h_pair(a.F + at), B ? pair(a.dout + r * a.F + at) : 0u, x, y);
+      for (int k = 0; k < 8 * (CW / 2); ++k) {
+        const int64_t r = row + rq * 8 + k / (CW / 2), at = c + k % (CW / 2) * 2;
+        const bool on = ok && r < a.M;
+        auto pair = [&](const uint16_t* p) { return on ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u; };
+        uint64_t x, y;
+        far_pair<BWD>(pair(a.h + r * a.ldh + at), pair(a.h + r * a.ldh + a.F + at), BWD ? pair(a.dout + r * a.F + at) : 0u, x, y);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int p = 0; p < CW / 2; ++p) {
-              if (k != i * (CW / 2) + p) continue;
-              v[i][p] = x;
-              if constexpr (B) v2[i][p] = y;
-            }
-        }
-      };
-      if constexpr (BWD && CK) {
-        if (a.aq1) {
-          values(std::false_type{});
-          put_act(a, tp, col, ok, lane, v, top);
-        }
+          for (int p = 0; p < CW / 2; ++p) {
+            if (k != i * (CW / 2) + p) continue;
+            v[i][p] = x;
+            if constexpr (BWD) v2[i][p] = y;
+          }
       }
-      values(std::integral_constant<bool, BWD>{});
       put_tile(a, tp, col, ok, lane, v, top);
       if constexpr (BWD) put_tile(a, tp, a.F + col, ok, lane, v2, top);
     }
@@ -416,14 +254,14 @@ FP8MOE_DEV void far_tiles(const SwigluArgs& a, TilePlace tp, int64_t row, int64_
 // its warps has the next tile's boxes loaded by TMA while it works on the
 // current one from registers.  Without PF every CTA has one tile (few tiles:
 // nothing to overlap), loaded straight into registers.
+// CK (forward): h goes to its MXFP8 checkpoint on the way.
 template <bool BWD, bool PF, bool CK>
 FP8MOE_DEV void swiglu_body(const CUtensorMap* th, const CUtensorMap* td, const SwigluArgs& a, int64_t cp0, int64_t cp1,
                             int col_tiles, int tiles, int per) {
   extern __shared__ __align__(128) uint8_t dsm[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rq = lane >> 3, cq = lane & 7;
-  constexpr int SETS = sets<BWD, CK>(), SET = set_bytes<BWD, CK>(), HBOX = h_box<BWD, CK>();
-  uint8_t* wbuf = dsm + warp * SETS * SET;
-  uint64_t* wbar = reinterpret_cast<uint64_t*>(dsm + SG_WARPS * SETS * SET) + warp * SETS;
+  uint8_t* wbuf = dsm + warp * warp_bytes<BWD>();
+  uint64_t* wbar = reinterpret_cast<uint64_t*>(dsm + SG_WARPS * warp_bytes<BWD>()) + warp;
   // the CTA's run of tiles, and a tile's place stepped along it
   const int t0 = blockIdx.x * per, t1 = tiles - t0 < per ? tiles : t0 + per;
   struct Place {
@@ -444,80 +282,49 @@ FP8MOE_DEV void swiglu_body(const CUtensorMap* th, const CUtensorMap* td, const 
     return p;
   };
   // the tile's boxes (one lane); a warp whose rows lie past M loads nothing
-  auto issue = [&](const Place& p, int set) {
+  auto issue = [&](const Place& p) {
     const int64_t r = p.row;
     const int c = p.col;
     if (r >= a.M || c >= a.F || (a.stall && blockIdx.x == 0 && warp == 0)) return;
-    uint64_t* bar = wbar + set;
-    uint8_t* buf = wbuf + set * SET;
-    mbar_expect_tx(bar, SET);
-    tma_load_2d(buf, th, bar, c, (int)r);
-    tma_load_2d(buf + HBOX, th, bar, (int)a.F + c, (int)r);
-    if (BWD) tma_load_2d(buf + 2 * HBOX, td, bar, c, (int)r);
-  };
-  // a checkpoint's scales of a tile: lane i's row i, gate's two blocks, then up's
-  auto load_scales = [&](const Place& p) {
-    if (p.row + lane >= a.M || p.col >= a.F) return 0u;
-    const uint8_t* s = a.hs + (int64_t)(p.row + lane) * (a.F / 16) + (p.col >> 5);
-    const uint32_t lo = __ldg(s) | (uint32_t)__ldg(s + (a.F >> 5)) << 16;
-    return p.col + 32 < a.F ? lo | (uint32_t)__ldg(s + 1) << 8 | (uint32_t)__ldg(s + (a.F >> 5) + 1) << 24 : lo;
+    mbar_expect_tx(wbar, warp_bytes<BWD>());
+    tma_load_2d(wbuf, th, wbar, c, (int)r);
+    tma_load_2d(wbuf + BOX_BYTES, th, wbar, (int)a.F + c, (int)r);
+    if (BWD) tma_load_2d(wbuf + 2 * BOX_BYTES, td, wbar, c, (int)r);
   };
   Place cur = first(t0);
   if (PF) {
     if (lane == 0) {
-      for (int i = 0; i < SETS; ++i) mbar_init(wbar + i, 1);
+      mbar_init(wbar, 1);
       mbar_fence_init();
-      issue(cur, 0);
+      issue(cur);
     }
     __syncwarp();
   }
-  uint32_t sc_next = 0;
-  if constexpr (BWD && CK) sc_next = load_scales(cur);
   TilePlace tp;
   tp.W = (int)(BWD ? 2 * a.F : a.F);
   tp.row0 = -1;
-  uint32_t parity = 0, top = 0;   // parity: bit i of set i
-  int set = 0;
+  uint32_t parity = 0, top = 0;
   for (int t = t0; t < t1; ++t) {
     const int row0 = cur.row;
     if (row0 >= a.M) break;   // column tiles are fastest: the later tiles' rows are not lower
     const int64_t col0 = cur.col, col = col0 + cq * CW;
     cur = next(cur);
-    const uint32_t sc = sc_next;
-    if constexpr (BWD && CK) {
-      if (t + 1 < t1) sc_next = load_scales(cur);
-    }
     if (col0 >= a.F) {   // this warp's half of the last column tile is empty
-      if (PF && lane == 0 && t + 1 < t1) issue(cur, set);
+      if (PF && lane == 0 && t + 1 < t1) issue(cur);
       continue;
-    }
-    if (PF && SETS == 2) {
-      __syncwarp();   // the other set is read
-      if (lane == 0 && t + 1 < t1) {
-        fence_proxy_async_smem();
-        issue(cur, set ^ 1);
-      }
     }
     const bool ok = col < a.F;
     const bool moved = row0 != tp.row0;
     tp.row0 = row0;
-    constexpr bool HQ = BWD && CK;   // h comes as codes
-    uint4 g[PF || HQ ? 1 : 8], u[PF || HQ ? 1 : 8], d[PF || !BWD ? 1 : 8];
-    uint2 gc[!PF && HQ ? 8 : 1], uc[!PF && HQ ? 8 : 1];
+    uint4 g[PF ? 1 : 8], u[PF ? 1 : 8], d[PF || !BWD ? 1 : 8];
     if constexpr (!PF) {
       const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int64_t r = (int64_t)row0 + rq * 8 + i;
         const bool on = ok && r < a.M;
-        if constexpr (HQ) {
-          const uint8_t* q = a.hq + r * 2 * a.F + col;
-          gc[i] = on ? __ldg(reinterpret_cast<const uint2*>(q)) : make_uint2(0, 0);
-          uc[i] = on ? __ldg(reinterpret_cast<const uint2*>(q + a.F)) : make_uint2(0, 0);
-        } else {
-          g[i] = on ? ld_nc16(a.h + r * a.ldh + col) : z;
-          u[i] = on ? ld_nc16(a.h + r * a.ldh + a.F + col) : z;
-        }
+        g[i] = on ? ld_nc16(a.h + r * a.ldh + col) : z;
+        u[i] = on ? ld_nc16(a.h + r * a.ldh + a.F + col) : z;
         if constexpr (BWD) d[i] = on ? ld_nc16(a.dout + r * a.F + col) : z;
       }
     }
@@ -535,77 +342,43 @@ FP8MOE_DEV void swiglu_body(const CUtensorMap* th, const CUtensorMap* td, const 
     }
     if (PF) {
       // (also before leaving on bad offsets: no load stays in flight)
-      if (!mbar_wait(wbar + set, parity >> set & 1u, nullptr)) {
+      if (!mbar_wait(wbar, parity, nullptr)) {
         set_status(a.status, FP8MOE_ERR_TIMEOUT);
-        (void)mbar_wait(wbar + set, parity >> set & 1u, nullptr);   // the late copies, again with a limit
+        (void)mbar_wait(wbar, parity, nullptr);   // the late copies, again with a limit
         fail = true;
       }
-      parity ^= 1u << set;
-      if (SETS == 2 && fail && lane == 0 && t + 1 < t1 && cur.row < a.M && cur.col < a.F &&
-          !(a.stall && blockIdx.x == 0 && warp == 0))
-        (void)mbar_wait(wbar + (set ^ 1), parity >> (set ^ 1) & 1u, nullptr);   // and the next tile's
+      parity ^= 1;
     }
     if (fail) break;
     uint64_t v[8][CW / 2], v2[BWD ? 8 : 1][CW / 2];
-    const uint8_t* lp = wbuf + set * SET + rq * 8 * 128 + cq * 16;
-    if constexpr (HQ) {
-      // the values of the codes, as bf16 words; then, where it is asked for, the
-      // activation, and behind it the gradients: not all at once in registers
-      uint32_t gw[8][CW / 2], uw[8][CW / 2];
-      const uint8_t* cp = wbuf + set * SET + rq * 8 * 64 + cq * 8;
+    const uint8_t* lp = wbuf + rq * 8 * 128 + cq * 16;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t w = __shfl_sync(0xffffffffu, sc, rq * 8 + i) >> (8 * (cq >> 2));
-        const uint4 gq = mx_unpack8_bf16(PF ? *reinterpret_cast<const uint2*>(cp + i * 64) : gc[PF ? 0 : i], mx_power(w & 255u));
-        const uint4 uq =
-            mx_unpack8_bf16(PF ? *reinterpret_cast<const uint2*>(cp + HBOX + i * 64) : uc[PF ? 0 : i], mx_power(w >> 16 & 255u));
-        gw[i][0] = gq.x, gw[i][1] = gq.y, gw[i][2] = gq.z, gw[i][3] = gq.w;
-        uw[i][0] = uq.x, uw[i][1] = uq.y, uw[i][2] = uq.z, uw[i][3] = uq.w;
-      }
-      if (a.aq1) {
+    for (int i = 0; i < 8; ++i) {
+      const uint4 gq = PF ? *reinterpret_cast<const uint4*>(lp + i * 128) : g[PF ? 0 : i];
+      const uint4 uq = PF ? *reinterpret_cast<const uint4*>(lp + BOX_BYTES + i * 128) : u[PF ? 0 : i];
+      uint4 dq = make_uint4(0, 0, 0, 0);
+      if constexpr (BWD) dq = PF ? *reinterpret_cast<const uint4*>(lp + 2 * BOX_BYTES + i * 128) : d[PF ? 0 : i];
+      const uint32_t gw[4] = {gq.x, gq.y, gq.z, gq.w}, uw[4] = {uq.x, uq.y, uq.z, uq.w};
+      const uint32_t dw[4] = {dq.x, dq.y, dq.z, dq.w};
+      if constexpr (CK) put_ckpt(a, (int64_t)row0 + rq * 8 + i, col, ok && row0 + rq * 8 + i < a.M, lane, gq, uq);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int p = 0; p < CW / 2; ++p) act_pair<false>(gw[i][p], uw[i][p], 0u, v[i][p], v2[i][p]);
-        put_act(a, tp, col0, ok, lane, v, top);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 dq = PF ? *reinterpret_cast<const uint4*>(lp + 2 * HBOX + i * 128) : d[PF ? 0 : i];
-        const uint32_t dw[4] = {dq.x, dq.y, dq.z, dq.w};
-#pragma unroll
-        for (int p = 0; p < CW / 2; ++p) act_pair<true>(gw[i][p], uw[i][p], dw[p], v[i][p], v2[i][p]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 gq = PF ? *reinterpret_cast<const uint4*>(lp + i * 128) : g[PF ? 0 : i];
-        const uint4 uq = PF ? *reinterpret_cast<const uint4*>(lp + HBOX + i * 128) : u[PF ? 0 : i];
-        uint4 dq = make_uint4(0, 0, 0, 0);
-        if constexpr (BWD) dq = PF ? *reinterpret_cast<const uint4*>(lp + 2 * HBOX + i * 128) : d[PF ? 0 : i];
-        const uint32_t gw[4] = {gq.x, gq.y, gq.z, gq.w}, uw[4] = {uq.x, uq.y, uq.z, uq.w};
-        const uint32_t dw[4] = {dq.x, dq.y, dq.z, dq.w};
-        if constexpr (CK) put_ckpt(a, (int64_t)row0 + rq * 8 + i, col, ok && row0 + rq * 8 + i < a.M, lane, gq, uq);
-#pragma unroll
-        for (int p = 0; p < CW / 2; ++p) {
-          act_pair<BWD>(gw[p], uw[p], dw[p], v[i][p], v2[BWD ? i : 0][p]);
-        }
+      for (int p = 0; p < CW / 2; ++p) {
+        act_pair<BWD>(gw[p], uw[p], dw[p], v[i][p], v2[BWD ? i : 0][p]);
       }
     }
-    if (PF && SETS == 1) {
+    if (PF) {
       __syncwarp();   // the boxes are read
       if (lane == 0 && t + 1 < t1) {
         fence_proxy_async_smem();
-        issue(cur, 0);
+        issue(cur);
       }
     }
-    set = SETS == 2 ? set ^ 1 : 0;
     put_tile(a, tp, col0, ok, lane, v, top);
     if constexpr (BWD) put_tile(a, tp, a.F + col0, ok, lane, v2, top);
   }
   if (__any_sync(0xffffffffu, top == MX_NOT_FINITE)) {
     const Place p = first(t0);
-    far_tiles<BWD, CK>(a, tp, p.row, p.col, t1 - t0, col_end, cp0, cp1);
+    far_tiles<BWD>(a, tp, p.row, p.col, t1 - t0, col_end, cp0, cp1);
   }
 }
 
@@ -658,16 +431,14 @@ cudaError_t launch_dir(SwigluArgs a, cudaStream_t st) {
     return cudaGetLastError();
   }
   CUtensorMap th{}, td{};
-  cudaError_t e = cudaFuncSetAttribute(k_swiglu_run<BWD, CK>, cudaFuncAttributeMaxDynamicSharedMemorySize, cta_bytes<BWD, CK>());
+  cudaError_t e = cudaFuncSetAttribute(k_swiglu_run<BWD, CK>, cudaFuncAttributeMaxDynamicSharedMemorySize, cta_bytes<BWD>());
   if (e != cudaSuccess) return e;
   static std::atomic<int> occ{0};
-  const int64_t per_sm = blocks_per_sm(occ, k_swiglu_run<BWD, CK>, SG_WARPS * 32, cta_bytes<BWD, CK>(), 1);
+  const int64_t per_sm = blocks_per_sm(occ, k_swiglu_run<BWD, CK>, SG_WARPS * 32, cta_bytes<BWD>(), 1);
   a.stall = take_ring_stall_hook();
   cuuint64_t dims[2] = {(cuuint64_t)(2 * a.F), (cuuint64_t)a.M}, strides[1] = {(cuuint64_t)(a.ldh * 2)};
   const cuuint32_t box[2] = {SG_COLS, SG_ROWS};
-  if (BWD && CK) strides[0] = (cuuint64_t)(2 * a.F);
-  if (!make_tmap(&th, BWD && CK ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                 BWD && CK ? (const void*)a.hq : a.h, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+  if (!make_tmap(&th, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.h, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   if (BWD) {
     dims[0] = (cuuint64_t)a.F;
@@ -676,7 +447,7 @@ cudaError_t launch_dir(SwigluArgs a, cudaStream_t st) {
       return cudaErrorInvalidValue;
   }
   const int64_t per = tiles_per_cta(tiles, a.num_sms, per_sm);
-  k_swiglu_run<BWD, CK><<<(unsigned)((tiles + per - 1) / per), SG_WARPS * 32, cta_bytes<BWD, CK>(), st>>>(
+  k_swiglu_run<BWD, CK><<<(unsigned)((tiles + per - 1) / per), SG_WARPS * 32, cta_bytes<BWD>(), st>>>(
       th, td, a, cp0, cp1, (int)col_tiles, (int)tiles, (int)per);
   return cudaGetLastError();
 }
@@ -684,7 +455,8 @@ cudaError_t launch_dir(SwigluArgs a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_swiglu(const SwigluArgs& a, cudaStream_t st) {
-  if (a.dout) return a.hq ? launch_dir<true, true>(a, st) : launch_dir<true, false>(a, st);
+  if (a.hq) return launch_swiglu_bwd_ckpt(a, st);
+  if (a.dout) return launch_dir<true, false>(a, st);
   return a.ckpt_q ? launch_dir<false, true>(a, st) : launch_dir<false, false>(a, st);
 }
 

@@ -203,19 +203,17 @@ def test_no_rows(F):
     assert z.shape == (0, 3)
 
 
-@pytest.mark.parametrize("what", ["fwd", "bwd", "norm", "decode"])
+@pytest.mark.parametrize("what", ["fwd", "norm", "decode"])
 def test_wait_timeout_sets_status(F, what):
     """A tile that never arrives: the bounded waits run out, the status says so,
     and the next call in the same context is exact."""
     M, Fd = 8192, 512
     h = _bf16((M, 2 * Fd), 1).to(DEV)
     hq, hs = F.fp8moe_mxfp8_quantize_dim0(h)
-    dout = _bf16((M, Fd), 2).to(DEV)
     rstd, w = torch.ones(M, device=DEV), torch.ones(2 * Fd, device=DEV)
     wq, ws = hq[:2 * Fd].view(1, 2 * Fd, 2 * Fd), torch.full((4 * Fd * Fd // 32,), 120, dtype=torch.uint8, device=DEV)
     idx, one = torch.zeros(3, 1, dtype=torch.int32, device=DEV), torch.ones(3, 1, device=DEV)
     call = {"fwd": lambda: F.fp8moe_swiglu_fwd_ckpt(h, dim0=True, dim1=True),
-            "bwd": lambda: F.fp8moe_swiglu_bwd_ckpt(dout, hq, hs, dim0=True, dim1=True, act1=True),
             "norm": lambda: F.fp8moe_add_rmsnorm_bwd_ckpt(h, hq, hs, rstd, w),
             "decode": lambda: (F.fp8moe_mxfp8_moe_decode(h[:3], idx, one, wq, ws, hq[:2 * Fd, :Fd].contiguous().view(1, 2 * Fd, Fd),
                                                          ws),)}[what]
