@@ -21,8 +21,10 @@
 // in order after a grid-wide meeting.  The terms of x and of the activation are
 // made once, into the workspace, as the tensor core reads them, and copied to a
 // ring beside the weights'; through registers, as bulk copies queue behind the
-// weights' in flight.  The weights' producer takes no part in the meetings: while
-// the others add, it fills its ring with W2.
+// weights' in flight.  One or two tokens (DIRECT): every CTA makes the terms of its
+// own run on the way to the ring, from x and from the first product's partial
+// sums, which saves two of the four meetings.  The weights' producer takes no part
+// in the meetings: while the others add, it fills its ring with W2.
 //   warps 0-3  accumulators to partial sums;  4  weights by TMA;  5  MMA issue;
 //   6  scales to tensor memory;  7-14  terms to shared memory;  all but 4-6  terms
 //   and the final sums.
@@ -294,7 +296,7 @@ FP8MOE_DEV void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(
 // run at a time, and each leaves its counters one grid further.  (A CTA that gives
 // up still comes.)
 enum { MEET_X = 0, MEET_SUMS, MEET_ACT, MEET_END, DC_MEETS };
-__device__ unsigned long long g_meets[DC_MEETS][16];
+__device__ unsigned long long g_meets[2][DC_MEETS][16];   // two forms of the kernel, with as many meetings each call
 FP8MOE_DEV uint64_t ld_acquire_gpu(const unsigned long long* p) {
   uint64_t v;
   asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
@@ -378,6 +380,7 @@ struct Terms {
   }
 };
 
+template <bool DIRECT>
 __global__ void __launch_bounds__(DC_THREADS, 1)
     k_decode(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2, DecodeArgs a, DecodeSmem L) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
                                    : make_uint4(0, 0, 0, 0);
   };
   uint4 x0 = make_uint4(0, 0, 0, 0);               // the first unit's, on its way while the plan is made
-  if (warp < DC_WARP_TMA || warp >= DC_WARP_B) x0 = x_at(unit0);
+  if (!DIRECT && (warp < DC_WARP_TMA || warp >= DC_WARP_B)) x0 = x_at(unit0);
   if (a.P <= 32) {
     if (warp == DC_WARP_TMA) plan_warp(a, pl, lane);
     __syncthreads();
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     // ======================= weights =======================
     // The first fills leave behind this CTA's terms of x: in front of them, what
     // follows them meets its first instructions and loads in a full memory system.
-    bar_sync(1, DC_JOIN + 32);
+    if constexpr (!DIRECT) bar_sync(1, DC_JOIN + 32);
     if (lane == 0) {
       Slot slot, late;
       uint32_t i = 0;
@@ -589,14 +592,14 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     // every meeting's count when all have come: the last one's stands still until
     // this CTA has been at the others
     uint64_t meets;
-    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(meets) : "l"(g_meets[MEET_END]));
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(meets) : "l"(g_meets[DIRECT][MEET_END]));
     meets += grid;
     // (`meanwhile`: what the next step can work out without the others' results)
     auto meeting = [&](int i, auto meanwhile) {
       bar_sync(2, DC_JOIN);
-      if (tid == 0) come(g_meets[i]);
+      if (tid == 0) come(g_meets[DIRECT][i]);
       meanwhile();
-      if (tid == 0) came(g_meets[i], meets, a.status, abort_flag);
+      if (tid == 0) came(g_meets[DIRECT][i], meets, a.status, abort_flag);
       bar_sync(2, DC_JOIN);
     };
 
@@ -680,6 +683,91 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       }
       // c is past the run's end: into the next run
     };
+    // The same, made here: a warp a tile, half a warp a pair (entries of at most two),
+    // the next piece's values on their way meanwhile.
+    auto make = [&](auto nt) {
+      constexpr int NT = decltype(nt)::value;
+      const Stream& s = NT == 2 ? s1 : s2;
+      const int K = NT == 2 ? K1 : K2, half = lane >> 4;
+      struct Values {
+        uint32_t ent;
+        bool in;
+        uint4 x;            // of x; or the first two partial sums of gate and up
+        float4 q[NT == 2 ? 1 : 4], u[NT == 2 ? 1 : 4];
+        Parts g, y;
+      } next;
+      auto fetch = [&]() {
+        next.ent = pl.ent[r.ent];
+        const int place = (int)(next.ent >> 10 & 1023u) + half, k = ((r.k + c) * DC_G + rank) * 128 + j16 * 8;
+        next.in = half < (int)(next.ent >> 20) && k < K;
+        if constexpr (NT == 2) {
+          next.x = make_uint4(0, 0, 0, 0);
+          if (next.in)
+            next.x = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)L.k.quot(pl.order[place]) * a.ldx + k));
+        } else {
+          const int64_t step = (int64_t)nlive * R1 / 4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) next.q[i] = next.u[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (next.in) {
+            next.g = parts_of(s1, a.part1, R1, place, k), next.y = parts_of(s1, a.part1, R1, place, a.F + k);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) next.q[i] = __ldcg(next.g.p + i), next.q[2 + i] = __ldcg(next.y.p + i);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (next.g.n > 1) next.u[i] = __ldcg(next.g.p + step + i);
+              if (next.y.n > 1) next.u[2 + i] = __ldcg(next.y.p + step + i);
+            }
+          }
+        }
+      };
+      if (team < L.teams && r.left > 0) fetch();
+      while (team < L.teams && r.left > 0) {
+        const Values now = next;
+        c += L.teams;
+        enter(s);
+        if (r.left > 0) fetch();
+        float v[8];
+        if constexpr (NT == 2) {
+          const uint32_t w[4] = {now.x.x, now.x.y, now.x.z, now.x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
+        } else {
+          float4 z[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            z[i] = make_float4(now.q[i].x + now.u[i].x, now.q[i].y + now.u[i].y, now.q[i].z + now.u[i].z, now.q[i].w + now.u[i].w);
+          if (now.in) {
+            const int64_t step = (int64_t)nlive * R1 / 4;
+            auto more = [&](const Parts& p, float4& z0, float4& z1) {
+              for (int i = 2; i < p.n; ++i) {
+                const float4 e = __ldcg(p.p + i * step), f = __ldcg(p.p + i * step + 1);
+                z0.x += e.x, z0.y += e.y, z0.z += e.z, z0.w += e.w;
+                z1.x += f.x, z1.y += f.y, z1.z += f.z, z1.w += f.w;
+              }
+            };
+            more(now.g, z[0], z[1]);
+            more(now.y, z[2], z[3]);
+          }
+          const float gs[8] = {z[0].x, z[0].y, z[0].z, z[0].w, z[1].x, z[1].y, z[1].z, z[1].w};
+          const float us[8] = {z[2].x, z[2].y, z[2].z, z[2].w, z[3].x, z[3].y, z[3].z, z[3].w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = gs[i] / (1.0f + expf(-gs[i])) * us[i];
+        }
+        __syncwarp();
+        const Terms<NT> terms(v);
+        if (!__all_sync(0xffffffffu, mbar_wait(&b_empty[slot.i], slot.turn ^ 1u, abort_flag))) {
+          fail();
+          break;
+        }
+        const TermTiles tt((int)(now.ent >> 20) * NT);
+        uint8_t* dst = smem + L.b + slot.i * L.b_bytes;
+        if (now.in) terms.put(dst + rank * tt.rows * 128, dst + DC_G * tt.rows * 128 + rank * tt.sf, half * NT, j16);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_full[slot.i]);
+        slot.step(L.teams, L.sb);
+      }
+    };
     // ======================= accumulators to partial sums =======================
     Slot acc;
     auto drain_acc = [&](auto nt) {
@@ -731,17 +819,21 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
                 (place - (int)(ent >> 10 & 1023u)) * NT, j16);
     };
     const int back = (jt >> 4 & 1) * (int)grid;     // a warp stays together for its shuffles
-    for (int u = unit0, units = a.P * kt1; u - back < units; u += unit_step) {
-      const uint4 q = u == unit0 ? x0 : x_at(u);
-      float v[8] = {bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y), bf16_lo(q.z), bf16_hi(q.z), bf16_lo(q.w), bf16_hi(q.w)};
-      const Terms<2> terms(v);
-      const int p = (int)L.kt[0].quot(u), c = u - p * kt1, place = u < units ? pl.pos[p] : DC_DEAD;
-      if (place != DC_DEAD && c * 128 + j16 * 8 < K1) put(terms, place, c, s1.kp.d);
+    if constexpr (!DIRECT) {
+      for (int u = unit0, units = a.P * kt1; u - back < units; u += unit_step) {
+        const uint4 q = u == unit0 ? x0 : x_at(u);
+        float v[8] = {bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y), bf16_lo(q.z), bf16_hi(q.z), bf16_lo(q.w), bf16_hi(q.w)};
+        const Terms<2> terms(v);
+        const int p = (int)L.kt[0].quot(u), c = u - p * kt1, place = u < units ? pl.pos[p] : DC_DEAD;
+        if (place != DC_DEAD && c * 128 + j16 * 8 < K1) put(terms, place, c, s1.kp.d);
+      }
+      asm volatile("bar.arrive 1, %0;" ::"n"(DC_JOIN + 32) : "memory");
+      meeting(MEET_X, [] {});
     }
-    asm volatile("bar.arrive 1, %0;" ::"n"(DC_JOIN + 32) : "memory");
-    meeting(MEET_X, [] {});
     if (epi) {
       drain_acc(Two{});
+    } else if constexpr (DIRECT) {
+      make(Two{});
     } else {
       feed(Two{});
     }
@@ -761,27 +853,34 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       n.y = n.in ? parts_of(s1, a.part1, R1, n.place, a.F + f) : Parts{nullptr, 0};
       return n;
     };
-    meeting(MEET_SUMS, [&] { next = act_of(unit0); });
-    for (int u = unit0; u - back < units; u += unit_step) {
-      const Parts src[4] = {next.g, {next.g.p + 1, next.g.n}, next.y, {next.y.p + 1, next.y.n}};
-      float4 q[4];
-      gather(R1, src, q);
-      const float gs[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
-      const float us[8] = {q[2].x, q[2].y, q[2].z, q[2].w, q[3].x, q[3].y, q[3].z, q[3].w};
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = gs[i] / (1.0f + expf(-gs[i])) * us[i];
-      const Terms<3> terms(v);
-      if (next.in) put(terms, next.place, next.c, s2.kp.d);
-      if (u + unit_step - back < units) next = act_of(u + unit_step);
-    }
-    meeting(MEET_ACT, [&] {
+    auto second_run = [&] {
       if (epi) return;
       r = Run(s2, cta);
       enter(s2);
-    });
+    };
+    if constexpr (DIRECT) {
+      meeting(MEET_SUMS, second_run);
+    } else {
+      meeting(MEET_SUMS, [&] { next = act_of(unit0); });
+      for (int u = unit0; u - back < units; u += unit_step) {
+        const Parts src[4] = {next.g, {next.g.p + 1, next.g.n}, next.y, {next.y.p + 1, next.y.n}};
+        float4 q[4];
+        gather(R1, src, q);
+        const float gs[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+        const float us[8] = {q[2].x, q[2].y, q[2].z, q[2].w, q[3].x, q[3].y, q[3].z, q[3].w};
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = gs[i] / (1.0f + expf(-gs[i])) * us[i];
+        const Terms<3> terms(v);
+        if (next.in) put(terms, next.place, next.c, s2.kp.d);
+        if (u + unit_step - back < units) next = act_of(u + unit_step);
+      }
+      meeting(MEET_ACT, second_run);
+    }
     if (epi) {
       drain_acc(Three{});
+    } else if constexpr (DIRECT) {
+      make(Three{});
     } else {
       feed(Three{});
     }
@@ -934,10 +1033,17 @@ cudaError_t launch_decode(DecodeArgs a, void* workspace, int num_sms, int max_sm
     const cuuint32_t box[3] = {128, 128, 1};
     if (!make_tmap(&tm[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, q[i], 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(k_decode, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem - 1024);
+  // Terms made on the way (entries of two pairs at most, two warps a slot, a tile
+  // each) where a CTA has few pieces and the meetings count: 6 experts of 1408 x 2048
+  // 22.2 us against 25.0, 8 of 2048 x 7168 (70 pieces a CTA) 73.1 and 73.5, 16 of
+  // them (140) 129.7 against 126.2, as the copies keep up with the weights better.
+  const int64_t pieces = a.P * (pieces_of(a.H) * L.rt[0].d + pieces_of(a.F) * L.rt[1].d);
+  const bool direct = a.nb == 2 && 1 << L.team_log == DC_G && pieces <= (int64_t)96 * num_sms;
+  const void* kern = direct ? (const void*)k_decode<true> : (const void*)k_decode<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem - 1024);
   if (e != cudaSuccess) return e;
   void* args[] = {&tm[0], &tm[1], &a, &L};
-  return cudaLaunchCooperativeKernel((const void*)k_decode, dim3((unsigned)num_sms), dim3(DC_THREADS), args, L.total + 1024, st);
+  return cudaLaunchCooperativeKernel(kern, dim3((unsigned)num_sms), dim3(DC_THREADS), args, L.total + 1024, st);
 }
 
 }  // namespace fp8moe
