@@ -612,7 +612,8 @@ fp8moe_status fp8moe_swiglu_bwd(const void* dout, const void* h, int64_t ldh, in
  *   [T, H/32] in place of h; H % 32 == 0; the same workspace.
  * fp8moe_route_weight_grad_ckpt: fp8moe_route_weight_grad_bounded with the expert
  *   outputs yq [rows, N] and ys [rows, N/32] in place of y; N % 32 == 0.
- * Codes 16-byte aligned.
+ * Codes 16-byte aligned; an output overlaps no input, but for the norm's dx as in
+ * fp8moe_add_rmsnorm_bwd.
  * ------------------------------------------------------------------------ */
 fp8moe_status fp8moe_swiglu_fwd_ckpt(const void* h, int64_t ldh, int64_t M, int64_t F, const int32_t* offs, int64_t E,
                                      void* out, void* q0, uint8_t* s0, int s0_layout, void* q1, uint8_t* s1,
@@ -647,13 +648,16 @@ fp8moe_status fp8moe_route_weight_grad_ckpt(const void* dout, const void* yq, co
  * Sums in fp32, in an order that hangs on the routing of the whole batch; x
  * counts with all its digits and the activation to 2^-12 of itself: the output
  * is rounded once.  The same call gives the
- * same bits.  A value of x that is not finite makes its token's row NaN, a NaN
- * weight those of the tokens that chose its expert; no other row.
+ * same bits.  A value of x or of the activation that is not finite makes its
+ * token's row NaN, a NaN weight those of the tokens that chose its expert; no
+ * other row.
  * workspace: caller-owned, fp8moe_mxfp8_moe_decode_workspace_bytes bytes (-1 for
  * sizes that are refused), 16-byte aligned, of no use after the call.
  * T * k <= FP8MOE_DECODE_MAX_PAIRS (more: the grouped products), 1 <= E <=
- * FP8MOE_MAX_GROUPS, H and F multiples of 32 up to 2^20.  An expert with more
- * than 64 choices is read once per 64.  One cooperative launch of a CTA per SM:
+ * FP8MOE_MAX_GROUPS, H and F multiples of 32 up to 2^20, less where the weights
+ * come to some 10^7 pieces of 32 KB.  A reading of an expert serves T of its
+ * choices up to 16 tokens, beyond that 16, 32 or 64 as T * k / E grows; an expert
+ * with more is read again.  One cooperative launch of a CTA per SM (at most 160):
  * it starts once every SM can take one.  A wait inside it that exceeds its limit
  * sets FP8MOE_ERR_TIMEOUT in the device status.
  * ------------------------------------------------------------------------ */

@@ -43,12 +43,12 @@ struct Rows {
   uint32_t step0;
   bool tiled0;
   uint8_t *q1, *s1, *aq1, *as1;  // columns'; s1 and as1: of the tile's block of rows
-  uint32_t band1;              // bytes of 128 columns' scales, 0: row-major
+  uint32_t band1;              // 128 columns' scales, in units of 128 bytes, 0: row-major
 };
 
 // Bytes from s1 to the scale of lane-column j (below 32) of a tile at column `col`.
 FP8MOE_DEV uint64_t column_scale(const Rows& r, uint32_t col, uint32_t j) {
-  return r.band1 ? wide(r.band1, col >> 7) + (col >> 5 & 3u) * 4 + j * 16 : wide(r.M / 32, col + j);
+  return r.band1 ? wide(r.band1, col >> 7) * 128 + (col >> 5 & 3u) * 4 + j * 16 : wide(r.M / 32, col + j);
 }
 
 // Codes and scales along the rows: v's columns are those from `col` of 2F.
@@ -237,7 +237,8 @@ __device__ __noinline__ void far_tile(const Rows& r, uint32_t col) {
 template <bool ACT>
 __global__ void __launch_bounds__(SC_WARPS * 32, SC_CTAS) k_swiglu_bwd_ckpt(SwigluArgs a, uint32_t cp0, uint32_t cp1, int col_tiles, int per) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rq = lane >> 3, cq = lane & 7;
-  const int row0 = ((int)blockIdx.y * 2 + (warp & 1)) * 32, c0 = blockIdx.x * per;
+  // row tiles beyond the grid's 65535 are its z
+  const int row0 = (int)((blockIdx.z * gridDim.y + blockIdx.y) * 2 + (warp & 1)) * 32, c0 = blockIdx.x * per;
   if (row0 >= a.M) return;
   int prow = row0;
   if (a.E0 + a.E1 > 0) {
@@ -260,8 +261,9 @@ __global__ void __launch_bounds__(SC_WARPS * 32, SC_CTAS) k_swiglu_bwd_ckpt(Swig
   r.step0 = r.tiled0 ? 16 : F / 16;
   r.s0 = a.s0 + (r.tiled0 ? tile_off(a.E0 > 0 ? prow : row0, 0, cp0) : (int64_t)wide(F / 16, row0)) + rq * 8 * r.step0;
   const bool tiled1 = a.s1_layout != FP8MOE_SCALES_ROWMAJOR;
-  const uint32_t blk1 = (a.E1 > 0 ? prow : row0) / 32, at1 = tiled1 ? (blk1 >> 2) * 512 + (blk1 & 3) : row0 / 32;
-  r.band1 = tiled1 ? cp1 * 128 : 0;
+  const uint32_t blk1 = (a.E1 > 0 ? prow : row0) / 32;
+  const uint64_t at1 = tiled1 ? wide(512, blk1 >> 2) + (blk1 & 3) : row0 / 32;
+  r.band1 = tiled1 ? cp1 : 0;
   const uint64_t col1 = wide(M, cq * 4) + first;
   r.q1 = a.q1 ? a.q1 + col1 : nullptr;
   r.s1 = a.s1 + at1;
@@ -290,9 +292,8 @@ cudaError_t launch_swiglu_bwd_ckpt(const SwigluArgs& a, cudaStream_t st) {
   const int64_t col_tiles = (a.F + 63) / 64, row_tiles = (a.M + 63) / 64;
   // Column tiles of a CTA: two where there are many
   const int64_t per = col_tiles * row_tiles > (int64_t)4 * SC_CTAS * a.num_sms ? 2 : 1;
-  const dim3 grid((unsigned)((col_tiles + per - 1) / per), (unsigned)row_tiles);
-  if (cp1 * 128 > UINT32_MAX) return cudaErrorInvalidValue;
-  if (grid.y > 65535) return cudaErrorInvalidValue;
+  const int64_t ny = row_tiles < 32768 ? row_tiles : 32768;
+  const dim3 grid((unsigned)((col_tiles + per - 1) / per), (unsigned)ny, (unsigned)((row_tiles + ny - 1) / ny));
   if (a.aq1) {
     k_swiglu_bwd_ckpt<true><<<grid, SC_WARPS * 32, 0, st>>>(a, (uint32_t)cp0, (uint32_t)cp1, (int)col_tiles, (int)per);
   } else {
