@@ -875,7 +875,10 @@ def bench_rows(F, iters=30, only=None):
         emit("ops", "k_norm_fwd", f"scout [{T},{H}] residual, bf16 and MXFP8", ms, nbytes=T * H * (9 + 1 / 32))
         ms = timed(lambda: F.fp8moe_add_rmsnorm_bwd(xn, h, rs, wn, rn, dx=y))
         emit("ops", "k_norm_bwd", f"scout [{T},{H}]", ms, nbytes=T * H * 8)
-        del xn, rn, h, y, q, s
+        hq, hs = F.fp8moe_mxfp8_quantize_dim0(h)
+        ms = timed(lambda: F.fp8moe_add_rmsnorm_bwd_ckpt(xn, hq, hs, rs, wn, rn, dx=y))
+        emit("ops", "k_norm_bwd_ckpt", f"scout [{T},{H}]", ms, nbytes=T * H * (7 + 1 / 32))
+        del xn, rn, h, y, q, s, hq, hs
         T, E, k = v3.tokens, v3.E, 8
         lg, bias = torch.randn(T, E, device=dev), 0.05 * torch.randn(E, device=dev)
         fwd = lambda: F.fp8moe_router_fwd(lg, k, score=F.SCORE_SIGMOID, bias=bias)
@@ -887,7 +890,10 @@ def bench_rows(F, iters=30, only=None):
         row_of = torch.randperm(T * k, device=dev).reshape(T, k).to(torch.int32)
         ms = timed(lambda: F.fp8moe_route_weight_grad(do, yr, row_of))
         emit("ops", "k_route_weight_grad", f"dsv3 [{T},{v3.K}] x {k}", ms, nbytes=T * v3.K * 2 * (k + 1))
-        del yr, do
+        yq, ys = F.fp8moe_mxfp8_quantize_dim0(yr)
+        ms = timed(lambda: F.fp8moe_route_weight_grad_ckpt(do, yq, ys, row_of))
+        emit("ops", "k_route_weight_grad_ckpt", f"dsv3 [{T},{v3.K}] x {k}", ms, nbytes=T * v3.K * (2 + k * 33 / 32))
+        del yr, do, yq, ys
         for wl in (v3, ds):
             offs = torch.from_numpy(wl.offs()).to(dev)
             M, Fd = wl.M // 32 * 32, wl.N
@@ -902,7 +908,34 @@ def bench_rows(F, iters=30, only=None):
             kw = dict(zip(("q0", "s0", "q1", "s1"), o[1:]))
             ms = timed(lambda: F.fp8moe_swiglu_bwd(do, hh, offs, *lay, need_dh=False, dim0=True, dim1=True, **kw))
             emit("ops", "k_swiglu<bwd>", f"{wl.name} [{M},{Fd}] both directions", ms, nbytes=M * Fd * (10 + 4 / 32))
-            del hh, do, o, kw
+            o = F.fp8moe_swiglu_fwd_ckpt(hh, offs, *lay, need_out=False, dim0=True)
+            hq, hs = o[5], o[6]
+            kw = dict(q0=o[1], s0=o[2], hq=hq, hs=hs)
+            ms = timed(lambda: F.fp8moe_swiglu_fwd_ckpt(hh, offs, *lay, need_out=False, dim0=True, **kw))
+            emit("ops", "k_swiglu<fwd, checkpoint>", f"{wl.name} [{M},{Fd}] rows", ms, nbytes=M * Fd * (7 + 3 / 32))
+            o = F.fp8moe_swiglu_bwd_ckpt(do, hq, hs, offs, *lay, need_dh=False, dim0=True, dim1=True, act1=True)
+            kw = dict(zip(("q0", "s0", "q1", "s1", "aq1", "as1"), o[1:]))
+            ms = timed(lambda: F.fp8moe_swiglu_bwd_ckpt(do, hq, hs, offs, *lay, need_dh=False, dim0=True, dim1=True, act1=True,
+                                                        **kw))
+            emit("ops", "k_swiglu_bwd_ckpt", f"{wl.name} [{M},{Fd}] both directions and the activation's columns", ms,
+                 nbytes=M * Fd * (9 + 7 / 32))
+            del hh, do, o, kw, hq, hs
+        # the expert layer of a few tokens: every expert met is read once
+        for wl, k, toks in ((ds, 6, (1, 16)), (v3, 8, (1, 16)), (sc, 1, (64,))):
+            E, H, Fd = wl.E, wl.K, wl.N
+            q1, q2 = codes(E, 2 * Fd, H), codes(E, H, Fd)
+            size = F.fp8moe_swizzled_scales_bytes
+            s1, s2 = (torch.full((size(E, r, c // 32, 0, F.NO_GROUPS),), 112, dtype=torch.uint8, device=dev)
+                      for r, c in ((2 * Fd, H), (H, Fd)))
+            for T in toks:
+                xt = rand(T, H)
+                idx = torch.rand(T, E, device=dev).topk(k, dim=1)[1].to(torch.int32)
+                wt, out = torch.full((T, k), 1.0 / k, device=dev), rand(T, H)
+                ws = torch.empty(F.fp8moe_mxfp8_moe_decode_workspace_bytes(T, k, E, H, Fd), dtype=torch.uint8, device=dev)
+                ms = timed(lambda: F.fp8moe_mxfp8_moe_decode(xt, idx, wt, q1, s1, q2, s2, out=out, workspace=ws))
+                emit("ops", "k_decode", f"{wl.name} {T} tokens, {k} of {E} experts of {Fd} x {H}", ms,
+                     nbytes=int(idx.unique().numel()) * 3 * H * Fd * 33 / 32)
+            del q1, q2, s1, s2
 
 
 def dual_case(F, dev):
