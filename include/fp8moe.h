@@ -656,7 +656,7 @@ fp8moe_status fp8moe_route_weight_grad_ckpt(const void* dout, const void* yq, co
  * T * k <= FP8MOE_DECODE_MAX_PAIRS (more: the grouped products), 1 <= E <=
  * FP8MOE_MAX_GROUPS, H and F multiples of 32 up to 2^20, less where the weights
  * come to some 10^7 pieces of 32 KB.  A reading of an expert serves T of its
- * choices up to 16 tokens, beyond that 16, 32 or 64 as T * k / E grows; an expert
+ * choices up to 24 tokens, beyond that 24, 32 or 64 as T * k / E grows; an expert
  * with more is read again.  One cooperative launch of a CTA per SM (at most 160):
  * it starts once every SM can take one.  A wait inside it that exceeds its limit
  * sets FP8MOE_ERR_TIMEOUT in the device status.

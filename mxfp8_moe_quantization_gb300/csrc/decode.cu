@@ -938,11 +938,14 @@ int64_t most_parts(int64_t ents, int64_t rt, int64_t kt) {
   return p < kt ? p : kt;
 }
 // Pairs of an entry, that is, of one reading of an expert: its terms have to fit a
-// ring slot, and larger slots leave room for fewer.  T where a token's choices
-// differ and T is small, else room for more than most experts get.
+// ring slot, and larger slots leave room for fewer: up to 24 pairs four, up to 32
+// three.  T, which is enough where a token's choices differ, as long as there is
+// room for four; beyond that room for more than most experts get.  (23 tokens, 8 of
+// 256 experts of 2048 x 7168, the busiest chosen by all: entries of 16 took 816 us,
+// of 23 791.)
 int entry_pairs(int64_t T, int64_t k, int64_t E) {
   const int64_t each = T * k / E;   // pairs an expert gets on average
-  return T < 2 ? 2 : T <= 16 ? (int)T : each <= 10 ? 16 : each <= 24 ? 32 : 64;
+  return T < 2 ? 2 : T <= 24 ? (int)T : each <= 14 ? 24 : each <= 24 ? 32 : 64;
 }
 
 // floats of the partial sums [parts][live pairs][R]: the most over any number of live pairs
@@ -961,7 +964,9 @@ DecodeSmem layout(int P, int nb, int max_ent, int max_smem) {
   DecodeSmem L{};
   // (up to 8 rows that no term fills are read behind a tile, up to 512 bytes behind its scales)
   L.b_bytes = (TermTiles(3 * nb).bytes() + 1023) / 1024 * 1024;
+  // (columns of N; and the drain reads eight pairs' at a time)
   L.acc = 3 * ((nb + 7) / 8 * 8);
+  if (L.acc < up16(TermTiles(3 * nb).rows)) L.acc = up16(TermTiles(3 * nb).rows);
   const int plan = 16 + max_ent * 4 + P * 10;
   const int bars = 8 * (5 * DC_MAX_SLOTS + 8);
   const int fixed = 1024 + bars + plan + 64;

@@ -71,7 +71,7 @@ def test_decode_partial_sums_fit(lib):
 
     for T, k, E, H, F in ((1, 6, 64, 2048, 1408), (2, 2, 4, 4128, 64), (23, 8, 256, 512, 256), (64, 16, 16, 1056, 352), (5, 3, 7, 96, 160)):
         each = T * k // E
-        nb = 2 if T < 2 else T if T <= 16 else 16 if each <= 10 else 32 if each <= 24 else 64
+        nb = 2 if T < 2 else T if T <= 24 else 24 if each <= 14 else 32 if each <= 24 else 64
         total = size(T, k, E, H, F)
         for n in {1, 2, T, T * k // 2 + 1, T * k}:
             for ents in {up(n, nb), min(n, E), min(n, E) + n // nb}:

@@ -235,3 +235,11 @@ def test_as_the_quantizer_lays_weights_out(F):
     ref, bound = OM.moe_decode(x.double().cpu().numpy(), idx.cpu().numpy(), w.cpu().numpy(), value(q1, s1), value(q2, s2),
                                _gamma(H, Fd), 2.0 ** -12 + 2.0 ** -20)
     check_bf16(out, ref, bound + 1e-30, "out")
+
+
+@pytest.mark.parametrize("T", [7, 8, 11, 17, 21, 24, 31])
+def test_one_expert_for_all(F, T):
+    """Every token's choice is the same expert, and a CTA's run has several row tiles:
+    both accumulators in use with as many columns as an entry has."""
+    x, idx, w, w1, w2 = _case(T, 65536, 64, 2, 1, seed=T)
+    _check(F, x, torch.ones_like(idx), w, w1, w2)
