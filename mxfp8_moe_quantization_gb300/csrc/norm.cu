@@ -526,10 +526,17 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
 // thread takes R rows at a time where rows are short: what a row costs besides its
 // elements (the wait, the sum over its warps, addresses) is as many instructions as
 // two chunks.
+//
+// HBM's share is 7.03 bytes an element with dh, 5.03 without, an eighth to a sixth
+// below the bf16 form's, but the codes' unpacking (a conversion to fp16 pairs, two to
+// fp32, a product by the block's power of two) comes on top of its instructions, and
+// from about 20 an element on it is issue and latency that bound: 16384 x 5120 with
+// dh 99 us = 5.9 TB/s (89% of a copy's rate), 16384 x 7168 135 us = 6.1, 20001 x 4096
+// 100 us = 5.7, 65536 x 512 44 us = 5.4.
 template <int V, int R>
-constexpr int norm_ck_threads() { return R > 1 ? 256 : V == 4 ? 512 : 640; }
+constexpr int norm_ck_threads() { return R == 4 ? 256 : R == 2 || V == 4 ? 512 : 640; }
 template <int V, int R>
-constexpr int norm_ck_ctas() { return R > 1 ? 2 : 1; }
+constexpr int norm_ck_ctas() { return R == 4 ? 2 : 1; }
 
 template <int V, int R, bool W32>
 __global__ void __launch_bounds__(norm_ck_threads<V, R>(), norm_ck_ctas<V, R>()) k_norm_bwd_ckpt(NormBwdArgs a, int wpr, int stages) {
@@ -570,14 +577,17 @@ __global__ void __launch_bounds__(norm_ck_threads<V, R>(), norm_ck_ctas<V, R>())
     for (int s = 0; s < stages - 1 && nblk < blocks; ++s) issue();
   }
   Vec8 dw[V];
-  // bf16 weights stay in registers where there is room; others come from L1
-  constexpr bool KEEP_W = !W32 && V <= 2;
+  // the weights stay in registers where there is room (fp32, 16384 x 5120 with dh: 118
+  // us from L1, 111), else they come from L1 (20001 x 4096: 107 us, 117 with spills)
+  constexpr bool KEEP_W = !W32 && V <= 2, KEEP_W32 = W32 && V == 2 && R == 1;
   uint4 w4[KEEP_W ? V : 1];
+  Vec8 wf[KEEP_W32 ? V : 1];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     dw[i] = Vec8{};
     if constexpr (KEEP_W)
       w4[i] = t + i * tpr < nch ? reinterpret_cast<const uint4*>(a.w)[t + i * tpr] : make_uint4(0, 0, 0, 0);
+    if constexpr (KEEP_W32) wf[i] = t + i * tpr < nch ? load_w8<W32>(a.w, t + i * tpr) : Vec8{};
   }
   // the rows' rstd and scales are loaded one block ahead (rows past T: 0, and nothing stored)
   int64_t row = (int64_t)blockIdx.x * block + group * R;
@@ -628,9 +638,9 @@ __global__ void __launch_bounds__(norm_ck_threads<V, R>(), norm_ck_ctas<V, R>())
         const Vec8 d = unpack8(dq);
         mx_unpack8(*reinterpret_cast<const uint2*>(src_h + r * (row_bytes / 2) + ch * 8), xs[r][i], xh[r][i].p);
         if constexpr (!KEEP_W) {
-          const Vec8 wf = load_w8<W32>(a.w, ch);
+          const Vec8 w = KEEP_W32 ? wf[KEEP_W32 ? i : 0] : load_w8<W32>(a.w, ch);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) g[r][i].p[j] = mul2(d.p[j], wf.p[j]);
+          for (int j = 0; j < 4; ++j) g[r][i].p[j] = mul2(d.p[j], w.p[j]);
         } else {
           g[r][i] = {{mulx(dq.x, w4[i].x), mulx(dq.y, w4[i].y), mulx(dq.z, w4[i].z), mulx(dq.w, w4[i].w)}};
         }
@@ -846,14 +856,19 @@ cudaError_t launch_bwd_t(NormBwdArgs a, float* dw, int num_sms, int max_smem, cu
 template <bool W32>
 cudaError_t launch_bwd_ckpt(NormBwdArgs a, float* dw, int num_sms, int max_smem, cudaStream_t st) {
   const int nch = a.H / 8;
-  // chunks and rows of a thread at a time
-  const int v = nch <= 256 ? 1 : nch <= 1024 ? 2 : 4, rows = nch <= 256 ? 4 : nch <= 512 ? 2 : 1;
+  // Chunks and rows of a thread at a time.  Several rows where they are short
+  // (65536 x 512 with dh: 54 us with one, 48 with four), and where registers leave
+  // room for one CTA an SM anyway (16384 x 7168: 162 and 135 with two); in between two
+  // CTAs of one row each are better (16384 x 5120: 100, 113 with two rows).
+  const int v = nch <= 256 ? 1 : nch <= 1024 ? 2 : 4, rows = nch <= 256 ? 4 : nch <= 512 || (nch > 640 && nch <= 1024) ? 2 : 1;
   int wpr = nch > NORM_MAX_CHUNKS ? 16 : (nch + 32 * v - 1) / (32 * v);
   int groups = wpr >= 8 ? 1 : 8 / wpr;
-  // the ring as the bf16 form's
+  // the ring as the bf16 form's, and as deep as fits where registers leave room for
+  // one CTA only (16384 x 7168 without dh: 118 us, 147 with half the memory)
   const int64_t budget = max_smem - 2048;
   const int64_t slot = (int64_t)a.H * (a.dh ? 5 : 3) * groups * rows;
-  int stages = (int)(budget / 2 / slot < NORM_BWD_STAGES ? budget / 2 / slot : NORM_BWD_STAGES);
+  const int64_t room = budget / (wpr * groups > (rows == 1 && v == 2 ? 10 : 8) ? 1 : 2);
+  int stages = (int)(room / slot < NORM_BWD_STAGES ? room / slot : NORM_BWD_STAGES);
   if (stages < (rows > 1 ? 2 : 3)) stages = slot * 3 <= budget ? 3 : 2;
   const bool ring = nch <= NORM_MAX_CHUNKS && slot * stages <= budget;
   if (!ring) wpr = 16, groups = 1;
