@@ -21,6 +21,10 @@
 // copy's rate); 51136 x 1408 backward 120 us = 6.1 TB/s (91%).  The first form,
 // with every lane deriving every scale, expf and a division, and 45
 // instructions per element instead of about 20, took 152 and 283 us.
+//
+// The forward with a checkpoint writes another 2.06 bytes an element and takes some 12
+// instructions more for it: 36448 x 2048 both directions 105 us = 5.8 TB/s (87%), bound
+// by issue (two instructions of three cycles a scheduler).
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "launch.h"
@@ -169,9 +173,20 @@ FP8MOE_DEV void put_tile(const SwigluArgs& a, const TilePlace& tp, int64_t col0,
   }
 }
 
+// Eight neighbouring values times a power of two (a bf16 pair of it), as codes; the
+// products in fp32, exact as in bf16, so that nothing has to be unpacked.
+FP8MOE_DEV uint2 enc8(const uint4& w, uint32_t p2) {
+  const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpk(mulx(q[i], p2), f[2 * i], f[2 * i + 1]);
+  return make_uint2(cvt4(f[0], f[1], f[2], f[3]), cvt4(f[4], f[5], f[6], f[7]));
+}
+
 // One row's chunks of gate and up (column col of both) into the checkpoint: the
-// dim0 quantizer's arithmetic; four lanes hold a block.
-FP8MOE_DEV void put_ckpt(const SwigluArgs& a, int64_t row, int64_t col, bool on, int lane, const uint4& g, const uint4& u) {
+// dim0 quantizer's arithmetic; four lanes hold a block.  The two scales, gate's below
+// up's, are returned: four rows' go out together.
+FP8MOE_DEV uint32_t put_ckpt(const SwigluArgs& a, int64_t row, int64_t col, bool on, const uint4& g, const uint4& u) {
   auto amax = [](const uint4& q) {
     constexpr uint32_t M = 0x7FFF7FFFu;
     const uint32_t m = umax16x2(umax16x2(q.x & M, q.y & M), umax16x2(q.z & M, q.w & M));
@@ -181,15 +196,12 @@ FP8MOE_DEV void put_ckpt(const SwigluArgs& a, int64_t row, int64_t col, bool on,
   m = umax16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = umax16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
   const uint32_t bg = mx_block_scale(m & 0xFFFFu, pg), bu = mx_block_scale(m >> 16, pu);
-  if (!on) return;
-  uint8_t* q = a.ckpt_q + row * 2 * a.F + col;
-  *reinterpret_cast<uint2*>(q) = enc_row8(g, pg);
-  *reinterpret_cast<uint2*>(q + a.F) = enc_row8(u, pu);
-  if ((lane & 3) == 0) {
-    uint8_t* s = a.ckpt_s + row * (a.F / 16) + (col >> 5);
-    s[0] = (uint8_t)bg;
-    s[a.F >> 5] = (uint8_t)bu;
+  if (on) {
+    uint8_t* q = a.ckpt_q + row * 2 * a.F + col;
+    *reinterpret_cast<uint2*>(q) = enc8(g, pg);
+    *reinterpret_cast<uint2*>(q + a.F) = enc8(u, pu);
   }
+  return bg | bu << 8;
 }
 
 // Shared memory of a warp with PF: one 32 x 64 box each of gate, up and, backward,
@@ -352,6 +364,7 @@ FP8MOE_DEV void swiglu_body(const CUtensorMap* th, const CUtensorMap* td, const 
     if (fail) break;
     uint64_t v[8][CW / 2], v2[BWD ? 8 : 1][CW / 2];
     const uint8_t* lp = wbuf + rq * 8 * 128 + cq * 16;
+    uint32_t ck[2] = {};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint4 gq = PF ? *reinterpret_cast<const uint4*>(lp + i * 128) : g[PF ? 0 : i];
@@ -360,10 +373,21 @@ FP8MOE_DEV void swiglu_body(const CUtensorMap* th, const CUtensorMap* td, const 
       if constexpr (BWD) dq = PF ? *reinterpret_cast<const uint4*>(lp + 2 * BOX_BYTES + i * 128) : d[PF ? 0 : i];
       const uint32_t gw[4] = {gq.x, gq.y, gq.z, gq.w}, uw[4] = {uq.x, uq.y, uq.z, uq.w};
       const uint32_t dw[4] = {dq.x, dq.y, dq.z, dq.w};
-      if constexpr (CK) put_ckpt(a, (int64_t)row0 + rq * 8 + i, col, ok && row0 + rq * 8 + i < a.M, lane, gq, uq);
+      if constexpr (CK) {
+        const uint32_t s = put_ckpt(a, (int64_t)row0 + rq * 8 + i, col, ok && row0 + rq * 8 + i < a.M, gq, uq);
+        if ((lane & 3) == (i & 3)) ck[i >> 2] = s;   // one of the block's four lanes keeps it
+      }
 #pragma unroll
       for (int p = 0; p < CW / 2; ++p) {
         act_pair<BWD>(gw[p], uw[p], dw[p], v[i][p], v2[BWD ? i : 0][p]);
+      }
+    }
+    if constexpr (CK) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t row = (int64_t)row0 + rq * 8 + i * 4 + (lane & 3);
+        uint8_t* s = a.ckpt_s + row * (a.F / 16) + (col >> 5);
+        if (ok && row < a.M) s[0] = (uint8_t)ck[i], s[a.F >> 5] = (uint8_t)(ck[i] >> 8);
       }
     }
     if (PF) {
