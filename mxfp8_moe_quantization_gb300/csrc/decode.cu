@@ -940,9 +940,7 @@ int64_t most_parts(int64_t ents, int64_t rt, int64_t kt) {
 // Pairs of an entry, that is, of one reading of an expert: its terms have to fit a
 // ring slot, and larger slots leave room for fewer: up to 24 pairs four, up to 32
 // three.  T, which is enough where a token's choices differ, as long as there is
-// room for four; beyond that room for more than most experts get.  (23 tokens, 8 of
-// 256 experts of 2048 x 7168, the busiest chosen by all: entries of 16 took 816 us,
-// of 23 791.)
+// room for four; beyond that room for more than most experts get.
 int entry_pairs(int64_t T, int64_t k, int64_t E) {
   const int64_t each = T * k / E;   // pairs an expert gets on average
   return T < 2 ? 2 : T <= 24 ? (int)T : each <= 14 ? 24 : each <= 24 ? 32 : 64;
