@@ -48,7 +48,6 @@ constexpr int DC_JOIN = DC_THREADS - 96;  // threads that make terms and add par
 constexpr int DC_G = 2;                   // tiles of 128 x 128 in a piece
 constexpr int DC_TILE = 128 * 128, DC_A_BYTES = DC_G * DC_TILE;
 constexpr int DC_MAX_SLOTS = 6;
-constexpr int DC_FLIGHT = 3;              // pieces of weights in flight at most
 constexpr int DC_DEAD = 0xFFFF;
 
 __host__ __device__ constexpr int up16(int v) { return (v + 15) / 16 * 16; }
@@ -68,7 +67,6 @@ struct Div {
 // of terms and their scales (sb slots), the plan.
 struct DecodeSmem {
   int sa, sb, b_bytes;
-  int flight;                              // pieces of weights in flight, at most sa
   int team_log, teams;                     // 2^team_log warps fill a slot of terms together
   int acc;                                 // tensor memory columns of an accumulator
   int sfa, b, bars, plan, total;
@@ -448,7 +446,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     // follows them meets its first instructions and loads in a full memory system.
     if constexpr (!DIRECT) bar_sync(1, DC_JOIN + 32);
     if (lane == 0) {
-      Slot slot, late;
+      Slot slot;
       uint32_t i = 0;
       bool ok = true;
       for (int ph = 0; ph < 2 && ok; ++ph) {
@@ -466,13 +464,6 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
               break;
             }
             if (a.stall && cta == 0 && i == 0) continue;
-            // no more in flight than keeps HBM busy: everything else in the memory
-            // system waits behind it
-            if (i >= (uint32_t)L.flight && !mbar_wait(&a_full[late.i], late.turn, abort_flag)) {
-              ok = false;
-              break;
-            }
-            if (i >= (uint32_t)L.flight) late.step(1, L.sa);
             const int tiles = min(DC_G, kt - x);
             uint8_t* dst = smem + slot.i * DC_A_BYTES;
             mbar_expect_tx(bar, tiles * (DC_TILE + 512));
@@ -972,7 +963,6 @@ DecodeSmem layout(int P, int nb, int max_ent, int max_smem) {
   L.sa = (max_smem - 2048 - fixed) / (DC_A_BYTES + DC_G * 512 + L.b_bytes);
   if (L.sa > DC_MAX_SLOTS) L.sa = DC_MAX_SLOTS;
   L.sb = L.sa;
-  L.flight = DC_FLIGHT < L.sa ? DC_FLIGHT : L.sa;
   L.team_log = L.sb >= 3 ? 1 : 2;
   L.teams = (DC_BWARPS >> L.team_log) < L.sb ? DC_BWARPS >> L.team_log : L.sb;
   L.b = L.sa * DC_A_BYTES;
