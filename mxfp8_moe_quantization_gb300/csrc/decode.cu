@@ -35,6 +35,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "moe_ops.h"
+#include "swiglu.cuh"
 #include "tcgen05.cuh"
 #include "tma.cuh"
 
@@ -203,6 +204,12 @@ FP8MOE_DEV void plan_block(const DecodeArgs& a, const Plan& pl, int* scratch) {
   __syncthreads();
 }
 
+FP8MOE_DEV float reciprocal(float x) {   // to 2^-23
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // One product's stream of pieces: nent entries x row tiles x pieces of K, in runs
 // of `base` pieces, one more for the first `rest` CTAs.
 struct Stream {
@@ -216,8 +223,8 @@ struct Stream {
     runs = want < grid.d ? want : grid.d;
     base = want < grid.d ? (C == 2 * runs ? 2 : 1) : grid.quot(C);
     rest = C - base * runs;
-    per0 = __frcp_rn((float)base);
-    per1 = __frcp_rn((float)(base + 1));
+    per0 = reciprocal((float)base);
+    per1 = reciprocal((float)(base + 1));
   }
   FP8MOE_DEV uint32_t first(uint32_t cta) const { return cta < runs ? cta * base + min(cta, rest) : C; }
   // the CTA whose run has piece c: below 2^8, so that the quotient in fp32 is off by
@@ -287,6 +294,7 @@ FP8MOE_DEV void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
+FP8MOE_DEV void prefetch_tmap(const CUtensorMap* m) { asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory"); }
 FP8MOE_DEV void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 // Grid-wide meetings: a counter each, to which every CTA of a launch adds one.
 // They are the library's own, per device, as no caller's memory starts at zero: a
@@ -324,6 +332,14 @@ FP8MOE_DEV float2 e4m3x2_value(uint32_t c) {
   float2 v;
   asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, u;\n}" : "=f"(v.x), "=f"(v.y) : "r"(h));
   return v;
+}
+
+// silu(g) u of two sums each.  The sigmoid of gates beyond +-88 is that of 88: 1, and
+// below 2^-126.  (Packed and without branches: eight divisions and expf in a row took
+// 1.5 us of a token's way, most of it to fetch their instructions.)
+FP8MOE_DEV void act_of_sums(const float* g, const float* u, float* v) {
+  auto near = [](float x) { return fminf(fmaxf(x, -88.0f), 88.0f); };
+  unpk(mul2(mul2(pk(g[0], g[1]), sigmoid2(pk(near(g[0]), near(g[1])))), pk(u[0], u[1])), v[0], v[1]);
 }
 
 // NT terms of eight neighbouring values of a row, four lanes a block: codes, and
@@ -402,6 +418,10 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     *abort_flag = 1;
   };
 
+  if (warp == DC_WARP_TMA && lane == 0) {
+    prefetch_tmap(&tm1);
+    prefetch_tmap(&tm2);
+  }
   if (warp == DC_WARP_MMA) {
     if (lane == 0) abort_s = 0;
     if (lane < L.sa) mbar_init(&a_full[lane], 1), mbar_init(&a_empty[lane], 1);
@@ -742,7 +762,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
           const float gs[8] = {z[0].x, z[0].y, z[0].z, z[0].w, z[1].x, z[1].y, z[1].z, z[1].w};
           const float us[8] = {z[2].x, z[2].y, z[2].z, z[2].w, z[3].x, z[3].y, z[3].z, z[3].w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = gs[i] / (1.0f + expf(-gs[i])) * us[i];
+          for (int i = 0; i < 4; ++i) act_of_sums(gs + 2 * i, us + 2 * i, v + 2 * i);
         }
         __syncwarp();
         const Terms<NT> terms(v);
@@ -861,7 +881,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         const float us[8] = {q[2].x, q[2].y, q[2].z, q[2].w, q[3].x, q[3].y, q[3].z, q[3].w};
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = gs[i] / (1.0f + expf(-gs[i])) * us[i];
+        for (int i = 0; i < 4; ++i) act_of_sums(gs + 2 * i, us + 2 * i, v + 2 * i);
         const Terms<3> terms(v);
         if (next.in) put(terms, next.place, next.c, s2.kp.d);
         if (u + unit_step - back < units) next = act_of(u + unit_step);
