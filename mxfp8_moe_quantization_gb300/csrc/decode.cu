@@ -64,10 +64,10 @@ struct Div {
   }
 };
 
-// Shared memory: the rings of weights (at 0) and of their scales (sa slots), that
-// of terms and their scales (sb slots), the plan.
+// Shared memory: the rings of weights (at 0), of their scales, of terms and their
+// scales (a piece has the same slot in all), the plan.
 struct DecodeSmem {
-  int sa, sb, b_bytes;
+  int slots, b_bytes;
   int team_log, teams;                     // 2^team_log warps fill a slot of terms together
   int acc;                                 // tensor memory columns of an accumulator
   int sfa, b, bars, plan, total;
@@ -276,6 +276,15 @@ struct Slot {
   }
 };
 
+// True in one lane of a converged warp, which the compiler then knows to be alone: its
+// descriptors need no loop over lanes (a copy of scales 10 cycles to issue, 50 with
+// lane == 0).
+FP8MOE_DEV bool elected() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // descriptor of a 128x4 scale tile: 32 rows of 16 bytes, no swizzle
 FP8MOE_DEV uint64_t sdesc_scales(uint32_t saddr) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
@@ -401,15 +410,14 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ int abort_s;
   __shared__ uint32_t tmem_s;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t cta = blockIdx.x, grid = gridDim.x;
   volatile int* abort_flag = &abort_s;
   uint64_t* a_full = (uint64_t*)(smem + L.bars);
-  uint64_t* a_empty = a_full + L.sa;
-  uint64_t* b_full = a_empty + L.sa;
-  uint64_t* b_empty = b_full + L.sb;
-  uint64_t* sf_full = b_empty + L.sb;
-  uint64_t* acc_full = sf_full + L.sb;
+  uint64_t* b_full = a_full + L.slots;
+  uint64_t* sf_full = b_full + L.slots;
+  uint64_t* empty = sf_full + L.slots;
+  uint64_t* acc_full = empty + L.slots;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;   // the issuer's, the copier's
   const Plan pl(smem + L.plan, a.P, a.max_ent);
@@ -424,8 +432,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   }
   if (warp == DC_WARP_MMA) {
     if (lane == 0) abort_s = 0;
-    if (lane < L.sa) mbar_init(&a_full[lane], 1), mbar_init(&a_empty[lane], 1);
-    if (lane < L.sb) mbar_init(&b_full[lane], 1 << L.team_log), mbar_init(&b_empty[lane], 1), mbar_init(&sf_full[lane], 1);
+    if (lane < L.slots)
+      mbar_init(&a_full[lane], 1), mbar_init(&b_full[lane], 1 << L.team_log), mbar_init(&sf_full[lane], 1), mbar_init(&empty[lane], 1);
     if (lane < 2) mbar_init(&acc_full[lane], 1), mbar_init(&acc_empty[lane], 4), mbar_init(&drain[lane], 1);
     mbar_fence_init();
   }
@@ -465,7 +473,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     // The first fills leave behind this CTA's terms of x: in front of them, what
     // follows them meets its first instructions and loads in a full memory system.
     if constexpr (!DIRECT) bar_sync(1, DC_JOIN + 32);
-    if (lane == 0) {
+    if (elected()) {
       Slot slot;
       uint32_t i = 0;
       bool ok = true;
@@ -477,9 +485,9 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
           const int e = (int)(pl.ent[r.ent] & 1023u);
           int x = r.k * DC_G;   // the piece's first tile
           const uint8_t* sc = (ph ? a.s2 : a.s1) + (((int64_t)e * s.rt.d + r.row) * kt + x) * 512;
-          for (int c = 0; c < r.n; ++c, ++i, x += DC_G, sc += DC_G * 512, slot.step(1, L.sa)) {
+          for (int c = 0; c < r.n; ++c, ++i, x += DC_G, sc += DC_G * 512, slot.step(1, L.slots)) {
             uint64_t* bar = &a_full[slot.i];
-            if (!mbar_wait(&a_empty[slot.i], slot.turn ^ 1u, abort_flag)) {
+            if (!mbar_wait(&empty[slot.i], slot.turn ^ 1u, abort_flag)) {
               ok = false;
               break;
             }
@@ -497,14 +505,14 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       if (!ok) fail();
       // no copy stays in flight after a wait that ran out
       if (*abort_flag)
-        for (uint32_t n = i > (uint32_t)L.sa ? i - L.sa : 0; n < i; ++n)
-          if (!(a.stall && cta == 0 && n == 0)) (void)mbar_wait(&a_full[n % L.sa], (n / (uint32_t)L.sa) & 1u, nullptr);
+        for (uint32_t n = i > (uint32_t)L.slots ? i - L.slots : 0; n < i; ++n)
+          if (!(a.stall && cta == 0 && n == 0)) (void)mbar_wait(&a_full[n % L.slots], (n / (uint32_t)L.slots) & 1u, nullptr);
     }
     __syncwarp();
   } else if (warp == DC_WARP_MMA) {
     // ======================= products =======================
-    if (lane == 0) {
-      Slot sa, sb, acc;
+    if (elected()) {
+      Slot slot, acc;
       const uint64_t ad0 = sdesc_sw128(smem_u32(smem)), bd0 = sdesc_sw128(smem_u32(smem + L.b));
       bool ok = true;
       for (int ph = 0; ph < 2 && ok; ++ph) {
@@ -518,19 +526,19 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
           if (!mbar_wait(&acc_empty[acc.i], acc.turn ^ 1u, abort_flag)) ok = false;
           uint32_t add = 0;
           for (int c = 0; c < r.n; ++c) {
-            if (!ok || !mbar_wait(&a_full[sa.i], sa.turn, abort_flag) || !mbar_wait(&b_full[sb.i], sb.turn, abort_flag) ||
-                !mbar_wait(&sf_full[sb.i], sb.turn, abort_flag)) {
+            if (!ok || !mbar_wait(&a_full[slot.i], slot.turn, abort_flag) || !mbar_wait(&b_full[slot.i], slot.turn, abort_flag) ||
+                !mbar_wait(&sf_full[slot.i], slot.turn, abort_flag)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t at_b = (uint32_t)(sb.i * L.b_bytes);
+            const uint32_t at_b = (uint32_t)(slot.i * L.b_bytes);
 #pragma unroll
             for (int g = 0; g < DC_G; ++g) {
               const int left = kt - (r.k + c) * DC_G - g;   // tiles of the row from this one on
               if (left <= 0) break;
-              const uint32_t sf = tmem + 2 * L.acc + (sb.i * DC_G + g) * 12;
-              const uint64_t ad = ad0 + ((uint32_t)(sa.i * DC_A_BYTES + g * DC_TILE) >> 4);
+              const uint32_t sf = tmem + 2 * L.acc + (slot.i * DC_G + g) * 12;
+              const uint64_t ad = ad0 + ((uint32_t)(slot.i * DC_A_BYTES + g * DC_TILE) >> 4);
               const uint64_t bd = bd0 + ((at_b + (uint32_t)(g * tt.rows * 128)) >> 4);
               auto block = [&](int k, uint32_t plus) {
                 mma_mx1(d, ad + 2 * k, bd + 2 * k, id | (uint32_t)k << 4 | (uint32_t)k << 29, sf, sf + 4, plus);
@@ -544,10 +552,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
               }
               add = 1;
             }
-            tc_commit(&a_empty[sa.i]);
-            tc_commit(&b_empty[sb.i]);
-            sa.step(1, L.sa);
-            sb.step(1, L.sb);
+            tc_commit(&empty[slot.i]);   // (once a piece: a commit holds its thread up for as long as seven products)
+            slot.step(1, L.slots);
           }
           if (!ok) break;
           tc_commit(&acc_full[acc.i]);
@@ -564,8 +570,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     // ======================= scales to tensor memory =======================
     // From a thread of their own the copies overlap the products.  A slot's columns
     // are free when its terms are new: the products of its last turn are over.
-    if (lane == 0) {
-      Slot sa, sb;
+    if (elected()) {
+      Slot slot;
       const uint64_t sfa0 = sdesc_scales(smem_u32(smem + L.sfa)), sfb0 = sdesc_scales(smem_u32(smem + L.b));
       bool ok = true;
       for (int ph = 0; ph < 2 && ok; ++ph) {
@@ -574,7 +580,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         for (Run r(s, cta); r.left > 0 && ok; r.next(s)) {
           const TermTiles tt((int)(pl.ent[r.ent] >> 20) * (ph ? 3 : 2));
           for (int c = 0; c < r.n; ++c) {
-            if (!mbar_wait(&a_full[sa.i], sa.turn, abort_flag) || !mbar_wait(&b_full[sb.i], sb.turn, abort_flag)) {
+            if (!mbar_wait(&a_full[slot.i], slot.turn, abort_flag) || !mbar_wait(&b_full[slot.i], slot.turn, abort_flag)) {
               ok = false;
               break;
             }
@@ -582,15 +588,14 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
 #pragma unroll
             for (int g = 0; g < DC_G; ++g) {
               if ((r.k + c) * DC_G + g >= kt) break;
-              const uint32_t sf = tmem + 2 * L.acc + (sb.i * DC_G + g) * 12;
-              const uint64_t sfb = sfb0 + ((uint32_t)(sb.i * L.b_bytes + DC_G * tt.rows * 128 + g * tt.sf) >> 4);
-              cp_scales(sf, sfa0 + (uint32_t)((sa.i * DC_G + g) * 32));
+              const uint32_t sf = tmem + 2 * L.acc + (slot.i * DC_G + g) * 12;
+              const uint64_t sfb = sfb0 + ((uint32_t)(slot.i * L.b_bytes + DC_G * tt.rows * 128 + g * tt.sf) >> 4);
+              cp_scales(sf, sfa0 + (uint32_t)((slot.i * DC_G + g) * 32));
               cp_scales(sf + 4, sfb);
               if (tt.rows > 128) cp_scales(sf + 8, sfb + 32);
             }
-            tc_commit(&sf_full[sb.i]);
-            sa.step(1, L.sa);
-            sb.step(1, L.sb);
+            tc_commit(&sf_full[slot.i]);
+            slot.step(1, L.slots);
           }
         }
       }
@@ -651,7 +656,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     // that has filled its last piece knows that the slots' turns before are over.)
     const int team = (warp - DC_WARP_B) >> L.team_log, rank = (warp - DC_WARP_B) & ((1 << L.team_log) - 1);
     Slot slot;
-    slot.step(team, L.sb);
+    slot.step(team, L.slots);
     Run r(s1, cta);                           // of the stream to come, at the team's next piece
     int c = team;                                    // this, counted in r's segment
     auto enter = [&](const Stream& s) {
@@ -664,7 +669,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     auto feed = [&](auto nt) {
       constexpr int NT = decltype(nt)::value;
       const Stream& s = NT == 2 ? s1 : s2;
-      for (; team < L.teams && r.left > 0; c += L.teams, slot.step(L.teams, L.sb), enter(s)) {
+      for (; team < L.teams && r.left > 0; c += L.teams, slot.step(L.teams, L.slots), enter(s)) {
         const uint32_t ent = pl.ent[r.ent];
         const TermTiles tt((int)(ent >> 20) * NT);
         uint4* dst = reinterpret_cast<uint4*>(smem + L.b + slot.i * L.b_bytes);
@@ -677,7 +682,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (i0 + step * i < chunks) q[i] = __ldcg(src + i0 + step * i);
-          if (!ready) ok = __all_sync(0xffffffffu, mbar_wait(&b_empty[slot.i], slot.turn ^ 1u, abort_flag));
+          if (!ready) ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot.i], slot.turn ^ 1u, abort_flag));
           ready = true;
           if (!ok) break;
 #pragma unroll
@@ -766,7 +771,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         }
         __syncwarp();
         const Terms<NT> terms(v);
-        if (!__all_sync(0xffffffffu, mbar_wait(&b_empty[slot.i], slot.turn ^ 1u, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot.i], slot.turn ^ 1u, abort_flag))) {
           fail();
           break;
         }
@@ -776,7 +781,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b_full[slot.i]);
-        slot.step(L.teams, L.sb);
+        slot.step(L.teams, L.slots);
       }
     };
     // ======================= accumulators to partial sums =======================
@@ -977,17 +982,16 @@ DecodeSmem layout(int P, int nb, int max_ent, int max_smem) {
   L.acc = 3 * ((nb + 7) / 8 * 8);
   if (L.acc < up16(TermTiles(3 * nb).rows)) L.acc = up16(TermTiles(3 * nb).rows);
   const int plan = 16 + max_ent * 4 + P * 10;
-  const int bars = 8 * (5 * DC_MAX_SLOTS + 8);
+  const int bars = 8 * (4 * DC_MAX_SLOTS + 8);
   const int fixed = 1024 + bars + plan + 64;
   // 1024 to align the rings, 1024 for what is static
-  L.sa = (max_smem - 2048 - fixed) / (DC_A_BYTES + DC_G * 512 + L.b_bytes);
-  if (L.sa > DC_MAX_SLOTS) L.sa = DC_MAX_SLOTS;
-  L.sb = L.sa;
-  L.team_log = L.sb >= 3 ? 1 : 2;
-  L.teams = (DC_BWARPS >> L.team_log) < L.sb ? DC_BWARPS >> L.team_log : L.sb;
-  L.b = L.sa * DC_A_BYTES;
-  L.sfa = L.b + L.sb * L.b_bytes + 1024;
-  L.bars = L.sfa + L.sa * DC_G * 512;
+  L.slots = (max_smem - 2048 - fixed) / (DC_A_BYTES + DC_G * 512 + L.b_bytes);
+  if (L.slots > DC_MAX_SLOTS) L.slots = DC_MAX_SLOTS;
+  L.team_log = L.slots >= 3 ? 1 : 2;
+  L.teams = (DC_BWARPS >> L.team_log) < L.slots ? DC_BWARPS >> L.team_log : L.slots;
+  L.b = L.slots * DC_A_BYTES;
+  L.sfa = L.b + L.slots * L.b_bytes + 1024;
+  L.bars = L.sfa + L.slots * DC_G * 512;
   L.plan = L.bars + bars;
   L.total = (L.plan + plan + 15) / 16 * 16;
   return L;
@@ -1026,8 +1030,8 @@ cudaError_t launch_decode(DecodeArgs a, void* workspace, int num_sms, int max_sm
   a.nb = entry_pairs(a.T, a.k, a.E);
   a.max_ent = (int)max_entries(a.P, a.E, a.nb);
   DecodeSmem L = layout(a.P, a.nb, a.max_ent, max_smem);
-  if (num_sms > DECODE_MAX_CTAS || L.sa < 2 || 2 * L.acc + 12 * DC_G * L.sb > 512 ||
-      (a.P > 32 && (a.E + a.P + 64) * 4 > L.sb * L.b_bytes))
+  if (num_sms > DECODE_MAX_CTAS || L.slots < 2 || 2 * L.acc + 12 * DC_G * L.slots > 512 ||
+      (a.P > 32 && (a.E + a.P + 64) * 4 > L.slots * L.b_bytes))
     return cudaErrorNotSupported;
   const DecodeSpace w = space_of(a.T, a.k, a.E, a.H, a.F);
   a.part1 = (float*)workspace;
