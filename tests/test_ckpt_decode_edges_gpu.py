@@ -265,3 +265,105 @@ def test_large_experts(F):
     small = F.fp8moe_mxfp8_moe_decode(x, torch.tensor([[1, 0]], dtype=I32, device=DEV), w, w1[pick], per(s1), w2[pick], per(s2))
     assert torch.equal(out, small) and bool(out.float().abs().max() > 0)
     assert F.fp8moe_get_device_status() == 0
+
+
+# --- long runs of tiles, odd addresses ---------------------------------------------------
+
+def _values(q, s):
+    v = q.view(torch.float8_e4m3fn).float().view(q.shape[0], -1, 32) * torch.exp2(s.float() - 127)[..., None]
+    return v.view(q.shape).to(BF16)
+
+
+def _at_odd(t):
+    """The same bytes one byte further."""
+    raw = torch.empty(t.numel() + 1, dtype=U8, device=DEV)
+    raw[1:].copy_(t.reshape(-1))
+    return raw[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("M,Fd", [(60032, 128), (60000, 160), (40000, 416), (80000, 512), (30016, 608)])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_backward_long_runs(F, M, Fd, grouped):
+    """Many tiles: a warp has several, and row scales go out as words, of gate and up in
+    step or not (F a multiple of 128 or not)."""
+    hq, hs = _ckpt(M, 2 * Fd)
+    v, dout = _values(hq, hs), _bf16((4096, Fd), 2).repeat(M // 4096 + 1, 1)[:M].contiguous()
+    ends = sorted({32 * i for i in (1, 7, 7, 300, M // 64)}) + [M]
+    offs = torch.tensor(ends, dtype=I32, device=DEV) if grouped else None
+    lay = (F.GROUP_ROWS, F.GROUP_COLS) if grouped else (F.NO_GROUPS, F.NO_GROUPS)
+    kw = dict(need_dh=False, dim0=True, dim1=True)
+    want = F.fp8moe_swiglu_bwd(dout, v, offs, *lay, **kw)
+    act = F.fp8moe_swiglu_fwd(v, offs, *lay, need_out=False, dim1=True)
+    for odd in (False, True):
+        more, scales = {}, hs
+        if odd:
+            scales = _at_odd(hs)
+            more = dict(s0=_at_odd(torch.zeros_like(want[2])), s1=_at_odd(torch.zeros_like(want[4])), q0=torch.empty_like(want[1]),
+                        q1=torch.empty_like(want[3]), aq1=torch.empty_like(act[3]), as1=_at_odd(torch.zeros_like(act[4])))
+        got = F.fp8moe_swiglu_bwd_ckpt(dout, hq, scales, offs, *lay, act1=True, **kw, **more)
+        for a, b in zip(got[1:], (*want[1:], act[3], act[4])):
+            assert torch.equal(a, b)
+        # rows alone, as the last rows are not whole
+        n = M - 5
+        if not grouped:
+            few = F.fp8moe_swiglu_bwd_ckpt(dout[:n], hq[:n], scales[:n] if odd else hs[:n], None, F.SCALES_ROWMAJOR, dim0=True)
+            ref = F.fp8moe_swiglu_bwd(dout[:n], v[:n], None, F.SCALES_ROWMAJOR, dim0=True)
+            assert all(torch.equal(a, b) for a, b in zip(few[:3], ref[:3]))
+    assert F.fp8moe_get_device_status() == 0
+
+
+@pytest.mark.parametrize("M,Fd", [(77, 96), (20001, 160)])
+def test_forward_scales_at_odd_addresses(F, M, Fd):
+    h = _bf16((M, 2 * Fd), 1)
+    want = F.fp8moe_swiglu_fwd_ckpt(h, need_out=False)
+    hs = _at_odd(torch.zeros_like(want[6]))
+    got = F.fp8moe_swiglu_fwd_ckpt(h, need_out=False, hs=hs)
+    assert torch.equal(got[5], want[5]) and torch.equal(hs, want[6])
+
+
+@pytest.mark.parametrize("T,H,w32", [(1301, 7168, False), (1300, 7168, True), (700, 8192, False), (2001, 4096, True), (2003, 1376, False)])
+@pytest.mark.parametrize("stream", [False, True])
+def test_norm_several_rows_a_thread(F, T, H, w32, stream):
+    """Rings that turn several times: against float64 on the device."""
+    hq, hs = _ckpt(T, H)
+    v, dy, dh = _values(hq, hs).double(), _bf16((T, H), 3), _bf16((T, H), 4) if stream else None
+    w = (torch.rand(H, device=DEV) + 0.5).to(F32 if w32 else BF16)
+    rstd = torch.rsqrt(v.square().mean(1)).float()
+    dx, dw = F.fp8moe_add_rmsnorm_bwd_ckpt(dy, hq, _at_odd(hs), rstd, w, dh)
+    r, g, xh = rstd.double()[:, None], dy.double() * w.double(), v * rstd.double()[:, None]
+    mean = (g * xh).mean(1, keepdim=True)
+    ref = r * (g - xh * mean) + (dh.double() if stream else 0)
+    size = r * (g.abs() + xh.abs() * (g * xh).abs().mean(1, keepdim=True)) + (dh.double().abs() if stream else 0)
+    assert bool(((dx.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2e-6 * size).all())
+    ref, parts = (dy.double() * xh).sum(0), (dy.double() * xh).abs().sum(0)
+    assert bool(((dw.double() - ref).abs() <= (T / 8 + 32) * 2.0 ** -24 * parts).all())
+    assert F.fp8moe_get_device_status() == 0
+
+
+# --- few tokens with many choices ----------------------------------------------------------
+
+@pytest.mark.parametrize("T,H,Fd,E,k", [(1, 64, 64, 64, 40), (1, 96, 32, 3, 1024), (2, 96, 64, 48, 30), (2, 32, 160, 1024, 512),
+                                        (24, 64, 96, 5, 4), (25, 64, 96, 5, 4)])
+def test_decode_many_choices(F, T, H, Fd, E, k):
+    """More than 32 pairs in the form for one or two tokens, the same expert often; both
+    sides of the entries' rule.  The sums in float64; the tolerances are those of the
+    other tests of this call."""
+    x, idx, w, w1, s1, w2, s2 = _layer(F, T, H, Fd, E, k, seed=k)
+    out = F.fp8moe_mxfp8_moe_decode(x, idx, w, w1, s1, w2, s2).double()
+    f = 2.0 ** (118 - 127)
+    a1, a2 = (m.view(torch.float8_e4m3fn).float().double() * f for m in (w1, w2))
+    gu = torch.einsum("enh,th->ten", a1, x.double())
+    size = torch.einsum("enh,th->ten", a1.abs(), x.double().abs())
+    g, u = gu.chunk(2, 2)
+    dg, du = ((max(H, Fd) / 32 + 64) * 2.0 ** -22 * size).chunk(2, 2)
+    s = g * torch.sigmoid(g)
+    act = s * u
+    dact = 1.1 * dg * (u.abs() + du) + s.abs() * du + (2.0 ** -12 + 2.0 ** -20) * act.abs()
+    y = torch.einsum("ehf,tef->teh", a2, act)
+    dy = torch.einsum("ehf,tef->teh", a2.abs(), dact + (max(H, Fd) / 32 + 64) * 2.0 ** -22 * act.abs())
+    share = torch.zeros(T, E, dtype=torch.float64, device=DEV).scatter_add_(1, idx.long(), w.double())
+    ref = torch.einsum("te,teh->th", share, y)
+    # k products added in fp32, each sum off by half a step
+    tol = torch.einsum("te,teh->th", share, dy + (k + 1) * 2.0 ** -24 * y.abs()) + 2.0 ** -8 * ref.abs() + 1e-30
+    assert bool(((out - ref).abs() <= tol).all())
+    assert F.fp8moe_get_device_status() == 0
