@@ -231,8 +231,8 @@ FP8MOE_DEV uint32_t powers(uint32_t sg, uint32_t su) {
 FP8MOE_DEV float power_of_gate(uint32_t w) { return __uint_as_float(w << 16); }
 FP8MOE_DEV float power_of_up(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// The warp's tiles from column `col` on up to column `end`.  The
-// next tile's loads are on their way while the gradients go out.
+// The warp's tiles from column `col` up to column `end`; the next tile's loads are on
+// their way while the gradients go out.
 template <bool ACT, bool ALL>
 FP8MOE_DEV uint32_t tiles(const SwigluArgs& a, const Rows& r, uint32_t col, uint32_t end, int lane) {
   const int rq = lane >> 3;
