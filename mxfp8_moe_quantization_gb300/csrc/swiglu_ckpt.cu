@@ -8,17 +8,19 @@
 // A warp's tile is 32 x 32, a lane's 8 x 4 (the bf16 form's is twice as wide): a block
 // of a row is one warp's eight lanes, so that its scale is read once a row, and three
 // warps a scheduler have room for a tile's values and for the next tile, whose loads are
-// on their way while this one's gradients go out (51136 x 1408: 205 us without).  A CTA
-// is a warp: nothing is shared, and the last round is the shorter (four: 159 us, twelve
-// 177).  Its tiles follow a row, four of them, whose scales are then read and written
-// as a word (each row's lie in a sector of their own; single bytes: 164 us).
+// on their way while this one's gradients go out.  A CTA is a warp: nothing is shared,
+// and the last round is the shorter.  Its tiles follow a row, four of them, whose scales
+// are then read and written as a word, as each row's lie in a sector of their own.  Maxima
+// go through the lanes two in a word.  (51136 x 1408 with a cold L2: 223 us without the
+// next tile's loads, 164 with single scale bytes and four warps a CTA, 159 with words, 155
+// with a warp a CTA, 151 with maxima in pairs; twelve warps a CTA 177.)
 //
-// Bound by the instructions, 47 an element of a (five block scalings, the unpacking and
+// Bound by the instructions, 46 an element of a (five block scalings, the unpacking and
 // the sigmoid), of which 0.6 a cycle and scheduler issue, and by an SM's memory pipe,
 // which takes every 32 bytes apart that a store's lanes have in one row or column, and
-// is two thirds busy.  HBM's 9.2 bytes an element would take 100 us; measured: 51136 x
-// 1408 in 64 groups, all outputs, 155 us = 4.3 TB/s (64% of a copy's rate), without the
-// activation 127.
+// is two thirds busy.  HBM's 9.2 bytes an element would take 100 us; measured, among
+// other passes: 51136 x 1408 in 64 groups, all outputs, 147 us = 4.5 TB/s (68% of a
+// copy's rate).
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "launch.h"
@@ -30,7 +32,7 @@
 namespace fp8moe {
 namespace {
 
-// Warps an SM: without the activation 128 registers do (127 us, 132 with twelve warps).
+// Warps an SM: without the activation 128 registers do (128 us cold, 132 with twelve warps).
 template <bool ACT>
 constexpr int sc_warps() { return ACT ? 12 : 16; }
 constexpr int CP = 2;                // column pairs of a lane
@@ -66,20 +68,41 @@ FP8MOE_DEV uint64_t column_scale(const Rows& r, uint32_t col, uint32_t j) {
   return r.at_s1 + (r.band1 ? wide(r.band1, col >> 7) * 128 + (col >> 5 & 3u) * 4 + j * 16 : wide(r.M / 32, col + j));
 }
 
+// Maxima on their way through the lanes, two in a word: a block's scale hangs on the upper
+// halves of their fp32 words only (NaN is the largest, infinity next).
+FP8MOE_DEV uint32_t upper2(float lo, float hi) { return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632); }
+// One step over lanes that differ in `mask`, as halve()
+template <int N>
+FP8MOE_DEV void halve2(const uint32_t (&m)[N], uint32_t (&out)[N / 2], int lane, int mask) {
+  const bool up = lane & mask;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i)
+    out[i] = umax16x2(up ? m[i + N / 2] : m[i], __shfl_xor_sync(0xffffffffu, up ? m[i] : m[i + N / 2], mask));
+}
+// The last step: a lane goes on with one of the two.
+FP8MOE_DEV uint32_t halve1(uint32_t m, int lane, int mask) {
+  m = umax16x2(m, __shfl_xor_sync(0xffffffffu, m, mask));
+  return lane & mask ? m >> 16 : m & 0xFFFFu;
+}
+// mx_byte of an upper half
+FP8MOE_DEV uint32_t mx_byte16(uint32_t h, float& mul) { return mx_byte(__uint_as_float(h << 16), mul); }
+
 // Codes and scales along the rows: v's columns are those from `col` of 2F.
 template <bool ALL>
 FP8MOE_DEV void put_rows(const SwigluArgs& a, const Rows& r, uint32_t col, int lane, const uint64_t (&v)[8][CP], RowScales& sc,
                          bool last, uint32_t& top) {
   const int cq = lane & 7;
-  float m[8], m4[4], m2[2], mk[1], mul;
+  float m[8], mul;
+  uint32_t w4[4], w2[2], w1[1];
 #pragma unroll
   for (int i = 0; i < 8; ++i) m[i] = amax3(amax3(0.0f, v[i][0]), v[i][1]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w4[i] = upper2(m[2 * i], m[2 * i + 1]);
   // a row's block is the eight lanes of a row group; a lane ends with row `own`
-  halve<8>(m, m4, lane, 1);
-  halve<4>(m4, m2, lane, 2);
-  halve<2>(m2, mk, lane, 4);
+  halve2<4>(w4, w2, lane, 1);
+  halve2<2>(w2, w1, lane, 2);
   const int own = (cq & 1) * 4 + (cq & 2) + (cq >> 2);
-  const uint32_t b = mx_byte(mk[0], mul), blk = col >> 5;
+  const uint32_t b = mx_byte16(halve1(w1[0], lane, 4), mul), blk = col >> 5;
   top = max(top, b);
   uint8_t* s0 = a.s0 + r.at_s0 + (uint32_t)own * r.step0 + (r.tiled0 ? (blk >> 2) * 512 : blk & ~3u);
   sc.word |= b << (blk & 3) * 8;
@@ -101,9 +124,9 @@ FP8MOE_DEV void put_rows(const SwigluArgs& a, const Rows& r, uint32_t col, int l
   for (int i = 0; i < 8; ++i) {
     const float s = __shfl_sync(0xffffffffu, mul, (lane & ~7) | (i >> 2) | (i & 2) | (i & 1) << 2);
     float f[4];
-    unpk(v[i][0], f[0], f[1]);
-    unpk(v[i][1], f[2], f[3]);
-    if (ALL || i < r.rows) *reinterpret_cast<uint32_t*>(q + wide(2 * r.F, i)) = cvt4(f[0] * s, f[1] * s, f[2] * s, f[3] * s);
+    unpk(mul2(v[i][0], pk(s, s)), f[0], f[1]);
+    unpk(mul2(v[i][1], pk(s, s)), f[2], f[3]);
+    if (ALL || i < r.rows) *reinterpret_cast<uint32_t*>(q + wide(2 * r.F, i)) = cvt4(f[0], f[1], f[2], f[3]);
   }
 }
 
@@ -111,7 +134,7 @@ FP8MOE_DEV void put_rows(const SwigluArgs& a, const Rows& r, uint32_t col, int l
 // row exists).
 FP8MOE_DEV void put_columns(const Rows& r, uint8_t* q1, uint8_t* s1, uint32_t col, int lane, const uint64_t (&v)[8][CP],
                             uint32_t& top) {
-  float m[4], m2[2], mk[1], mul;
+  float m[4], mul;
 #pragma unroll
   for (int p = 0; p < CP; ++p) {
     m[2 * p] = m[2 * p + 1] = 0.0f;
@@ -126,9 +149,10 @@ FP8MOE_DEV void put_columns(const Rows& r, uint8_t* q1, uint8_t* s1, uint32_t co
   }
   // a column's block is the four lanes that differ in the row group; a lane ends
   // with column `own`
-  halve<4>(m, m2, lane, 8);
-  halve<2>(m2, mk, lane, 16);
-  const uint32_t own = (uint32_t)(((lane >> 3) & 1) * 2 + (lane >> 4)), b = mx_byte(mk[0], mul);
+  const uint32_t w2[2] = {upper2(m[0], m[1]), upper2(m[2], m[3])};
+  uint32_t w1[1];
+  halve2<2>(w2, w1, lane, 8);
+  const uint32_t own = (uint32_t)(((lane >> 3) & 1) * 2 + (lane >> 4)), b = mx_byte16(halve1(w1[0], lane, 16), mul);
   top = max(top, b);
   s1[column_scale(r, col, (lane & 7) * 4 + own)] = (uint8_t)b;
   uint8_t* q = q1 + r.at1 + wide(r.M, col);
@@ -155,12 +179,10 @@ FP8MOE_DEV void put_pair(const Rows& r, uint8_t* q1, uint32_t col, int p, int la
   for (int i = 0; i < 8; ++i) unpk(v[i], x[i], y[i]);
 #pragma unroll
   for (int i = 0; i < 8; i += 2) m0 = amax3(m0, x[i], x[i + 1]), m1 = amax3(m1, y[i], y[i + 1]);
-#pragma unroll
-  for (int o = 8; o < 32; o <<= 1) {
-    m0 = nanmax(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-    m1 = nanmax(m1, __shfl_xor_sync(0xffffffffu, m1, o));
-  }
-  const uint32_t b0 = mx_byte(m0, k0), b1 = mx_byte(m1, k1);
+  uint32_t m = upper2(m0, m1);
+  m = umax16x2(m, __shfl_xor_sync(0xffffffffu, m, 8));
+  m = umax16x2(m, __shfl_xor_sync(0xffffffffu, m, 16));
+  const uint32_t b0 = mx_byte16(m & 0xFFFFu, k0), b1 = mx_byte16(m >> 16, k1);
   top = max(top, max(b0, b1));
   uint8_t* q = q1 + r.at1 + wide(r.M, col + 2 * p);
   *reinterpret_cast<uint2*>(q) =
@@ -256,10 +278,7 @@ FP8MOE_DEV uint32_t tiles(const SwigluArgs& a, const Rows& r, uint32_t col, uint
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float gs = power_of_gate(w[i]), us = power_of_up(w[i]);
-        float x, y, z, q;
-        unpk(e4m3x2_f32(t.g[i] >> (16 * p)), x, y);
-        unpk(e4m3x2_f32(t.u[i] >> (16 * p)), z, q);
-        act[i] = ckpt_pair(pk(x * gs, y * gs), pk(z * us, q * us), unpk_bf16(p ? t.d[i].y : t.d[i].x), v[i][p], v2[i][p]);
+        act[i] = ckpt_pair(mul2(e4m3x2_f32(t.g[i] >> (16 * p)), pk(gs, gs)), mul2(e4m3x2_f32(t.u[i] >> (16 * p)), pk(us, us)), unpk_bf16(p ? t.d[i].y : t.d[i].x), v[i][p], v2[i][p]);
       }
       if constexpr (ACT) put_pair(r, a.aq1, col, p, lane, act, mine, top);
     }
