@@ -21,8 +21,8 @@
 // in order after a grid-wide meeting.  The terms of x and of the activation are
 // made once, into the workspace, as the tensor core reads them, and copied to a
 // ring beside the weights'; through registers, as bulk copies queue behind the
-// weights' in flight.  One or two tokens (DIRECT): every CTA makes the terms of its
-// own run on the way to the ring, from x and from the first product's partial
+// weights' in flight.  Where an expert has few pairs, every CTA makes the terms of its
+// own run on the way to the ring instead, from x and from the first product's partial
 // sums, which saves two of the four meetings.  The weights' producer takes no part
 // in the meetings: while the others add, it fills its ring with W2.
 // Measured: one token of 6 experts of 1408 x 2048 18 us (8 of bytes, the rest the way
@@ -96,7 +96,7 @@ struct Plan {
   uint16_t* order;    // [live] pair of each place
   uint16_t* pos;      // [P] place of each pair, or DC_DEAD
   uint16_t* ent_of;   // [live] entry of each place
-  int* num;           // live pairs, entries
+  int* num;           // live pairs, entries, the largest entry's pairs
   FP8MOE_DEV Plan(uint8_t* p, int P, int max_ent) {
     num = (int*)p;
     ent = (uint32_t*)(p + 16);
@@ -140,7 +140,8 @@ FP8MOE_DEV void plan_warp(const DecodeArgs& a, const Plan& pl, int lane) {
     if (head) pl.ent[ent] = (uint32_t)e | (uint32_t)rank << 10 | (uint32_t)min(a.nb, same - before) << 20;
   }
   const int n = __popc(__ballot_sync(0xffffffffu, live));
-  if (lane == 0) pl.num[0] = n, pl.num[1] = __popc(heads);
+  const uint32_t most = __reduce_max_sync(0xffffffffu, live ? (uint32_t)min(a.nb, same) : 0u);
+  if (lane == 0) pl.num[0] = n, pl.num[1] = __popc(heads), pl.num[2] = (int)most;
   __syncwarp();
 }
 
@@ -184,7 +185,7 @@ FP8MOE_DEV void plan_block(const DecodeArgs& a, const Plan& pl, int* scratch) {
       if (lane >= o) v += u;
     }
     tot[lane] = (int)(v - own);
-    if (lane == 31) pl.num[0] = (int)(v >> 16), pl.num[1] = (int)(v & 0xFFFFu);
+    if (lane == 31) pl.num[0] = (int)(v >> 16), pl.num[1] = (int)(v & 0xFFFFu), pl.num[2] = 0;
   }
   __syncthreads();
   for (int p = tid; p < a.P; p += DC_THREADS) {
@@ -203,6 +204,7 @@ FP8MOE_DEV void plan_block(const DecodeArgs& a, const Plan& pl, int* scratch) {
     if (before % a.nb == 0) {
       for (int q = p; q < a.P && after < a.nb; ++q) after += ids[q] == e;
       pl.ent[ent] = (uint32_t)e | (uint32_t)place << 10 | (uint32_t)after << 20;
+      atomicMax(pl.num + 2, after);
     }
   }
   __syncthreads();
@@ -315,7 +317,7 @@ FP8MOE_DEV void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(
 // run at a time, and each leaves its counters one grid further.  (A CTA that gives
 // up still comes.)
 enum { MEET_X = 0, MEET_SUMS, MEET_ACT, MEET_END, DC_MEETS };
-__device__ unsigned long long g_meets[2][DC_MEETS][16];   // two forms of the kernel, with as many meetings each call
+__device__ unsigned long long g_meets[2][DC_MEETS][16];   // of calls with four meetings, and with two
 FP8MOE_DEV uint64_t ld_acquire_gpu(const unsigned long long* p) {
   uint64_t v;
   asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
@@ -407,7 +409,11 @@ struct Terms {
   }
 };
 
-template <bool DIRECT>
+// What the host knows of a call: nothing (the plan decides how terms are made), that
+// entries have few pairs (made on the way), that they have at most two.  (One token: 18.9
+// us if the plan decides, 18.5 as one of few, 17.9.)
+enum { DC_ANY = 0, DC_FEW, DC_TWO };
+template <int FORM>
 __global__ void __launch_bounds__(DC_THREADS, 1)
     k_decode(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2, DecodeArgs a, DecodeSmem L) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -458,7 +464,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
                                    : make_uint4(0, 0, 0, 0);
   };
   uint4 x0 = make_uint4(0, 0, 0, 0);               // the first unit's, on its way while the plan is made
-  if (!DIRECT && (warp < DC_WARP_TMA || warp >= DC_WARP_B)) x0 = x_at(unit0);
+  if (FORM == DC_ANY && (warp < DC_WARP_TMA || warp >= DC_WARP_B)) x0 = x_at(unit0);
   if (a.P <= 32) {
     if (warp == DC_WARP_TMA) plan_warp(a, pl, lane);
     __syncthreads();
@@ -468,6 +474,12 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_s;
   const int nlive = pl.num[0], nent = pl.num[1];
+  // Terms made on the way where entries have few pairs: no more than 8, as a warp of a
+  // team takes two at a time and must not be slower than the weights, and 1.5 on average.
+  // (8 of 256 experts of 2048 x 7168: 23 tokens (1.4 pairs an entry) 918 us against 942;
+  // 6 of 64 of 1408 x 2048: twelve (1.6) 83 and 82, sixteen (1.9) 99 and 92 with a cold
+  // L2, 24 (2.5) 111 and 106.)
+  const bool direct = FORM != DC_ANY || (L.team_log == 1 && pl.num[2] <= 8 && 2 * nlive <= 3 * nent);
   const Stream s1(nent, L.rt[0], L.kp[0], L.grid), s2(nent, L.rt[1], L.kp[1], L.grid);
   using Two = std::integral_constant<int, 2>;     // terms of a bf16 value: the first product's
   using Three = std::integral_constant<int, 3>;   // of an fp32 value: the second's
@@ -476,7 +488,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     // ======================= weights =======================
     // The first fills leave behind this CTA's terms of x: in front of them, what
     // follows them meets its first instructions and loads in a full memory system.
-    if constexpr (!DIRECT) bar_sync(1, DC_JOIN + 32);
+    if (!direct) bar_sync(1, DC_JOIN + 32);
     if (elected()) {
       Slot slot;
       uint32_t i = 0;
@@ -612,14 +624,14 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     // every meeting's count when all have come: the last one's stands still until
     // this CTA has been at the others
     uint64_t meets;
-    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(meets) : "l"(g_meets[DIRECT][MEET_END]));
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(meets) : "l"(g_meets[direct][MEET_END]));
     meets += grid;
     // (`meanwhile`: what the next step can work out without the others' results)
     auto meeting = [&](int i, auto meanwhile) {
       bar_sync(2, DC_JOIN);
-      if (tid == 0) come(g_meets[DIRECT][i]);
+      if (tid == 0) come(g_meets[direct][i]);
       meanwhile();
-      if (tid == 0) came(g_meets[DIRECT][i], meets, a.status, abort_flag);
+      if (tid == 0) came(g_meets[direct][i], meets, a.status, abort_flag);
       bar_sync(2, DC_JOIN);
     };
 
@@ -703,14 +715,16 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       }
       // c is past the run's end: into the next run
     };
-    // The same, made here: a warp a tile, half a warp a pair (entries of at most two),
-    // the next piece's values on their way meanwhile.
+    // The same, made here: a warp a tile, two pairs at a time, half a warp each, the next
+    // two's values on their way meanwhile.
     auto make = [&](auto nt) {
       constexpr int NT = decltype(nt)::value;
       const Stream& s = NT == 2 ? s1 : s2;
       const int K = NT == 2 ? K1 : K2, half = lane >> 4;
+      int pair = 0;         // r and c's piece: the first of the two
       struct Values {
         uint32_t ent;
+        int pair;
         bool in;
         uint4 x;            // of x; or the first two partial sums of gate and up
         float4 q[NT == 2 ? 1 : 4], u[NT == 2 ? 1 : 4];
@@ -718,8 +732,9 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       } next;
       auto fetch = [&]() {
         next.ent = pl.ent[r.ent];
-        const int place = (int)(next.ent >> 10 & 1023u) + half, k = ((r.k + c) * DC_G + rank) * 128 + j16 * 8;
-        next.in = half < (int)(next.ent >> 20) && k < K;
+        next.pair = pair + half;
+        const int place = (int)(next.ent >> 10 & 1023u) + next.pair, k = ((r.k + c) * DC_G + rank) * 128 + j16 * 8;
+        next.in = next.pair < (int)(next.ent >> 20) && k < K;
         if constexpr (NT == 2) {
           next.x = make_uint4(0, 0, 0, 0);
           if (next.in)
@@ -740,12 +755,19 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
           }
         }
       };
-      if (team < L.teams && r.left > 0) fetch();
-      while (team < L.teams && r.left > 0) {
+      bool more = team < L.teams && r.left > 0;
+      if (more) fetch();
+      while (more) {
         const Values now = next;
-        c += L.teams;
-        enter(s);
-        if (r.left > 0) fetch();
+        const int pairs = (int)(now.ent >> 20);
+        pair += 2;
+        if (FORM == DC_TWO || pair >= pairs) {
+          pair = 0;
+          c += L.teams;
+          enter(s);
+        }
+        more = r.left > 0;
+        if (more) fetch();
         float v[8];
         if constexpr (NT == 2) {
           const uint32_t w[4] = {now.x.x, now.x.y, now.x.z, now.x.w};
@@ -775,13 +797,14 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         }
         __syncwarp();
         const Terms<NT> terms(v);
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot.i], slot.turn ^ 1u, abort_flag))) {
+        if ((FORM == DC_TWO || now.pair == half) && !__all_sync(0xffffffffu, mbar_wait(&empty[slot.i], slot.turn ^ 1u, abort_flag))) {
           fail();
           break;
         }
-        const TermTiles tt((int)(now.ent >> 20) * NT);
+        const TermTiles tt(pairs * NT);
         uint8_t* dst = smem + L.b + slot.i * L.b_bytes;
-        if (now.in) terms.put(dst + rank * tt.rows * 128, dst + DC_G * tt.rows * 128 + rank * tt.sf, half * NT, j16);
+        if (now.in) terms.put(dst + rank * tt.rows * 128, dst + DC_G * tt.rows * 128 + rank * tt.sf, now.pair * NT, j16);
+        if (FORM != DC_TWO && now.pair - half + 2 < pairs) continue;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b_full[slot.i]);
@@ -839,7 +862,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
                 (place - (int)(ent >> 10 & 1023u)) * NT, j16);
     };
     const int back = (jt >> 4 & 1) * (int)grid;     // a warp stays together for its shuffles
-    if constexpr (!DIRECT) {
+    if (!direct) {
       for (int u = unit0, units = a.P * kt1; u - back < units; u += unit_step) {
         const uint4 q = u == unit0 ? x0 : x_at(u);
         float v[8] = {bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y), bf16_lo(q.z), bf16_hi(q.z), bf16_lo(q.w), bf16_hi(q.w)};
@@ -852,7 +875,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     }
     if (epi) {
       drain_acc(Two{});
-    } else if constexpr (DIRECT) {
+    } else if (direct) {
       make(Two{});
     } else {
       feed(Two{});
@@ -878,7 +901,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       r = Run(s2, cta);
       enter(s2);
     };
-    if constexpr (DIRECT) {
+    if (direct) {
       meeting(MEET_SUMS, second_run);
     } else {
       meeting(MEET_SUMS, [&] { next = act_of(unit0); });
@@ -899,7 +922,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     }
     if (epi) {
       drain_acc(Three{});
-    } else if constexpr (DIRECT) {
+    } else if (direct) {
       make(Three{});
     } else {
       feed(Three{});
@@ -1054,13 +1077,13 @@ cudaError_t launch_decode(DecodeArgs a, void* workspace, int num_sms, int max_sm
     const cuuint32_t box[3] = {128, 128, 1};
     if (!make_tmap(&tm[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, q[i], 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  // Terms made on the way (entries of two pairs at most, two warps a slot, a tile
-  // each) where a CTA has few pieces and the meetings count: 6 experts of 1408 x 2048
-  // 22.2 us against 25.0, 8 of 2048 x 7168 (70 pieces a CTA) 73.1 and 73.5, 16 of
-  // them (140) 129.7 against 126.2, as the copies keep up with the weights better.
-  const int64_t pieces = a.P * (pieces_of(a.H) * L.rt[0].d + pieces_of(a.F) * L.rt[1].d);
-  const bool direct = a.nb == 2 && 1 << L.team_log == DC_G && pieces <= (int64_t)96 * num_sms;
-  const void* kern = direct ? (const void*)k_decode<true> : (const void*)k_decode<false>;
+  // Up to eight tokens no entry has more than eight pairs; two at most of an expert on
+  // average (6 of 64 experts of 1408 x 2048: four tokens 42.5 us by copies of terms, 39.8
+  // made on the way, eight 70.3 and 66.8; eight tokens' one expert 21 and 26).
+  const bool few = a.T <= 8 && a.P <= 2 * a.E && L.team_log == 1;
+  const void* kern = !few        ? (const void*)k_decode<DC_ANY>
+                     : a.nb == 2 ? (const void*)k_decode<DC_TWO>
+                                 : (const void*)k_decode<DC_FEW>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem - 1024);
   if (e != cudaSuccess) return e;
   void* args[] = {&tm[0], &tm[1], &a, &L};

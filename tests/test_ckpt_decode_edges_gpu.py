@@ -342,13 +342,10 @@ def test_norm_several_rows_a_thread(F, T, H, w32, stream):
 
 # --- few tokens with many choices ----------------------------------------------------------
 
-@pytest.mark.parametrize("T,H,Fd,E,k", [(1, 64, 64, 64, 40), (1, 96, 32, 3, 1024), (2, 96, 64, 48, 30), (2, 32, 160, 1024, 512),
-                                        (24, 64, 96, 5, 4), (25, 64, 96, 5, 4)])
-def test_decode_many_choices(F, T, H, Fd, E, k):
-    """More than 32 pairs in the form for one or two tokens, the same expert often; both
-    sides of the entries' rule.  The sums in float64; the tolerances are those of the
-    other tests of this call."""
-    x, idx, w, w1, s1, w2, s2 = _layer(F, T, H, Fd, E, k, seed=k)
+def _decode_ok(F, args):
+    """The sums in float64; the tolerances are those of the other tests of this call."""
+    x, idx, w, w1, s1, w2, s2 = args
+    (T, H), (E, _, Fd), k = x.shape, w2.shape, idx.shape[1]
     out = F.fp8moe_mxfp8_moe_decode(x, idx, w, w1, s1, w2, s2).double()
     f = 2.0 ** (118 - 127)
     a1, a2 = (m.view(torch.float8_e4m3fn).float().double() * f for m in (w1, w2))
@@ -367,3 +364,32 @@ def test_decode_many_choices(F, T, H, Fd, E, k):
     tol = torch.einsum("te,teh->th", share, dy + (k + 1) * 2.0 ** -24 * y.abs()) + 2.0 ** -8 * ref.abs() + 1e-30
     assert bool(((out - ref).abs() <= tol).all())
     assert F.fp8moe_get_device_status() == 0
+
+
+@pytest.mark.parametrize("T,H,Fd,E,k", [(1, 64, 64, 64, 40), (1, 96, 32, 3, 1024), (2, 96, 64, 48, 30), (2, 32, 160, 1024, 512),
+                                        (24, 64, 96, 5, 4), (25, 64, 96, 5, 4)])
+def test_decode_many_choices(F, T, H, Fd, E, k):
+    """More than 32 pairs of one or two tokens, the same expert often; both sides of the
+    entries' rule."""
+    _decode_ok(F, _layer(F, T, H, Fd, E, k, seed=k))
+
+
+@pytest.mark.parametrize("T,H,Fd,E,k,hot", [(8, 160, 96, 8, 2, 8), (5, 96, 64, 6, 2, 5), (3, 4128, 64, 3, 2, 3), (8, 96, 4128, 16, 4, 7),
+                                            (7, 512, 256, 7, 2, 0), (20, 256, 96, 40, 4, 0), (23, 96, 160, 64, 3, 8),
+                                            (23, 96, 160, 64, 3, 9), (60, 64, 512, 128, 2, 5), (100, 32, 64, 200, 4, 8)])
+def test_decode_entries_of_several(F, T, H, Fd, E, k, hot):
+    """Entries of up to eight pairs whose terms are made on the way, and one pair more."""
+    args = _layer(F, T, H, Fd, E, k, seed=T)
+    # distinct choices, the first of `hot` tokens the same
+    args[1] = torch.rand(T, E, device=DEV)[:, 1:].topk(k, 1)[1].to(I32) + 1
+    args[1][:hot, 0] = 0
+    _decode_ok(F, args)
+    x, idx, w = args[0].clone(), args[1].clone(), args[2].clone()
+    w[T // 2] = 0          # and with a token that takes no part, whatever it holds
+    x[T // 2] = float("nan")
+    out = F.fp8moe_mxfp8_moe_decode(x, idx, w, *args[3:])
+    assert not out[T // 2].any() and bool(torch.isfinite(out.float()).all())
+    same = F.fp8moe_mxfp8_moe_decode(x, idx, w, *args[3:])
+    assert torch.equal(out, same)
+    x[T // 2] = 0
+    _decode_ok(F, [x, idx, w, *args[3:]])
