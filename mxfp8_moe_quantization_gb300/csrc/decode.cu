@@ -26,9 +26,9 @@
 // sums, which saves two of the four meetings.  The weights' producer takes no part
 // in the meetings: while the others add, it fills its ring with W2.
 // Measured: one token of 6 experts of 1408 x 2048 18 us (8 of bytes, the rest the way
-// through two products: 10.4 for a layer of almost no weights), of 8 of 2048 x 7168 65 us =
-// 5.6 TB/s; 23 tokens of 256 such 764 to 800 us = 6.3 to 6.6 TB/s (95 to 99% of a copy's
-// rate), 64 tokens of 16 experts of 8192 x 5120 326 us = 6.3 TB/s.
+// through two products: 10.4 for a layer of almost no weights), of 8 of 2048 x 7168 66 us =
+// 5.5 TB/s; 23 tokens of 256 such 764 us = 6.6 TB/s (99% of a copy's rate), 64 tokens of 16
+// experts of 8192 x 5120 325 us = 6.3 TB/s.
 //   warps 0-3  accumulators to partial sums;  4  weights by TMA;  5  MMA issue;
 //   6  scales to tensor memory;  7-14  terms to shared memory;  all but 4-6  terms
 //   and the final sums.
