@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
 // below the bf16 form's, but the codes' unpacking (a conversion to fp16 pairs, two to
 // fp32, a product by the block's power of two) comes on top of its instructions, and
 // from about 20 an element on it is issue and latency that bound: 16384 x 5120 with
-// dh 99 us = 5.9 TB/s (89% of a copy's rate), 16384 x 7168 135 us = 6.1, 20001 x 4096
+// dh 99 us = 5.9 TB/s (89% of a copy's rate), 16384 x 7168 131 us = 6.3, 20001 x 4096
 // 100 us = 5.7, 65536 x 512 44 us = 5.4.
 template <int V, int R>
 constexpr int norm_ck_threads() { return R == 4 ? 256 : R == 2 || V == 4 ? 512 : 640; }
@@ -590,25 +590,29 @@ __global__ void __launch_bounds__(norm_ck_threads<V, R>(), norm_ck_ctas<V, R>())
     if constexpr (KEEP_W32) wf[i] = t + i * tpr < nch ? load_w8<W32>(a.w, t + i * tpr) : Vec8{};
   }
   // the rows' rstd and scales are loaded one block ahead (rows past T: 0, and nothing stored)
-  int64_t row = (int64_t)blockIdx.x * block + group * R;
-  const int64_t step = (int64_t)gridDim.x * block;
+  uint32_t row = blockIdx.x * block + group * R;
+  const uint32_t T = (uint32_t)a.T, step = gridDim.x * block;
+  const float* prstd = a.rstd + row;
+  const uint8_t* phs = a.hs + (int64_t)row * ns + (t >> 2);
+  uint16_t* pdx = a.dx + (int64_t)row * a.H + t * 8;
   float rstd_next[R];
   uint32_t sc_next[R][V];
-  auto ahead = [&](int64_t r0) {
+  auto ahead = [&](uint32_t r0) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const bool on = r0 + r < a.T;
-      rstd_next[r] = on ? __ldg(a.rstd + r0 + r) : 0.0f;
-      const uint8_t* s = a.hs + (r0 + r) * ns + (t >> 2);
+      const bool on = r0 + r < T;
+      rstd_next[r] = on ? __ldg(prstd + r) : 0.0f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) sc_next[r][i] = on && t + i * tpr < nch ? (uint32_t)__ldg(s + i * (tpr >> 2)) : 0u;
+      for (int i = 0; i < V; ++i) sc_next[r][i] = on && t + i * tpr < nch ? (uint32_t)__ldg(phs + r * ns + i * (tpr >> 2)) : 0u;
     }
+    prstd += step;
+    phs += (int64_t)step * ns;
   };
   ahead(row);
   __syncthreads();
   int s = 0, par = 0;
   uint32_t phase = 0;
-  for (int b = blockIdx.x; b < blocks; b += gridDim.x, row += step) {
+  for (int b = blockIdx.x; b < blocks; b += gridDim.x, row += step, pdx += (int64_t)step * a.H) {
     // of a row's chunk: 2^e and 2^e rstd
     float rstd[R], xs[R][V];
 #pragma unroll
@@ -633,7 +637,7 @@ __global__ void __launch_bounds__(norm_ck_threads<V, R>(), norm_ck_ctas<V, R>())
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int ch = t + i * tpr;
-        if (ch >= nch || row + r >= a.T) continue;
+        if (ch >= nch || row + r >= T) continue;
         const uint4 dq = *reinterpret_cast<const uint4*>(src + r * row_bytes + ch * 16);
         const Vec8 d = unpack8(dq);
         mx_unpack8(*reinterpret_cast<const uint2*>(src_h + r * (row_bytes / 2) + ch * 8), xs[r][i], xh[r][i].p);
@@ -679,7 +683,6 @@ __global__ void __launch_bounds__(norm_ck_threads<V, R>(), norm_ck_ctas<V, R>())
         for (int r = 0; r < R; ++r) dot[r] += p[i * R + r];
     }
     par ^= 1;
-    uint16_t* pdx = a.dx + row * a.H;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       // -dot / H, rounded once: the quotient by the reciprocal and one step of
@@ -690,12 +693,12 @@ __global__ void __launch_bounds__(norm_ck_threads<V, R>(), norm_ck_ctas<V, R>())
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int ch = t + i * tpr;
-        if (ch >= nch || row + r >= a.T) continue;
+        if (ch >= nch || row + r >= T) continue;
         const Vec8 sv = a.dh ? unpack8(*reinterpret_cast<const uint4*>(src + ten_bytes + r * row_bytes + ch * 16)) : Vec8{};
         Vec8 o;
 #pragma unroll
         for (int j = 0; j < 4; ++j) o.p[j] = fma2(rstd2, fma2(xh[r][i].p[j], c2, g[r][i].p[j]), sv.p[j]);
-        *reinterpret_cast<uint4*>(pdx + r * a.H + ch * 8) = pack8(o);
+        *reinterpret_cast<uint4*>(pdx + r * a.H + i * tpr * 8) = pack8(o);
       }
     }
     if (++s == stages) {
@@ -864,7 +867,7 @@ cudaError_t launch_bwd_ckpt(NormBwdArgs a, float* dw, int num_sms, int max_smem,
   int wpr = nch > NORM_MAX_CHUNKS ? 16 : (nch + 32 * v - 1) / (32 * v);
   int groups = wpr >= 8 ? 1 : 8 / wpr;
   // the ring as the bf16 form's, and as deep as fits where registers leave room for
-  // one CTA only (16384 x 7168 without dh: 118 us, 147 with half the memory)
+  // one CTA only (16384 x 7168 without dh: 121 us, 147 with half the memory)
   const int64_t budget = max_smem - 2048;
   const int64_t slot = (int64_t)a.H * (a.dh ? 5 : 3) * groups * rows;
   const int64_t room = budget / (wpr * groups > (rows == 1 && v == 2 ? 10 : 8) ? 1 : 2);
