@@ -646,18 +646,19 @@ fp8moe_status fp8moe_route_weight_grad_ckpt(const void* dout, const void* yq, co
  *          bf16 weights, or fp8moe_mxfp8_quantize_dim0 and the swizzle
  * w2       [E, H, F], w2_scale likewise
  * out      [T, H] bf16, dense; overlaps no input
- * Sums in fp32, in an order that hangs on the routing of the whole batch; x
- * counts with all its digits and the activation to 2^-12 of itself: the output
- * is rounded once.  The same call gives the
- * same bits.  A value of x or of the activation that is not finite makes its
- * token's row NaN, a NaN weight those of the tokens that chose its expert; no
- * other row.
+ * Sums in fp32, in an order that hangs on the routing of the whole batch; the
+ * output is rounded once.  The same call gives the same bits.  The products take x and the
+ * activation in blocks of 32 along a row: x exactly from 2^-14 of its block's
+ * largest value on and to 2^-22 of that largest below, the activation to 2^-19
+ * of itself or 2^-32 of its block's largest, whichever is more.  A value of x or
+ * of the activation that is not finite makes its token's row NaN, a NaN weight
+ * those of the tokens that chose its expert; no other row.
  * workspace: caller-owned, fp8moe_mxfp8_moe_decode_workspace_bytes bytes (-1 for
  * sizes that are refused), 16-byte aligned, of no use after the call.
  * T * k <= FP8MOE_DECODE_MAX_PAIRS (more: the grouped products), 1 <= E <=
  * FP8MOE_MAX_GROUPS, H and F multiples of 32 up to 2^20, less where the weights
  * come to some 10^7 pieces of 32 KB.  A reading of an expert serves T of its
- * choices up to 24 tokens, beyond that 24, 32 or 64 as T * k / E grows; an expert
+ * choices up to 20 tokens, beyond that 20, 32 or 64 as T * k / E grows; an expert
  * with more is read again.  One cooperative launch of a CTA per SM (at most 160):
  * it starts once every SM can take one.  A wait inside it that exceeds its limit
  * sets FP8MOE_ERR_TIMEOUT in the device status.

@@ -8,11 +8,15 @@
 // expert, straight from HBM to shared memory to tcgen05.mma, never converted),
 // and the tokens its N operand.
 //
-// The tokens keep all their digits.  In a block of 32 values scaled so that the
+// The tokens keep their digits.  In a block of 32 values scaled so that the
 // largest lies in [128, 256), the nearest e4m3 value leaves a rest of at most 8,
-// which times 2^5 is again such a block, with its own scale: a bf16 value is two
-// such terms exactly (8 bits, four and four), an fp32 value three to 2^-13.  The
-// terms are further columns of N, where the tensor core has room: N is at least
+// which times 2^5 is again such a block, with its own scale: a term has five bits
+// of a value, down to a last place of 2^-9.  Two hold a bf16 value exactly from 2^-14 of its
+// block's largest on, and what is smaller to 2^-22 of that largest; four hold an fp32
+// value to 2^-19 of itself, or 2^-32 of the largest.  (With three, to 2^-14, one of a
+// hundred outputs was the neighbour of the bf16 number that it should be; with four one
+// of a thousand, as with five: the order of the sums.)
+// The terms are further columns of N, where the tensor core has room: N is at least
 // 16, and the weights' arrival leaves it idle most of the time.
 //
 // Both products are one stream of 32 KB pieces (128 rows x 256 of K) over all
@@ -53,6 +57,7 @@ constexpr int DC_JOIN = DC_THREADS - 96;  // threads that make terms and add par
 constexpr int DC_G = 2;                   // tiles of 128 x 128 in a piece
 constexpr int DC_TILE = 128 * 128, DC_A_BYTES = DC_G * DC_TILE;
 constexpr int DC_MAX_SLOTS = 6;
+constexpr int X_TERMS = 2, ACT_TERMS = 4;   // of a value of x, of the activation
 constexpr int DC_DEAD = 0xFFFF;
 
 __host__ __device__ constexpr int up16(int v) { return (v + 15) / 16 * 16; }
@@ -73,7 +78,7 @@ struct Div {
 struct DecodeSmem {
   int slots, b_bytes;
   int team_log, teams;                     // 2^team_log warps fill a slot of terms together
-  int acc;                                 // tensor memory columns of an accumulator
+  int acc, accs;                           // tensor memory columns of an accumulator; accumulators
   int sfa, b, bars, plan, total;
   // tiles and pieces of the products' K, tiles of their rows; the grid; H / 4; choices
   Div kt[2], kp[2], rt[2], grid, quads, k;
@@ -375,8 +380,9 @@ struct Terms {
       asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(u));
     }
     const uint32_t field = (__float_as_uint(m) >> 23) & 0xFFu;
-    // (blocks below 2^-110 are not scaled all the way up: the last term's byte stays above 0)
-    const uint32_t ef = field < 17u ? 17u : field;
+    // (the smallest blocks are not scaled all the way up: the last term's byte is not below 0)
+    constexpr uint32_t LEAST = 7 + 5 * (NT - 1);
+    const uint32_t ef = field < LEAST ? LEAST : field;
     finite = field != 255u;
     byte = ef - 7u;
     const float mul = __uint_as_float((261u - ef) << 23);
@@ -481,8 +487,8 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   // L2, 24 (2.5) 111 and 106.)
   const bool direct = FORM != DC_ANY || (L.team_log == 1 && pl.num[2] <= 8 && 2 * nlive <= 3 * nent);
   const Stream s1(nent, L.rt[0], L.kp[0], L.grid), s2(nent, L.rt[1], L.kp[1], L.grid);
-  using Two = std::integral_constant<int, 2>;     // terms of a bf16 value: the first product's
-  using Three = std::integral_constant<int, 3>;   // of an fp32 value: the second's
+  using First = std::integral_constant<int, X_TERMS>;      // the products, by their terms
+  using Second = std::integral_constant<int, ACT_TERMS>;
 
   if (warp == DC_WARP_TMA) {
     // ======================= weights =======================
@@ -536,7 +542,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         const int kt = ph ? kt2 : kt1;
         const int tail = ((ph ? K2 : K1) / 32 - 1) % 4 + 1;   // blocks of a row's last tile
         for (Run r(s, cta); r.left > 0 && ok; r.next(s)) {
-          const TermTiles tt((int)(pl.ent[r.ent] >> 20) * (ph ? 3 : 2));
+          const TermTiles tt((int)(pl.ent[r.ent] >> 20) * (ph ? ACT_TERMS : X_TERMS));
           const int cols = up16(tt.rows);
           const uint32_t id = (uint32_t)(cols >> 3) << 17 | 1u << 23 | 8u << 24, d = tmem + acc.i * L.acc;
           if (!mbar_wait(&acc_empty[acc.i], acc.turn ^ 1u, abort_flag)) ok = false;
@@ -553,7 +559,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
             for (int g = 0; g < DC_G; ++g) {
               const int left = kt - (r.k + c) * DC_G - g;   // tiles of the row from this one on
               if (left <= 0) break;
-              const uint32_t sf = tmem + 2 * L.acc + (slot.i * DC_G + g) * 12;
+              const uint32_t sf = tmem + L.accs * L.acc + (slot.i * DC_G + g) * 12;
               const uint64_t ad = ad0 + ((uint32_t)(slot.i * DC_A_BYTES + g * DC_TILE) >> 4);
               const uint64_t bd = bd0 + ((at_b + (uint32_t)(g * tt.rows * 128)) >> 4);
               auto block = [&](int k, uint32_t plus) {
@@ -573,7 +579,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
           }
           if (!ok) break;
           tc_commit(&acc_full[acc.i]);
-          acc.step(1, 2);
+          acc.step(1, L.accs);
         }
       }
       if (!ok) fail();
@@ -594,7 +600,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         const Stream& s = ph ? s2 : s1;
         const int kt = ph ? kt2 : kt1;
         for (Run r(s, cta); r.left > 0 && ok; r.next(s)) {
-          const TermTiles tt((int)(pl.ent[r.ent] >> 20) * (ph ? 3 : 2));
+          const TermTiles tt((int)(pl.ent[r.ent] >> 20) * (ph ? ACT_TERMS : X_TERMS));
           for (int c = 0; c < r.n; ++c) {
             if (!mbar_wait(&a_full[slot.i], slot.turn, abort_flag) || !mbar_wait(&b_full[slot.i], slot.turn, abort_flag)) {
               ok = false;
@@ -604,7 +610,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
 #pragma unroll
             for (int g = 0; g < DC_G; ++g) {
               if ((r.k + c) * DC_G + g >= kt) break;
-              const uint32_t sf = tmem + 2 * L.acc + (slot.i * DC_G + g) * 12;
+              const uint32_t sf = tmem + L.accs * L.acc + (slot.i * DC_G + g) * 12;
               const uint64_t sfb = sfb0 + ((uint32_t)(slot.i * L.b_bytes + DC_G * tt.rows * 128 + g * tt.sf) >> 4);
               cp_scales(sf, sfa0 + (uint32_t)((slot.i * DC_G + g) * 32));
               cp_scales(sf + 4, sfb);
@@ -684,7 +690,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     if (!epi) enter(s1);
     auto feed = [&](auto nt) {
       constexpr int NT = decltype(nt)::value;
-      const Stream& s = NT == 2 ? s1 : s2;
+      const Stream& s = NT == X_TERMS ? s1 : s2;
       for (; team < L.teams && r.left > 0; c += L.teams, slot.step(L.teams, L.slots), enter(s)) {
         const uint32_t ent = pl.ent[r.ent];
         const TermTiles tt((int)(ent >> 20) * NT);
@@ -719,15 +725,15 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     // two's values on their way meanwhile.
     auto make = [&](auto nt) {
       constexpr int NT = decltype(nt)::value;
-      const Stream& s = NT == 2 ? s1 : s2;
-      const int K = NT == 2 ? K1 : K2, half = lane >> 4;
+      const Stream& s = NT == X_TERMS ? s1 : s2;
+      const int K = NT == X_TERMS ? K1 : K2, half = lane >> 4;
       int pair = 0;         // r and c's piece: the first of the two
       struct Values {
         uint32_t ent;
         int pair;
         bool in;
         uint4 x;            // of x; or the first two partial sums of gate and up
-        float4 q[NT == 2 ? 1 : 4], u[NT == 2 ? 1 : 4];
+        float4 q[NT == X_TERMS ? 1 : 4], u[NT == X_TERMS ? 1 : 4];
         Parts g, y;
       } next;
       auto fetch = [&]() {
@@ -735,7 +741,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         next.pair = pair + half;
         const int place = (int)(next.ent >> 10 & 1023u) + next.pair, k = ((r.k + c) * DC_G + rank) * 128 + j16 * 8;
         next.in = next.pair < (int)(next.ent >> 20) && k < K;
-        if constexpr (NT == 2) {
+        if constexpr (NT == X_TERMS) {
           next.x = make_uint4(0, 0, 0, 0);
           if (next.in)
             next.x = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)L.k.quot(pl.order[place]) * a.ldx + k));
@@ -769,7 +775,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         more = r.left > 0;
         if (more) fetch();
         float v[8];
-        if constexpr (NT == 2) {
+        if constexpr (NT == X_TERMS) {
           const uint32_t w[4] = {now.x.x, now.x.y, now.x.z, now.x.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
@@ -815,9 +821,9 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
     Slot acc;
     auto drain_acc = [&](auto nt) {
       constexpr int NT = decltype(nt)::value;
-      const Stream& s = NT == 2 ? s1 : s2;
-      const int R = NT == 2 ? R1 : R2;
-      float* part = NT == 2 ? a.part1 : a.part2;
+      const Stream& s = NT == X_TERMS ? s1 : s2;
+      const int R = NT == X_TERMS ? R1 : R2;
+      float* part = NT == X_TERMS ? a.part1 : a.part2;
       for (Run r(s, cta); r.left > 0; r.next(s)) {
         const uint32_t ent = pl.ent[r.ent];
         const int first = (int)(ent >> 10 & 1023u), pairs = (int)(ent >> 20);
@@ -831,7 +837,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         tc_fence_after();
         const uint32_t src = tmem + acc.i * L.acc + ((uint32_t)(warp * 32) << 16);
         for (int i0 = 0; i0 < pairs; i0 += 8) {
-          uint32_t q[24];
+          uint32_t q[8 * NT];
 #pragma unroll
           for (int c = 0; c < NT; ++c) tmem_ld8(src + i0 * NT + c * 8, *reinterpret_cast<uint32_t(*)[8]>(q + c * 8));
           tmem_ld_wait();
@@ -848,7 +854,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
             if (i0 + i < pairs && row < R) dst[(int64_t)(i0 + i) * R] = v;
           }
         }
-        acc.step(1, 2);
+        acc.step(1, L.accs);
       }
     };
     // ======================= terms into the workspace =======================
@@ -866,7 +872,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       for (int u = unit0, units = a.P * kt1; u - back < units; u += unit_step) {
         const uint4 q = u == unit0 ? x0 : x_at(u);
         float v[8] = {bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y), bf16_lo(q.z), bf16_hi(q.z), bf16_lo(q.w), bf16_hi(q.w)};
-        const Terms<2> terms(v);
+        const Terms<X_TERMS> terms(v);
         const int p = (int)L.kt[0].quot(u), c = u - p * kt1, place = u < units ? pl.pos[p] : DC_DEAD;
         if (place != DC_DEAD && c * 128 + j16 * 8 < K1) put(terms, place, c, s1.kp.d);
       }
@@ -874,11 +880,11 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       meeting(MEET_X, [] {});
     }
     if (epi) {
-      drain_acc(Two{});
+      drain_acc(First{});
     } else if (direct) {
-      make(Two{});
+      make(First{});
     } else {
-      feed(Two{});
+      feed(First{});
     }
     // the activation, a unit a pair's tile
     struct Act {
@@ -914,18 +920,18 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
         float v[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) act_of_sums(gs + 2 * i, us + 2 * i, v + 2 * i);
-        const Terms<3> terms(v);
+        const Terms<ACT_TERMS> terms(v);
         if (next.in) put(terms, next.place, next.c, s2.kp.d);
         if (u + unit_step - back < units) next = act_of(u + unit_step);
       }
       meeting(MEET_ACT, second_run);
     }
     if (epi) {
-      drain_acc(Three{});
+      drain_acc(Second{});
     } else if (direct) {
-      make(Three{});
+      make(Second{});
     } else {
-      feed(Three{});
+      feed(Second{});
     }
     // the weighted sum over a token's experts, four neighbouring columns a thread,
     // runs of eight threads' a CTA in turn
@@ -981,12 +987,14 @@ int64_t most_parts(int64_t ents, int64_t rt, int64_t kt) {
   return p < kt ? p : kt;
 }
 // Pairs of an entry, that is, of one reading of an expert: its terms have to fit a
-// ring slot, and larger slots leave room for fewer: up to 24 pairs four, up to 32
-// three.  T, which is enough where a token's choices differ, as long as there is
-// room for four; beyond that room for more than most experts get.
+// ring slot, and larger slots leave room for fewer: up to 20 pairs four, up to 32
+// three, 64 (which N has room for) two.  T, which is enough where a token's choices
+// differ, as long as there is room for four; beyond that room for more than most experts
+// get.  (23 tokens of 8 of 256 experts of 2048 x 7168: 812 us with three slots for up to 24
+// pairs, 733 with four for 20; 64 of 1 of 16 of 8192 x 5120 340 and 328.)
 int entry_pairs(int64_t T, int64_t k, int64_t E) {
   const int64_t each = T * k / E;   // pairs an expert gets on average
-  return T < 2 ? 2 : T <= 24 ? (int)T : each <= 14 ? 24 : each <= 24 ? 32 : 64;
+  return T < 2 ? 2 : T <= 20 ? (int)T : each <= 12 ? 20 : each <= 24 ? 32 : 64;
 }
 
 // floats of the partial sums [parts][live pairs][R]: the most over any number of live pairs
@@ -1004,16 +1012,16 @@ int64_t part_floats(int64_t P, int64_t nb, int64_t R, int64_t K) {
 DecodeSmem layout(int P, int nb, int max_ent, int max_smem) {
   DecodeSmem L{};
   // (up to 8 rows that no term fills are read behind a tile, up to 512 bytes behind its scales)
-  L.b_bytes = (TermTiles(3 * nb).bytes() + 1023) / 1024 * 1024;
-  // (columns of N; and the drain reads eight pairs' at a time)
-  L.acc = 3 * ((nb + 7) / 8 * 8);
-  if (L.acc < up16(TermTiles(3 * nb).rows)) L.acc = up16(TermTiles(3 * nb).rows);
+  L.b_bytes = (TermTiles(ACT_TERMS * nb).bytes() + 1023) / 1024 * 1024;
+  L.acc = ACT_TERMS * ((nb + 7) / 8 * 8);   // (the drain reads eight pairs' columns at a time)
   const int plan = 16 + max_ent * 4 + P * 10;
   const int bars = 8 * (4 * DC_MAX_SLOTS + 8);
   const int fixed = 1024 + bars + plan + 64;
   // 1024 to align the rings, 1024 for what is static
   L.slots = (max_smem - 2048 - fixed) / (DC_A_BYTES + DC_G * 512 + L.b_bytes);
   if (L.slots > DC_MAX_SLOTS) L.slots = DC_MAX_SLOTS;
+  // (entries of 64 pairs fill half of tensor memory: no second accumulator)
+  L.accs = 2 * L.acc + 12 * DC_G * L.slots <= 512 ? 2 : 1;
   L.team_log = L.slots >= 3 ? 1 : 2;
   L.teams = (DC_BWARPS >> L.team_log) < L.slots ? DC_BWARPS >> L.team_log : L.slots;
   L.b = L.slots * DC_A_BYTES;
@@ -1042,7 +1050,7 @@ struct DecodeSpace {
 static DecodeSpace space_of(int64_t T, int64_t k, int64_t E, int64_t H, int64_t F) {
   const int64_t P = T * k, nb = entry_pairs(T, k, E), ents = max_entries(P, E, nb);
   auto terms = [&](int64_t K, int64_t nt) { return pieces_of(K) * DC_G * ((nt * P + 7 * ents) * 128 + 1024 * ents); };
-  const int64_t t1 = terms(H, 2), t2 = terms(F, 3);
+  const int64_t t1 = terms(H, X_TERMS), t2 = terms(F, ACT_TERMS);
   return {part_floats(P, nb, 2 * F, H) * (int64_t)sizeof(float), part_floats(P, nb, H, F) * (int64_t)sizeof(float),
           t1 > t2 ? t1 : t2};
 }
@@ -1057,7 +1065,7 @@ cudaError_t launch_decode(DecodeArgs a, void* workspace, int num_sms, int max_sm
   a.nb = entry_pairs(a.T, a.k, a.E);
   a.max_ent = (int)max_entries(a.P, a.E, a.nb);
   DecodeSmem L = layout(a.P, a.nb, a.max_ent, max_smem);
-  if (num_sms > DECODE_MAX_CTAS || L.slots < 2 || 2 * L.acc + 12 * DC_G * L.slots > 512 ||
+  if (num_sms > DECODE_MAX_CTAS || L.slots < 2 || L.accs * L.acc + 12 * DC_G * L.slots > 512 ||
       (a.P > 32 && (a.E + a.P + 64) * 4 > L.slots * L.b_bytes))
     return cudaErrorNotSupported;
   const DecodeSpace w = space_of(a.T, a.k, a.E, a.H, a.F);

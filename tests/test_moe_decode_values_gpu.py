@@ -1,0 +1,77 @@
+"""What the few tokens' expert layer keeps of its values between the products, on
+layers whose exact results are known.
+
+The activation goes to the second product in four e4m3 terms of five bits, each off
+by at most half a step: 2^-19 of itself; its sigmoid, a product and an fp32 sum of
+two products add less than 2^-20."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def F():
+    from mxfp8_moe_quantization_gb300 import build as B
+    B.build()
+    import mxfp8_moe_quantization_gb300 as m
+    return m
+
+
+def _codes(v):
+    """e4m3 codes of values that are e4m3 numbers."""
+    q = v.float().to(torch.float8_e4m3fn)
+    assert torch.equal(q.float(), v.float())
+    return q.view(torch.uint8).to(DEV)
+
+
+def _ones(F, E, R, K):
+    return torch.full((F.fp8moe_swizzled_scales_bytes(E, R, K // 32, 0, F.NO_GROUPS),), 127, dtype=torch.uint8, device=DEV)
+
+
+def _layer(F, x, idx, w1, w2):
+    """The call on E times the same expert, all scales and weights 1."""
+    E = int(idx.max()) + 1
+    many = lambda m: _codes(m).expand(E, *m.shape).contiguous()
+    out = F.fp8moe_mxfp8_moe_decode(x.to(DEV), idx.to(DEV), torch.ones(idx.shape, device=DEV), many(w1), _ones(F, E, *w1.shape),
+                                    many(w2), _ones(F, E, *w2.shape))
+    assert F.fp8moe_get_device_status() == 0
+    return out.double().cpu().numpy()
+
+
+def _choices(T, E):
+    idx = torch.arange(T, dtype=torch.int32)[:, None] % E
+    idx[-1] = E - 1
+    return idx
+
+
+@pytest.mark.parametrize("T,E", [(1, 1), (1, 3), (6, 4), (8, 1), (23, 4), (40, 4), (100, 4), (200, 4)])
+def test_digits_of_the_activation(F, T, E):
+    """Outputs are differences of two neighbouring activations that agree in their
+    first digits.  Gates are 64, whose sigmoid is 1 to 2^-92; up is a sum of integers
+    below 2^24, exact in any order."""
+    g = torch.Generator().manual_seed(T + E)
+    H, Fd = 64, 64
+    x = torch.zeros(T, H)
+    x[:, 0] = 64.0
+    x[:, 32:63] = torch.randint(-255, 256, (T, 31), generator=g).float()
+    x[:, 63] = torch.randint(-127, 128, (T,), generator=g).float()
+    w1 = torch.zeros(2 * Fd, H)
+    w1[:Fd, 0] = 1.0
+    up = torch.randint(8, 16, (Fd // 2, 31), generator=g) * 2 ** torch.randint(0, 5, (Fd // 2, 31), generator=g)
+    up = up * (1 - 2 * torch.randint(0, 2, up.shape, generator=g))
+    w1[Fd::2, 32:63] = w1[Fd + 1::2, 32:63] = up.float()
+    w1[Fd + 1::2, 63] = 1.0
+    w2 = torch.zeros(H, Fd)
+    pair = torch.arange(H) % (Fd // 2)
+    w2[torch.arange(H), 2 * pair], w2[torch.arange(H), 2 * pair + 1] = -1.0, 1.0
+    out = _layer(F, x.to(BF16), _choices(T, E), w1, w2)
+    a = 64.0 * (x.double() @ w1[Fd:].double().t()).numpy()
+    ref = np.broadcast_to(64.0 * x[:, 63:].double().numpy(), out.shape)
+    first, second = np.abs(a)[:, 2 * pair], np.abs(a)[:, 2 * pair + 1]
+    # the terms of both, and the bf16 output's rounding
+    tol = 2.0 ** -18 * (first + second)
+    assert np.all(np.abs(out - ref) <= tol + 2.0 ** -8 * (np.abs(ref) + tol))
