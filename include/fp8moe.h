@@ -650,7 +650,8 @@ fp8moe_status fp8moe_route_weight_grad_ckpt(const void* dout, const void* yq, co
  * output is rounded once.  The same call gives the same bits.  The products take x and the
  * activation in blocks of 32 along a row: x exactly from 2^-14 of its block's
  * largest value on and to 2^-22 of that largest below, the activation to 2^-19
- * of itself or 2^-32 of its block's largest, whichever is more.  A value of x or
+ * of itself (2^-15 where its gate is below -80) or 2^-32 of its block's largest,
+ * whichever is more.  A value of x or
  * of the activation that is not finite makes its token's row NaN, a NaN weight
  * those of the tokens that chose its expert; no other row.
  * workspace: caller-owned, fp8moe_mxfp8_moe_decode_workspace_bytes bytes (-1 for

@@ -354,12 +354,22 @@ FP8MOE_DEV float2 e4m3x2_value(uint32_t c) {
   return v;
 }
 
-// silu(g) u of two sums each.  The sigmoid of gates beyond +-88 is that of 88: 1, and
-// below 2^-126.  (Packed and without branches: eight divisions and expf in a row took
-// 1.5 us of a token's way, most of it to fetch their instructions.)
+// silu(g) u of two sums each.  Below -80 the sigmoid is that of -80 times e^(g + 80), as
+// two factors of half the exponent: they and every product on the way are normal as
+// long as the result can differ from 0 (|u| < 2^128: down to g = -195, where the rounded
+// exponents leave 2^-15 of it), and no product is beyond fp32 that the result is not
+// (-300 stands for every gate below).  (Packed and without branches: eight divisions and
+// expf in a row took 1.5 us of a token's way, most of it to fetch their instructions.)
 FP8MOE_DEV void act_of_sums(const float* g, const float* u, float* v) {
-  auto near = [](float x) { return fminf(fmaxf(x, -88.0f), 88.0f); };
-  unpk(mul2(mul2(pk(g[0], g[1]), sigmoid2(pk(near(g[0]), near(g[1])))), pk(u[0], u[1])), v[0], v[1]);
+  auto near = [](float x) { return fminf(fmaxf(x, -80.0f), 80.0f); };
+  auto half = [](float x) {   // e^((x + 80) / 2), at most 1
+    float h;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(fminf(x + 80.0f, 0.0f) * 0.72134752f));
+    return h;
+  };
+  const uint64_t f = pk(half(g[0]), half(g[1]));
+  const uint64_t s = mul2(pk(nanmax(g[0], -300.0f), nanmax(g[1], -300.0f)), sigmoid2(pk(near(g[0]), near(g[1]))));
+  unpk(mul2(mul2(mul2(s, pk(u[0], u[1])), f), f), v[0], v[1]);
 }
 
 // NT terms of eight neighbouring values of a row, four lanes a block: codes, and

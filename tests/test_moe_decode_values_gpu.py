@@ -75,3 +75,31 @@ def test_digits_of_the_activation(F, T, E):
     # the terms of both, and the bf16 output's rounding
     tol = 2.0 ** -18 * (first + second)
     assert np.all(np.abs(out - ref) <= tol + 2.0 ** -8 * (np.abs(ref) + tol))
+
+
+GATES = [0.0, 1.0, -1.0, 30.0, -30.0, 90.0, -79.5, -80.0, -80.5, -87.0, -88.0, -88.5, -89.0, -92.0, -100.0, -120.0, -150.0, -180.0,
+         -194.0, -200.0, -260.0, -300.0, -1e4, -1e20, -3e38]
+
+
+@pytest.mark.parametrize("up", [1.0, -3.5, 1e19, 2.0 ** 100, 3e38])
+@pytest.mark.parametrize("T", [1, 8, 0])
+def test_far_gates(F, up, T):
+    """silu(g) u for gates to both sides of where the sigmoid leaves fp32: 2^-15 of
+    itself below -80, where the exponent's argument is rounded; what each of the four
+    terms has below fp32's normal numbers may be lost."""
+    gates = torch.tensor(GATES).to(BF16)
+    gates = gates[gates * up < 1e38] if up > 0 else gates   # (a product beyond fp32 is not a number)
+    H, Fd = 64, 32
+    w1, w2 = torch.zeros(2 * Fd, H), torch.zeros(H, Fd)
+    w1[:Fd, 0], w1[Fd:, 32] = 1.0, 1.0
+    w2[torch.arange(H), torch.arange(H) % Fd] = 1.0
+    for part in gates.split(T or len(gates)):
+        x = torch.zeros(len(part), H)
+        x[:, 0], x[:, 32] = part.float(), up
+        x = x.to(BF16)
+        out = _layer(F, x, _choices(len(part), 4), w1, w2)
+        g, u = x[:, 0].double().numpy(), x[:, 32].double().numpy()
+        with np.errstate(over="ignore"):
+            ref = (g / (1.0 + np.exp(-g)) * u)[:, None]
+        tol = 2.0 ** -15 * np.abs(ref) + 2.0 ** -124
+        assert np.all(np.abs(out - ref) <= tol + 2.0 ** -8 * (np.abs(ref) + tol)), (part, out[:, 0], ref)
