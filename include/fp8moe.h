@@ -611,8 +611,7 @@ fp8moe_status fp8moe_swiglu_bwd(const void* dout, const void* h, int64_t ldh, in
  * fp8moe_add_rmsnorm_bwd_ckpt: fp8moe_add_rmsnorm_bwd with hq [T, H] and hs
  *   [T, H/32] in place of h; H % 32 == 0; the same workspace.
  * fp8moe_route_weight_grad_ckpt: fp8moe_route_weight_grad_bounded with the expert
- *   outputs yq [rows, N] and ys [rows, N/32] in place of y; N % 32 == 0.  dout times a
- *   code (at most 448) has to be within fp32, before the scale.
+ *   outputs yq [rows, N] and ys [rows, N/32] in place of y; N % 32 == 0.
  * Codes 16-byte aligned; an output overlaps no input, but for the norm's dx as in
  * fp8moe_add_rmsnorm_bwd.
  * ------------------------------------------------------------------------ */

@@ -740,6 +740,32 @@ __global__ void __launch_bounds__(256, 4) k_route_weight_grad(const uint16_t* __
 // 1.03 bytes a value of y: 4096 x 7168 x 8 53 us = 5.7 TB/s (85% of a copy's rate; its
 // 2048 CTAs are four and a half rounds, and the warps wait for memory), 8189 x 2048 x 6
 // 26 us (79%); whole CTAs a token, or persistent ones, are no faster.
+//
+// Sums that are not finite are taken once more in 64 bits: dout times a code (up to 448)
+// may be beyond fp32 where with the block's power of two it is not.  A warp's tokens have
+// `lanes` lanes each; of a token's n sums in dw those are taken that need it.  (At the end
+// of a token, where nothing else is in registers.)
+__device__ __noinline__ void far_sums(const uint16_t* dout, const uint8_t* yq, const uint8_t* ys, const int32_t* row_of,
+                                      uint32_t rows, uint32_t N, int n, bool on, float* dw, uint32_t lanes) {
+  const uint32_t l = threadIdx.x & (lanes - 1);
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const uint32_t row = on ? (uint32_t)row_of[j] : 0xFFFFFFFFu;
+    const bool far = row < rows && !(fabsf(dw[j]) <= 3.402823466e38f);
+    double sum = 0.0;
+#pragma unroll 1
+    for (uint32_t c = 2 * l; far && c < N; c += 2 * lanes) {
+      float x, y;
+      unpk(e4m3x2_f32(__ldg(reinterpret_cast<const uint16_t*>(yq + (uint64_t)row * N + c))), x, y);
+      const uint32_t d = __ldg(reinterpret_cast<const uint32_t*>(dout + c));
+      const double power = (double)mx_power((uint32_t)__ldg(ys + (uint64_t)row * (N / 32) + c / 32));
+      sum += ((double)bf16_lo(d) * (double)x + (double)bf16_hi(d) * (double)y) * power;
+    }
+    for (uint32_t o = lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (far && l == 0) dw[j] = (float)sum;
+  }
+}
+
 template <int L, int UK>
 __global__ void __launch_bounds__(256, 3) k_route_weight_grad_ckpt(const uint16_t* __restrict__ dout,
                                                                    const uint8_t* __restrict__ yq,
@@ -795,14 +821,20 @@ __global__ void __launch_bounds__(256, 3) k_route_weight_grad_ckpt(const uint16_
       if (WPT > 1 && (threadIdx.x & 31) == 0) red[warp][j] = acc[j];
     }
     if (WPT > 1) __syncthreads();
+    bool far = false;
     if (t < T && l == 0) {
 #pragma unroll
       for (int j = 0; j < UK; ++j) {
         float v = acc[j];
         if (WPT > 1)
           for (int i = 1; i < WPT; ++i) v += red[warp + i][j];
+        far |= there[j] && !(fabsf(v) <= 3.402823466e38f);
         if (j0 + j < k) dw[t * k + j0 + j] = there[j] ? v : 0.0f;
       }
+    }
+    if (__any_sync(0xffffffffu, far)) {   // (of a token's warps the first)
+      __syncwarp();
+      far_sums(dout + t * N, yq, ys, row_of + t * k + j0, rows, N, min(UK, k - j0), t < T, dw + t * k + j0, L < 32 ? L : 32);
     }
     if (WPT > 1) __syncthreads();
   }
