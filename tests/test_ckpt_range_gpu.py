@@ -54,3 +54,31 @@ def test_weight_grad_of_large_gradients(F, T, N, k):
     # the bf16 call on the same values
     bf = F.fp8moe_route_weight_grad(dout, y, row_of).double()
     assert bool(((got - bf).abs() <= (N / 8 + 32) * 2.0 ** -24 * size)[there].all())
+
+
+@pytest.mark.parametrize("M,Fd", [(7, 64), (33, 160), (20001, 160)])
+def test_activation_far_in_the_last_rows(F, M, Fd):
+    """Rows that are no whole block, with gates beyond the exponential, products beyond
+    fp32, NaN codes and NaN scales among the last of them: the bf16 call's results, and
+    nothing past the outputs."""
+    g = torch.Generator(device=DEV).manual_seed(M)
+    h = torch.randn(M, 2 * Fd, device=DEV, generator=g).mul_(2.0).to(BF16)
+    h[M - 1, :32], h[M - 2, Fd:Fd + 32], h[M - 3, :64] = -300.0, 3e38, -2e38
+    hq, hs, v = _pack(F, h)
+    hq[M - 4, 5], hs[M - 5, 1], hs[M - 1, Fd // 32] = 0x7F, 255, 255
+    v[M - 4, 5] = v[M - 5, 32:64] = v[M - 1, Fd:Fd + 32] = float("nan")
+    dout = torch.randn(M, Fd, device=DEV, generator=g).to(BF16)
+    dout[M - 2] *= 1e4
+    for layout in (F.SCALES_ROWMAJOR, F.NO_GROUPS):
+        n = M * Fd // 16 if layout == F.SCALES_ROWMAJOR else F.fp8moe_swizzled_scales_bytes(1, M, Fd // 16, 0, F.NO_GROUPS)
+        guard = Guarded()
+        s0 = guard((M, Fd // 16) if layout == F.SCALES_ROWMAJOR else (n,), U8)
+        s0.zero_()
+        got = F.fp8moe_swiglu_bwd_ckpt(dout, hq, hs, None, layout, dim0=True, out=guard((M, 2 * Fd), BF16),
+                                       q0=guard((M, 2 * Fd), U8), s0=s0)[:3]
+        want = F.fp8moe_swiglu_bwd(dout, v, None, layout, dim0=True)[:3]
+        guard.check("far rows")
+        assert torch.equal(got[0].isnan(), want[0].isnan())
+        assert torch.equal(torch.nan_to_num(got[0], 7.0), torch.nan_to_num(want[0], 7.0))
+        assert torch.equal(got[1] & 0x7F, want[1] & 0x7F) and torch.equal(got[2].view(-1), want[2].view(-1))   # (a NaN's sign is not told)
+    assert F.fp8moe_get_device_status() == 0
