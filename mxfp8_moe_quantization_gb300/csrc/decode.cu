@@ -29,10 +29,9 @@
 // own run on the way to the ring instead, from x and from the first product's partial
 // sums, which saves two of the four meetings.  The weights' producer takes no part
 // in the meetings: while the others add, it fills its ring with W2.
-// Measured: one token of 6 experts of 1408 x 2048 18 us (8 of bytes, the rest the way
-// through two products: 10.4 for a layer of almost no weights), of 8 of 2048 x 7168 66 us =
-// 5.5 TB/s; 23 tokens of 256 such 764 us = 6.6 TB/s (99% of a copy's rate), 64 tokens of 16
-// experts of 8192 x 5120 325 us = 6.3 TB/s.
+// Measured in a graph: one token of 6 of 64 experts of 1408 x 2048 19 us (8 of bytes, the rest
+// the way through two products: 10.5 for a layer of almost no weights), of 8 of 256 of 2048 x
+// 7168 66 us = 5.5 TB/s, 23 such 892 us = 6.7 TB/s; 64 of one of 16 of 8192 x 5120 330 us = 6.3 TB/s.
 //   warps 0-3  accumulators to partial sums;  4  weights by TMA;  5  MMA issue;
 //   6  scales to tensor memory;  7-14  terms to shared memory;  all but 4-6  terms
 //   and the final sums.
@@ -426,8 +425,8 @@ struct Terms {
 };
 
 // What the host knows of a call: nothing (the plan decides how terms are made), that
-// entries have few pairs (made on the way), that they have at most two.  (One token: 18.9
-// us if the plan decides, 18.5 as one of few, 17.9.)
+// entries have few pairs (made on the way), that they have at most two.  (One token of 6 of
+// 64 experts of 1408 x 2048: 20.4 us if the plan decides, 19.5 as one of few, 19.3.)
 enum { DC_ANY = 0, DC_FEW, DC_TWO };
 template <int FORM>
 __global__ void __launch_bounds__(DC_THREADS, 1)
@@ -491,11 +490,12 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   const uint32_t tmem = tmem_s;
   const int nlive = pl.num[0], nent = pl.num[1];
   // Terms made on the way where entries have few pairs: no more than 8, as a warp of a
-  // team takes two at a time and must not be slower than the weights, and 1.5 on average.
-  // (8 of 256 experts of 2048 x 7168: 23 tokens (1.4 pairs an entry) 918 us against 942;
-  // 6 of 64 of 1408 x 2048: twelve (1.6) 83 and 82, sixteen (1.9) 99 and 92 with a cold
-  // L2, 24 (2.5) 111 and 106.)
-  const bool direct = FORM != DC_ANY || (L.team_log == 1 && pl.num[2] <= 8 && 2 * nlive <= 3 * nent);
+  // team takes two at a time and must not be slower than the weights, and 1.2 on average.
+  // (In a graph, made and copied: 12 tokens of 2 of 256 experts of 1408 x 2048 (1.05 pairs
+  // an entry) 45 us and 47, 23 of 3 of 256 of 2048 x 7168 (1.13) 413 and 417; 16 of 6 of 160 of
+  // 1024 x 4096 (1.3) 157 and 156, 23 of 8 of 256 of 2048 x 7168 (1.4) 902 and 893.  With
+  // cold caches the copies are 0 to 2 us better with the first two, 5 and 15 with the others.)
+  const bool direct = FORM != DC_ANY || (L.team_log == 1 && pl.num[2] <= 8 && 5 * nlive <= 6 * nent);
   const Stream s1(nent, L.rt[0], L.kp[0], L.grid), s2(nent, L.rt[1], L.kp[1], L.grid);
   using First = std::integral_constant<int, X_TERMS>;      // the products, by their terms
   using Second = std::integral_constant<int, ACT_TERMS>;
@@ -1096,8 +1096,9 @@ cudaError_t launch_decode(DecodeArgs a, void* workspace, int num_sms, int max_sm
     if (!make_tmap(&tm[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, q[i], 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
   // Up to eight tokens no entry has more than eight pairs; two at most of an expert on
-  // average (6 of 64 experts of 1408 x 2048: four tokens 42.5 us by copies of terms, 39.8
-  // made on the way, eight 70.3 and 66.8; eight tokens' one expert 21 and 26).
+  // average (6 of 64 experts of 1408 x 2048: four tokens 43.5 us by copies of terms, 40.8
+  // made on the way, eight 67.8 and 65.2).  Their choices are not known here: eight tokens
+  // that all have the same one of 8 experts of 4096 x 2048 take 26 us, 22 by copies.
   const bool few = a.T <= 8 && a.P <= 2 * a.E && L.team_log == 1;
   const void* kern = !few        ? (const void*)k_decode<DC_ANY>
                      : a.nb == 2 ? (const void*)k_decode<DC_TWO>
