@@ -532,7 +532,8 @@ __global__ void __launch_bounds__(norm_bwd_threads<V>()) k_norm_bwd(NormBwdArgs 
 // fp32, a product by the block's power of two) comes on top of its instructions, and
 // from about 20 an element on it is issue and latency that bound: 16384 x 5120 with
 // dh 99 us = 5.9 TB/s (89% of a copy's rate), 16384 x 7168 131 us = 6.3, 20001 x 4096
-// 100 us = 5.7, 65536 x 512 44 us = 5.4.
+// 100 us = 5.7, 65536 x 512 49 us = 4.8.  Rows of more than 8192 elements, four chunks a
+// thread, have one CTA an SM: 8192 x 12288 195 us = 3.6 TB/s, the bf16 form 164.
 template <int V, int R>
 constexpr int norm_ck_threads() { return R == 4 ? 256 : R == 2 || V == 4 ? 512 : 640; }
 template <int V, int R>
@@ -861,13 +862,13 @@ cudaError_t launch_bwd_ckpt(NormBwdArgs a, float* dw, int num_sms, int max_smem,
   const int nch = a.H / 8;
   // Chunks and rows of a thread at a time.  Several rows where they are short
   // (65536 x 512 with dh: 54 us with one, 48 with four), and where registers leave
-  // room for one CTA an SM anyway (16384 x 7168: 162 and 135 with two); in between two
-  // CTAs of one row each are better (16384 x 5120: 100, 113 with two rows).
+  // room for one CTA an SM anyway (16384 x 7168: 164 and 131 with two); in between two
+  // CTAs of one row each are better (16384 x 5120: 99, 111 with two rows).
   const int v = nch <= 256 ? 1 : nch <= 1024 ? 2 : 4, rows = nch <= 256 ? 4 : nch <= 512 || (nch > 640 && nch <= 1024) ? 2 : 1;
   int wpr = nch > NORM_MAX_CHUNKS ? 16 : (nch + 32 * v - 1) / (32 * v);
   int groups = wpr >= 8 ? 1 : 8 / wpr;
   // the ring as the bf16 form's, and as deep as fits where registers leave room for
-  // one CTA only (16384 x 7168 without dh: 121 us, 147 with half the memory)
+  // one CTA only (16384 x 7168 without dh: 115 us, 145 with half the memory)
   const int64_t budget = max_smem - 2048;
   const int64_t slot = (int64_t)a.H * (a.dh ? 5 : 3) * groups * rows;
   const int64_t room = budget / (wpr * groups > (rows == 1 && v == 2 ? 10 : 8) ? 1 : 2);

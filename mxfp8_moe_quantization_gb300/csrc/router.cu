@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(256, 4) k_route_weight_grad(const uint16_t* __
 // fifth of its instructions (60000 x 128 x 8: 42 us, 26 without).  Bound by HBM, at
 // 1.03 bytes a value of y: 4096 x 7168 x 8 53 us = 5.7 TB/s (85% of a copy's rate; its
 // 2048 CTAs are four and a half rounds, and the warps wait for memory), 8189 x 2048 x 6
-// 26 us (79%); whole CTAs a token, or persistent ones, are no faster.
+// 26.6 us (78%); whole CTAs a token, or persistent ones, are no faster.
 //
 // Sums that are not finite are taken once more in 64 bits: dout times a code (up to 448)
 // may be beyond fp32 where with the block's power of two it is not.  A warp's tokens have

@@ -15,12 +15,13 @@
 // next tile's loads, 164 with single scale bytes and four warps a CTA, 159 with words, 155
 // with a warp a CTA, 151 with maxima in pairs; twelve warps a CTA 177.)
 //
-// Bound by the instructions, 46 an element of a (five block scalings, the unpacking and
-// the sigmoid), of which 0.6 a cycle and scheduler issue, and by an SM's memory pipe,
-// which takes every 32 bytes apart that a store's lanes have in one row or column, and
-// is two thirds busy.  HBM's 9.2 bytes an element would take 100 us; measured, among
-// other passes: 51136 x 1408 in 64 groups, all outputs, 147 us = 4.5 TB/s (68% of a
-// copy's rate).
+// Nothing is saturated: three warps a scheduler, all that the registers leave, issue 0.55
+// instructions a cycle, 44 an element of a (five block scalings, the unpacking and the
+// sigmoid), and wait in between for loads, shuffles and an SM's memory pipe, which takes
+// every 32 bytes apart that a store's lanes have in one row or column, and is 64% busy.
+// HBM's 9.2 bytes an element would take 100 us; measured, among other passes: 51136 x 1408
+// in 64 groups, all outputs, 147 us = 4.5 TB/s (67% of a copy's rate).  Without the
+// activation 119 us, as the bf16 form (its boxes by TMA), for 8.1 bytes against 10.1.
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "launch.h"
@@ -32,7 +33,7 @@
 namespace fp8moe {
 namespace {
 
-// Warps an SM: without the activation 128 registers do (128 us cold, 132 with twelve warps).
+// Warps an SM: without the activation 128 registers do (120 us, 123 with twelve warps).
 template <bool ACT>
 constexpr int sc_warps() { return ACT ? 12 : 16; }
 constexpr int CP = 2;                // column pairs of a lane
