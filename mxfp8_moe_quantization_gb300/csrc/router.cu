@@ -741,10 +741,13 @@ __global__ void __launch_bounds__(256, 4) k_route_weight_grad(const uint16_t* __
 // 2048 CTAs are four and a half rounds, and the warps wait for memory), 8189 x 2048 x 6
 // 26.6 us (78%); whole CTAs a token, or persistent ones, are no faster.
 //
-// Sums that are not finite are taken once more in 64 bits: dout times a code (up to 448)
-// may be beyond fp32 where with the block's power of two it is not.  A warp's tokens have
-// `lanes` lanes each; of a token's n sums in dw those are taken that need it.  (At the end
-// of a token, where nothing else is in registers.)
+// Sums that are not finite are taken once more: dout times a code (up to 448) may be
+// beyond fp32 where with the block's power of two it is not.  Where eight products' sum is
+// not finite, they are taken of gradients times 2^-16 (exact: bf16's last place is 2^-133),
+// and the sums are added in 64 bits; what is NaN stays so.  (4096 x 7168 x 8: 53 us, 970
+// where that holds for every sum.)  A warp's tokens have `lanes` lanes each; of a token's n
+// sums in dw those are taken that need it, at the end of a token, where nothing else is in
+// registers.
 __device__ __noinline__ void far_sums(const uint16_t* dout, const uint8_t* yq, const uint8_t* ys, const int32_t* row_of,
                                       uint32_t rows, uint32_t N, int n, bool on, float* dw, uint32_t lanes) {
   const uint32_t l = threadIdx.x & (lanes - 1);
@@ -754,24 +757,30 @@ __device__ __noinline__ void far_sums(const uint16_t* dout, const uint8_t* yq, c
     const bool far = row < rows && !(fabsf(dw[j]) <= 3.402823466e38f);
     double sum = 0.0;
 #pragma unroll 1
-    for (uint32_t c = 2 * l; far && c < N; c += 2 * lanes) {
-      float x, y;
-      unpk(e4m3x2_f32(__ldg(reinterpret_cast<const uint16_t*>(yq + (uint64_t)row * N + c))), x, y);
-      const uint32_t d = __ldg(reinterpret_cast<const uint32_t*>(dout + c));
-      const double power = (double)mx_power((uint32_t)__ldg(ys + (uint64_t)row * (N / 32) + c / 32));
-      sum += ((double)bf16_lo(d) * (double)x + (double)bf16_hi(d) * (double)y) * power;
+    for (uint32_t v = l; far && v < N / 8 && sum == sum; v += lanes) {
+      const uint4 d = ld_nc16(dout + v * 8);
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(yq + (uint64_t)row * N + v * 8));
+      const float power = mx_power((uint32_t)__ldg(ys + (uint64_t)row * (N / 32) + (v >> 2)));
+      auto dot = [&](float by) {
+        uint64_t s = fma2(mul2(unpk_bf16(d.x), pk(by, by)), e4m3x2_f32(q.x), 0);
+        s = fma2(mul2(unpk_bf16(d.y), pk(by, by)), e4m3x2_f32(q.x >> 16), s);
+        s = fma2(mul2(unpk_bf16(d.z), pk(by, by)), e4m3x2_f32(q.y), s);
+        return sum_of(fma2(mul2(unpk_bf16(d.w), pk(by, by)), e4m3x2_f32(q.y >> 16), s));
+      };
+      const float s = dot(1.0f);
+      sum += fabsf(s) <= 3.402823466e38f ? (double)s * (double)power : (double)dot(0x1p-16f) * (65536.0 * (double)power);
     }
     for (uint32_t o = lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (far && l == 0) dw[j] = (float)sum;
   }
 }
 
+// (Of one choice five CTAs an SM: 65536 x 1024 38 us, 43 with the four that registers would allow.)
 template <int L, int UK>
-__global__ void __launch_bounds__(256, 3) k_route_weight_grad_ckpt(const uint16_t* __restrict__ dout,
-                                                                   const uint8_t* __restrict__ yq,
-                                                                   const uint8_t* __restrict__ ys,
-                                                                   const int32_t* __restrict__ row_of, uint32_t rows,
-                                                                   int64_t T, uint32_t N, int k, float* __restrict__ dw) {
+__global__ void __launch_bounds__(256, UK == 1 ? 5 : 3)
+    k_route_weight_grad_ckpt(const uint16_t* __restrict__ dout, const uint8_t* __restrict__ yq, const uint8_t* __restrict__ ys,
+                             const int32_t* __restrict__ row_of, uint32_t rows, int64_t T, uint32_t N, int k,
+                             float* __restrict__ dw) {
   constexpr int WPT = L / 32;
   __shared__ float red[8][UK];
   const int warp = threadIdx.x >> 5, l = threadIdx.x % L;

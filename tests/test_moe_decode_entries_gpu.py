@@ -54,3 +54,21 @@ def test_many_row_tiles_of_a_cta(F, T, E):
     args = _layer(F, T, 64, 32768, E, 1, seed=T)
     args[1].fill_(E - 1)
     _decode_ok(F, args)
+
+
+def test_streams_of_two_priorities(F):
+    """Calls in flight at once, some of which go first, beside other kernels: the bits
+    of calls alone."""
+    one, few = _layer(F, 1, 2048, 1408, 8, 6), _layer(F, 20, 256, 512, 6, 2)
+    want = [F.fp8moe_mxfp8_moe_decode(*one), F.fp8moe_mxfp8_moe_decode(*few)]
+    x = torch.randn(4096, 2048, device=DEV).to(torch.bfloat16)
+    streams = [torch.cuda.Stream(priority=p) for p in (0, -1, 0)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(40):
+        got.append((F.fp8moe_mxfp8_moe_decode(*one, stream=streams[0]), want[0]))
+        got.append((F.fp8moe_mxfp8_moe_decode(*few, stream=streams[1]), want[1]))
+        if i % 4 == 0:
+            F.fp8moe_quantize_tensorwise(x, stream=streams[2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in got) and F.fp8moe_get_device_status() == 0
