@@ -15,7 +15,7 @@
 // block's largest on, and what is smaller to 2^-22 of that largest; four hold an fp32
 // value to 2^-19 of itself, or 2^-32 of the largest.  (With three, to 2^-14, one of a
 // hundred outputs was the neighbour of the bf16 number that it should be; with four one
-// of a thousand, as with five: the order of the sums.)
+// of a thousand, as with five, and half of that with the sums in chains, see Stream.)
 // The terms are further columns of N, where the tensor core has room: N is at least
 // 16, and the weights' arrival leaves it idle most of the time.
 //
@@ -78,6 +78,7 @@ struct DecodeSmem {
   int slots, b_bytes;
   int team_log, teams;                     // 2^team_log warps fill a slot of terms together
   int acc, accs;                           // tensor memory columns of an accumulator; accumulators
+  int chain;                               // pieces that are added in one
   int sfa, b, bars, plan, total;
   // tiles and pieces of the products' K, tiles of their rows; the grid; H / 4; choices
   Div kt[2], kp[2], rt[2], grid, quads, k;
@@ -221,12 +222,15 @@ FP8MOE_DEV float reciprocal(float x) {   // to 2^-23
 }
 
 // One product's stream of pieces: nent entries x row tiles x pieces of K, in runs
-// of `base` pieces, one more for the first `rest` CTAs.
+// of `base` pieces, one more for the first `rest` CTAs.  At most `chain` pieces in a row
+// are added in an accumulator, as the tensor core's sums are cut off, not rounded.
 struct Stream {
   uint32_t C, runs, base, rest;   // pieces; CTAs that have a run of them
   float per0, per1;               // 1 / base, 1 / (base + 1)
   const Div &rt, &kp;
-  FP8MOE_DEV Stream(int nent, const Div& rt_, const Div& kp_, const Div& grid) : rt(rt_), kp(kp_) {
+  const int& chain;
+  FP8MOE_DEV Stream(int nent, const Div& rt_, const Div& kp_, const Div& grid, const int& chain_)
+      : rt(rt_), kp(kp_), chain(chain_) {
     static_assert(DECODE_MIN_RUN == 2, "base of a short stream");
     C = (uint32_t)nent * rt.d * kp.d;
     const uint32_t want = (C + 1) / 2;
@@ -253,7 +257,7 @@ struct Stream {
 };
 
 // A CTA's run of a stream, segment by segment: the pieces of one tile that are
-// in the run.
+// in the run, a chain of them at a time.
 struct Run {
   uint32_t left, tile;   // pieces to go, this segment's among them; row tile over all entries
   int n, k;              // pieces of this segment, the first one's place along K
@@ -265,14 +269,18 @@ struct Run {
     k = (int)(lo - tile * s.kp.d);
     ent = (int)s.rt.quot(tile);
     row = (int)(tile - (uint32_t)ent * s.rt.d);
-    n = (int)min(left, (uint32_t)(s.kp.d - k));
+    n = segment(s);
   }
+  FP8MOE_DEV int segment(const Stream& s) const { return min(min((int)left, (int)s.kp.d - k), s.chain); }
   FP8MOE_DEV void next(const Stream& s) {
     left -= n;
-    k = 0;
-    ++tile;
-    if (++row == (int)s.rt.d) row = 0, ++ent;
-    n = (int)min(left, s.kp.d);
+    k += n;
+    if (k == (int)s.kp.d) {
+      k = 0;
+      ++tile;
+      if (++row == (int)s.rt.d) row = 0, ++ent;
+    }
+    n = segment(s);
   }
 };
 
@@ -496,7 +504,7 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
   // 1024 x 4096 (1.3) 157 and 156, 23 of 8 of 256 of 2048 x 7168 (1.4) 902 and 893.  With
   // cold caches the copies are 0 to 2 us better with the first two, 5 and 15 with the others.)
   const bool direct = FORM != DC_ANY || (L.team_log == 1 && pl.num[2] <= 8 && 5 * nlive <= 6 * nent);
-  const Stream s1(nent, L.rt[0], L.kp[0], L.grid), s2(nent, L.rt[1], L.kp[1], L.grid);
+  const Stream s1(nent, L.rt[0], L.kp[0], L.grid, L.chain), s2(nent, L.rt[1], L.kp[1], L.grid, L.chain);
   using First = std::integral_constant<int, X_TERMS>;      // the products, by their terms
   using Second = std::integral_constant<int, ACT_TERMS>;
 
@@ -834,8 +842,11 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
       const Stream& s = NT == X_TERMS ? s1 : s2;
       const int R = NT == X_TERMS ? R1 : R2;
       float* part = NT == X_TERMS ? a.part1 : a.part2;
+      uint32_t before = 0xFFFFFFFFu;               // the tile of the segment before
       for (Run r(s, cta); r.left > 0; r.next(s)) {
         const uint32_t ent = pl.ent[r.ent];
+        const bool again = r.tile == before;       // added to what this thread has written
+        before = r.tile;
         const int first = (int)(ent >> 10 & 1023u), pairs = (int)(ent >> 20);
         const int mine = (int)(cta - s.owner(r.tile * s.kp.d));
         const int row = r.row * 128 + warp * 32 + lane;
@@ -861,7 +872,10 @@ __global__ void __launch_bounds__(DC_THREADS, 1)
             float v = 0.0f;   // the smallest term first
 #pragma unroll
             for (int t = NT - 1; t >= 0; --t) v += __uint_as_float(q[i * NT + t]);
-            if (i0 + i < pairs && row < R) dst[(int64_t)(i0 + i) * R] = v;
+            if (i0 + i < pairs && row < R) {
+              float* p = dst + (int64_t)(i0 + i) * R;
+              *p = again ? *p + v : v;
+            }
           }
         }
         acc.step(1, L.accs);
@@ -1030,6 +1044,12 @@ DecodeSmem layout(int P, int nb, int max_ent, int max_smem) {
   // 1024 to align the rings, 1024 for what is static
   L.slots = (max_smem - 2048 - fixed) / (DC_A_BYTES + DC_G * 512 + L.b_bytes);
   if (L.slots > DC_MAX_SLOTS) L.slots = DC_MAX_SLOTS;
+  // Outputs that differ from the exact ones' bf16, 64 tokens of 1 of 16 experts of 8192 x
+  // 5120: 1.10 of a thousand without chains, 0.78 with 16 pieces, 0.52 with eight, 0.46 with
+  // four (products in 32 bits: 0.41), at the same time down to eight; four take 1% more.
+  // More pairs take longer to add up (64 choices of each of 8 experts of 4096 x 2048 116 us
+  // without or with 16, 128 with eight).
+  L.chain = nb <= 20 ? 8 : 16;
   // (entries of 64 pairs fill half of tensor memory: no second accumulator)
   L.accs = 2 * L.acc + 12 * DC_G * L.slots <= 512 ? 2 : 1;
   L.team_log = L.slots >= 3 ? 1 : 2;
